@@ -121,6 +121,31 @@ typedef struct pa_decode_meta {
     uint64_t workspace_bytes;   /* device workspace pa_decode needs */
 } pa_decode_meta;
 
+/* Packed plan of a shared-prefix decode (pa_pack_decode_shared). */
+typedef struct pa_shared_meta {
+    int32_t num_seqs;
+    int32_t num_groups;
+    int32_t max_blocks_per_seq; /* row pitch of the block tables */
+    int32_t num_items;          /* work items: (sequences, KV head, key range) */
+    int32_t num_ctas;           /* CTAs the items are dealt out to */
+    int32_t num_partials;       /* partial results in the workspace */
+    int32_t max_parts;          /* most parts any context is cut into */
+    int32_t rows_per_tile;      /* sequences per 128-row query tile (128 / group, floored) */
+    int32_t combine;            /* 1: some context has two or more parts, or none (merge launch) */
+    int32_t split_tokens;       /* keys per part, at most */
+    int32_t tables_packed;      /* 1: the image holds block tables and slots */
+    int32_t reserved;
+    uint64_t tokens_saved;       /* keys the groups read once instead of once per sequence */
+    uint64_t off_block_tables;   /* int32 [num_seqs][max_blocks_per_seq], -1 padded (tables_packed) */
+    uint64_t off_slot_mapping;   /* int32 [num_seqs] slot of each last token (tables_packed) */
+    uint64_t off_items;          /* int32 [num_items][8], CTA by CTA, longest first: first sequence,
+                                    sequences, KV head, block-table row, first key, end key, part, 0 */
+    uint64_t off_cta_items;      /* int32 [num_ctas+1] first work item of each CTA */
+    uint64_t off_seq_parts;      /* int32 [num_seqs][2] first partial slot and number of parts */
+    uint64_t total_bytes;
+    uint64_t workspace_bytes;    /* device workspace pa_decode_shared(_int8) needs */
+} pa_shared_meta;
+
 /* ------------------------------------------------------------------ host packing */
 
 /*
@@ -157,6 +182,40 @@ int pa_pack_prefill(const pa_dims *dims, int32_t num_seqs, const int32_t *seq_le
 int pa_pack_decode(const pa_dims *dims, int32_t num_seqs, const int32_t *context_lens,
                    const int32_t *block_offsets, const int32_t *block_ids, int32_t split_tokens,
                    void *host_buf, size_t host_buf_bytes, pa_decode_meta *meta);
+
+/*
+ * pa_pack_decode_shared — plan of a decode batch (one query token per
+ * sequence) whose sequences share prefixes.  Source: "vLLM / SGLang
+ * 面试源码深挖", section 4 (forked sequences and beams name the same blocks)
+ * and section 3 (requests behind one prompt hit the same cached blocks).
+ * The sequences come in groups of consecutive ones; those of a group begin
+ * with the same physical blocks.  Their query rows attend to the shared part
+ * together, to the rest of each context alone, and the parts are merged by
+ * log-sum-exp.  Groups of one, groups that share nothing and entries of
+ * context 0 (output rows of zeros) are allowed.
+ *   context_lens:  host int32 [num_seqs], each including the token being decoded
+ *   group_offsets: host int32 [num_groups+1], group i = sequences
+ *                  [group_offsets[i], group_offsets[i+1]), from 0 to num_seqs
+ *   shared_lens:   host int32 [num_groups], tokens the group shares, a multiple
+ *                  of block_size and at most the whole blocks of its shortest
+ *                  context (entries of context 0 do not count); NULL (with
+ *                  block lists only): the leading blocks that all of the
+ *                  group's lists have in common
+ * The block tables are either packed from host block lists,
+ *   block_offsets, block_ids: as in pa_pack_decode (table_rows must be NULL);
+ *                  shared blocks that differ are PA_ERR_INVALID_ARG
+ * or already on the device (e.g. a pa_pool's), when block_offsets is NULL:
+ *   table_rows:    host int32 [num_seqs], each sequence's row of that table
+ *                  (NULL: row b); a group reads its shared part through its
+ *                  first sequence's row
+ *   max_blocks_per_seq: that table's row pitch
+ * split_tokens: most keys per part, a multiple of 128 (0 = choose from the
+ * current device's SM count).  Buffer and error rules as pa_pack_decode.
+ */
+int pa_pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32_t *context_lens, int32_t num_groups,
+                          const int32_t *group_offsets, const int32_t *shared_lens, const int32_t *block_offsets,
+                          const int32_t *block_ids, const int32_t *table_rows, int32_t max_blocks_per_seq,
+                          int32_t split_tokens, void *host_buf, size_t host_buf_bytes, pa_shared_meta *meta);
 
 /* One asynchronous host-to-device copy of a packed metadata image. */
 int pa_upload(void *dev_dst, const void *host_src, size_t bytes, pa_stream_t stream);
@@ -290,6 +349,29 @@ int pa_decode_fused(const pa_dims *dims, const void *q, const void *k, const voi
                     const int32_t *slot_mapping, const int32_t *context_lens, const int32_t *block_tables,
                     float scale, void *out, const pa_decode_meta *meta, const int32_t *items,
                     const int32_t *seq_items, void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_decode_shared — pa_decode for a batch whose sequences share prefixes: the
+ * same result, with each shared block read once per group and not once per
+ * sequence.  Sources as pa_pack_decode_shared; merge as pa_decode.  One
+ * persistent tcgen05 launch for all parts and, if some context has several,
+ * one merge launch.  The K/V of every key must already be stored.
+ *   q, out:        device bf16 [meta->num_seqs][num_heads][head_dim]
+ *   block_tables:  device int32, row pitch meta->max_blocks_per_seq: the plan's
+ *                  (dev + meta->off_block_tables) or the caller's
+ *   items, cta_items, seq_parts: device copies of the plan's arrays
+ *   workspace:     device memory of at least meta->workspace_bytes (may be NULL
+ *                  when that is 0), 256-byte aligned; calls in flight at once
+ *                  need separate workspaces
+ * A block id outside [0, num_blocks) among a context's blocks reads as zeros
+ * (as do the key's score and value) and sets bit 6 of the device error word; a
+ * bounded wait that runs out sets bit 5 and leaves `out` undefined.
+ * scale must be finite and > 0.
+ */
+int pa_decode_shared(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                     const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
+                     const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts, void *workspace,
+                     size_t workspace_bytes, pa_stream_t stream);
 
 /*
  * pa_copy_blocks — copy-on-write of shared cache blocks.  Source: "vLLM /
@@ -489,7 +571,8 @@ const char *pa_last_error_string(void);
  * met a slot outside [-1, num_slots); 1 a bounded wait in the prefill kernel
  * timed out; 2 a block-copy triple was out of range; 3 a bounded wait in the
  * INT8 decode kernel timed out; 4 the wait of pa_selftest_bounded_wait timed
- * out.  Synchronises `stream`: for tests and debugging, never on the hot path.
+ * out; 5 a bounded wait in the shared-prefix decode timed out; 6 the
+ * shared-prefix decode met a block id outside the pool.  Synchronises `stream`: for tests and debugging, never on the hot path.
  */
 int pa_read_device_error(uint32_t *code, pa_stream_t stream);
 

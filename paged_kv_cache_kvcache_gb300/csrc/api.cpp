@@ -435,6 +435,88 @@ extern "C" int pa_decode_int8(const pa_dims *dims, const void *q, const void *k_
     return launch_decode_int8(a, stream);
 }
 
+// Host-side checks of a shared-prefix decode; fills `a`.  Sets *nothing when there is no work.
+static int prepare_shared(const char *fn, const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                          const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
+                          const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts, void *workspace,
+                          size_t workspace_bytes, SharedArgs *a, bool *nothing)
+{
+    *nothing = false;
+    int rc = check_dims(dims);
+    if (rc != PA_OK)
+        return rc;
+    if (!meta)
+        return fail(PA_ERR_INVALID_ARG, "meta is NULL");
+    if (meta->num_seqs < 0 || meta->num_items < 0 || meta->num_ctas < 0 || meta->num_ctas > meta->num_items ||
+        (meta->num_items > 0 && meta->num_ctas < 1) || meta->num_partials < 0 || meta->max_blocks_per_seq < 1)
+        return fail(PA_ERR_INVALID_ARG, "malformed shared decode meta");
+    if (!(scale > 0.f) || !std::isfinite(scale))
+        return fail(PA_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (meta->num_seqs == 0) {
+        *nothing = true;
+        return PA_OK;
+    }
+    const int group = dims->num_heads / dims->num_kv_heads;
+    if (meta->rows_per_tile != (kPrefillRows / group > 0 ? kPrefillRows / group : 1))
+        return fail(PA_ERR_INVALID_ARG, "%s: meta was packed for other dims", fn);
+    if (!q || !k_cache || !v_cache || !block_tables || !out || !items || !cta_items || !seq_parts)
+        return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out) || misaligned(items))
+        return fail(PA_ERR_INVALID_ARG, "%s: tensors and items must be 16-byte aligned", fn);
+    if ((reinterpret_cast<uintptr_t>(seq_parts) & 7u) || (reinterpret_cast<uintptr_t>(cta_items) & 3u) ||
+        (reinterpret_cast<uintptr_t>(block_tables) & 3u))
+        return fail(PA_ERR_INVALID_ARG, "%s: misaligned plan array or block table", fn);
+    if (meta->num_items > 0 && dims->num_blocks == 0)
+        return fail(PA_ERR_INVALID_ARG, "empty KV pool");
+    const size_t per = (size_t)dims->num_heads * dims->head_dim * 4;
+    const size_t o_bytes = align_up((size_t)meta->num_partials * per, 256);
+    if (meta->num_partials > 0) {
+        if (o_bytes + align_up((size_t)meta->num_partials * dims->num_heads * 4, 256) != meta->workspace_bytes)
+            return fail(PA_ERR_INVALID_ARG, "%s: meta was packed for other dims", fn);
+        if (workspace_bytes < meta->workspace_bytes)
+            return fail(PA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %llu", fn, workspace_bytes,
+                        (unsigned long long)meta->workspace_bytes);
+        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+            return fail(PA_ERR_INVALID_ARG, "%s: workspace must be non-NULL and 256-byte aligned", fn);
+    }
+    *a = SharedArgs{};
+    a->dims = *dims;
+    a->q = q;
+    a->k_cache = k_cache;
+    a->v_cache = v_cache;
+    a->block_tables = block_tables;
+    a->items = items;
+    a->cta_items = cta_items;
+    a->seq_parts = seq_parts;
+    a->out = out;
+    if (meta->num_partials > 0) {
+        a->part_o = static_cast<float *>(workspace);
+        a->part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + o_bytes);
+    }
+    a->scale = scale;
+    a->num_seqs = meta->num_seqs;
+    a->num_items = meta->num_items;
+    a->num_ctas = meta->num_ctas;
+    a->rows_per_tile = meta->rows_per_tile;
+    a->max_blocks_per_seq = meta->max_blocks_per_seq;
+    a->combine = meta->combine != 0;
+    return PA_OK;
+}
+
+extern "C" int pa_decode_shared(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
+                                const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts,
+                                void *workspace, size_t workspace_bytes, pa_stream_t stream)
+{
+    SharedArgs a;
+    bool nothing = false;
+    int rc = prepare_shared("pa_decode_shared", dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
+                            cta_items, seq_parts, workspace, workspace_bytes, &a, &nothing);
+    if (rc != PA_OK || nothing)
+        return rc;
+    return launch_decode_shared(a, stream);
+}
+
 extern "C" int pa_copy_blocks(const pa_dims *dims, void *k_cache, void *v_cache, const int32_t *triples,
                               int32_t num_triples, pa_stream_t stream)
 {
@@ -518,6 +600,8 @@ extern "C" int pa_read_device_error(uint32_t *code, pa_stream_t stream)
         rc = read_fused8_error(code);
     if (rc == PA_OK)
         rc = read_selftest_error(code);
+    if (rc == PA_OK)
+        rc = read_shared_error(code);
     return rc;
 }
 

@@ -1,0 +1,800 @@
+// Single-token decode of a batch whose sequences share long prefixes: the shared pages are
+// read once for the whole group instead of once per sequence.
+//
+// Sources (page title, section):
+//  - "vLLM / SGLang 面试源码深挖", section 4 (beam search and KV block fork): parent and
+//    child sequences share block ids; section 3: requests behind one prompt hit the same
+//    cached prefix blocks.
+//  - "面试问答准备: nano-vLLM 推理引擎优化", the Split-K entry: segments of a context emit a
+//    max, a normaliser and an fp32 accumulator, merged by log-sum-exp.
+//
+// Mathematics.  For a key range R let m = max_R s, l = sum_R 2^(s - m), o = sum_R 2^(s - m) v / l
+// (s in log2 units).  Ranges merge exactly: with e_R = m_R + log2 l_R and M = max e_R,
+//   out = sum_R 2^(e_R - M) o_R / sum_R 2^(e_R - M).
+// So a sequence's context may be cut at its group's shared prefix, and the prefix part of all
+// sequences of the group is ONE product: rows = (sequence, query head of the KV head's group),
+// all reading the same K/V.  With R rows a K/V byte is worth R flops (bf16), so a prefix is
+// bound by HBM up to about 290 rows per KV head and by the tensor cores beyond.
+//
+// One persistent launch runs every part: a work item is (up to 2 x 128 rows, KV head, key
+// range, block-table row); the prefix parts carry many sequences, the suffix parts one.  The
+// host cuts the key ranges and deals the items out to the CTAs (longest first onto the least
+// loaded).  Structure of a CTA as in the prefill kernel: K, V and query producers (TMA, one
+// 3-D box per physical block), one MMA warp (tcgen05, S and O in tensor memory, P fed back
+// through tensor memory), one softmax warpgroup per 128-row tile, every ring running on
+// across items.  A suffix part fills few of its tile's 128 rows; its products then run mostly
+// on padding, which costs nothing that matters: 128 keys x 128 rows take about 1100 cycles of
+// the tensor core while their K/V (64 KB) take about 2800 cycles of this SM's share of HBM.
+// Warps without a valid row skip the softmax.
+//
+// Every hand-off waits with a time limit; a wait that runs out sets an error bit and the
+// kernel returns.  A block id outside the pool reads as zeros and sets an error bit.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace pa {
+
+// bit 0: a bounded wait timed out; bit 1: a block id outside the pool was met
+__device__ uint32_t g_shared_error;
+
+namespace {
+
+// warps 0-7: softmax (two warpgroups), 8: K producer, 9: MMA issuer and TMEM owner, 10: V
+// producer, 11: query producer.  168 registers per thread at launch; setmaxnreg moves part of
+// warps 8-11's share to the softmax warps.
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+static_assert(128 * (2 * kSoftmaxRegs + kOtherRegs) == kThreads * kLaunchRegs, "register hand-over");
+constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10, kQWarp = 11;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f; // log2 units
+// An item of n key tiles owns n + 1 release events: its opening score products (K tile 0
+// read), then one per iteration (V tile j and K tile j + 1 read).  At most 2S - 1 events lie
+// between a refill of a ring of S slots and the event it waits for, so 8 keep parities apart.
+constexpr int kIterRing = 8;
+
+template <int D>
+struct ShLayout {
+    static constexpr int kPanels = D / 64;        // 64-element (128-byte) panels along head_dim
+    static constexpr int kPanelBytes = 128 * 128; // 128 rows x 128 bytes
+    static constexpr int kTileBytes = kPanels * kPanelBytes;
+    static constexpr int kKStages = D == 128 ? 3 : 4;
+    static constexpr int kVStages = D == 128 ? 2 : 4;
+    static constexpr int kQ = 0; // two query tiles
+    static constexpr int kK = kQ + 2 * kTileBytes;
+    static constexpr int kV = kK + kKStages * kTileBytes;
+    static constexpr int kBar = kV + kVStages * kTileBytes;
+    static constexpr int kSmemBytes = kBar + 512 + 1024; // + alignment slack
+    static_assert(kKStages <= 4 && kVStages <= 4, "barrier slots");
+    static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+};
+
+struct ShParams {
+    const int4 *items;
+    const int32_t *cta_items;
+    const int2 *seq_parts;
+    const int32_t *block_tables;
+    __nv_bfloat16 *out;
+    float *part_o;
+    float *part_lse;
+    float scale_log2;
+    int32_t num_heads;
+    int32_t group;
+    int32_t rows_per_tile; // sequences per 128-row tile
+    int32_t block_size;
+    int32_t box_rows;
+    int32_t max_blocks;
+    int32_t num_blocks;
+};
+
+struct Bars {
+    uint32_t base;
+    __device__ uint32_t q_full(int t) const { return base + 8 * t; }
+    __device__ uint32_t q_free(int t) const { return base + 8 * (2 + t); }
+    __device__ uint32_t k_full(int s) const { return base + 8 * (4 + s); }
+    __device__ uint32_t v_full(int s) const { return base + 8 * (8 + s); }
+    __device__ uint32_t released(int e) const { return base + 8 * (12 + (e & (kIterRing - 1))); }
+    __device__ uint32_t s_full(int t) const { return base + 8 * (20 + t); }
+    __device__ uint32_t p_full(int t) const { return base + 8 * (22 + t); }
+    __device__ uint32_t o_full(int t) const { return base + 8 * (24 + t); }
+    __device__ uint32_t v_tail(int s) const { return base + 8 * (26 + s); }
+    __device__ uint32_t tmem_slot() const { return base + 8 * 30; }
+};
+constexpr int kTmemSlotOffset = 8 * 30;
+constexpr int kAbortOffset = 8 * 31;
+
+struct Item {
+    int ord;          // position in this CTA's list
+    int s0, nseq, g;  // sequences s0 .. s0 + nseq - 1 (rows of q), KV head
+    int row, k0, k1;  // block-table row, key range (k0 a multiple of the box)
+    int part;         // which of each sequence's parts this is
+    int n0, n1;       // sequences of tiles 0 and 1
+    int nkt;          // key tiles
+    bool tail;        // the last key tile runs past k1
+};
+
+// This CTA's items, the next entry fetched while the current one runs.
+struct ItemIter {
+    const int4 *items;
+    int idx, end, ord, P;
+    int4 a0, a1;
+    __device__ ItemIter(const ShParams &p)
+        : items(p.items), idx(__ldg(p.cta_items + blockIdx.x)), end(__ldg(p.cta_items + blockIdx.x + 1)), ord(0),
+          P(p.rows_per_tile)
+    {
+        fetch();
+    }
+    __device__ bool more() const { return idx < end; }
+    __device__ void fetch()
+    {
+        if (idx < end) {
+            a0 = ptx::ld_nc_v4_now(items + 2 * idx);
+            a1 = ptx::ld_nc_v4_now(items + 2 * idx + 1);
+        }
+    }
+    __device__ Item peek() const
+    {
+        Item w;
+        w.ord = ord;
+        w.s0 = a0.x, w.nseq = a0.y, w.g = a0.z, w.row = a0.w;
+        w.k0 = a1.x, w.k1 = a1.y, w.part = a1.z;
+        w.n0 = min(P, w.nseq);
+        w.n1 = w.nseq - w.n0;
+        w.nkt = (w.k1 - w.k0 + 127) >> 7;
+        w.tail = ((w.k1 - w.k0) & 127) != 0;
+        return w;
+    }
+    __device__ Item next(bool fetch_now = true)
+    {
+        const Item w = peek();
+        ++ord;
+        ++idx;
+        if (fetch_now)
+            fetch();
+        return w;
+    }
+};
+
+struct Waiter {
+    volatile uint32_t *abort;
+    __device__ bool operator()(uint32_t bar, uint32_t parity) const
+    {
+        if (ptx::mbar_try_wait(bar, parity))
+            return true;
+        if (*abort)
+            return false;
+        if (ptx::mbar_wait(bar, parity))
+            return true;
+        *abort = 1u;
+        atomicOr(&g_shared_error, 1u);
+        return false;
+    }
+};
+
+// Release event of the key tile `back` places before global tile X, given the current item's
+// ordinal and the item-start bits of the last tiles (bit i: tile X - i opens its item).
+__device__ __forceinline__ int release_event(int X, int back, int ord, uint32_t starts, int v)
+{
+    return X - back + ord - __popc(starts & ((1u << back) - 1u)) + v;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_shared_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
+                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const ShParams p)
+{
+    using L = ShLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_u32(smem_raw);
+    const uint32_t sbase = (raw + 1023u) & ~1023u;
+    uint8_t *sgen = smem_raw + (sbase - raw);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const Bars bars{sbase + L::kBar};
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(sgen + L::kBar + kAbortOffset);
+    const Waiter wait{abort_flag};
+    const int G = p.group;
+    const int P = p.rows_per_tile;
+
+    // the combine launch may be set up now; it waits for this grid's end before it reads
+    ptx::launch_dependents();
+    if (warp >= 8 && lane == 0) {
+        if (warp == kQWarp) {
+            ptx::prefetch_tmap(&tm_q);
+            ptx::prefetch_tmap(&tm_q1);
+        } else if (warp == kKWarp) {
+            ptx::prefetch_tmap(&tm_k);
+        } else if (warp == kVWarp) {
+            ptx::prefetch_tmap(&tm_v);
+        }
+    }
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(bars.q_full(t), 1);
+            ptx::mbar_init(bars.q_free(t), 1);
+            ptx::mbar_init(bars.s_full(t), 1);
+            ptx::mbar_init(bars.p_full(t), 4);
+            ptx::mbar_init(bars.o_full(t), 1);
+        }
+        for (int s = 0; s < L::kKStages; ++s)
+            ptx::mbar_init(bars.k_full(s), 1);
+        for (int s = 0; s < L::kVStages; ++s) {
+            ptx::mbar_init(bars.v_full(s), 1);
+            ptx::mbar_init(bars.v_tail(s), 1);
+        }
+        for (int s = 0; s < kIterRing; ++s)
+            ptx::mbar_init(bars.released(s), 1);
+        *abort_flag = 0u;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(bars.tmem_slot(), kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ItemIter items(p);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sgen + L::kBar + kTmemSlotOffset);
+    auto wwait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+
+    if (warp >= 8) {
+        ptx::reg_dealloc<kOtherRegs>();
+        if (warp == kQWarp) {
+            // ------------------------------------------------------------ query producer
+            bool ok = true;
+            while (ok && items.more()) {
+                const Item w = items.next();
+                for (int t = 0; t < (w.n1 > 0 ? 2 : 1); ++t) {
+                    // Refill after the last score product of this tile that read the buffer.  A tile
+                    // that an item leaves empty is released with the item all the same, so the n-th
+                    // item waits for the (n - 1)-th release of both.  Tile 0 is waited for at every item
+                    // and before tile 1, so tile 1's barrier is at most one release behind and its
+                    // parity is not ambiguous although some items skip its wait.
+                    if (w.ord > 0 && !(ok = wwait(bars.q_free(t), (w.ord - 1) & 1)))
+                        break;
+                    if (lane == 0) {
+                        const bool one = w.nseq == 1;
+                        ptx::mbar_arrive_expect_tx(bars.q_full(t), (uint32_t)(L::kPanels * 128 * G * (one ? 1 : P)));
+                        for (int pp = 0; pp < L::kPanels; ++pp)
+                            ptx::tma_load_3d(sbase + L::kQ + t * L::kTileBytes + pp * L::kPanelBytes,
+                                             one ? &tm_q1 : &tm_q, bars.q_full(t), pp * 64, w.g * G, w.s0 + t * P);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if (warp == kKWarp || warp == kVWarp) {
+            // ------------------------------------------------------------ K and V producers
+            const bool is_k = warp == kKWarp;
+            const int nstages = is_k ? L::kKStages : L::kVStages;
+            const uint32_t ring = sbase + (is_k ? L::kK : L::kV);
+            const CUtensorMap *tm = is_k ? &tm_k : &tm_v;
+            const int bs = p.block_size;
+            const int box_rows = p.box_rows;
+            const int nsub = 128 / box_rows;
+            // cache row of sub-box `lane` of key tile j; one past the pool reads as zeros
+            auto sub_row = [&](const Item &w, const int32_t *bt, int j) -> int {
+                const int key = w.k0 + j * 128 + lane * box_rows;
+                if (lane >= nsub || key >= w.k1)
+                    return p.num_blocks * bs;
+                const int phys = __ldg(bt + key / bs);
+                if ((uint32_t)phys >= (uint32_t)p.num_blocks) {
+                    atomicOr(&g_shared_error, 2u);
+                    return p.num_blocks * bs;
+                }
+                return phys * bs + (key & (bs - 1));
+            };
+            uint32_t starts = 0;
+            int X = 0;
+            bool ok = true;
+            while (ok && items.more()) {
+                const Item w = items.next();
+                const int32_t *bt = p.block_tables + (size_t)w.row * p.max_blocks;
+                int next = sub_row(w, bt, 0);
+                for (int j = 0; j < w.nkt; ++j, ++X) {
+                    const int cur = next;
+                    if (j + 1 < w.nkt)
+                        next = sub_row(w, bt, j + 1);
+                    starts = (starts << 1) | (j == 0 ? 1u : 0u);
+                    const int st = X % nstages;
+                    if (X >= nstages) {
+                        const int e = release_event(X, nstages, w.ord, starts, is_k ? 0 : 1);
+                        if (!(ok = wwait(bars.released(e), (e / kIterRing) & 1)))
+                            break;
+                    }
+                    const uint32_t full = is_k ? bars.k_full(st) : bars.v_full(st);
+                    const uint32_t dst = ring + st * L::kTileBytes;
+                    if (lane == 0)
+                        ptx::mbar_arrive_expect_tx(full, (uint32_t)L::kTileBytes);
+                    if (lane < nsub) {
+                        for (int pp = 0; pp < L::kPanels; ++pp)
+                            ptx::tma_load_3d(dst + pp * L::kPanelBytes + lane * box_rows * 128, tm, full, pp * 64, w.g,
+                                             cur);
+                    }
+                    __syncwarp();
+                    if (!is_k && w.tail && j == w.nkt - 1) {
+                        // rows of keys past the range may hold anything (even NaN bit patterns): zeroed, so
+                        // that a weight of 0 cannot turn them into NaN
+                        if (!(ok = wwait(full, (X / nstages) & 1)))
+                            break;
+                        uint8_t *tile = sgen + L::kV + st * L::kTileBytes;
+                        const int first = w.k1 - w.k0 - j * 128;
+                        const int chunks = (128 - first) * 8;
+                        for (int pp = 0; pp < L::kPanels; ++pp)
+                            for (int c = lane; c < chunks; c += 32)
+                                *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + (first + (c >> 3)) * 128 +
+                                                           (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            ptx::mbar_arrive(bars.v_tail(st));
+                    }
+                }
+            }
+        } else if (warp == kMmaWarp) {
+            // ------------------------------------------------------------ MMA issuer (converged warp)
+            constexpr uint32_t idesc_s = ptx::idesc_bf16(128, 128, 0);
+            constexpr uint32_t idesc_o = ptx::idesc_bf16(128, D, 1);
+            const uint32_t hi_k = (uint32_t)(ptx::smem_desc(0, 16, 1024, ptx::kSwizzle128B) >> 32);
+            const uint32_t hi_v = (uint32_t)(ptx::smem_desc(0, L::kPanelBytes, 1024, ptx::kSwizzle128B) >> 32);
+            auto desc = [](uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; };
+            auto issue_s = [&](int t, int ks) {
+                uint32_t qa = (uint32_t)ptx::smem_desc(sbase + L::kQ + t * L::kTileBytes, 16, 1024, ptx::kSwizzle128B);
+                uint32_t kb = (uint32_t)ptx::smem_desc(sbase + L::kK + ks * L::kTileBytes, 16, 1024, ptx::kSwizzle128B);
+                asm volatile("" : "+r"(qa), "+r"(kb));
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = ((kk >> 2) * L::kPanelBytes + (kk & 3) * 32) >> 4;
+                    ptx::mma_bf16_ss_warp(tmem + t * 256, desc(qa + o, hi_k), desc(kb + o, hi_k), idesc_s, kk > 0);
+                }
+            };
+            auto issue_pv = [&](int t, int vs, bool first) {
+                uint32_t vb = (uint32_t)ptx::smem_desc(sbase + L::kV + vs * L::kTileBytes, L::kPanelBytes, 1024,
+                                                       ptx::kSwizzle128B);
+                asm volatile("" : "+r"(vb));
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    ptx::mma_bf16_ts_warp(tmem + t * 256 + 128, tmem + t * 256 + kk * 8,
+                                          desc(vb + kk * (2048 >> 4), hi_v), idesc_o, (!first || kk > 0) ? 1u : 0u);
+            };
+            int ks = 0, kph = 0, vs = 0, vph = 0;
+            uint32_t np = 0;      // bit t: parity of the P tiles of tile t consumed so far
+            uint32_t n1items = 0; // items with a second tile so far (its query buffer's parity)
+            uint32_t tailpar = 0; // bit s: parity of the tail tiles V slot s has held
+            int E = 0;
+            bool ok = true;
+            while (ok && items.more()) {
+                const Item w = items.next();
+                const int nt = w.n1 > 0 ? 2 : 1;
+                if (!(ok = wwait(bars.q_full(0), w.ord & 1) && wwait(bars.k_full(ks), kph)))
+                    break;
+                ptx::tc_fence_after();
+                issue_s(0, ks);
+                ptx::mma_commit_warp(bars.s_full(0));
+                if (nt == 2) {
+                    if (!(ok = wwait(bars.q_full(1), n1items & 1)))
+                        break;
+                    ++n1items;
+                    ptx::tc_fence_after();
+                    issue_s(1, ks);
+                    ptx::mma_commit_warp(bars.s_full(1));
+                }
+                ptx::mma_commit_warp(bars.released(E)); // K tile 0 read
+                if (w.nkt == 1)
+                    ptx::mma_commit_warp(bars.q_free(0));
+                if (nt == 1 || w.nkt == 1)
+                    ptx::mma_commit_warp(bars.q_free(1));
+                if (++ks == L::kKStages) {
+                    ks = 0;
+                    kph ^= 1;
+                }
+                for (int j = 0; ok && j < w.nkt; ++j) {
+                    const bool more = j + 1 < w.nkt;
+                    for (int t = 0; t < nt; ++t) { // PV(t, j), then S(t, j + 1) into the same columns
+                        if (!(ok = wwait(bars.p_full(t), (np >> t) & 1u)))
+                            break;
+                        np ^= 1u << t;
+                        if (t == 0) {
+                            if (!(ok = wwait(bars.v_full(vs), vph)))
+                                break;
+                            if (w.tail && !more) {
+                                if (!(ok = wwait(bars.v_tail(vs), (tailpar >> vs) & 1u)))
+                                    break;
+                                tailpar ^= 1u << vs;
+                            }
+                        }
+                        ptx::tc_fence_after();
+                        issue_pv(t, vs, j == 0);
+                        if (!more) {
+                            ptx::mma_commit_warp(bars.o_full(t));
+                        } else {
+                            if (t == 0) {
+                                if (!(ok = wwait(bars.k_full(ks), kph)))
+                                    break;
+                                ptx::tc_fence_after();
+                            }
+                            issue_s(t, ks);
+                            ptx::mma_commit_warp(bars.s_full(t));
+                            if (j + 2 == w.nkt)
+                                ptx::mma_commit_warp(bars.q_free(t));
+                        }
+                    }
+                    if (!ok)
+                        break;
+                    ptx::mma_commit_warp(bars.released(E + j + 1));
+                    if (++vs == L::kVStages) {
+                        vs = 0;
+                        vph ^= 1;
+                    }
+                    if (more && ++ks == L::kKStages) {
+                        ks = 0;
+                        kph ^= 1;
+                    }
+                }
+                E += w.nkt + 1;
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- softmax + epilogue
+        ptx::reg_alloc<kSoftmaxRegs>();
+        const int t = warp >> 2;
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane;
+        const int rpos = r / G, rhead = r % G;
+        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_col = tmem + lane_addr + t * 256;
+        const uint32_t o_col = s_col + 128;
+        const float sl2 = p.scale_log2;
+        uint32_t ns = 0, no = 0;
+        bool ok = true;
+        while (ok && items.more()) {
+            const Item w = items.next(false);
+            const int nseq = t == 0 ? w.n0 : w.n1;
+            if (nseq == 0) {
+                items.fetch();
+                continue;
+            }
+            const bool row_valid = r < G * nseq;
+            const bool warp_valid = quarter * 32 < G * nseq;
+            float m_ref = -INFINITY, l_sum = 0.f;
+            for (int j = 0; j < w.nkt; ++j) {
+                if (!(ok = wwait(bars.s_full(t), ns & 1)))
+                    break;
+                ns ^= 1;
+                if (warp_valid) {
+                    ptx::tc_fence_after();
+                    const int lim = w.k1 - w.k0 - j * 128; // keys of this tile (128 or more: all)
+                    uint32_t sr[128];
+                    float mx;
+                    if (lim < 128) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            ptx::tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            sr[c] = c < lim ? sr[c] : __float_as_uint(-INFINITY);
+                        float m8[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            m8[i] = ptx::max3(__uint_as_float(sr[16 * i]), __uint_as_float(sr[16 * i + 1]),
+                                              __uint_as_float(sr[16 * i + 2]));
+#pragma unroll
+                        for (int c = 3; c < 16; c += 2)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                m8[i] = c + 1 < 16 ? ptx::max3(m8[i], __uint_as_float(sr[16 * i + c]),
+                                                               __uint_as_float(sr[16 * i + c + 1]))
+                                                   : fmaxf(m8[i], __uint_as_float(sr[16 * i + c]));
+                        mx = fmaxf(fmaxf(ptx::max3(m8[0], m8[1], m8[2]), ptx::max3(m8[3], m8[4], m8[5])),
+                                   fmaxf(m8[6], m8[7]));
+                    } else {
+                        float m4[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            m4[q] = ptx::tmem_ld32_max(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
+                        ptx::tmem_wait_ld();
+                        mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    }
+                    const float mt = mx * sl2;
+                    float alpha = 1.f;
+                    bool rescale = false;
+                    if (row_valid && (mt > m_ref + kRescaleThreshold || (m_ref == -INFINITY && mt != -INFINITY))) {
+                        const float m_new = fmaxf(m_ref, mt);
+                        alpha = ptx::ex2(m_ref - m_new); // 0 on the first tile
+                        rescale = j > 0;
+                        l_sum *= alpha;
+                        m_ref = m_new;
+                    }
+                    // P = 2^(s * scale * log2 e - m) as bf16 pairs written over S (weights in [0, 2^8], rounded
+                    // to the values' own type: half an ulp, 2^-9 of each weight); the row sum stays fp32
+                    const uint64_t sl2x2 = ptx::f2(sl2, sl2);
+                    const float negm = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const uint64_t negm2 = ptx::f2(negm, negm);
+                    uint64_t sum2[4] = {ptx::f2(0.f, 0.f), ptx::f2(0.f, 0.f), ptx::f2(0.f, 0.f), ptx::f2(0.f, 0.f)};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int c = 64 * h; c < 64 * h + 64; c += 2) {
+                            float x0, x1;
+                            ptx::f2_split(ptx::f2_fma(ptx::f2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])),
+                                                      sl2x2, negm2),
+                                          x0, x1);
+                            const float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1); // masked columns: 2^-inf = 0
+                            sum2[(c >> 1) & 3] = ptx::f2_add(sum2[(c >> 1) & 3], ptx::f2(e0, e1));
+                            pk[(c >> 1) & 31] = ptx::pack_bf16(e0, e1);
+                        }
+                        ptx::tmem_st32(s_col + 32 * h, pk);
+                    }
+                    float s0, s1, s2, s3, s4, s5, s6, s7;
+                    ptx::f2_split(sum2[0], s0, s1);
+                    ptx::f2_split(sum2[1], s2, s3);
+                    ptx::f2_split(sum2[2], s4, s5);
+                    ptx::f2_split(sum2[3], s6, s7);
+                    l_sum += ((s0 + s1) + (s2 + s3)) + ((s4 + s5) + (s6 + s7));
+                    // O is stable here: PV(j-1) completed before S(j) did (in-order products), and PV(j)
+                    // waits for the arrival below
+                    if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+                        for (int cc = 0; cc < D / 32; ++cc) {
+                            uint32_t o[32];
+                            ptx::tmem_ld32(o_col + cc * 32, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                            ptx::tmem_st32(o_col + cc * 32, o);
+                        }
+                    }
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(bars.p_full(t));
+            }
+            items.fetch();
+            if (!ok)
+                break;
+            // epilogue: O / l to the output (a sequence's only part) or, in fp32 with its log2-sum-exp,
+            // to the workspace
+            if (!(ok = wwait(bars.o_full(t), no & 1)))
+                break;
+            no ^= 1;
+            if (!warp_valid)
+                continue;
+            ptx::tc_fence_after();
+            const float inv = (row_valid && l_sum > 0.f) ? 1.f / l_sum : 0.f;
+            const int seq = w.s0 + t * P + rpos;
+            const size_t head = (size_t)w.g * G + rhead;
+            // first slot and number of parts of this row's sequence (an item's sequences may differ: one
+            // whose context ends with the prefix has no suffix part)
+            const int2 sp = row_valid ? __ldg(p.seq_parts + seq) : make_int2(0, 1);
+            const bool partial = sp.y > 1;
+            const size_t slot = (size_t)sp.x + w.part;
+            float *po = p.part_o + (slot * p.num_heads + head) * D;
+            if (partial && !*abort_flag)
+                p.part_lse[slot * p.num_heads + head] = l_sum > 0.f ? m_ref + __log2f(l_sum) : -INFINITY;
+            __nv_bfloat16 *orow = p.out + ((size_t)seq * p.num_heads + head) * D;
+            uint32_t o[D / 32][32];
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc)
+                ptx::tmem_ld32(o_col + cc * 32, o[cc]);
+            ptx::tmem_wait_ld();
+            if (row_valid && !*abort_flag) {
+                if (partial) {
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc)
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                x[i] = __float_as_uint(__uint_as_float(o[cc][c + i]) * inv);
+                            ptx::st_global_v8(po + cc * 32 + c, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
+                        }
+                } else {
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; ++cc)
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                x[i] = ptx::pack_bf16(__uint_as_float(o[cc][c + 2 * i]) * inv,
+                                                      __uint_as_float(o[cc][c + 2 * i + 1]) * inv);
+                            *reinterpret_cast<uint4 *>(orow + cc * 32 + c) = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                }
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// out[b][h] = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over the parts of sequence b: none
+// (empty context) writes zeros, one was written by its work item.  One warp per (sequence,
+// head), D/32 values per lane, kBatch parts' loads in flight, summed in part order.
+template <int D>
+__global__ void __launch_bounds__(128) shared_combine_kernel(const float *__restrict__ part_o,
+                                                             const float *__restrict__ part_lse,
+                                                             const int2 *__restrict__ seq_parts,
+                                                             __nv_bfloat16 *__restrict__ out, int num_heads)
+{
+    constexpr int E = D / 32;
+    constexpr int kBatch = 8;
+    const int b = blockIdx.x;
+    const int h = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int2 sp = __ldg(seq_parts + b); // the plan's, written long before this launch's predecessor
+    ptx::grid_dependency_wait();          // the parts are complete and visible
+    const int n = sp.y;
+    if (n == 1 || h >= num_heads)
+        return;
+    const float *lse = part_lse + (size_t)sp.x * num_heads + h;
+    const float *po = part_o + ((size_t)sp.x * num_heads + h) * D + lane * E;
+    const size_t o_stride = (size_t)num_heads * D;
+    float M = -INFINITY;
+    for (int s = lane; s < n; s += 32)
+        M = fmaxf(M, lse[(size_t)s * num_heads]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        acc[e] = 0.f;
+    float W = 0.f;
+    for (int s = 0; s < n; s += kBatch) {
+        float l[kBatch];
+        float o[kBatch][E];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (s + i < n) {
+                l[i] = lse[(size_t)(s + i) * num_heads];
+                if constexpr (E == 4)
+                    *reinterpret_cast<float4 *>(o[i]) = *reinterpret_cast<const float4 *>(po + (size_t)(s + i) * o_stride);
+                else
+                    *reinterpret_cast<float2 *>(o[i]) = *reinterpret_cast<const float2 *>(po + (size_t)(s + i) * o_stride);
+            }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (s + i < n) {
+                const float w = l[i] == -INFINITY ? 0.f : ptx::ex2(l[i] - M);
+                W += w;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    acc[e] += w * o[i][e];
+            }
+    }
+    const float inv = W > 0.f ? 1.f / W : 0.f;
+    uint32_t x[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e)
+        x[e] = ptx::pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(out + ((size_t)b * num_heads + h) * D + lane * E);
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(x[0], x[1]);
+    else
+        dst[0] = x[0];
+}
+
+template <int D>
+int launch(const SharedArgs &a, cudaStream_t stream)
+{
+    using L = ShLayout<D>;
+    if (int rc = ensure_smem<decode_shared_kernel<D>>(L::kSmemBytes, "shared decode"))
+        return rc;
+    static std::atomic<int> launch_regs{0};
+    int nreg = launch_regs.load(std::memory_order_acquire);
+    if (nreg == 0) {
+        cudaFuncAttributes fa{};
+        const cudaError_t e = cudaFuncGetAttributes(&fa, decode_shared_kernel<D>);
+        if (e != cudaSuccess)
+            return fail(PA_ERR_CUDA, "shared decode kernel attributes: %s", cudaGetErrorString(e));
+        launch_regs.store(nreg = fa.numRegs, std::memory_order_release);
+    }
+    if (nreg != kLaunchRegs)
+        return fail(PA_ERR_UNSUPPORTED, "shared decode kernel built with %d registers per thread, needs %d", nreg,
+                    kLaunchRegs);
+    const pa_dims &d = a.dims;
+    const int G = d.num_heads / d.num_kv_heads;
+    if (a.num_items > 0) {
+        const uint64_t rows = (uint64_t)d.num_blocks * d.block_size;
+        const uint32_t box_rows = d.block_size < 128 ? (uint32_t)d.block_size : 128u;
+        constexpr CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+        const uint64_t qs = (uint64_t)d.num_heads * D * 2, cs = (uint64_t)d.num_kv_heads * D * 2;
+        CUtensorMap tq, tq1, tk, tv;
+        int rc;
+        if ((rc = encode_tmap_3d(&tq, bf16, a.q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
+                                 (uint32_t)G, (uint32_t)a.rows_per_tile, sw, "q")) != PA_OK ||
+            (rc = encode_tmap_3d(&tq1, bf16, a.q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
+                                 (uint32_t)G, 1, sw, "q")) != PA_OK ||
+            (rc = encode_tmap_3d(&tk, bf16, a.k_cache, D, d.num_kv_heads, rows, (uint64_t)D * 2, cs, 64, 1, box_rows,
+                                 sw, "k_cache")) != PA_OK ||
+            (rc = encode_tmap_3d(&tv, bf16, a.v_cache, D, d.num_kv_heads, rows, (uint64_t)D * 2, cs, 64, 1, box_rows,
+                                 sw, "v_cache")) != PA_OK)
+            return rc;
+        ShParams p{};
+        p.items = reinterpret_cast<const int4 *>(a.items);
+        p.cta_items = a.cta_items;
+        p.seq_parts = reinterpret_cast<const int2 *>(a.seq_parts);
+        p.block_tables = a.block_tables;
+        p.out = static_cast<__nv_bfloat16 *>(a.out);
+        p.part_o = a.part_o;
+        p.part_lse = a.part_lse;
+        p.scale_log2 = a.scale * kLog2e;
+        p.num_heads = d.num_heads;
+        p.group = G;
+        p.rows_per_tile = a.rows_per_tile;
+        p.block_size = d.block_size;
+        p.box_rows = (int32_t)box_rows;
+        p.max_blocks = a.max_blocks_per_seq;
+        p.num_blocks = d.num_blocks;
+        decode_shared_kernel<D><<<(unsigned)a.num_ctas, kThreads, L::kSmemBytes, stream>>>(tq, tq1, tk, tv, p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess)
+            return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
+    }
+    if (!a.combine)
+        return PA_OK;
+    // Programmatic launch: the combine's blocks are set up while the parts still run and wait
+    // inside for the end of that grid.  Without a grid before it, it waits for nothing.
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)a.num_seqs, (unsigned)((d.num_heads + 3) / 4));
+    cfg.blockDim = dim3(128);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = a.num_items > 0 ? 1 : 0;
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, shared_combine_kernel<D>, (const float *)a.part_o, (const float *)a.part_lse,
+                           reinterpret_cast<const int2 *>(a.seq_parts), static_cast<__nv_bfloat16 *>(a.out),
+                           (int)d.num_heads);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PA_ERR_CUDA, "shared decode combine launch: %s", cudaGetErrorString(e));
+    }
+    return PA_OK;
+}
+
+} // namespace
+
+int launch_decode_shared(const SharedArgs &a, void *stream)
+{
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return a.dims.head_dim == 128 ? launch<128>(a, s) : launch<64>(a, s);
+}
+
+int read_shared_error(uint32_t *code)
+{
+    uint32_t v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_shared_error, sizeof v);
+    if (e == cudaSuccess)
+        e = cudaMemcpyToSymbol(g_shared_error, &zero, sizeof zero);
+    if (e != cudaSuccess)
+        return fail(PA_ERR_CUDA, "reading shared-decode error word: %s", cudaGetErrorString(e));
+    *code |= (v & 3u) << 5;
+    return PA_OK;
+}
+
+} // namespace pa

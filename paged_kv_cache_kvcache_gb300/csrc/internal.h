@@ -23,6 +23,8 @@ constexpr int kPrefillItemInts = 8;
 constexpr int kDecodeChunk = 16;
 constexpr int kDecodeStep = 64;
 constexpr int kMaxGroup = 16;
+// work-list entry of the shared-prefix decode (see pa_shared_meta)
+constexpr int kSharedItemInts = 8;
 
 // Thread-local error text.
 void set_error(const char *fmt, ...);
@@ -32,6 +34,25 @@ int fail(int code, const char *fmt, ...);
 int check_dims(const pa_dims *dims);
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// ---- host packing (pack.cpp, pack_shared.cpp)
+// Offsets of a metadata image's arrays, 256-byte aligned.
+struct Layout {
+    size_t off = 0;
+    size_t take(size_t bytes)
+    {
+        size_t o = off;
+        off = align_up(off + bytes, 256);
+        return o;
+    }
+};
+
+// Every sequence has ceil(len / block_size) block ids inside the pool; *max_blocks = the most (at least 1).
+int check_seq_blocks(const pa_dims &d, int32_t num_seqs, const int32_t *lens, const int32_t *block_offsets,
+                     const int32_t *block_ids, int32_t *max_blocks);
+// Rows of mb ids, -1 padded.
+void write_block_tables(const pa_dims &d, int32_t num_seqs, const int32_t *lens, const int32_t *block_offsets,
+                        const int32_t *block_ids, int32_t mb, int32_t *bt);
 
 // Raise a kernel's dynamic shared-memory limit once per device (the attribute is
 // per device; a process may drive several GPUs).  One flag word per kernel.
@@ -164,6 +185,31 @@ int launch_decode_int8(const DecodeArgs &a, void *stream);
 // LSE merge of the split partials into out (no-op for plans without partials).
 int launch_decode_combine(const DecodeArgs &a, void *stream);
 
+// Shared-prefix decode (see pa_shared_meta for the plan's arrays).
+struct SharedArgs {
+    pa_dims dims;
+    const void *q;
+    const void *k_cache;
+    const void *v_cache;
+    const void *k_scale; // INT8 cache only
+    const void *v_scale;
+    const int32_t *block_tables;
+    const int32_t *items;
+    const int32_t *cta_items;
+    const int32_t *seq_parts;
+    void *out;
+    float *part_o;   // [num_partials][Hq][D]
+    float *part_lse; // [num_partials][Hq]
+    float scale;
+    int32_t num_seqs;
+    int32_t num_items;
+    int32_t num_ctas;
+    int32_t rows_per_tile;
+    int32_t max_blocks_per_seq;
+    bool combine; // some sequence has two or more parts, or none
+};
+int launch_decode_shared(const SharedArgs &a, void *stream);
+
 // Device address of the library-owned decode scratch on the current device
 // (looked up once per device).  Used only by pa_decode_static.
 int decode_static_scratch(void **ptr);
@@ -183,6 +229,7 @@ int read_copy_error(uint32_t *code);
 int read_decode_error(uint32_t *code);
 int read_fused_error(uint32_t *code);
 int read_fused8_error(uint32_t *code);
+int read_shared_error(uint32_t *code); // bit 0 -> 5 (wait), bit 1 -> 6 (block id outside the pool)
 int launch_selftest_wait(uint32_t timeout_us, int arrive_first, void *stream);
 int read_selftest_error(uint32_t *code);
 int launch_stream_read(const void *src, size_t bytes, uint32_t *sink, void *stream);

@@ -24,17 +24,6 @@
 #include "internal.h"
 
 namespace pa {
-namespace {
-
-struct Layout {
-    size_t off = 0;
-    size_t take(size_t bytes)
-    {
-        size_t o = off;
-        off = align_up(off + bytes, 256);
-        return o;
-    }
-};
 
 int check_seq_blocks(const pa_dims &d, int32_t num_seqs, const int32_t *lens, const int32_t *block_offsets,
                      const int32_t *block_ids, int32_t *max_blocks)
@@ -77,7 +66,6 @@ void write_block_tables(const pa_dims &d, int32_t num_seqs, const int32_t *lens,
     }
 }
 
-} // namespace
 } // namespace pa
 
 using namespace pa;

@@ -1,0 +1,355 @@
+// Host-side plan of the shared-prefix decode: key ranges, work items, their CTAs.
+//
+// Sources: as pack.cpp (metadata is built on the CPU next to the scheduling loop and uploaded
+// with one copy); "vLLM / SGLang 面试源码深挖", section 4 (forked sequences name the same
+// blocks) for what is shared.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <queue>
+#include <vector>
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace pa {
+namespace {
+
+constexpr int32_t kTile = kPrefillKeyTile;
+
+// Time model of the kernel in microseconds on one SM, used only to choose the key ranges and
+// to deal the items out (measured on GB300, D = 128): an iteration of 128 keys with two query
+// tiles is bound by the tensor core, with one by the loads of K and V; an item adds its query
+// load and its output.  The merge reads and writes every partial once at HBM speed.
+constexpr float kPairStep = 1.75f, kSingleStep = 1.25f, kItemCost = 1.5f, kMergeBytesPerUs = 5.0e6f;
+
+struct Run { // consecutive sequences of a group that share `shared` tokens
+    int32_t s0, n, shared;
+};
+
+struct Range { // one part of a context: units items per split
+    int32_t tiles, units_pair, units_single;
+};
+
+float item_cost(int32_t tiles, bool pair) { return (float)tiles * (pair ? kPairStep : kSingleStep) + kItemCost; }
+
+struct Work {
+    int32_t s0, n, g, row, k0, k1, part;
+    float cost;
+};
+
+int32_t splits_of(int32_t tiles, int32_t per) { return (tiles + per - 1) / per; }
+
+} // namespace
+} // namespace pa
+
+using namespace pa;
+
+static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32_t *context_lens,
+                              int32_t num_groups, const int32_t *group_offsets, const int32_t *shared_lens,
+                              const int32_t *block_offsets, const int32_t *block_ids, const int32_t *table_rows,
+                              int32_t max_blocks_per_seq, int32_t split_tokens, void *host_buf, size_t host_buf_bytes,
+                              pa_shared_meta *meta)
+{
+    int rc = check_dims(dims);
+    if (rc != PA_OK)
+        return rc;
+    if (!meta)
+        return fail(PA_ERR_INVALID_ARG, "meta is NULL");
+    if (num_seqs < 0 || num_groups < 0)
+        return fail(PA_ERR_INVALID_ARG, "num_seqs or num_groups < 0");
+    if (num_seqs > 0 && (!context_lens || !group_offsets))
+        return fail(PA_ERR_INVALID_ARG, "context_lens/group_offsets is NULL");
+    if (split_tokens < 0 || split_tokens % kTile != 0)
+        return fail(PA_ERR_INVALID_ARG, "split_tokens (%d) must be 0 or a positive multiple of %d", split_tokens, kTile);
+    const pa_dims &d = *dims;
+    const int32_t bs = d.block_size;
+    if (num_seqs > 0) {
+        if (group_offsets[0] != 0 || group_offsets[num_groups] != num_seqs)
+            return fail(PA_ERR_INVALID_ARG, "group_offsets must start at 0 and end at num_seqs (%d)", num_seqs);
+        for (int32_t i = 0; i < num_groups; ++i)
+            if (group_offsets[i + 1] < group_offsets[i])
+                return fail(PA_ERR_INVALID_ARG, "group_offsets not non-decreasing at group %d", i);
+    }
+    int32_t max_ctx = 0;
+    for (int32_t b = 0; b < num_seqs; ++b) {
+        if (context_lens[b] < 0)
+            return fail(PA_ERR_INVALID_ARG, "context_lens[%d] < 0", b);
+        if ((int64_t)context_lens[b] > (int64_t)INT32_MAX - 2 * kTile)
+            return fail(PA_ERR_INVALID_ARG, "context_lens[%d] too long", b);
+        max_ctx = std::max(max_ctx, context_lens[b]);
+    }
+    const bool packed = block_offsets != nullptr;
+    int32_t mb = 1;
+    if (packed) {
+        if (table_rows)
+            return fail(PA_ERR_INVALID_ARG, "table_rows goes with device tables: block lists give each sequence a row");
+        if (num_seqs > 0 &&
+            (rc = check_seq_blocks(d, num_seqs, context_lens, block_offsets, block_ids, &mb)) != PA_OK)
+            return rc;
+    } else if (num_seqs > 0) {
+        if (!shared_lens)
+            return fail(PA_ERR_INVALID_ARG, "shared_lens is NULL: without block lists it cannot be found");
+        mb = max_blocks_per_seq;
+        const int64_t need = ((int64_t)max_ctx + bs - 1) / bs;
+        if (mb < 1 || need > mb)
+            return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq (%d) must be positive and hold %lld blocks", mb,
+                        (long long)need);
+        if (table_rows)
+            for (int32_t b = 0; b < num_seqs; ++b)
+                if (table_rows[b] < 0)
+                    return fail(PA_ERR_INVALID_ARG, "table_rows[%d] < 0", b);
+    }
+    if (max_ctx > 0 && d.num_blocks == 0)
+        return fail(PA_ERR_INVALID_ARG, "empty KV pool");
+
+    // runs: a group's sequences with a context, consecutive ones together (entries of context 0
+    // take no part and end a run)
+    const int group = d.num_heads / d.num_kv_heads;
+    const int32_t P = std::max(1, kPrefillRows / group);
+    std::vector<Run> runs;
+    std::vector<int32_t> seq_shared(num_seqs, 0); // shared tokens of each sequence
+    for (int32_t i = 0; num_seqs > 0 && i < num_groups; ++i) {
+        const int32_t b0 = group_offsets[i], b1 = group_offsets[i + 1];
+        int32_t live = 0, least = INT32_MAX, first = -1;
+        for (int32_t b = b0; b < b1; ++b)
+            if (context_lens[b] > 0) {
+                ++live;
+                least = std::min(least, context_lens[b]);
+                first = first < 0 ? b : first;
+            }
+        if (live == 0)
+            continue;
+        const int32_t most = least / bs * bs; // whole blocks that every sequence of the group fills
+        int32_t shared = shared_lens ? shared_lens[i] : most;
+        if (shared_lens && (shared < 0 || shared % bs != 0 || shared > most))
+            return fail(PA_ERR_INVALID_ARG,
+                        "shared_lens[%d] = %d must be a multiple of the block size in [0, %d], the whole blocks of the "
+                        "group's shortest context",
+                        i, shared, most);
+        if (packed)
+            for (int32_t b = b0; b < b1; ++b) {
+                if (context_lens[b] == 0)
+                    continue;
+                const int32_t *x = block_ids + block_offsets[first], *y = block_ids + block_offsets[b];
+                int32_t n = 0;
+                while (n < shared / bs && x[n] == y[n])
+                    ++n;
+                if (shared_lens && n < shared / bs)
+                    return fail(PA_ERR_INVALID_ARG, "sequence %d does not share block %d of its group's %d", b, n,
+                                shared / bs);
+                shared = n * bs;
+            }
+        if (live == 1)
+            shared = 0; // one sequence shares nothing: its context is one part
+        for (int32_t b = b0; b < b1;) {
+            if (context_lens[b] == 0) {
+                ++b;
+                continue;
+            }
+            int32_t e = b;
+            while (e < b1 && context_lens[e] > 0)
+                seq_shared[e++] = shared;
+            runs.push_back({b, e - b, shared});
+            b = e;
+        }
+    }
+
+    // choose the key tiles per item: the least of a few candidates' estimated time
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaGetLastError();
+    std::vector<Range> ranges;
+    std::vector<int32_t> range_seqs; // sequences that get a slot per split of the range
+    for (const Run &r : runs) {
+        if (r.shared > 0) {
+            const int32_t pairs = r.n / (2 * P), rest = r.n % (2 * P);
+            ranges.push_back({(r.shared + kTile - 1) / kTile, (pairs + (rest > P)) * d.num_kv_heads,
+                              (rest > 0 && rest <= P ? 1 : 0) * d.num_kv_heads});
+            range_seqs.push_back(r.n);
+        }
+        for (int32_t b = r.s0; b < r.s0 + r.n; ++b)
+            if (context_lens[b] > r.shared) {
+                ranges.push_back({(context_lens[b] - r.shared + kTile - 1) / kTile, 0, d.num_kv_heads});
+                range_seqs.push_back(1);
+            }
+    }
+    int32_t per = split_tokens / kTile;
+    if (per == 0) {
+        static const int32_t kPer[] = {1, 2, 3, 4, 6, 8, 11, 16, 22, 32, 45, 64, 90, 128, 181, 256, 512, 1 << 24};
+        float best = INFINITY;
+        const float slot_us = (float)d.num_heads * d.head_dim * 8.f / kMergeBytesPerUs;
+        for (int32_t c : kPer) {
+            float work = 0.f, longest = 0.f, slots = 0.f;
+            int64_t items = 0;
+            for (size_t i = 0; i < ranges.size(); ++i) {
+                const Range &x = ranges[i];
+                const int32_t s = splits_of(x.tiles, c), len = splits_of(x.tiles, s);
+                const float whole = (float)x.tiles;
+                if (x.units_pair)
+                    longest = std::max(longest, item_cost(len, true));
+                if (x.units_single)
+                    longest = std::max(longest, item_cost(len, false));
+                work += x.units_pair * (whole * kPairStep + s * kItemCost) +
+                        x.units_single * (whole * kSingleStep + s * kItemCost);
+                items += (int64_t)s * (x.units_pair + x.units_single);
+                slots += (float)s * range_seqs[i];
+            }
+            // list scheduling ends at most one item late; with few items per SM that is what counts
+            const float even = work / sms;
+            const float t = (items <= sms ? longest : std::max(longest, even + 0.5f * longest)) + slots * slot_us;
+            if (t < best) {
+                best = t;
+                per = c;
+            }
+        }
+        per = std::max(per, 1);
+    }
+
+    // items and partial slots
+    std::vector<Work> works;
+    std::vector<int32_t> parts(num_seqs, 0); // parts of each sequence
+    for (const Run &r : runs) {
+        const int32_t ptiles = (r.shared + kTile - 1) / kTile;
+        const int32_t ps = ptiles > 0 ? splits_of(ptiles, per) : 0;
+        for (int32_t b = r.s0; b < r.s0 + r.n; ++b) {
+            const int32_t t = (context_lens[b] - r.shared + kTile - 1) / kTile;
+            parts[b] = ps + (t > 0 ? splits_of(t, per) : 0);
+        }
+    }
+    auto cut = [&](int32_t s0, int32_t n, int32_t row, int32_t from, int32_t to, int32_t first_part) {
+        const int32_t tiles = (to - from + kTile - 1) / kTile;
+        const int32_t s = splits_of(tiles, per);
+        for (int32_t i = 0; i < s; ++i) {
+            const int32_t t0 = (int32_t)((int64_t)tiles * i / s), t1 = (int32_t)((int64_t)tiles * (i + 1) / s);
+            const int32_t k0 = from + t0 * kTile, k1 = std::min(to, from + t1 * kTile);
+            for (int32_t g = 0; g < d.num_kv_heads; ++g)
+                for (int32_t q = 0; q < n; q += 2 * P) {
+                    const int32_t m = std::min(n - q, 2 * P);
+                    works.push_back({s0 + q, m, g, row, k0, k1, first_part + i, item_cost(t1 - t0, m > P)});
+                }
+        }
+    };
+    for (const Run &r : runs) {
+        const int32_t ptiles = (r.shared + kTile - 1) / kTile;
+        const int32_t ps = ptiles > 0 ? splits_of(ptiles, per) : 0;
+        if (ps > 0)
+            cut(r.s0, r.n, table_rows ? table_rows[r.s0] : r.s0, 0, r.shared, 0);
+        for (int32_t b = r.s0; b < r.s0 + r.n; ++b)
+            if (context_lens[b] > r.shared)
+                cut(b, 1, table_rows ? table_rows[b] : b, r.shared, context_lens[b], ps);
+    }
+    if (works.size() > (size_t)INT32_MAX / kSharedItemInts)
+        return fail(PA_ERR_INVALID_ARG, "too many work items");
+    int64_t partials = 0;
+    int32_t max_parts = 0;
+    bool combine = false;
+    for (int32_t b = 0; b < num_seqs; ++b) {
+        max_parts = std::max(max_parts, parts[b]);
+        partials += parts[b] > 1 ? parts[b] : 0;
+        combine = combine || parts[b] != 1;
+    }
+    if (partials > INT32_MAX)
+        return fail(PA_ERR_INVALID_ARG, "too many partial results");
+    const int32_t ctas = (int32_t)std::min<size_t>(works.size(), (size_t)sms);
+
+    Layout L;
+    *meta = pa_shared_meta{};
+    meta->num_seqs = num_seqs;
+    meta->num_groups = num_groups;
+    meta->max_blocks_per_seq = mb;
+    meta->num_items = (int32_t)works.size();
+    meta->num_ctas = ctas;
+    meta->num_partials = (int32_t)partials;
+    meta->max_parts = max_parts;
+    meta->rows_per_tile = P;
+    meta->combine = combine ? 1 : 0;
+    meta->split_tokens = (int32_t)std::min<int64_t>((int64_t)per * kTile, INT32_MAX / kTile * kTile);
+    meta->tables_packed = packed ? 1 : 0;
+    for (const Run &r : runs)
+        meta->tokens_saved += (uint64_t)r.shared * (uint64_t)(r.n - 1);
+    meta->off_block_tables = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs * mb : 0);
+    meta->off_slot_mapping = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs : 0);
+    meta->off_items = L.take(sizeof(int32_t) * kSharedItemInts * works.size());
+    meta->off_cta_items = L.take(sizeof(int32_t) * ((size_t)ctas + 1));
+    meta->off_seq_parts = L.take(sizeof(int32_t) * 2 * (size_t)num_seqs);
+    meta->total_bytes = L.off;
+    meta->workspace_bytes = partials > 0 ? align_up((size_t)partials * d.num_heads * d.head_dim * 4, 256) +
+                                               align_up((size_t)partials * d.num_heads * 4, 256)
+                                         : 0;
+    if (!host_buf)
+        return PA_OK;
+    if (host_buf_bytes < meta->total_bytes)
+        return fail(PA_ERR_WORKSPACE, "metadata buffer has %zu bytes, needs %llu", host_buf_bytes,
+                    (unsigned long long)meta->total_bytes);
+
+    char *base = static_cast<char *>(host_buf);
+    int32_t *it = reinterpret_cast<int32_t *>(base + meta->off_items);
+    int32_t *ci = reinterpret_cast<int32_t *>(base + meta->off_cta_items);
+    int32_t *sp = reinterpret_cast<int32_t *>(base + meta->off_seq_parts);
+    if (packed && num_seqs > 0) {
+        write_block_tables(d, num_seqs, context_lens, block_offsets, block_ids, mb,
+                           reinterpret_cast<int32_t *>(base + meta->off_block_tables));
+        int32_t *slots = reinterpret_cast<int32_t *>(base + meta->off_slot_mapping);
+        for (int32_t b = 0; b < num_seqs; ++b) {
+            const int32_t pos = context_lens[b] - 1;
+            slots[b] = pos < 0 ? -1 : block_ids[block_offsets[b] + pos / bs] * bs + pos % bs;
+        }
+    }
+    for (int32_t b = 0, slot = 0; b < num_seqs; ++b) {
+        sp[2 * b] = slot;
+        sp[2 * b + 1] = parts[b];
+        slot += parts[b] > 1 ? parts[b] : 0;
+    }
+    // deal out: longest first, each to the CTA with the least work so far
+    std::vector<int32_t> order(works.size()), cta_of(works.size()), fill((size_t)ctas + 1, 0);
+    for (size_t i = 0; i < order.size(); ++i)
+        order[i] = (int32_t)i;
+    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return works[x].cost > works[y].cost; });
+    using Load = std::pair<float, int32_t>;
+    std::priority_queue<Load, std::vector<Load>, std::greater<Load>> heap;
+    for (int32_t c = 0; c < ctas; ++c)
+        heap.push({0.f, c});
+    for (int32_t i : order) {
+        Load l = heap.top();
+        heap.pop();
+        cta_of[i] = l.second;
+        ++fill[(size_t)l.second + 1];
+        l.first += works[i].cost;
+        heap.push(l);
+    }
+    ci[0] = 0;
+    for (int32_t c = 0; c < ctas; ++c)
+        ci[c + 1] = ci[c] + fill[(size_t)c + 1];
+    std::vector<int32_t> at(ci, ci + ctas);
+    for (int32_t i : order) {
+        const Work &w = works[i];
+        int32_t *e = it + (size_t)kSharedItemInts * at[cta_of[i]]++;
+        e[0] = w.s0;
+        e[1] = w.n;
+        e[2] = w.g;
+        e[3] = w.row;
+        e[4] = w.k0;
+        e[5] = w.k1;
+        e[6] = w.part;
+        e[7] = 0;
+    }
+    return PA_OK;
+}
+
+extern "C" int pa_pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32_t *context_lens,
+                                     int32_t num_groups, const int32_t *group_offsets, const int32_t *shared_lens,
+                                     const int32_t *block_offsets, const int32_t *block_ids, const int32_t *table_rows,
+                                     int32_t max_blocks_per_seq, int32_t split_tokens, void *host_buf,
+                                     size_t host_buf_bytes, pa_shared_meta *meta)
+{
+    try { // no exception (out of memory) leaves a C entry point
+        return pack_decode_shared(dims, num_seqs, context_lens, num_groups, group_offsets, shared_lens, block_offsets,
+                                  block_ids, table_rows, max_blocks_per_seq, split_tokens, host_buf, host_buf_bytes,
+                                  meta);
+    } catch (...) {
+        return fail(PA_ERR_WORKSPACE, "pa_pack_decode_shared: out of host memory");
+    }
+}

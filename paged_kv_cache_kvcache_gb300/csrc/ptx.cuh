@@ -21,6 +21,14 @@ __device__ __forceinline__ uint64_t globaltimer()
     return t;
 }
 
+// ------------------------------------------------------------------ programmatic launch
+
+// Lets the next launch of the stream, if it was launched to allow that, be set up now.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the launches this one depends on are complete and their writes visible (at once
+// for an ordinary launch).
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)

@@ -24,6 +24,7 @@ EXPORTS = ("pa_pack_prefill", "pa_pack_decode", "pa_upload", "pa_store_kvcache",
            "pa_decode", "pa_decode_static", "pa_copy_blocks", "pa_store_kvcache_int8", "pa_decode_int8",
            "pa_prefill_varlen_int8", "pa_pack_decode_fixed", "pa_decode_fused", "pa_copy_blocks_int8",
            "pa_decode_int8_fused", "pa_prefill_varlen_fused", "pa_prefill_varlen_int8_fused",
+           "pa_pack_decode_shared", "pa_decode_shared",
            "pa_last_error_string", "pa_read_device_error", "pa_selftest_bounded_wait", "pa_stream_read",
            "pa_version")
 
@@ -53,6 +54,17 @@ class pa_decode_meta(ctypes.Structure):
                 ("num_partials", ctypes.c_int32), ("off_context_lens", ctypes.c_uint64),
                 ("off_block_tables", ctypes.c_uint64), ("off_slot_mapping", ctypes.c_uint64),
                 ("off_items", ctypes.c_uint64), ("off_seq_items", ctypes.c_uint64),
+                ("total_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class pa_shared_meta(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+                ("num_items", ctypes.c_int32), ("num_ctas", ctypes.c_int32), ("num_partials", ctypes.c_int32),
+                ("max_parts", ctypes.c_int32), ("rows_per_tile", ctypes.c_int32), ("combine", ctypes.c_int32),
+                ("split_tokens", ctypes.c_int32), ("tables_packed", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("tokens_saved", ctypes.c_uint64), ("off_block_tables", ctypes.c_uint64),
+                ("off_slot_mapping", ctypes.c_uint64), ("off_items", ctypes.c_uint64),
+                ("off_cta_items", ctypes.c_uint64), ("off_seq_parts", ctypes.c_uint64),
                 ("total_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
 
 
@@ -96,6 +108,8 @@ def lib() -> ctypes.CDLL:
             L.pa_decode_int8.argtypes = [P, P, P, P, P, P, P, P, ctypes.c_float, P, P, P, P, P, SZ, P]
             L.pa_prefill_varlen_int8.argtypes = [P] * 11 + [ctypes.c_float] + [P] * 4 + [SZ, P]
             L.pa_prefill_varlen_int8_fused.argtypes = [P] * 14 + [ctypes.c_float] + [P] * 4 + [SZ, P]
+            L.pa_pack_decode_shared.argtypes = [P, I32, P, I32, P, P, P, P, P, I32, I32, P, SZ, P]
+            L.pa_decode_shared.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, P, P, P, P, SZ, P]
             L.pa_last_error_string.argtypes = []
             L.pa_last_error_string.restype = ctypes.c_char_p
             L.pa_read_device_error.argtypes = [P, P]
@@ -198,6 +212,14 @@ class DecodePlan(_Plan):
         return self.dptr(self.meta.off_slot_mapping)
 
 
+class SharedPlan(_Plan):
+    @property
+    def slot_mapping(self) -> int:
+        """Device address of each last token's slot (plans packed from block lists)."""
+        assert self.meta.tables_packed, "the plan was packed for device tables: the slots are the caller's"
+        return self.dptr(self.meta.off_slot_mapping)
+
+
 def _pack(fn_name, meta, args, into, pin, cls):
     fn = getattr(lib(), fn_name)
     host = into.host if into is not None else None
@@ -250,6 +272,33 @@ def pa_pack_decode_fixed(dims: pa_dims, context_lens, block_lists, max_context: 
     args = (ctypes.byref(dims), len(ctx), _np_ptr(ctx), _np_ptr(off), _np_ptr(ids), int(max_context),
             int(split_tokens))
     return _pack("pa_pack_decode_fixed", pa_decode_meta(), args, into, pin, DecodePlan)
+
+
+def pa_pack_decode_shared(dims: pa_dims, context_lens, group_offsets=None, shared_lens=None, block_lists=None,
+                          table_rows=None, max_blocks: int = 0, split_tokens: int = 0, pin: bool = True,
+                          into: Optional["SharedPlan"] = None) -> "SharedPlan":
+    """Plan of a decode batch whose sequences share prefixes within groups of consecutive ones.
+
+    ``group_offsets`` None is one group of all.  With ``block_lists`` the tables are packed and the
+    shared length of each group is found (or, with ``shared_lens``, checked); without, the plan is for
+    a block table on the device (row ``table_rows[b]`` of it, ``max_blocks`` wide) and ``shared_lens``
+    is needed.
+    """
+    ctx = _i32(context_lens)
+    groups = _i32([0, len(ctx)] if group_offsets is None else group_offsets)
+    shared = None if shared_lens is None else _i32(shared_lens)
+    if shared is not None and len(shared) != len(groups) - 1:
+        raise ValueError(f"shared_lens has {len(shared)} entries for {len(groups) - 1} groups")
+    rows = None if table_rows is None else _i32(table_rows)
+    if rows is not None and len(rows) != len(ctx):
+        raise ValueError(f"table_rows has {len(rows)} entries for {len(ctx)} sequences")
+    off, ids = (None, None) if block_lists is None else _flatten(block_lists)
+    if off is not None and len(off) != len(ctx) + 1:
+        raise ValueError(f"block_lists has {len(off) - 1} entries for {len(ctx)} sequences")
+    opt = lambda a: None if a is None else _np_ptr(a)
+    args = (ctypes.byref(dims), len(ctx), _np_ptr(ctx), len(groups) - 1, _np_ptr(groups), opt(shared), opt(off),
+            opt(ids), opt(rows), int(max_blocks), int(split_tokens))
+    return _pack("pa_pack_decode_shared", pa_shared_meta(), args, into, pin, SharedPlan)
 
 
 def pa_upload(dev_dst, host_src, nbytes: int, stream=None):
@@ -322,6 +371,39 @@ def pa_decode_static(dims: pa_dims, q, k_cache, v_cache, plan: DecodePlan, scale
                                   plan.dptr(m.off_context_lens), plan.dptr(m.off_block_tables), float(scale),
                                   _ptr(out), ctypes.byref(m), plan.dptr(m.off_items), plan.dptr(m.off_seq_items),
                                   _stream(stream)), "pa_decode_static")
+
+
+def shared_workspace(plan: SharedPlan, device="cuda") -> Optional[torch.Tensor]:
+    n = int(plan.meta.workspace_bytes)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def _shared_args(plan: SharedPlan, block_tables, workspace):
+    """(tables, (items, cta_items, seq_parts), workspace bytes) of a shared-prefix decode call."""
+    m = plan.meta
+    if block_tables is None:
+        if not m.tables_packed and m.num_seqs > 0:
+            raise ValueError("the plan was packed for device tables: pass block_tables")
+        block_tables = plan.dptr(m.off_block_tables)
+    elif isinstance(block_tables, torch.Tensor):
+        if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or not block_tables.is_contiguous() or \
+                block_tables.shape[1] != m.max_blocks_per_seq:
+            raise ValueError(f"block_tables must be a contiguous int32 [rows, {m.max_blocks_per_seq}] tensor")
+    ws_bytes = int(workspace.numel()) if isinstance(workspace, torch.Tensor) else 0
+    return (_ptr(block_tables), (plan.dptr(m.off_items), plan.dptr(m.off_cta_items), plan.dptr(m.off_seq_parts)),
+            ws_bytes)
+
+
+def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale: float, out, workspace=None,
+                     block_tables=None, stream=None):
+    """pa_decode of a batch whose groups share prefixes: each shared block is read once per group.
+
+    ``block_tables``: the device table a plan without block lists was packed for.
+    """
+    bt, arrays, ws_bytes = _shared_args(plan, block_tables, workspace)
+    _check(lib().pa_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), bt, float(scale),
+                                  _ptr(out), ctypes.byref(plan.meta), *arrays, _ptr(workspace), ws_bytes,
+                                  _stream(stream)), "pa_decode_shared")
 
 
 def pa_copy_blocks(dims: pa_dims, k_cache, v_cache, triples, num_triples: Optional[int] = None, stream=None):

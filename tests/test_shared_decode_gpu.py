@@ -1,0 +1,251 @@
+"""Shared-prefix decode against an fp64 evaluation of its formula.
+
+Tolerance, per output element, from the roundings alone: the softmax weights are rounded to
+bf16 before the value product (at most 2^-8 of each weight) and the result once more (2^-8 of
+it); everything else is fp32 (scores of up to 128 products and a few hundred in magnitude,
+2^-24 each: below 2e-4 of the weights).  With a = sum_j w_j |v_j| >= |out|:
+    |err| <= 2^-8 (a + |out|) + 2e-4 a.
+"""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_kvcache_gb300 import pagedattn as pa
+from tests.test_shared_pack import make_batch
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -8
+
+
+def reference(q, kc, vc, lists, ctx, bs, scale):
+    """(out, a) in fp64 for q [B, Hq, D] over dense copies of each context."""
+    B, hq, d = q.shape
+    hkv = kc.shape[2]
+    out = torch.zeros(B, hq, d, dtype=torch.float64, device=q.device)
+    a = torch.zeros_like(out)
+    for b, n in enumerate(ctx):
+        if n == 0:
+            continue
+        ids = torch.tensor([int(x) for x in lists[b][:-(-n // bs)]], device=q.device)
+        k, v = (c[ids].reshape(-1, hkv, d)[:n].double() for c in (kc, vc))
+        s = torch.einsum("hgd,thd->hgt", q[b].double().view(hkv, -1, d), k) * scale
+        w = torch.softmax(s, -1)
+        out[b] = torch.einsum("hgt,thd->hgd", w, v).reshape(hq, d)
+        a[b] = torch.einsum("hgt,thd->hgd", w, v.abs()).reshape(hq, d)
+    return out, a
+
+
+def assert_within(out, ref, a, what=""):
+    err = (out.double() - ref).abs()
+    tol = U * (a + ref.abs()) + 2e-4 * a
+    assert torch.isfinite(out.float()).all(), what
+    worst = float((err / tol.clamp_min(1e-30)).max())
+    print(f"[shared] {what}: worst error is {worst:.3f} of its bound")
+    assert worst <= 1.0, (what, worst)
+
+
+def values(shape, seed, device="cuda"):
+    g = torch.Generator(device=device).manual_seed(seed)
+    return torch.randn(*shape, generator=g, device=device).to(torch.bfloat16)
+
+
+def pool(nb, bs, hkv, d, seed, ctx, lists):
+    """Caches whose rows behind every context hold NaN."""
+    kc, vc = values((nb, bs, hkv, d), seed), values((nb, bs, hkv, d), seed + 1)
+    live = torch.zeros(nb * bs, dtype=torch.bool)
+    for n, blocks in zip(ctx, lists):
+        for pos in range(n):
+            live[int(blocks[pos // bs]) * bs + pos % bs] = True
+    dead = ~live.cuda()
+    kc.view(nb * bs, hkv, d)[dead] = float("nan")
+    vc.view(nb * bs, hkv, d)[dead] = float("nan")
+    return kc, vc
+
+
+def decode(dims, q, kc, vc, plan, scale, block_tables=None, stream=None, junk=True):
+    out = torch.full_like(q, 7.0)
+    ws = pa.shared_workspace(plan)
+    if ws is not None and junk:
+        ws.fill_(0xFF)  # NaN in every partial that nobody writes
+    pa.pa_decode_shared(dims, q, kc, vc, plan, scale, out, ws, block_tables=block_tables, stream=stream)
+    return out
+
+
+CASES = [  # sizes, shared blocks, tails, bs, hq, hkv, d
+    ([1], [0], [1], 16, 1, 1, 64),                                 # one sequence, one key, one head
+    ([2], [1], [1, 2], 16, 2, 1, 64),
+    ([4], [3], [1, 0, 16, 40], 16, 8, 2, 64),                      # a context that is all prefix
+    ([5], [9], [130, 127, 128, 129, 1], 16, 16, 8, 128),           # tails around a key tile
+    ([8], [1], [44] * 8, 256, 16, 8, 128),                         # samples of a 300-token prompt
+    ([3, 1, 2], [2, 4, 0], [7, 300, 1, 9, 33, 2], 32, 28, 4, 128), # several groups, one without sharing
+    ([37, 20], [9, 1], [1 + 3 * i for i in range(57)], 64, 28, 4, 128),  # 18 a tile: pairs, a pair and one, one
+    ([33], [5], [3 + i for i in range(33)], 16, 16, 1, 128),       # group of 16 heads: 8 a tile
+    ([130], [3], [1 + i % 40 for i in range(130)], 128, 8, 8, 128),  # 128 a tile and two more
+    ([5], [2], [4, None, 6, None, 9], 16, 4, 4, 64),               # entries of context 0
+    ([2], [0], [None, None], 16, 4, 2, 128),                       # nothing else
+    ([3], [2], [1500, 3, 700], 1024, 12, 1, 64),                   # large blocks
+    ([2], [130], [5, 2000], 16, 7, 1, 128),                        # a long prefix of small blocks
+]
+
+
+@pytest.mark.parametrize("split", [0, 128, 384])
+@pytest.mark.parametrize("case", CASES, ids=range(len(CASES)))
+def test_parity(case, split):
+    sizes, sh, tails, bs, hq, hkv, d = case
+    ctx, lists, groups, nb = make_batch(5, sizes, sh, tails, bs)
+    kc, vc = pool(nb, bs, hkv, d, 50, ctx, lists)
+    q = values((len(ctx), hq, d), 52)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=split).upload()
+    out = decode(dims, q, kc, vc, plan, d ** -0.5)
+    ref, a = reference(q, kc, vc, lists, ctx, bs, d ** -0.5)
+    for b, n in enumerate(ctx):
+        if n == 0:
+            assert (out[b] == 0).all()
+    assert_within(out, ref, a, f"{case[:2]} split {split}")
+    again = decode(dims, q, kc, vc, plan, d ** -0.5)
+    assert torch.equal(out, again)  # no order of arrival enters the result
+
+
+def test_large_scores_and_scale():
+    """Scores of several hundred and a prefix far above the suffix (and below it): the merge neither overflows nor
+    loses the smaller part's weight."""
+    bs, hq, hkv, d = 16, 8, 2, 128
+    ctx, lists, groups, nb = make_batch(6, [6], [12], [9, 20, 33, 1, 64, 100], bs)
+    for up in (True, False):
+        kc, vc = pool(nb, bs, hkv, d, 60, ctx, lists)
+        shared = torch.tensor([int(x) for x in lists[0][:12]], device="cuda")
+        kc[shared] *= 6.0 if up else 0.25
+        q = values((6, hq, d), 62) * 4
+        dims = pa.make_dims(nb, bs, hq, hkv, d)
+        plan = pa.pa_pack_decode_shared(dims, ctx, block_lists=lists, split_tokens=128).upload()
+        out = decode(dims, q, kc, vc, plan, 0.25)
+        ref, a = reference(q, kc, vc, lists, ctx, bs, 0.25)
+        # scores reach 6 * 4 * 128 * 0.25 = 768 at the most here: 2^-24 of that per score, in log2 units 7e-5
+        assert_within(out, ref, a, f"large scores {up}")
+
+
+def test_equals_pa_decode():
+    """The same batch through pa_decode: both within their roundings of the same sums."""
+    bs, hq, hkv, d = 16, 28, 4, 128
+    ctx, lists, groups, nb = make_batch(7, [24, 9], [40, 17], [1 + 13 * i for i in range(33)], bs)
+    kc, vc = pool(nb, bs, hkv, d, 70, ctx, lists)
+    q = values((33, hq, d), 72)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    out = decode(dims, q, kc, vc, pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists).upload(), d ** -0.5)
+    plain = torch.empty_like(q)
+    plan = pa.pa_pack_decode(dims, ctx, lists).upload()
+    pa.pa_decode(dims, q, kc, vc, plan, d ** -0.5, plain, pa.decode_workspace(plan))
+    ref, a = reference(q, kc, vc, lists, ctx, bs, d ** -0.5)
+    assert ((out.double() - plain.double()).abs() <= 2 * (U * (a + ref.abs()) + 2e-4 * a)).all()
+
+
+def test_device_table_and_rows():
+    """A plan for a table on the device whose rows are in another order."""
+    bs, hq, hkv, d = 32, 8, 2, 64
+    ctx, lists, groups, nb = make_batch(8, [3, 2], [4, 2], [5, 60, 33, 1, 2], bs)
+    kc, vc = pool(nb, bs, hkv, d, 80, ctx, lists)
+    q = values((5, hq, d), 82)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    rows = [7, 2, 5, 0, 3]
+    table = np.full((9, 8), -1, np.int32)
+    for b, r in enumerate(rows):
+        table[r, :len(lists[b])] = lists[b]
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, shared_lens=[4 * bs, 2 * bs], table_rows=rows, max_blocks=8).upload()
+    out = decode(dims, q, kc, vc, plan, d ** -0.5, block_tables=torch.tensor(table, device="cuda"))
+    ref, a = reference(q, kc, vc, lists, ctx, bs, d ** -0.5)
+    assert_within(out, ref, a, "device table")
+    with pytest.raises(ValueError):
+        decode(dims, q, kc, vc, plan, d ** -0.5)
+    with pytest.raises(ValueError):
+        decode(dims, q, kc, vc, plan, d ** -0.5, block_tables=torch.tensor(table[:, :7].copy(), device="cuda"))
+
+
+def test_block_ids_outside_the_pool_read_as_zeros():
+    bs, hq, hkv, d = 16, 4, 2, 64
+    ctx, lists, groups, nb = make_batch(9, [2], [8], [20, 40], bs)
+    kc, vc = pool(nb, bs, hkv, d, 90, ctx, lists)
+    q = values((2, hq, d), 92)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    width = max(len(x) for x in lists)
+    table = np.full((2, width), -1, np.int32)
+    for b in range(2):
+        table[b, :len(lists[b])] = lists[b]
+    table[:, 3], table[1, 9] = -5, nb + 100
+    plan = pa.pa_pack_decode_shared(dims, ctx, shared_lens=[8 * bs], max_blocks=width).upload()
+    out = decode(dims, q, kc, vc, plan, d ** -0.5, block_tables=torch.tensor(table, device="cuda"))
+    torch.cuda.synchronize()
+    assert pa.pa_read_device_error() == 1 << 6
+    kz, vz = (torch.cat([c, torch.zeros_like(c[:1])]) for c in (kc, vc))  # block nb: zeros
+    zeroed = [[x if 0 <= x < nb else nb for x in table[b, :len(lists[b])].tolist()] for b in range(2)]
+    ref, a = reference(q, kz, vz, zeroed, ctx, bs, d ** -0.5)
+    assert_within(out, ref, a, "bad ids")
+
+
+def test_offsets_past_32_bits():
+    """Blocks at the end of a cache of more than 2^32 elements."""
+    bs, hq, hkv, d = 1024, 16, 8, 128
+    nb = (1 << 32) // (bs * hkv * d) + 6
+    kc = torch.zeros(nb, bs, hkv, d, dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    lists = [[nb - 1, 0, nb - 3], [nb - 1, 0, nb - 2]]
+    ctx = [2 * bs + 77, 2 * bs + 1000]
+    for i, x in enumerate((nb - 1, 0, nb - 3, nb - 2)):
+        kc[x], vc[x] = values((bs, hkv, d), 100 + i), values((bs, hkv, d), 110 + i)
+    q = values((2, hq, d), 120)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    plan = pa.pa_pack_decode_shared(dims, ctx, block_lists=lists).upload()
+    assert plan.meta.tokens_saved == 2 * bs
+    out = decode(dims, q, kc, vc, plan, d ** -0.5)
+    ref, a = reference(q, kc, vc, lists, ctx, bs, d ** -0.5)
+    assert_within(out, ref, a, "past 32 bits")
+
+
+def test_two_streams_and_a_captured_call():
+    """Two calls at once with workspaces of their own, and replays of a captured one over new queries."""
+    bs, hq, hkv, d = 16, 28, 4, 128
+    ctx, lists, groups, nb = make_batch(10, [20], [30], [1 + 17 * i for i in range(20)], bs)
+    kc, vc = pool(nb, bs, hkv, d, 130, ctx, lists)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    qs = [values((20, hq, d), 132 + i) for i in range(4)]
+    refs = [reference(q, kc, vc, lists, ctx, bs, d ** -0.5) for q in qs]
+    plans = [pa.pa_pack_decode_shared(dims, ctx, block_lists=lists, split_tokens=s).upload() for s in (128, 512)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(qs[0]) for _ in range(2)]
+    wss = [pa.shared_workspace(p) for p in plans]
+    for _ in range(5):
+        for i in range(2):
+            pa.pa_decode_shared(dims, qs[i], kc, vc, plans[i], d ** -0.5, outs[i], wss[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert_within(outs[i], *refs[i], f"stream {i}")
+
+    q, out = qs[0].clone(), torch.empty_like(qs[0])
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        pa.pa_decode_shared(dims, q, kc, vc, plans[0], d ** -0.5, out, wss[0])
+    for i in (2, 3):
+        q.copy_(qs[i])
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_within(out, *refs[i], f"replay {i}")
+
+
+def test_store_then_shared_decode():
+    """The serving step: the new tokens' rows go to the plan's slots, then the batch decodes."""
+    bs, hq, hkv, d = 16, 8, 2, 128
+    ctx, lists, groups, nb = make_batch(11, [7], [6], [1, 16, 17, 32, 5, 48, 33], bs)
+    kc, vc = pool(nb, bs, hkv, d, 140, [c - 1 for c in ctx], lists)
+    k, v, q = values((7, hkv, d), 142), values((7, hkv, d), 143), values((7, hq, d), 144)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    plan = pa.pa_pack_decode_shared(dims, ctx, block_lists=lists).upload()
+    pa.pa_store_kvcache(dims, k, v, kc, vc, plan.slot_mapping, 7)
+    out = decode(dims, q, kc, vc, plan, d ** -0.5)
+    for b in range(7):
+        blk, off = int(lists[b][(ctx[b] - 1) // bs]), (ctx[b] - 1) % bs
+        assert torch.equal(kc[blk, off], k[b]) and torch.equal(vc[blk, off], v[b])
+    ref, a = reference(q, kc, vc, lists, ctx, bs, d ** -0.5)
+    assert_within(out, ref, a, "store then decode")
