@@ -146,6 +146,29 @@ typedef struct pa_shared_meta {
     uint64_t workspace_bytes;    /* device workspace pa_decode_shared(_int8) needs */
 } pa_shared_meta;
 
+/*
+ * A page pool kept on the device (pa_pool_*): the caller's arrays, all device
+ * memory.  Row r holds context_lens[r] tokens in the pages named by the first
+ * ceil(context_lens[r] / block_size) entries of its table row; the entries
+ * behind them are -1.  ref_counts[p] is the number of entries that name page p;
+ * 0 is a free page.  An empty pool is tables of -1 and zeros elsewhere.
+ */
+typedef struct pa_pool {
+    int32_t num_rows;       /* rows of the block tables */
+    int32_t max_blocks;     /* their width; num_rows * max_blocks fits an int32 */
+    int32_t num_layers;     /* layers of the cache; a page id names the page in all of them */
+    int32_t reserved;       /* 0 */
+    int32_t *block_tables;  /* int32 [num_rows][max_blocks] */
+    int32_t *context_lens;  /* int32 [num_rows] */
+    int32_t *ref_counts;    /* int32 [num_blocks], 16-byte aligned */
+    void *k_cache;          /* layer 0, laid out as pa_store_kvcache's (bf16) or pa_store_kvcache_int8's */
+    void *v_cache;
+    void *k_scale;          /* layer 0 of an INT8 cache's scales; NULL, both, for a bf16 cache */
+    void *v_scale;
+    uint64_t layer_stride;       /* bytes from a layer of k_cache (and v_cache) to the next, a multiple of 16 */
+    uint64_t scale_layer_stride; /* the same for the scales */
+} pa_pool;
+
 /* ------------------------------------------------------------------ host packing */
 
 /*
@@ -390,6 +413,77 @@ int pa_decode_shared(const pa_dims *dims, const void *q, const void *k_cache, co
 int pa_copy_blocks(const pa_dims *dims, void *k_cache, void *v_cache, const int32_t *triples,
                    int32_t num_triples, pa_stream_t stream);
 
+/* ------------------------------------------------------------------ page pool */
+
+/*
+ * Pages are given out, shared, copied and taken back on the device, in stream
+ * order with the stores and decodes that use them, so that a step needs no
+ * block id from the host (it knows the lengths; pa_decode, pa_decode_shared
+ * and pa_store_kvcache take the pool's tables and the slots written here).
+ * Source: "手搓 vLLM 推理引擎", Step 2 (BlockManager: reference counts,
+ * allocate, may_append, deallocate); "vLLM / SGLang 面试源码深挖", section 4
+ * (fork).  New pages are always the free pages of the lowest ids, so the
+ * result depends on the state alone.
+ *
+ * append, fork and compact are all or nothing: a call that cannot be carried out
+ * changes neither tables, lengths, counts nor pages and sets the device error
+ * word, bit 7 (too few free pages, or a row longer than its table row) or bit 8
+ * (an argument or a state the call's rules exclude).  Calls on one pool use its
+ * state and the workspace and must not overlap: one stream, or ordered.
+ *   workspace: device memory of the bytes pa_pool_workspace gives, 256-byte
+ *              aligned; it needs no initial contents
+ */
+int pa_pool_workspace(const pa_dims *dims, const pa_pool *pool, uint64_t *bytes);
+
+/*
+ * pa_pool_append — n rows gain tokens at their ends: row rows[i] gets
+ * cu_new[i+1] - cu_new[i] (>= 0), a prompt's or a decode step's; pages are
+ * added as the row needs them, row by row in argument order, and the slots of
+ * the new tokens written, packed as cu_new counts.
+ *   rows:         device int32 [n], each row at most once
+ *   cu_new:       device int32 [n+1], from 0 to num_tokens
+ *   slot_mapping: device int32 [num_tokens]; all -1 (which the stores skip) if
+ *                 the call is refused
+ * A row whose last page is partly filled must be its only user (pa_pool_fork
+ * leaves it so): bit 8 otherwise.
+ */
+int pa_pool_append(const pa_dims *dims, const pa_pool *pool, const int32_t *rows, const int32_t *cu_new, int32_t n,
+                   int32_t *slot_mapping, int32_t num_tokens, void *workspace, size_t workspace_bytes,
+                   pa_stream_t stream);
+
+/*
+ * pa_pool_fork — row children[i] becomes a copy of row parents[i]: it names the
+ * same full pages (their counts go up) and gets a page of its own for a partly
+ * filled one, whose filled rows are copied in all layers, K and V (and scales),
+ * bit for bit; the new page's other rows stay as they were.
+ *   parents, children: device int32 [n]; a parent may occur several times, a
+ *                      child once, empty before, and not as a parent
+ */
+int pa_pool_fork(const pa_dims *dims, const pa_pool *pool, const int32_t *parents, const int32_t *children, int32_t n,
+                 void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_pool_free — rows are emptied and their pages' counts go down.  Pages keep
+ * their contents.  An empty row, or a row named again, gives nothing back; a
+ * row outside the tables, or an entry that names no page in use, is skipped and
+ * sets bit 8.
+ *   rows: device int32 [n]
+ */
+int pa_pool_free(const pa_dims *dims, const pa_pool *pool, const int32_t *rows, int32_t n, pa_stream_t stream);
+
+/*
+ * pa_pool_compact — moves the pages in use to the lowest ids: with U pages in
+ * use, those of id >= U move, in order, to the free ids below U, in all
+ * layers, and the tables and counts name them by their new ids.
+ *   remap:            device int32 [num_blocks], new id of each page, -1 for free ones
+ *   block_tables_out, ref_counts_out: arrays shaped as the pool's, or the
+ *                     pool's own.  With other arrays the old tables stay valid for
+ *                     reading until the next pa_pool_append or pa_pool_fork: the
+ *                     pages moved away from keep their contents.
+ */
+int pa_pool_compact(const pa_dims *dims, const pa_pool *pool, int32_t *remap, int32_t *block_tables_out,
+                    int32_t *ref_counts_out, void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
 /* ------------------------------------------------------------------ INT8 KV cache */
 
 /*
@@ -572,7 +666,8 @@ const char *pa_last_error_string(void);
  * timed out; 2 a block-copy triple was out of range; 3 a bounded wait in the
  * INT8 decode kernel timed out; 4 the wait of pa_selftest_bounded_wait timed
  * out; 5 a bounded wait in the shared-prefix decode timed out; 6 the
- * shared-prefix decode met a block id outside the pool.  Synchronises `stream`: for tests and debugging, never on the hot path.
+ * shared-prefix decode met a block id outside the pool; 7 a pa_pool call was
+ * refused for lack of room; 8 a pa_pool call was malformed, or the pool's state.  Synchronises `stream`: for tests and debugging, never on the hot path.
  */
 int pa_read_device_error(uint32_t *code, pa_stream_t stream);
 

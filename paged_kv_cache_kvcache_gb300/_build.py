@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libpagedattn.so")
 
 SOURCES = ["api.cpp", "pack.cpp", "pack_shared.cpp", "store_kv.cu", "decode.cu", "decode_int8.cu", "decode_shared.cu",
-           "prefill.cu", "copy_blocks.cu", "tmap.cpp", "selftest.cu"]
+           "prefill.cu", "copy_blocks.cu", "pool.cu", "tmap.cpp", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -552,6 +552,129 @@ extern "C" int pa_copy_blocks_int8(const pa_dims *dims, void *k_cache, void *v_c
     return launch_copy_blocks(*dims, k_cache, v_cache, triples, num_triples, stream, k_scale, v_scale);
 }
 
+// Host-side checks of the pa_pool calls; fills `a`.
+static int prepare_pool(const char *fn, const pa_dims *dims, const pa_pool *pool, const void *workspace,
+                        size_t workspace_bytes, bool needs_workspace, bool needs_pages, PoolArgs *a)
+{
+    int rc = check_dims(dims);
+    if (rc != PA_OK)
+        return rc;
+    if (!pool)
+        return fail(PA_ERR_INVALID_ARG, "%s: pool is NULL", fn);
+    const pa_pool &o = *pool;
+    if (o.num_rows < 1 || o.max_blocks < 1 || o.num_layers < 1)
+        return fail(PA_ERR_INVALID_ARG, "%s: num_rows, max_blocks and num_layers must be positive", fn);
+    if ((int64_t)o.num_rows * o.max_blocks > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "%s: num_rows * max_blocks exceeds int32", fn);
+    if (dims->num_blocks == 0)
+        return fail(PA_ERR_INVALID_ARG, "empty KV pool");
+    if (!o.block_tables || !o.context_lens || !o.ref_counts)
+        return fail(PA_ERR_INVALID_ARG, "%s: NULL pool array", fn);
+    auto unaligned = [](const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; };
+    if (unaligned(o.block_tables, 4) || unaligned(o.context_lens, 4) || unaligned(o.ref_counts, 16))
+        return fail(PA_ERR_INVALID_ARG, "%s: misaligned pool array (ref_counts: 16 bytes)", fn);
+    if (needs_pages) {
+        if (!o.k_cache || !o.v_cache || !o.k_scale != !o.v_scale)
+            return fail(PA_ERR_INVALID_ARG, "%s: k_cache and v_cache, and both scales or neither, must be given", fn);
+        const uint64_t scales = (uint64_t)dims->num_blocks * dims->block_size * dims->num_kv_heads * 2;
+        const uint64_t layer = scales / 2 * dims->head_dim * (o.k_scale ? 1 : 2);
+        if (misaligned(o.k_cache) || misaligned(o.v_cache) || misaligned(o.k_scale) || misaligned(o.v_scale))
+            return fail(PA_ERR_INVALID_ARG, "%s: caches and scales must be 16-byte aligned", fn);
+        if (o.num_layers > 1 && (o.layer_stride % 16 != 0 || o.layer_stride < layer))
+            return fail(PA_ERR_INVALID_ARG, "%s: layer_stride must be a multiple of 16 of at least a layer's %llu bytes",
+                        fn, (unsigned long long)layer);
+        if (o.num_layers > 1 && o.k_scale && (o.scale_layer_stride % 2 != 0 || o.scale_layer_stride < scales))
+            return fail(PA_ERR_INVALID_ARG, "%s: scale_layer_stride must be even and at least a layer's %llu bytes", fn,
+                        (unsigned long long)scales);
+    }
+    if (needs_workspace) {
+        const size_t need = pool_workspace_bytes(o.num_rows, dims->num_blocks);
+        if (workspace_bytes < need)
+            return fail(PA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn, workspace_bytes, need);
+        if (!workspace || unaligned(workspace, 256))
+            return fail(PA_ERR_INVALID_ARG, "%s: workspace must be non-NULL and 256-byte aligned", fn);
+    }
+    a->dims = *dims;
+    a->pool = o;
+    a->workspace = const_cast<void *>(workspace);
+    return PA_OK;
+}
+
+extern "C" int pa_pool_workspace(const pa_dims *dims, const pa_pool *pool, uint64_t *bytes)
+{
+    int rc = check_dims(dims);
+    if (rc != PA_OK)
+        return rc;
+    if (!pool || !bytes || pool->num_rows < 1)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_workspace: NULL pointer or num_rows < 1");
+    *bytes = pool_workspace_bytes(pool->num_rows, dims->num_blocks);
+    return PA_OK;
+}
+
+extern "C" int pa_pool_append(const pa_dims *dims, const pa_pool *pool, const int32_t *rows, const int32_t *cu_new,
+                              int32_t n, int32_t *slot_mapping, int32_t num_tokens, void *workspace,
+                              size_t workspace_bytes, pa_stream_t stream)
+{
+    PoolArgs a;
+    int rc = prepare_pool("pa_pool_append", dims, pool, workspace, workspace_bytes, true, false, &a);
+    if (rc != PA_OK)
+        return rc;
+    if (n < 0 || n > pool->num_rows || num_tokens < 0 || (n == 0 && num_tokens > 0))
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_append: %d rows, %d tokens (the pool has %d rows)", n, num_tokens,
+                    pool->num_rows);
+    if (n == 0)
+        return PA_OK;
+    if (!rows || !cu_new || (!slot_mapping && num_tokens > 0))
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_append: NULL pointer");
+    return launch_pool_append(a, rows, cu_new, n, slot_mapping, num_tokens, stream);
+}
+
+extern "C" int pa_pool_fork(const pa_dims *dims, const pa_pool *pool, const int32_t *parents, const int32_t *children,
+                            int32_t n, void *workspace, size_t workspace_bytes, pa_stream_t stream)
+{
+    PoolArgs a;
+    int rc = prepare_pool("pa_pool_fork", dims, pool, workspace, workspace_bytes, true, true, &a);
+    if (rc != PA_OK)
+        return rc;
+    if (n < 0 || n > pool->num_rows)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_fork: %d children (the pool has %d rows)", n, pool->num_rows);
+    if (n == 0)
+        return PA_OK;
+    if (!parents || !children)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_fork: NULL pointer");
+    return launch_pool_fork(a, parents, children, n, stream);
+}
+
+extern "C" int pa_pool_free(const pa_dims *dims, const pa_pool *pool, const int32_t *rows, int32_t n,
+                            pa_stream_t stream)
+{
+    PoolArgs a;
+    int rc = prepare_pool("pa_pool_free", dims, pool, nullptr, 0, false, false, &a);
+    if (rc != PA_OK)
+        return rc;
+    if (n < 0)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_free: n < 0");
+    if (n == 0)
+        return PA_OK;
+    if (!rows)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_free: NULL pointer");
+    return launch_pool_free(a, rows, n, stream);
+}
+
+extern "C" int pa_pool_compact(const pa_dims *dims, const pa_pool *pool, int32_t *remap, int32_t *block_tables_out,
+                               int32_t *ref_counts_out, void *workspace, size_t workspace_bytes, pa_stream_t stream)
+{
+    PoolArgs a;
+    int rc = prepare_pool("pa_pool_compact", dims, pool, workspace, workspace_bytes, true, true, &a);
+    if (rc != PA_OK)
+        return rc;
+    if (!remap || !block_tables_out || !ref_counts_out)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_compact: NULL pointer");
+    if (remap == pool->ref_counts || remap == ref_counts_out || remap == pool->block_tables || remap == block_tables_out)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_compact: remap must be an array of its own");
+    return launch_pool_compact(a, remap, block_tables_out, ref_counts_out, stream);
+}
+
 // pa_decode for callers that cannot allocate: the workspace is the library's
 // own scratch array (see the header for its limit, set-up and sharing rules).
 extern "C" int pa_decode_static(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
@@ -602,6 +725,8 @@ extern "C" int pa_read_device_error(uint32_t *code, pa_stream_t stream)
         rc = read_selftest_error(code);
     if (rc == PA_OK)
         rc = read_shared_error(code);
+    if (rc == PA_OK)
+        rc = read_pool_error(code);
     return rc;
 }
 

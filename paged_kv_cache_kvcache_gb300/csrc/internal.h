@@ -210,6 +210,19 @@ struct SharedArgs {
 };
 int launch_decode_shared(const SharedArgs &a, void *stream);
 
+// Page pool (pool.cu).
+struct PoolArgs {
+    pa_dims dims;
+    pa_pool pool;
+    void *workspace;
+};
+size_t pool_workspace_bytes(int num_rows, int num_blocks);
+int launch_pool_append(const PoolArgs &a, const int32_t *rows, const int32_t *cu, int n, int32_t *slots, int num_tokens,
+                       void *stream);
+int launch_pool_fork(const PoolArgs &a, const int32_t *parents, const int32_t *children, int n, void *stream);
+int launch_pool_free(const PoolArgs &a, const int32_t *rows, int n, void *stream);
+int launch_pool_compact(const PoolArgs &a, int32_t *remap, int32_t *tables_out, int32_t *refs_out, void *stream);
+
 // Device address of the library-owned decode scratch on the current device
 // (looked up once per device).  Used only by pa_decode_static.
 int decode_static_scratch(void **ptr);
@@ -230,6 +243,7 @@ int read_decode_error(uint32_t *code);
 int read_fused_error(uint32_t *code);
 int read_fused8_error(uint32_t *code);
 int read_shared_error(uint32_t *code); // bit 0 -> 5 (wait), bit 1 -> 6 (block id outside the pool)
+int read_pool_error(uint32_t *code);   // bit 0 -> 7 (no room), bit 1 -> 8 (malformed)
 int launch_selftest_wait(uint32_t timeout_us, int arrive_first, void *stream);
 int read_selftest_error(uint32_t *code);
 int launch_stream_read(const void *src, size_t bytes, uint32_t *sink, void *stream);

@@ -24,7 +24,8 @@ EXPORTS = ("pa_pack_prefill", "pa_pack_decode", "pa_upload", "pa_store_kvcache",
            "pa_decode", "pa_decode_static", "pa_copy_blocks", "pa_store_kvcache_int8", "pa_decode_int8",
            "pa_prefill_varlen_int8", "pa_pack_decode_fixed", "pa_decode_fused", "pa_copy_blocks_int8",
            "pa_decode_int8_fused", "pa_prefill_varlen_fused", "pa_prefill_varlen_int8_fused",
-           "pa_pack_decode_shared", "pa_decode_shared",
+           "pa_pack_decode_shared", "pa_decode_shared", "pa_pool_workspace", "pa_pool_append", "pa_pool_fork",
+           "pa_pool_free", "pa_pool_compact",
            "pa_last_error_string", "pa_read_device_error", "pa_selftest_bounded_wait", "pa_stream_read",
            "pa_version")
 
@@ -66,6 +67,14 @@ class pa_shared_meta(ctypes.Structure):
                 ("off_slot_mapping", ctypes.c_uint64), ("off_items", ctypes.c_uint64),
                 ("off_cta_items", ctypes.c_uint64), ("off_seq_parts", ctypes.c_uint64),
                 ("total_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class pa_pool(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int32), ("max_blocks", ctypes.c_int32), ("num_layers", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("block_tables", ctypes.c_void_p), ("context_lens", ctypes.c_void_p),
+                ("ref_counts", ctypes.c_void_p), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("layer_stride", ctypes.c_uint64),
+                ("scale_layer_stride", ctypes.c_uint64)]
 
 
 class PagedAttnError(RuntimeError):
@@ -110,6 +119,11 @@ def lib() -> ctypes.CDLL:
             L.pa_prefill_varlen_int8_fused.argtypes = [P] * 14 + [ctypes.c_float] + [P] * 4 + [SZ, P]
             L.pa_pack_decode_shared.argtypes = [P, I32, P, I32, P, P, P, P, P, I32, I32, P, SZ, P]
             L.pa_decode_shared.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, P, P, P, P, SZ, P]
+            L.pa_pool_workspace.argtypes = [P, P, P]
+            L.pa_pool_append.argtypes = [P, P, P, P, I32, P, I32, P, SZ, P]
+            L.pa_pool_fork.argtypes = [P, P, P, P, I32, P, SZ, P]
+            L.pa_pool_free.argtypes = [P, P, P, I32, P]
+            L.pa_pool_compact.argtypes = [P, P, P, P, P, P, SZ, P]
             L.pa_last_error_string.argtypes = []
             L.pa_last_error_string.restype = ctypes.c_char_p
             L.pa_read_device_error.argtypes = [P, P]
@@ -411,6 +425,102 @@ def pa_copy_blocks(dims: pa_dims, k_cache, v_cache, triples, num_triples: Option
     n = int(triples.shape[0]) if num_triples is None else int(num_triples)
     _check(lib().pa_copy_blocks(ctypes.byref(dims), _ptr(k_cache), _ptr(v_cache), _ptr(triples), n,
                                 _stream(stream)), "pa_copy_blocks")
+
+
+def _int32(t, what: str, count: Optional[int] = None) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous() or \
+            (count is not None and t.numel() != count):
+        raise ValueError(f"{what} must be a contiguous int32 tensor" + ("" if count is None else f" of {count}"))
+    return t
+
+
+class PagePool:
+    """A page pool on the device: block tables, context lengths, reference counts and the pages of all layers.
+
+    k_cache, v_cache: [layers, num_blocks, block_size, Hkv, D] (or one layer without that dimension), each
+    layer contiguous; bf16, or int8 with k_scale, v_scale fp16 [layers, num_blocks, Hkv, block_size].
+    block_tables int32 [rows, max_blocks], context_lens int32 [rows], ref_counts int32 [num_blocks].
+    """
+
+    def __init__(self, dims: pa_dims, k_cache, v_cache, block_tables, context_lens, ref_counts, k_scale=None,
+                 v_scale=None):
+        rows, width = block_tables.shape
+        _int32(block_tables, "block_tables")
+        _int32(context_lens, "context_lens", rows)
+        _int32(ref_counts, "ref_counts", dims.num_blocks)
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("k_scale and v_scale go together")
+        page = (dims.num_blocks, dims.block_size, dims.num_kv_heads, dims.head_dim)
+        scale = (dims.num_blocks, dims.num_kv_heads, dims.block_size)
+        k, v = self._layers(k_cache, page, k_scale is not None), self._layers(v_cache, page, k_scale is not None)
+        ks, vs = ((None, None) if k_scale is None else (self._layers(x, scale, None) for x in (k_scale, v_scale)))
+        parts = [x for x in (k, v, ks, vs) if x is not None]
+        if any(x.shape[0] != k.shape[0] for x in parts) or k.stride(0) != v.stride(0) or \
+                (ks is not None and ks.stride(0) != vs.stride(0)):
+            raise ValueError("K and V (and their scales) must agree in layers and in the stride between them")
+        if any(x.device != block_tables.device for x in parts + [context_lens, ref_counts]):
+            raise ValueError("the pool's arrays must be on one device")
+        self.block_tables, self.context_lens, self.ref_counts = block_tables, context_lens, ref_counts
+        self.k_cache, self.v_cache, self.k_scale, self.v_scale = k_cache, v_cache, k_scale, v_scale
+        self.struct = pa_pool(rows, width, k.shape[0], 0, _ptr(block_tables), _ptr(context_lens), _ptr(ref_counts),
+                              _ptr(k), _ptr(v), _ptr(ks), _ptr(vs), k.stride(0) * k.element_size(),
+                              0 if ks is None else ks.stride(0) * ks.element_size())
+        self.ref = ctypes.byref(self.struct)
+        n = ctypes.c_uint64(0)
+        _check(lib().pa_pool_workspace(ctypes.byref(dims), self.ref, ctypes.byref(n)), "pa_pool_workspace")
+        self.workspace = torch.empty(n.value, dtype=torch.uint8, device=block_tables.device)
+        self.workspace_bytes = n.value
+
+    @staticmethod
+    def _layers(x, shape, int8):
+        """x as [layers, *shape], each layer contiguous."""
+        want = torch.float16 if int8 is None else torch.int8 if int8 else torch.bfloat16
+        x = x.unsqueeze(0) if x.dim() == len(shape) else x
+        if x.dtype != want or tuple(x.shape[1:]) != shape or not x[0].is_contiguous():
+            raise ValueError(f"expected {want} [layers, {', '.join(map(str, shape))}] with contiguous layers, got "
+                             f"{x.dtype} {tuple(x.shape)}")
+        return x
+
+
+def page_pool(dims: pa_dims, k_cache, v_cache, num_rows: int, max_blocks: int, k_scale=None, v_scale=None) -> PagePool:
+    """An empty pool over the given caches."""
+    new = lambda *shape, fill: torch.full(shape, fill, dtype=torch.int32, device=k_cache.device)
+    return PagePool(dims, k_cache, v_cache, new(num_rows, max_blocks, fill=-1), new(num_rows, fill=0),
+                    new(dims.num_blocks, fill=0), k_scale, v_scale)
+
+
+def pa_pool_append(dims: pa_dims, pool: PagePool, rows, cu_new, slot_mapping, stream=None):
+    """Give row rows[i] its next cu_new[i+1] - cu_new[i] tokens; their slots go to slot_mapping."""
+    n = int(rows.numel())
+    _int32(rows, "rows"), _int32(cu_new, "cu_new", n + 1), _int32(slot_mapping, "slot_mapping")
+    _check(lib().pa_pool_append(ctypes.byref(dims), pool.ref, _ptr(rows), _ptr(cu_new), n, _ptr(slot_mapping),
+                                int(slot_mapping.numel()), _ptr(pool.workspace), pool.workspace_bytes, _stream(stream)),
+           "pa_pool_append")
+
+
+def pa_pool_fork(dims: pa_dims, pool: PagePool, parents, children, stream=None):
+    """Row children[i] shares row parents[i]'s full pages and gets a copy of its partly filled one."""
+    n = int(children.numel())
+    _int32(parents, "parents", n), _int32(children, "children")
+    _check(lib().pa_pool_fork(ctypes.byref(dims), pool.ref, _ptr(parents), _ptr(children), n, _ptr(pool.workspace),
+                              pool.workspace_bytes, _stream(stream)), "pa_pool_fork")
+
+
+def pa_pool_free(dims: pa_dims, pool: PagePool, rows, stream=None):
+    """Empty the rows and give their pages back."""
+    _check(lib().pa_pool_free(ctypes.byref(dims), pool.ref, _ptr(_int32(rows, "rows")), int(rows.numel()),
+                              _stream(stream)), "pa_pool_free")
+
+
+def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None, ref_counts_out=None, stream=None):
+    """Move the used pages to the lowest ids; remap[p] is page p's new id.  Tables and counts are rewritten in
+    place, or into the given arrays."""
+    tables = pool.block_tables if block_tables_out is None else block_tables_out
+    refs = pool.ref_counts if ref_counts_out is None else ref_counts_out
+    _int32(remap, "remap", pool.ref_counts.numel()), _int32(refs, "ref_counts_out", pool.ref_counts.numel())
+    _int32(tables, "block_tables_out", pool.block_tables.numel())
+    _check(lib().pa_pool_compact(ctypes.byref(dims), pool.ref, _ptr(remap), _ptr(tables), _ptr(refs),
+                                 _ptr(pool.workspace), pool.workspace_bytes, _stream(stream)), "pa_pool_compact")
 
 
 def int8_cache(dims: pa_dims, device="cuda"):
