@@ -131,16 +131,18 @@ typedef struct pa_shared_meta {
     int32_t num_partials;       /* partial results in the workspace */
     int32_t max_parts;          /* most parts any context is cut into */
     int32_t rows_per_tile;      /* sequences per 128-row query tile (128 / group, floored) */
-    int32_t combine;            /* 1: some context has two or more parts, or none (merge launch) */
+    int32_t merge;              /* 1: some context has two or more parts, or none */
     int32_t split_tokens;       /* keys per part, at most */
     int32_t tables_packed;      /* 1: the image holds block tables and slots */
     int32_t reserved;
     uint64_t tokens_saved;       /* keys the groups read once instead of once per sequence */
     uint64_t off_block_tables;   /* int32 [num_seqs][max_blocks_per_seq], -1 padded (tables_packed) */
     uint64_t off_slot_mapping;   /* int32 [num_seqs] slot of each last token (tables_packed) */
-    uint64_t off_items;          /* int32 [num_items][8], CTA by CTA, longest first: first sequence,
-                                    sequences, KV head, block-table row, first key, end key, part, 0 */
-    uint64_t off_cta_items;      /* int32 [num_ctas+1] first work item of each CTA */
+    uint64_t off_items;          /* int32 [num_items][8]: first sequence, sequences, KV head,
+                                    block-table row, first key, end key, part, 0 */
+    uint64_t off_cta_items;      /* int32 [num_ctas][4]: a CTA's items of more than rows_per_tile
+                                    sequences start at the first, those of its two lanes at the
+                                    second and third and end before the fourth, longest first each */
     uint64_t off_seq_parts;      /* int32 [num_seqs][2] first partial slot and number of parts */
     uint64_t total_bytes;
     uint64_t workspace_bytes;    /* device workspace pa_decode_shared(_int8) needs */

@@ -463,7 +463,7 @@ static int prepare_shared(const char *fn, const pa_dims *dims, const void *q, co
         return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
     if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out) || misaligned(items))
         return fail(PA_ERR_INVALID_ARG, "%s: tensors and items must be 16-byte aligned", fn);
-    if ((reinterpret_cast<uintptr_t>(seq_parts) & 7u) || (reinterpret_cast<uintptr_t>(cta_items) & 3u) ||
+    if ((reinterpret_cast<uintptr_t>(seq_parts) & 7u) || misaligned(cta_items) ||
         (reinterpret_cast<uintptr_t>(block_tables) & 3u))
         return fail(PA_ERR_INVALID_ARG, "%s: misaligned plan array or block table", fn);
     if (meta->num_items > 0 && dims->num_blocks == 0)
@@ -499,7 +499,7 @@ static int prepare_shared(const char *fn, const pa_dims *dims, const void *q, co
     a->num_ctas = meta->num_ctas;
     a->rows_per_tile = meta->rows_per_tile;
     a->max_blocks_per_seq = meta->max_blocks_per_seq;
-    a->combine = meta->combine != 0;
+    a->merge = meta->merge != 0;
     return PA_OK;
 }
 

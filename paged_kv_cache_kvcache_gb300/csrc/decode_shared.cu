@@ -16,16 +16,21 @@
 // all reading the same K/V.  With R rows a K/V byte is worth R flops (bf16), so a prefix is
 // bound by HBM up to about 290 rows per KV head and by the tensor cores beyond.
 //
-// One persistent launch runs every part: a work item is (up to 2 x 128 rows, KV head, key
-// range, block-table row); the prefix parts carry many sequences, the suffix parts one.  The
-// host cuts the key ranges and deals the items out to the CTAs (longest first onto the least
-// loaded).  Structure of a CTA as in the prefill kernel: K, V and query producers (TMA, one
-// 3-D box per physical block), one MMA warp (tcgen05, S and O in tensor memory, P fed back
-// through tensor memory), one softmax warpgroup per 128-row tile, every ring running on
-// across items.  A suffix part fills few of its tile's 128 rows; its products then run mostly
-// on padding, which costs nothing that matters: 128 keys x 128 rows take about 1100 cycles of
-// the tensor core while their K/V (64 KB) take about 2800 cycles of this SM's share of HBM.
-// Warps without a valid row skip the softmax.
+// One persistent launch runs every part.  A work item is (rows, KV head, key range, block-table
+// row): a prefix part carries many sequences, a suffix part one.  A CTA holds two query tiles of
+// 128 rows and runs its items in two ways:
+//  * a prefix part of more than 128 rows is a PAIR: both tiles against one stream of K/V, bound
+//    by the tensor core (measured 1.75 us per 128 keys);
+//  * every other part is a SINGLE: one tile, 128 keys whose products take about 1100 cycles of the
+//    tensor core while their 64 KB of K/V take about 2800 cycles of this SM's share of HBM.  But
+//    score product, softmax and value product of one tile follow one another (about 2300 cycles
+//    with their hand-offs), so the two tiles are two LANES, each walking singles of its own, one's
+//    products under the other's softmax and loads.  Most of a single's rows are padding; warps
+//    without a valid row skip the softmax.
+// The host cuts the key ranges and deals pairs to CTAs and singles to lanes (longest first onto
+// the least loaded).  Structure of a CTA as in the prefill kernel: K, V and query producers
+// (TMA, one 3-D box per physical block), one MMA warp (tcgen05, S and O in tensor memory, P fed
+// back through tensor memory), one softmax warpgroup per tile; the rings run on across items.
 //
 // Every hand-off waits with a time limit; a wait that runs out sets an error bit and the
 // kernel returns.  A block id outside the pool reads as zeros and sets an error bit.
@@ -51,14 +56,12 @@ constexpr int kLaunchRegs = 168;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 static_assert(128 * (2 * kSoftmaxRegs + kOtherRegs) == kThreads * kLaunchRegs, "register hand-over");
 constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10, kQWarp = 11;
+// Rows of a TMA box of large blocks: a range's last boxes read past its end, 16 rows on average
+// (with one box of 128 per tile a batch of 200 suffixes of 350 keys read 12 % more than its keys).
+constexpr int kBoxRows = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f; // log2 units
-// An item of n key tiles owns n + 1 release events: its opening score products (K tile 0
-// read), then one per iteration (V tile j and K tile j + 1 read).  At most 2S - 1 events lie
-// between a refill of a ring of S slots and the event it waits for, so 8 keep parities apart.
-constexpr int kIterRing = 8;
-
 template <int D>
 struct ShLayout {
     static constexpr int kPanels = D / 64;        // 64-element (128-byte) panels along head_dim
@@ -77,7 +80,7 @@ struct ShLayout {
 
 struct ShParams {
     const int4 *items;
-    const int32_t *cta_items;
+    const int4 *cta_items;
     const int2 *seq_parts;
     const int32_t *block_tables;
     __nv_bfloat16 *out;
@@ -98,8 +101,9 @@ struct Bars {
     __device__ uint32_t q_full(int t) const { return base + 8 * t; }
     __device__ uint32_t q_free(int t) const { return base + 8 * (2 + t); }
     __device__ uint32_t k_full(int s) const { return base + 8 * (4 + s); }
-    __device__ uint32_t v_full(int s) const { return base + 8 * (8 + s); }
-    __device__ uint32_t released(int e) const { return base + 8 * (12 + (e & (kIterRing - 1))); }
+    __device__ uint32_t k_free(int s) const { return base + 8 * (8 + s); }
+    __device__ uint32_t v_full(int s) const { return base + 8 * (12 + s); }
+    __device__ uint32_t v_free(int s) const { return base + 8 * (16 + s); }
     __device__ uint32_t s_full(int t) const { return base + 8 * (20 + t); }
     __device__ uint32_t p_full(int t) const { return base + 8 * (22 + t); }
     __device__ uint32_t o_full(int t) const { return base + 8 * (24 + t); }
@@ -110,26 +114,19 @@ constexpr int kTmemSlotOffset = 8 * 30;
 constexpr int kAbortOffset = 8 * 31;
 
 struct Item {
-    int ord;          // position in this CTA's list
-    int s0, nseq, g;  // sequences s0 .. s0 + nseq - 1 (rows of q), KV head
-    int row, k0, k1;  // block-table row, key range (k0 a multiple of the box)
-    int part;         // which of each sequence's parts this is
-    int n0, n1;       // sequences of tiles 0 and 1
-    int nkt;          // key tiles
-    bool tail;        // the last key tile runs past k1
+    int s0, nseq, g; // sequences s0 .. s0 + nseq - 1 (rows of q), KV head
+    int row, k0, k1; // block-table row, key range (k0 a multiple of the box)
+    int part;        // which of each sequence's parts this is
+    __device__ int tiles() const { return (k1 - k0 + 127) >> 7; }
+    __device__ bool tail() const { return ((k1 - k0) & 127) != 0; } // the last key tile runs past k1
 };
 
-// This CTA's items, the next entry fetched while the current one runs.
+// Entries [idx, end) of the item list, the next one fetched while the current one runs.
 struct ItemIter {
     const int4 *items;
-    int idx, end, ord, P;
+    int idx, end;
     int4 a0, a1;
-    __device__ ItemIter(const ShParams &p)
-        : items(p.items), idx(__ldg(p.cta_items + blockIdx.x)), end(__ldg(p.cta_items + blockIdx.x + 1)), ord(0),
-          P(p.rows_per_tile)
-    {
-        fetch();
-    }
+    __device__ ItemIter(const int4 *items_, int from, int to) : items(items_), idx(from), end(to) { fetch(); }
     __device__ bool more() const { return idx < end; }
     __device__ void fetch()
     {
@@ -138,26 +135,42 @@ struct ItemIter {
             a1 = ptx::ld_nc_v4_now(items + 2 * idx + 1);
         }
     }
-    __device__ Item peek() const
-    {
-        Item w;
-        w.ord = ord;
-        w.s0 = a0.x, w.nseq = a0.y, w.g = a0.z, w.row = a0.w;
-        w.k0 = a1.x, w.k1 = a1.y, w.part = a1.z;
-        w.n0 = min(P, w.nseq);
-        w.n1 = w.nseq - w.n0;
-        w.nkt = (w.k1 - w.k0 + 127) >> 7;
-        w.tail = ((w.k1 - w.k0) & 127) != 0;
-        return w;
-    }
+    __device__ Item peek() const { return {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z}; }
     __device__ Item next(bool fetch_now = true)
     {
         const Item w = peek();
-        ++ord;
         ++idx;
         if (fetch_now)
             fetch();
         return w;
+    }
+};
+
+// A lane's place in its singles: key tile j of n of the current one.
+struct Lane {
+    ItemIter it;
+    Item w;
+    int j, n;
+    bool active;
+    __device__ Lane(const int4 *items, int from, int to) : it(items, from, to), w{}, j(0), n(0), active(it.more())
+    {
+        if (active) {
+            w = it.next();
+            n = w.tiles();
+        }
+    }
+    // past the current key tile; true if that began a new item
+    __device__ bool step()
+    {
+        if (++j < n)
+            return false;
+        j = 0;
+        active = it.more();
+        if (active) {
+            w = it.next();
+            n = w.tiles();
+        }
+        return true;
     }
 };
 
@@ -176,13 +189,6 @@ struct Waiter {
         return false;
     }
 };
-
-// Release event of the key tile `back` places before global tile X, given the current item's
-// ordinal and the item-start bits of the last tiles (bit i: tile X - i opens its item).
-__device__ __forceinline__ int release_event(int X, int back, int ord, uint32_t starts, int v)
-{
-    return X - back + ord - __popc(starts & ((1u << back) - 1u)) + v;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = p.group;
     const int P = p.rows_per_tile;
 
-    // the combine launch may be set up now; it waits for this grid's end before it reads
+    // the merge launch may be set up now; it waits for this grid's end before it reads
     ptx::launch_dependents();
     if (warp >= 8 && lane == 0) {
         if (warp == kQWarp) {
@@ -224,14 +230,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bars.p_full(t), 4);
             ptx::mbar_init(bars.o_full(t), 1);
         }
-        for (int s = 0; s < L::kKStages; ++s)
+        for (int s = 0; s < L::kKStages; ++s) {
             ptx::mbar_init(bars.k_full(s), 1);
+            ptx::mbar_init(bars.k_free(s), 1);
+        }
         for (int s = 0; s < L::kVStages; ++s) {
             ptx::mbar_init(bars.v_full(s), 1);
+            ptx::mbar_init(bars.v_free(s), 1);
             ptx::mbar_init(bars.v_tail(s), 1);
         }
-        for (int s = 0; s < kIterRing; ++s)
-            ptx::mbar_init(bars.released(s), 1);
         *abort_flag = 0u;
         ptx::fence_mbar_init();
     }
@@ -239,7 +246,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(bars.tmem_slot(), kTmemCols);
         ptx::tmem_relinquish();
     }
-    ItemIter items(p);
+    // This CTA's pairs and its lanes' singles.  What the roles look up first (an item, then, by the K
+    // and V producers, its blocks) is brought into L1 while the barriers and the tensor memory are
+    // set up: three dependent loads otherwise stand before the first tile.
+    const int4 span = __ldg(p.cta_items + blockIdx.x);
+    if (warp == kKWarp || warp == kVWarp) {
+        const int first = span.x < span.y ? span.x : span.y, second = span.x < span.y ? span.x : span.z;
+        for (int i = first;; i = second) {
+            if (i < span.w) {
+                const int4 a0 = __ldg(p.items + 2 * i), a1 = __ldg(p.items + 2 * i + 1);
+                const int key = a1.x + lane * p.box_rows;
+                if (lane * p.box_rows < 128 && key < a1.y)
+                    ptx::prefetch_l1(p.block_tables + (size_t)a0.w * p.max_blocks + key / p.block_size);
+            }
+            if (i == second)
+                break;
+        }
+    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -250,26 +273,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::reg_dealloc<kOtherRegs>();
         if (warp == kQWarp) {
             // ------------------------------------------------------------ query producer
+            uint32_t nq0 = 0, nq1 = 0; // loads of each tile so far
             bool ok = true;
-            while (ok && items.more()) {
-                const Item w = items.next();
-                for (int t = 0; t < (w.n1 > 0 ? 2 : 1); ++t) {
-                    // Refill after the last score product of this tile that read the buffer.  A tile
-                    // that an item leaves empty is released with the item all the same, so the n-th
-                    // item waits for the (n - 1)-th release of both.  Tile 0 is waited for at every item
-                    // and before tile 1, so tile 1's barrier is at most one release behind and its
-                    // parity is not ambiguous although some items skip its wait.
-                    if (w.ord > 0 && !(ok = wwait(bars.q_free(t), (w.ord - 1) & 1)))
-                        break;
-                    if (lane == 0) {
-                        const bool one = w.nseq == 1;
-                        ptx::mbar_arrive_expect_tx(bars.q_full(t), (uint32_t)(L::kPanels * 128 * G * (one ? 1 : P)));
-                        for (int pp = 0; pp < L::kPanels; ++pp)
-                            ptx::tma_load_3d(sbase + L::kQ + t * L::kTileBytes + pp * L::kPanelBytes,
-                                             one ? &tm_q1 : &tm_q, bars.q_full(t), pp * 64, w.g * G, w.s0 + t * P);
-                    }
-                    __syncwarp();
+            // query rows of `w` (from sequence w.s0 + skip) into tile t, once the last score product
+            // that read the buffer is complete
+            auto load = [&](const Item &w, int t, int skip) {
+                uint32_t &n = t == 0 ? nq0 : nq1;
+                if (n > 0 && !(ok = wwait(bars.q_free(t), (n - 1) & 1)))
+                    return;
+                ++n;
+                if (lane == 0) {
+                    const bool one = w.nseq == 1;
+                    ptx::mbar_arrive_expect_tx(bars.q_full(t), (uint32_t)(L::kPanels * 128 * G * (one ? 1 : P)));
+                    for (int pp = 0; pp < L::kPanels; ++pp)
+                        ptx::tma_load_3d(sbase + L::kQ + t * L::kTileBytes + pp * L::kPanelBytes, one ? &tm_q1 : &tm_q,
+                                         bars.q_full(t), pp * 64, w.g * G, w.s0 + skip);
                 }
+                __syncwarp();
+            };
+            for (ItemIter it(p.items, span.x, span.y); ok && it.more();) {
+                const Item w = it.next();
+                load(w, 0, 0);
+                if (ok)
+                    load(w, 1, P);
+            }
+            // the lanes advance tile by tile together: loads in the order in which they are needed
+            ItemIter i0(p.items, span.y, span.z), i1(p.items, span.z, span.w);
+            int at0 = 0, at1 = 0; // key tiles before each lane's next item
+            while (ok && (i0.more() || i1.more())) {
+                const bool first = i0.more() && (!i1.more() || at0 <= at1);
+                const Item w = first ? i0.next() : i1.next();
+                load(w, first ? 0 : 1, 0);
+                (first ? at0 : at1) += w.tiles();
             }
         } else if (warp == kKWarp || warp == kVWarp) {
             // ------------------------------------------------------------ K and V producers
@@ -280,64 +315,85 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int bs = p.block_size;
             const int box_rows = p.box_rows;
             const int nsub = 128 / box_rows;
+            int st = 0;
+            uint32_t ph = 0; // times the ring has wrapped
+            const uint64_t once = ptx::policy_evict_first(), keep = ptx::policy_evict_last();
+            bool ok = true;
             // cache row of sub-box `lane` of key tile j; one past the pool reads as zeros
-            auto sub_row = [&](const Item &w, const int32_t *bt, int j) -> int {
+            auto sub_row = [&](const Item &w, int j) -> int {
                 const int key = w.k0 + j * 128 + lane * box_rows;
                 if (lane >= nsub || key >= w.k1)
                     return p.num_blocks * bs;
-                const int phys = __ldg(bt + key / bs);
+                const int phys = __ldg(p.block_tables + (size_t)w.row * p.max_blocks + key / bs);
                 if ((uint32_t)phys >= (uint32_t)p.num_blocks) {
                     atomicOr(&g_shared_error, 2u);
                     return p.num_blocks * bs;
                 }
                 return phys * bs + (key & (bs - 1));
             };
-            uint32_t starts = 0;
-            int X = 0;
-            bool ok = true;
-            while (ok && items.more()) {
-                const Item w = items.next();
-                const int32_t *bt = p.block_tables + (size_t)w.row * p.max_blocks;
-                int next = sub_row(w, bt, 0);
-                for (int j = 0; j < w.nkt; ++j, ++X) {
-                    const int cur = next;
-                    if (j + 1 < w.nkt)
-                        next = sub_row(w, bt, j + 1);
-                    starts = (starts << 1) | (j == 0 ? 1u : 0u);
-                    const int st = X % nstages;
-                    if (X >= nstages) {
-                        const int e = release_event(X, nstages, w.ord, starts, is_k ? 0 : 1);
-                        if (!(ok = wwait(bars.released(e), (e / kIterRing) & 1)))
-                            break;
-                    }
-                    const uint32_t full = is_k ? bars.k_full(st) : bars.v_full(st);
-                    const uint32_t dst = ring + st * L::kTileBytes;
-                    if (lane == 0)
-                        ptx::mbar_arrive_expect_tx(full, (uint32_t)L::kTileBytes);
-                    if (lane < nsub) {
-                        for (int pp = 0; pp < L::kPanels; ++pp)
-                            ptx::tma_load_3d(dst + pp * L::kPanelBytes + lane * box_rows * 128, tm, full, pp * 64, w.g,
-                                             cur);
-                    }
-                    __syncwarp();
-                    if (!is_k && w.tail && j == w.nkt - 1) {
-                        // rows of keys past the range may hold anything (even NaN bit patterns): zeroed, so
-                        // that a weight of 0 cannot turn them into NaN
-                        if (!(ok = wwait(full, (X / nstages) & 1)))
-                            break;
-                        uint8_t *tile = sgen + L::kV + st * L::kTileBytes;
-                        const int first = w.k1 - w.k0 - j * 128;
-                        const int chunks = (128 - first) * 8;
-                        for (int pp = 0; pp < L::kPanels; ++pp)
-                            for (int c = lane; c < chunks; c += 32)
-                                *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + (first + (c >> 3)) * 128 +
-                                                           (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0)
-                            ptx::mbar_arrive(bars.v_tail(st));
-                    }
+            // key tile j of w, whose sub-boxes lie at cache row `cur`, into the next slot
+            auto load = [&](const Item &w, int j, int cur, uint64_t policy) {
+                const uint32_t full = is_k ? bars.k_full(st) : bars.v_full(st);
+                if (ph > 0 && !(ok = wwait(is_k ? bars.k_free(st) : bars.v_free(st), (ph - 1) & 1)))
+                    return;
+                const uint32_t dst = ring + st * L::kTileBytes;
+                if (lane == 0)
+                    ptx::mbar_arrive_expect_tx(full, (uint32_t)L::kTileBytes);
+                __syncwarp();
+                if (lane < nsub) {
+                    for (int pp = 0; pp < L::kPanels; ++pp)
+                        ptx::tma_load_3d_hint(dst + pp * L::kPanelBytes + lane * box_rows * 128, tm, full, pp * 64, w.g,
+                                              cur, policy);
                 }
+                __syncwarp();
+                if (!is_k && (w.k1 - w.k0) - j * 128 < 128) {
+                    // rows of keys past the range may hold anything (even NaN bit patterns): zeroed, so
+                    // that a weight of 0 cannot turn them into NaN
+                    if (!(ok = wwait(full, ph & 1)))
+                        return;
+                    uint8_t *tile = sgen + L::kV + st * L::kTileBytes;
+                    const int first = w.k1 - w.k0 - j * 128;
+                    const int chunks = (128 - first) * 8;
+                    for (int pp = 0; pp < L::kPanels; ++pp)
+                        for (int c = lane; c < chunks; c += 32)
+                            *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + (first + (c >> 3)) * 128 +
+                                                       (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(bars.v_tail(st));
+                }
+                if (++st == nstages) {
+                    st = 0;
+                    ++ph;
+                }
+            };
+            for (ItemIter it(p.items, span.x, span.y); ok && it.more();) {
+                const Item w = it.next();
+                const int n = w.tiles();
+                int next = sub_row(w, 0);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int cur = next;
+                    if (j + 1 < n)
+                        next = sub_row(w, j + 1);
+                    load(w, j, cur, keep);
+                }
+            }
+            Lane l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
+            int r0 = l0.active ? sub_row(l0.w, 0) : 0, r1 = l1.active ? sub_row(l1.w, 0) : 0;
+            auto advance = [&](Lane &l, int &r) { // this tile's load, the next one's row looked up before it
+                const Item w = l.w;
+                const int j = l.j, cur = r;
+                l.step();
+                if (l.active)
+                    r = sub_row(l.w, l.j);
+                load(w, j, cur, w.nseq == 1 ? once : keep);
+            };
+            while (ok && (l0.active || l1.active)) {
+                if (l0.active)
+                    advance(l0, r0);
+                if (ok && l1.active)
+                    advance(l1, r1);
             }
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------------------ MMA issuer (converged warp)
@@ -346,7 +402,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t hi_k = (uint32_t)(ptx::smem_desc(0, 16, 1024, ptx::kSwizzle128B) >> 32);
             const uint32_t hi_v = (uint32_t)(ptx::smem_desc(0, L::kPanelBytes, 1024, ptx::kSwizzle128B) >> 32);
             auto desc = [](uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; };
-            auto issue_s = [&](int t, int ks) {
+            int ks = 0, kph = 0, vs = 0, vph = 0;
+            uint32_t qpar = 0, ppar = 0; // bit t: parity of tile t's queries and weights consumed so far
+            uint32_t tailpar = 0;        // bit s: parity of the tail tiles V slot s has held
+            bool ok = true;
+            auto issue_s = [&](int t) {
                 uint32_t qa = (uint32_t)ptx::smem_desc(sbase + L::kQ + t * L::kTileBytes, 16, 1024, ptx::kSwizzle128B);
                 uint32_t kb = (uint32_t)ptx::smem_desc(sbase + L::kK + ks * L::kTileBytes, 16, 1024, ptx::kSwizzle128B);
                 asm volatile("" : "+r"(qa), "+r"(kb));
@@ -355,8 +415,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t o = ((kk >> 2) * L::kPanelBytes + (kk & 3) * 32) >> 4;
                     ptx::mma_bf16_ss_warp(tmem + t * 256, desc(qa + o, hi_k), desc(kb + o, hi_k), idesc_s, kk > 0);
                 }
+                ptx::mma_commit_warp(bars.s_full(t));
             };
-            auto issue_pv = [&](int t, int vs, bool first) {
+            auto issue_pv = [&](int t, bool first) {
                 uint32_t vb = (uint32_t)ptx::smem_desc(sbase + L::kV + vs * L::kTileBytes, L::kPanelBytes, 1024,
                                                        ptx::kSwizzle128B);
                 asm volatile("" : "+r"(vb));
@@ -365,81 +426,127 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::mma_bf16_ts_warp(tmem + t * 256 + 128, tmem + t * 256 + kk * 8,
                                           desc(vb + kk * (2048 >> 4), hi_v), idesc_o, (!first || kk > 0) ? 1u : 0u);
             };
-            int ks = 0, kph = 0, vs = 0, vph = 0;
-            uint32_t np = 0;      // bit t: parity of the P tiles of tile t consumed so far
-            uint32_t n1items = 0; // items with a second tile so far (its query buffer's parity)
-            uint32_t tailpar = 0; // bit s: parity of the tail tiles V slot s has held
-            int E = 0;
-            bool ok = true;
-            while (ok && items.more()) {
-                const Item w = items.next();
-                const int nt = w.n1 > 0 ? 2 : 1;
-                if (!(ok = wwait(bars.q_full(0), w.ord & 1) && wwait(bars.k_full(ks), kph)))
-                    break;
+            auto wait_q = [&](int t) {
+                ok = ok && wwait(bars.q_full(t), (qpar >> t) & 1u);
+                qpar ^= 1u << t;
+            };
+            auto wait_p = [&](int t) {
+                ok = ok && wwait(bars.p_full(t), (ppar >> t) & 1u);
+                ppar ^= 1u << t;
+            };
+            auto wait_k = [&]() {
+                ok = ok && wwait(bars.k_full(ks), kph);
                 ptx::tc_fence_after();
-                issue_s(0, ks);
-                ptx::mma_commit_warp(bars.s_full(0));
-                if (nt == 2) {
-                    if (!(ok = wwait(bars.q_full(1), n1items & 1)))
-                        break;
-                    ++n1items;
-                    ptx::tc_fence_after();
-                    issue_s(1, ks);
-                    ptx::mma_commit_warp(bars.s_full(1));
+            };
+            auto wait_v = [&](bool tail) {
+                ok = ok && wwait(bars.v_full(vs), vph);
+                if (tail) {
+                    ok = ok && wwait(bars.v_tail(vs), (tailpar >> vs) & 1u);
+                    tailpar ^= 1u << vs;
                 }
-                ptx::mma_commit_warp(bars.released(E)); // K tile 0 read
-                if (w.nkt == 1)
-                    ptx::mma_commit_warp(bars.q_free(0));
-                if (nt == 1 || w.nkt == 1)
-                    ptx::mma_commit_warp(bars.q_free(1));
+                ptx::tc_fence_after();
+            };
+            auto pass_k = [&]() { // the K tile has been read by everything issued so far
+                ptx::mma_commit_warp(bars.k_free(ks));
                 if (++ks == L::kKStages) {
                     ks = 0;
                     kph ^= 1;
                 }
-                for (int j = 0; ok && j < w.nkt; ++j) {
-                    const bool more = j + 1 < w.nkt;
-                    for (int t = 0; t < nt; ++t) { // PV(t, j), then S(t, j + 1) into the same columns
-                        if (!(ok = wwait(bars.p_full(t), (np >> t) & 1u)))
+            };
+            auto pass_v = [&]() {
+                ptx::mma_commit_warp(bars.v_free(vs));
+                if (++vs == L::kVStages) {
+                    vs = 0;
+                    vph ^= 1;
+                }
+            };
+            for (ItemIter it(p.items, span.x, span.y); ok && it.more();) {
+                const Item w = it.next();
+                const int n = w.tiles();
+                const bool tail = w.tail();
+                wait_q(0);
+                wait_k();
+                if (!ok)
+                    break;
+                issue_s(0);
+                wait_q(1);
+                if (!ok)
+                    break;
+                ptx::tc_fence_after();
+                issue_s(1);
+                if (n == 1) {
+                    ptx::mma_commit_warp(bars.q_free(0));
+                    ptx::mma_commit_warp(bars.q_free(1));
+                }
+                pass_k();
+                for (int j = 0; j < n; ++j) {
+                    const bool more = j + 1 < n;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) { // PV(t, j), then S(t, j + 1) into the same columns
+                        wait_p(t);
+                        if (t == 0)
+                            wait_v(tail && !more);
+                        else
+                            ptx::tc_fence_after();
+                        if (!ok)
                             break;
-                        np ^= 1u << t;
-                        if (t == 0) {
-                            if (!(ok = wwait(bars.v_full(vs), vph)))
-                                break;
-                            if (w.tail && !more) {
-                                if (!(ok = wwait(bars.v_tail(vs), (tailpar >> vs) & 1u)))
-                                    break;
-                                tailpar ^= 1u << vs;
-                            }
-                        }
-                        ptx::tc_fence_after();
-                        issue_pv(t, vs, j == 0);
+                        issue_pv(t, j == 0);
                         if (!more) {
                             ptx::mma_commit_warp(bars.o_full(t));
                         } else {
-                            if (t == 0) {
-                                if (!(ok = wwait(bars.k_full(ks), kph)))
-                                    break;
-                                ptx::tc_fence_after();
-                            }
-                            issue_s(t, ks);
-                            ptx::mma_commit_warp(bars.s_full(t));
-                            if (j + 2 == w.nkt)
+                            if (t == 0)
+                                wait_k();
+                            if (!ok)
+                                break;
+                            issue_s(t);
+                            if (j + 2 == n)
                                 ptx::mma_commit_warp(bars.q_free(t));
                         }
                     }
                     if (!ok)
                         break;
-                    ptx::mma_commit_warp(bars.released(E + j + 1));
-                    if (++vs == L::kVStages) {
-                        vs = 0;
-                        vph ^= 1;
-                    }
-                    if (more && ++ks == L::kKStages) {
-                        ks = 0;
-                        kph ^= 1;
-                    }
+                    pass_v();
+                    if (more)
+                        pass_k();
                 }
-                E += w.nkt + 1;
+            }
+            Lane l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
+            // score product of the lane's current key tile
+            auto score = [&](const Lane &l, int t) {
+                if (l.j == 0)
+                    wait_q(t);
+                wait_k();
+                if (!ok)
+                    return;
+                issue_s(t);
+                if (l.j + 1 == l.n)
+                    ptx::mma_commit_warp(bars.q_free(t));
+                pass_k();
+            };
+            // value product of the lane's current key tile, then the next one's scores
+            auto step = [&](Lane &l, int t) {
+                const bool last = l.j + 1 == l.n;
+                wait_p(t);
+                wait_v(last && l.w.tail());
+                if (!ok)
+                    return;
+                issue_pv(t, l.j == 0);
+                if (last)
+                    ptx::mma_commit_warp(bars.o_full(t));
+                pass_v();
+                l.step();
+                if (l.active)
+                    score(l, t);
+            };
+            if (ok && l0.active)
+                score(l0, 0);
+            if (ok && l1.active)
+                score(l1, 1);
+            while (ok && (l0.active || l1.active)) {
+                if (l0.active)
+                    step(l0, 0);
+                if (ok && l1.active)
+                    step(l1, 1);
             }
         }
         __syncwarp();
@@ -456,17 +563,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sl2 = p.scale_log2;
         uint32_t ns = 0, no = 0;
         bool ok = true;
-        while (ok && items.more()) {
-            const Item w = items.next(false);
-            const int nseq = t == 0 ? w.n0 : w.n1;
-            if (nseq == 0) {
-                items.fetch();
+        ItemIter items(p.items, span.x, span.y);
+        bool single = false;
+        while (ok) {
+            if (!items.more()) {
+                if (single)
+                    break;
+                single = true;
+                items = t == 0 ? ItemIter(p.items, span.y, span.z) : ItemIter(p.items, span.z, span.w);
                 continue;
             }
+            const Item w = items.next(false);
+            const int nseq = single ? w.nseq : t == 0 ? P : w.nseq - P;
+            const int n = w.tiles();
             const bool row_valid = r < G * nseq;
             const bool warp_valid = quarter * 32 < G * nseq;
+            const int seq = w.s0 + (single ? 0 : t * P) + rpos;
+            // first slot and number of parts of this row's sequence (an item's sequences may differ: one
+            // whose context ends with the prefix has no suffix part)
+            const int2 sp = row_valid ? __ldg(p.seq_parts + seq) : make_int2(0, 1);
             float m_ref = -INFINITY, l_sum = 0.f;
-            for (int j = 0; j < w.nkt; ++j) {
+            for (int j = 0; j < n; ++j) {
                 if (!(ok = wwait(bars.s_full(t), ns & 1)))
                     break;
                 ns ^= 1;
@@ -575,11 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             ptx::tc_fence_after();
             const float inv = (row_valid && l_sum > 0.f) ? 1.f / l_sum : 0.f;
-            const int seq = w.s0 + t * P + rpos;
             const size_t head = (size_t)w.g * G + rhead;
-            // first slot and number of parts of this row's sequence (an item's sequences may differ: one
-            // whose context ends with the prefix has no suffix part)
-            const int2 sp = row_valid ? __ldg(p.seq_parts + seq) : make_int2(0, 1);
             const bool partial = sp.y > 1;
             const size_t slot = (size_t)sp.x + w.part;
             float *po = p.part_o + (slot * p.num_heads + head) * D;
@@ -717,7 +830,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     const int G = d.num_heads / d.num_kv_heads;
     if (a.num_items > 0) {
         const uint64_t rows = (uint64_t)d.num_blocks * d.block_size;
-        const uint32_t box_rows = d.block_size < 128 ? (uint32_t)d.block_size : 128u;
+        const uint32_t box_rows = d.block_size < kBoxRows ? (uint32_t)d.block_size : (uint32_t)kBoxRows;
         constexpr CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
         constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
         const uint64_t qs = (uint64_t)d.num_heads * D * 2, cs = (uint64_t)d.num_kv_heads * D * 2;
@@ -734,7 +847,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
             return rc;
         ShParams p{};
         p.items = reinterpret_cast<const int4 *>(a.items);
-        p.cta_items = a.cta_items;
+        p.cta_items = reinterpret_cast<const int4 *>(a.cta_items);
         p.seq_parts = reinterpret_cast<const int2 *>(a.seq_parts);
         p.block_tables = a.block_tables;
         p.out = static_cast<__nv_bfloat16 *>(a.out);
@@ -753,10 +866,12 @@ int launch(const SharedArgs &a, cudaStream_t stream)
         if (e != cudaSuccess)
             return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
     }
-    if (!a.combine)
+    if (!a.merge)
         return PA_OK;
-    // Programmatic launch: the combine's blocks are set up while the parts still run and wait
-    // inside for the end of that grid.  Without a grid before it, it waits for nothing.
+    // Programmatic launch: the merge's blocks are set up while the parts still run and wait
+    // inside for the end of that grid.  Without a grid before it, it waits for nothing.  (One
+    // cooperative launch whose CTAs met before merging took 3 us longer on a batch of 8 x 300
+    // tokens and 15 us longer on 256 x 33300.)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.num_seqs, (unsigned)((d.num_heads + 3) / 4));
     cfg.blockDim = dim3(128);
@@ -772,7 +887,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
                            (int)d.num_heads);
     if (e != cudaSuccess) {
         cudaGetLastError();
-        return fail(PA_ERR_CUDA, "shared decode combine launch: %s", cudaGetErrorString(e));
+        return fail(PA_ERR_CUDA, "shared decode merge launch: %s", cudaGetErrorString(e));
     }
     return PA_OK;
 }

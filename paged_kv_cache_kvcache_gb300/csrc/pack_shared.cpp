@@ -18,11 +18,12 @@ namespace {
 
 constexpr int32_t kTile = kPrefillKeyTile;
 
-// Time model of the kernel in microseconds on one SM, used only to choose the key ranges and
-// to deal the items out (measured on GB300, D = 128): an iteration of 128 keys with two query
-// tiles is bound by the tensor core, with one by the loads of K and V; an item adds its query
-// load and its output.  The merge reads and writes every partial once at HBM speed.
-constexpr float kPairStep = 1.75f, kSingleStep = 1.25f, kItemCost = 1.5f, kMergeBytesPerUs = 5.0e6f;
+// Time model of the kernel in microseconds, used only to choose the key ranges and to deal the
+// items out (measured on GB300, D = 128).  A pair (two query tiles on one K/V stream) occupies
+// both lanes of its CTA and is bound by the tensor core; a single occupies one lane, and two
+// lanes' loads share the SM's part of the HBM rate.  An item adds its query load and its
+// output.  The merge reads and writes every partial once.
+constexpr float kPairStep = 1.62f, kSingleStep = 2.8f, kPairItem = 2.5f, kSingleItem = 1.5f, kMergeBytesPerUs = 5.0e6f;
 
 struct Run { // consecutive sequences of a group that share `shared` tokens
     int32_t s0, n, shared;
@@ -32,7 +33,10 @@ struct Range { // one part of a context: units items per split
     int32_t tiles, units_pair, units_single;
 };
 
-float item_cost(int32_t tiles, bool pair) { return (float)tiles * (pair ? kPairStep : kSingleStep) + kItemCost; }
+float item_cost(int32_t tiles, bool pair)
+{
+    return pair ? (float)tiles * kPairStep + kPairItem : (float)tiles * kSingleStep + kSingleItem;
+}
 
 struct Work {
     int32_t s0, n, g, row, k0, k1, part;
@@ -182,24 +186,27 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         float best = INFINITY;
         const float slot_us = (float)d.num_heads * d.head_dim * 8.f / kMergeBytesPerUs;
         for (int32_t c : kPer) {
-            float work = 0.f, longest = 0.f, slots = 0.f;
-            int64_t items = 0;
+            float work = 0.f, pair = 0.f, single = 0.f, slots = 0.f; // lane time, longest items, partial slots
+            int64_t pairs = 0, singles = 0;
             for (size_t i = 0; i < ranges.size(); ++i) {
                 const Range &x = ranges[i];
                 const int32_t s = splits_of(x.tiles, c), len = splits_of(x.tiles, s);
-                const float whole = (float)x.tiles;
                 if (x.units_pair)
-                    longest = std::max(longest, item_cost(len, true));
+                    pair = std::max(pair, item_cost(len, true));
                 if (x.units_single)
-                    longest = std::max(longest, item_cost(len, false));
-                work += x.units_pair * (whole * kPairStep + s * kItemCost) +
-                        x.units_single * (whole * kSingleStep + s * kItemCost);
-                items += (int64_t)s * (x.units_pair + x.units_single);
+                    single = std::max(single, item_cost(len, false));
+                work += 2 * x.units_pair * (x.tiles * kPairStep + s * kPairItem) +
+                        x.units_single * (x.tiles * kSingleStep + s * kSingleItem);
+                pairs += (int64_t)s * x.units_pair;
+                singles += (int64_t)s * x.units_single;
                 slots += (float)s * range_seqs[i];
             }
-            // list scheduling ends at most one item late; with few items per SM that is what counts
-            const float even = work / sms;
-            const float t = (items <= sms ? longest : std::max(longest, even + 0.5f * longest)) + slots * slot_us;
+            // pairs are dealt out first, in rounds over the CTAs; singles fill up what the rounds leave
+            // uneven, and the lanes then end within about half of a single of one another
+            float t = std::max((float)((pairs + sms - 1) / sms) * pair, single);
+            if (2 * pairs + singles > 2 * sms)
+                t = std::max(t, work / (2 * sms) + 0.5f * single);
+            t += slots * slot_us;
             if (t < best) {
                 best = t;
                 per = c;
@@ -245,11 +252,11 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         return fail(PA_ERR_INVALID_ARG, "too many work items");
     int64_t partials = 0;
     int32_t max_parts = 0;
-    bool combine = false;
+    bool merge = false;
     for (int32_t b = 0; b < num_seqs; ++b) {
         max_parts = std::max(max_parts, parts[b]);
         partials += parts[b] > 1 ? parts[b] : 0;
-        combine = combine || parts[b] != 1;
+        merge = merge || parts[b] != 1;
     }
     if (partials > INT32_MAX)
         return fail(PA_ERR_INVALID_ARG, "too many partial results");
@@ -265,7 +272,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->num_partials = (int32_t)partials;
     meta->max_parts = max_parts;
     meta->rows_per_tile = P;
-    meta->combine = combine ? 1 : 0;
+    meta->merge = merge ? 1 : 0;
     meta->split_tokens = (int32_t)std::min<int64_t>((int64_t)per * kTile, INT32_MAX / kTile * kTile);
     meta->tables_packed = packed ? 1 : 0;
     for (const Run &r : runs)
@@ -273,7 +280,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->off_block_tables = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs * mb : 0);
     meta->off_slot_mapping = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs : 0);
     meta->off_items = L.take(sizeof(int32_t) * kSharedItemInts * works.size());
-    meta->off_cta_items = L.take(sizeof(int32_t) * ((size_t)ctas + 1));
+    meta->off_cta_items = L.take(sizeof(int32_t) * 4 * (size_t)ctas);
     meta->off_seq_parts = L.take(sizeof(int32_t) * 2 * (size_t)num_seqs);
     meta->total_bytes = L.off;
     meta->workspace_bytes = partials > 0 ? align_up((size_t)partials * d.num_heads * d.head_dim * 4, 256) +
@@ -303,30 +310,52 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         sp[2 * b + 1] = parts[b];
         slot += parts[b] > 1 ? parts[b] : 0;
     }
-    // deal out: longest first, each to the CTA with the least work so far
-    std::vector<int32_t> order(works.size()), cta_of(works.size()), fill((size_t)ctas + 1, 0);
+    // Deal out, longest first, to the least loaded: pairs to CTAs (both lanes), then singles to
+    // lanes.  Queue 3c holds CTA c's pairs, 3c + 1 and 3c + 2 its lanes' singles.
+    std::vector<int32_t> order(works.size()), queue_of(works.size()), fill(3 * (size_t)ctas, 0);
     for (size_t i = 0; i < order.size(); ++i)
         order[i] = (int32_t)i;
-    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return works[x].cost > works[y].cost; });
+    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) {
+        const bool px = works[x].n > P, py = works[y].n > P;
+        return px != py ? px : works[x].cost > works[y].cost;
+    });
     using Load = std::pair<float, int32_t>;
+    std::vector<float> load((size_t)ctas, 0.f);
     std::priority_queue<Load, std::vector<Load>, std::greater<Load>> heap;
     for (int32_t c = 0; c < ctas; ++c)
         heap.push({0.f, c});
-    for (int32_t i : order) {
+    size_t at = 0;
+    for (; at < order.size() && works[order[at]].n > P; ++at) {
         Load l = heap.top();
         heap.pop();
-        cta_of[i] = l.second;
-        ++fill[(size_t)l.second + 1];
-        l.first += works[i].cost;
+        queue_of[order[at]] = 3 * l.second;
+        ++fill[3 * (size_t)l.second];
+        load[l.second] = l.first += works[order[at]].cost;
         heap.push(l);
     }
-    ci[0] = 0;
-    for (int32_t c = 0; c < ctas; ++c)
-        ci[c + 1] = ci[c] + fill[(size_t)c + 1];
-    std::vector<int32_t> at(ci, ci + ctas);
+    heap = {};
+    for (int32_t c = 0; c < 2 * ctas; ++c) // first lanes before second ones
+        heap.push({load[c % ctas], c});
+    for (; at < order.size(); ++at) {
+        Load l = heap.top();
+        heap.pop();
+        const int32_t q = 3 * (l.second % ctas) + 1 + l.second / ctas;
+        queue_of[order[at]] = q;
+        ++fill[q];
+        l.first += works[order[at]].cost;
+        heap.push(l);
+    }
+    std::vector<int32_t> next(fill.size(), 0);
+    for (size_t q = 1; q < fill.size(); ++q)
+        next[q] = next[q - 1] + fill[q - 1];
+    for (int32_t c = 0; c < ctas; ++c) {
+        for (int32_t i = 0; i < 3; ++i)
+            ci[4 * c + i] = next[3 * (size_t)c + i];
+        ci[4 * c + 3] = next[3 * (size_t)c + 2] + fill[3 * (size_t)c + 2];
+    }
     for (int32_t i : order) {
         const Work &w = works[i];
-        int32_t *e = it + (size_t)kSharedItemInts * at[cta_of[i]]++;
+        int32_t *e = it + (size_t)kSharedItemInts * next[queue_of[i]]++;
         e[0] = w.s0;
         e[1] = w.n;
         e[2] = w.g;

@@ -61,7 +61,7 @@ class pa_decode_meta(ctypes.Structure):
 class pa_shared_meta(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
                 ("num_items", ctypes.c_int32), ("num_ctas", ctypes.c_int32), ("num_partials", ctypes.c_int32),
-                ("max_parts", ctypes.c_int32), ("rows_per_tile", ctypes.c_int32), ("combine", ctypes.c_int32),
+                ("max_parts", ctypes.c_int32), ("rows_per_tile", ctypes.c_int32), ("merge", ctypes.c_int32),
                 ("split_tokens", ctypes.c_int32), ("tables_packed", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("tokens_saved", ctypes.c_uint64), ("off_block_tables", ctypes.c_uint64),
                 ("off_slot_mapping", ctypes.c_uint64), ("off_items", ctypes.c_uint64),
@@ -150,8 +150,15 @@ def pa_version() -> int:
     return int(lib().pa_version())
 
 
+# torch's own lookup of the current stream without building a Stream object (3 us of a call's 10)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cur_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None and _cur_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_cur_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -164,6 +171,13 @@ def _ptr(t) -> Optional[int]:
     if isinstance(t, torch.Tensor):
         return t.data_ptr() if t.numel() > 0 else None
     return int(t)
+
+
+def _int32(t, what: str, count: Optional[int] = None) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous() or \
+            (count is not None and t.numel() != count):
+        raise ValueError(f"{what} must be a contiguous int32 tensor" + ("" if count is None else f" of {count}"))
+    return t
 
 
 def make_dims(num_blocks: int, block_size: int, num_heads: int, num_kv_heads: int, head_dim: int) -> pa_dims:
@@ -227,6 +241,14 @@ class DecodePlan(_Plan):
 
 
 class SharedPlan(_Plan):
+    def upload(self, device="cuda", stream=None) -> "SharedPlan":
+        super().upload(device, stream)
+        m, base = self.meta, self.dev.data_ptr()
+        self.call_ref = ctypes.byref(m)
+        self.call_tables = base + m.off_block_tables if m.tables_packed or m.num_seqs == 0 else None
+        self.call_arrays = tuple(base + x for x in (m.off_items, m.off_cta_items, m.off_seq_parts))
+        return self
+
     @property
     def slot_mapping(self) -> int:
         """Device address of each last token's slot (plans packed from block lists)."""
@@ -387,25 +409,26 @@ def pa_decode_static(dims: pa_dims, q, k_cache, v_cache, plan: DecodePlan, scale
                                   _stream(stream)), "pa_decode_static")
 
 
+def _nbytes(workspace) -> int:
+    return workspace.numel() if isinstance(workspace, torch.Tensor) else 0
+
+
 def shared_workspace(plan: SharedPlan, device="cuda") -> Optional[torch.Tensor]:
     n = int(plan.meta.workspace_bytes)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
-def _shared_args(plan: SharedPlan, block_tables, workspace):
-    """(tables, (items, cta_items, seq_parts), workspace bytes) of a shared-prefix decode call."""
-    m = plan.meta
+def _shared_tables(plan: SharedPlan, block_tables) -> int:
+    """Address of the block tables of a shared-prefix decode: the plan's, or the caller's."""
+    assert plan.dev is not None, "upload the plan first"
     if block_tables is None:
-        if not m.tables_packed and m.num_seqs > 0:
+        if plan.call_tables is None:
             raise ValueError("the plan was packed for device tables: pass block_tables")
-        block_tables = plan.dptr(m.off_block_tables)
-    elif isinstance(block_tables, torch.Tensor):
-        if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or not block_tables.is_contiguous() or \
-                block_tables.shape[1] != m.max_blocks_per_seq:
-            raise ValueError(f"block_tables must be a contiguous int32 [rows, {m.max_blocks_per_seq}] tensor")
-    ws_bytes = int(workspace.numel()) if isinstance(workspace, torch.Tensor) else 0
-    return (_ptr(block_tables), (plan.dptr(m.off_items), plan.dptr(m.off_cta_items), plan.dptr(m.off_seq_parts)),
-            ws_bytes)
+        return plan.call_tables
+    _int32(block_tables, "block_tables")
+    if block_tables.dim() != 2 or block_tables.shape[1] != plan.meta.max_blocks_per_seq:
+        raise ValueError(f"block_tables must be [rows, {plan.meta.max_blocks_per_seq}]")
+    return block_tables.data_ptr()
 
 
 def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale: float, out, workspace=None,
@@ -414,9 +437,9 @@ def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale
 
     ``block_tables``: the device table a plan without block lists was packed for.
     """
-    bt, arrays, ws_bytes = _shared_args(plan, block_tables, workspace)
-    _check(lib().pa_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), bt, float(scale),
-                                  _ptr(out), ctypes.byref(plan.meta), *arrays, _ptr(workspace), ws_bytes,
+    bt = _shared_tables(plan, block_tables)
+    _check(lib().pa_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), bt, scale, _ptr(out),
+                                  plan.call_ref, *plan.call_arrays, _ptr(workspace), _nbytes(workspace),
                                   _stream(stream)), "pa_decode_shared")
 
 
@@ -425,13 +448,6 @@ def pa_copy_blocks(dims: pa_dims, k_cache, v_cache, triples, num_triples: Option
     n = int(triples.shape[0]) if num_triples is None else int(num_triples)
     _check(lib().pa_copy_blocks(ctypes.byref(dims), _ptr(k_cache), _ptr(v_cache), _ptr(triples), n,
                                 _stream(stream)), "pa_copy_blocks")
-
-
-def _int32(t, what: str, count: Optional[int] = None) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous() or \
-            (count is not None and t.numel() != count):
-        raise ValueError(f"{what} must be a contiguous int32 tensor" + ("" if count is None else f" of {count}"))
-    return t
 
 
 class PagePool:

@@ -32,7 +32,7 @@ def make_batch(seed, sizes, shared_blocks, tails, bs):
 def arrays(plan):
     m = plan.meta
     return (plan.host_array(m.off_items, 8 * m.num_items).reshape(-1, 8),
-            plan.host_array(m.off_cta_items, m.num_ctas + 1),
+            plan.host_array(m.off_cta_items, 4 * m.num_ctas).reshape(-1, 4),
             plan.host_array(m.off_seq_parts, 2 * m.num_seqs).reshape(-1, 2))
 
 
@@ -59,7 +59,11 @@ def test_parts_cover_every_key_once(case):
     B = len(ctx)
     P = 128 // (hq // hkv)
     assert m.rows_per_tile == P and m.num_seqs == B
-    assert cta[0] == 0 and cta[-1] == m.num_items and (np.diff(cta) >= 1).all()
+    if m.num_items:  # CTA by CTA: pairs, first lane, second lane
+        assert cta[0, 0] == 0 and cta[-1, 3] == m.num_items and (cta[1:, 0] == cta[:-1, 3]).all()
+        assert (np.diff(cta, axis=1) >= 0).all() and (cta[:, 3] > cta[:, 0]).all()
+        for first, l0, l1, end in cta.tolist():
+            assert (items[first:l0, 1] > P).all() and (items[l0:end, 1] <= P).all()
     table = plan.host_array(m.off_block_tables, B * m.max_blocks_per_seq).reshape(B, -1)
     for b in range(B):
         n = -(-ctx[b] // bs)
@@ -82,7 +86,7 @@ def test_parts_cover_every_key_once(case):
     slots = [s for b in range(B) if parts[b, 1] > 1 for s in range(parts[b, 0], parts[b, 0] + parts[b, 1])]
     assert slots == list(range(m.num_partials))
     assert all(parts[b, 1] == 0 for b in range(B) if ctx[b] == 0) and m.max_parts == max(parts[:, 1])
-    assert m.combine == int(any(parts[:, 1] != 1))
+    assert m.merge == int(any(parts[:, 1] != 1))
     # what a group of n live sequences with s shared tokens saves
     saved, at = 0, 0
     for n, s in zip(sizes, sh):
@@ -94,13 +98,13 @@ def test_parts_cover_every_key_once(case):
 
 
 def test_items_are_dealt_out_evenly():
-    """No CTA gets more than one item's worth of key tiles above the mean."""
+    """No lane gets more than one item's worth of time above the mean."""
     ctx, lists, groups, nb = make_batch(2, [64], [40], [5 + 11 * i for i in range(64)], 64)
     dims = pa.make_dims(nb, 64, 28, 4, 128)
     plan = pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=256, pin=False)
     items, cta, _ = arrays(plan)
-    cost = [(1.75 if n > 18 else 1.25) * -(-(k1 - k0) // 128) + 1.5 for _, n, _, _, k0, k1, _, _ in items.tolist()]
-    load = [sum(cost[a:b]) for a, b in zip(cta[:-1], cta[1:])]
+    cost = [(1.62 if n > 18 else 2.8) * -(-(k1 - k0) // 128) + (2.5 if n > 18 else 1.5) for _, n, _, _, k0, k1, _, _ in items.tolist()]
+    load = [sum(cost[p:l0]) + sum(cost[a:b]) for p, l0, l1, end in cta.tolist() for a, b in ((l0, l1), (l1, end))]
     assert max(load) <= sum(load) / len(load) + max(cost)
 
 
@@ -185,5 +189,5 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     assert call(ws=None, nbytes=4096) == pa.PA_ERR_INVALID_ARG
     m.workspace_bytes = 512                                                    # not this batch's size
     assert call(ws=256, nbytes=4096) == pa.PA_ERR_INVALID_ARG
-    m.num_ctas = 5
+    m.num_ctas = 0
     assert call(ws=256, nbytes=4096) == pa.PA_ERR_INVALID_ARG
