@@ -517,6 +517,35 @@ extern "C" int pa_decode_shared(const pa_dims *dims, const void *q, const void *
     return launch_decode_shared(a, stream);
 }
 
+extern "C" int pa_decode_shared_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                                     const void *k_scale, const void *v_scale, const int32_t *block_tables, float scale,
+                                     void *out, const pa_shared_meta *meta, const int32_t *items,
+                                     const int32_t *cta_items, const int32_t *seq_parts, const int32_t *single_items,
+                                     const int32_t *table_rows, void *workspace, size_t workspace_bytes,
+                                     pa_stream_t stream)
+{
+    SharedArgs a;
+    bool nothing = false;
+    int rc = prepare_shared("pa_decode_shared_int8", dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
+                            cta_items, seq_parts, workspace, workspace_bytes, &a, &nothing);
+    if (rc != PA_OK || nothing)
+        return rc;
+    if (meta->num_single_items < 0 || meta->num_shared_items < 0 || meta->num_shared_items > meta->num_items)
+        return fail(PA_ERR_INVALID_ARG, "malformed shared decode meta");
+    if (!k_scale || !v_scale || !single_items || !table_rows)
+        return fail(PA_ERR_INVALID_ARG, "pa_decode_shared_int8: NULL pointer");
+    if (misaligned(k_scale) || misaligned(v_scale) || misaligned(single_items) ||
+        (reinterpret_cast<uintptr_t>(table_rows) & 3u))
+        return fail(PA_ERR_INVALID_ARG, "pa_decode_shared_int8: scales and items must be 16-byte aligned");
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.single_items = single_items;
+    a.table_rows = table_rows;
+    a.num_items = meta->num_shared_items;
+    a.num_single_items = meta->num_single_items;
+    return launch_decode_shared(a, stream);
+}
+
 extern "C" int pa_copy_blocks(const pa_dims *dims, void *k_cache, void *v_cache, const int32_t *triples,
                               int32_t num_triples, pa_stream_t stream)
 {

@@ -120,6 +120,9 @@ struct DecParams8 {
     const int32_t *slot_mapping;
     const int32_t *context_lens;
     int64_t num_slots;
+    // parts of a shared-prefix decode (SHARED kernels only): block-table row of each sequence, pool size
+    const int32_t *table_rows;
+    int32_t num_blocks;
 };
 
 __device__ uint32_t g_fused8_error; // bit 0: a fused-store slot outside [-1, num_slots) was skipped
@@ -152,7 +155,10 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[D / 32], float
 // being decoded) quantises that token's K/V rows of its head, writes codes and
 // scales into the cache slot and takes the key from its own registers (the
 // dequantised values the cache now holds) instead of from the cache.
-template <int D, int NT, bool FUSED>
+// SHARED: the items are a shared-prefix decode's parts of single sequences.  Their table may
+// be the caller's: a block id outside the pool reads as zeros and sets bit 1 of g_decode_error.
+// The launch may run beside the one before it (the shared parts); its last block ends after that one.
+template <int D, int NT, bool FUSED, bool SHARED>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     decode_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const DecParams8 p)
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     const uint32_t wbase = sbase + warp * L::kWarpBytes;
     const uint32_t sc_base = sbase + L::kScaleOff + warp * kStages * 64;
     const uint32_t bar_base = sbase + L::kBarOff + warp * kStages * 8;
-    const int32_t *bt_row = p.block_tables + (size_t)b * p.max_blocks;
+    const int32_t *bt_row = p.block_tables + (size_t)(SHARED ? __ldg(p.table_rows + b) : b) * p.max_blocks;
     const int bs = p.block_size;
     const int Hkv = p.num_kv_heads;
     int blk_cache = 0;
@@ -199,14 +205,22 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
             const int key = k0 + 16 * (warp + kWarps * (i + lane));
             blk_cache = key < k1 ? __ldg(bt_row + key / bs) : 0;
         }
-        const int phys = __shfl_sync(0xffffffffu, blk_cache, i & 31);
+        int phys = __shfl_sync(0xffffffffu, blk_cache, i & 31);
         if (lane == 0) {
+            bool inside = true;
+            if constexpr (SHARED) {
+                inside = (uint32_t)phys < (uint32_t)p.num_blocks;
+                if (!inside) {
+                    phys = p.num_blocks; // past the pool: the codes read as zeros
+                    atomicOr(&g_decode_error, 2u);
+                }
+            }
             const int key0 = k0 + 16 * (warp + kWarps * i);
             const int off0 = key0 & (bs - 1); // a chunk never crosses a block (bs >= 16, key0 % 16 == 0)
             const int st = i % kStages;
             const uint32_t bar = bar_base + 8 * st;
             const uint32_t dst = wbase + st * L::kStageBytes;
-            const size_t si = ((size_t)phys * Hkv + g) * bs + off0;
+            const size_t si = inside ? ((size_t)phys * Hkv + g) * bs + off0 : 0; // (zeros times any scale)
             ptx::mbar_arrive_expect_tx(bar, L::kTxBytes);
             ptx::tma_load_3d(dst, &tm_k, bar, 0, g, phys * bs + off0);
             ptx::tma_load_3d(dst + L::kChunkBytes, &tm_v, bar, 0, g, phys * bs + off0);
@@ -498,12 +512,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
                 p.part_lse[(size_t)pslot * Hq + h] = Lsum > 0.f ? M + __log2f(Lsum) : -INFINITY;
         }
     }
+    if constexpr (SHARED) {
+        if (blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
+            ptx::grid_dependency_wait();
+    }
 }
 
-template <int D, int NT, bool FUSED>
+template <int D, int NT, bool FUSED, bool SHARED = false>
 int launch_int8(const DecodeArgs &a, const DecParams8 &p, cudaStream_t stream)
 {
-    if (int rc = ensure_smem<decode_int8_kernel<D, NT, FUSED>>(DecLayout8<D>::kSmemBytes, "decode_int8"))
+    if (int rc = ensure_smem<decode_int8_kernel<D, NT, FUSED, SHARED>>(DecLayout8<D>::kSmemBytes, "decode_int8"))
         return rc;
     // codes as uint8 [num_slots][Hkv][D]: box = one head's D bytes x 16 token rows
     const pa_dims &d = a.dims;
@@ -520,7 +538,25 @@ int launch_int8(const DecodeArgs &a, const DecParams8 &p, cudaStream_t stream)
     // flat grid, heads of one work item adjacent: they read neighbouring
     // segments of the same token rows at about the same time (DRAM locality)
     dim3 grid((unsigned)(a.num_items * a.dims.num_kv_heads));
-    decode_int8_kernel<D, NT, FUSED><<<grid, kWarps * 32, DecLayout8<D>::kSmemBytes, stream>>>(tk, tv, p);
+    if constexpr (SHARED) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kWarps * 32);
+        cfg.dynamicSmemBytes = DecLayout8<D>::kSmemBytes;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = a.beside ? 1 : 0;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, decode_int8_kernel<D, NT, FUSED, SHARED>, tk, tv, p);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return fail(PA_ERR_CUDA, "shared decode_int8 launch: %s", cudaGetErrorString(e));
+        }
+        return PA_OK;
+    }
+    decode_int8_kernel<D, NT, FUSED, SHARED><<<grid, kWarps * 32, DecLayout8<D>::kSmemBytes, stream>>>(tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "decode_int8 launch: %s", cudaGetErrorString(e));
@@ -548,6 +584,13 @@ int launch_decode_int8(const DecodeArgs &a, void *stream)
     p.max_blocks = a.max_blocks_per_seq;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool two = p.group > 8;
+    if (a.table_rows) { // parts of a shared-prefix decode
+        p.table_rows = a.table_rows;
+        p.num_blocks = a.dims.num_blocks;
+        if (a.dims.head_dim == 128)
+            return two ? launch_int8<128, 2, false, true>(a, p, s) : launch_int8<128, 1, false, true>(a, p, s);
+        return two ? launch_int8<64, 2, false, true>(a, p, s) : launch_int8<64, 1, false, true>(a, p, s);
+    }
     if (a.k_new) { // fused quantising store + decode
         p.k_new = static_cast<const __nv_bfloat16 *>(a.k_new);
         p.v_new = static_cast<const __nv_bfloat16 *>(a.v_new);
@@ -587,7 +630,8 @@ int read_decode_error(uint32_t *code)
         e = cudaMemcpyToSymbol(g_decode_error, &zero, sizeof zero);
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "reading decode error word: %s", cudaGetErrorString(e));
-    *code |= v << 3;
+    *code |= (v & 1u) << 3;
+    *code |= (v & 2u) << 5; // the shared-prefix decode's bit 6
     return PA_OK;
 }
 

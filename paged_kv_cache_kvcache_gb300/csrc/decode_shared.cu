@@ -32,10 +32,17 @@
 // (TMA, one 3-D box per physical block), one MMA warp (tcgen05, S and O in tensor memory, P fed
 // back through tensor memory), one softmax warpgroup per tile; the rings run on across items.
 //
+// INT8 cache.  The codes are exact in bf16, so the products run on them and the scales enter in the
+// softmax: the keys' scale multiplies the score (fp32), the values' scale the weight before it is
+// rounded to bf16.  K and V codes come by TMA in granules of 32 keys; two warps turn them into the
+// bf16 tiles.  That keeps up with pairs but not with HBM, so parts of single sequences go to
+// the INT8 decode kernel, in a launch that may run beside this one.
+//
 // Every hand-off waits with a time limit; a wait that runs out sets an error bit and the
 // kernel returns.  A block id outside the pool reads as zeros and sets an error bit.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -62,23 +69,36 @@ constexpr int kBoxRows = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f; // log2 units
-template <int D>
+template <int D, bool kInt8>
 struct ShLayout {
     static constexpr int kPanels = D / 64;        // 64-element (128-byte) panels along head_dim
     static constexpr int kPanelBytes = 128 * 128; // 128 rows x 128 bytes
     static constexpr int kTileBytes = kPanels * kPanelBytes;
-    static constexpr int kKStages = D == 128 ? 3 : 4;
-    static constexpr int kVStages = D == 128 ? 2 : 4;
+    static constexpr int kKStages = D == 64 ? 4 : kInt8 ? 2 : 3;
+    static constexpr int kVStages = D == 64 ? 4 : 2;
     static constexpr int kQ = 0; // two query tiles
     static constexpr int kK = kQ + 2 * kTileBytes;
     static constexpr int kV = kK + kKStages * kTileBytes;
-    static constexpr int kBar = kV + kVStages * kTileBytes;
+    // INT8: codes of K and of V as they come from the cache, in granules of 32 keys, and for each
+    // query tile the scales (K's, V's) of its last kScaleSlots key tiles
+    static constexpr int kGranule = 32 * D;
+    static constexpr int kGranules = D == 64 ? 8 : 3;
+    static constexpr int kScaleSlots = D == 64 ? 8 : 4;
+    static constexpr int kCodes = kV + kVStages * kTileBytes;
+    static constexpr int kScales = kCodes + (kInt8 ? 2 * kGranules * kGranule : 0);
+    static constexpr int kBar = kScales + (kInt8 ? 2 * kScaleSlots * 2 * 128 * 4 : 0);
     static constexpr int kSmemBytes = kBar + 512 + 1024; // + alignment slack
+    // A slot is rewritten for key tile m of a lane once the score product at most kKStages tiles
+    // before is complete, and that one came after the softmax of the tile before it.
+    static_assert(!kInt8 || kScaleSlots >= kKStages + 2, "scales in use");
     static_assert(kKStages <= 4 && kVStages <= 4, "barrier slots");
     static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 };
 
 struct ShParams {
+    const uint16_t *k_scale; // INT8 cache: fp16 [num_blocks][num_kv_heads][block_size]
+    const uint16_t *v_scale;
+    int32_t num_kv_heads;
     const int4 *items;
     const int4 *cta_items;
     const int2 *seq_parts;
@@ -109,6 +129,9 @@ struct Bars {
     __device__ uint32_t o_full(int t) const { return base + 8 * (24 + t); }
     __device__ uint32_t v_tail(int s) const { return base + 8 * (26 + s); }
     __device__ uint32_t tmem_slot() const { return base + 8 * 30; }
+    // INT8: granule s of the codes of K (v = 0) or V (v = 1)
+    __device__ uint32_t g_full(int v, int s) const { return base + 8 * (32 + 8 * v + s); }
+    __device__ uint32_t g_free(int v, int s) const { return base + 8 * (48 + 8 * v + s); }
 };
 constexpr int kTmemSlotOffset = 8 * 30;
 constexpr int kAbortOffset = 8 * 31;
@@ -121,7 +144,10 @@ struct Item {
     __device__ bool tail() const { return ((k1 - k0) & 127) != 0; } // the last key tile runs past k1
 };
 
-// Entries [idx, end) of the item list, the next one fetched while the current one runs.
+// Entries [idx, end) of the item list, the next one fetched while the current one runs.  INT8:
+// up to the first part of a single sequence (the lists are sorted that way): those are the
+// INT8 decode kernel's.
+template <bool kInt8>
 struct ItemIter {
     const int4 *items;
     int idx, end;
@@ -133,6 +159,8 @@ struct ItemIter {
         if (idx < end) {
             a0 = ptx::ld_nc_v4_now(items + 2 * idx);
             a1 = ptx::ld_nc_v4_now(items + 2 * idx + 1);
+            if (kInt8 && a0.y == 1)
+                end = idx;
         }
     }
     __device__ Item peek() const { return {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z}; }
@@ -147,8 +175,9 @@ struct ItemIter {
 };
 
 // A lane's place in its singles: key tile j of n of the current one.
+template <bool kInt8>
 struct Lane {
-    ItemIter it;
+    ItemIter<kInt8> it;
     Item w;
     int j, n;
     bool active;
@@ -190,13 +219,32 @@ struct Waiter {
     }
 };
 
-template <int D>
+// 16 INT8 codes (one 16-byte vector) to bf16, exactly, as two 16-byte vectors.  A byte b is a code
+// c = (b & 0x7f) - (b & 0x80); 0x4300 | m is the bf16 number 128 + m for m < 128 and 256 for
+// m = 0x80, so c = bf16(0x4300 | b & 0x7f) - bf16(0x4300 | b & 0x80), both and their difference
+// exact (8 significant bits).
+__device__ __forceinline__ void codes_to_bf16(const uint4 &c, uint4 &lo, uint4 &hi)
+{
+    uint32_t w[8];
+    const uint32_t u[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t b = ptx::prmt(u[i], 0u, h ? 0x4342 : 0x4140); // two codes, one per 16 bits
+            w[2 * i + h] = ptx::sub_bf16x2((b & 0x007f007fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u);
+        }
+    lo = make_uint4(w[0], w[1], w[2], w[3]);
+    hi = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <int D, bool kInt8>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_shared_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const ShParams p)
 {
-    using L = ShLayout<D>;
+    using L = ShLayout<D, kInt8>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -239,6 +287,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bars.v_free(s), 1);
             ptx::mbar_init(bars.v_tail(s), 1);
         }
+        if constexpr (kInt8) {
+            for (int v = 0; v < 2; ++v)
+                for (int s = 0; s < L::kGranules; ++s) {
+                    ptx::mbar_init(bars.g_full(v, s), 1);
+                    ptx::mbar_init(bars.g_free(v, s), 1);
+                }
+        }
         *abort_flag = 0u;
         ptx::fence_mbar_init();
     }
@@ -271,42 +326,213 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= 8) {
         ptx::reg_dealloc<kOtherRegs>();
-        if (warp == kQWarp) {
-            // ------------------------------------------------------------ query producer
-            uint32_t nq0 = 0, nq1 = 0; // loads of each tile so far
+        uint32_t nq0 = 0, nq1 = 0; // query loads of each tile so far
+        // query rows of `w` (from sequence w.s0 + skip) into tile t, once the last score product that
+        // read the buffer is complete
+        auto load_q = [&](const Item &w, int t, int skip) -> bool {
+            uint32_t &n = t == 0 ? nq0 : nq1;
+            if (n > 0 && !wwait(bars.q_free(t), (n - 1) & 1))
+                return false;
+            ++n;
+            if (lane == 0) {
+                const bool one = w.nseq == 1;
+                ptx::mbar_arrive_expect_tx(bars.q_full(t), (uint32_t)(L::kPanels * 128 * G * (one ? 1 : P)));
+                for (int pp = 0; pp < L::kPanels; ++pp)
+                    ptx::tma_load_3d(sbase + L::kQ + t * L::kTileBytes + pp * L::kPanelBytes, one ? &tm_q1 : &tm_q,
+                                     bars.q_full(t), pp * 64, w.g * G, w.s0 + skip);
+            }
+            __syncwarp();
+            return true;
+        };
+        if (kInt8 && warp == kKWarp) {
+            // ------------------------------------------------------------ INT8: codes of K and V
+            const int bs = p.block_size;
+            const int box_rows = p.box_rows;
+            const int per_granule = 32 / box_rows; // boxes: 1 or 2
+            int st = 0;
+            uint32_t ph = 0;
             bool ok = true;
-            // query rows of `w` (from sequence w.s0 + skip) into tile t, once the last score product
-            // that read the buffer is complete
-            auto load = [&](const Item &w, int t, int skip) {
-                uint32_t &n = t == 0 ? nq0 : nq1;
-                if (n > 0 && !(ok = wwait(bars.q_free(t), (n - 1) & 1)))
-                    return;
-                ++n;
-                if (lane == 0) {
-                    const bool one = w.nseq == 1;
-                    ptx::mbar_arrive_expect_tx(bars.q_full(t), (uint32_t)(L::kPanels * 128 * G * (one ? 1 : P)));
-                    for (int pp = 0; pp < L::kPanels; ++pp)
-                        ptx::tma_load_3d(sbase + L::kQ + t * L::kTileBytes + pp * L::kPanelBytes, one ? &tm_q1 : &tm_q,
-                                         bars.q_full(t), pp * 64, w.g * G, w.s0 + skip);
+            auto sub_row = [&](const Item &w, int j) -> int { // as below, for the boxes of a whole tile
+                const int key = w.k0 + j * 128 + lane * box_rows;
+                if (lane * box_rows >= 128 || key >= w.k1)
+                    return p.num_blocks * bs;
+                const int phys = __ldg(p.block_tables + (size_t)w.row * p.max_blocks + key / bs);
+                if ((uint32_t)phys >= (uint32_t)p.num_blocks) {
+                    atomicOr(&g_shared_error, 2u);
+                    return p.num_blocks * bs;
                 }
-                __syncwarp();
+                return phys * bs + (key & (bs - 1));
             };
-            for (ItemIter it(p.items, span.x, span.y); ok && it.more();) {
+            auto load = [&](const Item &w, int cur) {
+                for (int gi = 0; gi < 4; ++gi) {
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        if (ph > 0 && !(ok = wwait(bars.g_free(v, st), (ph - 1) & 1)))
+                            return;
+                        if (lane == 0)
+                            ptx::mbar_arrive_expect_tx(bars.g_full(v, st), (uint32_t)L::kGranule);
+                        __syncwarp();
+                        const int sub = lane - gi * per_granule;
+                        if (sub >= 0 && sub < per_granule)
+                            ptx::tma_load_3d(sbase + L::kCodes + (v * L::kGranules + st) * L::kGranule + sub * box_rows * D,
+                                             v ? &tm_v : &tm_k, bars.g_full(v, st), 0, w.g, cur);
+                        __syncwarp();
+                    }
+                    if (++st == L::kGranules) {
+                        st = 0;
+                        ++ph;
+                    }
+                }
+            };
+            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
                 const Item w = it.next();
-                load(w, 0, 0);
-                if (ok)
-                    load(w, 1, P);
+                const int n = w.tiles();
+                int next = sub_row(w, 0);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int cur = next;
+                    if (j + 1 < n)
+                        next = sub_row(w, j + 1);
+                    load(w, cur);
+                }
+            }
+            Lane<kInt8> l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
+            auto advance = [&](Lane<kInt8> &l) {
+                load(l.w, sub_row(l.w, l.j));
+                l.step();
+            };
+            while (ok && (l0.active || l1.active)) {
+                if (l0.active)
+                    advance(l0);
+                if (ok && l1.active)
+                    advance(l1);
+            }
+        } else if (kInt8 && (warp == kVWarp || warp == kQWarp)) {
+            // ------------------------------------------------------------ INT8: codes to bf16 tiles.  One
+            // warp converts K (and brings the scales of both), the other V (and loads the queries: its
+            // last tile of an item is converted when the item's last score product is under way).
+            const bool is_k = warp == kVWarp;
+            const int v = is_k ? 0 : 1;
+            const int nstages = is_k ? L::kKStages : L::kVStages;
+            int gs = 0, st = 0, sc0 = 0, sc1 = 0;
+            uint32_t gph = 0, ph = 0;
+            bool ok = true;
+            auto convert = [&](const Item &w, int j, bool to0, bool to1) { // for query tiles 0 and/or 1
+                uint2 s4[2]; // the scales of keys 4 lane .. 4 lane + 3; 0 for keys past the range
+                if (is_k) {
+                    const int key = w.k0 + j * 128 + lane * 4;
+                    s4[0] = s4[1] = make_uint2(0u, 0u);
+                    if (key < w.k1) {
+                        const int phys = __ldg(p.block_tables + (size_t)w.row * p.max_blocks + key / p.block_size);
+                        if ((uint32_t)phys < (uint32_t)p.num_blocks) {
+                            const size_t at = ((size_t)phys * p.num_kv_heads + w.g) * p.block_size +
+                                              (key & (p.block_size - 1));
+                            s4[0] = __ldg(reinterpret_cast<const uint2 *>(p.k_scale + at));
+                            s4[1] = __ldg(reinterpret_cast<const uint2 *>(p.v_scale + at));
+                        }
+                    }
+                }
+                if (ph > 0 && !(ok = wwait(is_k ? bars.k_free(st) : bars.v_free(st), (ph - 1) & 1)))
+                    return;
+                uint8_t *tile = sgen + (is_k ? L::kK : L::kV) + st * L::kTileBytes;
+                if (is_k) {
+                    const int left = w.k1 - (w.k0 + j * 128 + lane * 4);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&s4[x].x));
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&s4[x].y));
+                        const float4 f = make_float4(left > 0 ? a.x : 0.f, left > 1 ? a.y : 0.f, left > 2 ? b.x : 0.f,
+                                                     left > 3 ? b.y : 0.f);
+                        float4 *slot = reinterpret_cast<float4 *>(sgen + L::kScales) + x * 32 + lane;
+                        if (to0)
+                            slot[sc0 * 64] = f;
+                        if (to1)
+                            slot[(L::kScaleSlots + sc1) * 64] = f;
+                    }
+                    if (to0 && ++sc0 == L::kScaleSlots)
+                        sc0 = 0;
+                    if (to1 && ++sc1 == L::kScaleSlots)
+                        sc1 = 0;
+                }
+                for (int gi = 0; gi < 4; ++gi) {
+                    if (!(ok = wwait(bars.g_full(v, gs), gph & 1)))
+                        return;
+                    const uint32_t from = sbase + L::kCodes + (v * L::kGranules + gs) * L::kGranule;
+                    constexpr int kVecs = D / 16, kBatch = 4; // 16-byte vectors per key
+#pragma unroll
+                    for (int i0 = 0; i0 < kVecs; i0 += kBatch) {
+                        uint4 c[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+                            c[i] = ptx::lds_v4(from + ((i0 + i) * 32 + lane) * 16);
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int e = (i0 + i) * 32 + lane;
+                            const int r = gi * 32 + e / kVecs, x = 2 * (e % kVecs); // key, first 16-byte chunk of its row
+                            uint4 lo, hi;
+                            codes_to_bf16(c[i], lo, hi);
+                            uint8_t *row = tile + (x >> 3) * L::kPanelBytes + r * 128;
+                            *reinterpret_cast<uint4 *>(row + (((x & 7) ^ (r & 7)) << 4)) = lo;
+                            *reinterpret_cast<uint4 *>(row + ((((x & 7) + 1) ^ (r & 7)) << 4)) = hi;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        ptx::mbar_arrive(bars.g_free(v, gs));
+                    if (++gs == L::kGranules) {
+                        gs = 0;
+                        ++gph;
+                    }
+                }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    ptx::mbar_arrive(is_k ? bars.k_full(st) : bars.v_full(st));
+                if (++st == nstages) {
+                    st = 0;
+                    ++ph;
+                }
+            };
+            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
+                const Item w = it.next();
+                const int n = w.tiles();
+                if (!is_k && !(ok = load_q(w, 0, 0) && load_q(w, 1, P)))
+                    break;
+                for (int j = 0; ok && j < n; ++j)
+                    convert(w, j, true, true);
+            }
+            Lane<kInt8> l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
+            if (!is_k && ok && l0.active)
+                ok = load_q(l0.w, 0, 0);
+            if (!is_k && ok && l1.active)
+                ok = load_q(l1.w, 1, 0);
+            auto advance = [&](Lane<kInt8> &l, int t) {
+                convert(l.w, l.j, t == 0, t == 1);
+                if (ok && l.step() && l.active && !is_k)
+                    ok = load_q(l.w, t, 0);
+            };
+            while (ok && (l0.active || l1.active)) {
+                if (l0.active)
+                    advance(l0, 0);
+                if (ok && l1.active)
+                    advance(l1, 1);
+            }
+        } else if (!kInt8 && warp == kQWarp) {
+            // ------------------------------------------------------------ query producer
+            bool ok = true;
+            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
+                const Item w = it.next();
+                ok = load_q(w, 0, 0) && load_q(w, 1, P);
             }
             // the lanes advance tile by tile together: loads in the order in which they are needed
-            ItemIter i0(p.items, span.y, span.z), i1(p.items, span.z, span.w);
+            ItemIter<kInt8> i0(p.items, span.y, span.z), i1(p.items, span.z, span.w);
             int at0 = 0, at1 = 0; // key tiles before each lane's next item
             while (ok && (i0.more() || i1.more())) {
                 const bool first = i0.more() && (!i1.more() || at0 <= at1);
                 const Item w = first ? i0.next() : i1.next();
-                load(w, first ? 0 : 1, 0);
+                ok = load_q(w, first ? 0 : 1, 0);
                 (first ? at0 : at1) += w.tiles();
             }
-        } else if (warp == kKWarp || warp == kVWarp) {
+        } else if (!kInt8 && (warp == kKWarp || warp == kVWarp)) {
             // ------------------------------------------------------------ K and V producers
             const bool is_k = warp == kKWarp;
             const int nstages = is_k ? L::kKStages : L::kVStages;
@@ -368,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++ph;
                 }
             };
-            for (ItemIter it(p.items, span.x, span.y); ok && it.more();) {
+            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
                 const Item w = it.next();
                 const int n = w.tiles();
                 int next = sub_row(w, 0);
@@ -379,9 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     load(w, j, cur, keep);
                 }
             }
-            Lane l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
+            Lane<kInt8> l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
             int r0 = l0.active ? sub_row(l0.w, 0) : 0, r1 = l1.active ? sub_row(l1.w, 0) : 0;
-            auto advance = [&](Lane &l, int &r) { // this tile's load, the next one's row looked up before it
+            auto advance = [&](Lane<kInt8> &l, int &r) { // this tile's load, the next one's row looked up before it
                 const Item w = l.w;
                 const int j = l.j, cur = r;
                 l.step();
@@ -440,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto wait_v = [&](bool tail) {
                 ok = ok && wwait(bars.v_full(vs), vph);
-                if (tail) {
+                if (!kInt8 && tail) { // (codes are finite: nothing to zero)
                     ok = ok && wwait(bars.v_tail(vs), (tailpar >> vs) & 1u);
                     tailpar ^= 1u << vs;
                 }
@@ -460,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     vph ^= 1;
                 }
             };
-            for (ItemIter it(p.items, span.x, span.y); ok && it.more();) {
+            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
                 const Item w = it.next();
                 const int n = w.tiles();
                 const bool tail = w.tail();
@@ -510,9 +736,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pass_k();
                 }
             }
-            Lane l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
+            Lane<kInt8> l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
             // score product of the lane's current key tile
-            auto score = [&](const Lane &l, int t) {
+            auto score = [&](const Lane<kInt8> &l, int t) {
                 if (l.j == 0)
                     wait_q(t);
                 wait_k();
@@ -524,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pass_k();
             };
             // value product of the lane's current key tile, then the next one's scores
-            auto step = [&](Lane &l, int t) {
+            auto step = [&](Lane<kInt8> &l, int t) {
                 const bool last = l.j + 1 == l.n;
                 wait_p(t);
                 wait_v(last && l.w.tail());
@@ -562,15 +788,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t o_col = s_col + 128;
         const float sl2 = p.scale_log2;
         uint32_t ns = 0, no = 0;
+        int sc = 0; // INT8: scale slot of the next key tile
         bool ok = true;
-        ItemIter items(p.items, span.x, span.y);
+        ItemIter<kInt8> items(p.items, span.x, span.y);
         bool single = false;
         while (ok) {
             if (!items.more()) {
                 if (single)
                     break;
                 single = true;
-                items = t == 0 ? ItemIter(p.items, span.y, span.z) : ItemIter(p.items, span.z, span.w);
+                items = t == 0 ? ItemIter<kInt8>(p.items, span.y, span.z) : ItemIter<kInt8>(p.items, span.z, span.w);
                 continue;
             }
             const Item w = items.next(false);
@@ -587,19 +814,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wwait(bars.s_full(t), ns & 1)))
                     break;
                 ns ^= 1;
+                const float4 *scales = reinterpret_cast<const float4 *>(sgen + L::kScales) +
+                                       (t * L::kScaleSlots + sc) * 64; // INT8: 32 of K's, then 32 of V's
+                if (kInt8 && ++sc == L::kScaleSlots)
+                    sc = 0;
                 if (warp_valid) {
                     ptx::tc_fence_after();
                     const int lim = w.k1 - w.k0 - j * 128; // keys of this tile (128 or more: all)
                     uint32_t sr[128];
                     float mx;
-                    if (lim < 128) {
+                    if (kInt8 || lim < 128) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             ptx::tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
                         ptx::tmem_wait_ld();
+                        if constexpr (kInt8) { // scores of the codes times the keys' scales
 #pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            sr[c] = c < lim ? sr[c] : __float_as_uint(-INFINITY);
+                            for (int c = 0; c < 128; c += 4) {
+                                const float4 f = scales[c >> 2];
+                                sr[c] = __float_as_uint(__uint_as_float(sr[c]) * f.x);
+                                sr[c + 1] = __float_as_uint(__uint_as_float(sr[c + 1]) * f.y);
+                                sr[c + 2] = __float_as_uint(__uint_as_float(sr[c + 2]) * f.z);
+                                sr[c + 3] = __float_as_uint(__uint_as_float(sr[c + 3]) * f.w);
+                            }
+                        }
+                        if (lim < 128) {
+#pragma unroll
+                            for (int c = 0; c < 128; ++c)
+                                sr[c] = c < lim ? sr[c] : __float_as_uint(-INFINITY);
+                        }
                         float m8[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -649,7 +892,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           x0, x1);
                             const float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1); // masked columns: 2^-inf = 0
                             sum2[(c >> 1) & 3] = ptx::f2_add(sum2[(c >> 1) & 3], ptx::f2(e0, e1));
-                            pk[(c >> 1) & 31] = ptx::pack_bf16(e0, e1);
+                            if constexpr (kInt8) { // the values' scales, before the rounding
+                                const float4 f = scales[32 + (c >> 2)];
+                                pk[(c >> 1) & 31] = c & 2 ? ptx::pack_bf16(e0 * f.z, e1 * f.w)
+                                                          : ptx::pack_bf16(e0 * f.x, e1 * f.y);
+                            } else {
+                                pk[(c >> 1) & 31] = ptx::pack_bf16(e0, e1);
+                            }
                         }
                         ptx::tmem_st32(s_col + 32 * h, pk);
                     }
@@ -808,17 +1057,28 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const float *__rest
         dst[0] = x[0];
 }
 
-template <int D>
+// One KV head's rows of a cache: bf16 in 128-byte swizzled panels of 64, INT8 codes row by row.
+template <int D, bool kInt8>
+int encode_cache(CUtensorMap *m, const void *cache, const pa_dims &d, uint32_t box_rows, const char *what)
+{
+    constexpr int kElem = kInt8 ? 1 : 2;
+    return encode_tmap_3d(m, kInt8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache, D,
+                          d.num_kv_heads, (uint64_t)d.num_blocks * d.block_size, (uint64_t)D * kElem,
+                          (uint64_t)d.num_kv_heads * D * kElem, kInt8 ? D : 64, 1, box_rows,
+                          kInt8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+
+template <int D, bool kInt8>
 int launch(const SharedArgs &a, cudaStream_t stream)
 {
-    using L = ShLayout<D>;
-    if (int rc = ensure_smem<decode_shared_kernel<D>>(L::kSmemBytes, "shared decode"))
+    using L = ShLayout<D, kInt8>;
+    if (int rc = ensure_smem<decode_shared_kernel<D, kInt8>>(L::kSmemBytes, "shared decode"))
         return rc;
     static std::atomic<int> launch_regs{0};
     int nreg = launch_regs.load(std::memory_order_acquire);
     if (nreg == 0) {
         cudaFuncAttributes fa{};
-        const cudaError_t e = cudaFuncGetAttributes(&fa, decode_shared_kernel<D>);
+        const cudaError_t e = cudaFuncGetAttributes(&fa, decode_shared_kernel<D, kInt8>);
         if (e != cudaSuccess)
             return fail(PA_ERR_CUDA, "shared decode kernel attributes: %s", cudaGetErrorString(e));
         launch_regs.store(nreg = fa.numRegs, std::memory_order_release);
@@ -829,21 +1089,18 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     const pa_dims &d = a.dims;
     const int G = d.num_heads / d.num_kv_heads;
     if (a.num_items > 0) {
-        const uint64_t rows = (uint64_t)d.num_blocks * d.block_size;
         const uint32_t box_rows = d.block_size < kBoxRows ? (uint32_t)d.block_size : (uint32_t)kBoxRows;
         constexpr CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
         constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
-        const uint64_t qs = (uint64_t)d.num_heads * D * 2, cs = (uint64_t)d.num_kv_heads * D * 2;
+        const uint64_t qs = (uint64_t)d.num_heads * D * 2;
         CUtensorMap tq, tq1, tk, tv;
         int rc;
         if ((rc = encode_tmap_3d(&tq, bf16, a.q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
                                  (uint32_t)G, (uint32_t)a.rows_per_tile, sw, "q")) != PA_OK ||
             (rc = encode_tmap_3d(&tq1, bf16, a.q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
                                  (uint32_t)G, 1, sw, "q")) != PA_OK ||
-            (rc = encode_tmap_3d(&tk, bf16, a.k_cache, D, d.num_kv_heads, rows, (uint64_t)D * 2, cs, 64, 1, box_rows,
-                                 sw, "k_cache")) != PA_OK ||
-            (rc = encode_tmap_3d(&tv, bf16, a.v_cache, D, d.num_kv_heads, rows, (uint64_t)D * 2, cs, 64, 1, box_rows,
-                                 sw, "v_cache")) != PA_OK)
+            (rc = encode_cache<D, kInt8>(&tk, a.k_cache, d, box_rows, "k_cache")) != PA_OK ||
+            (rc = encode_cache<D, kInt8>(&tv, a.v_cache, d, box_rows, "v_cache")) != PA_OK)
             return rc;
         ShParams p{};
         p.items = reinterpret_cast<const int4 *>(a.items);
@@ -861,10 +1118,37 @@ int launch(const SharedArgs &a, cudaStream_t stream)
         p.box_rows = (int32_t)box_rows;
         p.max_blocks = a.max_blocks_per_seq;
         p.num_blocks = d.num_blocks;
-        decode_shared_kernel<D><<<(unsigned)a.num_ctas, kThreads, L::kSmemBytes, stream>>>(tq, tq1, tk, tv, p);
+        p.k_scale = static_cast<const uint16_t *>(a.k_scale);
+        p.v_scale = static_cast<const uint16_t *>(a.v_scale);
+        p.num_kv_heads = d.num_kv_heads;
+        decode_shared_kernel<D, kInt8><<<(unsigned)a.num_ctas, kThreads, L::kSmemBytes, stream>>>(tq, tq1, tk, tv, p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess)
             return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
+    }
+    if (kInt8 && a.num_single_items > 0) {
+        // the parts of single sequences: the INT8 decode kernel reads codes at 0.9 of the HBM rate, the
+        // conversion through shared memory above could not; it may run beside the shared parts
+        DecodeArgs s{};
+        s.dims = a.dims;
+        s.q = a.q;
+        s.k_cache = a.k_cache;
+        s.v_cache = a.v_cache;
+        s.k_scale = a.k_scale;
+        s.v_scale = a.v_scale;
+        s.block_tables = a.block_tables;
+        s.items = a.single_items;
+        s.out = a.out;
+        s.part_o = a.part_o;
+        s.part_lse = a.part_lse;
+        s.scale = a.scale;
+        s.num_seqs = a.num_seqs;
+        s.num_items = a.num_single_items;
+        s.max_blocks_per_seq = a.max_blocks_per_seq;
+        s.table_rows = a.table_rows;
+        s.beside = a.num_items > 0;
+        if (int rc = launch_decode_int8(s, stream))
+            return rc;
     }
     if (!a.merge)
         return PA_OK;
@@ -880,7 +1164,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = a.num_items > 0 ? 1 : 0;
+    cfg.numAttrs = a.num_items + (kInt8 ? a.num_single_items : 0) > 0 ? 1 : 0;
     const cudaError_t e =
         cudaLaunchKernelEx(&cfg, shared_combine_kernel<D>, (const float *)a.part_o, (const float *)a.part_lse,
                            reinterpret_cast<const int2 *>(a.seq_parts), static_cast<__nv_bfloat16 *>(a.out),
@@ -897,7 +1181,9 @@ int launch(const SharedArgs &a, cudaStream_t stream)
 int launch_decode_shared(const SharedArgs &a, void *stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return a.dims.head_dim == 128 ? launch<128>(a, s) : launch<64>(a, s);
+    if (a.k_scale)
+        return a.dims.head_dim == 128 ? launch<128, true>(a, s) : launch<64, true>(a, s);
+    return a.dims.head_dim == 128 ? launch<128, false>(a, s) : launch<64, false>(a, s);
 }
 
 int read_shared_error(uint32_t *code)

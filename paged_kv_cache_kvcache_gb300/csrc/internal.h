@@ -179,6 +179,9 @@ struct DecodeArgs {
     const void *k_new;
     const void *v_new;
     const int32_t *slot_mapping;
+    // parts of a shared-prefix decode on an INT8 cache (else NULL): no merge is launched
+    const int32_t *table_rows; // block-table row of each sequence
+    bool beside;               // may run beside the launch before it
 };
 int launch_decode(const DecodeArgs &a, void *stream);
 int launch_decode_int8(const DecodeArgs &a, void *stream);
@@ -197,12 +200,15 @@ struct SharedArgs {
     const int32_t *items;
     const int32_t *cta_items;
     const int32_t *seq_parts;
+    const int32_t *single_items; // INT8 cache only
+    const int32_t *table_rows;
     void *out;
     float *part_o;   // [num_partials][Hq][D]
     float *part_lse; // [num_partials][Hq]
     float scale;
     int32_t num_seqs;
-    int32_t num_items;
+    int32_t num_items; // to launch: INT8 those of several sequences, bf16 all
+    int32_t num_single_items;
     int32_t num_ctas;
     int32_t rows_per_tile;
     int32_t max_blocks_per_seq;

@@ -260,6 +260,11 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     }
     if (partials > INT32_MAX)
         return fail(PA_ERR_INVALID_ARG, "too many partial results");
+    int32_t singles = 0, shared_items = 0;
+    for (const Work &w : works) {
+        singles += w.n == 1 && w.g == 0;
+        shared_items += w.n > 1;
+    }
     const int32_t ctas = (int32_t)std::min<size_t>(works.size(), (size_t)sms);
 
     Layout L;
@@ -275,6 +280,8 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->merge = merge ? 1 : 0;
     meta->split_tokens = (int32_t)std::min<int64_t>((int64_t)per * kTile, INT32_MAX / kTile * kTile);
     meta->tables_packed = packed ? 1 : 0;
+    meta->num_single_items = singles;
+    meta->num_shared_items = shared_items;
     for (const Run &r : runs)
         meta->tokens_saved += (uint64_t)r.shared * (uint64_t)(r.n - 1);
     meta->off_block_tables = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs * mb : 0);
@@ -282,6 +289,8 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->off_items = L.take(sizeof(int32_t) * kSharedItemInts * works.size());
     meta->off_cta_items = L.take(sizeof(int32_t) * 4 * (size_t)ctas);
     meta->off_seq_parts = L.take(sizeof(int32_t) * 2 * (size_t)num_seqs);
+    meta->off_single_items = L.take(sizeof(int32_t) * 4 * (size_t)singles);
+    meta->off_table_rows = L.take(sizeof(int32_t) * (size_t)num_seqs);
     meta->total_bytes = L.off;
     meta->workspace_bytes = partials > 0 ? align_up((size_t)partials * d.num_heads * d.head_dim * 4, 256) +
                                                align_up((size_t)partials * d.num_heads * 4, 256)
@@ -305,19 +314,23 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
             slots[b] = pos < 0 ? -1 : block_ids[block_offsets[b] + pos / bs] * bs + pos % bs;
         }
     }
+    int32_t *rows = reinterpret_cast<int32_t *>(base + meta->off_table_rows);
+    for (int32_t b = 0; b < num_seqs; ++b)
+        rows[b] = table_rows ? table_rows[b] : b;
     for (int32_t b = 0, slot = 0; b < num_seqs; ++b) {
         sp[2 * b] = slot;
         sp[2 * b + 1] = parts[b];
         slot += parts[b] > 1 ? parts[b] : 0;
     }
     // Deal out, longest first, to the least loaded: pairs to CTAs (both lanes), then singles to
-    // lanes.  Queue 3c holds CTA c's pairs, 3c + 1 and 3c + 2 its lanes' singles.
+    // lanes, those of several sequences before those of one.  Queue 3c holds CTA c's pairs, 3c + 1 and 3c + 2 its lanes' singles.
     std::vector<int32_t> order(works.size()), queue_of(works.size()), fill(3 * (size_t)ctas, 0);
     for (size_t i = 0; i < order.size(); ++i)
         order[i] = (int32_t)i;
     std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) {
-        const bool px = works[x].n > P, py = works[y].n > P;
-        return px != py ? px : works[x].cost > works[y].cost;
+        // pairs, parts of several sequences, parts of one
+        auto rank = [&](int32_t i) { return works[i].n > P ? 0 : works[i].n > 1 ? 1 : 2; };
+        return rank(x) != rank(y) ? rank(x) < rank(y) : works[x].cost > works[y].cost;
     });
     using Load = std::pair<float, int32_t>;
     std::vector<float> load((size_t)ctas, 0.f);
@@ -353,8 +366,16 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
             ci[4 * c + i] = next[3 * (size_t)c + i];
         ci[4 * c + 3] = next[3 * (size_t)c + 2] + fill[3 * (size_t)c + 2];
     }
+    int32_t *one = reinterpret_cast<int32_t *>(base + meta->off_single_items);
     for (int32_t i : order) {
         const Work &w = works[i];
+        if (w.n == 1 && w.g == 0) {
+            one[0] = w.s0;
+            one[1] = w.k0;
+            one[2] = w.k1;
+            one[3] = parts[w.s0] > 1 ? sp[2 * w.s0] + w.part : -1;
+            one += 4;
+        }
         int32_t *e = it + (size_t)kSharedItemInts * next[queue_of[i]]++;
         e[0] = w.s0;
         e[1] = w.n;

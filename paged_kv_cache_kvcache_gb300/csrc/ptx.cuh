@@ -398,6 +398,13 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
     return d;
 }
 
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 __device__ __forceinline__ uint4 lds_v4(uint32_t addr)
 {
     uint4 v;

@@ -24,7 +24,7 @@ EXPORTS = ("pa_pack_prefill", "pa_pack_decode", "pa_upload", "pa_store_kvcache",
            "pa_decode", "pa_decode_static", "pa_copy_blocks", "pa_store_kvcache_int8", "pa_decode_int8",
            "pa_prefill_varlen_int8", "pa_pack_decode_fixed", "pa_decode_fused", "pa_copy_blocks_int8",
            "pa_decode_int8_fused", "pa_prefill_varlen_fused", "pa_prefill_varlen_int8_fused",
-           "pa_pack_decode_shared", "pa_decode_shared", "pa_pool_workspace", "pa_pool_append", "pa_pool_fork",
+           "pa_pack_decode_shared", "pa_decode_shared", "pa_decode_shared_int8", "pa_pool_workspace", "pa_pool_append", "pa_pool_fork",
            "pa_pool_free", "pa_pool_compact",
            "pa_last_error_string", "pa_read_device_error", "pa_selftest_bounded_wait", "pa_stream_read",
            "pa_version")
@@ -62,10 +62,12 @@ class pa_shared_meta(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
                 ("num_items", ctypes.c_int32), ("num_ctas", ctypes.c_int32), ("num_partials", ctypes.c_int32),
                 ("max_parts", ctypes.c_int32), ("rows_per_tile", ctypes.c_int32), ("merge", ctypes.c_int32),
-                ("split_tokens", ctypes.c_int32), ("tables_packed", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("split_tokens", ctypes.c_int32), ("tables_packed", ctypes.c_int32),
+                ("num_single_items", ctypes.c_int32), ("num_shared_items", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("tokens_saved", ctypes.c_uint64), ("off_block_tables", ctypes.c_uint64),
                 ("off_slot_mapping", ctypes.c_uint64), ("off_items", ctypes.c_uint64),
                 ("off_cta_items", ctypes.c_uint64), ("off_seq_parts", ctypes.c_uint64),
+                ("off_single_items", ctypes.c_uint64), ("off_table_rows", ctypes.c_uint64),
                 ("total_bytes", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
 
 
@@ -119,6 +121,7 @@ def lib() -> ctypes.CDLL:
             L.pa_prefill_varlen_int8_fused.argtypes = [P] * 14 + [ctypes.c_float] + [P] * 4 + [SZ, P]
             L.pa_pack_decode_shared.argtypes = [P, I32, P, I32, P, P, P, P, P, I32, I32, P, SZ, P]
             L.pa_decode_shared.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, P, P, P, P, SZ, P]
+            L.pa_decode_shared_int8.argtypes = [P] * 7 + [ctypes.c_float] + [P] * 8 + [SZ, P]
             L.pa_pool_workspace.argtypes = [P, P, P]
             L.pa_pool_append.argtypes = [P, P, P, P, I32, P, I32, P, SZ, P]
             L.pa_pool_fork.argtypes = [P, P, P, P, I32, P, SZ, P]
@@ -247,6 +250,7 @@ class SharedPlan(_Plan):
         self.call_ref = ctypes.byref(m)
         self.call_tables = base + m.off_block_tables if m.tables_packed or m.num_seqs == 0 else None
         self.call_arrays = tuple(base + x for x in (m.off_items, m.off_cta_items, m.off_seq_parts))
+        self.call_singles = (base + m.off_single_items, base + m.off_table_rows)
         return self
 
     @property
@@ -441,6 +445,16 @@ def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale
     _check(lib().pa_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), bt, scale, _ptr(out),
                                   plan.call_ref, *plan.call_arrays, _ptr(workspace), _nbytes(workspace),
                                   _stream(stream)), "pa_decode_shared")
+
+
+def pa_decode_shared_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, plan: SharedPlan, scale: float, out,
+                          workspace=None, block_tables=None, stream=None):
+    """pa_decode_shared over an INT8 cache (same plan and workspace)."""
+    bt = _shared_tables(plan, block_tables)
+    _check(lib().pa_decode_shared_int8(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                       _ptr(v_scale), bt, scale, _ptr(out), plan.call_ref, *plan.call_arrays,
+                                       *plan.call_singles, _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "pa_decode_shared_int8")
 
 
 def pa_copy_blocks(dims: pa_dims, k_cache, v_cache, triples, num_triples: Optional[int] = None, stream=None):

@@ -71,6 +71,33 @@ def decode(dims, q, kc, vc, plan, scale, block_tables=None, stream=None, junk=Tr
     return out
 
 
+def int8_pool(nb, bs, hkv, d, seed, ctx, lists):
+    """INT8 caches [codes, codes, scales, scales] whose rows behind every context have the scale NaN, and the
+    values they stand for in fp64 (0 there)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = [torch.randint(-127, 128, (nb, bs, hkv, d), generator=g, device="cuda", dtype=torch.int8) for _ in range(2)]
+    scales = [(torch.rand(nb, hkv, bs, generator=g, device="cuda") * 0.03 + 0.002).to(torch.float16) for _ in range(2)]
+    dead = torch.ones(nb, bs, dtype=torch.bool)
+    for n, blocks in zip(ctx, lists):
+        for pos in range(n):
+            dead[int(blocks[pos // bs]), pos % bs] = False
+    dead = dead.cuda()
+    dense = []
+    for c, s in zip(codes, scales):
+        s.masked_fill_(dead[:, None, :], float("nan"))
+        dense.append(c.double() * s.double().nan_to_num(0.0).transpose(1, 2)[..., None])
+    return codes + scales, dense
+
+
+def decode8(dims, q, cache, plan, scale, block_tables=None):
+    out = torch.full_like(q, 7.0)
+    ws = pa.shared_workspace(plan)
+    if ws is not None:
+        ws.fill_(0xFF)
+    pa.pa_decode_shared_int8(dims, q, *cache, plan, scale, out, ws, block_tables=block_tables)
+    return out
+
+
 CASES = [  # sizes, shared blocks, tails, bs, hq, hkv, d
     ([1], [0], [1], 16, 1, 1, 64),                                 # one sequence, one key, one head
     ([2], [1], [1, 2], 16, 2, 1, 64),
@@ -105,6 +132,89 @@ def test_parity(case, split):
     assert_within(out, ref, a, f"{case[:2]} split {split}")
     again = decode(dims, q, kc, vc, plan, d ** -0.5)
     assert torch.equal(out, again)  # no order of arrival enters the result
+
+
+@pytest.mark.parametrize("split", [0, 128, 384])
+@pytest.mark.parametrize("case", CASES, ids=range(len(CASES)))
+def test_parity_int8(case, split):
+    sizes, sh, tails, bs, hq, hkv, d = case
+    ctx, lists, groups, nb = make_batch(15, sizes, sh, tails, bs)
+    cache, dense = int8_pool(nb, bs, hkv, d, 150, ctx, lists)
+    q = values((len(ctx), hq, d), 152)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=split).upload()
+    out = decode8(dims, q, cache, plan, d ** -0.5)
+    ref, a = reference(q, *dense, lists, ctx, bs, d ** -0.5)
+    for b, n in enumerate(ctx):
+        if n == 0:
+            assert (out[b] == 0).all()
+    assert_within(out, ref, a, f"int8 {case[:2]} split {split}")
+    assert torch.equal(out, decode8(dims, q, cache, plan, d ** -0.5))
+
+
+def test_int8_every_code():
+    """All 255 codes in keys and values, one key carrying nearly all the weight at a time: the conversion is exact."""
+    bs, hq, hkv, d = 256, 4, 1, 128
+    ctx, lists = [256, 256], [[0], [0]]
+    k = torch.zeros(2, bs, hkv, d, dtype=torch.int8, device="cuda")
+    v = ((torch.arange(bs, device="cuda")[:, None] + torch.arange(d, device="cuda")) % 255 - 127).to(torch.int8)
+    k[0, :, 0, :] = v.roll(5, 0)
+    cache = [k, torch.stack([v, v])[:, :, None, :].contiguous()] + [
+        torch.full((2, hkv, bs), s, dtype=torch.float16, device="cuda") for s in (0.0625, 0.25)]
+    q = values((2, hq, d), 155)
+    dims = pa.make_dims(2, bs, hq, hkv, d)
+    plan = pa.pa_pack_decode_shared(dims, ctx, block_lists=lists).upload()
+    assert plan.meta.num_shared_items > 0 and plan.meta.num_single_items == 0
+    out = decode8(dims, q, cache, plan, 0.5)
+    dense = [c.double() * s for c, s in zip(cache[:2], (0.0625, 0.25))]
+    ref, a = reference(q, *dense, lists, ctx, bs, 0.5)
+    assert_within(out, ref, a, "every code")
+
+
+def test_int8_block_ids_outside_the_pool_read_as_zeros():
+    bs, hq, hkv, d = 16, 4, 2, 64
+    ctx, lists, groups, nb = make_batch(9, [2], [8], [20, 40], bs)
+    cache, dense = int8_pool(nb, bs, hkv, d, 90, ctx, lists)
+    q = values((2, hq, d), 92)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    width = max(len(x) for x in lists)
+    table = np.full((4, width), -1, np.int32)
+    for b, r in enumerate((3, 1)):
+        table[r, :len(lists[b])] = lists[b]
+    table[[1, 3], 3], table[1, 9] = -5, nb + 100
+    plan = pa.pa_pack_decode_shared(dims, ctx, shared_lens=[8 * bs], table_rows=[3, 1], max_blocks=width).upload()
+    out = decode8(dims, q, cache, plan, d ** -0.5, block_tables=torch.tensor(table, device="cuda"))
+    torch.cuda.synchronize()
+    assert pa.pa_read_device_error() == 1 << 6
+    kz, vz = (torch.cat([c, torch.zeros_like(c[:1])]) for c in dense)
+    zeroed = [[x if 0 <= x < nb else nb for x in table[r, :len(lists[b])].tolist()] for b, r in enumerate((3, 1))]
+    ref, a = reference(q, kz, vz, zeroed, ctx, bs, d ** -0.5)
+    assert_within(out, ref, a, "bad ids int8")
+
+
+def test_int8_equals_pa_decode_int8_and_replays():
+    bs, hq, hkv, d = 16, 28, 4, 128
+    ctx, lists, groups, nb = make_batch(17, [40, 9], [40, 17], [1 + 13 * i for i in range(49)], bs)
+    cache, dense = int8_pool(nb, bs, hkv, d, 170, ctx, lists)
+    q = values((49, hq, d), 172)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists).upload()
+    ws, out = pa.shared_workspace(plan), torch.empty_like(q)
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        pa.pa_decode_shared_int8(dims, q, *cache, plan, d ** -0.5, out, ws)
+    p2 = pa.pa_pack_decode(dims, ctx, lists).upload()
+    for rep in range(3):
+        q.copy_(values((49, hq, d), 172 + rep))
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, a = reference(q, *dense, lists, ctx, bs, d ** -0.5)
+        assert_within(out, ref, a, f"replay {rep}")
+        plain = torch.empty_like(q)
+        pa.pa_decode_int8(dims, q, *cache, p2, d ** -0.5, plain, pa.decode_workspace(p2))
+        assert ((out.double() - plain.double()).abs() <= 2 * (U * (a + ref.abs()) + 2e-4 * a)).all()
 
 
 def test_large_scores_and_scale():

@@ -83,6 +83,16 @@ def test_parts_cover_every_key_once(case):
         shared_reads += (n - 1) * (k1 - k0) if g == 0 else 0
     for b in range(B):
         assert (seen[b] == 1).all()
+    # the parts of single sequences, once more per (sequence, range) with their slots
+    ones = plan.host_array(m.off_single_items, 4 * m.num_single_items).reshape(-1, 4).tolist()
+    want = {(s0, k0, k1, parts[s0, 0] + part if parts[s0, 1] > 1 else -1)
+            for s0, n, g, _, k0, k1, part, _ in items.tolist() if n == 1}
+    assert len(ones) == len(want) and set(map(tuple, ones)) == want
+    assert m.num_shared_items == sum(i[1] > 1 for i in items.tolist())
+    assert plan.host_array(m.off_table_rows, B).tolist() == list(range(B))
+    for _, l0, l1, end in cta.tolist():  # in each lane parts of several sequences come first
+        for a, b in ((l0, l1), (l1, end)):
+            assert (np.diff((items[a:b, 1] == 1).astype(int)) >= 0).all()
     slots = [s for b in range(B) if parts[b, 1] > 1 for s in range(parts[b, 0], parts[b, 0] + parts[b, 1])]
     assert slots == list(range(m.num_partials))
     assert all(parts[b, 1] == 0 for b in range(B) if ctx[b] == 0) and m.max_parts == max(parts[:, 1])
@@ -189,5 +199,18 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     assert call(ws=None, nbytes=4096) == pa.PA_ERR_INVALID_ARG
     m.workspace_bytes = 512                                                    # not this batch's size
     assert call(ws=256, nbytes=4096) == pa.PA_ERR_INVALID_ARG
+    m.workspace_bytes = 1024 * 3 + 256
+
+    def call8(**change):
+        a = dict(ks=16, vs=16, one=16, rows=16)
+        a.update(change)
+        return L.pa_decode_shared_int8(ctypes.byref(dims), 16, 16, 16, a["ks"], a["vs"], 16, ctypes.c_float(0.1), 16,
+                                       ctypes.byref(m), 16, 16, 16, a["one"], a["rows"], 256, 4096, None)
+
+    m.num_shared_items = 5  # more than there are items
+    assert call8() == pa.PA_ERR_INVALID_ARG
+    m.num_shared_items = 2
+    for bad in (dict(ks=None), dict(vs=None), dict(ks=24), dict(one=None), dict(one=8), dict(rows=None), dict(rows=18)):
+        assert call8(**bad) == pa.PA_ERR_INVALID_ARG, bad
     m.num_ctas = 0
     assert call(ws=256, nbytes=4096) == pa.PA_ERR_INVALID_ARG
