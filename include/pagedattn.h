@@ -136,12 +136,12 @@ typedef struct pa_shared_meta {
     int32_t tables_packed;      /* 1: the image holds block tables and slots */
     int32_t num_single_items;   /* (sequence, key range) parts of single sequences (INT8) */
     int32_t num_shared_items;   /* work items of several sequences */
-    int32_t reserved;
+    int32_t num_scratch_tiles;  /* 128-key tiles of the groups' shared parts (INT8) */
     uint64_t tokens_saved;       /* keys the groups read once instead of once per sequence */
     uint64_t off_block_tables;   /* int32 [num_seqs][max_blocks_per_seq], -1 padded (tables_packed) */
     uint64_t off_slot_mapping;   /* int32 [num_seqs] slot of each last token (tables_packed) */
     uint64_t off_items;          /* int32 [num_items][8]: first sequence, sequences, KV head,
-                                    block-table row, first key, end key, part, 0 */
+                                    block-table row, first key, end key, part, scratch row of key 0 */
     uint64_t off_cta_items;      /* int32 [num_ctas][4]: a CTA's items of more than rows_per_tile
                                     sequences start at the first, those of its two lanes at the
                                     second and third and end before the fourth, in each those of
@@ -150,8 +150,11 @@ typedef struct pa_shared_meta {
     uint64_t off_single_items;   /* int32 [num_single_items][4]: sequence, first key, end key,
                                     partial slot or -1 */
     uint64_t off_table_rows;     /* int32 [num_seqs] block-table row of each sequence */
+    uint64_t off_scratch_tiles;  /* int32 [num_scratch_tiles][4]: block-table row, first key, shared
+                                    tokens, scratch row of the first key */
     uint64_t total_bytes;
-    uint64_t workspace_bytes;    /* device workspace pa_decode_shared(_int8) needs */
+    uint64_t workspace_bytes;    /* device workspace pa_decode_shared needs */
+    uint64_t workspace_bytes_int8; /* and pa_decode_shared_int8: the shared parts and q in fp16 too */
 } pa_shared_meta;
 
 /*
@@ -619,18 +622,19 @@ int pa_decode_int8_fused(const pa_dims *dims, const void *q, const void *k, cons
 
 /*
  * pa_decode_shared_int8 — pa_decode_shared over an INT8 cache: the same plan
- * (pa_pack_decode_shared), workspace, rules and result, with the cached K and V
- * read as code * scale.  The shared parts' products run on the codes (exact in
- * bf16) with fp32 accumulation, the key scale multiplies the score and the value
- * scale the softmax weight; the parts of single sequences are computed as
- * pa_decode_int8 computes them.
- *   single_items, table_rows: device copies of the plan's arrays
+ * (pa_pack_decode_shared), rules and result, with the cached K and V read as
+ * code * scale.  A launch turns the shared parts' keys and values, and q, into
+ * fp16 in the workspace (rounded to nearest even, clamped to +-65504); their
+ * products run on those with fp32 accumulation.  The parts of single sequences
+ * are computed as pa_decode_int8 computes them.
+ *   single_items, table_rows, scratch_tiles: device copies of the plan's arrays
+ *   workspace:  at least meta->workspace_bytes_int8
  */
 int pa_decode_shared_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                           const void *k_scale, const void *v_scale, const int32_t *block_tables, float scale, void *out,
                           const pa_shared_meta *meta, const int32_t *items, const int32_t *cta_items,
                           const int32_t *seq_parts, const int32_t *single_items, const int32_t *table_rows,
-                          void *workspace, size_t workspace_bytes, pa_stream_t stream);
+                          const int32_t *scratch_tiles, void *workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /*
  * pa_copy_blocks_int8 — pa_copy_blocks on an INT8 cache: for each (src, dst, n)

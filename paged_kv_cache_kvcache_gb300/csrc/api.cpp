@@ -436,7 +436,7 @@ extern "C" int pa_decode_int8(const pa_dims *dims, const void *q, const void *k_
 }
 
 // Host-side checks of a shared-prefix decode; fills `a`.  Sets *nothing when there is no work.
-static int prepare_shared(const char *fn, const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                           const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
                           const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts, void *workspace,
                           size_t workspace_bytes, SharedArgs *a, bool *nothing)
@@ -468,17 +468,15 @@ static int prepare_shared(const char *fn, const pa_dims *dims, const void *q, co
         return fail(PA_ERR_INVALID_ARG, "%s: misaligned plan array or block table", fn);
     if (meta->num_items > 0 && dims->num_blocks == 0)
         return fail(PA_ERR_INVALID_ARG, "empty KV pool");
-    const size_t per = (size_t)dims->num_heads * dims->head_dim * 4;
-    const size_t o_bytes = align_up((size_t)meta->num_partials * per, 256);
-    if (meta->num_partials > 0) {
-        if (o_bytes + align_up((size_t)meta->num_partials * dims->num_heads * 4, 256) != meta->workspace_bytes)
-            return fail(PA_ERR_INVALID_ARG, "%s: meta was packed for other dims", fn);
-        if (workspace_bytes < meta->workspace_bytes)
-            return fail(PA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %llu", fn, workspace_bytes,
-                        (unsigned long long)meta->workspace_bytes);
-        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-            return fail(PA_ERR_INVALID_ARG, "%s: workspace must be non-NULL and 256-byte aligned", fn);
-    }
+    if (meta->num_scratch_tiles < 0 || meta->workspace_bytes != shared_part_bytes(*dims, meta->num_partials) ||
+        meta->workspace_bytes_int8 - meta->workspace_bytes != shared_scratch_bytes(*dims, meta->num_scratch_tiles, meta->num_seqs))
+        return fail(PA_ERR_INVALID_ARG, "%s: meta was packed for other dims", fn);
+    const uint64_t need = int8 ? meta->workspace_bytes_int8 : meta->workspace_bytes;
+    if (workspace_bytes < need)
+        return fail(PA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %llu", fn, workspace_bytes,
+                    (unsigned long long)need);
+    if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return fail(PA_ERR_INVALID_ARG, "%s: workspace must be non-NULL and 256-byte aligned", fn);
     *a = SharedArgs{};
     a->dims = *dims;
     a->q = q;
@@ -491,8 +489,11 @@ static int prepare_shared(const char *fn, const pa_dims *dims, const void *q, co
     a->out = out;
     if (meta->num_partials > 0) {
         a->part_o = static_cast<float *>(workspace);
-        a->part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) + o_bytes);
+        a->part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                                shared_part_o_bytes(*dims, meta->num_partials));
     }
+    a->scratch = static_cast<char *>(workspace) + meta->workspace_bytes;
+    a->num_scratch_tiles = meta->num_scratch_tiles;
     a->scale = scale;
     a->num_seqs = meta->num_seqs;
     a->num_items = meta->num_items;
@@ -510,7 +511,7 @@ extern "C" int pa_decode_shared(const pa_dims *dims, const void *q, const void *
 {
     SharedArgs a;
     bool nothing = false;
-    int rc = prepare_shared("pa_decode_shared", dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
+    int rc = prepare_shared("pa_decode_shared", false, dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
                             cta_items, seq_parts, workspace, workspace_bytes, &a, &nothing);
     if (rc != PA_OK || nothing)
         return rc;
@@ -521,26 +522,27 @@ extern "C" int pa_decode_shared_int8(const pa_dims *dims, const void *q, const v
                                      const void *k_scale, const void *v_scale, const int32_t *block_tables, float scale,
                                      void *out, const pa_shared_meta *meta, const int32_t *items,
                                      const int32_t *cta_items, const int32_t *seq_parts, const int32_t *single_items,
-                                     const int32_t *table_rows, void *workspace, size_t workspace_bytes,
-                                     pa_stream_t stream)
+                                     const int32_t *table_rows, const int32_t *scratch_tiles, void *workspace,
+                                     size_t workspace_bytes, pa_stream_t stream)
 {
     SharedArgs a;
     bool nothing = false;
-    int rc = prepare_shared("pa_decode_shared_int8", dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
+    int rc = prepare_shared("pa_decode_shared_int8", true, dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
                             cta_items, seq_parts, workspace, workspace_bytes, &a, &nothing);
     if (rc != PA_OK || nothing)
         return rc;
     if (meta->num_single_items < 0 || meta->num_shared_items < 0 || meta->num_shared_items > meta->num_items)
         return fail(PA_ERR_INVALID_ARG, "malformed shared decode meta");
-    if (!k_scale || !v_scale || !single_items || !table_rows)
+    if (!k_scale || !v_scale || !single_items || !table_rows || !scratch_tiles)
         return fail(PA_ERR_INVALID_ARG, "pa_decode_shared_int8: NULL pointer");
-    if (misaligned(k_scale) || misaligned(v_scale) || misaligned(single_items) ||
+    if (misaligned(k_scale) || misaligned(v_scale) || misaligned(single_items) || misaligned(scratch_tiles) ||
         (reinterpret_cast<uintptr_t>(table_rows) & 3u))
         return fail(PA_ERR_INVALID_ARG, "pa_decode_shared_int8: scales and items must be 16-byte aligned");
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.single_items = single_items;
     a.table_rows = table_rows;
+    a.scratch_tiles = scratch_tiles;
     a.num_items = meta->num_shared_items;
     a.num_single_items = meta->num_single_items;
     return launch_decode_shared(a, stream);

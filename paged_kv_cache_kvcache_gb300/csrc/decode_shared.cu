@@ -32,10 +32,11 @@
 // (TMA, one 3-D box per physical block), one MMA warp (tcgen05, S and O in tensor memory, P fed
 // back through tensor memory), one softmax warpgroup per tile; the rings run on across items.
 //
-// INT8 cache.  The codes are exact in bf16, so the products run on them and the scales enter in the
-// softmax: the keys' scale multiplies the score (fp32), the values' scale the weight before it is
-// rounded to bf16.  K and V codes come by TMA in granules of 32 keys; two warps turn them into the
-// bf16 tiles.  That keeps up with pairs but not with HBM, so parts of single sequences go to
+// INT8 cache.  A launch before turns what the shared parts read into fp16, once for all query
+// tiles and heads: keys and values (code * scale, rounded by 2^-12 at most; fp16 holds them to
+// 65504) and the queries.  The products then run as on a bf16 cache, with fp16 weights.  (Exact
+// codes with the scales in the softmax took 3.4 us per 128 keys and pair instead of 1.6: 64 more
+// 16-byte loads per row; converting in shared memory took 4.2.)  Parts of single sequences go to
 // the INT8 decode kernel, in a launch that may run beside this one.
 //
 // Every hand-off waits with a time limit; a wait that runs out sets an error bit and the
@@ -69,36 +70,24 @@ constexpr int kBoxRows = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f; // log2 units
-template <int D, bool kInt8>
+template <int D>
 struct ShLayout {
     static constexpr int kPanels = D / 64;        // 64-element (128-byte) panels along head_dim
     static constexpr int kPanelBytes = 128 * 128; // 128 rows x 128 bytes
     static constexpr int kTileBytes = kPanels * kPanelBytes;
-    static constexpr int kKStages = D == 64 ? 4 : kInt8 ? 2 : 3;
-    static constexpr int kVStages = D == 64 ? 4 : 2;
+    static constexpr int kKStages = D == 128 ? 3 : 4;
+    static constexpr int kVStages = D == 128 ? 2 : 4;
     static constexpr int kQ = 0; // two query tiles
     static constexpr int kK = kQ + 2 * kTileBytes;
     static constexpr int kV = kK + kKStages * kTileBytes;
-    // INT8: codes of K and of V as they come from the cache, in granules of 32 keys, and for each
-    // query tile the scales (K's, V's) of its last kScaleSlots key tiles
-    static constexpr int kGranule = 32 * D;
-    static constexpr int kGranules = D == 64 ? 8 : 3;
-    static constexpr int kScaleSlots = D == 64 ? 8 : 4;
-    static constexpr int kCodes = kV + kVStages * kTileBytes;
-    static constexpr int kScales = kCodes + (kInt8 ? 2 * kGranules * kGranule : 0);
-    static constexpr int kBar = kScales + (kInt8 ? 2 * kScaleSlots * 2 * 128 * 4 : 0);
-    static constexpr int kSmemBytes = kBar + 512 + 1024; // + alignment slack
-    // A slot is rewritten for key tile m of a lane once the score product at most kKStages tiles
-    // before is complete, and that one came after the softmax of the tile before it.
-    static_assert(!kInt8 || kScaleSlots >= kKStages + 2, "scales in use");
+    static constexpr int kBar = kV + kVStages * kTileBytes;
+    static constexpr int kSmemBytes = kBar + 256 + 1024; // + alignment slack
     static_assert(kKStages <= 4 && kVStages <= 4, "barrier slots");
     static_assert(kSmemBytes <= 232448, "shared memory per CTA");
 };
 
 struct ShParams {
-    const uint16_t *k_scale; // INT8 cache: fp16 [num_blocks][num_kv_heads][block_size]
-    const uint16_t *v_scale;
-    int32_t num_kv_heads;
+    int32_t scratch_rows; // INT8: rows of the scratch cache
     const int4 *items;
     const int4 *cta_items;
     const int2 *seq_parts;
@@ -129,9 +118,6 @@ struct Bars {
     __device__ uint32_t o_full(int t) const { return base + 8 * (24 + t); }
     __device__ uint32_t v_tail(int s) const { return base + 8 * (26 + s); }
     __device__ uint32_t tmem_slot() const { return base + 8 * 30; }
-    // INT8: granule s of the codes of K (v = 0) or V (v = 1)
-    __device__ uint32_t g_full(int v, int s) const { return base + 8 * (32 + 8 * v + s); }
-    __device__ uint32_t g_free(int v, int s) const { return base + 8 * (48 + 8 * v + s); }
 };
 constexpr int kTmemSlotOffset = 8 * 30;
 constexpr int kAbortOffset = 8 * 31;
@@ -140,6 +126,7 @@ struct Item {
     int s0, nseq, g; // sequences s0 .. s0 + nseq - 1 (rows of q), KV head
     int row, k0, k1; // block-table row, key range (k0 a multiple of the box)
     int part;        // which of each sequence's parts this is
+    int scratch;     // INT8: scratch row of key 0
     __device__ int tiles() const { return (k1 - k0 + 127) >> 7; }
     __device__ bool tail() const { return ((k1 - k0) & 127) != 0; } // the last key tile runs past k1
 };
@@ -163,7 +150,7 @@ struct ItemIter {
                 end = idx;
         }
     }
-    __device__ Item peek() const { return {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z}; }
+    __device__ Item peek() const { return {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w}; }
     __device__ Item next(bool fetch_now = true)
     {
         const Item w = peek();
@@ -219,23 +206,99 @@ struct Waiter {
     }
 };
 
-// 16 INT8 codes (one 16-byte vector) to bf16, exactly, as two 16-byte vectors.  A byte b is a code
-// c = (b & 0x7f) - (b & 0x80); 0x4300 | m is the bf16 number 128 + m for m < 128 and 256 for
-// m = 0x80, so c = bf16(0x4300 | b & 0x7f) - bf16(0x4300 | b & 0x80), both and their difference
-// exact (8 significant bits).
-__device__ __forceinline__ void codes_to_bf16(const uint4 &c, uint4 &lo, uint4 &hi)
+// 16 INT8 codes (one 16-byte vector) times a scale, rounded to fp16 (as two 16-byte vectors),
+// clamped to fp16's range.  The product is exact in fp32 (7 and 11 significant bits).
+__device__ __forceinline__ void codes_to_f16(const uint4 &c, float scale, uint4 &lo, uint4 &hi)
 {
     uint32_t w[8];
     const uint32_t u[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t b = ptx::prmt(u[i], 0u, h ? 0x4342 : 0x4140); // two codes, one per 16 bits
-            w[2 * i + h] = ptx::sub_bf16x2((b & 0x007f007fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u);
-        }
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = u[i >> 1] >> (16 * (i & 1));
+        const float x = (float)(int8_t)b * scale, y = (float)(int8_t)(b >> 8) * scale;
+        w[i] = ptx::pack_f16(fminf(fmaxf(x, -65504.f), 65504.f), fminf(fmaxf(y, -65504.f), 65504.f));
+    }
     lo = make_uint4(w[0], w[1], w[2], w[3]);
     hi = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+struct CodesParams {
+    const int4 *tiles; // block-table row, first key, shared tokens, scratch row of the first key
+    const int32_t *block_tables;
+    const uint4 *k_codes, *v_codes;    // INT8 cache, 16 codes each
+    const uint16_t *k_scale, *v_scale; // fp16 bits
+    uint4 *k_out, *v_out;              // fp16 scratch [scratch_rows][num_kv_heads][D]
+    const uint4 *q;                    // bf16
+    uint4 *q_out;                      // fp16
+    int32_t block_size, max_blocks, num_blocks, num_kv_heads, key_vecs, head_vecs;
+    int32_t tile_ctas; // CTAs that convert keys; the others convert queries
+    int64_t q_vecs;    // of 8 values
+};
+
+// What the shared parts' products read on an INT8 cache, in fp16: the shared prefixes' keys and
+// values (code * scale; 32 keys per CTA, K and V) and the queries.  Rows behind a prefix and
+// those of block ids outside the pool become zeros.  Bound by HBM: 1 byte read and 2 written per code.
+constexpr int kCodesKeys = 32;
+__global__ void __launch_bounds__(256) shared_codes_kernel(const CodesParams p)
+{
+    if ((int)blockIdx.x >= p.tile_ctas) {
+        const int64_t i = (int64_t)((int)blockIdx.x - p.tile_ctas) * 256 + threadIdx.x;
+        if (i >= p.q_vecs)
+            return;
+        const uint4 v = __ldg(p.q + i);
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float lo = __uint_as_float(u[e] << 16), hi = __uint_as_float(u[e] & 0xffff0000u);
+            w[e] = ptx::pack_f16(fminf(fmaxf(lo, -65504.f), 65504.f), fminf(fmaxf(hi, -65504.f), 65504.f));
+        }
+        p.q_out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+    }
+    const int4 t = p.tiles[blockIdx.x / (128 / kCodesKeys)];
+    const int first = t.y + (int)(blockIdx.x % (128 / kCodesKeys)) * kCodesKeys;
+    const int out0 = t.w + first - t.y;
+    const int bs = p.block_size;
+    const int total = kCodesKeys * p.key_vecs;
+    constexpr int kU = 2;
+    for (int i0 = threadIdx.x; i0 < total; i0 += 256 * kU) {
+        uint4 k[kU], v[kU];
+        float ks[kU], vs[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int i = i0 + 256 * u;
+            k[u] = v[u] = make_uint4(0, 0, 0, 0);
+            ks[u] = vs[u] = 0.f;
+            const int key = first + i / p.key_vecs;
+            if (i < total && key < t.z) {
+                const int phys = __ldg(p.block_tables + (size_t)t.x * p.max_blocks + key / bs);
+                if ((uint32_t)phys < (uint32_t)p.num_blocks) {
+                    const int vec = i % p.key_vecs, off = key & (bs - 1);
+                    const size_t at = ((size_t)phys * bs + off) * p.key_vecs + vec;
+                    const size_t sc = ((size_t)phys * p.num_kv_heads + vec / p.head_vecs) * bs + off;
+                    k[u] = __ldg(p.k_codes + at);
+                    v[u] = __ldg(p.v_codes + at);
+                    ks[u] = __half2float(__ushort_as_half(__ldg(p.k_scale + sc)));
+                    vs[u] = __half2float(__ushort_as_half(__ldg(p.v_scale + sc)));
+                } else {
+                    atomicOr(&g_shared_error, 2u);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int i = i0 + 256 * u;
+            if (i < total) {
+                const size_t at = 2 * ((size_t)out0 * p.key_vecs + i);
+                uint4 lo, hi;
+                codes_to_f16(k[u], ks[u], lo, hi);
+                ptx::st_global_v8(p.k_out + at, lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w);
+                codes_to_f16(v[u], vs[u], lo, hi);
+                ptx::st_global_v8(p.v_out + at, lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w);
+            }
+        }
+    }
 }
 
 template <int D, bool kInt8>
@@ -244,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const ShParams p)
 {
-    using L = ShLayout<D, kInt8>;
+    using L = ShLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -287,13 +350,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(bars.v_free(s), 1);
             ptx::mbar_init(bars.v_tail(s), 1);
         }
-        if constexpr (kInt8) {
-            for (int v = 0; v < 2; ++v)
-                for (int s = 0; s < L::kGranules; ++s) {
-                    ptx::mbar_init(bars.g_full(v, s), 1);
-                    ptx::mbar_init(bars.g_free(v, s), 1);
-                }
-        }
         *abort_flag = 0u;
         ptx::fence_mbar_init();
     }
@@ -305,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // and V producers, its blocks) is brought into L1 while the barriers and the tensor memory are
     // set up: three dependent loads otherwise stand before the first tile.
     const int4 span = __ldg(p.cta_items + blockIdx.x);
-    if (warp == kKWarp || warp == kVWarp) {
+    if (!kInt8 && (warp == kKWarp || warp == kVWarp)) {
         const int first = span.x < span.y ? span.x : span.y, second = span.x < span.y ? span.x : span.z;
         for (int i = first;; i = second) {
             if (i < span.w) {
@@ -344,179 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             return true;
         };
-        if (kInt8 && warp == kKWarp) {
-            // ------------------------------------------------------------ INT8: codes of K and V
-            const int bs = p.block_size;
-            const int box_rows = p.box_rows;
-            const int per_granule = 32 / box_rows; // boxes: 1 or 2
-            int st = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            auto sub_row = [&](const Item &w, int j) -> int { // as below, for the boxes of a whole tile
-                const int key = w.k0 + j * 128 + lane * box_rows;
-                if (lane * box_rows >= 128 || key >= w.k1)
-                    return p.num_blocks * bs;
-                const int phys = __ldg(p.block_tables + (size_t)w.row * p.max_blocks + key / bs);
-                if ((uint32_t)phys >= (uint32_t)p.num_blocks) {
-                    atomicOr(&g_shared_error, 2u);
-                    return p.num_blocks * bs;
-                }
-                return phys * bs + (key & (bs - 1));
-            };
-            auto load = [&](const Item &w, int cur) {
-                for (int gi = 0; gi < 4; ++gi) {
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        if (ph > 0 && !(ok = wwait(bars.g_free(v, st), (ph - 1) & 1)))
-                            return;
-                        if (lane == 0)
-                            ptx::mbar_arrive_expect_tx(bars.g_full(v, st), (uint32_t)L::kGranule);
-                        __syncwarp();
-                        const int sub = lane - gi * per_granule;
-                        if (sub >= 0 && sub < per_granule)
-                            ptx::tma_load_3d(sbase + L::kCodes + (v * L::kGranules + st) * L::kGranule + sub * box_rows * D,
-                                             v ? &tm_v : &tm_k, bars.g_full(v, st), 0, w.g, cur);
-                        __syncwarp();
-                    }
-                    if (++st == L::kGranules) {
-                        st = 0;
-                        ++ph;
-                    }
-                }
-            };
-            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
-                const Item w = it.next();
-                const int n = w.tiles();
-                int next = sub_row(w, 0);
-                for (int j = 0; ok && j < n; ++j) {
-                    const int cur = next;
-                    if (j + 1 < n)
-                        next = sub_row(w, j + 1);
-                    load(w, cur);
-                }
-            }
-            Lane<kInt8> l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
-            auto advance = [&](Lane<kInt8> &l) {
-                load(l.w, sub_row(l.w, l.j));
-                l.step();
-            };
-            while (ok && (l0.active || l1.active)) {
-                if (l0.active)
-                    advance(l0);
-                if (ok && l1.active)
-                    advance(l1);
-            }
-        } else if (kInt8 && (warp == kVWarp || warp == kQWarp)) {
-            // ------------------------------------------------------------ INT8: codes to bf16 tiles.  One
-            // warp converts K (and brings the scales of both), the other V (and loads the queries: its
-            // last tile of an item is converted when the item's last score product is under way).
-            const bool is_k = warp == kVWarp;
-            const int v = is_k ? 0 : 1;
-            const int nstages = is_k ? L::kKStages : L::kVStages;
-            int gs = 0, st = 0, sc0 = 0, sc1 = 0;
-            uint32_t gph = 0, ph = 0;
-            bool ok = true;
-            auto convert = [&](const Item &w, int j, bool to0, bool to1) { // for query tiles 0 and/or 1
-                uint2 s4[2]; // the scales of keys 4 lane .. 4 lane + 3; 0 for keys past the range
-                if (is_k) {
-                    const int key = w.k0 + j * 128 + lane * 4;
-                    s4[0] = s4[1] = make_uint2(0u, 0u);
-                    if (key < w.k1) {
-                        const int phys = __ldg(p.block_tables + (size_t)w.row * p.max_blocks + key / p.block_size);
-                        if ((uint32_t)phys < (uint32_t)p.num_blocks) {
-                            const size_t at = ((size_t)phys * p.num_kv_heads + w.g) * p.block_size +
-                                              (key & (p.block_size - 1));
-                            s4[0] = __ldg(reinterpret_cast<const uint2 *>(p.k_scale + at));
-                            s4[1] = __ldg(reinterpret_cast<const uint2 *>(p.v_scale + at));
-                        }
-                    }
-                }
-                if (ph > 0 && !(ok = wwait(is_k ? bars.k_free(st) : bars.v_free(st), (ph - 1) & 1)))
-                    return;
-                uint8_t *tile = sgen + (is_k ? L::kK : L::kV) + st * L::kTileBytes;
-                if (is_k) {
-                    const int left = w.k1 - (w.k0 + j * 128 + lane * 4);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&s4[x].x));
-                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&s4[x].y));
-                        const float4 f = make_float4(left > 0 ? a.x : 0.f, left > 1 ? a.y : 0.f, left > 2 ? b.x : 0.f,
-                                                     left > 3 ? b.y : 0.f);
-                        float4 *slot = reinterpret_cast<float4 *>(sgen + L::kScales) + x * 32 + lane;
-                        if (to0)
-                            slot[sc0 * 64] = f;
-                        if (to1)
-                            slot[(L::kScaleSlots + sc1) * 64] = f;
-                    }
-                    if (to0 && ++sc0 == L::kScaleSlots)
-                        sc0 = 0;
-                    if (to1 && ++sc1 == L::kScaleSlots)
-                        sc1 = 0;
-                }
-                for (int gi = 0; gi < 4; ++gi) {
-                    if (!(ok = wwait(bars.g_full(v, gs), gph & 1)))
-                        return;
-                    const uint32_t from = sbase + L::kCodes + (v * L::kGranules + gs) * L::kGranule;
-                    constexpr int kVecs = D / 16, kBatch = 4; // 16-byte vectors per key
-#pragma unroll
-                    for (int i0 = 0; i0 < kVecs; i0 += kBatch) {
-                        uint4 c[kBatch];
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            c[i] = ptx::lds_v4(from + ((i0 + i) * 32 + lane) * 16);
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) {
-                            const int e = (i0 + i) * 32 + lane;
-                            const int r = gi * 32 + e / kVecs, x = 2 * (e % kVecs); // key, first 16-byte chunk of its row
-                            uint4 lo, hi;
-                            codes_to_bf16(c[i], lo, hi);
-                            uint8_t *row = tile + (x >> 3) * L::kPanelBytes + r * 128;
-                            *reinterpret_cast<uint4 *>(row + (((x & 7) ^ (r & 7)) << 4)) = lo;
-                            *reinterpret_cast<uint4 *>(row + ((((x & 7) + 1) ^ (r & 7)) << 4)) = hi;
-                        }
-                    }
-                    __syncwarp();
-                    if (lane == 0)
-                        ptx::mbar_arrive(bars.g_free(v, gs));
-                    if (++gs == L::kGranules) {
-                        gs = 0;
-                        ++gph;
-                    }
-                }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    ptx::mbar_arrive(is_k ? bars.k_full(st) : bars.v_full(st));
-                if (++st == nstages) {
-                    st = 0;
-                    ++ph;
-                }
-            };
-            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
-                const Item w = it.next();
-                const int n = w.tiles();
-                if (!is_k && !(ok = load_q(w, 0, 0) && load_q(w, 1, P)))
-                    break;
-                for (int j = 0; ok && j < n; ++j)
-                    convert(w, j, true, true);
-            }
-            Lane<kInt8> l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
-            if (!is_k && ok && l0.active)
-                ok = load_q(l0.w, 0, 0);
-            if (!is_k && ok && l1.active)
-                ok = load_q(l1.w, 1, 0);
-            auto advance = [&](Lane<kInt8> &l, int t) {
-                convert(l.w, l.j, t == 0, t == 1);
-                if (ok && l.step() && l.active && !is_k)
-                    ok = load_q(l.w, t, 0);
-            };
-            while (ok && (l0.active || l1.active)) {
-                if (l0.active)
-                    advance(l0, 0);
-                if (ok && l1.active)
-                    advance(l1, 1);
-            }
-        } else if (!kInt8 && warp == kQWarp) {
+        if (warp == kQWarp) {
             // ------------------------------------------------------------ query producer
             bool ok = true;
             for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
@@ -532,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = load_q(w, first ? 0 : 1, 0);
                 (first ? at0 : at1) += w.tiles();
             }
-        } else if (!kInt8 && (warp == kKWarp || warp == kVWarp)) {
+        } else if (warp == kKWarp || warp == kVWarp) {
             // ------------------------------------------------------------ K and V producers
             const bool is_k = warp == kKWarp;
             const int nstages = is_k ? L::kKStages : L::kVStages;
@@ -549,7 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto sub_row = [&](const Item &w, int j) -> int {
                 const int key = w.k0 + j * 128 + lane * box_rows;
                 if (lane >= nsub || key >= w.k1)
-                    return p.num_blocks * bs;
+                    return kInt8 ? p.scratch_rows : p.num_blocks * bs;
+                if (kInt8)
+                    return w.scratch + key;
                 const int phys = __ldg(p.block_tables + (size_t)w.row * p.max_blocks + key / bs);
                 if ((uint32_t)phys >= (uint32_t)p.num_blocks) {
                     atomicOr(&g_shared_error, 2u);
@@ -572,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               cur, policy);
                 }
                 __syncwarp();
-                if (!is_k && (w.k1 - w.k0) - j * 128 < 128) {
+                if (!kInt8 && !is_k && (w.k1 - w.k0) - j * 128 < 128) {
                     // rows of keys past the range may hold anything (even NaN bit patterns): zeroed, so
                     // that a weight of 0 cannot turn them into NaN
                     if (!(ok = wwait(full, ph & 1)))
@@ -623,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kMmaWarp) {
             // ------------------------------------------------------------ MMA issuer (converged warp)
-            constexpr uint32_t idesc_s = ptx::idesc_bf16(128, 128, 0);
-            constexpr uint32_t idesc_o = ptx::idesc_bf16(128, D, 1);
+            constexpr uint32_t idesc_s = kInt8 ? ptx::idesc_f16(128, 128, 0) : ptx::idesc_bf16(128, 128, 0);
+            constexpr uint32_t idesc_o = kInt8 ? ptx::idesc_f16(128, D, 1) : ptx::idesc_bf16(128, D, 1);
             const uint32_t hi_k = (uint32_t)(ptx::smem_desc(0, 16, 1024, ptx::kSwizzle128B) >> 32);
             const uint32_t hi_v = (uint32_t)(ptx::smem_desc(0, L::kPanelBytes, 1024, ptx::kSwizzle128B) >> 32);
             auto desc = [](uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; };
@@ -666,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto wait_v = [&](bool tail) {
                 ok = ok && wwait(bars.v_full(vs), vph);
-                if (!kInt8 && tail) { // (codes are finite: nothing to zero)
+                if (!kInt8 && tail) { // (the scratch rows behind a prefix are zeros)
                     ok = ok && wwait(bars.v_tail(vs), (tailpar >> vs) & 1u);
                     tailpar ^= 1u << vs;
                 }
@@ -787,8 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_col = tmem + lane_addr + t * 256;
         const uint32_t o_col = s_col + 128;
         const float sl2 = p.scale_log2;
+        constexpr float kBias = kInt8 ? 7.f : 0.f; // 2^(7 + kRescaleThreshold) stays in fp16
         uint32_t ns = 0, no = 0;
-        int sc = 0; // INT8: scale slot of the next key tile
         bool ok = true;
         ItemIter<kInt8> items(p.items, span.x, span.y);
         bool single = false;
@@ -814,35 +700,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wwait(bars.s_full(t), ns & 1)))
                     break;
                 ns ^= 1;
-                const float4 *scales = reinterpret_cast<const float4 *>(sgen + L::kScales) +
-                                       (t * L::kScaleSlots + sc) * 64; // INT8: 32 of K's, then 32 of V's
-                if (kInt8 && ++sc == L::kScaleSlots)
-                    sc = 0;
                 if (warp_valid) {
                     ptx::tc_fence_after();
                     const int lim = w.k1 - w.k0 - j * 128; // keys of this tile (128 or more: all)
                     uint32_t sr[128];
                     float mx;
-                    if (kInt8 || lim < 128) {
+                    if (lim < 128) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             ptx::tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
                         ptx::tmem_wait_ld();
-                        if constexpr (kInt8) { // scores of the codes times the keys' scales
 #pragma unroll
-                            for (int c = 0; c < 128; c += 4) {
-                                const float4 f = scales[c >> 2];
-                                sr[c] = __float_as_uint(__uint_as_float(sr[c]) * f.x);
-                                sr[c + 1] = __float_as_uint(__uint_as_float(sr[c + 1]) * f.y);
-                                sr[c + 2] = __float_as_uint(__uint_as_float(sr[c + 2]) * f.z);
-                                sr[c + 3] = __float_as_uint(__uint_as_float(sr[c + 3]) * f.w);
-                            }
-                        }
-                        if (lim < 128) {
-#pragma unroll
-                            for (int c = 0; c < 128; ++c)
-                                sr[c] = c < lim ? sr[c] : __float_as_uint(-INFINITY);
-                        }
+                        for (int c = 0; c < 128; ++c)
+                            sr[c] = c < lim ? sr[c] : __float_as_uint(-INFINITY);
                         float m8[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -875,10 +745,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l_sum *= alpha;
                         m_ref = m_new;
                     }
-                    // P = 2^(s * scale * log2 e - m) as bf16 pairs written over S (weights in [0, 2^8], rounded
-                    // to the values' own type: half an ulp, 2^-9 of each weight); the row sum stays fp32
+                    // P = 2^(s * scale * log2 e - m) written over S as pairs of the values' own type: bf16 (weights
+                    // in [0, 2^8], each rounded by 2^-9 of it at most), or fp16 with 2^kBias times the weight
+                    // (2^-12; the weights that fp16 cannot hold, below 2^-31 of the largest, are lost: 2^-16 of
+                    // the sum over 32768 keys).  The row sum stays fp32.
                     const uint64_t sl2x2 = ptx::f2(sl2, sl2);
-                    const float negm = m_ref == -INFINITY ? 0.f : -m_ref;
+                    const float negm = m_ref == -INFINITY ? 0.f : kBias - m_ref;
                     const uint64_t negm2 = ptx::f2(negm, negm);
                     uint64_t sum2[4] = {ptx::f2(0.f, 0.f), ptx::f2(0.f, 0.f), ptx::f2(0.f, 0.f), ptx::f2(0.f, 0.f)};
 #pragma unroll
@@ -892,13 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           x0, x1);
                             const float e0 = ptx::ex2(x0), e1 = ptx::ex2(x1); // masked columns: 2^-inf = 0
                             sum2[(c >> 1) & 3] = ptx::f2_add(sum2[(c >> 1) & 3], ptx::f2(e0, e1));
-                            if constexpr (kInt8) { // the values' scales, before the rounding
-                                const float4 f = scales[32 + (c >> 2)];
-                                pk[(c >> 1) & 31] = c & 2 ? ptx::pack_bf16(e0 * f.z, e1 * f.w)
-                                                          : ptx::pack_bf16(e0 * f.x, e1 * f.y);
-                            } else {
-                                pk[(c >> 1) & 31] = ptx::pack_bf16(e0, e1);
-                            }
+                            pk[(c >> 1) & 31] = kInt8 ? ptx::pack_f16(e0, e1) : ptx::pack_bf16(e0, e1);
                         }
                         ptx::tmem_st32(s_col + 32 * h, pk);
                     }
@@ -946,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t slot = (size_t)sp.x + w.part;
             float *po = p.part_o + (slot * p.num_heads + head) * D;
             if (partial && !*abort_flag)
-                p.part_lse[slot * p.num_heads + head] = l_sum > 0.f ? m_ref + __log2f(l_sum) : -INFINITY;
+                p.part_lse[slot * p.num_heads + head] = l_sum > 0.f ? m_ref - kBias + __log2f(l_sum) : -INFINITY;
             __nv_bfloat16 *orow = p.out + ((size_t)seq * p.num_heads + head) * D;
             uint32_t o[D / 32][32];
 #pragma unroll
@@ -1057,21 +923,18 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const float *__rest
         dst[0] = x[0];
 }
 
-// One KV head's rows of a cache: bf16 in 128-byte swizzled panels of 64, INT8 codes row by row.
-template <int D, bool kInt8>
-int encode_cache(CUtensorMap *m, const void *cache, const pa_dims &d, uint32_t box_rows, const char *what)
+// One KV head's rows of a bf16 cache in 128-byte swizzled panels of 64.
+template <int D>
+int encode_cache(CUtensorMap *m, const void *cache, int num_kv_heads, uint64_t rows, uint32_t box_rows, const char *what)
 {
-    constexpr int kElem = kInt8 ? 1 : 2;
-    return encode_tmap_3d(m, kInt8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache, D,
-                          d.num_kv_heads, (uint64_t)d.num_blocks * d.block_size, (uint64_t)D * kElem,
-                          (uint64_t)d.num_kv_heads * D * kElem, kInt8 ? D : 64, 1, box_rows,
-                          kInt8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, what);
+    return encode_tmap_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache, D, num_kv_heads, rows, (uint64_t)D * 2,
+                          (uint64_t)num_kv_heads * D * 2, 64, 1, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, what);
 }
 
 template <int D, bool kInt8>
 int launch(const SharedArgs &a, cudaStream_t stream)
 {
-    using L = ShLayout<D, kInt8>;
+    using L = ShLayout<D>;
     if (int rc = ensure_smem<decode_shared_kernel<D, kInt8>>(L::kSmemBytes, "shared decode"))
         return rc;
     static std::atomic<int> launch_regs{0};
@@ -1089,20 +952,52 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     const pa_dims &d = a.dims;
     const int G = d.num_heads / d.num_kv_heads;
     if (a.num_items > 0) {
-        const uint32_t box_rows = d.block_size < kBoxRows ? (uint32_t)d.block_size : (uint32_t)kBoxRows;
-        constexpr CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const uint32_t box_rows = !kInt8 && d.block_size < kBoxRows ? (uint32_t)d.block_size : (uint32_t)kBoxRows;
+        // INT8: the products read the scratch cache
+        const size_t half = (size_t)a.num_scratch_tiles * 128 * d.num_kv_heads * D * 2;
+        const void *q = kInt8 ? static_cast<const char *>(a.scratch) + 2 * half : a.q;
+        const void *k_cache = kInt8 ? a.scratch : a.k_cache;
+        const void *v_cache = kInt8 ? static_cast<const char *>(a.scratch) + half : a.v_cache;
+        const uint64_t rows = kInt8 ? (uint64_t)a.num_scratch_tiles * 128 : (uint64_t)d.num_blocks * d.block_size;
+        constexpr CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16; // (copies bits: fp16 as well)
         constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
         const uint64_t qs = (uint64_t)d.num_heads * D * 2;
         CUtensorMap tq, tq1, tk, tv;
         int rc;
-        if ((rc = encode_tmap_3d(&tq, bf16, a.q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
+        if ((rc = encode_tmap_3d(&tq, bf16, q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
                                  (uint32_t)G, (uint32_t)a.rows_per_tile, sw, "q")) != PA_OK ||
-            (rc = encode_tmap_3d(&tq1, bf16, a.q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
+            (rc = encode_tmap_3d(&tq1, bf16, q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
                                  (uint32_t)G, 1, sw, "q")) != PA_OK ||
-            (rc = encode_cache<D, kInt8>(&tk, a.k_cache, d, box_rows, "k_cache")) != PA_OK ||
-            (rc = encode_cache<D, kInt8>(&tv, a.v_cache, d, box_rows, "v_cache")) != PA_OK)
+            (rc = encode_cache<D>(&tk, k_cache, d.num_kv_heads, rows, box_rows, "k_cache")) != PA_OK ||
+            (rc = encode_cache<D>(&tv, v_cache, d.num_kv_heads, rows, box_rows, "v_cache")) != PA_OK)
             return rc;
         ShParams p{};
+        if constexpr (kInt8) {
+            CodesParams c{};
+            c.tiles = reinterpret_cast<const int4 *>(a.scratch_tiles);
+            c.block_tables = a.block_tables;
+            c.k_codes = static_cast<const uint4 *>(a.k_cache);
+            c.v_codes = static_cast<const uint4 *>(a.v_cache);
+            c.k_scale = static_cast<const uint16_t *>(a.k_scale);
+            c.v_scale = static_cast<const uint16_t *>(a.v_scale);
+            c.k_out = static_cast<uint4 *>(a.scratch);
+            c.v_out = reinterpret_cast<uint4 *>(static_cast<char *>(a.scratch) + half);
+            c.q = static_cast<const uint4 *>(a.q);
+            c.q_out = reinterpret_cast<uint4 *>(static_cast<char *>(a.scratch) + 2 * half);
+            c.block_size = d.block_size;
+            c.max_blocks = a.max_blocks_per_seq;
+            c.num_blocks = d.num_blocks;
+            c.num_kv_heads = d.num_kv_heads;
+            c.key_vecs = d.num_kv_heads * D / 16;
+            c.head_vecs = D / 16;
+            c.tile_ctas = a.num_scratch_tiles * (128 / kCodesKeys);
+            c.q_vecs = (int64_t)a.num_seqs * d.num_heads * D / 8;
+            shared_codes_kernel<<<(unsigned)(c.tile_ctas + (c.q_vecs + 255) / 256), 256, 0, stream>>>(c);
+            const cudaError_t e = cudaGetLastError();
+            if (e != cudaSuccess)
+                return fail(PA_ERR_CUDA, "shared decode code conversion launch: %s", cudaGetErrorString(e));
+            p.scratch_rows = a.num_scratch_tiles * 128;
+        }
         p.items = reinterpret_cast<const int4 *>(a.items);
         p.cta_items = reinterpret_cast<const int4 *>(a.cta_items);
         p.seq_parts = reinterpret_cast<const int2 *>(a.seq_parts);
@@ -1118,17 +1013,13 @@ int launch(const SharedArgs &a, cudaStream_t stream)
         p.box_rows = (int32_t)box_rows;
         p.max_blocks = a.max_blocks_per_seq;
         p.num_blocks = d.num_blocks;
-        p.k_scale = static_cast<const uint16_t *>(a.k_scale);
-        p.v_scale = static_cast<const uint16_t *>(a.v_scale);
-        p.num_kv_heads = d.num_kv_heads;
         decode_shared_kernel<D, kInt8><<<(unsigned)a.num_ctas, kThreads, L::kSmemBytes, stream>>>(tq, tq1, tk, tv, p);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess)
             return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
     }
     if (kInt8 && a.num_single_items > 0) {
-        // the parts of single sequences: the INT8 decode kernel reads codes at 0.9 of the HBM rate, the
-        // conversion through shared memory above could not; it may run beside the shared parts
+        // the parts of single sequences; may run beside the shared parts
         DecodeArgs s{};
         s.dims = a.dims;
         s.q = a.q;

@@ -202,6 +202,9 @@ struct SharedArgs {
     const int32_t *seq_parts;
     const int32_t *single_items; // INT8 cache only
     const int32_t *table_rows;
+    const int32_t *scratch_tiles;
+    void *scratch; // fp16: the shared prefixes' K, then V, then the queries
+    int32_t num_scratch_tiles;
     void *out;
     float *part_o;   // [num_partials][Hq][D]
     float *part_lse; // [num_partials][Hq]
@@ -215,6 +218,21 @@ struct SharedArgs {
     bool merge; // some sequence has two or more parts, or none
 };
 int launch_decode_shared(const SharedArgs &a, void *stream);
+// Workspace layout of a shared-prefix decode: partial outputs, their log-sum-exps, then (INT8) the scratch.
+inline size_t shared_part_o_bytes(const pa_dims &d, int64_t partials)
+{
+    return align_up((size_t)partials * d.num_heads * d.head_dim * 4, 256);
+}
+inline size_t shared_part_bytes(const pa_dims &d, int64_t partials)
+{
+    return partials > 0 ? shared_part_o_bytes(d, partials) + align_up((size_t)partials * d.num_heads * 4, 256) : 0;
+}
+inline size_t shared_scratch_bytes(const pa_dims &d, int64_t tiles, int64_t num_seqs)
+{
+    return tiles == 0 ? 0
+                      : (size_t)tiles * 128 * d.num_kv_heads * d.head_dim * 2 * 2 +
+                            align_up((size_t)num_seqs * d.num_heads * d.head_dim * 2, 256);
+}
 
 // Page pool (pool.cu).
 struct PoolArgs {

@@ -27,6 +27,7 @@ constexpr float kPairStep = 1.62f, kSingleStep = 2.8f, kPairItem = 2.5f, kSingle
 
 struct Run { // consecutive sequences of a group that share `shared` tokens
     int32_t s0, n, shared;
+    int32_t scratch; // row of key 0 in the INT8 decode's scratch cache
 };
 
 struct Range { // one part of a context: units items per split
@@ -39,7 +40,7 @@ float item_cost(int32_t tiles, bool pair)
 }
 
 struct Work {
-    int32_t s0, n, g, row, k0, k1, part;
+    int32_t s0, n, g, row, k0, k1, part, scratch;
     float cost;
 };
 
@@ -113,7 +114,11 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     const int group = d.num_heads / d.num_kv_heads;
     const int32_t P = std::max(1, kPrefillRows / group);
     std::vector<Run> runs;
-    std::vector<int32_t> seq_shared(num_seqs, 0); // shared tokens of each sequence
+    struct Prefix {
+        int32_t row, shared, scratch;
+    };
+    std::vector<Prefix> groups_scratch;
+    int64_t scratch_tiles = 0;
     for (int32_t i = 0; num_seqs > 0 && i < num_groups; ++i) {
         const int32_t b0 = group_offsets[i], b1 = group_offsets[i + 1];
         int32_t live = 0, least = INT32_MAX, first = -1;
@@ -147,6 +152,12 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
             }
         if (live == 1)
             shared = 0; // one sequence shares nothing: its context is one part
+        // (several runs of a group read the same scratch rows)
+        const int32_t group_scratch = (int32_t)std::min<int64_t>(scratch_tiles * kTile, INT32_MAX);
+        if (shared > 0) {
+            groups_scratch.push_back({table_rows ? table_rows[first] : first, shared, group_scratch});
+            scratch_tiles += (shared + kTile - 1) / kTile;
+        }
         for (int32_t b = b0; b < b1;) {
             if (context_lens[b] == 0) {
                 ++b;
@@ -154,8 +165,8 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
             }
             int32_t e = b;
             while (e < b1 && context_lens[e] > 0)
-                seq_shared[e++] = shared;
-            runs.push_back({b, e - b, shared});
+                ++e;
+            runs.push_back({b, e - b, shared, group_scratch});
             b = e;
         }
     }
@@ -226,7 +237,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
             parts[b] = ps + (t > 0 ? splits_of(t, per) : 0);
         }
     }
-    auto cut = [&](int32_t s0, int32_t n, int32_t row, int32_t from, int32_t to, int32_t first_part) {
+    auto cut = [&](int32_t s0, int32_t n, int32_t row, int32_t from, int32_t to, int32_t first_part, int32_t scratch) {
         const int32_t tiles = (to - from + kTile - 1) / kTile;
         const int32_t s = splits_of(tiles, per);
         for (int32_t i = 0; i < s; ++i) {
@@ -235,7 +246,8 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
             for (int32_t g = 0; g < d.num_kv_heads; ++g)
                 for (int32_t q = 0; q < n; q += 2 * P) {
                     const int32_t m = std::min(n - q, 2 * P);
-                    works.push_back({s0 + q, m, g, row, k0, k1, first_part + i, item_cost(t1 - t0, m > P)});
+                    works.push_back({s0 + q, m, g, row, k0, k1, first_part + i, scratch,
+                                     item_cost(t1 - t0, m > P)});
                 }
         }
     };
@@ -243,10 +255,10 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         const int32_t ptiles = (r.shared + kTile - 1) / kTile;
         const int32_t ps = ptiles > 0 ? splits_of(ptiles, per) : 0;
         if (ps > 0)
-            cut(r.s0, r.n, table_rows ? table_rows[r.s0] : r.s0, 0, r.shared, 0);
+            cut(r.s0, r.n, table_rows ? table_rows[r.s0] : r.s0, 0, r.shared, 0, r.scratch);
         for (int32_t b = r.s0; b < r.s0 + r.n; ++b)
             if (context_lens[b] > r.shared)
-                cut(b, 1, table_rows ? table_rows[b] : b, r.shared, context_lens[b], ps);
+                cut(b, 1, table_rows ? table_rows[b] : b, r.shared, context_lens[b], ps, 0);
     }
     if (works.size() > (size_t)INT32_MAX / kSharedItemInts)
         return fail(PA_ERR_INVALID_ARG, "too many work items");
@@ -260,6 +272,8 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     }
     if (partials > INT32_MAX)
         return fail(PA_ERR_INVALID_ARG, "too many partial results");
+    if (scratch_tiles * kTile > INT32_MAX)
+        return fail(PA_ERR_INVALID_ARG, "the groups' shared tokens exceed int32");
     int32_t singles = 0, shared_items = 0;
     for (const Work &w : works) {
         singles += w.n == 1 && w.g == 0;
@@ -282,6 +296,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->tables_packed = packed ? 1 : 0;
     meta->num_single_items = singles;
     meta->num_shared_items = shared_items;
+    meta->num_scratch_tiles = (int32_t)scratch_tiles;
     for (const Run &r : runs)
         meta->tokens_saved += (uint64_t)r.shared * (uint64_t)(r.n - 1);
     meta->off_block_tables = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs * mb : 0);
@@ -291,10 +306,10 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->off_seq_parts = L.take(sizeof(int32_t) * 2 * (size_t)num_seqs);
     meta->off_single_items = L.take(sizeof(int32_t) * 4 * (size_t)singles);
     meta->off_table_rows = L.take(sizeof(int32_t) * (size_t)num_seqs);
+    meta->off_scratch_tiles = L.take(sizeof(int32_t) * 4 * (size_t)scratch_tiles);
     meta->total_bytes = L.off;
-    meta->workspace_bytes = partials > 0 ? align_up((size_t)partials * d.num_heads * d.head_dim * 4, 256) +
-                                               align_up((size_t)partials * d.num_heads * 4, 256)
-                                         : 0;
+    meta->workspace_bytes = shared_part_bytes(d, partials);
+    meta->workspace_bytes_int8 = meta->workspace_bytes + shared_scratch_bytes(d, scratch_tiles, num_seqs);
     if (!host_buf)
         return PA_OK;
     if (host_buf_bytes < meta->total_bytes)
@@ -317,6 +332,14 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     int32_t *rows = reinterpret_cast<int32_t *>(base + meta->off_table_rows);
     for (int32_t b = 0; b < num_seqs; ++b)
         rows[b] = table_rows ? table_rows[b] : b;
+    int32_t *tile = reinterpret_cast<int32_t *>(base + meta->off_scratch_tiles);
+    for (const Prefix &x : groups_scratch)
+        for (int32_t k = 0; k < x.shared; k += kTile, tile += 4) {
+            tile[0] = x.row;
+            tile[1] = k;
+            tile[2] = x.shared;
+            tile[3] = x.scratch + k;
+        }
     for (int32_t b = 0, slot = 0; b < num_seqs; ++b) {
         sp[2 * b] = slot;
         sp[2 * b + 1] = parts[b];
@@ -384,7 +407,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         e[4] = w.k0;
         e[5] = w.k1;
         e[6] = w.part;
-        e[7] = 0;
+        e[7] = w.scratch;
     }
     return PA_OK;
 }

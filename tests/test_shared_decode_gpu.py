@@ -153,7 +153,7 @@ def test_parity_int8(case, split):
 
 
 def test_int8_every_code():
-    """All 255 codes in keys and values, one key carrying nearly all the weight at a time: the conversion is exact."""
+    """All 255 codes in keys and values, with scales whose products fp16 holds exactly."""
     bs, hq, hkv, d = 256, 4, 1, 128
     ctx, lists = [256, 256], [[0], [0]]
     k = torch.zeros(2, bs, hkv, d, dtype=torch.int8, device="cuda")

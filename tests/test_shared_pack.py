@@ -71,8 +71,14 @@ def test_parts_cover_every_key_once(case):
     seen = [np.zeros((hkv, c), np.int32) for c in ctx]
     used = {}
     shared_reads = 0
-    for s0, n, g, row, k0, k1, part, zero in items.tolist():
-        assert zero == 0 and 1 <= n <= 2 * P and 0 <= k0 < k1 and 0 <= g < hkv
+    tiles = {tuple(x) for x in plan.host_array(m.off_scratch_tiles, 4 * m.num_scratch_tiles).reshape(-1, 4).tolist()}
+    assert len({x[3] for x in tiles}) == m.num_scratch_tiles and all(x[3] % 128 == 0 and x[1] < x[2] for x in tiles)
+    for s0, n, g, row, k0, k1, part, scratch in items.tolist():
+        if n > 1:  # every key tile of a shared part is in the scratch cache, at the item's row
+            for k in range(k0, k1, 128):
+                x, = [x for x in tiles if x[1] == k and x[3] == scratch + k]
+                assert x[2] >= min(k1, k + 128) and table[x[0], :x[2] // bs].tolist() == table[row, :x[2] // bs].tolist()
+        assert 1 <= n <= 2 * P and 0 <= k0 < k1 and 0 <= g < hkv
         assert k0 % min(bs, 128) == 0 and (split == 0 or k1 - k0 <= split)
         for b in range(s0, s0 + n):
             seen[b][g, k0:k1] += 1
@@ -163,7 +169,7 @@ def test_plan_for_a_device_table():
 def test_empty_batch_and_small_buffer():
     dims = pa.make_dims(8, 16, 4, 2, 64)
     plan = pa.pa_pack_decode_shared(dims, [], block_lists=[], pin=False)
-    assert plan.meta.num_items == 0 and plan.meta.workspace_bytes == 0
+    assert plan.meta.num_items == 0 and plan.meta.workspace_bytes == 0 and plan.meta.workspace_bytes_int8 == 0
     meta = pa.pa_shared_meta()
     ctx, off, groups = (np.array(x, np.int32) for x in ([20], [0, 2], [0, 1]))
     ids, buf = np.array([1, 2], np.int32), np.zeros(64, np.uint8)
@@ -193,24 +199,29 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     assert call(bt=None) == pa.PA_ERR_INVALID_ARG
     assert call(dims=pa.make_dims(8, 16, 8, 2, 64)) == pa.PA_ERR_INVALID_ARG   # packed for group 2
     assert call(dims=pa.make_dims(0, 16, 4, 2, 64)) == pa.PA_ERR_INVALID_ARG   # empty pool
-    m.num_partials, m.workspace_bytes = 3, 1024 * 3 + 256
+    m.num_partials, m.workspace_bytes, m.workspace_bytes_int8 = 3, 1024 * 3 + 256, 1024 * 3 + 256
     assert call(ws=256, nbytes=1024) == pa.PA_ERR_WORKSPACE
     assert call(ws=16, nbytes=4096) == pa.PA_ERR_INVALID_ARG                   # not 256-byte aligned
     assert call(ws=None, nbytes=4096) == pa.PA_ERR_INVALID_ARG
     m.workspace_bytes = 512                                                    # not this batch's size
     assert call(ws=256, nbytes=4096) == pa.PA_ERR_INVALID_ARG
-    m.workspace_bytes = 1024 * 3 + 256
+    m.workspace_bytes, m.num_scratch_tiles = 1024 * 3 + 256, 2
+    m.workspace_bytes_int8 = m.workspace_bytes + 2 * 128 * 2 * 64 * 4 + 2 * 4 * 64 * 2
 
     def call8(**change):
-        a = dict(ks=16, vs=16, one=16, rows=16)
+        a = dict(ks=16, vs=16, one=16, rows=16, tiles=16, nbytes=1 << 20)
         a.update(change)
         return L.pa_decode_shared_int8(ctypes.byref(dims), 16, 16, 16, a["ks"], a["vs"], 16, ctypes.c_float(0.1), 16,
-                                       ctypes.byref(m), 16, 16, 16, a["one"], a["rows"], 256, 4096, None)
+                                       ctypes.byref(m), 16, 16, 16, a["one"], a["rows"], a["tiles"], 256, a["nbytes"], None)
 
     m.num_shared_items = 5  # more than there are items
     assert call8() == pa.PA_ERR_INVALID_ARG
     m.num_shared_items = 2
-    for bad in (dict(ks=None), dict(vs=None), dict(ks=24), dict(one=None), dict(one=8), dict(rows=None), dict(rows=18)):
+    for bad in (dict(ks=None), dict(vs=None), dict(ks=24), dict(one=None), dict(one=8), dict(rows=None), dict(rows=18), dict(tiles=None),
+                dict(tiles=8)):
         assert call8(**bad) == pa.PA_ERR_INVALID_ARG, bad
+    assert call8(nbytes=m.workspace_bytes) == pa.PA_ERR_WORKSPACE  # bf16's would do
+    m.num_scratch_tiles = 1
+    assert call8() == pa.PA_ERR_INVALID_ARG
     m.num_ctas = 0
     assert call(ws=256, nbytes=4096) == pa.PA_ERR_INVALID_ARG
