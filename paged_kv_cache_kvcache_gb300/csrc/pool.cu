@@ -8,12 +8,13 @@
 // taken lowest id first: the result then depends on the state alone and not on the order in
 // which pages came back, and nothing but the counts has to be kept consistent.
 //
-// append, fork and compact need order-dependent counts (the i-th new page is the i-th free
-// id), so one thread-block cluster plans the call: every CTA holds a slice of the ids or
-// rows, block-wide scans give ranks, and the CTAs' totals meet through distributed shared
-// memory.  The plan is all or nothing: it is checked to the end before any state changes, and a
-// refused call sets an error bit and leaves the pool as it was.  Moving pages is a second,
-// grid-wide launch, bound by HBM (each byte read and written once); it is launched
+// append, fork and compact need order-dependent counts (the i-th new page is the i-th free id), so
+// a call is planned where threads can scan: by one CTA for small pools (everything in shared
+// memory, bound by its four dependent look-ups: row, length, last page, its count), by a cluster of
+// eight for large ones (the ids scanned by all, the CTAs' totals meeting through distributed shared
+// memory).  The plan is all or nothing: it is checked to the end before any state changes, and a
+// refused call sets an error bit and leaves the pool as it was.  What is many (slots of a prompt
+// batch, pages to move) is a second, grid-wide launch, bound by HBM; it is launched
 // programmatically, so that its start-up runs under the plan.
 #include <algorithm>
 
@@ -34,16 +35,19 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kIdsPerThread = 4;
+constexpr int kIds = 16;              // ids per thread and round of a search for free pages
+constexpr int kClusterCtas = 8;
 constexpr int kMoveThreads = 256;
 constexpr int kPieceBytes = 16 << 10; // one CTA's unit of page copying: 4 x 16 bytes per thread
+constexpr int kRowBits = 65536;       // rows whose use in a call is kept in a bitmap in shared memory
+constexpr int kSmallList = 4096;      // free ids kept in shared memory
 
-// Workspace: header, marks [num_rows], starts [num_rows], copies int4 [num_rows],
+// Workspace: header, copies int4 [num_rows], marks, starts, lens, cums [num_rows],
 // list [num_blocks], list2 [num_blocks].
 struct Ws {
-    int32_t *head; // [0] copies or moves of the call
-    int32_t *marks, *starts;
+    int32_t *head; // [0] copies or moves of the call, -1: refused; [1] pieces of the copies; [2] compact: u(U)
     int4 *copies;
+    int32_t *marks, *starts, *lens, *cums;
     int32_t *list, *list2;
 };
 
@@ -55,33 +59,47 @@ __host__ __device__ inline Ws carve(void *p, int num_rows, int num_blocks)
     w.copies = reinterpret_cast<int4 *>(q + 16);
     w.marks = q + 16 + 4 * (size_t)num_rows;
     w.starts = w.marks + num_rows;
-    w.list = w.starts + num_rows;
+    w.lens = w.starts + num_rows;
+    w.cums = w.lens + num_rows;
+    w.list = w.cums + num_rows;
     w.list2 = w.list + num_blocks;
     return w;
 }
+constexpr int kWsRowInts = 8, kWsBlockInts = 2;
 
 struct Smem {
-    int warp[kWarps];
-    int total[2];      // this CTA's total of a scan, by scan parity
-    int flags[2];      // this CTA's OR, by parity
+    int warp[2][kWarps];
+    int total[2];          // this CTA's total of a scan, by scan parity
+    int bad;               // first CTA: refusal bits
+    int want;              // and pages the call needs
+    uint32_t bits[kRowBits / 32];
+    int starts[kThreads], lens[kThreads];
+    int list[kSmallList];
 };
 
-// Scans and reductions over the cluster's threads in (CTA rank, thread) order.  Each call is
-// one cluster barrier; totals alternate between two words, so the next call's writes cannot
-// meet a slow reader of this call's.
-struct ClusterOps {
+// Scans over the threads of one CTA (kCluster false) or of the cluster, in (CTA rank, thread)
+// order.  Buffers alternate by call, so one barrier per call is enough: the next call's writes
+// cannot meet a slow reader of this one's.
+template <bool kCluster>
+struct Team {
     Smem &s;
-    cg::cluster_group cl;
-    int parity = 0;
+    int parity = 0; // of this CTA's scans (the first CTA's counting of rows makes it differ between CTAs)
+    int turn = 0;   // of the team's
 
-    __device__ explicit ClusterOps(Smem &s_) : s(s_), cl(cg::this_cluster()) {}
-    __device__ int ctas() const { return (int)cl.num_blocks(); }
-    __device__ int rank() const { return (int)cl.block_rank(); }
+    __device__ explicit Team(Smem &s_) : s(s_) {}
+    __device__ int ctas() const { return kCluster ? (int)cg::this_cluster().num_blocks() : 1; }
+    __device__ int rank() const { return kCluster ? (int)cg::this_cluster().block_rank() : 0; }
     __device__ int threads() const { return ctas() * kThreads; }
     __device__ int thread() const { return rank() * kThreads + (int)threadIdx.x; }
-
-    // exclusive sum of v over all threads before this one; *total = the sum over all
-    __device__ int scan(int v, int *total)
+    __device__ void sync()
+    {
+        if constexpr (kCluster)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
+    }
+    // exclusive sum of v over the CTA's threads before this one; *total = the CTA's sum
+    __device__ int scan_cta(int v, int *total)
     {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         int x = v;
@@ -92,9 +110,9 @@ struct ClusterOps {
                 x += y;
         }
         if (lane == 31)
-            s.warp[warp] = x;
+            s.warp[parity][warp] = x;
         __syncthreads();
-        const int w = s.warp[lane];
+        const int w = s.warp[parity][lane];
         int wx = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -102,32 +120,38 @@ struct ClusterOps {
             if (lane >= o)
                 wx += y;
         }
-        const int before = __shfl_sync(0xffffffffu, wx - w, warp);
-        if (threadIdx.x == kThreads - 1)
-            s.total[parity] = wx;
-        cl.sync(); // also orders s.warp's reads before the next call's writes
+        parity ^= 1;
+        *total = __shfl_sync(0xffffffffu, wx, 31);
+        return __shfl_sync(0xffffffffu, wx - w, warp) + x - v;
+    }
+    // the same over all threads of the team
+    __device__ int scan(int v, int *total)
+    {
+        int mine;
+        const int before = scan_cta(v, &mine);
+        if constexpr (!kCluster) {
+            *total = mine;
+            return before;
+        }
+        if (threadIdx.x == 0)
+            s.total[turn] = mine;
+        sync();
         int base = 0, sum = 0;
         for (int c = 0; c < ctas(); ++c) {
-            const int t = *cl.map_shared_rank(&s.total[parity], c);
+            const int t = *cg::this_cluster().map_shared_rank(&s.total[turn], c);
             base += c < rank() ? t : 0;
             sum += t;
         }
-        parity ^= 1;
+        turn ^= 1;
         *total = sum;
-        return base + before + x - v;
+        return base + before;
     }
-    // OR over all threads of the cluster
-    __device__ int any(int v)
+    // a word of the first CTA's shared memory, after the barrier that follows its write
+    __device__ int of_first(int *word)
     {
-        const int mine = __syncthreads_or(v & 1) | (__syncthreads_or(v & 2) ? 2 : 0);
-        if (threadIdx.x == 0)
-            s.flags[parity] = mine;
-        cl.sync();
-        int f = 0;
-        for (int c = 0; c < ctas(); ++c)
-            f |= *cl.map_shared_rank(&s.flags[parity], c);
-        parity ^= 1;
-        return f;
+        if constexpr (kCluster)
+            return *cg::this_cluster().map_shared_rank(word, 0);
+        return *word;
     }
 };
 
@@ -138,31 +162,47 @@ struct PoolParams {
     int32_t num_rows, max_blocks, num_blocks, block_size;
 };
 
-// The lowest `want` ids of reference count 0 into list; returns how many there are (at most
-// want).  Rounds of 4 ids per thread, ending when enough are found.
-__device__ int lowest_free(ClusterOps &ops, const PoolParams &p, int want, int32_t *list)
+// Counts of 16 consecutive ids; those past the pool count as used.
+__device__ __forceinline__ void load_refs(const PoolParams &p, int id, int4 (&r)[kIds / 4])
 {
-    const int per_round = ops.threads() * kIdsPerThread;
-    int found = 0;
-    for (int base = 0; base < p.num_blocks && found < want; base += per_round) {
-        const int id = base + ops.thread() * kIdsPerThread;
-        uint32_t free = 0;
-        if (id + kIdsPerThread <= p.num_blocks) {
-            const int4 r = *reinterpret_cast<const int4 *>(p.refs + id); // 16-byte aligned: checked on the host
-            free = (r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3;
-        } else {
-            for (int i = 0; i < kIdsPerThread; ++i)
-                if (id + i < p.num_blocks && p.refs[id + i] == 0)
-                    free |= 1u << i;
+#pragma unroll
+    for (int i = 0; i < kIds / 4; ++i) {
+        const int at = id + 4 * i;
+        r[i] = make_int4(1, 1, 1, 1);
+        if (at + 4 <= p.num_blocks) {
+            r[i] = *reinterpret_cast<const int4 *>(p.refs + at); // 16-byte aligned: checked on the host
+        } else if (at < p.num_blocks) {
+            r[i].x = p.refs[at];
+            r[i].y = at + 1 < p.num_blocks ? p.refs[at + 1] : 1;
+            r[i].z = at + 2 < p.num_blocks ? p.refs[at + 2] : 1;
         }
+    }
+}
+__device__ __forceinline__ uint32_t free_mask(const int4 (&r)[kIds / 4])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kIds / 4; ++i)
+        m |= (uint32_t)((r[i].x == 0) | (r[i].y == 0) << 1 | (r[i].z == 0) << 2 | (r[i].w == 0) << 3) << (4 * i);
+    return m;
+}
+
+// The lowest `want` ids of count 0 into list; returns how many there are (at most want).  `r`:
+// the counts of this thread's ids of the first round, loaded by the caller ahead of time.
+template <bool kCluster>
+__device__ int lowest_free(Team<kCluster> &team, const PoolParams &p, int want, int32_t *list, int4 (&r)[kIds / 4])
+{
+    const int per_round = team.threads() * kIds;
+    int found = 0;
+    for (int64_t base = 0; base < p.num_blocks && found < want; base += per_round) {
+        const int id = (int)min(base + (int64_t)team.thread() * kIds, (int64_t)p.num_blocks);
+        if (base > 0)
+            load_refs(p, id, r);
+        uint32_t m = free_mask(r);
         int sum;
-        int at = found + ops.scan(__popc(free), &sum);
-        for (int i = 0; i < kIdsPerThread; ++i)
-            if (free >> i & 1u) {
-                if (at < want)
-                    list[at] = id + i;
-                ++at;
-            }
+        int at = found + team.scan(__popc(m), &sum);
+        for (; m && at < want; m &= m - 1)
+            list[at++] = id + __ffs(m) - 1;
         found += sum;
     }
     return min(found, want);
@@ -170,184 +210,302 @@ __device__ int lowest_free(ClusterOps &ops, const PoolParams &p, int want, int32
 
 __device__ __forceinline__ int pages(int tokens, int bs) { return (tokens + bs - 1) / bs; }
 
+// Notes that entry i of the call names row r; true if another entry already did (bitmap), or, for
+// pools of very many rows, to be asked again with marked_twice after a barrier.
+__device__ __forceinline__ bool mark_row(Smem &s, const Ws &w, int num_rows, int r, int i)
+{
+    if (num_rows <= kRowBits)
+        return atomicOr(&s.bits[r >> 5], 1u << (r & 31)) >> (r & 31) & 1u;
+    w.marks[r] = i;
+    return false;
+}
+__device__ __forceinline__ bool marked_twice(const Ws &w, int num_rows, int r, int i)
+{
+    return num_rows > kRowBits && w.marks[r] != i;
+}
+
+// The last index of [0, n) whose entry of the ascending `a` is at most x (a[0] <= x).
+__device__ __forceinline__ int last_at_most(const int32_t *a, int n, int x)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// What the planning kernels begin with: shared memory cleared, this thread's counts on their way.
+template <bool kCluster>
+__device__ __forceinline__ void plan_begin(Team<kCluster> &team, const PoolParams &p, int4 (&refs)[kIds / 4])
+{
+    load_refs(p, (int)min((int64_t)team.thread() * kIds, (int64_t)p.num_blocks), refs);
+    const int words = (min(p.num_rows, kRowBits) + 31) / 32;
+    if (team.rank() == 0)
+        for (int i = threadIdx.x; i < words; i += kThreads)
+            team.s.bits[i] = 0;
+    if (threadIdx.x == 0)
+        team.s.bad = 0;
+    __syncthreads();
+}
+
 // ---------------------------------------------------------------- append
 
+// Slots of new tokens: token t of entry i is token lens[i] + t - cu[i] of its row.
+__device__ __forceinline__ int slot_of(const PoolParams &p, int row, int pos)
+{
+    return p.tables[(size_t)row * p.max_blocks + pos / p.block_size] * p.block_size + pos % p.block_size;
+}
+
+// The rows are checked and counted by the first CTA, the free ids found by all.  kSlots: the slots
+// are written here (few tokens), else by pool_slots_kernel.
+template <bool kCluster, bool kSlots>
 __global__ void __launch_bounds__(kThreads)
     pool_append_kernel(const PoolParams p, const int32_t *__restrict__ rows, const int32_t *__restrict__ cu, int n,
                        int32_t *__restrict__ slots, int num_tokens, void *workspace)
 {
     __shared__ Smem sm;
-    ClusterOps ops(sm);
+    if (!kSlots)
+        ptx::launch_dependents();
+    Team<kCluster> team(sm);
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
-    const int nt = ops.threads(), me = ops.thread(), bs = p.block_size;
-    int bad = 0, want = 0;
-    if (me == 0 && (cu[0] != 0 || cu[n] != num_tokens))
-        bad = 2;
-    for (int base = 0; base < n; base += nt) {
-        const int i = base + me;
-        int need = 0;
-        if (i < n) {
-            const int r = rows[i];
-            const int64_t count = (int64_t)cu[i + 1] - cu[i];
-            if ((uint32_t)r >= (uint32_t)p.num_rows || count < 0) {
-                bad |= 2;
-            } else {
-                w.marks[r] = i;
-                const int ctx = p.context_lens[r];
-                if (ctx < 0 || (int64_t)ctx > (int64_t)p.max_blocks * bs) {
-                    bad |= 2;
-                } else if (ctx + count > (int64_t)p.max_blocks * bs) {
-                    bad |= 1;
+    const int nt = team.threads(), me = team.thread(), bs = p.block_size;
+    int4 refs[kIds / 4];
+    plan_begin(team, p, refs);
+    const bool small = !kCluster && n <= kThreads; // the rows' counts stay in shared memory
+    int32_t *starts = small ? sm.starts : w.starts, *lens = small ? sm.lens : w.lens;
+    if (team.rank() == 0) {
+        int want = 0;
+        if (threadIdx.x == 0 && (cu[0] != 0 || cu[n] != num_tokens))
+            atomicOr(&sm.bad, 2);
+        for (int base = 0; base < n; base += kThreads) {
+            const int i = base + (int)threadIdx.x;
+            int need = 0, bad = 0, ctx = 0;
+            if (i < n) {
+                const int r = rows[i];
+                const int64_t count = (int64_t)cu[i + 1] - cu[i];
+                if ((uint32_t)r >= (uint32_t)p.num_rows || count < 0) {
+                    bad = 2;
                 } else {
-                    need = pages(ctx + (int)count, bs) - pages(ctx, bs);
-                    if (count > 0 && ctx % bs != 0) { // the partly filled page takes the first tokens: it must be the row's own
-                        const int page = p.tables[(size_t)r * p.max_blocks + ctx / bs];
-                        if ((uint32_t)page >= (uint32_t)p.num_blocks || p.refs[page] != 1)
-                            bad |= 2;
+                    ctx = p.context_lens[r];
+                    bad = mark_row(sm, w, p.num_rows, r, i) ? 2 : 0;
+                    if (ctx < 0 || (int64_t)ctx > (int64_t)p.max_blocks * bs) {
+                        bad = 2;
+                    } else if (ctx + count > (int64_t)p.max_blocks * bs) {
+                        bad |= 1;
+                    } else {
+                        need = pages(ctx + (int)count, bs) - pages(ctx, bs);
+                        if (count > 0 && ctx % bs != 0) { // the partly filled page must be the row's own
+                            const int page = p.tables[(size_t)r * p.max_blocks + ctx / bs];
+                            if ((uint32_t)page >= (uint32_t)p.num_blocks || p.refs[page] != 1)
+                                bad |= 2;
+                        }
                     }
                 }
+                lens[i] = ctx;
             }
+            if (bad)
+                atomicOr(&sm.bad, bad);
+            int sum;
+            const int at = want + team.scan_cta(need, &sum); // at most num_rows * max_blocks: an int32
+            if (i < n)
+                starts[i] = at;
+            want += sum;
         }
-        int sum;
-        const int at = want + ops.scan(need, &sum);
-        if (i < n)
-            w.starts[i] = at;
-        want += sum;
-        if (want < 0 || want > p.num_blocks) { // more than the pool holds: no need to count on
-            bad |= 1;
-            break;
+        if (p.num_rows > kRowBits) {
+            __syncthreads(); // all marks
+            for (int i = threadIdx.x; i < n; i += kThreads)
+                if ((uint32_t)rows[i] < (uint32_t)p.num_rows && marked_twice(w, p.num_rows, rows[i], i))
+                    atomicOr(&sm.bad, 2);
         }
+        if (threadIdx.x == 0)
+            sm.want = want;
     }
-    if (!(ops.any(bad))) { // all marks are written
-        for (int i = me; i < n; i += nt)
-            if (w.marks[rows[i]] != i)
-                bad |= 2; // the same row twice
-    }
-    bad = ops.any(bad);
-    if (!bad && lowest_free(ops, p, want, w.list) < want)
+    team.sync();
+    const int want = team.of_first(&sm.want);
+    int bad = team.of_first(&sm.bad);
+    if (want > p.num_blocks)
+        bad |= 1;
+    int32_t *list = !kCluster && want <= kSmallList ? sm.list : w.list;
+    if (!bad && lowest_free(team, p, want, list, refs) < want)
         bad = 1;
     if (bad) {
-        if (me == 0)
+        if (me == 0) {
             atomicOr(&g_pool_error, (uint32_t)bad);
-        for (int t = me; t < num_tokens; t += nt)
-            slots[t] = -1;
-        ops.cl.sync();
+            w.head[0] = -1;
+        }
+        if (kSlots)
+            for (int t = me; t < num_tokens; t += nt)
+                slots[t] = -1;
+        team.sync(); // nobody leaves while its shared memory may be read
         return;
     }
-    ops.cl.sync(); // the list
-    // tokens: a warp's 32 consecutive ones lie in one row or a few neighbouring ones
-    for (int t0 = me & ~31; t0 < num_tokens; t0 += nt) {
-        int lo = 0, hi = n; // cu[lo] <= t0 < cu[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] <= t0)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const int t = t0 + (me & 31);
-        if (t < num_tokens) {
-            int i = lo;
-            while (cu[i + 1] <= t)
-                ++i;
-            const int r = rows[i], ctx = p.context_lens[r], pos = ctx + t - cu[i];
-            const int page = pos / bs, old = pages(ctx, bs);
-            const int id = page < old ? p.tables[(size_t)r * p.max_blocks + page] : w.list[w.starts[i] + page - old];
-            slots[t] = id * bs + pos % bs;
-        }
-    }
-    // new pages into the tables
-    for (int j = me; j < want; j += nt) {
-        int lo = 0, hi = n; // the last row whose pages start at or before j
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (w.starts[mid] <= j)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const int r = rows[lo], id = w.list[j];
-        p.tables[(size_t)r * p.max_blocks + pages(p.context_lens[r], bs) + j - w.starts[lo]] = id;
+    if (!kSlots && me == 0)
+        w.head[0] = n;
+    team.sync(); // the list
+    for (int j = me; j < want; j += nt) { // new pages into the tables
+        const int i = last_at_most(starts, n, j), id = list[j];
+        p.tables[(size_t)rows[i] * p.max_blocks + pages(lens[i], bs) + j - starts[i]] = id;
         p.refs[id] = 1;
     }
-    ops.cl.sync(); // every reader of the old lengths is done
     for (int i = me; i < n; i += nt) {
         const int count = cu[i + 1] - cu[i];
         if (count > 0)
-            p.context_lens[rows[i]] += count;
+            p.context_lens[rows[i]] = lens[i] + count;
+    }
+    if (kSlots) {
+        for (int t = me; t < num_tokens; t += nt) {
+            const int i = last_at_most(cu, n, t), pos = lens[i] + t - cu[i];
+            const int page = pos / bs, old = pages(lens[i], bs);
+            // (the tables' new entries are other threads' writes: the list has them)
+            slots[t] = page < old ? slot_of(p, rows[i], pos) : list[starts[i] + page - old] * bs + pos % bs;
+        }
+    }
+    team.sync();
+}
+
+// The slots of many tokens, from the tables as the plan left them: four tokens per thread, the
+// warp's first row found once.
+__global__ void __launch_bounds__(256)
+    pool_slots_kernel(const PoolParams p, const int32_t *__restrict__ rows, const int32_t *__restrict__ cu, int n,
+                      int32_t *__restrict__ slots, int num_tokens, void *workspace)
+{
+    ptx::grid_dependency_wait();
+    const bool refused = *static_cast<const int32_t *>(workspace) < 0;
+    const int64_t t0 = ((int64_t)blockIdx.x * 256 + (threadIdx.x & ~31u)) * 4, t = t0 + 4 * (threadIdx.x & 31u);
+    if (t >= num_tokens)
+        return;
+    int v[4] = {-1, -1, -1, -1};
+    const int m = (int)min((int64_t)4, num_tokens - t);
+    if (!refused) {
+        int i = last_at_most(cu, n, (int)t0);
+        int begin = cu[i], end = cu[i + 1];
+        int row = -1, from = 0; // the row, and the position of its token `begin`
+        for (int e = 0; e < m; ++e) {
+            while (end <= t + e) {
+                begin = end;
+                end = cu[++i + 1];
+                row = -1;
+            }
+            if (row < 0) {
+                row = rows[i];
+                from = p.context_lens[row] - (end - begin);
+            }
+            v[e] = slot_of(p, row, from + (int)(t + e) - begin);
+        }
+    }
+    if (m == 4 && (reinterpret_cast<uintptr_t>(slots) & 15u) == 0) {
+        *reinterpret_cast<int4 *>(slots + t) = make_int4(v[0], v[1], v[2], v[3]);
+    } else {
+        for (int e = 0; e < m; ++e)
+            slots[t + e] = v[e];
     }
 }
 
 // ---------------------------------------------------------------- fork
 
+template <bool kCluster>
 __global__ void __launch_bounds__(kThreads)
     pool_fork_kernel(const PoolParams p, const int32_t *__restrict__ parents, const int32_t *__restrict__ children,
-                     int n, void *workspace)
+                     int n, int row_bytes, void *workspace)
 {
     __shared__ Smem sm;
     ptx::launch_dependents();
-    ClusterOps ops(sm);
+    Team<kCluster> team(sm);
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
-    const int nt = ops.threads(), me = ops.thread(), bs = p.block_size;
-    int bad = 0, want = 0;
-    for (int base = 0; base < n; base += nt) {
-        const int i = base + me;
-        int need = 0;
-        if (i < n) {
-            const int r = parents[i], c = children[i];
-            if ((uint32_t)r >= (uint32_t)p.num_rows || (uint32_t)c >= (uint32_t)p.num_rows) {
-                bad |= 2;
-            } else {
-                w.marks[c] = i;
-                const int ctx = p.context_lens[r];
-                if (ctx < 0 || (int64_t)ctx > (int64_t)p.max_blocks * bs || p.context_lens[c] != 0) {
-                    bad |= 2;
-                } else if (ctx % bs != 0) {
-                    need = 1;
-                    const int page = p.tables[(size_t)r * p.max_blocks + ctx / bs];
-                    if ((uint32_t)page >= (uint32_t)p.num_blocks)
-                        bad |= 2;
+    const int nt = team.threads(), me = team.thread(), bs = p.block_size;
+    int4 refs[kIds / 4];
+    plan_begin(team, p, refs);
+    const bool small = !kCluster && n <= kThreads;
+    int32_t *starts = small ? sm.starts : w.starts, *lens = small ? sm.lens : w.lens;
+    if (team.rank() == 0) {
+        int want = 0, pieces = 0;
+        for (int base = 0; base < n; base += kThreads) {
+            const int i = base + (int)threadIdx.x;
+            int need = 0, bad = 0, ctx = 0, bits = 0;
+            if (i < n) {
+                const int r = parents[i], c = children[i];
+                if ((uint32_t)r >= (uint32_t)p.num_rows || (uint32_t)c >= (uint32_t)p.num_rows) {
+                    bad = 2;
+                } else {
+                    ctx = p.context_lens[r];
+                    bad = mark_row(sm, w, p.num_rows, c, i) ? 2 : 0;
+                    if (ctx < 0 || (int64_t)ctx > (int64_t)p.max_blocks * bs || p.context_lens[c] != 0) {
+                        bad = 2;
+                    } else if (ctx % bs != 0) {
+                        need = 1;
+                        bits = (int)(((int64_t)(ctx % bs) * row_bytes + kPieceBytes - 1) / kPieceBytes);
+                        const int page = p.tables[(size_t)r * p.max_blocks + ctx / bs];
+                        if ((uint32_t)page >= (uint32_t)p.num_blocks)
+                            bad |= 2;
+                    }
                 }
+                lens[i] = ctx;
             }
+            if (bad)
+                atomicOr(&sm.bad, bad);
+            int sum;
+            const int at = want + team.scan_cta(need, &sum);
+            if (i < n)
+                starts[i] = at;
+            want += sum;
+            const int first = pieces + team.scan_cta(bits, &sum);
+            if (i < n)
+                w.cums[i] = first;
+            pieces += sum;
         }
-        int sum;
-        const int at = want + ops.scan(need, &sum);
-        if (i < n)
-            w.starts[i] = need ? at : -1;
-        want += sum;
-    }
-    if (!ops.any(bad)) {
-        for (int i = me; i < n; i += nt) {
-            // a child named twice, or a child that is a parent too (its mark, if it is one of this call's)
-            const int r = parents[i], m = w.marks[r];
-            if (w.marks[children[i]] != i || ((uint32_t)m < (uint32_t)n && children[m] == r))
-                bad |= 2;
+        __syncthreads(); // all marks
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const int r = parents[i], c = children[i];
+            if ((uint32_t)r >= (uint32_t)p.num_rows || (uint32_t)c >= (uint32_t)p.num_rows)
+                continue;
+            bool wrong; // a child named twice, or a parent that is a child of this call
+            if (p.num_rows <= kRowBits) {
+                wrong = sm.bits[r >> 5] >> (r & 31) & 1u;
+            } else {
+                const int m = w.marks[r];
+                wrong = marked_twice(w, p.num_rows, c, i) || ((uint32_t)m < (uint32_t)n && children[m] == r);
+            }
+            if (wrong)
+                atomicOr(&sm.bad, 2);
+        }
+        if (threadIdx.x == 0) {
+            sm.want = want;
+            w.head[1] = pieces;
         }
     }
-    bad = ops.any(bad);
-    if (!bad && lowest_free(ops, p, want, w.list) < want)
+    team.sync();
+    const int want = team.of_first(&sm.want);
+    int bad = team.of_first(&sm.bad);
+    int32_t *list = !kCluster && want <= kSmallList ? sm.list : w.list;
+    if (!bad && lowest_free(team, p, want, list, refs) < want)
         bad = 1;
     if (bad) {
         if (me == 0) {
             atomicOr(&g_pool_error, (uint32_t)bad);
-            w.head[0] = 0;
+            w.head[0] = -1;
         }
-        ops.cl.sync();
+        team.sync();
         return;
     }
-    ops.cl.sync(); // the list
+    team.sync(); // the list
     for (int i = me; i < n; i += nt) {
-        const int r = parents[i], ctx = p.context_lens[r], s = w.starts[i];
-        const int src = s >= 0 ? p.tables[(size_t)r * p.max_blocks + ctx / bs] : -1;
-        const int dst = s >= 0 ? w.list[s] : -1;
-        w.copies[i] = make_int4(src, dst, ctx % bs, ctx / bs);
-        if (s >= 0)
+        const int r = parents[i], ctx = lens[i];
+        int src = -1, dst = -1;
+        if (ctx % bs != 0) {
+            src = p.tables[(size_t)r * p.max_blocks + ctx / bs];
+            dst = list[starts[i]];
             p.refs[dst] = 1;
-        p.context_lens[children[i]] = ctx; // a child is no parent, so no reader of this call sees it
+        }
+        w.copies[i] = make_int4(src, dst, ctx % bs, ctx / bs);
+        p.context_lens[children[i]] = ctx; // (lens has the parents': no reader of this call sees it)
     }
     if (me == 0)
         w.head[0] = n;
-    ops.cl.sync();
+    team.sync();
 }
 
 // Pages of all layers: K, V and, for an INT8 cache, the scales.
@@ -358,11 +516,10 @@ struct Planes {
     int32_t layers, page_vecs, row_vecs, pieces, block_size, num_kv_heads;
 };
 
-// Piece `u` (layer, K or V, 16 KB of the page) of copying the first `rows` rows of page src to dst.
-__device__ __forceinline__ void copy_piece(const Planes &q, int u, int src, int dst, int rows)
+// Piece `piece` (16 KB) of the first `rows` rows of page src to page dst, in plane (layer, K or V).
+__device__ __forceinline__ void copy_piece(const Planes &q, int plane, int piece, int src, int dst, int rows)
 {
     constexpr int kU = kPieceBytes / 16 / kMoveThreads;
-    const int piece = u % q.pieces, plane = u / q.pieces;
     const int layer = plane >> 1;
     uint4 *base = (plane & 1 ? q.v : q.k) + (size_t)layer * q.layer_vecs;
     const int first = piece * (kPieceBytes / 16);
@@ -392,14 +549,23 @@ __device__ __forceinline__ void copy_piece(const Planes &q, int u, int src, int 
     }
 }
 
-// The forked rows' tables and counts, and their partly filled pages.
+// The forked rows' tables and counts, and their partly filled pages: all layers of the i-th of
+// all pieces before those of the next.
 __global__ void __launch_bounds__(kMoveThreads)
     pool_fork_copy_kernel(const PoolParams p, const Planes q, const int32_t *__restrict__ parents,
                           const int32_t *__restrict__ children, void *workspace)
 {
     ptx::grid_dependency_wait();
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
-    const int n = w.head[0]; // 0: refused
+    const int n = w.head[0], planes = 2 * q.layers;
+    if (n < 0) // refused
+        return;
+    const int64_t units = (int64_t)w.head[1] * planes;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int g = (int)(u / planes), i = last_at_most(w.cums, n, g);
+        const int4 c = w.copies[i];
+        copy_piece(q, (int)(u % planes), g - w.cums[i], c.x, c.y, c.z);
+    }
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const int4 c = w.copies[i];
         const int32_t *from = p.tables + (size_t)parents[i] * p.max_blocks;
@@ -414,13 +580,6 @@ __global__ void __launch_bounds__(kMoveThreads)
         }
         if (threadIdx.x == 0 && c.y >= 0)
             to[c.w] = c.y;
-    }
-    const int per = 2 * q.layers * q.pieces;
-    const int64_t units = (int64_t)n * per;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int4 c = w.copies[u / per];
-        if (c.y >= 0)
-            copy_piece(q, (int)(u % per), c.x, c.y, c.z);
     }
 }
 
@@ -462,52 +621,90 @@ __global__ void __launch_bounds__(128) pool_free_kernel(const PoolParams p, cons
 // ---------------------------------------------------------------- compact
 
 // remap, the counts under the new ids and the moves (list2[k] -> list[k]).  U used pages: the
-// used ids >= U move, in order, to the free ids < U.  Sources and destinations are disjoint.
+// used ids >= U move, in order, to the free ids < U; sources and destinations are disjoint.  With
+// u(id) the used ids before id, a free id < U is hole id - u(id), and a used id >= U takes
+// hole u(id) - u(U).
+template <bool kCluster>
 __global__ void __launch_bounds__(kThreads)
     pool_compact_kernel(const PoolParams p, int32_t *__restrict__ remap, int32_t *refs_out, void *workspace)
 {
     __shared__ Smem sm;
     ptx::launch_dependents();
-    ClusterOps ops(sm);
+    Team<kCluster> team(sm);
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
-    const int nt = ops.threads(), me = ops.thread(), N = p.num_blocks;
+    const int nt = team.threads(), me = team.thread(), N = p.num_blocks;
+    const int per_round = nt * kIds;
+    int4 refs[kIds / 4];
+    // U and, where one round holds all ids, u(this thread's first id)
     int mine = 0;
-    for (int id = me; id < N; id += nt)
-        mine += p.refs[id] > 0;
-    int U;
-    ops.scan(mine, &U);
-    int holes = 0, high = 0; // free ids below U and used ids from U on, so far
-    for (int base = 0; base < N; base += nt) {
-        const int id = base + me;
-        const bool used = id < N && p.refs[id] > 0;
-        const bool hole = id < U && id < N && !used, move = used && id >= U;
-        int sum; // both ranks in one scan: at most 8192 threads, so 14 bits each
-        const int at = ops.scan((int)hole | (int)move << 16, &sum);
-        if (hole)
-            w.list[holes + (at & 0xffff)] = id;
-        if (move)
-            w.list2[high + (at >> 16)] = id;
-        if (id < N && !move)
-            remap[id] = used ? id : -1;
-        holes += sum & 0xffff;
-        high += sum >> 16;
+    const bool one = N <= per_round;
+    for (int64_t base = 0; base < N; base += per_round) {
+        const int id = (int)min(base + (int64_t)me * kIds, (int64_t)N);
+        load_refs(p, id, refs);
+        mine += min(kIds, N - id) - __popc(free_mask(refs));
     }
-    ops.cl.sync(); // both lists; holes == high
-    for (int k = me; k < high; k += nt) {
+    int U, before = team.scan(mine, &U);
+    // u(U): by the thread that holds id U, in the round that holds it
+    int seen = 0;
+    for (int64_t base = 0; base < N; base += per_round) {
+        const int id = (int)min(base + (int64_t)me * kIds, (int64_t)N);
+        int sum = U;
+        if (!one) {
+            load_refs(p, id, refs);
+            before = seen + team.scan(min(kIds, N - id) - __popc(free_mask(refs)), &sum);
+        }
+        if (id <= U && U < id + kIds && id < N)
+            w.head[2] = before + __popc(~free_mask(refs) & ((1u << (U - id)) - 1u));
+        seen += sum;
+    }
+    if (me == 0 && U == N)
+        w.head[2] = N; // no id U: nothing moves
+    team.sync();
+    const int below = w.head[2];
+    seen = 0;
+    for (int64_t base = 0; base < N; base += per_round) {
+        const int id = (int)min(base + (int64_t)me * kIds, (int64_t)N);
+        int sum;
+        if (!one) {
+            load_refs(p, id, refs);
+            before = seen + team.scan(min(kIds, N - id) - __popc(free_mask(refs)), &sum);
+            seen += sum;
+        }
+        const uint32_t m = free_mask(refs);
+        int u = before;
+        for (int e = 0; e < kIds && id + e < N; ++e) {
+            const bool is_free = m >> e & 1u;
+            const int x = id + e;
+            if (is_free) {
+                if (x < U)
+                    w.list[x - u] = x;
+                remap[x] = -1;
+            } else {
+                if (x >= U)
+                    w.list2[u - below] = x;
+                else
+                    remap[x] = x;
+                ++u;
+            }
+        }
+    }
+    const int moves = U - below;
+    if (me == 0)
+        w.head[0] = moves;
+    team.sync(); // both lists
+    for (int k = me; k < moves; k += nt) {
         const int src = w.list2[k], dst = w.list[k];
         remap[src] = dst;
         refs_out[dst] = p.refs[src];
     }
-    if (me == 0)
-        w.head[0] = high;
-    ops.cl.sync(); // the sources' counts are read
+    team.sync(); // the sources' counts are read
     for (int id = me; id < N; id += nt) {
         if (id >= U)
             refs_out[id] = 0;
         else if (refs_out != p.refs && p.refs[id] > 0)
             refs_out[id] = p.refs[id];
     }
-    ops.cl.sync();
+    team.sync();
 }
 
 __global__ void __launch_bounds__(kMoveThreads)
@@ -532,8 +729,8 @@ __global__ void __launch_bounds__(kMoveThreads)
     const int per = 2 * q.layers * q.pieces;
     const int64_t units = (int64_t)w.head[0] * per;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int k = (int)(u / per);
-        copy_piece(q, (int)(u % per), w.list2[k], w.list[k], q.block_size);
+        const int k = (int)(u / per), v = (int)(u % per);
+        copy_piece(q, v / q.pieces, v % q.pieces, w.list2[k], w.list[k], q.block_size);
     }
 }
 
@@ -592,22 +789,32 @@ int launch_ex(const char *what, void (*kernel)(P...), unsigned grid, unsigned bl
     return PA_OK;
 }
 
-// CTAs of the planning cluster.
-unsigned plan_ctas(int64_t work) { return work <= 4 * kThreads ? 1u : 8u; }
+// One CTA looks through 16384 ids in a round of about 1 us; a cluster costs about 3 us more to
+// start and meet.
+bool plan_by_cluster(const PoolArgs &a) { return a.dims.num_blocks > 3 * kThreads * kIds; }
 
 } // namespace
 
 size_t pool_workspace_bytes(int num_rows, int num_blocks)
 {
-    return align_up((16 + 6 * (size_t)num_rows + 2 * (size_t)num_blocks) * 4, 256);
+    return align_up((16 + kWsRowInts * (size_t)num_rows + kWsBlockInts * (size_t)num_blocks) * 4, 256);
 }
 
 int launch_pool_append(const PoolArgs &a, const int32_t *rows, const int32_t *cu, int n, int32_t *slots, int num_tokens,
                        void *stream)
 {
-    const unsigned c = plan_ctas(std::max<int64_t>(a.dims.num_blocks, std::max(num_tokens, n)));
-    return launch_ex("pool append", pool_append_kernel, c, kThreads, c, false, stream, params_of(a), rows, cu, n, slots,
-                     num_tokens, a.workspace);
+    // a planning CTA writes a few thousand slots in the time that another launch takes
+    const bool many = num_tokens > 4 * kThreads, cluster = plan_by_cluster(a);
+    auto kernel = many ? (cluster ? pool_append_kernel<true, false> : pool_append_kernel<false, false>)
+                       : (cluster ? pool_append_kernel<true, true> : pool_append_kernel<false, true>);
+    const unsigned c = cluster ? kClusterCtas : 1;
+    if (int rc = launch_ex("pool append", kernel, c, kThreads, c, false, stream, params_of(a), rows, cu, n, slots,
+                           num_tokens, a.workspace))
+        return rc;
+    if (!many)
+        return PA_OK;
+    return launch_ex("pool slots", pool_slots_kernel, (unsigned)(((int64_t)num_tokens + 1023) / 1024), 256, 1, true, stream,
+                     params_of(a), rows, cu, n, slots, num_tokens, a.workspace);
 }
 
 int launch_pool_fork(const PoolArgs &a, const int32_t *parents, const int32_t *children, int n, void *stream)
@@ -615,11 +822,12 @@ int launch_pool_fork(const PoolArgs &a, const int32_t *parents, const int32_t *c
     int sms = 0;
     if (int rc = sm_count(&sms))
         return rc;
-    const unsigned c = plan_ctas(std::max(a.dims.num_blocks, n));
-    if (int rc = launch_ex("pool fork", pool_fork_kernel, c, kThreads, c, false, stream, params_of(a), parents, children,
-                           n, a.workspace))
-        return rc;
     const Planes q = planes_of(a);
+    const bool cluster = plan_by_cluster(a);
+    const unsigned c = cluster ? kClusterCtas : 1;
+    if (int rc = launch_ex("pool fork", cluster ? pool_fork_kernel<true> : pool_fork_kernel<false>, c, kThreads, c, false,
+                           stream, params_of(a), parents, children, n, (int)(q.row_vecs * 16), a.workspace))
+        return rc;
     const int64_t units = std::max<int64_t>(n, (int64_t)n * 2 * q.layers * q.pieces);
     return launch_ex("pool fork copy", pool_fork_copy_kernel, (unsigned)std::min<int64_t>(units, (int64_t)sms * 8),
                      kMoveThreads, 1, true, stream, params_of(a), q, parents, children, a.workspace);
@@ -639,9 +847,10 @@ int launch_pool_compact(const PoolArgs &a, int32_t *remap, int32_t *tables_out, 
     int sms = 0;
     if (int rc = sm_count(&sms))
         return rc;
-    const unsigned c = plan_ctas(a.dims.num_blocks);
-    if (int rc = launch_ex("pool compact", pool_compact_kernel, c, kThreads, c, false, stream, params_of(a), remap,
-                           refs_out, a.workspace))
+    const bool cluster = plan_by_cluster(a);
+    const unsigned c = cluster ? kClusterCtas : 1;
+    if (int rc = launch_ex("pool compact", cluster ? pool_compact_kernel<true> : pool_compact_kernel<false>, c, kThreads,
+                           c, false, stream, params_of(a), remap, refs_out, a.workspace))
         return rc;
     const Planes q = planes_of(a);
     const int64_t cells = (int64_t)a.pool.num_rows * a.pool.max_blocks;

@@ -224,6 +224,55 @@ def test_large_pools(nb, bs, n, most):
     m.check()
 
 
+@pytest.mark.parametrize("nb", [900, 60000])
+def test_very_many_rows(nb):
+    """More rows than the bitmap of a call's rows holds."""
+    rows = 70000
+    dims, pool, m = both(layers=1, nb=nb, bs=16, hkv=1, d=64, rows=rows, width=3, seed=4)
+    some = [69999, 0, 65536, 65535, 40000]
+    assert append(dims, pool, m, some, [5, 16, 30, 1, 0])
+    for rows_, counts in (([1, 69999, 1], [1, 1, 1]), ([65536 + 7, 9, 65536 + 7], [1, 1, 1])):
+        assert not append(dims, pool, m, rows_, counts)
+        assert pa.pa_read_device_error() == MALFORMED
+    for parents, children in (([0, 69999], [68000, 68000]), ([69999, 5], [5, 68000]), ([69998], [69999])):
+        pa.pa_pool_fork(dims, pool, i32(parents), i32(children))
+        assert not m.fork(parents, children)
+        assert pa.pa_read_device_error() == MALFORMED
+    pa.pa_pool_fork(dims, pool, i32([69999, 65536, 65536]), i32([69998, 1, 66000]))
+    assert m.fork([69999, 65536, 65536], [69998, 1, 66000])
+    pa.pa_pool_free(dims, pool, i32([0, 65536]))
+    m.free([0, 65536])
+    remap = torch.empty(nb, dtype=torch.int32, device="cuda")
+    pa.pa_pool_compact(dims, pool, remap)
+    assert np.array_equal(remap.cpu().numpy(), m.compact())
+    assert_same(pool, m)
+
+
+def test_fragmented_pools():
+    """Used and free pages in random places, over one and over several rounds of ids."""
+    for nb, used in ((1, 1), (15, 7), (17, 16), (4097, 2000), (16384, 16000), (50001, 20000), (300007, 150000)):
+        dims, pool, m = both(layers=1, nb=nb, bs=16, hkv=1, d=64, rows=3, width=max(used // 2 + 1, 6000), seed=5)
+        rng = np.random.default_rng(nb)
+        ids = rng.permutation(nb)[:used].astype(np.int32)
+        half = used // 2
+        for r, part in ((0, ids[:half]), (2, ids[half:])):
+            m.tables[r, :len(part)], m.ctx[r] = part, 16 * len(part)
+        m.refs[ids] = 1
+        m.check()
+        pool.block_tables.copy_(i32(m.tables)), pool.context_lens.copy_(i32(m.ctx)), pool.ref_counts.copy_(i32(m.refs))
+        n = min(nb - used, 5000)
+        assert append(dims, pool, m, [1], [16 * n])     # the lowest free ids, wherever they are
+        assert_same(pool, m, f"append {nb}")
+        pa.pa_pool_free(dims, pool, i32([0]))
+        m.free([0])
+        remap = torch.empty(nb, dtype=torch.int32, device="cuda")
+        tables, refs = torch.full_like(pool.block_tables, 99), torch.full_like(pool.ref_counts, 99)
+        pa.pa_pool_compact(dims, pool, remap, tables, refs)
+        assert np.array_equal(remap.cpu().numpy(), m.compact())
+        pool.block_tables.copy_(tables), pool.ref_counts.copy_(refs)
+        assert_same(pool, m, f"compact {nb}")
+
+
 def test_full_and_empty_pools():
     dims, pool, m = both(nb=9, rows=4, width=9)
     remap = torch.empty(9, dtype=torch.int32, device="cuda")

@@ -59,7 +59,7 @@ def test_pool_calls_reject_bad_args_without_touching_the_gpu():
     dims = pa.make_dims(32, 16, 4, 2, 64)      # a layer's K: 32 * 16 * 2 * 64 * 2 = 131072 bytes
     L, ref = pa.lib(), ctypes.byref
     n = ctypes.c_uint64(0)
-    assert L.pa_pool_workspace(ref(dims), ref(_pool()), ref(n)) == pa.PA_OK and n.value >= 4 * (6 * 4 + 2 * 32)
+    assert L.pa_pool_workspace(ref(dims), ref(_pool()), ref(n)) == pa.PA_OK and n.value >= 4 * (8 * 4 + 2 * 32)
     assert L.pa_pool_workspace(ref(dims), None, ref(n)) == pa.PA_ERR_INVALID_ARG
     ws = n.value
     ok = _pool(layer_stride=131072)
