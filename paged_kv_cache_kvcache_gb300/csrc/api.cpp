@@ -500,6 +500,7 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
     a->num_ctas = meta->num_ctas;
     a->rows_per_tile = meta->rows_per_tile;
     a->max_blocks_per_seq = meta->max_blocks_per_seq;
+    a->max_parts = meta->max_parts;
     a->merge = meta->merge != 0;
     return PA_OK;
 }

@@ -37,7 +37,7 @@
 // 65504) and the queries.  The products then run as on a bf16 cache, with fp16 weights.  (Exact
 // codes with the scales in the softmax took 3.4 us per 128 keys and pair instead of 1.6: 64 more
 // 16-byte loads per row; converting in shared memory took 4.2.)  Parts of single sequences go to
-// the INT8 decode kernel, in a launch that may run beside this one.
+// the INT8 decode kernel, in a launch that may run beside the products.
 //
 // Every hand-off waits with a time limit; a wait that runs out sets an error bit and the
 // kernel returns.  A block id outside the pool reads as zeros and sets an error bit.
@@ -857,33 +857,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // out[b][h] = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over the parts of sequence b: none
-// (empty context) writes zeros, one was written by its work item.  One warp per (sequence,
-// head), D/32 values per lane, kBatch parts' loads in flight, summed in part order.
-template <int D>
-__global__ void __launch_bounds__(128) shared_combine_kernel(const float *__restrict__ part_o,
-                                                             const float *__restrict__ part_lse,
-                                                             const int2 *__restrict__ seq_parts,
-                                                             __nv_bfloat16 *__restrict__ out, int num_heads)
+// (empty context) writes zeros, one was written by its work item.  D/32 values per lane, kBatch
+// parts' loads in flight; a (sequence, head)'s parts are shared out in order to kSplit warps (of
+// the four or eight of a block), whose sums meet in shared memory in warp order.  Bound by the
+// latency of the loads: 65 parts in one warp took 18 us, in eight 3.
+template <int D, int kSplit>
+__global__ void __launch_bounds__(kSplit == 8 ? 256 : 128)
+    shared_combine_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse,
+                          const int2 *__restrict__ seq_parts, __nv_bfloat16 *__restrict__ out, int num_heads)
 {
     constexpr int E = D / 32;
     constexpr int kBatch = 8;
-    const int b = blockIdx.x;
-    const int h = blockIdx.y * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    constexpr int kHeads = kSplit == 1 ? 4 : 1; // heads per block
+    const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = blockIdx.y * kHeads + (kSplit == 1 ? warp : 0);
     const int2 sp = __ldg(seq_parts + b); // the plan's, written long before this launch's predecessor
     ptx::grid_dependency_wait();          // the parts are complete and visible
-    const int n = sp.y;
-    if (n == 1 || h >= num_heads)
+    if (sp.y == 1 || h >= num_heads)
         return;
+    const int per = kSplit == 1 ? sp.y : (sp.y + kSplit - 1) / kSplit;
+    const int from = kSplit == 1 ? 0 : min(warp * per, sp.y), n = min(sp.y - from, per);
     const float *lse = part_lse + (size_t)sp.x * num_heads + h;
-    const float *po = part_o + ((size_t)sp.x * num_heads + h) * D + lane * E;
+    const float *po = part_o + (((size_t)sp.x + from) * num_heads + h) * D + lane * E;
     const size_t o_stride = (size_t)num_heads * D;
     float M = -INFINITY;
-    for (int s = lane; s < n; s += 32)
+    for (int s = lane; s < sp.y; s += 32)
         M = fmaxf(M, lse[(size_t)s * num_heads]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    lse += (size_t)from * num_heads;
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -911,6 +914,28 @@ __global__ void __launch_bounds__(128) shared_combine_kernel(const float *__rest
                     acc[e] += w * o[i][e];
             }
     }
+    if constexpr (kSplit > 1) {
+        __shared__ float sums[kSplit][D + 1]; // a warp's D sums, then its weight
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            sums[warp][lane * E + e] = acc[e];
+        if (lane == 0)
+            sums[warp][D] = W;
+        __syncthreads();
+        if (warp != 0)
+            return;
+        W = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = 0.f;
+#pragma unroll
+        for (int s = 0; s < kSplit; ++s) {
+            W += sums[s][D];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] += sums[s][lane * E + e];
+        }
+    }
     const float inv = W > 0.f ? 1.f / W : 0.f;
     uint32_t x[E / 2];
 #pragma unroll
@@ -929,6 +954,63 @@ int encode_cache(CUtensorMap *m, const void *cache, int num_kv_heads, uint64_t r
 {
     return encode_tmap_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache, D, num_kv_heads, rows, (uint64_t)D * 2,
                           (uint64_t)num_kv_heads * D * 2, 64, 1, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+
+// INT8: the scratch copies for the shared parts.
+int launch_codes(const SharedArgs &a, cudaStream_t stream)
+{
+    const pa_dims &d = a.dims;
+    const size_t half = (size_t)a.num_scratch_tiles * 128 * d.num_kv_heads * d.head_dim * 2;
+    CodesParams c{};
+    c.tiles = reinterpret_cast<const int4 *>(a.scratch_tiles);
+    c.block_tables = a.block_tables;
+    c.k_codes = static_cast<const uint4 *>(a.k_cache);
+    c.v_codes = static_cast<const uint4 *>(a.v_cache);
+    c.k_scale = static_cast<const uint16_t *>(a.k_scale);
+    c.v_scale = static_cast<const uint16_t *>(a.v_scale);
+    c.k_out = static_cast<uint4 *>(a.scratch);
+    c.v_out = reinterpret_cast<uint4 *>(static_cast<char *>(a.scratch) + half);
+    c.q = static_cast<const uint4 *>(a.q);
+    c.q_out = reinterpret_cast<uint4 *>(static_cast<char *>(a.scratch) + 2 * half);
+    c.block_size = d.block_size;
+    c.max_blocks = a.max_blocks_per_seq;
+    c.num_blocks = d.num_blocks;
+    c.num_kv_heads = d.num_kv_heads;
+    c.head_vecs = d.head_dim / 16;
+    c.key_vecs = d.num_kv_heads * c.head_vecs;
+    c.tile_ctas = a.num_scratch_tiles * (128 / kCodesKeys);
+    c.q_vecs = (int64_t)a.num_seqs * d.num_heads * d.head_dim / 8;
+    shared_codes_kernel<<<(unsigned)(c.tile_ctas + (c.q_vecs + 255) / 256), 256, 0, stream>>>(c);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return fail(PA_ERR_CUDA, "shared decode code conversion launch: %s", cudaGetErrorString(e));
+    return PA_OK;
+}
+
+// INT8: the parts of single sequences; may run beside the shared parts' products.  (Beside the
+// conversion instead, with the products after both, 64 x 16384 took 75 us, not 50: these parts
+// are long and few, and the products waited for them.)
+int launch_singles(const SharedArgs &a, cudaStream_t stream)
+{
+    DecodeArgs s{};
+    s.dims = a.dims;
+    s.q = a.q;
+    s.k_cache = a.k_cache;
+    s.v_cache = a.v_cache;
+    s.k_scale = a.k_scale;
+    s.v_scale = a.v_scale;
+    s.block_tables = a.block_tables;
+    s.items = a.single_items;
+    s.out = a.out;
+    s.part_o = a.part_o;
+    s.part_lse = a.part_lse;
+    s.scale = a.scale;
+    s.num_seqs = a.num_seqs;
+    s.num_items = a.num_single_items;
+    s.max_blocks_per_seq = a.max_blocks_per_seq;
+    s.table_rows = a.table_rows;
+    s.beside = a.num_items > 0;
+    return launch_decode_int8(s, stream);
 }
 
 template <int D, bool kInt8>
@@ -952,6 +1034,9 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     const pa_dims &d = a.dims;
     const int G = d.num_heads / d.num_kv_heads;
     if (a.num_items > 0) {
+        if (kInt8)
+            if (int rc = launch_codes(a, stream))
+                return rc;
         const uint32_t box_rows = !kInt8 && d.block_size < kBoxRows ? (uint32_t)d.block_size : (uint32_t)kBoxRows;
         // INT8: the products read the scratch cache
         const size_t half = (size_t)a.num_scratch_tiles * 128 * d.num_kv_heads * D * 2;
@@ -972,32 +1057,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
             (rc = encode_cache<D>(&tv, v_cache, d.num_kv_heads, rows, box_rows, "v_cache")) != PA_OK)
             return rc;
         ShParams p{};
-        if constexpr (kInt8) {
-            CodesParams c{};
-            c.tiles = reinterpret_cast<const int4 *>(a.scratch_tiles);
-            c.block_tables = a.block_tables;
-            c.k_codes = static_cast<const uint4 *>(a.k_cache);
-            c.v_codes = static_cast<const uint4 *>(a.v_cache);
-            c.k_scale = static_cast<const uint16_t *>(a.k_scale);
-            c.v_scale = static_cast<const uint16_t *>(a.v_scale);
-            c.k_out = static_cast<uint4 *>(a.scratch);
-            c.v_out = reinterpret_cast<uint4 *>(static_cast<char *>(a.scratch) + half);
-            c.q = static_cast<const uint4 *>(a.q);
-            c.q_out = reinterpret_cast<uint4 *>(static_cast<char *>(a.scratch) + 2 * half);
-            c.block_size = d.block_size;
-            c.max_blocks = a.max_blocks_per_seq;
-            c.num_blocks = d.num_blocks;
-            c.num_kv_heads = d.num_kv_heads;
-            c.key_vecs = d.num_kv_heads * D / 16;
-            c.head_vecs = D / 16;
-            c.tile_ctas = a.num_scratch_tiles * (128 / kCodesKeys);
-            c.q_vecs = (int64_t)a.num_seqs * d.num_heads * D / 8;
-            shared_codes_kernel<<<(unsigned)(c.tile_ctas + (c.q_vecs + 255) / 256), 256, 0, stream>>>(c);
-            const cudaError_t e = cudaGetLastError();
-            if (e != cudaSuccess)
-                return fail(PA_ERR_CUDA, "shared decode code conversion launch: %s", cudaGetErrorString(e));
-            p.scratch_rows = a.num_scratch_tiles * 128;
-        }
+        p.scratch_rows = kInt8 ? a.num_scratch_tiles * 128 : 0;
         p.items = reinterpret_cast<const int4 *>(a.items);
         p.cta_items = reinterpret_cast<const int4 *>(a.cta_items);
         p.seq_parts = reinterpret_cast<const int2 *>(a.seq_parts);
@@ -1018,29 +1078,9 @@ int launch(const SharedArgs &a, cudaStream_t stream)
         if (e != cudaSuccess)
             return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
     }
-    if (kInt8 && a.num_single_items > 0) {
-        // the parts of single sequences; may run beside the shared parts
-        DecodeArgs s{};
-        s.dims = a.dims;
-        s.q = a.q;
-        s.k_cache = a.k_cache;
-        s.v_cache = a.v_cache;
-        s.k_scale = a.k_scale;
-        s.v_scale = a.v_scale;
-        s.block_tables = a.block_tables;
-        s.items = a.single_items;
-        s.out = a.out;
-        s.part_o = a.part_o;
-        s.part_lse = a.part_lse;
-        s.scale = a.scale;
-        s.num_seqs = a.num_seqs;
-        s.num_items = a.num_single_items;
-        s.max_blocks_per_seq = a.max_blocks_per_seq;
-        s.table_rows = a.table_rows;
-        s.beside = a.num_items > 0;
-        if (int rc = launch_decode_int8(s, stream))
+    if (kInt8 && a.num_single_items > 0)
+        if (int rc = launch_singles(a, stream))
             return rc;
-    }
     if (!a.merge)
         return PA_OK;
     // Programmatic launch: the merge's blocks are set up while the parts still run and wait
@@ -1048,16 +1088,21 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     // cooperative launch whose CTAs met before merging took 3 us longer on a batch of 8 x 300
     // tokens and 15 us longer on 256 x 33300.)
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)a.num_seqs, (unsigned)((d.num_heads + 3) / 4));
-    cfg.blockDim = dim3(128);
+    // several warps per (sequence, head) where there are few of them: with 1792 (9 parts each) four made
+    // the merge 8.8 us, not 6.1; with 224 (65 parts), eight made a call 16.7 us, not 28
+    const int64_t merges = (int64_t)a.num_seqs * d.num_heads;
+    const int split = a.max_parts <= 8 || merges > 1024 ? 1 : a.max_parts <= 32 ? 4 : 8;
+    cfg.gridDim = dim3((unsigned)a.num_seqs, (unsigned)(split == 1 ? (d.num_heads + 3) / 4 : d.num_heads));
+    cfg.blockDim = dim3(split == 8 ? 256 : 128);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = a.num_items + (kInt8 ? a.num_single_items : 0) > 0 ? 1 : 0;
+    auto combine = split == 1 ? shared_combine_kernel<D, 1> : split == 4 ? shared_combine_kernel<D, 4> : shared_combine_kernel<D, 8>;
     const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, shared_combine_kernel<D>, (const float *)a.part_o, (const float *)a.part_lse,
+        cudaLaunchKernelEx(&cfg, combine, (const float *)a.part_o, (const float *)a.part_lse,
                            reinterpret_cast<const int2 *>(a.seq_parts), static_cast<__nv_bfloat16 *>(a.out),
                            (int)d.num_heads);
     if (e != cudaSuccess) {

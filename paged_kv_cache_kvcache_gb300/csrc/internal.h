@@ -215,6 +215,7 @@ struct SharedArgs {
     int32_t num_ctas;
     int32_t rows_per_tile;
     int32_t max_blocks_per_seq;
+    int32_t max_parts;
     bool merge; // some sequence has two or more parts, or none
 };
 int launch_decode_shared(const SharedArgs &a, void *stream);

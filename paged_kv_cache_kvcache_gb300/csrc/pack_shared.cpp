@@ -23,7 +23,7 @@ constexpr int32_t kTile = kPrefillKeyTile;
 // both lanes of its CTA and is bound by the tensor core; a single occupies one lane, and two
 // lanes' loads share the SM's part of the HBM rate.  An item adds its query load and its
 // output.  The merge reads and writes every partial once.
-constexpr float kPairStep = 1.62f, kSingleStep = 2.8f, kPairItem = 2.5f, kSingleItem = 1.5f, kMergeBytesPerUs = 5.0e6f;
+constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kPairItem = 2.5f, kSingleItem = 1.0f, kMergeBytesPerUs = 8.0e6f;
 
 struct Run { // consecutive sequences of a group that share `shared` tokens
     int32_t s0, n, shared;
@@ -197,7 +197,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         float best = INFINITY;
         const float slot_us = (float)d.num_heads * d.head_dim * 8.f / kMergeBytesPerUs;
         for (int32_t c : kPer) {
-            float work = 0.f, pair = 0.f, single = 0.f, slots = 0.f; // lane time, longest items, partial slots
+            float pair_work = 0.f, single_work = 0.f, pair = 0.f, single = 0.f, slots = 0.f; // lane time, longest, slots
             int64_t pairs = 0, singles = 0;
             for (size_t i = 0; i < ranges.size(); ++i) {
                 const Range &x = ranges[i];
@@ -206,17 +206,18 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
                     pair = std::max(pair, item_cost(len, true));
                 if (x.units_single)
                     single = std::max(single, item_cost(len, false));
-                work += 2 * x.units_pair * (x.tiles * kPairStep + s * kPairItem) +
-                        x.units_single * (x.tiles * kSingleStep + s * kSingleItem);
+                pair_work += 2 * x.units_pair * (x.tiles * kPairStep + s * kPairItem);
+                single_work += x.units_single * (x.tiles * kSingleStep + s * kSingleItem);
                 pairs += (int64_t)s * x.units_pair;
                 singles += (int64_t)s * x.units_single;
                 slots += (float)s * range_seqs[i];
             }
-            // pairs are dealt out first, in rounds over the CTAs; singles fill up what the rounds leave
-            // uneven, and the lanes then end within about half of a single of one another
+            // pairs are dealt out first, in rounds over the CTAs; singles, longest first, fill up what the
+            // rounds leave uneven, and the lanes then end within about half a mean single of one another
             float t = std::max((float)((pairs + sms - 1) / sms) * pair, single);
             if (2 * pairs + singles > 2 * sms)
-                t = std::max(t, work / (2 * sms) + 0.5f * single);
+                t = std::max(t, (pair_work + single_work) / (2 * sms) +
+                                    (singles ? 0.5f * single_work / (float)singles : 0.f));
             t += slots * slot_us;
             if (t < best) {
                 best = t;

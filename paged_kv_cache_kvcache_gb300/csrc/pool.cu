@@ -516,36 +516,70 @@ struct Planes {
     int32_t layers, page_vecs, row_vecs, pieces, block_size, num_kv_heads;
 };
 
-// Piece `piece` (16 KB) of the first `rows` rows of page src to page dst, in plane (layer, K or V).
-__device__ __forceinline__ void copy_piece(const Planes &q, int plane, int piece, int src, int dst, int rows)
+// One piece of a copy: (plane = layer, K or V), 16 KB of the first `rows` rows of page src.
+struct Piece {
+    const uint4 *from;
+    uint4 *to;
+    int n; // 16-byte vectors
+    int plane, src, dst, scale_rows; // scale_rows: the page's first piece brings that many rows' scales
+};
+__device__ __forceinline__ Piece piece_of(const Planes &q, int plane, int piece, int src, int dst, int rows)
+{
+    constexpr int kVecs = kPieceBytes / 16;
+    uint4 *base = (plane & 1 ? q.v : q.k) + (size_t)(plane >> 1) * q.layer_vecs + (size_t)piece * kVecs;
+    return {base + (size_t)src * q.page_vecs, base + (size_t)dst * q.page_vecs,
+            min(kVecs, rows * q.row_vecs - piece * kVecs), plane, src, dst, piece == 0 ? rows : 0};
+}
+
+// Copies pieces u = blockIdx.x, + gridDim.x, ... < units, of(u) giving each; a piece is loaded
+// before the one before it is stored, so that a CTA always has loads in flight.
+template <typename F>
+__device__ __forceinline__ void copy_pieces(const Planes &q, int64_t units, F of)
 {
     constexpr int kU = kPieceBytes / 16 / kMoveThreads;
-    const int layer = plane >> 1;
-    uint4 *base = (plane & 1 ? q.v : q.k) + (size_t)layer * q.layer_vecs;
-    const int first = piece * (kPieceBytes / 16);
-    const int last = min(first + kPieceBytes / 16, rows * q.row_vecs);
-    const uint4 *from = base + (size_t)src * q.page_vecs;
-    uint4 *to = base + (size_t)dst * q.page_vecs;
-    uint4 x[kU];
+    auto load = [&](const Piece &c, uint4 (&x)[kU]) {
 #pragma unroll
-    for (int e = 0; e < kU; ++e) {
-        const int i = first + e * kMoveThreads + (int)threadIdx.x;
-        if (i < last)
-            x[e] = __ldcs(from + i);
-    }
-#pragma unroll
-    for (int e = 0; e < kU; ++e) {
-        const int i = first + e * kMoveThreads + (int)threadIdx.x;
-        if (i < last)
-            __stcs(to + i, x[e]);
-    }
-    if (q.ks && piece == 0) { // each KV head's run of `rows` scales
-        uint16_t *sc = (plane & 1 ? q.vs : q.ks) + (size_t)layer * q.scale_layer;
-        const size_t page = (size_t)q.num_kv_heads * q.block_size;
-        for (int i = threadIdx.x; i < rows * q.num_kv_heads; i += kMoveThreads) {
-            const size_t at = (size_t)(i / rows) * q.block_size + i % rows;
-            sc[dst * page + at] = sc[src * page + at];
+        for (int e = 0; e < kU; ++e) {
+            const int i = e * kMoveThreads + (int)threadIdx.x;
+            if (i < c.n)
+                x[e] = __ldcs(c.from + i);
         }
+    };
+    int64_t u = blockIdx.x;
+    if (u >= units)
+        return;
+    Piece c = of(u);
+    uint4 x[kU];
+    load(c, x);
+    for (;;) {
+        u += gridDim.x;
+        const bool more = u < units;
+        Piece d = c;
+        uint4 y[kU];
+        if (more) {
+            d = of(u);
+            load(d, y);
+        }
+#pragma unroll
+        for (int e = 0; e < kU; ++e) {
+            const int i = e * kMoveThreads + (int)threadIdx.x;
+            if (i < c.n)
+                __stcs(c.to + i, x[e]);
+        }
+        if (q.ks && c.scale_rows > 0) { // each KV head's run of scales
+            uint16_t *sc = (c.plane & 1 ? q.vs : q.ks) + (size_t)(c.plane >> 1) * q.scale_layer;
+            const size_t page = (size_t)q.num_kv_heads * q.block_size;
+            for (int i = threadIdx.x; i < c.scale_rows * q.num_kv_heads; i += kMoveThreads) {
+                const size_t at = (size_t)(i / c.scale_rows) * q.block_size + i % c.scale_rows;
+                sc[c.dst * page + at] = sc[c.src * page + at];
+            }
+        }
+        if (!more)
+            return;
+        c = d;
+#pragma unroll
+        for (int e = 0; e < kU; ++e)
+            x[e] = y[e];
     }
 }
 
@@ -561,11 +595,11 @@ __global__ void __launch_bounds__(kMoveThreads)
     if (n < 0) // refused
         return;
     const int64_t units = (int64_t)w.head[1] * planes;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    copy_pieces(q, units, [&](int64_t u) {
         const int g = (int)(u / planes), i = last_at_most(w.cums, n, g);
         const int4 c = w.copies[i];
-        copy_piece(q, (int)(u % planes), g - w.cums[i], c.x, c.y, c.z);
-    }
+        return piece_of(q, (int)(u % planes), g - w.cums[i], c.x, c.y, c.z);
+    });
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const int4 c = w.copies[i];
         const int32_t *from = p.tables + (size_t)parents[i] * p.max_blocks;
@@ -728,10 +762,10 @@ __global__ void __launch_bounds__(kMoveThreads)
     }
     const int per = 2 * q.layers * q.pieces;
     const int64_t units = (int64_t)w.head[0] * per;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    copy_pieces(q, units, [&](int64_t u) {
         const int k = (int)(u / per), v = (int)(u % per);
-        copy_piece(q, v / q.pieces, v % q.pieces, w.list2[k], w.list[k], q.block_size);
-    }
+        return piece_of(q, v / q.pieces, v % q.pieces, w.list2[k], w.list[k], q.block_size);
+    });
 }
 
 // ---------------------------------------------------------------- launches
@@ -780,7 +814,7 @@ int launch_ex(const char *what, void (*kernel)(P...), unsigned grid, unsigned bl
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     }
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = dependent || cluster > 1 ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e != cudaSuccess) {
         cudaGetLastError();

@@ -178,11 +178,12 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
-def _int32(t, what: str, count: Optional[int] = None) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_contiguous() or \
+def _int32(t, what: str, count: Optional[int] = None) -> int:
+    """Address of a contiguous int32 tensor (of `count` values)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous() or \
             (count is not None and t.numel() != count):
         raise ValueError(f"{what} must be a contiguous int32 tensor" + ("" if count is None else f" of {count}"))
-    return t
+    return t.data_ptr()
 
 
 def make_dims(num_blocks: int, block_size: int, num_heads: int, num_kv_heads: int, head_dim: int) -> pa_dims:
@@ -433,10 +434,10 @@ def _shared_tables(plan: SharedPlan, block_tables) -> int:
         if plan.call_tables is None:
             raise ValueError("the plan was packed for device tables: pass block_tables")
         return plan.call_tables
-    _int32(block_tables, "block_tables")
+    at = _int32(block_tables, "block_tables")
     if block_tables.dim() != 2 or block_tables.shape[1] != plan.meta.max_blocks_per_seq:
         raise ValueError(f"block_tables must be [rows, {plan.meta.max_blocks_per_seq}]")
-    return block_tables.data_ptr()
+    return at
 
 
 def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale: float, out, workspace=None,
@@ -446,7 +447,7 @@ def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale
     ``block_tables``: the device table a plan without block lists was packed for.
     """
     bt = _shared_tables(plan, block_tables)
-    _check(lib().pa_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), bt, scale, _ptr(out),
+    _check((_lib or lib()).pa_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), bt, scale, _ptr(out),
                                   plan.call_ref, *plan.call_arrays, _ptr(workspace), _nbytes(workspace),
                                   _stream(stream)), "pa_decode_shared")
 
@@ -455,7 +456,7 @@ def pa_decode_shared_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, 
                           workspace=None, block_tables=None, stream=None):
     """pa_decode_shared over an INT8 cache (same plan and workspace)."""
     bt = _shared_tables(plan, block_tables)
-    _check(lib().pa_decode_shared_int8(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+    _check((_lib or lib()).pa_decode_shared_int8(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
                                        _ptr(v_scale), bt, scale, _ptr(out), plan.call_ref, *plan.call_arrays,
                                        *plan.call_singles, _ptr(workspace), _nbytes(workspace), _stream(stream)),
            "pa_decode_shared_int8")
@@ -503,7 +504,7 @@ class PagePool:
         n = ctypes.c_uint64(0)
         _check(lib().pa_pool_workspace(ctypes.byref(dims), self.ref, ctypes.byref(n)), "pa_pool_workspace")
         self.workspace = torch.empty(n.value, dtype=torch.uint8, device=block_tables.device)
-        self.workspace_bytes = n.value
+        self.ws = (self.workspace.data_ptr(), n.value)
 
     @staticmethod
     def _layers(x, shape, int8):
@@ -525,25 +526,23 @@ def page_pool(dims: pa_dims, k_cache, v_cache, num_rows: int, max_blocks: int, k
 
 def pa_pool_append(dims: pa_dims, pool: PagePool, rows, cu_new, slot_mapping, stream=None):
     """Give row rows[i] its next cu_new[i+1] - cu_new[i] tokens; their slots go to slot_mapping."""
-    n = int(rows.numel())
-    _int32(rows, "rows"), _int32(cu_new, "cu_new", n + 1), _int32(slot_mapping, "slot_mapping")
-    _check(lib().pa_pool_append(ctypes.byref(dims), pool.ref, _ptr(rows), _ptr(cu_new), n, _ptr(slot_mapping),
-                                int(slot_mapping.numel()), _ptr(pool.workspace), pool.workspace_bytes, _stream(stream)),
+    n, tokens = rows.numel(), slot_mapping.numel()
+    args = (_int32(rows, "rows"), _int32(cu_new, "cu_new", n + 1), n, _int32(slot_mapping, "slot_mapping"), tokens)
+    _check((_lib or lib()).pa_pool_append(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
            "pa_pool_append")
 
 
 def pa_pool_fork(dims: pa_dims, pool: PagePool, parents, children, stream=None):
     """Row children[i] shares row parents[i]'s full pages and gets a copy of its partly filled one."""
-    n = int(children.numel())
-    _int32(parents, "parents", n), _int32(children, "children")
-    _check(lib().pa_pool_fork(ctypes.byref(dims), pool.ref, _ptr(parents), _ptr(children), n, _ptr(pool.workspace),
-                              pool.workspace_bytes, _stream(stream)), "pa_pool_fork")
+    n = children.numel()
+    args = (_int32(parents, "parents", n), _int32(children, "children"), n)
+    _check((_lib or lib()).pa_pool_fork(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)), "pa_pool_fork")
 
 
 def pa_pool_free(dims: pa_dims, pool: PagePool, rows, stream=None):
     """Empty the rows and give their pages back."""
-    _check(lib().pa_pool_free(ctypes.byref(dims), pool.ref, _ptr(_int32(rows, "rows")), int(rows.numel()),
-                              _stream(stream)), "pa_pool_free")
+    _check((_lib or lib()).pa_pool_free(ctypes.byref(dims), pool.ref, _int32(rows, "rows"), rows.numel(),
+                                        _stream(stream)), "pa_pool_free")
 
 
 def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None, ref_counts_out=None, stream=None):
@@ -551,10 +550,11 @@ def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None,
     place, or into the given arrays."""
     tables = pool.block_tables if block_tables_out is None else block_tables_out
     refs = pool.ref_counts if ref_counts_out is None else ref_counts_out
-    _int32(remap, "remap", pool.ref_counts.numel()), _int32(refs, "ref_counts_out", pool.ref_counts.numel())
-    _int32(tables, "block_tables_out", pool.block_tables.numel())
-    _check(lib().pa_pool_compact(ctypes.byref(dims), pool.ref, _ptr(remap), _ptr(tables), _ptr(refs),
-                                 _ptr(pool.workspace), pool.workspace_bytes, _stream(stream)), "pa_pool_compact")
+    pages = pool.ref_counts.numel()
+    args = (_int32(remap, "remap", pages), _int32(tables, "block_tables_out", pool.block_tables.numel()),
+            _int32(refs, "ref_counts_out", pages))
+    _check((_lib or lib()).pa_pool_compact(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
+           "pa_pool_compact")
 
 
 def int8_cache(dims: pa_dims, device="cuda"):

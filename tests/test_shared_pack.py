@@ -119,7 +119,7 @@ def test_items_are_dealt_out_evenly():
     dims = pa.make_dims(nb, 64, 28, 4, 128)
     plan = pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=256, pin=False)
     items, cta, _ = arrays(plan)
-    cost = [(1.62 if n > 18 else 2.8) * -(-(k1 - k0) // 128) + (2.5 if n > 18 else 1.5) for _, n, _, _, k0, k1, _, _ in items.tolist()]
+    cost = [(1.62 if n > 18 else 2.4) * -(-(k1 - k0) // 128) + (2.5 if n > 18 else 1.0) for _, n, _, _, k0, k1, _, _ in items.tolist()]
     load = [sum(cost[p:l0]) + sum(cost[a:b]) for p, l0, l1, end in cta.tolist() for a, b in ((l0, l1), (l1, end))]
     assert max(load) <= sum(load) / len(load) + max(cost)
 
