@@ -429,8 +429,9 @@ int pa_copy_blocks(const pa_dims *dims, void *k_cache, void *v_cache, const int3
 /*
  * Pages are given out, shared, copied and taken back on the device, in stream
  * order with the stores and decodes that use them, so that a step needs no
- * block id from the host (it knows the lengths; pa_decode, pa_decode_shared
- * and pa_store_kvcache take the pool's tables and the slots written here).
+ * block id from the host (it knows the lengths): the stores take the slots
+ * written here, pa_decode_shared(_int8) the pool's tables (its groups may be of
+ * one, and an entry that a refused call left -1 reads as zeros there).
  * Source: "手搓 vLLM 推理引擎", Step 2 (BlockManager: reference counts,
  * allocate, may_append, deallocate); "vLLM / SGLang 面试源码深挖", section 4
  * (fork).  New pages are always the free pages of the lowest ids, so the

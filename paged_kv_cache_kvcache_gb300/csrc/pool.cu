@@ -160,6 +160,7 @@ struct PoolParams {
     int32_t *context_lens;
     int32_t *refs;
     int32_t num_rows, max_blocks, num_blocks, block_size;
+    int32_t row_tokens; // most tokens a row can hold (an int32 with room for a page)
 };
 
 // Counts of 16 consecutive ids; those past the pool count as used.
@@ -292,9 +293,9 @@ __global__ void __launch_bounds__(kThreads)
                 } else {
                     ctx = p.context_lens[r];
                     bad = mark_row(sm, w, p.num_rows, r, i) ? 2 : 0;
-                    if (ctx < 0 || (int64_t)ctx > (int64_t)p.max_blocks * bs) {
+                    if (ctx < 0 || ctx > p.row_tokens) {
                         bad = 2;
-                    } else if (ctx + count > (int64_t)p.max_blocks * bs) {
+                    } else if (ctx + count > p.row_tokens) {
                         bad |= 1;
                     } else {
                         need = pages(ctx + (int)count, bs) - pages(ctx, bs);
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads)
                 } else {
                     ctx = p.context_lens[r];
                     bad = mark_row(sm, w, p.num_rows, c, i) ? 2 : 0;
-                    if (ctx < 0 || (int64_t)ctx > (int64_t)p.max_blocks * bs || p.context_lens[c] != 0) {
+                    if (ctx < 0 || ctx > p.row_tokens || p.context_lens[c] != 0) {
                         bad = 2;
                     } else if (ctx % bs != 0) {
                         need = 1;
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(128) pool_free_kernel(const PoolParams p, cons
         s_ctx = atomicExch(p.context_lens + r, 0);
     __syncthreads();
     const int ctx = s_ctx;
-    if (ctx < 0 || (int64_t)ctx > (int64_t)p.max_blocks * p.block_size) {
+    if (ctx < 0 || ctx > p.row_tokens) {
         if (threadIdx.x == 0)
             atomicOr(&g_pool_error, 2u);
         return;
@@ -772,8 +773,10 @@ __global__ void __launch_bounds__(kMoveThreads)
 
 PoolParams params_of(const PoolArgs &a)
 {
-    return {a.pool.block_tables, a.pool.context_lens,  a.pool.ref_counts, a.pool.num_rows,
-            a.pool.max_blocks,   a.dims.num_blocks,    a.dims.block_size};
+    const int64_t tokens = (int64_t)a.pool.max_blocks * a.dims.block_size;
+    return {a.pool.block_tables, a.pool.context_lens, a.pool.ref_counts,  a.pool.num_rows,
+            a.pool.max_blocks,   a.dims.num_blocks,   a.dims.block_size,
+            (int32_t)std::min<int64_t>(tokens, INT32_MAX - a.dims.block_size)};
 }
 
 Planes planes_of(const PoolArgs &a)

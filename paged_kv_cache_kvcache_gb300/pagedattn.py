@@ -178,6 +178,14 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
+def _here(*tensors) -> None:
+    """Refuse tensors that are not on the current device (a kernel launched there could not read them)."""
+    dev = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+
+
 def _int32(t, what: str, count: Optional[int] = None) -> int:
     """Address of a contiguous int32 tensor (of `count` values)."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous() or \
@@ -447,6 +455,7 @@ def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale
     ``block_tables``: the device table a plan without block lists was packed for.
     """
     bt = _shared_tables(plan, block_tables)
+    _here(q, k_cache, v_cache, out, workspace, block_tables, plan.dev)
     _check((_lib or lib()).pa_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), bt, scale, _ptr(out),
                                   plan.call_ref, *plan.call_arrays, _ptr(workspace), _nbytes(workspace),
                                   _stream(stream)), "pa_decode_shared")
@@ -456,6 +465,7 @@ def pa_decode_shared_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, 
                           workspace=None, block_tables=None, stream=None):
     """pa_decode_shared over an INT8 cache (same plan and workspace)."""
     bt = _shared_tables(plan, block_tables)
+    _here(q, k_cache, v_cache, k_scale, v_scale, out, workspace, block_tables, plan.dev)
     _check((_lib or lib()).pa_decode_shared_int8(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
                                        _ptr(v_scale), bt, scale, _ptr(out), plan.call_ref, *plan.call_arrays,
                                        *plan.call_singles, _ptr(workspace), _nbytes(workspace), _stream(stream)),
@@ -528,6 +538,7 @@ def pa_pool_append(dims: pa_dims, pool: PagePool, rows, cu_new, slot_mapping, st
     """Give row rows[i] its next cu_new[i+1] - cu_new[i] tokens; their slots go to slot_mapping."""
     n, tokens = rows.numel(), slot_mapping.numel()
     args = (_int32(rows, "rows"), _int32(cu_new, "cu_new", n + 1), n, _int32(slot_mapping, "slot_mapping"), tokens)
+    _here(pool.block_tables, rows, cu_new, slot_mapping)
     _check((_lib or lib()).pa_pool_append(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
            "pa_pool_append")
 
@@ -536,13 +547,16 @@ def pa_pool_fork(dims: pa_dims, pool: PagePool, parents, children, stream=None):
     """Row children[i] shares row parents[i]'s full pages and gets a copy of its partly filled one."""
     n = children.numel()
     args = (_int32(parents, "parents", n), _int32(children, "children"), n)
+    _here(pool.block_tables, parents, children)
     _check((_lib or lib()).pa_pool_fork(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)), "pa_pool_fork")
 
 
 def pa_pool_free(dims: pa_dims, pool: PagePool, rows, stream=None):
     """Empty the rows and give their pages back."""
-    _check((_lib or lib()).pa_pool_free(ctypes.byref(dims), pool.ref, _int32(rows, "rows"), rows.numel(),
-                                        _stream(stream)), "pa_pool_free")
+    at = _int32(rows, "rows")
+    _here(pool.block_tables, rows)
+    _check((_lib or lib()).pa_pool_free(ctypes.byref(dims), pool.ref, at, rows.numel(), _stream(stream)),
+           "pa_pool_free")
 
 
 def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None, ref_counts_out=None, stream=None):
@@ -553,6 +567,7 @@ def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None,
     pages = pool.ref_counts.numel()
     args = (_int32(remap, "remap", pages), _int32(tables, "block_tables_out", pool.block_tables.numel()),
             _int32(refs, "ref_counts_out", pages))
+    _here(pool.block_tables, remap, tables, refs)
     _check((_lib or lib()).pa_pool_compact(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
            "pa_pool_compact")
 

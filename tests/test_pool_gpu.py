@@ -179,6 +179,29 @@ def test_shared_partly_filled_page_is_not_written():
     assert all(torch.equal(a, b) for a, b in zip(before, (pool.block_tables, pool.context_lens, pool.ref_counts)))
 
 
+def test_rows_of_nearly_2_to_31_tokens():
+    """A table wide enough for more tokens than an int32 counts: the row is refused before its length wraps."""
+    dims, pool, m = both(layers=1, nb=8, bs=1024, hkv=1, d=64, rows=2, width=(1 << 21) + 4, seed=6)
+    pool.context_lens[1] = (1 << 31) - 1 - 1024 - 5          # (its pages do not matter here)
+    for count in (6, 1024, 5000):
+        append_only(dims, pool, [1], [count])
+        torch.cuda.synchronize()
+        assert pa.pa_read_device_error() & NO_ROOM
+    assert int(pool.context_lens[1]) == (1 << 31) - 1 - 1024 - 5 and int(pool.ref_counts.sum()) == 0
+
+
+def test_tensors_of_the_host_are_refused():
+    dims, pool, m = both()
+    rows, cu, slots = i32([1]), i32([0, 1]), torch.empty(1, dtype=torch.int32, device="cuda")
+    for bad in (lambda: pa.pa_pool_append(dims, pool, rows.cpu(), cu, slots),
+                lambda: pa.pa_pool_append(dims, pool, rows, cu, slots.cpu()),
+                lambda: pa.pa_pool_fork(dims, pool, rows, rows.cpu()), lambda: pa.pa_pool_free(dims, pool, rows.cpu()),
+                lambda: pa.pa_pool_compact(dims, pool, torch.empty(40, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            bad()
+    assert_same(pool, m)
+
+
 def test_free_twice_empty_and_outside():
     dims, pool, m = both()
     assert append(dims, pool, m, [0, 1, 2], [20, 33, 1])

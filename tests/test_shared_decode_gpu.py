@@ -271,6 +271,17 @@ def test_device_table_and_rows():
         decode(dims, q, kc, vc, plan, d ** -0.5, block_tables=torch.tensor(table[:, :7].copy(), device="cuda"))
 
 
+def test_tensors_of_the_host_are_refused():
+    dims = pa.make_dims(4, 16, 2, 1, 64)
+    kc, q = values((4, 16, 1, 64), 1), values((2, 2, 64), 2)
+    plan = pa.pa_pack_decode_shared(dims, [20, 30], block_lists=[[0, 1], [0, 2]]).upload()
+    ws, out = pa.shared_workspace(plan), torch.empty_like(q)
+    for args in ((q.cpu(), kc, kc, out, ws), (q, kc.cpu(), kc, out, ws), (q, kc, kc, out.cpu(), ws),
+                 (q, kc, kc, out, ws.cpu())):
+        with pytest.raises(ValueError):
+            pa.pa_decode_shared(dims, args[0], args[1], args[2], plan, 0.1, args[3], args[4])
+
+
 def test_block_ids_outside_the_pool_read_as_zeros():
     bs, hq, hkv, d = 16, 4, 2, 64
     ctx, lists, groups, nb = make_batch(9, [2], [8], [20, 40], bs)
