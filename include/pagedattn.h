@@ -142,10 +142,12 @@ typedef struct pa_shared_meta {
     uint64_t off_slot_mapping;   /* int32 [num_seqs] slot of each last token (tables_packed) */
     uint64_t off_items;          /* int32 [num_items][8]: first sequence, sequences, KV head,
                                     block-table row, first key, end key, part, scratch row of key 0 */
-    uint64_t off_cta_items;      /* int32 [num_ctas][4]: a CTA's items of more than rows_per_tile
-                                    sequences start at the first, those of its two lanes at the
-                                    second and third and end before the fourth, in each those of
-                                    several sequences before those of one, longest first */
+    uint64_t off_cta_items;      /* int32 [num_ctas][32]: [0..3] a CTA's items of more than
+                                    rows_per_tile sequences start at the first, those of its two
+                                    lanes at the second and third and end before the fourth, in
+                                    each those of several sequences before those of one, longest
+                                    first; [8..15] a copy of its first item (of the first list, or
+                                    of lane 0's), [16..23] of lane 1's first */
     uint64_t off_seq_parts;      /* int32 [num_seqs][2] first partial slot and number of parts */
     uint64_t off_single_items;   /* int32 [num_single_items][4]: sequence, first key, end key,
                                     partial slot or -1 */

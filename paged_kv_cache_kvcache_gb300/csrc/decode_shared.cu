@@ -168,25 +168,25 @@ struct Lane {
     Item w;
     int j, n;
     bool active;
-    __device__ Lane(const int4 *items, int from, int to) : it(items, from, to), w{}, j(0), n(0), active(it.more())
+    // `first`: item `from`, already at hand
+    __device__ Lane(const int4 *items, int from, int to, const Item &first)
+        : it(items, min(from + 1, to), to), w(first), j(0), n(first.tiles()),
+          active(from < to && !(kInt8 && first.nseq == 1))
     {
-        if (active) {
-            w = it.next();
-            n = w.tiles();
-        }
     }
-    // past the current key tile; true if that began a new item
-    __device__ bool step()
+    __device__ void next_item()
     {
-        if (++j < n)
-            return false;
         j = 0;
         active = it.more();
         if (active) {
             w = it.next();
             n = w.tiles();
         }
-        return true;
+    }
+    __device__ void step() // past the current key tile
+    {
+        if (++j == n)
+            next_item();
     }
 };
 
@@ -357,23 +357,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(bars.tmem_slot(), kTmemCols);
         ptx::tmem_relinquish();
     }
-    // This CTA's pairs and its lanes' singles.  What the roles look up first (an item, then, by the K
-    // and V producers, its blocks) is brought into L1 while the barriers and the tensor memory are
-    // set up: three dependent loads otherwise stand before the first tile.
-    const int4 span = __ldg(p.cta_items + blockIdx.x);
-    if (!kInt8 && (warp == kKWarp || warp == kVWarp)) {
-        const int first = span.x < span.y ? span.x : span.y, second = span.x < span.y ? span.x : span.z;
-        for (int i = first;; i = second) {
-            if (i < span.w) {
-                const int4 a0 = __ldg(p.items + 2 * i), a1 = __ldg(p.items + 2 * i + 1);
-                const int key = a1.x + lane * p.box_rows;
-                if (lane * p.box_rows < 128 && key < a1.y)
-                    ptx::prefetch_l1(p.block_tables + (size_t)a0.w * p.max_blocks + key / p.block_size);
-            }
-            if (i == second)
-                break;
+    // This CTA's pairs and its lanes' singles.  The K and V producers look up the rows of their first
+    // key tiles while the barriers and the tensor memory are set up: three dependent loads (list,
+    // item, block) would otherwise stand before the first tile, 0.6 us of a small call's 5.
+    const int4 *record = p.cta_items + (size_t)blockIdx.x * (kSharedCtaInts / 4);
+    const int4 span = __ldg(record);
+    // cache row of sub-box `lane` of key tile j of w; one past the pool reads as zeros
+    auto sub_row = [&](const Item &w, int j) -> int {
+        const int key = w.k0 + j * 128 + lane * p.box_rows;
+        if (lane * p.box_rows >= 128 || key >= w.k1)
+            return kInt8 ? p.scratch_rows : p.num_blocks * p.block_size;
+        if (kInt8)
+            return w.scratch + key;
+        const int phys = __ldg(p.block_tables + (size_t)w.row * p.max_blocks + key / p.block_size);
+        if ((uint32_t)phys >= (uint32_t)p.num_blocks) {
+            atomicOr(&g_shared_error, 2u);
+            return p.num_blocks * p.block_size;
+        }
+        return phys * p.block_size + (key & (p.block_size - 1));
+    };
+    // the first pair or else lane 0's first item, and lane 1's (zeros, no keys, where there is none)
+    Item first{}, second{};
+    int row0 = 0, row1 = 0;
+    if (warp >= 8) {
+        const int4 a0 = __ldg(record + 2), a1 = __ldg(record + 3), b0 = __ldg(record + 4), b1 = __ldg(record + 5);
+        first = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+        second = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+        if (warp == kKWarp || warp == kVWarp) {
+            row0 = sub_row(first, 0);
+            row1 = sub_row(second, 0);
         }
     }
+    // lane 0's first item: the record has it if there are no pairs
+    auto lane0_first = [&]() -> Item {
+        if (span.x == span.y || span.y == span.z)
+            return first;
+        const int4 a0 = __ldg(p.items + 2 * span.y), a1 = __ldg(p.items + 2 * span.y + 1);
+        return {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+    };
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -408,13 +429,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = load_q(w, 0, 0) && load_q(w, 1, P);
             }
             // the lanes advance tile by tile together: loads in the order in which they are needed
-            ItemIter<kInt8> i0(p.items, span.y, span.z), i1(p.items, span.z, span.w);
+            Lane<kInt8> l0(p.items, span.y, span.z, lane0_first()), l1(p.items, span.z, span.w, second);
             int at0 = 0, at1 = 0; // key tiles before each lane's next item
-            while (ok && (i0.more() || i1.more())) {
-                const bool first = i0.more() && (!i1.more() || at0 <= at1);
-                const Item w = first ? i0.next() : i1.next();
-                ok = load_q(w, first ? 0 : 1, 0);
-                (first ? at0 : at1) += w.tiles();
+            while (ok && (l0.active || l1.active)) {
+                const bool is0 = l0.active && (!l1.active || at0 <= at1);
+                ok = load_q(is0 ? l0.w : l1.w, is0 ? 0 : 1, 0);
+                if (is0) {
+                    at0 += l0.n;
+                    l0.next_item();
+                } else {
+                    at1 += l1.n;
+                    l1.next_item();
+                }
             }
         } else if (warp == kKWarp || warp == kVWarp) {
             // ------------------------------------------------------------ K and V producers
@@ -422,27 +448,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nstages = is_k ? L::kKStages : L::kVStages;
             const uint32_t ring = sbase + (is_k ? L::kK : L::kV);
             const CUtensorMap *tm = is_k ? &tm_k : &tm_v;
-            const int bs = p.block_size;
             const int box_rows = p.box_rows;
             const int nsub = 128 / box_rows;
             int st = 0;
             uint32_t ph = 0; // times the ring has wrapped
+            int X = 0;       // key tiles of pairs so far
             const uint64_t once = ptx::policy_evict_first(), keep = ptx::policy_evict_last();
             bool ok = true;
-            // cache row of sub-box `lane` of key tile j; one past the pool reads as zeros
-            auto sub_row = [&](const Item &w, int j) -> int {
-                const int key = w.k0 + j * 128 + lane * box_rows;
-                if (lane >= nsub || key >= w.k1)
-                    return kInt8 ? p.scratch_rows : p.num_blocks * bs;
-                if (kInt8)
-                    return w.scratch + key;
-                const int phys = __ldg(p.block_tables + (size_t)w.row * p.max_blocks + key / bs);
-                if ((uint32_t)phys >= (uint32_t)p.num_blocks) {
-                    atomicOr(&g_shared_error, 2u);
-                    return p.num_blocks * bs;
-                }
-                return phys * bs + (key & (bs - 1));
-            };
             // key tile j of w, whose sub-boxes lie at cache row `cur`, into the next slot
             auto load = [&](const Item &w, int j, int cur, uint64_t policy) {
                 const uint32_t full = is_k ? bars.k_full(st) : bars.v_full(st);
@@ -483,16 +495,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
                 const Item w = it.next();
                 const int n = w.tiles();
-                int next = sub_row(w, 0);
-                for (int j = 0; ok && j < n; ++j) {
+                int next = X == 0 ? row0 : sub_row(w, 0);
+                for (int j = 0; ok && j < n; ++j, ++X) {
                     const int cur = next;
                     if (j + 1 < n)
                         next = sub_row(w, j + 1);
                     load(w, j, cur, keep);
                 }
             }
-            Lane<kInt8> l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
-            int r0 = l0.active ? sub_row(l0.w, 0) : 0, r1 = l1.active ? sub_row(l1.w, 0) : 0;
+            Lane<kInt8> l0(p.items, span.y, span.z, lane0_first()), l1(p.items, span.z, span.w, second);
+            int r0 = X == 0 ? row0 : l0.active ? sub_row(l0.w, 0) : 0, r1 = row1;
             auto advance = [&](Lane<kInt8> &l, int &r) { // this tile's load, the next one's row looked up before it
                 const Item w = l.w;
                 const int j = l.j, cur = r;
@@ -622,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pass_k();
                 }
             }
-            Lane<kInt8> l0(p.items, span.y, span.z), l1(p.items, span.z, span.w);
+            Lane<kInt8> l0(p.items, span.y, span.z, lane0_first()), l1(p.items, span.z, span.w, second);
             // score product of the lane's current key tile
             auto score = [&](const Lane<kInt8> &l, int t) {
                 if (l.j == 0)

@@ -23,8 +23,9 @@ constexpr int kPrefillItemInts = 8;
 constexpr int kDecodeChunk = 16;
 constexpr int kDecodeStep = 64;
 constexpr int kMaxGroup = 16;
-// work-list entry of the shared-prefix decode (see pa_shared_meta)
+// work-list entry and CTA record of the shared-prefix decode (see pa_shared_meta)
 constexpr int kSharedItemInts = 8;
+constexpr int kSharedCtaInts = 32;
 
 // Thread-local error text.
 void set_error(const char *fmt, ...);

@@ -303,7 +303,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->off_block_tables = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs * mb : 0);
     meta->off_slot_mapping = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs : 0);
     meta->off_items = L.take(sizeof(int32_t) * kSharedItemInts * works.size());
-    meta->off_cta_items = L.take(sizeof(int32_t) * 4 * (size_t)ctas);
+    meta->off_cta_items = L.take(sizeof(int32_t) * kSharedCtaInts * (size_t)ctas);
     meta->off_seq_parts = L.take(sizeof(int32_t) * 2 * (size_t)num_seqs);
     meta->off_single_items = L.take(sizeof(int32_t) * 4 * (size_t)singles);
     meta->off_table_rows = L.take(sizeof(int32_t) * (size_t)num_seqs);
@@ -386,9 +386,11 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     for (size_t q = 1; q < fill.size(); ++q)
         next[q] = next[q - 1] + fill[q - 1];
     for (int32_t c = 0; c < ctas; ++c) {
+        int32_t *e = ci + (size_t)kSharedCtaInts * c;
+        std::memset(e, 0, sizeof(int32_t) * kSharedCtaInts);
         for (int32_t i = 0; i < 3; ++i)
-            ci[4 * c + i] = next[3 * (size_t)c + i];
-        ci[4 * c + 3] = next[3 * (size_t)c + 2] + fill[3 * (size_t)c + 2];
+            e[i] = next[3 * (size_t)c + i];
+        e[3] = next[3 * (size_t)c + 2] + fill[3 * (size_t)c + 2];
     }
     int32_t *one = reinterpret_cast<int32_t *>(base + meta->off_single_items);
     for (int32_t i : order) {
@@ -409,6 +411,14 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         e[5] = w.k1;
         e[6] = w.part;
         e[7] = w.scratch;
+    }
+    for (int32_t c = 0; c < ctas; ++c) { // what a CTA loads first, beside its lists' bounds
+        int32_t *e = ci + (size_t)kSharedCtaInts * c;
+        const int32_t first = e[0] < e[1] ? e[0] : e[1], second = e[2];
+        if (first < (e[0] < e[1] ? e[1] : e[2]))
+            std::memcpy(e + 8, it + (size_t)kSharedItemInts * first, sizeof(int32_t) * kSharedItemInts);
+        if (second < e[3])
+            std::memcpy(e + 16, it + (size_t)kSharedItemInts * second, sizeof(int32_t) * kSharedItemInts);
     }
     return PA_OK;
 }

@@ -32,7 +32,7 @@ def make_batch(seed, sizes, shared_blocks, tails, bs):
 def arrays(plan):
     m = plan.meta
     return (plan.host_array(m.off_items, 8 * m.num_items).reshape(-1, 8),
-            plan.host_array(m.off_cta_items, 4 * m.num_ctas).reshape(-1, 4),
+            plan.host_array(m.off_cta_items, 32 * m.num_ctas).reshape(-1, 32)[:, :4],
             plan.host_array(m.off_seq_parts, 2 * m.num_seqs).reshape(-1, 2))
 
 
@@ -62,8 +62,12 @@ def test_parts_cover_every_key_once(case):
     if m.num_items:  # CTA by CTA: pairs, first lane, second lane
         assert cta[0, 0] == 0 and cta[-1, 3] == m.num_items and (cta[1:, 0] == cta[:-1, 3]).all()
         assert (np.diff(cta, axis=1) >= 0).all() and (cta[:, 3] > cta[:, 0]).all()
-        for first, l0, l1, end in cta.tolist():
+        records = plan.host_array(m.off_cta_items, 32 * m.num_ctas).reshape(-1, 32)
+        for (first, l0, l1, end), r in zip(cta.tolist(), records):
             assert (items[first:l0, 1] > P).all() and (items[l0:end, 1] <= P).all()
+            # copies of the first items; zeros (no keys) where there is none
+            assert r[8:16].tolist() == (items[first].tolist() if first < l1 else [0] * 8)
+            assert r[16:24].tolist() == (items[l1].tolist() if l1 < end else [0] * 8)
     table = plan.host_array(m.off_block_tables, B * m.max_blocks_per_seq).reshape(B, -1)
     for b in range(B):
         n = -(-ctx[b] // bs)
