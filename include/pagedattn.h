@@ -137,6 +137,9 @@ typedef struct pa_shared_meta {
     int32_t num_single_items;   /* (sequence, key range) parts of single sequences (INT8) */
     int32_t num_shared_items;   /* work items of several sequences */
     int32_t num_scratch_tiles;  /* 128-key tiles of the groups' shared parts (INT8) */
+    int32_t direct;             /* bit 0 (bf16), bit 1 (INT8): contexts so short that they are
+                                   decoded whole, without sharing (never with a given split) */
+    int32_t reserved;
     uint64_t tokens_saved;       /* keys the groups read once instead of once per sequence */
     uint64_t off_block_tables;   /* int32 [num_seqs][max_blocks_per_seq], -1 padded (tables_packed) */
     uint64_t off_slot_mapping;   /* int32 [num_seqs] slot of each last token (tables_packed) */
@@ -152,6 +155,7 @@ typedef struct pa_shared_meta {
     uint64_t off_single_items;   /* int32 [num_single_items][4]: sequence, first key, end key,
                                     partial slot or -1 */
     uint64_t off_table_rows;     /* int32 [num_seqs] block-table row of each sequence */
+    uint64_t off_direct_items;   /* int32 [num_seqs][4]: sequence, 0, context length, -1 */
     uint64_t off_scratch_tiles;  /* int32 [num_scratch_tiles][4]: block-table row, first key, shared
                                     tokens, scratch row of the first key */
     uint64_t total_bytes;
@@ -395,7 +399,8 @@ int pa_decode_fused(const pa_dims *dims, const void *q, const void *k, const voi
  *   q, out:        device bf16 [meta->num_seqs][num_heads][head_dim]
  *   block_tables:  device int32, row pitch meta->max_blocks_per_seq: the plan's
  *                  (dev + meta->off_block_tables) or the caller's
- *   items, cta_items, seq_parts: device copies of the plan's arrays
+ *   items, cta_items, seq_parts, direct_items, table_rows: device copies of the
+ *                  plan's arrays
  *   workspace:     device memory of at least meta->workspace_bytes (may be NULL
  *                  when that is 0), 256-byte aligned; calls in flight at once
  *                  need separate workspaces
@@ -406,8 +411,9 @@ int pa_decode_fused(const pa_dims *dims, const void *q, const void *k, const voi
  */
 int pa_decode_shared(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                      const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
-                     const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts, void *workspace,
-                     size_t workspace_bytes, pa_stream_t stream);
+                     const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts,
+                     const int32_t *direct_items, const int32_t *table_rows, void *workspace, size_t workspace_bytes,
+                     pa_stream_t stream);
 
 /*
  * pa_copy_blocks — copy-on-write of shared cache blocks.  Source: "vLLM /
@@ -630,14 +636,15 @@ int pa_decode_int8_fused(const pa_dims *dims, const void *q, const void *k, cons
  * fp16 in the workspace (rounded to nearest even, clamped to +-65504); their
  * products run on those with fp32 accumulation.  The parts of single sequences
  * are computed as pa_decode_int8 computes them.
- *   single_items, table_rows, scratch_tiles: device copies of the plan's arrays
+ *   single_items, scratch_tiles: device copies of the plan's arrays
  *   workspace:  at least meta->workspace_bytes_int8
  */
 int pa_decode_shared_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                           const void *k_scale, const void *v_scale, const int32_t *block_tables, float scale, void *out,
                           const pa_shared_meta *meta, const int32_t *items, const int32_t *cta_items,
-                          const int32_t *seq_parts, const int32_t *single_items, const int32_t *table_rows,
-                          const int32_t *scratch_tiles, void *workspace, size_t workspace_bytes, pa_stream_t stream);
+                          const int32_t *seq_parts, const int32_t *direct_items, const int32_t *table_rows,
+                          const int32_t *single_items, const int32_t *scratch_tiles, void *workspace,
+                          size_t workspace_bytes, pa_stream_t stream);
 
 /*
  * pa_copy_blocks_int8 — pa_copy_blocks on an INT8 cache: for each (src, dst, n)

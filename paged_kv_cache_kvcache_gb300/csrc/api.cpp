@@ -438,7 +438,8 @@ extern "C" int pa_decode_int8(const pa_dims *dims, const void *q, const void *k_
 // Host-side checks of a shared-prefix decode; fills `a`.  Sets *nothing when there is no work.
 static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                           const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
-                          const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts, void *workspace,
+                          const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts,
+                          const int32_t *direct_items, const int32_t *table_rows, void *workspace,
                           size_t workspace_bytes, SharedArgs *a, bool *nothing)
 {
     *nothing = false;
@@ -459,19 +460,26 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
     const int group = dims->num_heads / dims->num_kv_heads;
     if (meta->rows_per_tile != (kPrefillRows / group > 0 ? kPrefillRows / group : 1))
         return fail(PA_ERR_INVALID_ARG, "%s: meta was packed for other dims", fn);
-    if (!q || !k_cache || !v_cache || !block_tables || !out || !items || !cta_items || !seq_parts)
+    if (!q || !k_cache || !v_cache || !block_tables || !out || !items || !cta_items || !seq_parts ||
+        !direct_items || !table_rows)
         return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
-    if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out) || misaligned(items))
+    if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out) || misaligned(items) ||
+        misaligned(direct_items))
         return fail(PA_ERR_INVALID_ARG, "%s: tensors and items must be 16-byte aligned", fn);
     if ((reinterpret_cast<uintptr_t>(seq_parts) & 7u) || misaligned(cta_items) ||
-        (reinterpret_cast<uintptr_t>(block_tables) & 3u))
+        (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(table_rows) & 3u))
         return fail(PA_ERR_INVALID_ARG, "%s: misaligned plan array or block table", fn);
     if (meta->num_items > 0 && dims->num_blocks == 0)
         return fail(PA_ERR_INVALID_ARG, "empty KV pool");
-    if (meta->num_scratch_tiles < 0 || meta->workspace_bytes != shared_part_bytes(*dims, meta->num_partials) ||
-        meta->workspace_bytes_int8 - meta->workspace_bytes != shared_scratch_bytes(*dims, meta->num_scratch_tiles, meta->num_seqs))
+    if (meta->num_scratch_tiles < 0)
+        return fail(PA_ERR_INVALID_ARG, "malformed shared decode meta");
+    const bool direct = (meta->direct & (int8 ? 2 : 1)) != 0;
+    const size_t part_bytes = shared_part_bytes(*dims, meta->num_partials);
+    const uint64_t need = direct ? 0
+                          : int8 ? part_bytes + shared_scratch_bytes(*dims, meta->num_scratch_tiles, meta->num_seqs)
+                                 : part_bytes;
+    if (need != (int8 ? meta->workspace_bytes_int8 : meta->workspace_bytes))
         return fail(PA_ERR_INVALID_ARG, "%s: meta was packed for other dims", fn);
-    const uint64_t need = int8 ? meta->workspace_bytes_int8 : meta->workspace_bytes;
     if (workspace_bytes < need)
         return fail(PA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %llu", fn, workspace_bytes,
                     (unsigned long long)need);
@@ -486,13 +494,15 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
     a->items = items;
     a->cta_items = cta_items;
     a->seq_parts = seq_parts;
+    a->table_rows = table_rows;
+    a->direct_items = direct ? direct_items : nullptr;
     a->out = out;
-    if (meta->num_partials > 0) {
+    if (need > 0) {
         a->part_o = static_cast<float *>(workspace);
         a->part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                                 shared_part_o_bytes(*dims, meta->num_partials));
+        a->scratch = static_cast<char *>(workspace) + part_bytes;
     }
-    a->scratch = static_cast<char *>(workspace) + meta->workspace_bytes;
     a->num_scratch_tiles = meta->num_scratch_tiles;
     a->scale = scale;
     a->num_seqs = meta->num_seqs;
@@ -508,12 +518,13 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
 extern "C" int pa_decode_shared(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                                 const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
                                 const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts,
-                                void *workspace, size_t workspace_bytes, pa_stream_t stream)
+                                const int32_t *direct_items, const int32_t *table_rows, void *workspace,
+                                size_t workspace_bytes, pa_stream_t stream)
 {
     SharedArgs a;
     bool nothing = false;
     int rc = prepare_shared("pa_decode_shared", false, dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
-                            cta_items, seq_parts, workspace, workspace_bytes, &a, &nothing);
+                            cta_items, seq_parts, direct_items, table_rows, workspace, workspace_bytes, &a, &nothing);
     if (rc != PA_OK || nothing)
         return rc;
     return launch_decode_shared(a, stream);
@@ -522,27 +533,26 @@ extern "C" int pa_decode_shared(const pa_dims *dims, const void *q, const void *
 extern "C" int pa_decode_shared_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                                      const void *k_scale, const void *v_scale, const int32_t *block_tables, float scale,
                                      void *out, const pa_shared_meta *meta, const int32_t *items,
-                                     const int32_t *cta_items, const int32_t *seq_parts, const int32_t *single_items,
-                                     const int32_t *table_rows, const int32_t *scratch_tiles, void *workspace,
-                                     size_t workspace_bytes, pa_stream_t stream)
+                                     const int32_t *cta_items, const int32_t *seq_parts, const int32_t *direct_items,
+                                     const int32_t *table_rows, const int32_t *single_items,
+                                     const int32_t *scratch_tiles, void *workspace, size_t workspace_bytes,
+                                     pa_stream_t stream)
 {
     SharedArgs a;
     bool nothing = false;
     int rc = prepare_shared("pa_decode_shared_int8", true, dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
-                            cta_items, seq_parts, workspace, workspace_bytes, &a, &nothing);
+                            cta_items, seq_parts, direct_items, table_rows, workspace, workspace_bytes, &a, &nothing);
     if (rc != PA_OK || nothing)
         return rc;
     if (meta->num_single_items < 0 || meta->num_shared_items < 0 || meta->num_shared_items > meta->num_items)
         return fail(PA_ERR_INVALID_ARG, "malformed shared decode meta");
-    if (!k_scale || !v_scale || !single_items || !table_rows || !scratch_tiles)
+    if (!k_scale || !v_scale || !single_items || !scratch_tiles)
         return fail(PA_ERR_INVALID_ARG, "pa_decode_shared_int8: NULL pointer");
-    if (misaligned(k_scale) || misaligned(v_scale) || misaligned(single_items) || misaligned(scratch_tiles) ||
-        (reinterpret_cast<uintptr_t>(table_rows) & 3u))
+    if (misaligned(k_scale) || misaligned(v_scale) || misaligned(single_items) || misaligned(scratch_tiles))
         return fail(PA_ERR_INVALID_ARG, "pa_decode_shared_int8: scales and items must be 16-byte aligned");
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.single_items = single_items;
-    a.table_rows = table_rows;
     a.scratch_tiles = scratch_tiles;
     a.num_items = meta->num_shared_items;
     a.num_single_items = meta->num_single_items;

@@ -74,15 +74,21 @@ struct DecParams {
     const int32_t *slot_mapping;
     const int32_t *context_lens;
     int64_t num_slots;
+    // a shared-prefix decode's contexts (SHARED kernels only): block-table row of each sequence, pool size
+    const int32_t *table_rows;
+    int32_t num_blocks;
 };
 
-__device__ uint32_t g_fused_error; // bit 0: a fused-store slot outside [-1, num_slots) was skipped
+// bit 0: a fused-store slot outside [-1, num_slots) was skipped; bit 1: SHARED met a block id outside the pool
+__device__ uint32_t g_fused_error;
 
 // FUSED: the CTA whose work item ends at the sequence's last key (the token
 // being decoded) writes that token's K/V rows into the cache slot and takes
 // its key from the input instead of the cache, so store and attention need
 // no ordering between launches.
-template <int D, int NT, bool FUSED>
+// SHARED: the items are short contexts of a shared-prefix decode.  Their table may be the
+// caller's: a block id outside the pool reads as zeros and sets bit 1 of g_fused_error.
+template <int D, int NT, bool FUSED, bool SHARED>
 __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecParams p)
 {
     using L = DecLayout<D>;
@@ -116,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecP
     const int nchunks = (k1 - k0 + 15) >> 4;
     const int my_n = nchunks > warp ? (nchunks - warp + kWarps - 1) / kWarps : 0;
     const uint32_t wbase = ptx::smem_u32(smem) + warp * L::kWarpBytes;
-    const int32_t *bt_row = p.block_tables + (size_t)b * p.max_blocks;
+    const int32_t *bt_row = p.block_tables + (size_t)(SHARED ? __ldg(p.table_rows + b) : b) * p.max_blocks;
     const int bs = p.block_size;
     const int Hkv = p.num_kv_heads;
     int blk_cache = 0;
@@ -128,6 +134,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecP
         }
         const int phys = __shfl_sync(0xffffffffu, blk_cache, i & 31);
         const int key0 = k0 + 16 * (warp + kWarps * i);
+        const bool inside = !SHARED || (uint32_t)phys < (uint32_t)p.num_blocks;
+        if (SHARED && !inside && lane == 0)
+            atomicOr(&g_fused_error, 2u);
         const int64_t row0 = (int64_t)phys * bs + (key0 & (bs - 1));
         const uint32_t sbase = wbase + (i % kStages) * L::kStageBytes;
 #pragma unroll
@@ -135,7 +144,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecP
             const int e = r * 32 + lane;
             const int t = e / L::kVecPerRow;
             const int c = e % L::kVecPerRow;
-            const bool valid = key0 + t < k1;
+            const bool valid = key0 + t < k1 && (!SHARED || inside);
             const size_t off = ((size_t)(row0 + t) * Hkv + g) * D + c * 8;
             const uint32_t dst = sbase + t * L::kRowBytes + ((c ^ (t & 7)) << 4);
             ptx::cp_async_16(dst, valid ? (const void *)(p.k_cache + off) : (const void *)p.k_cache, valid ? 16u : 0u);
@@ -398,28 +407,28 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const float *__rest
         dst[e] = __float2bfloat16_rn(accv[e] * inv);
 }
 
-template <int D, int NT, bool FUSED>
+template <int D, int NT, bool FUSED, bool SHARED = false>
 int launch_split(const DecodeArgs &a, const DecParams &p, cudaStream_t stream)
 {
-    if (int rc = ensure_smem<decode_split_kernel<D, NT, FUSED>>(DecLayout<D>::kSmemBytes, "decode"))
+    if (int rc = ensure_smem<decode_split_kernel<D, NT, FUSED, SHARED>>(DecLayout<D>::kSmemBytes, "decode"))
         return rc;
     // flat grid, heads of one work item adjacent: they read neighbouring
     // segments of the same token rows at about the same time (DRAM locality)
     dim3 grid((unsigned)(a.num_items * a.dims.num_kv_heads));
-    decode_split_kernel<D, NT, FUSED><<<grid, kWarps * 32, DecLayout<D>::kSmemBytes, stream>>>(p);
+    decode_split_kernel<D, NT, FUSED, SHARED><<<grid, kWarps * 32, DecLayout<D>::kSmemBytes, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
-    return launch_decode_combine(a, stream);
+    return SHARED ? PA_OK : launch_decode_combine(a, stream);
 }
 
 template <int D, int NT>
 int occupancy()
 {
     int n = 0;
-    cudaFuncSetAttribute(decode_split_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(decode_split_kernel<D, NT, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          DecLayout<D>::kSmemBytes);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<D, NT, false>, kWarps * 32,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<D, NT, false, false>, kWarps * 32,
                                                       DecLayout<D>::kSmemBytes) != cudaSuccess) {
         cudaGetLastError();
         return 2;
@@ -462,6 +471,13 @@ int launch_decode(const DecodeArgs &a, void *stream)
     p.max_blocks = a.max_blocks_per_seq;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool two = p.group > 8;
+    if (a.table_rows) { // short contexts of a shared-prefix decode
+        p.table_rows = a.table_rows;
+        p.num_blocks = a.dims.num_blocks;
+        if (a.dims.head_dim == 128)
+            return two ? launch_split<128, 2, false, true>(a, p, s) : launch_split<128, 1, false, true>(a, p, s);
+        return two ? launch_split<64, 2, false, true>(a, p, s) : launch_split<64, 1, false, true>(a, p, s);
+    }
     if (a.k_new) { // fused store + decode
         p.k_new = static_cast<const __nv_bfloat16 *>(a.k_new);
         p.v_new = static_cast<const __nv_bfloat16 *>(a.v_new);
@@ -487,7 +503,8 @@ int read_fused_error(uint32_t *code)
         e = cudaMemcpyToSymbol(g_fused_error, &zero, sizeof zero);
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "reading fused-store error word: %s", cudaGetErrorString(e));
-    *code |= v; // same meaning as the store kernel's bit 0
+    *code |= v & 1u;        // same meaning as the store kernel's bit 0
+    *code |= (v & 2u) << 5; // the shared-prefix decode's bit 6
     return PA_OK;
 }
 

@@ -39,6 +39,9 @@
 // 16-byte loads per row; converting in shared memory took 4.2.)  Parts of single sequences go to
 // the INT8 decode kernel, in a launch that may run beside the products.
 //
+// Short contexts (the plan decides, see pack_shared.cpp) gain nothing from sharing: they go whole
+// through the decode kernels, which start in half the time and have nothing to merge.
+//
 // Every hand-off waits with a time limit; a wait that runs out sets an error bit and the
 // kernel returns.  A block id outside the pool reads as zeros and sets an error bit.
 #include <cuda.h>
@@ -999,10 +1002,11 @@ int launch_codes(const SharedArgs &a, cudaStream_t stream)
     return PA_OK;
 }
 
-// INT8: the parts of single sequences; may run beside the shared parts' products.  (Beside the
-// conversion instead, with the products after both, 64 x 16384 took 75 us, not 50: these parts
-// are long and few, and the products waited for them.)
-int launch_singles(const SharedArgs &a, cudaStream_t stream)
+// Items (sequence, key range, partial slot) of single sequences through the decode kernels.  On an
+// INT8 cache, `beside`, they may run beside the shared parts' products.  (Beside the conversion
+// instead, with the products after both, 64 x 16384 took 75 us, not 50: these parts are long and
+// few, and the products waited for them.)
+int launch_singles(const SharedArgs &a, const int32_t *items, int32_t num_items, bool beside, cudaStream_t stream)
 {
     DecodeArgs s{};
     s.dims = a.dims;
@@ -1012,17 +1016,17 @@ int launch_singles(const SharedArgs &a, cudaStream_t stream)
     s.k_scale = a.k_scale;
     s.v_scale = a.v_scale;
     s.block_tables = a.block_tables;
-    s.items = a.single_items;
+    s.items = items;
     s.out = a.out;
     s.part_o = a.part_o;
     s.part_lse = a.part_lse;
     s.scale = a.scale;
     s.num_seqs = a.num_seqs;
-    s.num_items = a.num_single_items;
+    s.num_items = num_items;
     s.max_blocks_per_seq = a.max_blocks_per_seq;
     s.table_rows = a.table_rows;
-    s.beside = a.num_items > 0;
-    return launch_decode_int8(s, stream);
+    s.beside = beside;
+    return a.k_scale ? launch_decode_int8(s, stream) : launch_decode(s, stream);
 }
 
 template <int D, bool kInt8>
@@ -1091,7 +1095,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
             return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
     }
     if (kInt8 && a.num_single_items > 0)
-        if (int rc = launch_singles(a, stream))
+        if (int rc = launch_singles(a, a.single_items, a.num_single_items, a.num_items > 0, stream))
             return rc;
     if (!a.merge)
         return PA_OK;
@@ -1129,6 +1133,8 @@ int launch(const SharedArgs &a, cudaStream_t stream)
 int launch_decode_shared(const SharedArgs &a, void *stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (a.direct_items)
+        return launch_singles(a, a.direct_items, a.num_seqs, false, s);
     if (a.k_scale)
         return a.dims.head_dim == 128 ? launch<128, true>(a, s) : launch<64, true>(a, s);
     return a.dims.head_dim == 128 ? launch<128, false>(a, s) : launch<64, false>(a, s);

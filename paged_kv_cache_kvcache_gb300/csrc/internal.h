@@ -180,7 +180,7 @@ struct DecodeArgs {
     const void *k_new;
     const void *v_new;
     const int32_t *slot_mapping;
-    // parts of a shared-prefix decode on an INT8 cache (else NULL): no merge is launched
+    // contexts or parts of a shared-prefix decode (else NULL): no merge is launched
     const int32_t *table_rows; // block-table row of each sequence
     bool beside;               // may run beside the launch before it
 };
@@ -203,6 +203,7 @@ struct SharedArgs {
     const int32_t *seq_parts;
     const int32_t *single_items; // INT8 cache only
     const int32_t *table_rows;
+    const int32_t *direct_items; // set: every context is decoded whole, nothing is shared
     const int32_t *scratch_tiles;
     void *scratch; // fp16: the shared prefixes' K, then V, then the queries
     int32_t num_scratch_tiles;

@@ -23,7 +23,15 @@ constexpr int32_t kTile = kPrefillKeyTile;
 // both lanes of its CTA and is bound by the tensor core; a single occupies one lane, and two
 // lanes' loads share the SM's part of the HBM rate.  An item adds its query load and its
 // output.  The merge reads and writes every partial once.
-constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kPairItem = 2.5f, kSingleItem = 1.0f, kMergeBytesPerUs = 8.0e6f;
+constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kPairItem = 2.5f, kSingleItem = 2.0f, kMergeBytesPerUs = 8.0e6f;
+// What a call takes beyond that (set-up and merge), and what the decode kernels take for the contexts
+// whole, one part each: a start, a step of 64 keys after the other, or the bytes of all contexts
+// from L2 and HBM.  Measured (28 / 4 heads of 128): 2 x 84 tokens 4.5 us against 8.6 shared, 8 x 300
+// 6.4 against 9.0, 8 x 808 10.3 against 9.2; 128 x 300 14.1 against 17.4, 128 x 556 19.2 against
+// 17.5; INT8 8 x 300 7.5 against 14.4, 8 x 1068 16.0 against 15.0, 128 x 1068 28.0 against 23.5.
+constexpr float kSharedStart = 6.5f, kSharedStartInt8 = 11.f;
+constexpr float kDirectStart = 4.0f, kDirectKey = 0.0075f, kDirectKeyInt8 = 0.011f, kDirectBytesPerUs = 8.0e6f,
+                kDirectBytesPerUsInt8 = 6.5e6f;
 
 struct Run { // consecutive sequences of a group that share `shared` tokens
     int32_t s0, n, shared;
@@ -192,9 +200,9 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
             }
     }
     int32_t per = split_tokens / kTile;
+    float best = INFINITY; // the chosen ranges' time
     if (per == 0) {
         static const int32_t kPer[] = {1, 2, 3, 4, 6, 8, 11, 16, 22, 32, 45, 64, 90, 128, 181, 256, 512, 1 << 24};
-        float best = INFINITY;
         const float slot_us = (float)d.num_heads * d.head_dim * 8.f / kMergeBytesPerUs;
         for (int32_t c : kPer) {
             float pair_work = 0.f, single_work = 0.f, pair = 0.f, single = 0.f, slots = 0.f; // lane time, longest, slots
@@ -226,6 +234,16 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         }
         per = std::max(per, 1);
     }
+
+    int64_t all_keys = 0;
+    for (int32_t b = 0; b < num_seqs; ++b)
+        all_keys += context_lens[b];
+    const float keys_bytes = (float)all_keys * d.num_kv_heads * d.head_dim * 2;
+    const bool direct = split_tokens == 0 && kDirectStart + std::max(kDirectKey * max_ctx, 2 * keys_bytes / kDirectBytesPerUs) <
+                                                 kSharedStart + best;
+    const bool direct_int8 =
+        split_tokens == 0 && kDirectStart + std::max(kDirectKeyInt8 * max_ctx, keys_bytes / kDirectBytesPerUsInt8) <
+                                 kSharedStartInt8 + best;
 
     // items and partial slots
     std::vector<Work> works;
@@ -298,6 +316,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->num_single_items = singles;
     meta->num_shared_items = shared_items;
     meta->num_scratch_tiles = (int32_t)scratch_tiles;
+    meta->direct = (direct ? 1 : 0) | (direct_int8 ? 2 : 0);
     for (const Run &r : runs)
         meta->tokens_saved += (uint64_t)r.shared * (uint64_t)(r.n - 1);
     meta->off_block_tables = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs * mb : 0);
@@ -307,10 +326,12 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->off_seq_parts = L.take(sizeof(int32_t) * 2 * (size_t)num_seqs);
     meta->off_single_items = L.take(sizeof(int32_t) * 4 * (size_t)singles);
     meta->off_table_rows = L.take(sizeof(int32_t) * (size_t)num_seqs);
+    meta->off_direct_items = L.take(sizeof(int32_t) * 4 * (size_t)num_seqs);
     meta->off_scratch_tiles = L.take(sizeof(int32_t) * 4 * (size_t)scratch_tiles);
     meta->total_bytes = L.off;
-    meta->workspace_bytes = shared_part_bytes(d, partials);
-    meta->workspace_bytes_int8 = meta->workspace_bytes + shared_scratch_bytes(d, scratch_tiles, num_seqs);
+    meta->workspace_bytes = direct ? 0 : shared_part_bytes(d, partials);
+    meta->workspace_bytes_int8 =
+        direct_int8 ? 0 : shared_part_bytes(d, partials) + shared_scratch_bytes(d, scratch_tiles, num_seqs);
     if (!host_buf)
         return PA_OK;
     if (host_buf_bytes < meta->total_bytes)
@@ -331,8 +352,20 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         }
     }
     int32_t *rows = reinterpret_cast<int32_t *>(base + meta->off_table_rows);
-    for (int32_t b = 0; b < num_seqs; ++b)
+    std::vector<int32_t> longest(num_seqs);
+    for (int32_t b = 0; b < num_seqs; ++b) {
         rows[b] = table_rows ? table_rows[b] : b;
+        longest[b] = b;
+    }
+    std::stable_sort(longest.begin(), longest.end(), [&](int32_t x, int32_t y) { return context_lens[x] > context_lens[y]; });
+    int32_t *whole = reinterpret_cast<int32_t *>(base + meta->off_direct_items);
+    for (int32_t b : longest) {
+        whole[0] = b;
+        whole[1] = 0;
+        whole[2] = context_lens[b];
+        whole[3] = -1;
+        whole += 4;
+    }
     int32_t *tile = reinterpret_cast<int32_t *>(base + meta->off_scratch_tiles);
     for (const Prefix &x : groups_scratch)
         for (int32_t k = 0; k < x.shared; k += kTile, tile += 4) {

@@ -64,12 +64,13 @@ class pa_shared_meta(ctypes.Structure):
                 ("max_parts", ctypes.c_int32), ("rows_per_tile", ctypes.c_int32), ("merge", ctypes.c_int32),
                 ("split_tokens", ctypes.c_int32), ("tables_packed", ctypes.c_int32),
                 ("num_single_items", ctypes.c_int32), ("num_shared_items", ctypes.c_int32),
-                ("num_scratch_tiles", ctypes.c_int32),
+                ("num_scratch_tiles", ctypes.c_int32), ("direct", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("tokens_saved", ctypes.c_uint64), ("off_block_tables", ctypes.c_uint64),
                 ("off_slot_mapping", ctypes.c_uint64), ("off_items", ctypes.c_uint64),
                 ("off_cta_items", ctypes.c_uint64), ("off_seq_parts", ctypes.c_uint64),
                 ("off_single_items", ctypes.c_uint64), ("off_table_rows", ctypes.c_uint64),
-                ("off_scratch_tiles", ctypes.c_uint64), ("total_bytes", ctypes.c_uint64),
+                ("off_direct_items", ctypes.c_uint64), ("off_scratch_tiles", ctypes.c_uint64),
+                ("total_bytes", ctypes.c_uint64),
                 ("workspace_bytes", ctypes.c_uint64), ("workspace_bytes_int8", ctypes.c_uint64)]
 
 
@@ -122,8 +123,8 @@ def lib() -> ctypes.CDLL:
             L.pa_prefill_varlen_int8.argtypes = [P] * 11 + [ctypes.c_float] + [P] * 4 + [SZ, P]
             L.pa_prefill_varlen_int8_fused.argtypes = [P] * 14 + [ctypes.c_float] + [P] * 4 + [SZ, P]
             L.pa_pack_decode_shared.argtypes = [P, I32, P, I32, P, P, P, P, P, I32, I32, P, SZ, P]
-            L.pa_decode_shared.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, P, P, P, P, SZ, P]
-            L.pa_decode_shared_int8.argtypes = [P] * 7 + [ctypes.c_float] + [P] * 9 + [SZ, P]
+            L.pa_decode_shared.argtypes = [P] * 5 + [ctypes.c_float] + [P] * 8 + [SZ, P]
+            L.pa_decode_shared_int8.argtypes = [P] * 7 + [ctypes.c_float] + [P] * 10 + [SZ, P]
             L.pa_pool_workspace.argtypes = [P, P, P]
             L.pa_pool_append.argtypes = [P, P, P, P, I32, P, I32, P, SZ, P]
             L.pa_pool_fork.argtypes = [P, P, P, P, I32, P, SZ, P]
@@ -260,8 +261,9 @@ class SharedPlan(_Plan):
         m, base = self.meta, self.dev.data_ptr()
         self.call_ref = ctypes.byref(m)
         self.call_tables = base + m.off_block_tables if m.tables_packed or m.num_seqs == 0 else None
-        self.call_arrays = tuple(base + x for x in (m.off_items, m.off_cta_items, m.off_seq_parts))
-        self.call_singles = (base + m.off_single_items, base + m.off_table_rows, base + m.off_scratch_tiles)
+        self.call_arrays = tuple(base + x for x in (m.off_items, m.off_cta_items, m.off_seq_parts, m.off_direct_items,
+                                                   m.off_table_rows))
+        self.call_singles = (base + m.off_single_items, base + m.off_scratch_tiles)
         return self
 
     @property
@@ -429,9 +431,11 @@ def _nbytes(workspace) -> int:
 
 
 def shared_workspace(plan: SharedPlan, device="cuda", int8: bool = True) -> Optional[torch.Tensor]:
-    """Workspace of a shared-prefix decode; with int8=False only pa_decode_shared's (without the fp16 copy
-    of the shared parts)."""
-    n = int(plan.meta.workspace_bytes_int8 if int8 else plan.meta.workspace_bytes)
+    """Workspace of a shared-prefix decode on either cache; with int8=False only pa_decode_shared's (without
+    the fp16 copy of the shared parts)."""
+    n = int(plan.meta.workspace_bytes)
+    if int8:
+        n = max(n, int(plan.meta.workspace_bytes_int8))
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 

@@ -163,7 +163,7 @@ def test_int8_every_code():
         torch.full((2, hkv, bs), s, dtype=torch.float16, device="cuda") for s in (0.0625, 0.25)]
     q = values((2, hq, d), 155)
     dims = pa.make_dims(2, bs, hq, hkv, d)
-    plan = pa.pa_pack_decode_shared(dims, ctx, block_lists=lists).upload()
+    plan = pa.pa_pack_decode_shared(dims, ctx, block_lists=lists, split_tokens=128).upload()
     assert plan.meta.num_shared_items > 0 and plan.meta.num_single_items == 0
     out = decode8(dims, q, cache, plan, 0.5)
     dense = [c.double() * s for c, s in zip(cache[:2], (0.0625, 0.25))]
@@ -171,7 +171,8 @@ def test_int8_every_code():
     assert_within(out, ref, a, "every code")
 
 
-def test_int8_block_ids_outside_the_pool_read_as_zeros():
+@pytest.mark.parametrize("split", [0, 128])
+def test_int8_block_ids_outside_the_pool_read_as_zeros(split):
     bs, hq, hkv, d = 16, 4, 2, 64
     ctx, lists, groups, nb = make_batch(9, [2], [8], [20, 40], bs)
     cache, dense = int8_pool(nb, bs, hkv, d, 90, ctx, lists)
@@ -182,7 +183,8 @@ def test_int8_block_ids_outside_the_pool_read_as_zeros():
     for b, r in enumerate((3, 1)):
         table[r, :len(lists[b])] = lists[b]
     table[[1, 3], 3], table[1, 9] = -5, nb + 100
-    plan = pa.pa_pack_decode_shared(dims, ctx, shared_lens=[8 * bs], table_rows=[3, 1], max_blocks=width).upload()
+    plan = pa.pa_pack_decode_shared(dims, ctx, shared_lens=[8 * bs], table_rows=[3, 1], max_blocks=width,
+                                    split_tokens=split).upload()
     out = decode8(dims, q, cache, plan, d ** -0.5, block_tables=torch.tensor(table, device="cuda"))
     torch.cuda.synchronize()
     assert pa.pa_read_device_error() == 1 << 6
@@ -250,7 +252,8 @@ def test_equals_pa_decode():
     assert ((out.double() - plain.double()).abs() <= 2 * (U * (a + ref.abs()) + 2e-4 * a)).all()
 
 
-def test_device_table_and_rows():
+@pytest.mark.parametrize("split", [0, 128])
+def test_device_table_and_rows(split):
     """A plan for a table on the device whose rows are in another order."""
     bs, hq, hkv, d = 32, 8, 2, 64
     ctx, lists, groups, nb = make_batch(8, [3, 2], [4, 2], [5, 60, 33, 1, 2], bs)
@@ -261,7 +264,8 @@ def test_device_table_and_rows():
     table = np.full((9, 8), -1, np.int32)
     for b, r in enumerate(rows):
         table[r, :len(lists[b])] = lists[b]
-    plan = pa.pa_pack_decode_shared(dims, ctx, groups, shared_lens=[4 * bs, 2 * bs], table_rows=rows, max_blocks=8).upload()
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, shared_lens=[4 * bs, 2 * bs], table_rows=rows, max_blocks=8,
+                                    split_tokens=split).upload()
     out = decode(dims, q, kc, vc, plan, d ** -0.5, block_tables=torch.tensor(table, device="cuda"))
     ref, a = reference(q, kc, vc, lists, ctx, bs, d ** -0.5)
     assert_within(out, ref, a, "device table")
@@ -274,7 +278,7 @@ def test_device_table_and_rows():
 def test_tensors_of_the_host_are_refused():
     dims = pa.make_dims(4, 16, 2, 1, 64)
     kc, q = values((4, 16, 1, 64), 1), values((2, 2, 64), 2)
-    plan = pa.pa_pack_decode_shared(dims, [20, 30], block_lists=[[0, 1], [0, 2]]).upload()
+    plan = pa.pa_pack_decode_shared(dims, [20, 30], block_lists=[[0, 1], [0, 2]], split_tokens=128).upload()
     ws, out = pa.shared_workspace(plan), torch.empty_like(q)
     for args in ((q.cpu(), kc, kc, out, ws), (q, kc.cpu(), kc, out, ws), (q, kc, kc, out.cpu(), ws),
                  (q, kc, kc, out, ws.cpu())):
@@ -282,7 +286,8 @@ def test_tensors_of_the_host_are_refused():
             pa.pa_decode_shared(dims, args[0], args[1], args[2], plan, 0.1, args[3], args[4])
 
 
-def test_block_ids_outside_the_pool_read_as_zeros():
+@pytest.mark.parametrize("split", [0, 128])
+def test_block_ids_outside_the_pool_read_as_zeros(split):
     bs, hq, hkv, d = 16, 4, 2, 64
     ctx, lists, groups, nb = make_batch(9, [2], [8], [20, 40], bs)
     kc, vc = pool(nb, bs, hkv, d, 90, ctx, lists)
@@ -293,7 +298,8 @@ def test_block_ids_outside_the_pool_read_as_zeros():
     for b in range(2):
         table[b, :len(lists[b])] = lists[b]
     table[:, 3], table[1, 9] = -5, nb + 100
-    plan = pa.pa_pack_decode_shared(dims, ctx, shared_lens=[8 * bs], max_blocks=width).upload()
+    plan = pa.pa_pack_decode_shared(dims, ctx, shared_lens=[8 * bs], max_blocks=width, split_tokens=split).upload()
+    assert plan.meta.direct == (3 if split == 0 else 0)
     out = decode(dims, q, kc, vc, plan, d ** -0.5, block_tables=torch.tensor(table, device="cuda"))
     torch.cuda.synchronize()
     assert pa.pa_read_device_error() == 1 << 6

@@ -128,6 +128,24 @@ def test_items_are_dealt_out_evenly():
     assert max(load) <= sum(load) / len(load) + max(cost)
 
 
+def test_short_contexts_are_decoded_whole():
+    """The plan decides by lengths; with a given split it never does.  Every sequence is in the list once."""
+    dims = pa.make_dims(4000, 16, 28, 4, 128)
+
+    def plan(n, shared, tail, split=0):
+        ctx, lists, groups, nb = make_batch(3, [n], [shared // 16], [tail + i % 3 for i in range(n)], 16)
+        return ctx, pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=split, pin=False)
+
+    for n, shared, tail, direct in ((2, 64, 20, 3), (8, 256, 44, 3), (8, 8192, 44, 0), (64, 4096, 200, 0)):
+        ctx, p = plan(n, shared, tail)
+        m = p.meta
+        assert m.direct == direct and plan(n, shared, tail, 128)[1].meta.direct == 0
+        assert (m.workspace_bytes == 0) == bool(direct & 1) and (m.workspace_bytes_int8 == 0) == bool(direct & 2)
+        whole = p.host_array(m.off_direct_items, 4 * n).reshape(-1, 4)
+        assert sorted(whole[:, 0].tolist()) == list(range(n)) and (np.diff(whole[:, 2]) <= 0).all()
+        assert all(x == [b, 0, ctx[b], -1] for x in whole.tolist() for b in x[:1])
+
+
 def test_shared_length_is_found_and_checked():
     dims = pa.make_dims(64, 16, 4, 2, 64)
     ctx, lists = [100, 90, 70], [[1, 2, 3, 4, 5, 6, 7], [1, 2, 3, 9, 10, 11], [1, 2, 3, 4, 20]]
@@ -188,9 +206,9 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     m = pa.pa_shared_meta()
     L = pa.lib()
 
-    def call(scale=0.1, q=16, out=16, ws=None, nbytes=0, bt=16, items=16, dims=dims):
+    def call(scale=0.1, q=16, out=16, ws=None, nbytes=0, bt=16, items=16, whole=16, rows=16, dims=dims):
         return L.pa_decode_shared(ctypes.byref(dims), q, 16, 16, bt, ctypes.c_float(scale), out, ctypes.byref(m), items,
-                                  16, 16, ws, nbytes, None)
+                                  16, 16, whole, rows, ws, nbytes, None)
 
     m.num_seqs, m.num_items, m.num_ctas, m.max_blocks_per_seq, m.rows_per_tile = 0, 0, 0, 1, 64
     assert call() == pa.PA_OK                                   # nothing to do
@@ -200,7 +218,7 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     assert call(q=None) == pa.PA_ERR_INVALID_ARG
     assert call(out=8) == pa.PA_ERR_INVALID_ARG
     assert call(items=24) == pa.PA_ERR_INVALID_ARG
-    assert call(bt=None) == pa.PA_ERR_INVALID_ARG
+    assert call(bt=None) == call(whole=None) == call(whole=8) == call(rows=None) == call(rows=18) == pa.PA_ERR_INVALID_ARG
     assert call(dims=pa.make_dims(8, 16, 8, 2, 64)) == pa.PA_ERR_INVALID_ARG   # packed for group 2
     assert call(dims=pa.make_dims(0, 16, 4, 2, 64)) == pa.PA_ERR_INVALID_ARG   # empty pool
     m.num_partials, m.workspace_bytes, m.workspace_bytes_int8 = 3, 1024 * 3 + 256, 1024 * 3 + 256
@@ -216,7 +234,7 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
         a = dict(ks=16, vs=16, one=16, rows=16, tiles=16, nbytes=1 << 20)
         a.update(change)
         return L.pa_decode_shared_int8(ctypes.byref(dims), 16, 16, 16, a["ks"], a["vs"], 16, ctypes.c_float(0.1), 16,
-                                       ctypes.byref(m), 16, 16, 16, a["one"], a["rows"], a["tiles"], 256, a["nbytes"], None)
+                                       ctypes.byref(m), 16, 16, 16, 16, a["rows"], a["one"], a["tiles"], 256, a["nbytes"], None)
 
     m.num_shared_items = 5  # more than there are items
     assert call8() == pa.PA_ERR_INVALID_ARG
@@ -226,6 +244,8 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
         assert call8(**bad) == pa.PA_ERR_INVALID_ARG, bad
     assert call8(nbytes=m.workspace_bytes) == pa.PA_ERR_WORKSPACE  # bf16's would do
     m.num_scratch_tiles = 1
+    assert call8() == pa.PA_ERR_INVALID_ARG
+    m.num_scratch_tiles, m.direct = 2, 2  # INT8 would decode whole contexts: it needs no workspace
     assert call8() == pa.PA_ERR_INVALID_ARG
     m.num_ctas = 0
     assert call(ws=256, nbytes=4096) == pa.PA_ERR_INVALID_ARG
