@@ -244,6 +244,7 @@ struct CodesParams {
 constexpr int kCodesKeys = 32;
 __global__ void __launch_bounds__(256) shared_codes_kernel(const CodesParams p)
 {
+    ptx::launch_dependents();
     if ((int)blockIdx.x >= p.tile_ctas) {
         const int64_t i = (int64_t)((int)blockIdx.x - p.tile_ctas) * 256 + threadIdx.x;
         if (i >= p.q_vecs)
@@ -406,6 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= 8) {
         ptx::reg_dealloc<kOtherRegs>();
+        // INT8: this launch is set up while the scratch copies are written; nothing is read before they are
+        if (kInt8 && warp != kMmaWarp)
+            ptx::grid_dependency_wait();
         uint32_t nq0 = 0, nq1 = 0; // query loads of each tile so far
         // query rows of `w` (from sequence w.s0 + skip) into tile t, once the last score product that
         // read the buffer is complete
@@ -1089,10 +1093,21 @@ int launch(const SharedArgs &a, cudaStream_t stream)
         p.box_rows = (int32_t)box_rows;
         p.max_blocks = a.max_blocks_per_seq;
         p.num_blocks = d.num_blocks;
-        decode_shared_kernel<D, kInt8><<<(unsigned)a.num_ctas, kThreads, L::kSmemBytes, stream>>>(tq, tq1, tk, tv, p);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess)
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)a.num_ctas);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = L::kSmemBytes;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = kInt8 ? 1 : 0;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_shared_kernel<D, kInt8>, tq, tq1, tk, tv, p);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
             return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
+        }
     }
     if (kInt8 && a.num_single_items > 0)
         if (int rc = launch_singles(a, a.single_items, a.num_single_items, a.num_items > 0, stream))
