@@ -826,9 +826,15 @@ int launch_ex(const char *what, void (*kernel)(P...), unsigned grid, unsigned bl
     return PA_OK;
 }
 
-// One CTA looks through 16384 ids in a round of about 1 us; a cluster costs about 3 us more to
-// start and meet.
-bool plan_by_cluster(const PoolArgs &a) { return a.dims.num_blocks > 3 * kThreads * kIds; }
+// One CTA looks through 16384 ids in a round, a cluster through 131072, but it takes 2.5 us more to
+// start and meet.  A search for free pages ends when it has found enough: a round over pages in use
+// costs one CTA 1.6 us, so in a pool half full the two meet at 3 rounds (8 tokens appended to 8
+// rows, then freed, one CTA against the cluster: 49152 pages 9.9 / 10.9 us, 131072 14.9 / 10.9).
+// A compaction goes through all ids three times and writes them all, 14 us a round (16384 pages
+// 14.9 / 16.4 us, 24000 24.1 / 16.5, 49152 44.4 / 16.9).
+constexpr int kRoundIds = kThreads * kIds;
+bool search_by_cluster(const PoolArgs &a) { return a.dims.num_blocks > 3 * kRoundIds; }
+bool compact_by_cluster(const PoolArgs &a) { return a.dims.num_blocks > kRoundIds; }
 
 } // namespace
 
@@ -841,7 +847,7 @@ int launch_pool_append(const PoolArgs &a, const int32_t *rows, const int32_t *cu
                        void *stream)
 {
     // a planning CTA writes a few thousand slots in the time that another launch takes
-    const bool many = num_tokens > 4 * kThreads, cluster = plan_by_cluster(a);
+    const bool many = num_tokens > 4 * kThreads, cluster = search_by_cluster(a);
     auto kernel = many ? (cluster ? pool_append_kernel<true, false> : pool_append_kernel<false, false>)
                        : (cluster ? pool_append_kernel<true, true> : pool_append_kernel<false, true>);
     const unsigned c = cluster ? kClusterCtas : 1;
@@ -860,7 +866,7 @@ int launch_pool_fork(const PoolArgs &a, const int32_t *parents, const int32_t *c
     if (int rc = sm_count(&sms))
         return rc;
     const Planes q = planes_of(a);
-    const bool cluster = plan_by_cluster(a);
+    const bool cluster = search_by_cluster(a);
     const unsigned c = cluster ? kClusterCtas : 1;
     if (int rc = launch_ex("pool fork", cluster ? pool_fork_kernel<true> : pool_fork_kernel<false>, c, kThreads, c, false,
                            stream, params_of(a), parents, children, n, (int)(q.row_vecs * 16), a.workspace))
@@ -884,7 +890,7 @@ int launch_pool_compact(const PoolArgs &a, int32_t *remap, int32_t *tables_out, 
     int sms = 0;
     if (int rc = sm_count(&sms))
         return rc;
-    const bool cluster = plan_by_cluster(a);
+    const bool cluster = compact_by_cluster(a);
     const unsigned c = cluster ? kClusterCtas : 1;
     if (int rc = launch_ex("pool compact", cluster ? pool_compact_kernel<true> : pool_compact_kernel<false>, c, kThreads,
                            c, false, stream, params_of(a), remap, refs_out, a.workspace))
