@@ -153,6 +153,20 @@ struct Team {
             return *cg::this_cluster().map_shared_rank(word, 0);
         return *word;
     }
+    // the first CTA's n starts and lens into every CTA's shared memory
+    __device__ void rows_of_first(int n)
+    {
+        if constexpr (kCluster) {
+            if (rank() == 0)
+                return;
+            const int *starts = cg::this_cluster().map_shared_rank(s.starts, 0);
+            const int *lens = cg::this_cluster().map_shared_rank(s.lens, 0);
+            for (int i = threadIdx.x; i < n; i += kThreads) {
+                s.starts[i] = starts[i];
+                s.lens[i] = lens[i];
+            }
+        }
+    }
 };
 
 struct PoolParams {
@@ -239,6 +253,19 @@ __device__ __forceinline__ int last_at_most(const int32_t *a, int n, int x)
     return lo;
 }
 
+// The same by a warp, all lanes with the same arguments: 32 entries are compared in the time of one.
+__device__ __forceinline__ int last_at_most_warp(const int32_t *a, int n, int x)
+{
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = (int)(threadIdx.x & 31u) * step;
+        const int upto = __popc(__ballot_sync(0xffffffffu, at < n && a[lo + at] <= x)) - 1;
+        lo += upto * step;
+        n = min(step, n - upto * step);
+    }
+    return lo;
+}
+
 // What the planning kernels begin with: shared memory cleared, this thread's counts on their way.
 template <bool kCluster>
 __device__ __forceinline__ void plan_begin(Team<kCluster> &team, const PoolParams &p, int4 (&refs)[kIds / 4])
@@ -276,7 +303,7 @@ __global__ void __launch_bounds__(kThreads)
     const int nt = team.threads(), me = team.thread(), bs = p.block_size;
     int4 refs[kIds / 4];
     plan_begin(team, p, refs);
-    const bool small = !kCluster && n <= kThreads; // the rows' counts stay in shared memory
+    const bool small = n <= kThreads; // the rows' counts stay in shared memory
     int32_t *starts = small ? sm.starts : w.starts, *lens = small ? sm.lens : w.lens;
     if (team.rank() == 0) {
         int want = 0;
@@ -328,6 +355,8 @@ __global__ void __launch_bounds__(kThreads)
     team.sync();
     const int want = team.of_first(&sm.want);
     int bad = team.of_first(&sm.bad);
+    if (small)
+        team.rows_of_first(n); // (there is a barrier between here and their use)
     if (want > p.num_blocks)
         bad |= 1;
     int32_t *list = !kCluster && want <= kSmallList ? sm.list : w.list;
@@ -377,12 +406,12 @@ __global__ void __launch_bounds__(256)
     ptx::grid_dependency_wait();
     const bool refused = *static_cast<const int32_t *>(workspace) < 0;
     const int64_t t0 = ((int64_t)blockIdx.x * 256 + (threadIdx.x & ~31u)) * 4, t = t0 + 4 * (threadIdx.x & 31u);
-    if (t >= num_tokens)
+    if (t0 >= num_tokens)
         return;
     int v[4] = {-1, -1, -1, -1};
-    const int m = (int)min((int64_t)4, num_tokens - t);
+    const int m = (int)min((int64_t)4, num_tokens - t); // at most 0: nothing for this lane
     if (!refused) {
-        int i = last_at_most(cu, n, (int)t0);
+        int i = last_at_most_warp(cu, n, (int)t0);
         int begin = cu[i], end = cu[i + 1];
         int row = -1, from = 0; // the row, and the position of its token `begin`
         for (int e = 0; e < m; ++e) {
@@ -420,7 +449,7 @@ __global__ void __launch_bounds__(kThreads)
     const int nt = team.threads(), me = team.thread(), bs = p.block_size;
     int4 refs[kIds / 4];
     plan_begin(team, p, refs);
-    const bool small = !kCluster && n <= kThreads;
+    const bool small = n <= kThreads;
     int32_t *starts = small ? sm.starts : w.starts, *lens = small ? sm.lens : w.lens;
     if (team.rank() == 0) {
         int want = 0, pieces = 0;
@@ -481,6 +510,8 @@ __global__ void __launch_bounds__(kThreads)
     team.sync();
     const int want = team.of_first(&sm.want);
     int bad = team.of_first(&sm.bad);
+    if (small)
+        team.rows_of_first(n);
     int32_t *list = !kCluster && want <= kSmallList ? sm.list : w.list;
     if (!bad && lowest_free(team, p, want, list, refs) < want)
         bad = 1;
@@ -597,7 +628,7 @@ __global__ void __launch_bounds__(kMoveThreads)
         return;
     const int64_t units = (int64_t)w.head[1] * planes;
     copy_pieces(q, units, [&](int64_t u) {
-        const int g = (int)(u / planes), i = last_at_most(w.cums, n, g);
+        const int g = (int)(u / planes), i = last_at_most_warp(w.cums, n, g);
         const int4 c = w.copies[i];
         return piece_of(q, (int)(u % planes), g - w.cums[i], c.x, c.y, c.z);
     });
