@@ -22,15 +22,19 @@ constexpr int32_t kTile = kPrefillKeyTile;
 // items out (measured on GB300, D = 128).  A pair (two query tiles on one K/V stream) occupies
 // both lanes of its CTA and is bound by the tensor core; a single occupies one lane, and two
 // lanes' loads share the SM's part of the HBM rate.  An item adds its query load and its
-// output.  The merge reads and writes every partial once.
-constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kPairItem = 2.5f, kSingleItem = 2.0f, kMergeBytesPerUs = 8.0e6f;
+// output.  A partial costs its bytes written and read again; the rate is what fits best the times
+// of 33 batches (1 to 200 sequences behind 512 to 16384 tokens, three head layouts, both caches)
+// with 22 lengths each: with it the length chosen is 3.5 % slower than the best one in the mean.
+constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kPairItem = 2.5f, kSingleItem = 2.0f, kMergeBytesPerUs = 3.0e6f;
 // What a call takes beyond that (set-up and merge), and what the decode kernels take for the contexts
 // whole, one part each: a start, a step of 64 keys after the other, or the bytes of all contexts
-// from L2 and HBM.  Measured (28 / 4 heads of 128): 2 x 84 tokens 4.5 us against 8.6 shared, 8 x 300
-// 6.4 against 9.0, 8 x 808 10.3 against 9.2; 128 x 300 14.1 against 17.4, 128 x 556 19.2 against
-// 17.5; INT8 8 x 300 7.5 against 14.4, 8 x 1068 16.0 against 15.0, 128 x 1068 28.0 against 23.5.
-constexpr float kSharedStart = 6.5f, kSharedStartInt8 = 11.f;
-constexpr float kDirectStart = 4.0f, kDirectKey = 0.0075f, kDirectKeyInt8 = 0.011f, kDirectBytesPerUs = 8.0e6f,
+// from L2 and HBM.  Fitted to 120 batches of 2 to 128 sequences of 84 to 1580 tokens; the choice is
+// 1 % slower than the better one in the mean.  Measured (28 / 4 heads of 128, direct against
+// shared): 8 x 300 6.7 and 8.9 us, 8 x 808 10.8 and 9.1, 128 x 300 14.3 and 17.4, 128 x 808 24.9 and
+// 18.8; INT8 8 x 300 8.1 and 11.4, 8 x 808 13.7 and 11.8, 128 x 300 12.6 and 17.3, 128 x 808 23.3
+// and 19.3.
+constexpr float kSharedStart = 5.5f, kSharedStartInt8 = 6.5f;
+constexpr float kDirectStart = 4.0f, kDirectKey = 0.0075f, kDirectKeyInt8 = 0.011f, kDirectBytesPerUs = 11.0e6f,
                 kDirectBytesPerUsInt8 = 6.5e6f;
 
 struct Run { // consecutive sequences of a group that share `shared` tokens
@@ -202,7 +206,8 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     int32_t per = split_tokens / kTile;
     float best = INFINITY; // the chosen ranges' time
     if (per == 0) {
-        static const int32_t kPer[] = {1, 2, 3, 4, 6, 8, 11, 16, 22, 32, 45, 64, 90, 128, 181, 256, 512, 1 << 24};
+        static const int32_t kPer[] = {1,  2,  3,  4,  5,  6,  7,  8,  9,  10,  11,  12,  13,  14,
+                                       16, 18, 20, 22, 26, 32, 45, 64, 90, 128, 181, 256, 512, 1 << 24};
         const float slot_us = (float)d.num_heads * d.head_dim * 8.f / kMergeBytesPerUs;
         for (int32_t c : kPer) {
             float pair_work = 0.f, single_work = 0.f, pair = 0.f, single = 0.f, slots = 0.f; // lane time, longest, slots
@@ -221,11 +226,11 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
                 slots += (float)s * range_seqs[i];
             }
             // pairs are dealt out first, in rounds over the CTAs; singles, longest first, fill up what the
-            // rounds leave uneven, and the lanes then end within about half a mean single of one another
+            // rounds leave uneven, and the lanes then end within about a quarter of a mean single of one another
             float t = std::max((float)((pairs + sms - 1) / sms) * pair, single);
             if (2 * pairs + singles > 2 * sms)
                 t = std::max(t, (pair_work + single_work) / (2 * sms) +
-                                    (singles ? 0.5f * single_work / (float)singles : 0.f));
+                                    (singles ? 0.25f * single_work / (float)singles : 0.f));
             t += slots * slot_us;
             if (t < best) {
                 best = t;
