@@ -139,7 +139,8 @@ typedef struct pa_shared_meta {
     int32_t num_scratch_tiles;  /* 128-key tiles of the groups' shared parts (INT8) */
     int32_t direct;             /* bit 0 (bf16), bit 1 (INT8): contexts so short that they are
                                    decoded whole, without sharing (never with a given split) */
-    int32_t reserved;
+    int32_t apart;              /* 1: items has those of several sequences only; the parts of single
+                                   sequences run in the decode kernels (INT8: always) */
     uint64_t tokens_saved;       /* keys the groups read once instead of once per sequence */
     uint64_t off_block_tables;   /* int32 [num_seqs][max_blocks_per_seq], -1 padded (tables_packed) */
     uint64_t off_slot_mapping;   /* int32 [num_seqs] slot of each last token (tables_packed) */
@@ -394,13 +395,15 @@ int pa_decode_fused(const pa_dims *dims, const void *q, const void *k, const voi
  * pa_decode_shared — pa_decode for a batch whose sequences share prefixes: the
  * same result, with each shared block read once per group and not once per
  * sequence.  Sources as pa_pack_decode_shared; merge as pa_decode.  One
- * persistent tcgen05 launch for all parts and, if some context has several,
- * one merge launch.  The K/V of every key must already be stored.
+ * persistent tcgen05 launch for all parts, or for those of several sequences
+ * with the others beside it as pa_decode computes them, and, if some context
+ * has several parts, one merge launch.  The K/V of every key must already be
+ * stored.
  *   q, out:        device bf16 [meta->num_seqs][num_heads][head_dim]
  *   block_tables:  device int32, row pitch meta->max_blocks_per_seq: the plan's
  *                  (dev + meta->off_block_tables) or the caller's
- *   items, cta_items, seq_parts, direct_items, table_rows: device copies of the
- *                  plan's arrays
+ *   items, cta_items, seq_parts, direct_items, table_rows, single_items: device
+ *                  copies of the plan's arrays
  *   workspace:     device memory of at least meta->workspace_bytes (may be NULL
  *                  when that is 0), 256-byte aligned; calls in flight at once
  *                  need separate workspaces
@@ -412,8 +415,8 @@ int pa_decode_fused(const pa_dims *dims, const void *q, const void *k, const voi
 int pa_decode_shared(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                      const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
                      const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts,
-                     const int32_t *direct_items, const int32_t *table_rows, void *workspace, size_t workspace_bytes,
-                     pa_stream_t stream);
+                     const int32_t *direct_items, const int32_t *table_rows, const int32_t *single_items,
+                     void *workspace, size_t workspace_bytes, pa_stream_t stream);
 
 /*
  * pa_copy_blocks — copy-on-write of shared cache blocks.  Source: "vLLM /
@@ -636,7 +639,7 @@ int pa_decode_int8_fused(const pa_dims *dims, const void *q, const void *k, cons
  * fp16 in the workspace (rounded to nearest even, clamped to +-65504); their
  * products run on those with fp32 accumulation.  The parts of single sequences
  * are computed as pa_decode_int8 computes them.
- *   single_items, scratch_tiles: device copies of the plan's arrays
+ *   scratch_tiles: device copy of the plan's array
  *   workspace:  at least meta->workspace_bytes_int8
  */
 int pa_decode_shared_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,

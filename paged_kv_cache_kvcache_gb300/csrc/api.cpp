@@ -439,8 +439,8 @@ extern "C" int pa_decode_int8(const pa_dims *dims, const void *q, const void *k_
 static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                           const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
                           const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts,
-                          const int32_t *direct_items, const int32_t *table_rows, void *workspace,
-                          size_t workspace_bytes, SharedArgs *a, bool *nothing)
+                          const int32_t *direct_items, const int32_t *table_rows, const int32_t *single_items,
+                          void *workspace, size_t workspace_bytes, SharedArgs *a, bool *nothing)
 {
     *nothing = false;
     int rc = check_dims(dims);
@@ -461,17 +461,18 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
     if (meta->rows_per_tile != (kPrefillRows / group > 0 ? kPrefillRows / group : 1))
         return fail(PA_ERR_INVALID_ARG, "%s: meta was packed for other dims", fn);
     if (!q || !k_cache || !v_cache || !block_tables || !out || !items || !cta_items || !seq_parts ||
-        !direct_items || !table_rows)
+        !direct_items || !table_rows || !single_items)
         return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
     if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(out) || misaligned(items) ||
-        misaligned(direct_items))
+        misaligned(direct_items) || misaligned(single_items))
         return fail(PA_ERR_INVALID_ARG, "%s: tensors and items must be 16-byte aligned", fn);
     if ((reinterpret_cast<uintptr_t>(seq_parts) & 7u) || misaligned(cta_items) ||
         (reinterpret_cast<uintptr_t>(block_tables) & 3u) || (reinterpret_cast<uintptr_t>(table_rows) & 3u))
         return fail(PA_ERR_INVALID_ARG, "%s: misaligned plan array or block table", fn);
     if (meta->num_items > 0 && dims->num_blocks == 0)
         return fail(PA_ERR_INVALID_ARG, "empty KV pool");
-    if (meta->num_scratch_tiles < 0)
+    if (meta->num_scratch_tiles < 0 || meta->num_single_items < 0 || meta->num_shared_items < 0 ||
+        meta->num_shared_items > meta->num_items)
         return fail(PA_ERR_INVALID_ARG, "malformed shared decode meta");
     const bool direct = (meta->direct & (int8 ? 2 : 1)) != 0;
     const size_t part_bytes = shared_part_bytes(*dims, meta->num_partials);
@@ -506,7 +507,11 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
     a->num_scratch_tiles = meta->num_scratch_tiles;
     a->scale = scale;
     a->num_seqs = meta->num_seqs;
-    a->num_items = meta->num_items;
+    // parts of single sequences: in the CTAs' lists, or apart in the decode kernels
+    const bool apart = int8 || meta->apart != 0;
+    a->single_items = single_items;
+    a->num_items = apart ? meta->num_shared_items : meta->num_items;
+    a->num_single_items = apart ? meta->num_single_items : 0;
     a->num_ctas = meta->num_ctas;
     a->rows_per_tile = meta->rows_per_tile;
     a->max_blocks_per_seq = meta->max_blocks_per_seq;
@@ -518,13 +523,14 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
 extern "C" int pa_decode_shared(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                                 const int32_t *block_tables, float scale, void *out, const pa_shared_meta *meta,
                                 const int32_t *items, const int32_t *cta_items, const int32_t *seq_parts,
-                                const int32_t *direct_items, const int32_t *table_rows, void *workspace,
-                                size_t workspace_bytes, pa_stream_t stream)
+                                const int32_t *direct_items, const int32_t *table_rows, const int32_t *single_items,
+                                void *workspace, size_t workspace_bytes, pa_stream_t stream)
 {
     SharedArgs a;
     bool nothing = false;
     int rc = prepare_shared("pa_decode_shared", false, dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
-                            cta_items, seq_parts, direct_items, table_rows, workspace, workspace_bytes, &a, &nothing);
+                            cta_items, seq_parts, direct_items, table_rows, single_items, workspace, workspace_bytes, &a,
+                            &nothing);
     if (rc != PA_OK || nothing)
         return rc;
     return launch_decode_shared(a, stream);
@@ -541,21 +547,17 @@ extern "C" int pa_decode_shared_int8(const pa_dims *dims, const void *q, const v
     SharedArgs a;
     bool nothing = false;
     int rc = prepare_shared("pa_decode_shared_int8", true, dims, q, k_cache, v_cache, block_tables, scale, out, meta, items,
-                            cta_items, seq_parts, direct_items, table_rows, workspace, workspace_bytes, &a, &nothing);
+                            cta_items, seq_parts, direct_items, table_rows, single_items, workspace, workspace_bytes, &a,
+                            &nothing);
     if (rc != PA_OK || nothing)
         return rc;
-    if (meta->num_single_items < 0 || meta->num_shared_items < 0 || meta->num_shared_items > meta->num_items)
-        return fail(PA_ERR_INVALID_ARG, "malformed shared decode meta");
-    if (!k_scale || !v_scale || !single_items || !scratch_tiles)
+    if (!k_scale || !v_scale || !scratch_tiles)
         return fail(PA_ERR_INVALID_ARG, "pa_decode_shared_int8: NULL pointer");
-    if (misaligned(k_scale) || misaligned(v_scale) || misaligned(single_items) || misaligned(scratch_tiles))
+    if (misaligned(k_scale) || misaligned(v_scale) || misaligned(scratch_tiles))
         return fail(PA_ERR_INVALID_ARG, "pa_decode_shared_int8: scales and items must be 16-byte aligned");
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    a.single_items = single_items;
     a.scratch_tiles = scratch_tiles;
-    a.num_items = meta->num_shared_items;
-    a.num_single_items = meta->num_single_items;
     return launch_decode_shared(a, stream);
 }
 

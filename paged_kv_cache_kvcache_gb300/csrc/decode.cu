@@ -86,8 +86,10 @@ __device__ uint32_t g_fused_error;
 // being decoded) writes that token's K/V rows into the cache slot and takes
 // its key from the input instead of the cache, so store and attention need
 // no ordering between launches.
-// SHARED: the items are short contexts of a shared-prefix decode.  Their table may be the
-// caller's: a block id outside the pool reads as zeros and sets bit 1 of g_fused_error.
+// SHARED: the items are short contexts of a shared-prefix decode, or its parts of single sequences.
+// Their table may be the caller's: a block id outside the pool reads as zeros and sets bit 1 of
+// g_fused_error.  The launch may run beside the one before it (the shared parts); its last block
+// ends after that one.
 template <int D, int NT, bool FUSED, bool SHARED>
 __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecParams p)
 {
@@ -348,6 +350,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecP
                 p.part_lse[(size_t)pslot * Hq + h] = Lsum > 0.f ? M + __log2f(Lsum) : -INFINITY;
         }
     }
+    if constexpr (SHARED) {
+        if (blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
+            ptx::grid_dependency_wait();
+    }
 }
 
 // out[b][h] = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M), over the splits of sequence b.
@@ -415,11 +421,29 @@ int launch_split(const DecodeArgs &a, const DecParams &p, cudaStream_t stream)
     // flat grid, heads of one work item adjacent: they read neighbouring
     // segments of the same token rows at about the same time (DRAM locality)
     dim3 grid((unsigned)(a.num_items * a.dims.num_kv_heads));
+    if constexpr (SHARED) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kWarps * 32);
+        cfg.dynamicSmemBytes = DecLayout<D>::kSmemBytes;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = a.beside ? 1 : 0;
+        cudaError_t e = cudaLaunchKernelEx(&cfg, decode_split_kernel<D, NT, FUSED, SHARED>, p);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
+        }
+        return PA_OK;
+    }
     decode_split_kernel<D, NT, FUSED, SHARED><<<grid, kWarps * 32, DecLayout<D>::kSmemBytes, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
-    return SHARED ? PA_OK : launch_decode_combine(a, stream);
+    return launch_decode_combine(a, stream);
 }
 
 template <int D, int NT>

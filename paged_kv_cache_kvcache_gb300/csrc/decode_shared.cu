@@ -23,10 +23,11 @@
 //    by the tensor core (measured 1.75 us per 128 keys);
 //  * every other part is a SINGLE: one tile, 128 keys whose products take about 1100 cycles of the
 //    tensor core while their 64 KB of K/V take about 2800 cycles of this SM's share of HBM.  But
-//    score product, softmax and value product of one tile follow one another (about 2300 cycles
+//    score product, softmax and value product of one tile follow one another (about 2700 cycles
 //    with their hand-offs), so the two tiles are two LANES, each walking singles of its own, one's
 //    products under the other's softmax and loads.  Most of a single's rows are padding; warps
-//    without a valid row skip the softmax.
+//    without a valid row skip the softmax.  Where there are more items than lanes, the parts of
+//    single sequences run apart, in the decode kernels, in a launch that may run beside this one.
 // The host cuts the key ranges and deals pairs to CTAs and singles to lanes (longest first onto
 // the least loaded).  Structure of a CTA as in the prefill kernel: K, V and query producers
 // (TMA, one 3-D box per physical block), one MMA warp (tcgen05, S and O in tensor memory, P fed
@@ -36,8 +37,8 @@
 // tiles and heads: keys and values (code * scale, rounded by 2^-12 at most; fp16 holds them to
 // 65504) and the queries.  The products then run as on a bf16 cache, with fp16 weights.  (Exact
 // codes with the scales in the softmax took 3.4 us per 128 keys and pair instead of 1.6: 64 more
-// 16-byte loads per row; converting in shared memory took 4.2.)  Parts of single sequences go to
-// the INT8 decode kernel, in a launch that may run beside the products.
+// 16-byte loads per row; converting in shared memory took 4.2.)  Parts of single sequences always
+// run apart.
 //
 // Short contexts (the plan decides, see pack_shared.cpp) gain nothing from sharing: they go whole
 // through the decode kernels, which start in half the time and have nothing to merge.
@@ -1011,10 +1012,10 @@ int launch_codes(const SharedArgs &a, cudaStream_t stream)
     return PA_OK;
 }
 
-// Items (sequence, key range, partial slot) of single sequences through the decode kernels.  On an
-// INT8 cache, `beside`, they may run beside the shared parts' products.  (Beside the conversion
-// instead, with the products after both, 64 x 16384 took 75 us, not 50: these parts are long and
-// few, and the products waited for them.)
+// Items (sequence, key range, partial slot) of single sequences through the decode kernels;
+// `beside`: while the shared parts' products still run, on the SMs that those leave.  (INT8, beside
+// the conversion instead, with the products after both: 64 x 16384 took 75 us, not 50; these parts
+// are long and few, and the products waited for them.)
 int launch_singles(const SharedArgs &a, const int32_t *items, int32_t num_items, bool beside, cudaStream_t stream)
 {
     DecodeArgs s{};
@@ -1114,7 +1115,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
             return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
         }
     }
-    if (kInt8 && a.num_single_items > 0)
+    if (a.num_single_items > 0)
         if (int rc = launch_singles(a, a.single_items, a.num_single_items, a.num_items > 0, stream))
             return rc;
     if (!a.merge)
@@ -1135,7 +1136,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = a.num_items + (kInt8 ? a.num_single_items : 0) > 0 ? 1 : 0;
+    cfg.numAttrs = a.num_items + a.num_single_items > 0 ? 1 : 0;
     auto combine = split == 1 ? shared_combine_kernel<D, 1> : split == 4 ? shared_combine_kernel<D, 4> : shared_combine_kernel<D, 8>;
     const cudaError_t e =
         cudaLaunchKernelEx(&cfg, combine, (const float *)a.part_o, (const float *)a.part_lse,

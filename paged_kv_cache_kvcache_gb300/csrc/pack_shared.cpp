@@ -18,14 +18,24 @@ namespace {
 
 constexpr int32_t kTile = kPrefillKeyTile;
 
-// Time model of the kernel in microseconds, used only to choose the key ranges and to deal the
-// items out (measured on GB300, D = 128).  A pair (two query tiles on one K/V stream) occupies
-// both lanes of its CTA and is bound by the tensor core; a single occupies one lane, and two
-// lanes' loads share the SM's part of the HBM rate.  An item adds its query load and its
-// output.  A partial costs its bytes written and read again; the rate is what fits best the times
-// of 33 batches (1 to 200 sequences behind 512 to 16384 tokens, three head layouts, both caches)
-// with 22 lengths each: with it the length chosen is 3.5 % slower than the best one in the mean.
-constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kPairItem = 2.5f, kSingleItem = 2.0f, kMergeBytesPerUs = 3.0e6f;
+// Time model in microseconds, used only to choose the key ranges and to deal the items out
+// (measured on GB300, D = 128).  A pair (two query tiles on one K/V stream) occupies both lanes of
+// its CTA and is bound by the tensor core.  A single occupies one lane; alone in its CTA its step
+// takes kSharedStep, beside another's kSingleStep.  An item adds its query load and its output.  A
+// partial costs its bytes written and read again.
+//
+// The parts of single sequences run in the lanes' lists too where every item has a lane of its own
+// (4 x 2148 tokens 9.5 us, 8 x 16500 17.0); where there are more items they run apart, in the decode
+// kernels on the SMs that the shared parts leave (10.3 and 17.8 us there, but 64 x 4600 20.8 us
+// instead of 28.4, 200 x 16600 63.8 instead of 66.7, and 24 ragged groups 69 instead of 82): several
+// of their CTAs on an SM hide one another's latency, where a CTA of ours has two lanes.
+// The rates are those that fit best the times of 33 batches (1 to 200 sequences behind 512 to 16384
+// tokens, three head layouts, both caches, 22 lengths of the parts): the length chosen is 3 %
+// slower than the best one in the mean.
+constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kSharedStep = 1.9f, kPairItem = 2.5f, kSingleItem = 2.0f,
+                kMergeBytesPerUs = 3.0e6f;
+constexpr float kBytesPerUs = 6.9e6f, kSmBytesPerUs = 0.08e6f; // the decode kernels', all SMs and one
+constexpr float kApartStart = 1.f, kApartTail = 2.f, kApartKey = 0.006f;
 // What a call takes beyond that (set-up and merge), and what the decode kernels take for the contexts
 // whole, one part each: a start, a step of 64 keys after the other, or the bytes of all contexts
 // from L2 and HBM.  Fitted to 120 batches of 2 to 128 sequences of 84 to 1580 tokens; the choice is
@@ -33,7 +43,7 @@ constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kPairItem = 2.5f, kSingle
 // shared): 8 x 300 6.7 and 8.9 us, 8 x 808 10.8 and 9.1, 128 x 300 14.3 and 17.4, 128 x 808 24.9 and
 // 18.8; INT8 8 x 300 8.1 and 11.4, 8 x 808 13.7 and 11.8, 128 x 300 12.6 and 17.3, 128 x 808 23.3
 // and 19.3.
-constexpr float kSharedStart = 5.5f, kSharedStartInt8 = 6.5f;
+constexpr float kSharedStart = 5.0f, kSharedStartInt8 = 6.0f;
 constexpr float kDirectStart = 4.0f, kDirectKey = 0.0075f, kDirectKeyInt8 = 0.011f, kDirectBytesPerUs = 11.0e6f,
                 kDirectBytesPerUsInt8 = 6.5e6f;
 
@@ -42,8 +52,8 @@ struct Run { // consecutive sequences of a group that share `shared` tokens
     int32_t scratch; // row of key 0 in the INT8 decode's scratch cache
 };
 
-struct Range { // one part of a context: units items per split
-    int32_t tiles, units_pair, units_single;
+struct Range { // one part of `seqs` contexts: units items per split
+    int32_t keys, units_pair, units_single, seqs;
 };
 
 float item_cost(int32_t tiles, bool pair)
@@ -189,49 +199,66 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     cudaGetLastError();
     std::vector<Range> ranges;
-    std::vector<int32_t> range_seqs; // sequences that get a slot per split of the range
     for (const Run &r : runs) {
         if (r.shared > 0) {
             const int32_t pairs = r.n / (2 * P), rest = r.n % (2 * P);
-            ranges.push_back({(r.shared + kTile - 1) / kTile, (pairs + (rest > P)) * d.num_kv_heads,
-                              (rest > 0 && rest <= P ? 1 : 0) * d.num_kv_heads});
-            range_seqs.push_back(r.n);
+            ranges.push_back({r.shared, (pairs + (rest > P)) * d.num_kv_heads,
+                              (rest > 0 && rest <= P ? 1 : 0) * d.num_kv_heads, r.n});
         }
         for (int32_t b = r.s0; b < r.s0 + r.n; ++b)
-            if (context_lens[b] > r.shared) {
-                ranges.push_back({(context_lens[b] - r.shared + kTile - 1) / kTile, 0, d.num_kv_heads});
-                range_seqs.push_back(1);
-            }
+            if (context_lens[b] > r.shared)
+                ranges.push_back({context_lens[b] - r.shared, 0, d.num_kv_heads, 1});
     }
+    const float key_bytes = (float)d.num_kv_heads * d.head_dim * 4;
+    const float slot_us = (float)d.num_heads * d.head_dim * 8.f / kMergeBytesPerUs;
+    bool apart = false;
+    // parts of c key tiles at most: the time, and whether the parts of single sequences run apart
+    auto estimate = [&](int32_t c) -> float {
+        float pair = 0.f, shared = 0.f, one = 0.f, work = 0.f; // longest items, CTA time of the shared parts
+        float bytes = 0.f, one_bytes = 0.f, slots = 0.f, longest = 0.f;
+        int64_t pairs = 0, singles = 0, ones = 0;
+        for (const Range &x : ranges) {
+            const int32_t tiles = splits_of(x.keys, kTile), s = splits_of(tiles, c), len = splits_of(tiles, s);
+            slots += (float)s * x.seqs;
+            if (x.seqs == 1) {
+                ones += (int64_t)s * x.units_single;
+                one = std::max(one, item_cost(len, false));
+                one_bytes += x.keys * key_bytes;
+                longest = std::max(longest, (float)std::min(len * kTile, x.keys));
+                continue;
+            }
+            pairs += (int64_t)s * x.units_pair;
+            singles += (int64_t)s * x.units_single;
+            if (x.units_pair)
+                pair = std::max(pair, item_cost(len, true));
+            if (x.units_single)
+                shared = std::max(shared, len * kSharedStep + kSingleItem);
+            work += x.units_pair * (tiles * kPairStep + s * kPairItem) + x.units_single * (tiles * kSharedStep + s * kSingleItem);
+            bytes += x.units_pair > d.num_kv_heads ? 0.f : x.keys * key_bytes;
+        }
+        const float merge = slots * slot_us;
+        apart = 2 * pairs + singles + ones > 2 * (int64_t)sms;
+        if (!apart)
+            return std::max(std::max(pair, shared * (kSingleStep / kSharedStep)), one) + merge;
+        // the shared parts in equal rounds over as few CTAs as that takes; on the SMs left and, after
+        // them, on all, those of single sequences
+        const int64_t units = pairs + singles, rounds = (units + sms - 1) / sms;
+        const int64_t ctas = units ? (units + rounds - 1) / rounds : 0;
+        float t = std::max(pair, shared);
+        if (rounds > 1)
+            t = std::max(t, work / (float)ctas + 0.25f * work / (float)units);
+        const float left = std::max(0.f, one_bytes - t * std::min(kBytesPerUs, (float)(sms - ctas) * kSmBytesPerUs));
+        t += left > 0.f ? left / kBytesPerUs + kApartTail : 0.f;
+        t = std::max(t, kApartTail + kApartKey * longest);
+        return std::max(t, (bytes + one_bytes) / kBytesPerUs) + kApartStart + merge;
+    };
     int32_t per = split_tokens / kTile;
     float best = INFINITY; // the chosen ranges' time
     if (per == 0) {
         static const int32_t kPer[] = {1,  2,  3,  4,  5,  6,  7,  8,  9,  10,  11,  12,  13,  14,
                                        16, 18, 20, 22, 26, 32, 45, 64, 90, 128, 181, 256, 512, 1 << 24};
-        const float slot_us = (float)d.num_heads * d.head_dim * 8.f / kMergeBytesPerUs;
         for (int32_t c : kPer) {
-            float pair_work = 0.f, single_work = 0.f, pair = 0.f, single = 0.f, slots = 0.f; // lane time, longest, slots
-            int64_t pairs = 0, singles = 0;
-            for (size_t i = 0; i < ranges.size(); ++i) {
-                const Range &x = ranges[i];
-                const int32_t s = splits_of(x.tiles, c), len = splits_of(x.tiles, s);
-                if (x.units_pair)
-                    pair = std::max(pair, item_cost(len, true));
-                if (x.units_single)
-                    single = std::max(single, item_cost(len, false));
-                pair_work += 2 * x.units_pair * (x.tiles * kPairStep + s * kPairItem);
-                single_work += x.units_single * (x.tiles * kSingleStep + s * kSingleItem);
-                pairs += (int64_t)s * x.units_pair;
-                singles += (int64_t)s * x.units_single;
-                slots += (float)s * range_seqs[i];
-            }
-            // pairs are dealt out first, in rounds over the CTAs; singles, longest first, fill up what the
-            // rounds leave uneven, and the lanes then end within about a quarter of a mean single of one another
-            float t = std::max((float)((pairs + sms - 1) / sms) * pair, single);
-            if (2 * pairs + singles > 2 * sms)
-                t = std::max(t, (pair_work + single_work) / (2 * sms) +
-                                    (singles ? 0.25f * single_work / (float)singles : 0.f));
-            t += slots * slot_us;
+            const float t = estimate(c);
             if (t < best) {
                 best = t;
                 per = c;
@@ -239,6 +266,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         }
         per = std::max(per, 1);
     }
+    estimate(per); // (apart)
 
     int64_t all_keys = 0;
     for (int32_t b = 0; b < num_seqs; ++b)
@@ -303,14 +331,18 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         singles += w.n == 1 && w.g == 0;
         shared_items += w.n > 1;
     }
-    const int32_t ctas = (int32_t)std::min<size_t>(works.size(), (size_t)sms);
+    // apart: the CTAs' lists hold the parts of several sequences only, on the CTAs of their rounds
+    const int32_t listed = apart ? shared_items : (int32_t)works.size();
+    const int32_t rounds = apart ? (listed + sms - 1) / sms : 1;
+    const int32_t ctas = rounds > 0 ? std::min(sms, (listed + rounds - 1) / rounds) : 0;
 
     Layout L;
     *meta = pa_shared_meta{};
     meta->num_seqs = num_seqs;
     meta->num_groups = num_groups;
     meta->max_blocks_per_seq = mb;
-    meta->num_items = (int32_t)works.size();
+    meta->num_items = listed;
+    meta->apart = apart ? 1 : 0;
     meta->num_ctas = ctas;
     meta->num_partials = (int32_t)partials;
     meta->max_parts = max_parts;
@@ -326,7 +358,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         meta->tokens_saved += (uint64_t)r.shared * (uint64_t)(r.n - 1);
     meta->off_block_tables = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs * mb : 0);
     meta->off_slot_mapping = L.take(packed ? sizeof(int32_t) * (size_t)num_seqs : 0);
-    meta->off_items = L.take(sizeof(int32_t) * kSharedItemInts * works.size());
+    meta->off_items = L.take(sizeof(int32_t) * kSharedItemInts * (size_t)listed);
     meta->off_cta_items = L.take(sizeof(int32_t) * kSharedCtaInts * (size_t)ctas);
     meta->off_seq_parts = L.take(sizeof(int32_t) * 2 * (size_t)num_seqs);
     meta->off_single_items = L.take(sizeof(int32_t) * 4 * (size_t)singles);
@@ -411,7 +443,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     heap = {};
     for (int32_t c = 0; c < 2 * ctas; ++c) // first lanes before second ones
         heap.push({load[c % ctas], c});
-    for (; at < order.size(); ++at) {
+    for (; at < (size_t)listed; ++at) {
         Load l = heap.top();
         heap.pop();
         const int32_t q = 3 * (l.second % ctas) + 1 + l.second / ctas;
@@ -440,6 +472,8 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
             one[3] = parts[w.s0] > 1 ? sp[2 * w.s0] + w.part : -1;
             one += 4;
         }
+        if (apart && w.n == 1)
+            continue;
         int32_t *e = it + (size_t)kSharedItemInts * next[queue_of[i]]++;
         e[0] = w.s0;
         e[1] = w.n;

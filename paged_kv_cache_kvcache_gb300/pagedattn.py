@@ -64,7 +64,7 @@ class pa_shared_meta(ctypes.Structure):
                 ("max_parts", ctypes.c_int32), ("rows_per_tile", ctypes.c_int32), ("merge", ctypes.c_int32),
                 ("split_tokens", ctypes.c_int32), ("tables_packed", ctypes.c_int32),
                 ("num_single_items", ctypes.c_int32), ("num_shared_items", ctypes.c_int32),
-                ("num_scratch_tiles", ctypes.c_int32), ("direct", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("num_scratch_tiles", ctypes.c_int32), ("direct", ctypes.c_int32), ("apart", ctypes.c_int32),
                 ("tokens_saved", ctypes.c_uint64), ("off_block_tables", ctypes.c_uint64),
                 ("off_slot_mapping", ctypes.c_uint64), ("off_items", ctypes.c_uint64),
                 ("off_cta_items", ctypes.c_uint64), ("off_seq_parts", ctypes.c_uint64),
@@ -123,7 +123,7 @@ def lib() -> ctypes.CDLL:
             L.pa_prefill_varlen_int8.argtypes = [P] * 11 + [ctypes.c_float] + [P] * 4 + [SZ, P]
             L.pa_prefill_varlen_int8_fused.argtypes = [P] * 14 + [ctypes.c_float] + [P] * 4 + [SZ, P]
             L.pa_pack_decode_shared.argtypes = [P, I32, P, I32, P, P, P, P, P, I32, I32, P, SZ, P]
-            L.pa_decode_shared.argtypes = [P] * 5 + [ctypes.c_float] + [P] * 8 + [SZ, P]
+            L.pa_decode_shared.argtypes = [P] * 5 + [ctypes.c_float] + [P] * 9 + [SZ, P]
             L.pa_decode_shared_int8.argtypes = [P] * 7 + [ctypes.c_float] + [P] * 10 + [SZ, P]
             L.pa_pool_workspace.argtypes = [P, P, P]
             L.pa_pool_append.argtypes = [P, P, P, P, I32, P, I32, P, SZ, P]
@@ -262,8 +262,8 @@ class SharedPlan(_Plan):
         self.call_ref = ctypes.byref(m)
         self.call_tables = base + m.off_block_tables if m.tables_packed or m.num_seqs == 0 else None
         self.call_arrays = tuple(base + x for x in (m.off_items, m.off_cta_items, m.off_seq_parts, m.off_direct_items,
-                                                   m.off_table_rows))
-        self.call_singles = (base + m.off_single_items, base + m.off_scratch_tiles)
+                                                   m.off_table_rows, m.off_single_items))
+        self.call_tiles = base + m.off_scratch_tiles
         return self
 
     @property
@@ -472,7 +472,7 @@ def pa_decode_shared_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, 
     _here(q, k_cache, v_cache, k_scale, v_scale, out, workspace, block_tables, plan.dev)
     _check((_lib or lib()).pa_decode_shared_int8(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
                                        _ptr(v_scale), bt, scale, _ptr(out), plan.call_ref, *plan.call_arrays,
-                                       *plan.call_singles, _ptr(workspace), _nbytes(workspace), _stream(stream)),
+                                       plan.call_tiles, _ptr(workspace), _nbytes(workspace), _stream(stream)),
            "pa_decode_shared_int8")
 
 

@@ -77,7 +77,16 @@ def test_parts_cover_every_key_once(case):
     shared_reads = 0
     tiles = {tuple(x) for x in plan.host_array(m.off_scratch_tiles, 4 * m.num_scratch_tiles).reshape(-1, 4).tolist()}
     assert len({x[3] for x in tiles}) == m.num_scratch_tiles and all(x[3] % 128 == 0 and x[1] < x[2] for x in tiles)
-    for s0, n, g, row, k0, k1, part, scratch in items.tolist():
+    # the parts of single sequences, per (sequence, range) with their slots: instead of those in the CTAs' lists where
+    # they run apart, beside them (for an INT8 cache) elsewhere
+    ones = plan.host_array(m.off_single_items, 4 * m.num_single_items).reshape(-1, 4).tolist()
+    everything = items.tolist()
+    if m.apart:
+        assert all(x[1] > 1 for x in everything)
+        everything += [[b, 1, g, b, k0, k1, max(slot - parts[b, 0], 0) if slot >= 0 else 0, 0]
+                       for b, k0, k1, slot in ones for g in range(hkv)]
+        assert all((slot >= 0) == (parts[b, 1] > 1) for b, _, _, slot in ones)
+    for s0, n, g, row, k0, k1, part, scratch in everything:
         if n > 1:  # every key tile of a shared part is in the scratch cache, at the item's row
             for k in range(k0, k1, 128):
                 x, = [x for x in tiles if x[1] == k and x[3] == scratch + k]
@@ -93,10 +102,8 @@ def test_parts_cover_every_key_once(case):
         shared_reads += (n - 1) * (k1 - k0) if g == 0 else 0
     for b in range(B):
         assert (seen[b] == 1).all()
-    # the parts of single sequences, once more per (sequence, range) with their slots
-    ones = plan.host_array(m.off_single_items, 4 * m.num_single_items).reshape(-1, 4).tolist()
     want = {(s0, k0, k1, parts[s0, 0] + part if parts[s0, 1] > 1 else -1)
-            for s0, n, g, _, k0, k1, part, _ in items.tolist() if n == 1}
+            for s0, n, g, _, k0, k1, part, _ in everything if n == 1}
     assert len(ones) == len(want) and set(map(tuple, ones)) == want
     assert m.num_shared_items == sum(i[1] > 1 for i in items.tolist())
     assert plan.host_array(m.off_table_rows, B).tolist() == list(range(B))
@@ -118,12 +125,13 @@ def test_parts_cover_every_key_once(case):
 
 
 def test_items_are_dealt_out_evenly():
-    """No lane gets more than one item's worth of time above the mean."""
+    """No lane gets more than one item's worth of time above the mean; more items than lanes run in two launches."""
     ctx, lists, groups, nb = make_batch(2, [64], [40], [5 + 11 * i for i in range(64)], 64)
     dims = pa.make_dims(nb, 64, 28, 4, 128)
     plan = pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=256, pin=False)
     items, cta, _ = arrays(plan)
-    cost = [(1.62 if n > 18 else 2.4) * -(-(k1 - k0) // 128) + (2.5 if n > 18 else 1.0) for _, n, _, _, k0, k1, _, _ in items.tolist()]
+    assert plan.meta.apart and len(items) == plan.meta.num_shared_items
+    cost = [(1.62 if n > 18 else 2.4) * -(-(k1 - k0) // 128) + (2.5 if n > 18 else 2.0) for _, n, _, _, k0, k1, _, _ in items.tolist()]
     load = [sum(cost[p:l0]) + sum(cost[a:b]) for p, l0, l1, end in cta.tolist() for a, b in ((l0, l1), (l1, end))]
     assert max(load) <= sum(load) / len(load) + max(cost)
 
@@ -206,9 +214,9 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     m = pa.pa_shared_meta()
     L = pa.lib()
 
-    def call(scale=0.1, q=16, out=16, ws=None, nbytes=0, bt=16, items=16, whole=16, rows=16, dims=dims):
+    def call(scale=0.1, q=16, out=16, ws=None, nbytes=0, bt=16, items=16, whole=16, rows=16, ones=16, dims=dims):
         return L.pa_decode_shared(ctypes.byref(dims), q, 16, 16, bt, ctypes.c_float(scale), out, ctypes.byref(m), items,
-                                  16, 16, whole, rows, ws, nbytes, None)
+                                  16, 16, whole, rows, ones, ws, nbytes, None)
 
     m.num_seqs, m.num_items, m.num_ctas, m.max_blocks_per_seq, m.rows_per_tile = 0, 0, 0, 1, 64
     assert call() == pa.PA_OK                                   # nothing to do
@@ -218,7 +226,7 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     assert call(q=None) == pa.PA_ERR_INVALID_ARG
     assert call(out=8) == pa.PA_ERR_INVALID_ARG
     assert call(items=24) == pa.PA_ERR_INVALID_ARG
-    assert call(bt=None) == call(whole=None) == call(whole=8) == call(rows=None) == call(rows=18) == pa.PA_ERR_INVALID_ARG
+    assert call(bt=None) == call(whole=None) == call(whole=8) == call(rows=None) == call(rows=18) == call(ones=None) == call(ones=8) == pa.PA_ERR_INVALID_ARG
     assert call(dims=pa.make_dims(8, 16, 8, 2, 64)) == pa.PA_ERR_INVALID_ARG   # packed for group 2
     assert call(dims=pa.make_dims(0, 16, 4, 2, 64)) == pa.PA_ERR_INVALID_ARG   # empty pool
     m.num_partials, m.workspace_bytes, m.workspace_bytes_int8 = 3, 1024 * 3 + 256, 1024 * 3 + 256
