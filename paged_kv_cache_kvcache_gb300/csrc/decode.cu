@@ -38,16 +38,17 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kFewWarps = 8; // of a shared-prefix decode's few items, each with an SM to itself
 constexpr int kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D>
+template <int D, int W = kWarps>
 struct DecLayout {
     static constexpr int kRowBytes = D * 2;             // one head row of one token
     static constexpr int kChunkBytes = 16 * kRowBytes;  // 16 tokens of K (or V)
     static constexpr int kStageBytes = 2 * kChunkBytes; // K + V
     static constexpr int kWarpBytes = kStages * kStageBytes;
-    static constexpr int kSmemBytes = kWarps * kWarpBytes;
+    static constexpr int kSmemBytes = W * kWarpBytes;
     static constexpr int kVecPerRow = D / 8;            // 16-byte vectors per row
 };
 
@@ -90,10 +91,10 @@ __device__ uint32_t g_fused_error;
 // Their table may be the caller's: a block id outside the pool reads as zeros and sets bit 1 of
 // g_fused_error.  The launch may run beside the one before it (the shared parts); its last block
 // ends after that one.
-template <int D, int NT, bool FUSED, bool SHARED>
-__global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecParams p)
+template <int D, int NT, bool FUSED, bool SHARED, int W>
+__global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1) decode_split_kernel(const DecParams p)
 {
-    using L = DecLayout<D>;
+    using L = DecLayout<D, W>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -122,7 +123,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecP
     }
 
     const int nchunks = (k1 - k0 + 15) >> 4;
-    const int my_n = nchunks > warp ? (nchunks - warp + kWarps - 1) / kWarps : 0;
+    const int my_n = nchunks > warp ? (nchunks - warp + W - 1) / W : 0;
     const uint32_t wbase = ptx::smem_u32(smem) + warp * L::kWarpBytes;
     const int32_t *bt_row = p.block_tables + (size_t)(SHARED ? __ldg(p.table_rows + b) : b) * p.max_blocks;
     const int bs = p.block_size;
@@ -131,11 +132,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecP
 
     auto issue = [&](int i) {
         if ((i & 31) == 0) { // refresh the block ids of local chunks i .. i+31, one per lane
-            const int key = k0 + 16 * (warp + kWarps * (i + lane));
+            const int key = k0 + 16 * (warp + W * (i + lane));
             blk_cache = key < k1 ? __ldg(bt_row + key / bs) : 0;
         }
         const int phys = __shfl_sync(0xffffffffu, blk_cache, i & 31);
-        const int key0 = k0 + 16 * (warp + kWarps * i);
+        const int key0 = k0 + 16 * (warp + W * i);
         const bool inside = !SHARED || (uint32_t)phys < (uint32_t)p.num_blocks;
         if (SHARED && !inside && lane == 0)
             atomicOr(&g_fused_error, 2u);
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecP
 
         const uint32_t kb = wbase + (i % kStages) * L::kStageBytes;
         const uint32_t vb = kb + L::kChunkBytes;
-        const int key0 = k0 + 16 * (warp + kWarps * i);
+        const int key0 = k0 + 16 * (warp + W * i);
 
         float sc[NT][4];
 #pragma unroll
@@ -259,18 +260,18 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecP
             for (int o = 4; o < 32; o <<= 1)
                 l_r[nt][j] += __shfl_xor_sync(0xffffffffu, l_r[nt][j], o);
 
-    // merge the 4 warps through shared memory (pipeline buffers are free now)
+    // merge the warps through shared memory (pipeline buffers are free now)
     __syncthreads();
     constexpr int H8 = 8 * NT;
     float *mrg_m = reinterpret_cast<float *>(smem);
-    float *mrg_l = mrg_m + kWarps * H8;
-    float *mrg_o = mrg_l + kWarps * H8; // [warp][head][D]
-    float *s_new = mrg_o + (size_t)kWarps * H8 * D; // FUSED: the new key's score per head (log2 units)
+    float *mrg_l = mrg_m + W * H8;
+    float *mrg_o = mrg_l + W * H8; // [warp][head][D]
+    float *s_new = mrg_o + (size_t)W * H8 * D; // FUSED: the new key's score per head (log2 units)
     if constexpr (FUSED) {
         if (has_new) {
             const size_t row = ((size_t)b * p.num_kv_heads + g) * D;
             // the new key's score for each head of the group: one warp per head, D/32 values per lane
-            for (int hl = warp; hl < G; hl += kWarps) {
+            for (int hl = warp; hl < G; hl += W) {
                 const __nv_bfloat16 *qr = p.q + ((size_t)b * Hq + (size_t)g * G + hl) * D;
                 float acc_s = 0.f;
 #pragma unroll
@@ -322,14 +323,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_split_kernel(const DecP
         const int hl = idx / D, d = idx % D;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
+        for (int w = 0; w < W; ++w)
             M = fmaxf(M, mrg_m[w * H8 + hl]);
         float Lsum = 0.f, O = 0.f;
         if (FUSED && has_new)
             M = fmaxf(M, s_new[hl]);
         if (M != -INFINITY) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const float f = ptx::ex2(mrg_m[w * H8 + hl] - M);
                 Lsum += f * mrg_l[w * H8 + hl];
                 O += f * mrg_o[((size_t)w * H8 + hl) * D + d];
@@ -413,10 +414,10 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const float *__rest
         dst[e] = __float2bfloat16_rn(accv[e] * inv);
 }
 
-template <int D, int NT, bool FUSED, bool SHARED = false>
+template <int D, int NT, bool FUSED, bool SHARED = false, int W = kWarps>
 int launch_split(const DecodeArgs &a, const DecParams &p, cudaStream_t stream)
 {
-    if (int rc = ensure_smem<decode_split_kernel<D, NT, FUSED, SHARED>>(DecLayout<D>::kSmemBytes, "decode"))
+    if (int rc = ensure_smem<decode_split_kernel<D, NT, FUSED, SHARED, W>>(DecLayout<D, W>::kSmemBytes, "decode"))
         return rc;
     // flat grid, heads of one work item adjacent: they read neighbouring
     // segments of the same token rows at about the same time (DRAM locality)
@@ -424,22 +425,22 @@ int launch_split(const DecodeArgs &a, const DecParams &p, cudaStream_t stream)
     if constexpr (SHARED) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = grid;
-        cfg.blockDim = dim3(kWarps * 32);
-        cfg.dynamicSmemBytes = DecLayout<D>::kSmemBytes;
+        cfg.blockDim = dim3(W * 32);
+        cfg.dynamicSmemBytes = DecLayout<D, W>::kSmemBytes;
         cfg.stream = stream;
         cudaLaunchAttribute attr{};
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr.val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = a.beside ? 1 : 0;
-        cudaError_t e = cudaLaunchKernelEx(&cfg, decode_split_kernel<D, NT, FUSED, SHARED>, p);
+        cudaError_t e = cudaLaunchKernelEx(&cfg, decode_split_kernel<D, NT, FUSED, SHARED, W>, p);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return fail(PA_ERR_CUDA, "shared decode launch: %s", cudaGetErrorString(e));
         }
         return PA_OK;
     }
-    decode_split_kernel<D, NT, FUSED, SHARED><<<grid, kWarps * 32, DecLayout<D>::kSmemBytes, stream>>>(p);
+    decode_split_kernel<D, NT, FUSED, SHARED, W><<<grid, W * 32, DecLayout<D, W>::kSmemBytes, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
@@ -450,9 +451,9 @@ template <int D, int NT>
 int occupancy()
 {
     int n = 0;
-    cudaFuncSetAttribute(decode_split_kernel<D, NT, false, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaFuncSetAttribute(decode_split_kernel<D, NT, false, false, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                          DecLayout<D>::kSmemBytes);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<D, NT, false, false>, kWarps * 32,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_split_kernel<D, NT, false, false, kWarps>, kWarps * 32,
                                                       DecLayout<D>::kSmemBytes) != cudaSuccess) {
         cudaGetLastError();
         return 2;
@@ -495,9 +496,16 @@ int launch_decode(const DecodeArgs &a, void *stream)
     p.max_blocks = a.max_blocks_per_seq;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool two = p.group > 8;
-    if (a.table_rows) { // short contexts of a shared-prefix decode
+    if (a.table_rows) { // contexts or parts of a shared-prefix decode
         p.table_rows = a.table_rows;
         p.num_blocks = a.dims.num_blocks;
+        if (a.few) {
+            if (a.dims.head_dim == 128)
+                return two ? launch_split<128, 2, false, true, kFewWarps>(a, p, s)
+                           : launch_split<128, 1, false, true, kFewWarps>(a, p, s);
+            return two ? launch_split<64, 2, false, true, kFewWarps>(a, p, s)
+                       : launch_split<64, 1, false, true, kFewWarps>(a, p, s);
+        }
         if (a.dims.head_dim == 128)
             return two ? launch_split<128, 2, false, true>(a, p, s) : launch_split<128, 1, false, true>(a, p, s);
         return two ? launch_split<64, 2, false, true>(a, p, s) : launch_split<64, 1, false, true>(a, p, s);

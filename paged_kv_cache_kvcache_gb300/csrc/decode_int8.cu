@@ -45,17 +45,18 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kFewWarps = 8; // of a shared-prefix decode's few items, each with an SM to itself
 constexpr int kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D>
+template <int D, int W = kWarps>
 struct DecLayout8 {
     static constexpr int kChunkBytes = 16 * D;          // 16 tokens of int8 codes
     static constexpr int kStageBytes = 2 * kChunkBytes; // K codes, V codes
     static constexpr int kWarpBytes = kStages * kStageBytes;
-    static constexpr int kScaleOff = kWarps * kWarpBytes; // [warp][stage]: 16 K + 16 V fp16 scales
-    static constexpr int kBarOff = kScaleOff + kWarps * kStages * 64;
-    static constexpr int kUsed = kBarOff + kWarps * kStages * 8;
+    static constexpr int kScaleOff = W * kWarpBytes; // [warp][stage]: 16 K + 16 V fp16 scales
+    static constexpr int kBarOff = kScaleOff + W * kStages * 64;
+    static constexpr int kUsed = kBarOff + W * kStages * 8;
     static constexpr int kSmemBytes = kUsed + 1024; // + slack to align the base to the swizzle atom
     static constexpr uint32_t kTxBytes = 2 * kChunkBytes + 64;
 };
@@ -158,12 +159,12 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[D / 32], float
 // SHARED: the items are a shared-prefix decode's parts of single sequences.  Their table may
 // be the caller's: a block id outside the pool reads as zeros and sets bit 1 of g_decode_error.
 // The launch may run beside the one before it (the shared parts); its last block ends after that one.
-template <int D, int NT, bool FUSED, bool SHARED>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
+template <int D, int NT, bool FUSED, bool SHARED, int W>
+__global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
     decode_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const DecParams8 p)
 {
-    using L = DecLayout8<D>;
+    using L = DecLayout8<D, W>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_u32(smem_raw);
     const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     const int Hq = p.num_heads;
 
     const int nchunks = (k1 - k0 + 15) >> 4;
-    const int my_n = nchunks > warp ? (nchunks - warp + kWarps - 1) / kWarps : 0;
+    const int my_n = nchunks > warp ? (nchunks - warp + W - 1) / W : 0;
     const uint32_t wbase = sbase + warp * L::kWarpBytes;
     const uint32_t sc_base = sbase + L::kScaleOff + warp * kStages * 64;
     const uint32_t bar_base = sbase + L::kBarOff + warp * kStages * 8;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     // Chunk i of this warp into stage i % kStages (whole warp: the block id comes by shuffle).
     auto issue = [&](int i) {
         if ((i & 31) == 0) { // refresh the block ids of local chunks i .. i+31, one per lane
-            const int key = k0 + 16 * (warp + kWarps * (i + lane));
+            const int key = k0 + 16 * (warp + W * (i + lane));
             blk_cache = key < k1 ? __ldg(bt_row + key / bs) : 0;
         }
         int phys = __shfl_sync(0xffffffffu, blk_cache, i & 31);
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
                     atomicOr(&g_decode_error, 2u);
                 }
             }
-            const int key0 = k0 + 16 * (warp + kWarps * i);
+            const int key0 = k0 + 16 * (warp + W * i);
             const int off0 = key0 & (bs - 1); // a chunk never crosses a block (bs >= 16, key0 % 16 == 0)
             const int st = i % kStages;
             const uint32_t bar = bar_base + 8 * st;
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
         const uint32_t kb = wbase + st * L::kStageBytes;
         const uint32_t vb = kb + L::kChunkBytes;
         const uint32_t sb = sc_base + st * 64;
-        const int key0 = k0 + 16 * (warp + kWarps * i);
+        const int key0 = k0 + 16 * (warp + W * i);
 
         // K codes of tokens r and r + 8: bytes [c*D/4, (c+1)*D/4) of each row
         uint32_t kw[2][D / 16];
@@ -402,9 +403,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     constexpr int H8 = 8 * NT;
     constexpr int kRow = D + 4; // padded head row (floats): the float4 stores below conflict at most 2-way
     float *mrg_m = reinterpret_cast<float *>(smem);
-    float *mrg_l = mrg_m + kWarps * H8;
-    float *mrg_o = mrg_l + kWarps * H8; // [warp][head][kRow], d in natural order
-    float *s_new = mrg_o + (size_t)kWarps * H8 * kRow; // FUSED: the new key's score per head (log2 units)
+    float *mrg_l = mrg_m + W * H8;
+    float *mrg_o = mrg_l + W * H8; // [warp][head][kRow], d in natural order
+    float *s_new = mrg_o + (size_t)W * H8 * kRow; // FUSED: the new key's score per head (log2 units)
     float *v_new = s_new + H8;                         // FUSED: the new value, dequantised
     if constexpr (FUSED) {
         if (has_new && warp < 2) {
@@ -484,14 +485,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
         const int hl = idx / D, d = idx % D;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
+        for (int w = 0; w < W; ++w)
             M = fmaxf(M, mrg_m[w * H8 + hl]);
         float Lsum = 0.f, O = 0.f;
         if (FUSED && has_new)
             M = fmaxf(M, s_new[hl]);
         if (M != -INFINITY) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const float f = ptx::ex2(mrg_m[w * H8 + hl] - M);
                 Lsum += f * mrg_l[w * H8 + hl];
                 O += f * mrg_o[((size_t)w * H8 + hl) * kRow + d];
@@ -518,10 +519,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
     }
 }
 
-template <int D, int NT, bool FUSED, bool SHARED = false>
+template <int D, int NT, bool FUSED, bool SHARED = false, int W = kWarps>
 int launch_int8(const DecodeArgs &a, const DecParams8 &p, cudaStream_t stream)
 {
-    if (int rc = ensure_smem<decode_int8_kernel<D, NT, FUSED, SHARED>>(DecLayout8<D>::kSmemBytes, "decode_int8"))
+    if (int rc = ensure_smem<decode_int8_kernel<D, NT, FUSED, SHARED, W>>(DecLayout8<D, W>::kSmemBytes, "decode_int8"))
         return rc;
     // codes as uint8 [num_slots][Hkv][D]: box = one head's D bytes x 16 token rows
     const pa_dims &d = a.dims;
@@ -541,22 +542,22 @@ int launch_int8(const DecodeArgs &a, const DecParams8 &p, cudaStream_t stream)
     if constexpr (SHARED) {
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = grid;
-        cfg.blockDim = dim3(kWarps * 32);
-        cfg.dynamicSmemBytes = DecLayout8<D>::kSmemBytes;
+        cfg.blockDim = dim3(W * 32);
+        cfg.dynamicSmemBytes = DecLayout8<D, W>::kSmemBytes;
         cfg.stream = stream;
         cudaLaunchAttribute attr{};
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr.val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = a.beside ? 1 : 0;
-        cudaError_t e = cudaLaunchKernelEx(&cfg, decode_int8_kernel<D, NT, FUSED, SHARED>, tk, tv, p);
+        cudaError_t e = cudaLaunchKernelEx(&cfg, decode_int8_kernel<D, NT, FUSED, SHARED, W>, tk, tv, p);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return fail(PA_ERR_CUDA, "shared decode_int8 launch: %s", cudaGetErrorString(e));
         }
         return PA_OK;
     }
-    decode_int8_kernel<D, NT, FUSED, SHARED><<<grid, kWarps * 32, DecLayout8<D>::kSmemBytes, stream>>>(tk, tv, p);
+    decode_int8_kernel<D, NT, FUSED, SHARED, W><<<grid, W * 32, DecLayout8<D, W>::kSmemBytes, stream>>>(tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "decode_int8 launch: %s", cudaGetErrorString(e));
@@ -587,6 +588,13 @@ int launch_decode_int8(const DecodeArgs &a, void *stream)
     if (a.table_rows) { // parts of a shared-prefix decode
         p.table_rows = a.table_rows;
         p.num_blocks = a.dims.num_blocks;
+        if (a.few) {
+            if (a.dims.head_dim == 128)
+                return two ? launch_int8<128, 2, false, true, kFewWarps>(a, p, s)
+                           : launch_int8<128, 1, false, true, kFewWarps>(a, p, s);
+            return two ? launch_int8<64, 2, false, true, kFewWarps>(a, p, s)
+                       : launch_int8<64, 1, false, true, kFewWarps>(a, p, s);
+        }
         if (a.dims.head_dim == 128)
             return two ? launch_int8<128, 2, false, true>(a, p, s) : launch_int8<128, 1, false, true>(a, p, s);
         return two ? launch_int8<64, 2, false, true>(a, p, s) : launch_int8<64, 1, false, true>(a, p, s);

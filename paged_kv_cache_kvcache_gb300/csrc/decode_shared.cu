@@ -41,7 +41,7 @@
 // run apart.
 //
 // Short contexts (the plan decides, see pack_shared.cpp) gain nothing from sharing: they go whole
-// through the decode kernels, which start in half the time and have nothing to merge.
+// through the decode kernels, which start in less time and have nothing to merge.
 //
 // Every hand-off waits with a time limit; a wait that runs out sets an error bit and the
 // kernel returns.  A block id outside the pool reads as zeros and sets an error bit.
@@ -1036,6 +1036,13 @@ int launch_singles(const SharedArgs &a, const int32_t *items, int32_t num_items,
     s.max_blocks_per_seq = a.max_blocks_per_seq;
     s.table_rows = a.table_rows;
     s.beside = beside;
+    int sms = 0;
+    if (int rc = sm_count(&sms))
+        return rc;
+    // then eight warps each instead of four, which shortens the chain of steps: 8 contexts of 300 tokens
+    // 6.2 us instead of 6.6, of 808 9.2 instead of 11.0, INT8 10.6 instead of 13.8; with more items than
+    // SMs the wider ones have no room beside one another
+    s.few = (int64_t)num_items * a.dims.num_kv_heads <= sms - (beside ? a.num_ctas : 0);
     return a.k_scale ? launch_decode_int8(s, stream) : launch_decode(s, stream);
 }
 

@@ -183,6 +183,7 @@ struct DecodeArgs {
     // contexts or parts of a shared-prefix decode (else NULL): no merge is launched
     const int32_t *table_rows; // block-table row of each sequence
     bool beside;               // may run beside the launch before it
+    bool few;                  // each (item, KV head) has an SM to itself
 };
 int launch_decode(const DecodeArgs &a, void *stream);
 int launch_decode_int8(const DecodeArgs &a, void *stream);

@@ -37,15 +37,12 @@ constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kSharedStep = 1.9f, kPair
 constexpr float kBytesPerUs = 6.9e6f, kSmBytesPerUs = 0.08e6f; // the decode kernels', all SMs and one
 constexpr float kApartStart = 1.f, kApartTail = 2.f, kApartKey = 0.006f;
 // What a call takes beyond that (set-up and merge), and what the decode kernels take for the contexts
-// whole, one part each: a start, a step of 64 keys after the other, or the bytes of all contexts
-// from L2 and HBM.  Fitted to 120 batches of 2 to 128 sequences of 84 to 1580 tokens; the choice is
-// 1 % slower than the better one in the mean.  Measured (28 / 4 heads of 128, direct against
-// shared): 8 x 300 6.7 and 8.9 us, 8 x 808 10.8 and 9.1, 128 x 300 14.3 and 17.4, 128 x 808 24.9 and
-// 18.8; INT8 8 x 300 8.1 and 11.4, 8 x 808 13.7 and 11.8, 128 x 300 12.6 and 17.3, 128 x 808 23.3
-// and 19.3.
+// whole, one part each: a start, a step of 16 keys per warp after the other (twice the warps where
+// there are few contexts), or the bytes of all contexts from L2 and HBM.  Fitted to 120 batches of 2
+// to 128 sequences of 84 to 1580 tokens.
 constexpr float kSharedStart = 5.0f, kSharedStartInt8 = 6.0f;
-constexpr float kDirectStart = 4.0f, kDirectKey = 0.0075f, kDirectKeyInt8 = 0.011f, kDirectBytesPerUs = 11.0e6f,
-                kDirectBytesPerUsInt8 = 6.5e6f;
+constexpr float kDirectStart = 4.0f, kDirectKey = 0.0075f, kDirectKeyInt8 = 0.011f, kDirectKeyFew = 0.0064f,
+                kDirectKeyFewInt8 = 0.0082f, kDirectBytesPerUs = 11.0e6f, kDirectBytesPerUsInt8 = 6.5e6f;
 
 struct Run { // consecutive sequences of a group that share `shared` tokens
     int32_t s0, n, shared;
@@ -272,11 +269,13 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     for (int32_t b = 0; b < num_seqs; ++b)
         all_keys += context_lens[b];
     const float keys_bytes = (float)all_keys * d.num_kv_heads * d.head_dim * 2;
-    const bool direct = split_tokens == 0 && kDirectStart + std::max(kDirectKey * max_ctx, 2 * keys_bytes / kDirectBytesPerUs) <
+    const bool few = (int64_t)num_seqs * d.num_kv_heads <= sms;
+    const float steps = max_ctx * (few ? kDirectKeyFew : kDirectKey);
+    const float steps_int8 = max_ctx * (few ? kDirectKeyFewInt8 : kDirectKeyInt8);
+    const bool direct = split_tokens == 0 && kDirectStart + std::max(steps, 2 * keys_bytes / kDirectBytesPerUs) <
                                                  kSharedStart + best;
-    const bool direct_int8 =
-        split_tokens == 0 && kDirectStart + std::max(kDirectKeyInt8 * max_ctx, keys_bytes / kDirectBytesPerUsInt8) <
-                                 kSharedStartInt8 + best;
+    const bool direct_int8 = split_tokens == 0 && kDirectStart + std::max(steps_int8, keys_bytes / kDirectBytesPerUsInt8) <
+                                                      kSharedStartInt8 + best;
 
     // items and partial slots
     std::vector<Work> works;
