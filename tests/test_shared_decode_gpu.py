@@ -376,3 +376,107 @@ def test_store_then_shared_decode():
         assert torch.equal(kc[blk, off], k[b]) and torch.equal(vc[blk, off], v[b])
     ref, a = reference(q, kc, vc, lists, ctx, bs, d ** -0.5)
     assert_within(out, ref, a, "store then decode")
+
+
+APART = [  # sizes, shared blocks, tails, bs, hq, hkv, d: more items than the lanes of 152 CTAs at 128 keys each
+    ([90], [30], [1 + 7 * i for i in range(90)], 16, 28, 4, 128),     # pairs
+    ([12, 30, 1], [9, 0, 2], [3 + 37 * i for i in range(43)], 64, 16, 8, 64),  # a tile, no sharing, a group of one
+    ([1] * 100, [3] * 100, [5 + i for i in range(100)], 128, 8, 4, 128),  # nothing shared: the decode kernels only
+    ([400], [8], [0, 9, 200, None] * 100, 16, 16, 1, 64),             # contexts that are all prefix, and empty ones
+]
+
+
+@pytest.mark.parametrize("case", APART, ids=range(len(APART)))
+def test_more_items_than_lanes(case):
+    """The parts of single sequences run beside the others; the results of both caches stay what they are."""
+    sizes, sh, tails, bs, hq, hkv, d = case
+    ctx, lists, groups, nb = make_batch(12, sizes, sh, tails, bs)
+    q = values((len(ctx), hq, d), 150)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=128).upload()
+    m = plan.meta
+    assert m.apart == 1 and m.num_items == m.num_shared_items and (m.num_items > 0) == (max(sizes) > 1)
+    kc, vc = pool(nb, bs, hkv, d, 151, ctx, lists)
+    out = decode(dims, q, kc, vc, plan, d ** -0.5)
+    assert_within(out, *reference(q, kc, vc, lists, ctx, bs, d ** -0.5), f"apart {case[:2]}")
+    assert all((out[b] == 0).all() for b, n in enumerate(ctx) if n == 0)
+    assert torch.equal(out, decode(dims, q, kc, vc, plan, d ** -0.5))
+    cache, dense = int8_pool(nb, bs, hkv, d, 152, ctx, lists)
+    out = decode8(dims, q, cache, plan, d ** -0.5)
+    assert_within(out, *reference(q, *dense, lists, ctx, bs, d ** -0.5), f"apart int8 {case[:2]}")
+    assert torch.equal(out, decode8(dims, q, cache, plan, d ** -0.5))
+
+
+def test_more_items_than_lanes_on_two_streams_and_replayed():
+    """Calls of three launches at once, with workspaces of their own, and a captured chain of them: each call's
+    queries are the last one's result, so a launch that began too early would be seen."""
+    sizes, sh, tails, bs, hq, hkv, d = APART[0]
+    ctx, lists, groups, nb = make_batch(13, sizes, sh, tails, bs)
+    kc, vc = pool(nb, bs, hkv, d, 160, ctx, lists)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=128).upload()
+    assert plan.meta.apart == 1
+    qs = [values((len(ctx), hq, d), 162 + i) for i in range(2)]
+    want = [decode(dims, q, kc, vc, plan, d ** -0.5) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wss, outs = [pa.shared_workspace(plan) for _ in range(2)], [torch.empty_like(qs[0]) for _ in range(2)]
+    for _ in range(5):
+        for i in range(2):
+            pa.pa_decode_shared(dims, qs[i], kc, vc, plan, d ** -0.5, outs[i], wss[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(outs[i], want[i]) for i in range(2))
+
+    chain = [qs[0]]
+    for _ in range(4):
+        chain.append(decode(dims, chain[-1], kc, vc, plan, d ** -0.5))
+        torch.cuda.synchronize()
+    x, y = qs[0].clone(), torch.empty_like(qs[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):  # the result becomes the queries, in place of the ones before
+            pa.pa_decode_shared(dims, x, kc, vc, plan, d ** -0.5, y, wss[0])
+            pa.pa_decode_shared(dims, y, kc, vc, plan, d ** -0.5, x, wss[0])
+    x.copy_(qs[0])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(x, chain[4]) and torch.equal(y, chain[3])
+
+
+def test_more_items_than_lanes_with_ids_outside_the_pool():
+    sizes, sh, tails, bs, hq, hkv, d = APART[0]
+    ctx, lists, groups, nb = make_batch(14, sizes, sh, tails, bs)
+    kc, vc = pool(nb, bs, hkv, d, 170, ctx, lists)
+    q = values((len(ctx), hq, d), 172)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    width = max(len(x) for x in lists)
+    table = np.full((len(ctx), width), -1, np.int32)
+    for b, x in enumerate(lists):
+        table[b, :len(x)] = x
+    table[:, 3], table[80, 31], table[7, 30] = -5, nb, 1 << 30  # a shared block, two of single sequences
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, shared_lens=[sh[0] * bs], max_blocks=width, split_tokens=128).upload()
+    assert plan.meta.apart == 1
+    out = decode(dims, q, kc, vc, plan, d ** -0.5, block_tables=torch.tensor(table, device="cuda"))
+    torch.cuda.synchronize()
+    assert pa.pa_read_device_error() == 1 << 6
+    kz, vz = (torch.cat([c, torch.zeros_like(c[:1])]) for c in (kc, vc))  # block nb: zeros
+    zeroed = [[x if 0 <= x < nb else nb for x in table[b, :len(lists[b])].tolist()] for b in range(len(ctx))]
+    assert_within(out, *reference(q, kz, vz, zeroed, ctx, bs, d ** -0.5), "apart bad ids")
+
+
+@pytest.mark.parametrize("n, hq, hkv, d", [(4, 28, 4, 128), (60, 28, 4, 128), (9, 16, 1, 64), (200, 4, 1, 64), (19, 16, 8, 128),
+                                           (20, 16, 8, 128)])
+def test_short_contexts_few_and_many(n, hq, hkv, d):
+    """Contexts decoded whole, with fewer and with more (context, KV head) pairs than SMs."""
+    bs = 16
+    ctx, lists, groups, nb = make_batch(15, [n], [2], [1 + 5 * i % 90 for i in range(n)], bs)
+    q = values((n, hq, d), 180)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists).upload()
+    assert plan.meta.direct == 3
+    kc, vc = pool(nb, bs, hkv, d, 181, ctx, lists)
+    out = decode(dims, q, kc, vc, plan, d ** -0.5)
+    assert_within(out, *reference(q, kc, vc, lists, ctx, bs, d ** -0.5), f"direct {n}")
+    cache, dense = int8_pool(nb, bs, hkv, d, 182, ctx, lists)
+    out = decode8(dims, q, cache, plan, d ** -0.5)
+    assert_within(out, *reference(q, *dense, lists, ctx, bs, d ** -0.5), f"direct int8 {n}")
