@@ -1080,12 +1080,13 @@ int launch(const SharedArgs &a, cudaStream_t stream)
         constexpr CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16; // (copies bits: fp16 as well)
         constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
         const uint64_t qs = (uint64_t)d.num_heads * D * 2;
-        CUtensorMap tq, tq1, tk, tv;
+        CUtensorMap tq, tq1{}, tk, tv;
         int rc;
         if ((rc = encode_tmap_3d(&tq, bf16, q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
                                  (uint32_t)G, (uint32_t)a.rows_per_tile, sw, "q")) != PA_OK ||
-            (rc = encode_tmap_3d(&tq1, bf16, q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
-                                 (uint32_t)G, 1, sw, "q")) != PA_OK ||
+            (a.num_single_items == 0 && // (else the lists have no parts of single sequences)
+             (rc = encode_tmap_3d(&tq1, bf16, q, D, d.num_heads, (uint64_t)a.num_seqs, (uint64_t)D * 2, qs, 64,
+                                  (uint32_t)G, 1, sw, "q")) != PA_OK) ||
             (rc = encode_cache<D>(&tk, k_cache, d.num_kv_heads, rows, box_rows, "k_cache")) != PA_OK ||
             (rc = encode_cache<D>(&tv, v_cache, d.num_kv_heads, rows, box_rows, "v_cache")) != PA_OK)
             return rc;

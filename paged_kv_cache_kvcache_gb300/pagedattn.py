@@ -179,19 +179,35 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
-def _here(*tensors) -> None:
-    """Refuse tensors that are not on the current device (a kernel launched there could not read them)."""
-    dev = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+def _device() -> int:
+    return _cur_device() if _cur_device is not None else torch.cuda.current_device()
+
+
+def _elsewhere(t, dev: int):
+    return ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+
+
+def _here(*tensors) -> list:
+    """Addresses of tensors (or None); refuses one that is not on the current device (a kernel launched there
+    could not read it)."""
+    dev, at = _device(), []
     for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
+        if t is None:
+            at.append(None)
+        elif t.get_device() != dev:
+            raise _elsewhere(t, dev)
+        else:
+            at.append(t.data_ptr())
+    return at
 
 
-def _int32(t, what: str, count: Optional[int] = None) -> int:
-    """Address of a contiguous int32 tensor (of `count` values)."""
+def _int32(t, what: str, count: Optional[int] = None, dev: Optional[int] = None) -> int:
+    """Address of a contiguous int32 tensor (of `count` values, on device `dev`)."""
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous() or \
             (count is not None and t.numel() != count):
         raise ValueError(f"{what} must be a contiguous int32 tensor" + ("" if count is None else f" of {count}"))
+    if dev is not None and t.get_device() != dev:
+        raise _elsewhere(t, dev)
     return t.data_ptr()
 
 
@@ -426,10 +442,6 @@ def pa_decode_static(dims: pa_dims, q, k_cache, v_cache, plan: DecodePlan, scale
                                   _stream(stream)), "pa_decode_static")
 
 
-def _nbytes(workspace) -> int:
-    return workspace.numel() if isinstance(workspace, torch.Tensor) else 0
-
-
 def shared_workspace(plan: SharedPlan, device="cuda", int8: bool = True) -> Optional[torch.Tensor]:
     """Workspace of a shared-prefix decode on either cache; with int8=False only pa_decode_shared's (without
     the fp16 copy of the shared parts)."""
@@ -459,20 +471,21 @@ def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale
     ``block_tables``: the device table a plan without block lists was packed for.
     """
     bt = _shared_tables(plan, block_tables)
-    _here(q, k_cache, v_cache, out, workspace, block_tables, plan.dev)
-    _check((_lib or lib()).pa_decode_shared(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), bt, scale, _ptr(out),
-                                  plan.call_ref, *plan.call_arrays, _ptr(workspace), _nbytes(workspace),
-                                  _stream(stream)), "pa_decode_shared")
+    q, k_cache, v_cache, out, ws, _, _ = _here(q, k_cache, v_cache, out, workspace, block_tables, plan.dev)
+    _check((_lib or lib()).pa_decode_shared(ctypes.byref(dims), q, k_cache, v_cache, bt, scale, out, plan.call_ref,
+                                            *plan.call_arrays, ws, 0 if ws is None else workspace.numel(),
+                                            _stream(stream)), "pa_decode_shared")
 
 
 def pa_decode_shared_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, plan: SharedPlan, scale: float, out,
                           workspace=None, block_tables=None, stream=None):
     """pa_decode_shared over an INT8 cache (same plan and workspace)."""
     bt = _shared_tables(plan, block_tables)
-    _here(q, k_cache, v_cache, k_scale, v_scale, out, workspace, block_tables, plan.dev)
-    _check((_lib or lib()).pa_decode_shared_int8(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                       _ptr(v_scale), bt, scale, _ptr(out), plan.call_ref, *plan.call_arrays,
-                                       plan.call_tiles, _ptr(workspace), _nbytes(workspace), _stream(stream)),
+    q, k_cache, v_cache, k_scale, v_scale, out, ws, _, _ = _here(q, k_cache, v_cache, k_scale, v_scale, out, workspace,
+                                                                 block_tables, plan.dev)
+    _check((_lib or lib()).pa_decode_shared_int8(ctypes.byref(dims), q, k_cache, v_cache, k_scale, v_scale, bt, scale,
+                                                 out, plan.call_ref, *plan.call_arrays, plan.call_tiles, ws,
+                                                 0 if ws is None else workspace.numel(), _stream(stream)),
            "pa_decode_shared_int8")
 
 
@@ -519,6 +532,13 @@ class PagePool:
         _check(lib().pa_pool_workspace(ctypes.byref(dims), self.ref, ctypes.byref(n)), "pa_pool_workspace")
         self.workspace = torch.empty(n.value, dtype=torch.uint8, device=block_tables.device)
         self.ws = (self.workspace.data_ptr(), n.value)
+        self.device = block_tables.get_device()
+
+    def here(self) -> int:
+        """The pool's device; refuses a call made with another one current."""
+        if self.device < 0 or _device() != self.device:
+            raise ValueError(f"the pool is on {self.block_tables.device}, which is not the current CUDA device")
+        return self.device
 
     @staticmethod
     def _layers(x, shape, int8):
@@ -540,39 +560,37 @@ def page_pool(dims: pa_dims, k_cache, v_cache, num_rows: int, max_blocks: int, k
 
 def pa_pool_append(dims: pa_dims, pool: PagePool, rows, cu_new, slot_mapping, stream=None):
     """Give row rows[i] its next cu_new[i+1] - cu_new[i] tokens; their slots go to slot_mapping."""
-    n, tokens = rows.numel(), slot_mapping.numel()
-    args = (_int32(rows, "rows"), _int32(cu_new, "cu_new", n + 1), n, _int32(slot_mapping, "slot_mapping"), tokens)
-    _here(pool.block_tables, rows, cu_new, slot_mapping)
-    _check((_lib or lib()).pa_pool_append(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
-           "pa_pool_append")
+    dev, n, tokens = pool.here(), rows.numel(), slot_mapping.numel()
+    _check((_lib or lib()).pa_pool_append(ctypes.byref(dims), pool.ref, _int32(rows, "rows", None, dev),
+                                          _int32(cu_new, "cu_new", n + 1, dev), n,
+                                          _int32(slot_mapping, "slot_mapping", None, dev), tokens, *pool.ws,
+                                          _stream(stream)), "pa_pool_append")
 
 
 def pa_pool_fork(dims: pa_dims, pool: PagePool, parents, children, stream=None):
     """Row children[i] shares row parents[i]'s full pages and gets a copy of its partly filled one."""
-    n = children.numel()
-    args = (_int32(parents, "parents", n), _int32(children, "children"), n)
-    _here(pool.block_tables, parents, children)
-    _check((_lib or lib()).pa_pool_fork(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)), "pa_pool_fork")
+    dev, n = pool.here(), children.numel()
+    _check((_lib or lib()).pa_pool_fork(ctypes.byref(dims), pool.ref, _int32(parents, "parents", n, dev),
+                                        _int32(children, "children", None, dev), n, *pool.ws, _stream(stream)),
+           "pa_pool_fork")
 
 
 def pa_pool_free(dims: pa_dims, pool: PagePool, rows, stream=None):
     """Empty the rows and give their pages back."""
-    at = _int32(rows, "rows")
-    _here(pool.block_tables, rows)
-    _check((_lib or lib()).pa_pool_free(ctypes.byref(dims), pool.ref, at, rows.numel(), _stream(stream)),
-           "pa_pool_free")
+    _check((_lib or lib()).pa_pool_free(ctypes.byref(dims), pool.ref, _int32(rows, "rows", None, pool.here()),
+                                        rows.numel(), _stream(stream)), "pa_pool_free")
 
 
 def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None, ref_counts_out=None, stream=None):
     """Move the used pages to the lowest ids; remap[p] is page p's new id.  Tables and counts are rewritten in
     place, or into the given arrays."""
+    dev = pool.here()
     tables = pool.block_tables if block_tables_out is None else block_tables_out
     refs = pool.ref_counts if ref_counts_out is None else ref_counts_out
     pages = pool.ref_counts.numel()
-    args = (_int32(remap, "remap", pages), _int32(tables, "block_tables_out", pool.block_tables.numel()),
-            _int32(refs, "ref_counts_out", pages))
-    _here(pool.block_tables, remap, tables, refs)
-    _check((_lib or lib()).pa_pool_compact(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
+    _check((_lib or lib()).pa_pool_compact(ctypes.byref(dims), pool.ref, _int32(remap, "remap", pages, dev),
+                                           _int32(tables, "block_tables_out", pool.block_tables.numel(), dev),
+                                           _int32(refs, "ref_counts_out", pages, dev), *pool.ws, _stream(stream)),
            "pa_pool_compact")
 
 
