@@ -29,13 +29,15 @@ constexpr int32_t kTile = kPrefillKeyTile;
 // kernels on the SMs that the shared parts leave (10.3 and 17.8 us there, but 64 x 4600 20.8 us
 // instead of 28.4, 200 x 16600 63.8 instead of 66.7, and 24 ragged groups 69 instead of 82): several
 // of their CTAs on an SM hide one another's latency, where a CTA of ours has two lanes.
-// The rates are those that fit best the times of 33 batches (1 to 200 sequences behind 512 to 16384
-// tokens, three head layouts, both caches, 22 lengths of the parts): the length chosen is 3 %
-// slower than the best one in the mean.
-constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kSharedStep = 1.9f, kPairItem = 2.5f, kSingleItem = 2.0f,
+// One plan serves both caches: the length chosen makes the product of their two times least.  The
+// rates are those that fit best the times of 36 batches (1 to 256 sequences behind 512 to 32768
+// tokens, three head layouts, both caches, 22 lengths of the parts, every call on tensors that L2 has
+// lost): the length chosen is 1.5 % (bf16) and 2 % (INT8) slower than the best one in the mean.
+constexpr float kPairStep = 1.62f, kSingleStep = 2.4f, kSharedStep = 1.9f, kPairItem = 4.0f, kSingleItem = 2.0f,
                 kMergeBytesPerUs = 3.0e6f;
-constexpr float kBytesPerUs = 6.9e6f, kSmBytesPerUs = 0.08e6f; // the decode kernels', all SMs and one
-constexpr float kApartStart = 1.f, kApartTail = 2.f, kApartKey = 0.006f;
+constexpr float kBytesPerUs = 6.9e6f, kSmBytesPerUs = 0.06e6f; // the decode kernels', all SMs and one
+constexpr float kInt8Rate = 0.8f, kCodesPerUs = 6.0e6f;        // part of those rates, conversion
+constexpr float kApartStart = 1.f, kApartTail = 4.f, kApartBegin = 2.f, kApartKey = 0.006f, kApartKeyInt8 = 0.0085f;
 // What a call takes beyond that (set-up and merge), and what the decode kernels take for the contexts
 // whole, one part each: a start, a step of 16 keys per warp after the other (twice the warps where
 // there are few contexts), or the bytes of all contexts from L2 and HBM.  Fitted to 120 batches of 2
@@ -209,10 +211,13 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     const float key_bytes = (float)d.num_kv_heads * d.head_dim * 4;
     const float slot_us = (float)d.num_heads * d.head_dim * 8.f / kMergeBytesPerUs;
     bool apart = false;
-    // parts of c key tiles at most: the time, and whether the parts of single sequences run apart
-    auto estimate = [&](int32_t c) -> float {
+    struct Times {
+        float bf16, int8;
+    };
+    // parts of c key tiles at most: the times, and whether the parts of single sequences run apart
+    auto estimate = [&](int32_t c) -> Times {
         float pair = 0.f, shared = 0.f, one = 0.f, work = 0.f; // longest items, CTA time of the shared parts
-        float bytes = 0.f, one_bytes = 0.f, slots = 0.f, longest = 0.f;
+        float bytes = 0.f, one_bytes = 0.f, codes = 0.f, slots = 0.f, longest = 0.f;
         int64_t pairs = 0, singles = 0, ones = 0;
         for (const Range &x : ranges) {
             const int32_t tiles = splits_of(x.keys, kTile), s = splits_of(tiles, c), len = splits_of(tiles, s);
@@ -232,38 +237,43 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
                 shared = std::max(shared, len * kSharedStep + kSingleItem);
             work += x.units_pair * (tiles * kPairStep + s * kPairItem) + x.units_single * (tiles * kSharedStep + s * kSingleItem);
             bytes += x.units_pair > d.num_kv_heads ? 0.f : x.keys * key_bytes;
+            codes += x.keys * key_bytes / 2;
         }
-        const float merge = slots * slot_us;
-        apart = 2 * pairs + singles + ones > 2 * (int64_t)sms;
-        if (!apart)
-            return std::max(std::max(pair, shared * (kSingleStep / kSharedStep)), one) + merge;
         // the shared parts in equal rounds over as few CTAs as that takes; on the SMs left and, after
         // them, on all, those of single sequences
+        const float merge = slots * slot_us;
         const int64_t units = pairs + singles, rounds = (units + sms - 1) / sms;
         const int64_t ctas = units ? (units + rounds - 1) / rounds : 0;
         float t = std::max(pair, shared);
         if (rounds > 1)
             t = std::max(t, work / (float)ctas + 0.25f * work / (float)units);
-        const float left = std::max(0.f, one_bytes - t * std::min(kBytesPerUs, (float)(sms - ctas) * kSmBytesPerUs));
-        t += left > 0.f ? left / kBytesPerUs + kApartTail : 0.f;
-        t = std::max(t, kApartTail + kApartKey * longest);
-        return std::max(t, (bytes + one_bytes) / kBytesPerUs) + kApartStart + merge;
+        auto beside = [&](float n, float rate, float per_key) {
+            const float left = std::max(0.f, n - t * rate * std::min(kBytesPerUs, (float)(sms - ctas) * kSmBytesPerUs));
+            return std::max(t + (left > 0.f ? left / (rate * kBytesPerUs) + kApartTail : 0.f), kApartBegin + per_key * longest) +
+                   kApartStart;
+        };
+        const float int8 = beside(one_bytes / 2, kInt8Rate, kApartKeyInt8) + codes / kCodesPerUs + merge;
+        apart = 2 * pairs + singles + ones > 2 * (int64_t)sms;
+        if (!apart)
+            return {std::max(std::max(pair, shared * (kSingleStep / kSharedStep)), one) + merge, int8};
+        return {std::max(beside(one_bytes, 1.f, kApartKey), (bytes + one_bytes) / kBytesPerUs) + merge, int8};
     };
     int32_t per = split_tokens / kTile;
-    float best = INFINITY; // the chosen ranges' time
     if (per == 0) {
         static const int32_t kPer[] = {1,  2,  3,  4,  5,  6,  7,  8,  9,  10,  11,  12,  13,  14,
                                        16, 18, 20, 22, 26, 32, 45, 64, 90, 128, 181, 256, 512, 1 << 24};
+        float best = INFINITY;
         for (int32_t c : kPer) {
-            const float t = estimate(c);
-            if (t < best) {
-                best = t;
+            const Times t = estimate(c);
+            const float both = (kSharedStart + t.bf16) * (kSharedStartInt8 + t.int8);
+            if (both < best) {
+                best = both;
                 per = c;
             }
         }
         per = std::max(per, 1);
     }
-    estimate(per); // (apart)
+    const Times times = estimate(per); // (and apart)
 
     int64_t all_keys = 0;
     for (int32_t b = 0; b < num_seqs; ++b)
@@ -273,9 +283,9 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     const float steps = max_ctx * (few ? kDirectKeyFew : kDirectKey);
     const float steps_int8 = max_ctx * (few ? kDirectKeyFewInt8 : kDirectKeyInt8);
     const bool direct = split_tokens == 0 && kDirectStart + std::max(steps, 2 * keys_bytes / kDirectBytesPerUs) <
-                                                 kSharedStart + best;
+                                                 kSharedStart + times.bf16;
     const bool direct_int8 = split_tokens == 0 && kDirectStart + std::max(steps_int8, keys_bytes / kDirectBytesPerUsInt8) <
-                                                      kSharedStartInt8 + best;
+                                                      kSharedStartInt8 + times.int8;
 
     // items and partial slots
     std::vector<Work> works;
