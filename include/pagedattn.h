@@ -134,13 +134,13 @@ typedef struct pa_shared_meta {
     int32_t merge;              /* 1: some context has two or more parts, or none */
     int32_t split_tokens;       /* keys per part, at most */
     int32_t tables_packed;      /* 1: the image holds block tables and slots */
-    int32_t num_single_items;   /* (sequence, key range) parts of single sequences (INT8) */
+    int32_t num_single_items;   /* (sequence, key range) parts of single sequences */
     int32_t num_shared_items;   /* work items of several sequences */
-    int32_t num_scratch_tiles;  /* 128-key tiles of the groups' shared parts (INT8) */
+    int32_t num_scratch_tiles;  /* 128-key tiles of what the items read (INT8) */
     int32_t direct;             /* bit 0 (bf16), bit 1 (INT8): contexts so short that they are
                                    decoded whole, without sharing (never with a given split) */
     int32_t apart;              /* 1: items has those of several sequences only; the parts of single
-                                   sequences run in the decode kernels (INT8: always) */
+                                   sequences run in the decode kernels */
     uint64_t tokens_saved;       /* keys the groups read once instead of once per sequence */
     uint64_t off_block_tables;   /* int32 [num_seqs][max_blocks_per_seq], -1 padded (tables_packed) */
     uint64_t off_slot_mapping;   /* int32 [num_seqs] slot of each last token (tables_packed) */
@@ -157,11 +157,11 @@ typedef struct pa_shared_meta {
                                     partial slot or -1 */
     uint64_t off_table_rows;     /* int32 [num_seqs] block-table row of each sequence */
     uint64_t off_direct_items;   /* int32 [num_seqs][4]: sequence, 0, context length, -1 */
-    uint64_t off_scratch_tiles;  /* int32 [num_scratch_tiles][4]: block-table row, first key, shared
-                                    tokens, scratch row of the first key */
+    uint64_t off_scratch_tiles;  /* int32 [num_scratch_tiles][4]: block-table row, first key, end of
+                                    the keys, scratch row of the first key */
     uint64_t total_bytes;
     uint64_t workspace_bytes;    /* device workspace pa_decode_shared needs */
-    uint64_t workspace_bytes_int8; /* and pa_decode_shared_int8: the shared parts and q in fp16 too */
+    uint64_t workspace_bytes_int8; /* and pa_decode_shared_int8: what the items read in fp16 too */
 } pa_shared_meta;
 
 /*
@@ -635,10 +635,10 @@ int pa_decode_int8_fused(const pa_dims *dims, const void *q, const void *k, cons
 /*
  * pa_decode_shared_int8 — pa_decode_shared over an INT8 cache: the same plan
  * (pa_pack_decode_shared), rules and result, with the cached K and V read as
- * code * scale.  A launch turns the shared parts' keys and values, and q, into
- * fp16 in the workspace (rounded to nearest even, clamped to +-65504); their
- * products run on those with fp32 accumulation.  The parts of single sequences
- * are computed as pa_decode_int8 computes them.
+ * code * scale.  A launch turns the keys and values of the plan's items, and q,
+ * into fp16 in the workspace (rounded to nearest even, clamped to +-65504); their
+ * products run on those with fp32 accumulation.  Parts of single sequences that
+ * run apart are computed as pa_decode_int8 computes them.
  *   scratch_tiles: device copy of the plan's array
  *   workspace:  at least meta->workspace_bytes_int8
  */

@@ -508,10 +508,9 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
     a->scale = scale;
     a->num_seqs = meta->num_seqs;
     // parts of single sequences: in the CTAs' lists, or apart in the decode kernels
-    const bool apart = int8 || meta->apart != 0;
     a->single_items = single_items;
-    a->num_items = apart ? meta->num_shared_items : meta->num_items;
-    a->num_single_items = apart ? meta->num_single_items : 0;
+    a->num_items = meta->num_items;
+    a->num_single_items = meta->apart ? meta->num_single_items : 0;
     a->num_ctas = meta->num_ctas;
     a->rows_per_tile = meta->rows_per_tile;
     a->max_blocks_per_seq = meta->max_blocks_per_seq;

@@ -37,8 +37,7 @@
 // tiles and heads: keys and values (code * scale, rounded by 2^-12 at most; fp16 holds them to
 // 65504) and the queries.  The products then run as on a bf16 cache, with fp16 weights.  (Exact
 // codes with the scales in the softmax took 3.4 us per 128 keys and pair instead of 1.6: 64 more
-// 16-byte loads per row; converting in shared memory took 4.2.)  Parts of single sequences always
-// run apart.
+// 16-byte loads per row; converting in shared memory took 4.2.)
 //
 // Short contexts (the plan decides, see pack_shared.cpp) gain nothing from sharing: they go whole
 // through the decode kernels, which start in less time and have nothing to merge.
@@ -135,10 +134,7 @@ struct Item {
     __device__ bool tail() const { return ((k1 - k0) & 127) != 0; } // the last key tile runs past k1
 };
 
-// Entries [idx, end) of the item list, the next one fetched while the current one runs.  INT8:
-// up to the first part of a single sequence (the lists are sorted that way): those are the
-// INT8 decode kernel's.
-template <bool kInt8>
+// Entries [idx, end) of the item list, the next one fetched while the current one runs.
 struct ItemIter {
     const int4 *items;
     int idx, end;
@@ -150,8 +146,6 @@ struct ItemIter {
         if (idx < end) {
             a0 = ptx::ld_nc_v4_now(items + 2 * idx);
             a1 = ptx::ld_nc_v4_now(items + 2 * idx + 1);
-            if (kInt8 && a0.y == 1)
-                end = idx;
         }
     }
     __device__ Item peek() const { return {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w}; }
@@ -166,16 +160,15 @@ struct ItemIter {
 };
 
 // A lane's place in its singles: key tile j of n of the current one.
-template <bool kInt8>
 struct Lane {
-    ItemIter<kInt8> it;
+    ItemIter it;
     Item w;
     int j, n;
     bool active;
     // `first`: item `from`, already at hand
     __device__ Lane(const int4 *items, int from, int to, const Item &first)
         : it(items, min(from + 1, to), to), w(first), j(0), n(first.tiles()),
-          active(from < to && !(kInt8 && first.nseq == 1))
+          active(from < to)
     {
     }
     __device__ void next_item()
@@ -232,7 +225,7 @@ __device__ __forceinline__ void codes_to_f16(const uint4 &c, __half2 scale, uint
 }
 
 struct CodesParams {
-    const int4 *tiles; // block-table row, first key, shared tokens, scratch row of the first key
+    const int4 *tiles; // block-table row, first key, end of the keys, scratch row of the first key
     const int32_t *block_tables;
     const uint4 *k_codes, *v_codes;    // INT8 cache, 16 codes each
     const uint16_t *k_scale, *v_scale; // fp16 bits
@@ -244,8 +237,8 @@ struct CodesParams {
     int64_t q_vecs;    // of 8 values
 };
 
-// What the shared parts' products read on an INT8 cache, in fp16: the shared prefixes' keys and
-// values (code * scale; 16 keys per CTA, K and V) and the queries.  Rows behind a prefix and
+// What the products of the CTAs' lists read on an INT8 cache, in fp16: the shared prefixes' (and,
+// where single sequences do not run apart, the other) keys and values (code * scale; 16 keys per CTA, K and V) and the queries.  Rows behind the last key and
 // those of block ids outside the pool become zeros.  Bound by HBM: 1 byte read and 2 written per code.
 constexpr int kCodesKeys = 16;
 __global__ void __launch_bounds__(256) shared_codes_kernel(const CodesParams p)
@@ -437,12 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kQWarp) {
             // ------------------------------------------------------------ query producer
             bool ok = true;
-            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
+            for (ItemIter it(p.items, span.x, span.y); ok && it.more();) {
                 const Item w = it.next();
                 ok = load_q(w, 0, 0) && load_q(w, 1, P);
             }
             // the lanes advance tile by tile together: loads in the order in which they are needed
-            Lane<kInt8> l0(p.items, span.y, span.z, lane0_first()), l1(p.items, span.z, span.w, second);
+            Lane l0(p.items, span.y, span.z, lane0_first()), l1(p.items, span.z, span.w, second);
             int at0 = 0, at1 = 0; // key tiles before each lane's next item
             while (ok && (l0.active || l1.active)) {
                 const bool is0 = l0.active && (!l1.active || at0 <= at1);
@@ -505,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++ph;
                 }
             };
-            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
+            for (ItemIter it(p.items, span.x, span.y); ok && it.more();) {
                 const Item w = it.next();
                 const int n = w.tiles();
                 int next = X == 0 ? row0 : sub_row(w, 0);
@@ -516,9 +509,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     load(w, j, cur, keep);
                 }
             }
-            Lane<kInt8> l0(p.items, span.y, span.z, lane0_first()), l1(p.items, span.z, span.w, second);
+            Lane l0(p.items, span.y, span.z, lane0_first()), l1(p.items, span.z, span.w, second);
             int r0 = X == 0 ? row0 : l0.active ? sub_row(l0.w, 0) : 0, r1 = row1;
-            auto advance = [&](Lane<kInt8> &l, int &r) { // this tile's load, the next one's row looked up before it
+            auto advance = [&](Lane &l, int &r) { // this tile's load, the next one's row looked up before it
                 const Item w = l.w;
                 const int j = l.j, cur = r;
                 l.step();
@@ -577,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto wait_v = [&](bool tail) {
                 ok = ok && wwait(bars.v_full(vs), vph);
-                if (!kInt8 && tail) { // (the scratch rows behind a prefix are zeros)
+                if (!kInt8 && tail) { // (the scratch rows behind a context are zeros)
                     ok = ok && wwait(bars.v_tail(vs), (tailpar >> vs) & 1u);
                     tailpar ^= 1u << vs;
                 }
@@ -597,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     vph ^= 1;
                 }
             };
-            for (ItemIter<kInt8> it(p.items, span.x, span.y); ok && it.more();) {
+            for (ItemIter it(p.items, span.x, span.y); ok && it.more();) {
                 const Item w = it.next();
                 const int n = w.tiles();
                 const bool tail = w.tail();
@@ -647,9 +640,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pass_k();
                 }
             }
-            Lane<kInt8> l0(p.items, span.y, span.z, lane0_first()), l1(p.items, span.z, span.w, second);
+            Lane l0(p.items, span.y, span.z, lane0_first()), l1(p.items, span.z, span.w, second);
             // score product of the lane's current key tile
-            auto score = [&](const Lane<kInt8> &l, int t) {
+            auto score = [&](const Lane &l, int t) {
                 if (l.j == 0)
                     wait_q(t);
                 wait_k();
@@ -661,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pass_k();
             };
             // value product of the lane's current key tile, then the next one's scores
-            auto step = [&](Lane<kInt8> &l, int t) {
+            auto step = [&](Lane &l, int t) {
                 const bool last = l.j + 1 == l.n;
                 wait_p(t);
                 wait_v(last && l.w.tail());
@@ -701,14 +694,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr float kBias = kInt8 ? 7.f : 0.f; // 2^(7 + kRescaleThreshold) stays in fp16
         uint32_t ns = 0, no = 0;
         bool ok = true;
-        ItemIter<kInt8> items(p.items, span.x, span.y);
+        ItemIter items(p.items, span.x, span.y);
         bool single = false;
         while (ok) {
             if (!items.more()) {
                 if (single)
                     break;
                 single = true;
-                items = t == 0 ? ItemIter<kInt8>(p.items, span.y, span.z) : ItemIter<kInt8>(p.items, span.z, span.w);
+                items = t == 0 ? ItemIter(p.items, span.y, span.z) : ItemIter(p.items, span.z, span.w);
                 continue;
             }
             const Item w = items.next(false);
@@ -981,7 +974,7 @@ int encode_cache(CUtensorMap *m, const void *cache, int num_kv_heads, uint64_t r
                           (uint64_t)num_kv_heads * D * 2, 64, 1, box_rows, CU_TENSOR_MAP_SWIZZLE_128B, what);
 }
 
-// INT8: the scratch copies for the shared parts.
+// INT8: the scratch copies for the CTAs' lists.
 int launch_codes(const SharedArgs &a, cudaStream_t stream)
 {
     const pa_dims &d = a.dims;

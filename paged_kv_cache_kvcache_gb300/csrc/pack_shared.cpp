@@ -25,7 +25,7 @@ constexpr int32_t kTile = kPrefillKeyTile;
 // partial costs its bytes written and read again.
 //
 // The parts of single sequences run in the lanes' lists too where every item has a lane of its own
-// (4 x 2148 tokens 9.5 us, 8 x 16500 17.0); where there are more items they run apart, in the decode
+// (4 x 2148 tokens 9.5 us, 8 x 16500 17.0); where there are more items, or none is shared, they run apart, in the decode
 // kernels on the SMs that the shared parts leave (10.3 and 17.8 us there, but 64 x 4600 20.8 us
 // instead of 28.4, 200 x 16600 63.8 instead of 66.7, and 24 ragged groups 69 instead of 82): several
 // of their CTAs on an SM hide one another's latency, where a CTA of ours has two lanes.
@@ -135,10 +135,10 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     const int group = d.num_heads / d.num_kv_heads;
     const int32_t P = std::max(1, kPrefillRows / group);
     std::vector<Run> runs;
-    struct Prefix {
-        int32_t row, shared, scratch;
+    struct Copied { // keys [from, to) of a row, at a scratch row
+        int32_t row, from, to, scratch;
     };
-    std::vector<Prefix> groups_scratch;
+    std::vector<Copied> copies; // what the INT8 decode's items read
     int64_t scratch_tiles = 0;
     for (int32_t i = 0; num_seqs > 0 && i < num_groups; ++i) {
         const int32_t b0 = group_offsets[i], b1 = group_offsets[i + 1];
@@ -176,7 +176,7 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         // (several runs of a group read the same scratch rows)
         const int32_t group_scratch = (int32_t)std::min<int64_t>(scratch_tiles * kTile, INT32_MAX);
         if (shared > 0) {
-            groups_scratch.push_back({table_rows ? table_rows[first] : first, shared, group_scratch});
+            copies.push_back({table_rows ? table_rows[first] : first, 0, shared, group_scratch});
             scratch_tiles += (shared + kTile - 1) / kTile;
         }
         for (int32_t b = b0; b < b1;) {
@@ -252,11 +252,13 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
             return std::max(t + (left > 0.f ? left / (rate * kBytesPerUs) + kApartTail : 0.f), kApartBegin + per_key * longest) +
                    kApartStart;
         };
-        const float int8 = beside(one_bytes / 2, kInt8Rate, kApartKeyInt8) + codes / kCodesPerUs + merge;
-        apart = 2 * pairs + singles + ones > 2 * (int64_t)sms;
-        if (!apart)
-            return {std::max(std::max(pair, shared * (kSingleStep / kSharedStep)), one) + merge, int8};
-        return {std::max(beside(one_bytes, 1.f, kApartKey), (bytes + one_bytes) / kBytesPerUs) + merge, int8};
+        apart = units == 0 || 2 * pairs + singles + ones > 2 * (int64_t)sms;
+        if (!apart) {
+            const float in = std::max(std::max(pair, shared * (kSingleStep / kSharedStep)), one) + merge;
+            return {in, in + (codes + one_bytes / 2) / kCodesPerUs};
+        }
+        return {std::max(beside(one_bytes, 1.f, kApartKey), (bytes + one_bytes) / kBytesPerUs) + merge,
+                beside(one_bytes / 2, kInt8Rate, kApartKeyInt8) + codes / kCodesPerUs + merge};
     };
     int32_t per = split_tokens / kTile;
     if (per == 0) {
@@ -318,8 +320,15 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         if (ps > 0)
             cut(r.s0, r.n, table_rows ? table_rows[r.s0] : r.s0, 0, r.shared, 0, r.scratch);
         for (int32_t b = r.s0; b < r.s0 + r.n; ++b)
-            if (context_lens[b] > r.shared)
-                cut(b, 1, table_rows ? table_rows[b] : b, r.shared, context_lens[b], ps, 0);
+            if (context_lens[b] > r.shared) {
+                const int32_t row = table_rows ? table_rows[b] : b;
+                const int32_t at = (int32_t)std::min<int64_t>(scratch_tiles * kTile, INT32_MAX);
+                if (!apart) {
+                    copies.push_back({row, r.shared, context_lens[b], at});
+                    scratch_tiles += splits_of(context_lens[b] - r.shared, kTile);
+                }
+                cut(b, 1, row, r.shared, context_lens[b], ps, apart ? 0 : at - r.shared);
+            }
     }
     if (works.size() > (size_t)INT32_MAX / kSharedItemInts)
         return fail(PA_ERR_INVALID_ARG, "too many work items");
@@ -413,12 +422,12 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
         whole += 4;
     }
     int32_t *tile = reinterpret_cast<int32_t *>(base + meta->off_scratch_tiles);
-    for (const Prefix &x : groups_scratch)
-        for (int32_t k = 0; k < x.shared; k += kTile, tile += 4) {
+    for (const Copied &x : copies)
+        for (int32_t k = x.from; k < x.to; k += kTile, tile += 4) {
             tile[0] = x.row;
             tile[1] = k;
-            tile[2] = x.shared;
-            tile[3] = x.scratch + k;
+            tile[2] = x.to;
+            tile[3] = x.scratch + k - x.from;
         }
     for (int32_t b = 0, slot = 0; b < num_seqs; ++b) {
         sp[2 * b] = slot;

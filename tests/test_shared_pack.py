@@ -87,7 +87,7 @@ def test_parts_cover_every_key_once(case):
                        for b, k0, k1, slot in ones for g in range(hkv)]
         assert all((slot >= 0) == (parts[b, 1] > 1) for b, _, _, slot in ones)
     for s0, n, g, row, k0, k1, part, scratch in everything:
-        if n > 1:  # every key tile of a shared part is in the scratch cache, at the item's row
+        if n > 1 or not m.apart:  # every key tile of the lists' items is in the scratch cache, at the item's row
             for k in range(k0, k1, 128):
                 x, = [x for x in tiles if x[1] == k and x[3] == scratch + k]
                 assert x[2] >= min(k1, k + 128) and table[x[0], :x[2] // bs].tolist() == table[row, :x[2] // bs].tolist()
@@ -175,7 +175,13 @@ def test_plan_for_a_device_table():
                                     pin=False)
     items, _, parts = arrays(plan)
     assert not plan.meta.tables_packed and plan.meta.max_blocks_per_seq == 7
-    assert {(int(s), int(r)) for s, r in items[:, [0, 3]]} == {(0, 5), (2, 2)}
+    m = plan.meta  # the empty entry parts the two that share: the decode kernels only
+    assert len(items) == 0 and m.apart == 1 and m.num_ctas == 0
+    assert set(plan.host_array(m.off_single_items, 4 * m.num_single_items).reshape(-1, 4)[:, 0].tolist()) == {0, 2}
+    plan2 = pa.pa_pack_decode_shared(dims, [100, 70, 0], [0, 3], shared_lens=[48], table_rows=[5, 2, 9], max_blocks=7,
+                                     pin=False)
+    items, _, _ = arrays(plan2)
+    assert {(int(s), int(n), int(r)) for s, n, r in items[:, [0, 1, 3]]} == {(0, 2, 5), (0, 1, 5), (1, 1, 2)}
     with pytest.raises(AssertionError):
         plan.slot_mapping
     bad = [dict(shared_lens=None), dict(max_blocks=6), dict(max_blocks=0), dict(table_rows=[5, -1, 2]),
