@@ -78,6 +78,7 @@ struct DecParams {
     // a shared-prefix decode's contexts (SHARED kernels only): block-table row of each sequence, pool size
     const int32_t *table_rows;
     int32_t num_blocks;
+    int32_t beside;
 };
 
 // bit 0: a fused-store slot outside [-1, num_slots) was skipped; bit 1: SHARED met a block id outside the pool
@@ -100,6 +101,11 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1) decode_split_kern
     const int lane = threadIdx.x & 31;
     const int4 item = p.items[blockIdx.x / p.num_kv_heads];
     const int b = item.x, k0 = item.y, pslot = item.w;
+    if constexpr (SHARED) { // the items are the plan's; everything else may be the launch before's
+        ptx::launch_dependents();
+        if (!p.beside)
+            ptx::grid_dependency_wait();
+    }
     const int g = blockIdx.x % p.num_kv_heads;
     const int G = p.group;
     const int Hq = p.num_heads;
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1) decode_split_kern
         }
     }
     if constexpr (SHARED) {
-        if (blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
+        if (p.beside && blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
             ptx::grid_dependency_wait();
     }
 }
@@ -432,7 +438,7 @@ int launch_split(const DecodeArgs &a, const DecParams &p, cudaStream_t stream)
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr.val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = &attr;
-        cfg.numAttrs = a.beside ? 1 : 0;
+        cfg.numAttrs = 1;
         cudaError_t e = cudaLaunchKernelEx(&cfg, decode_split_kernel<D, NT, FUSED, SHARED, W>, p);
         if (e != cudaSuccess) {
             cudaGetLastError();
@@ -499,6 +505,7 @@ int launch_decode(const DecodeArgs &a, void *stream)
     if (a.table_rows) { // contexts or parts of a shared-prefix decode
         p.table_rows = a.table_rows;
         p.num_blocks = a.dims.num_blocks;
+        p.beside = a.beside;
         if (a.few) {
             if (a.dims.head_dim == 128)
                 return two ? launch_split<128, 2, false, true, kFewWarps>(a, p, s)

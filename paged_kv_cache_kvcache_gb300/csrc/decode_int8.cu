@@ -124,6 +124,7 @@ struct DecParams8 {
     // parts of a shared-prefix decode (SHARED kernels only): block-table row of each sequence, pool size
     const int32_t *table_rows;
     int32_t num_blocks;
+    int32_t beside;
 };
 
 __device__ uint32_t g_fused8_error; // bit 0: a fused-store slot outside [-1, num_slots) was skipped
@@ -174,6 +175,11 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
     const int r = lane >> 2, c = lane & 3;
     const int4 item = p.items[blockIdx.x / p.num_kv_heads];
     const int b = item.x, k0 = item.y, pslot = item.w;
+    if constexpr (SHARED) { // the items are the plan's; everything else may be the launch before's
+        ptx::launch_dependents();
+        if (!p.beside)
+            ptx::grid_dependency_wait();
+    }
     // FUSED: does this item hold the new token?  Then the cache supplies keys k0 .. ctx-2.
     const bool has_new = FUSED && item.z > 0 && item.z == __ldg(p.context_lens + b);
     const int k1 = has_new ? item.z - 1 : item.z;
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
         }
     }
     if constexpr (SHARED) {
-        if (blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
+        if (p.beside && blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
             ptx::grid_dependency_wait();
     }
 }
@@ -549,7 +555,7 @@ int launch_int8(const DecodeArgs &a, const DecParams8 &p, cudaStream_t stream)
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr.val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = &attr;
-        cfg.numAttrs = a.beside ? 1 : 0;
+        cfg.numAttrs = 1;
         cudaError_t e = cudaLaunchKernelEx(&cfg, decode_int8_kernel<D, NT, FUSED, SHARED, W>, tk, tv, p);
         if (e != cudaSuccess) {
             cudaGetLastError();
@@ -588,6 +594,7 @@ int launch_decode_int8(const DecodeArgs &a, void *stream)
     if (a.table_rows) { // parts of a shared-prefix decode
         p.table_rows = a.table_rows;
         p.num_blocks = a.dims.num_blocks;
+        p.beside = a.beside;
         if (a.few) {
             if (a.dims.head_dim == 128)
                 return two ? launch_int8<128, 2, false, true, kFewWarps>(a, p, s)

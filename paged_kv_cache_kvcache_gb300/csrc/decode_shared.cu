@@ -243,6 +243,7 @@ struct CodesParams {
 constexpr int kCodesKeys = 16;
 __global__ void __launch_bounds__(256) shared_codes_kernel(const CodesParams p)
 {
+    ptx::grid_dependency_wait(); // (before the line below: what it starts counts on this)
     ptx::launch_dependents();
     if ((int)blockIdx.x >= p.tile_ctas) {
         const int64_t i = (int64_t)((int)blockIdx.x - p.tile_ctas) * 256 + threadIdx.x;
@@ -324,8 +325,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int G = p.group;
     const int P = p.rows_per_tile;
 
-    // the merge launch may be set up now; it waits for this grid's end before it reads
-    ptx::launch_dependents();
+    // The launch after this one may be set up: a merge, which waits for this grid's end, or the parts of
+    // single sequences, which count on the end of the grid before this one only (INT8: of the one
+    // before the conversion, which has waited for that).
+    if (kInt8)
+        ptx::launch_dependents();
     if (warp >= 8 && lane == 0) {
         if (warp == kQWarp) {
             ptx::prefetch_tmap(&tm_q);
@@ -383,6 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item first{}, second{};
     int row0 = 0, row1 = 0;
     if (warp >= 8) {
+        if (!kInt8) { // nothing but the plan is read before
+            ptx::grid_dependency_wait();
+            ptx::launch_dependents();
+        }
         const int4 a0 = __ldg(record + 2), a1 = __ldg(record + 3), b0 = __ldg(record + 4), b1 = __ldg(record + 5);
         first = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
         second = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
@@ -890,6 +898,7 @@ __global__ void __launch_bounds__(kSplit == 8 ? 256 : 128)
     const int b = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int h = blockIdx.y * kHeads + (kSplit == 1 ? warp : 0);
     const int2 sp = __ldg(seq_parts + b); // the plan's, written long before this launch's predecessor
+    ptx::launch_dependents();
     ptx::grid_dependency_wait();          // the parts are complete and visible
     if (sp.y == 1 || h >= num_heads)
         return;
@@ -998,10 +1007,20 @@ int launch_codes(const SharedArgs &a, cudaStream_t stream)
     c.key_vecs = d.num_kv_heads * c.head_vecs;
     c.tile_ctas = a.num_scratch_tiles * (128 / kCodesKeys);
     c.q_vecs = (int64_t)a.num_seqs * d.num_heads * d.head_dim / 8;
-    shared_codes_kernel<<<(unsigned)(c.tile_ctas + (c.q_vecs + 255) / 256), 256, 0, stream>>>(c);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(c.tile_ctas + (c.q_vecs + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_codes_kernel, c);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
         return fail(PA_ERR_CUDA, "shared decode code conversion launch: %s", cudaGetErrorString(e));
+    }
     return PA_OK;
 }
 
@@ -1109,7 +1128,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
         attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr.val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = &attr;
-        cfg.numAttrs = kInt8 ? 1 : 0;
+        cfg.numAttrs = 1;
         const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_shared_kernel<D, kInt8>, tq, tq1, tk, tv, p);
         if (e != cudaSuccess) {
             cudaGetLastError();
@@ -1137,7 +1156,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
-    cfg.numAttrs = a.num_items + a.num_single_items > 0 ? 1 : 0;
+    cfg.numAttrs = 1;
     auto combine = split == 1 ? shared_combine_kernel<D, 1> : split == 4 ? shared_combine_kernel<D, 4> : shared_combine_kernel<D, 8>;
     const cudaError_t e =
         cudaLaunchKernelEx(&cfg, combine, (const float *)a.part_o, (const float *)a.part_lse,

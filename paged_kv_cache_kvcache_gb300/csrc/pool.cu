@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(kThreads)
     __shared__ Smem sm;
     if (!kSlots)
         ptx::launch_dependents();
+    ptx::grid_dependency_wait();
     Team<kCluster> team(sm);
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
     const int nt = team.threads(), me = team.thread(), bs = p.block_size;
@@ -444,6 +445,7 @@ __global__ void __launch_bounds__(kThreads)
 {
     __shared__ Smem sm;
     ptx::launch_dependents();
+    ptx::grid_dependency_wait();
     Team<kCluster> team(sm);
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
     const int nt = team.threads(), me = team.thread(), bs = p.block_size;
@@ -655,6 +657,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 __global__ void __launch_bounds__(128) pool_free_kernel(const PoolParams p, const int32_t *__restrict__ rows)
 {
     __shared__ int s_ctx;
+    ptx::grid_dependency_wait();
     const int r = rows[blockIdx.x];
     if ((uint32_t)r >= (uint32_t)p.num_rows) {
         if (threadIdx.x == 0)
@@ -696,6 +699,7 @@ __global__ void __launch_bounds__(kThreads)
 {
     __shared__ Smem sm;
     ptx::launch_dependents();
+    ptx::grid_dependency_wait();
     Team<kCluster> team(sm);
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
     const int nt = team.threads(), me = team.thread(), N = p.num_blocks;
@@ -831,24 +835,22 @@ Planes planes_of(const PoolArgs &a)
 }
 
 template <typename... P, typename... A>
-int launch_ex(const char *what, void (*kernel)(P...), unsigned grid, unsigned block, unsigned cluster, bool dependent,
-              void *stream, A... args)
+int launch_ex(const char *what, void (*kernel)(P...), unsigned grid, unsigned block, unsigned cluster, void *stream,
+              A... args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    if (dependent) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-    } else {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = cluster;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    }
+    // every kernel here waits for the launch before it (and may be set up during it)
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = dependent || cluster > 1 ? 1 : 0;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -882,12 +884,12 @@ int launch_pool_append(const PoolArgs &a, const int32_t *rows, const int32_t *cu
     auto kernel = many ? (cluster ? pool_append_kernel<true, false> : pool_append_kernel<false, false>)
                        : (cluster ? pool_append_kernel<true, true> : pool_append_kernel<false, true>);
     const unsigned c = cluster ? kClusterCtas : 1;
-    if (int rc = launch_ex("pool append", kernel, c, kThreads, c, false, stream, params_of(a), rows, cu, n, slots,
+    if (int rc = launch_ex("pool append", kernel, c, kThreads, c, stream, params_of(a), rows, cu, n, slots,
                            num_tokens, a.workspace))
         return rc;
     if (!many)
         return PA_OK;
-    return launch_ex("pool slots", pool_slots_kernel, (unsigned)(((int64_t)num_tokens + 1023) / 1024), 256, 1, true, stream,
+    return launch_ex("pool slots", pool_slots_kernel, (unsigned)(((int64_t)num_tokens + 1023) / 1024), 256, 1, stream,
                      params_of(a), rows, cu, n, slots, num_tokens, a.workspace);
 }
 
@@ -899,21 +901,17 @@ int launch_pool_fork(const PoolArgs &a, const int32_t *parents, const int32_t *c
     const Planes q = planes_of(a);
     const bool cluster = search_by_cluster(a);
     const unsigned c = cluster ? kClusterCtas : 1;
-    if (int rc = launch_ex("pool fork", cluster ? pool_fork_kernel<true> : pool_fork_kernel<false>, c, kThreads, c, false,
+    if (int rc = launch_ex("pool fork", cluster ? pool_fork_kernel<true> : pool_fork_kernel<false>, c, kThreads, c,
                            stream, params_of(a), parents, children, n, (int)(q.row_vecs * 16), a.workspace))
         return rc;
     const int64_t units = std::max<int64_t>(n, (int64_t)n * 2 * q.layers * q.pieces);
     return launch_ex("pool fork copy", pool_fork_copy_kernel, (unsigned)std::min<int64_t>(units, (int64_t)sms * 8),
-                     kMoveThreads, 1, true, stream, params_of(a), q, parents, children, a.workspace);
+                     kMoveThreads, 1, stream, params_of(a), q, parents, children, a.workspace);
 }
 
 int launch_pool_free(const PoolArgs &a, const int32_t *rows, int n, void *stream)
 {
-    pool_free_kernel<<<(unsigned)n, 128, 0, static_cast<cudaStream_t>(stream)>>>(params_of(a), rows);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return fail(PA_ERR_CUDA, "pool free launch: %s", cudaGetErrorString(e));
-    return PA_OK;
+    return launch_ex("pool free", pool_free_kernel, (unsigned)n, 128, 1, stream, params_of(a), rows);
 }
 
 int launch_pool_compact(const PoolArgs &a, int32_t *remap, int32_t *tables_out, int32_t *refs_out, void *stream)
@@ -924,14 +922,14 @@ int launch_pool_compact(const PoolArgs &a, int32_t *remap, int32_t *tables_out, 
     const bool cluster = compact_by_cluster(a);
     const unsigned c = cluster ? kClusterCtas : 1;
     if (int rc = launch_ex("pool compact", cluster ? pool_compact_kernel<true> : pool_compact_kernel<false>, c, kThreads,
-                           c, false, stream, params_of(a), remap, refs_out, a.workspace))
+                           c, stream, params_of(a), remap, refs_out, a.workspace))
         return rc;
     const Planes q = planes_of(a);
     const int64_t cells = (int64_t)a.pool.num_rows * a.pool.max_blocks;
     const int64_t units = std::max<int64_t>((cells + kMoveThreads - 1) / kMoveThreads,
                                             (int64_t)(a.dims.num_blocks / 2) * 2 * q.layers * q.pieces);
-    return launch_ex("pool move", pool_move_kernel, (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, sms * 8)), kMoveThreads, 1, true, stream, params_of(a), q,
-                     (const int32_t *)remap, tables_out, a.workspace);
+    return launch_ex("pool move", pool_move_kernel, (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, sms * 8)), kMoveThreads, 1,
+                     stream, params_of(a), q,                     (const int32_t *)remap, tables_out, a.workspace);
 }
 
 int read_pool_error(uint32_t *code)

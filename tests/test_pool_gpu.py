@@ -411,3 +411,42 @@ def test_serving_run(kind):
             ref, a = reference(q, *dense, [range(i * ctx, (i + 1) * ctx) for i in range(B)], [ctx] * B, 1, d ** -0.5)
             assert_within(out, ref, a, f"step {step} layer {layer}")
     assert int((pool.ref_counts > 0).sum()) == n // bs + 2 and (pool.ref_counts[:n // bs + 2] > 0).all()
+
+
+def test_order_with_the_launches_before():
+    """A call may be set up during the launch before it: rows and counts that a kernel or a copy changes right
+    before the call, and the state that the call before leaves, are the ones it reads."""
+    dims, pool, m = both("bf16", layers=2, nb=200, rows=24, width=6, seed=77)
+    rows, cu, slots = i32([0] * 4), i32([0] * 5), torch.zeros(4 * 37, dtype=torch.int32, device="cuda")
+    remap = torch.empty(200, dtype=torch.int32, device="cuda")
+    pinned = torch.zeros(4, dtype=torch.int32).pin_memory()
+    rng = np.random.default_rng(78)
+    torch.cuda.synchronize()
+    for step in range(40):
+        some = [int(x) for x in rng.permutation(12)[:4]]
+        want = i32(some)
+        if step % 2:
+            rows.copy_(want)
+        else:
+            torch.cuda.synchronize()  # (the copy before has read the pinned words)
+            pinned.copy_(torch.tensor(some, dtype=torch.int32))
+            rows.copy_(pinned, non_blocking=True)
+        pa.pa_pool_free(dims, pool, rows)
+        m.free(some)
+        torch.mul(torch.arange(5, dtype=torch.int32, device="cuda"), 1 + step % 37, out=cu)
+        n = 4 * (1 + step % 37)
+        pa.pa_pool_append(dims, pool, rows, cu, slots[:n])
+        m.append(some, [1 + step % 37] * 4)
+        parents = rows.clone()
+        torch.add(rows, 12, out=rows)
+        pa.pa_pool_free(dims, pool, rows)
+        m.free([x + 12 for x in some])
+        pa.pa_pool_fork(dims, pool, parents, rows)
+        assert m.fork(some, [x + 12 for x in some])
+        if step % 5 == 4:
+            pa.pa_pool_compact(dims, pool, remap)
+            m.compact()
+    torch.cuda.synchronize()
+    assert pa.pa_read_device_error() == 0
+    assert_same(pool, m, "end")
+    m.check()

@@ -480,3 +480,89 @@ def test_short_contexts_few_and_many(n, hq, hkv, d):
     cache, dense = int8_pool(nb, bs, hkv, d, 182, ctx, lists)
     out = decode8(dims, q, cache, plan, d ** -0.5)
     assert_within(out, *reference(q, *dense, lists, ctx, bs, d ** -0.5), f"direct int8 {n}")
+
+
+CHAINS = [  # group size, shared blocks, tails: decoded whole, in one launch, in launches side by side
+    (6, 2, [1 + 9 * i for i in range(6)], 0),
+    (5, 70, [1 + 40 * i for i in range(5)], 128),
+    (90, 30, [1 + 7 * i for i in range(90)], 128),
+]
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("case", CHAINS, ids=range(len(CHAINS)))
+def test_order_with_the_launches_before(case, int8):
+    """The launches may be set up during the one before: queries, keys and the plan itself, changed right before a
+    call by a kernel and by a copy, are the ones it reads; in a captured graph too, also behind another stream."""
+    n, sh, tails, split = case
+    bs, hq, hkv, d = 16, 28, 4, 128
+    dims, batches = None, []
+    for seed in (20, 21):  # the same lengths in other blocks
+        ctx, lists, groups, nb = make_batch(seed, [n], [sh], tails, bs)
+        dims = pa.make_dims(nb, bs, hq, hkv, d)
+        batches.append(pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=split))
+    if int8:
+        g = torch.Generator(device="cuda").manual_seed(190)
+        src = [[torch.randint(-127, 128, (nb, bs, hkv, d), generator=g, device="cuda", dtype=torch.int8) for _ in range(2)]
+               for _ in range(2)]
+        scales = [(torch.rand(nb, hkv, bs, generator=g, device="cuda") * 0.03 + 0.002).to(torch.float16) for _ in range(2)]
+    else:
+        src, scales = [[values((nb, bs, hkv, d), 191 + 2 * i + j) for j in range(2)] for i in range(2)], []
+    qs = [values((n, hq, d), 196 + i) for i in range(2)]
+    call = pa.pa_decode_shared_int8 if int8 else pa.pa_decode_shared
+    assert {bool(p.meta.direct) for p in batches} == {split == 0} and {p.meta.apart for p in batches} == {int(n == 90)}
+
+    image = torch.empty(int(max(p.meta.total_bytes for p in batches)), dtype=torch.uint8, device="cuda")
+    for p in batches:
+        p.dev = image
+    q, kv, out = torch.empty_like(qs[0]), [torch.empty_like(x) for x in src[0]], torch.empty_like(qs[0])
+    wss = [pa.shared_workspace(p) for p in batches]
+
+    def step(i, sync):
+        p, c = batches[i & 1], src[i >> 1 & 1]
+        for x, y in zip(kv, c):
+            torch.add(y, 0, out=x)  # kernels
+        torch.mul(qs[i >> 2 & 1], 1, out=q)
+        p.upload()                  # a copy
+        if i & 1:
+            torch.add(c[0], 0, out=kv[0])  # and a kernel between the two
+        if sync:
+            torch.cuda.synchronize()
+        call(dims, q, *kv, *scales, p, d ** -0.5, out, wss[i & 1])
+        return out.clone()
+
+    want = [step(i, True) for i in range(8)]
+    assert len({w.double().sum().item() for w in want}) == 8
+    torch.cuda.synchronize()
+    got = [step(i, False) for i in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    # captured: behind a copy, behind a kernel, behind another stream's work
+    batches[0].upload()
+    pinned = [x.cpu().pin_memory() for x in qs]
+    host_q = torch.empty_like(pinned[0]).pin_memory()
+    side, graph, results = torch.cuda.Stream(), torch.cuda.CUDAGraph(), [torch.empty_like(out) for _ in range(3)]
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        q.copy_(host_q, non_blocking=True)
+        call(dims, q, *kv, *scales, batches[0], d ** -0.5, results[0], wss[0])
+        torch.neg(q, out=q)
+        call(dims, q, *kv, *scales, batches[0], d ** -0.5, results[1], wss[0])
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            q.copy_(host_q, non_blocking=True)
+        torch.cuda.current_stream().wait_stream(side)
+        call(dims, q, *kv, *scales, batches[0], d ** -0.5, results[2], wss[0])
+    for x, y in zip(kv, src[0]):
+        x.copy_(y)
+    for i in range(2):
+        host_q.copy_(pinned[i])
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(results[0], want[4 * i]) and torch.equal(results[2], want[4 * i])
+        q.copy_(-qs[i])
+        call(dims, q, *kv, *scales, batches[0], d ** -0.5, out, wss[0])
+        torch.cuda.synchronize()
+        assert torch.equal(results[1], out)
