@@ -162,6 +162,7 @@ typedef struct pa_shared_meta {
     uint64_t total_bytes;
     uint64_t workspace_bytes;    /* device workspace pa_decode_shared needs */
     uint64_t workspace_bytes_int8; /* and pa_decode_shared_int8: what the items read in fp16 too */
+    int32_t num_heads, num_kv_heads, head_dim, block_size; /* of the dims it was packed for */
 } pa_shared_meta;
 
 /*

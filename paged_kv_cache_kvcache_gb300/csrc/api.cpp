@@ -458,7 +458,9 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
         return PA_OK;
     }
     const int group = dims->num_heads / dims->num_kv_heads;
-    if (meta->rows_per_tile != (kPrefillRows / group > 0 ? kPrefillRows / group : 1))
+    if (meta->num_heads != dims->num_heads || meta->num_kv_heads != dims->num_kv_heads ||
+        meta->head_dim != dims->head_dim || meta->block_size != dims->block_size ||
+        meta->rows_per_tile != (kPrefillRows / group > 0 ? kPrefillRows / group : 1))
         return fail(PA_ERR_INVALID_ARG, "%s: meta was packed for other dims", fn);
     if (!q || !k_cache || !v_cache || !block_tables || !out || !items || !cta_items || !seq_parts ||
         !direct_items || !table_rows || !single_items)

@@ -358,6 +358,10 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     *meta = pa_shared_meta{};
     meta->num_seqs = num_seqs;
     meta->num_groups = num_groups;
+    meta->num_heads = d.num_heads;
+    meta->num_kv_heads = d.num_kv_heads;
+    meta->head_dim = d.head_dim;
+    meta->block_size = bs;
     meta->max_blocks_per_seq = mb;
     meta->num_items = listed;
     meta->apart = apart ? 1 : 0;

@@ -71,7 +71,9 @@ class pa_shared_meta(ctypes.Structure):
                 ("off_single_items", ctypes.c_uint64), ("off_table_rows", ctypes.c_uint64),
                 ("off_direct_items", ctypes.c_uint64), ("off_scratch_tiles", ctypes.c_uint64),
                 ("total_bytes", ctypes.c_uint64),
-                ("workspace_bytes", ctypes.c_uint64), ("workspace_bytes_int8", ctypes.c_uint64)]
+                ("workspace_bytes", ctypes.c_uint64), ("workspace_bytes_int8", ctypes.c_uint64),
+                ("num_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_size", ctypes.c_int32)]
 
 
 class pa_pool(ctypes.Structure):
@@ -187,15 +189,19 @@ def _elsewhere(t, dev: int):
     return ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
 
 
-def _here(*tensors) -> list:
-    """Addresses of tensors (or None); refuses one that is not on the current device (a kernel launched there
-    could not read it)."""
+def _here(plan_device: int, *tensors) -> list:
+    """Addresses of tensors (or None); refuses one that is not on the current device, the plan's (a kernel
+    launched there could not read it), or not contiguous."""
     dev, at = _device(), []
+    if plan_device != dev:
+        raise ValueError(f"the plan is on cuda:{plan_device}, the current device is cuda:{dev}")
     for t in tensors:
         if t is None:
             at.append(None)
         elif t.get_device() != dev:
             raise _elsewhere(t, dev)
+        elif not t.is_contiguous():
+            raise ValueError(f"tensors must be contiguous, got strides {t.stride()}")
         else:
             at.append(t.data_ptr())
     return at
@@ -272,9 +278,12 @@ class DecodePlan(_Plan):
 
 
 class SharedPlan(_Plan):
+    num_rows = 0  # rows that the block table must have
+
     def upload(self, device="cuda", stream=None) -> "SharedPlan":
         super().upload(device, stream)
         m, base = self.meta, self.dev.data_ptr()
+        self.device = self.dev.get_device()
         self.call_ref = ctypes.byref(m)
         self.call_tables = base + m.off_block_tables if m.tables_packed or m.num_seqs == 0 else None
         self.call_arrays = tuple(base + x for x in (m.off_items, m.off_cta_items, m.off_seq_parts, m.off_direct_items,
@@ -367,7 +376,9 @@ def pa_pack_decode_shared(dims: pa_dims, context_lens, group_offsets=None, share
     opt = lambda a: None if a is None else _np_ptr(a)
     args = (ctypes.byref(dims), len(ctx), _np_ptr(ctx), len(groups) - 1, _np_ptr(groups), opt(shared), opt(off),
             opt(ids), opt(rows), int(max_blocks), int(split_tokens))
-    return _pack("pa_pack_decode_shared", pa_shared_meta(), args, into, pin, SharedPlan)
+    plan = _pack("pa_pack_decode_shared", pa_shared_meta(), args, into, pin, SharedPlan)
+    plan.num_rows = len(ctx) if rows is None or len(rows) == 0 else int(rows.max()) + 1
+    return plan
 
 
 def pa_upload(dev_dst, host_src, nbytes: int, stream=None):
@@ -459,8 +470,9 @@ def _shared_tables(plan: SharedPlan, block_tables) -> int:
             raise ValueError("the plan was packed for device tables: pass block_tables")
         return plan.call_tables
     at = _int32(block_tables, "block_tables")
-    if block_tables.dim() != 2 or block_tables.shape[1] != plan.meta.max_blocks_per_seq:
-        raise ValueError(f"block_tables must be [rows, {plan.meta.max_blocks_per_seq}]")
+    if block_tables.dim() != 2 or block_tables.shape[1] != plan.meta.max_blocks_per_seq or \
+            block_tables.shape[0] < plan.num_rows:
+        raise ValueError(f"block_tables must be [{plan.num_rows} rows or more, {plan.meta.max_blocks_per_seq}]")
     return at
 
 
@@ -471,7 +483,7 @@ def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale
     ``block_tables``: the device table a plan without block lists was packed for.
     """
     bt = _shared_tables(plan, block_tables)
-    q, k_cache, v_cache, out, ws, _, _ = _here(q, k_cache, v_cache, out, workspace, block_tables, plan.dev)
+    q, k_cache, v_cache, out, ws, _ = _here(plan.device, q, k_cache, v_cache, out, workspace, block_tables)
     _check((_lib or lib()).pa_decode_shared(ctypes.byref(dims), q, k_cache, v_cache, bt, scale, out, plan.call_ref,
                                             *plan.call_arrays, ws, 0 if ws is None else workspace.numel(),
                                             _stream(stream)), "pa_decode_shared")
@@ -481,8 +493,8 @@ def pa_decode_shared_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, 
                           workspace=None, block_tables=None, stream=None):
     """pa_decode_shared over an INT8 cache (same plan and workspace)."""
     bt = _shared_tables(plan, block_tables)
-    q, k_cache, v_cache, k_scale, v_scale, out, ws, _, _ = _here(q, k_cache, v_cache, k_scale, v_scale, out, workspace,
-                                                                 block_tables, plan.dev)
+    q, k_cache, v_cache, k_scale, v_scale, out, ws, _ = _here(plan.device, q, k_cache, v_cache, k_scale, v_scale, out,
+                                                              workspace, block_tables)
     _check((_lib or lib()).pa_decode_shared_int8(ctypes.byref(dims), q, k_cache, v_cache, k_scale, v_scale, bt, scale,
                                                  out, plan.call_ref, *plan.call_arrays, plan.call_tiles, ws,
                                                  0 if ws is None else workspace.numel(), _stream(stream)),
@@ -533,12 +545,14 @@ class PagePool:
         self.workspace = torch.empty(n.value, dtype=torch.uint8, device=block_tables.device)
         self.ws = (self.workspace.data_ptr(), n.value)
         self.device = block_tables.get_device()
+        self.dims = bytes(dims)
 
-    def here(self) -> int:
-        """The pool's device; refuses a call made with another one current."""
+    def check(self, dims: pa_dims) -> None:
+        """Refuses a call with other dims than the pool's, or made with another device current."""
+        if bytes(dims) != self.dims:
+            raise ValueError("the pool was made with other dims")
         if self.device < 0 or _device() != self.device:
             raise ValueError(f"the pool is on {self.block_tables.device}, which is not the current CUDA device")
-        return self.device
 
     @staticmethod
     def _layers(x, shape, int8):
@@ -560,37 +574,41 @@ def page_pool(dims: pa_dims, k_cache, v_cache, num_rows: int, max_blocks: int, k
 
 def pa_pool_append(dims: pa_dims, pool: PagePool, rows, cu_new, slot_mapping, stream=None):
     """Give row rows[i] its next cu_new[i+1] - cu_new[i] tokens; their slots go to slot_mapping."""
-    dev, n, tokens = pool.here(), rows.numel(), slot_mapping.numel()
-    _check((_lib or lib()).pa_pool_append(ctypes.byref(dims), pool.ref, _int32(rows, "rows", None, dev),
-                                          _int32(cu_new, "cu_new", n + 1, dev), n,
-                                          _int32(slot_mapping, "slot_mapping", None, dev), tokens, *pool.ws,
-                                          _stream(stream)), "pa_pool_append")
+    dev, n, tokens = pool.device, rows.numel(), slot_mapping.numel()
+    args = (_int32(rows, "rows", None, dev), _int32(cu_new, "cu_new", n + 1, dev), n,
+            _int32(slot_mapping, "slot_mapping", None, dev), tokens)
+    pool.check(dims)
+    _check((_lib or lib()).pa_pool_append(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
+           "pa_pool_append")
 
 
 def pa_pool_fork(dims: pa_dims, pool: PagePool, parents, children, stream=None):
     """Row children[i] shares row parents[i]'s full pages and gets a copy of its partly filled one."""
-    dev, n = pool.here(), children.numel()
-    _check((_lib or lib()).pa_pool_fork(ctypes.byref(dims), pool.ref, _int32(parents, "parents", n, dev),
-                                        _int32(children, "children", None, dev), n, *pool.ws, _stream(stream)),
-           "pa_pool_fork")
+    dev, n = pool.device, children.numel()
+    args = (_int32(parents, "parents", n, dev), _int32(children, "children", None, dev), n)
+    pool.check(dims)
+    _check((_lib or lib()).pa_pool_fork(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)), "pa_pool_fork")
 
 
 def pa_pool_free(dims: pa_dims, pool: PagePool, rows, stream=None):
     """Empty the rows and give their pages back."""
-    _check((_lib or lib()).pa_pool_free(ctypes.byref(dims), pool.ref, _int32(rows, "rows", None, pool.here()),
-                                        rows.numel(), _stream(stream)), "pa_pool_free")
+    at = _int32(rows, "rows", None, pool.device)
+    pool.check(dims)
+    _check((_lib or lib()).pa_pool_free(ctypes.byref(dims), pool.ref, at, rows.numel(), _stream(stream)),
+           "pa_pool_free")
 
 
 def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None, ref_counts_out=None, stream=None):
     """Move the used pages to the lowest ids; remap[p] is page p's new id.  Tables and counts are rewritten in
     place, or into the given arrays."""
-    dev = pool.here()
+    dev = pool.device
     tables = pool.block_tables if block_tables_out is None else block_tables_out
     refs = pool.ref_counts if ref_counts_out is None else ref_counts_out
     pages = pool.ref_counts.numel()
-    _check((_lib or lib()).pa_pool_compact(ctypes.byref(dims), pool.ref, _int32(remap, "remap", pages, dev),
-                                           _int32(tables, "block_tables_out", pool.block_tables.numel(), dev),
-                                           _int32(refs, "ref_counts_out", pages, dev), *pool.ws, _stream(stream)),
+    args = (_int32(remap, "remap", pages, dev), _int32(tables, "block_tables_out", pool.block_tables.numel(), dev),
+            _int32(refs, "ref_counts_out", pages, dev))
+    pool.check(dims)
+    _check((_lib or lib()).pa_pool_compact(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
            "pa_pool_compact")
 
 

@@ -123,5 +123,12 @@ def test_page_pool_checks_its_tensors():
                 lambda: pa.pa_pool_fork(dims, pool, i32(2), i32(1)),
                 lambda: pa.pa_pool_free(dims, pool, i32(2).long()),
                 lambda: pa.pa_pool_compact(dims, pool, i32(5))):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="expected|must|agree|go together"):
             bad()
+    more = pa.make_dims(7, 16, 2, 2, 64)
+    for bad in (lambda: pa.pa_pool_append(more, pool, i32(2), i32(3), i32(4)), lambda: pa.pa_pool_free(more, pool, i32(2)),
+                lambda: pa.pa_pool_fork(more, pool, i32(2), i32(2)), lambda: pa.pa_pool_compact(more, pool, i32(6))):
+        with pytest.raises(ValueError, match="other dims"):
+            bad()
+    with pytest.raises(ValueError, match="current CUDA device"):
+        pa.pa_pool_free(dims, pool, i32(2))

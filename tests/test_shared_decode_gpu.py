@@ -284,6 +284,10 @@ def test_tensors_of_the_host_are_refused():
                  (q, kc, kc, out, ws.cpu())):
         with pytest.raises(ValueError):
             pa.pa_decode_shared(dims, args[0], args[1], args[2], plan, 0.1, args[3], args[4])
+    wide = values((2, 3, 64), 2)[:, :2]                       # heads of a larger tensor
+    for args in ((wide, kc, kc, out), (q, kc.transpose(0, 1), kc, out), (q, kc, kc, wide)):
+        with pytest.raises(ValueError, match="contiguous"):
+            pa.pa_decode_shared(dims, *args[:3], plan, 0.1, args[3], ws)
 
 
 @pytest.mark.parametrize("split", [0, 128])

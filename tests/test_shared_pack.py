@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 from paged_kv_cache_kvcache_gb300 import pagedattn as pa
 
@@ -227,6 +228,7 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     m.num_seqs, m.num_items, m.num_ctas, m.max_blocks_per_seq, m.rows_per_tile = 0, 0, 0, 1, 64
     assert call() == pa.PA_OK                                   # nothing to do
     m.num_seqs, m.num_items, m.num_ctas = 2, 4, 4
+    m.num_heads, m.num_kv_heads, m.head_dim, m.block_size = 4, 2, 64, 16
     for bad in (0.0, -1.0, float("inf"), float("nan")):
         assert call(scale=bad) == pa.PA_ERR_INVALID_ARG
     assert call(q=None) == pa.PA_ERR_INVALID_ARG
@@ -234,6 +236,8 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     assert call(items=24) == pa.PA_ERR_INVALID_ARG
     assert call(bt=None) == call(whole=None) == call(whole=8) == call(rows=None) == call(rows=18) == call(ones=None) == call(ones=8) == pa.PA_ERR_INVALID_ARG
     assert call(dims=pa.make_dims(8, 16, 8, 2, 64)) == pa.PA_ERR_INVALID_ARG   # packed for group 2
+    for other in ((8, 16, 2, 1, 64), (8, 16, 8, 4, 64), (8, 16, 4, 2, 128), (8, 32, 4, 2, 64)):  # or for other heads or blocks
+        assert call(dims=pa.make_dims(*other)) == pa.PA_ERR_INVALID_ARG
     assert call(dims=pa.make_dims(0, 16, 4, 2, 64)) == pa.PA_ERR_INVALID_ARG   # empty pool
     m.num_partials, m.workspace_bytes, m.workspace_bytes_int8 = 3, 1024 * 3 + 256, 1024 * 3 + 256
     assert call(ws=256, nbytes=1024) == pa.PA_ERR_WORKSPACE
@@ -263,3 +267,16 @@ def test_shared_decode_rejects_bad_args_without_touching_the_gpu():
     assert call8() == pa.PA_ERR_INVALID_ARG
     m.num_ctas = 0
     assert call(ws=256, nbytes=4096) == pa.PA_ERR_INVALID_ARG
+
+
+def test_a_plan_keeps_its_dims_and_its_rows():
+    dims = pa.make_dims(64, 16, 4, 2, 64)
+    plan = pa.pa_pack_decode_shared(dims, [100, 70], shared_lens=[48], table_rows=[5, 2], max_blocks=7, pin=False)
+    m = plan.meta
+    assert (m.num_heads, m.num_kv_heads, m.head_dim, m.block_size) == (4, 2, 64, 16) and plan.num_rows == 6
+    assert pa.pa_pack_decode_shared(dims, [100, 70], shared_lens=[48], max_blocks=7, pin=False).num_rows == 2
+    plan.dev = torch.zeros(1, dtype=torch.uint8)
+    for bad in (torch.zeros(5, 7), torch.zeros(6, 8), torch.zeros(42)):
+        with pytest.raises(ValueError):
+            pa._shared_tables(plan, bad.int())
+    assert pa._shared_tables(plan, torch.zeros(6, 7, dtype=torch.int32))
