@@ -20,7 +20,7 @@
 // row): a prefix part carries many sequences, a suffix part one.  A CTA holds two query tiles of
 // 128 rows and runs its items in two ways:
 //  * a prefix part of more than 128 rows is a PAIR: both tiles against one stream of K/V, bound
-//    by the tensor core (measured 1.75 us per 128 keys);
+//    by the tensor core (measured 1.62 us per 128 keys, of which the products are 1.0);
 //  * every other part is a SINGLE: one tile, 128 keys whose products take about 1100 cycles of the
 //    tensor core while their 64 KB of K/V take about 2800 cycles of this SM's share of HBM.  But
 //    score product, softmax and value product of one tile follow one another (about 2700 cycles
@@ -34,7 +34,7 @@
 // back through tensor memory), one softmax warpgroup per tile; the rings run on across items.
 //
 // INT8 cache.  A launch before turns what the shared parts read into fp16, once for all query
-// tiles and heads: keys and values (code * scale, rounded by 2^-12 at most; fp16 holds them to
+// tiles and heads: keys and values (code * scale, rounded by 2^-11 of it at most; fp16 holds them to
 // 65504) and the queries.  The products then run as on a bf16 cache, with fp16 weights.  (Exact
 // codes with the scales in the softmax took 3.4 us per 128 keys and pair instead of 1.6: 64 more
 // 16-byte loads per row; converting in shared memory took 4.2.)
@@ -238,8 +238,10 @@ struct CodesParams {
 };
 
 // What the products of the CTAs' lists read on an INT8 cache, in fp16: the shared prefixes' (and,
-// where single sequences do not run apart, the other) keys and values (code * scale; 16 keys per CTA, K and V) and the queries.  Rows behind the last key and
-// those of block ids outside the pool become zeros.  Bound by HBM: 1 byte read and 2 written per code.
+// where single sequences do not run apart, the other) keys and values (code * scale; 16 keys per
+// CTA, K and V) and the queries.  Rows behind the last key and those of block ids outside the pool
+// become zeros.  1 byte read and 2 written (to L2) per code; bound by its chain of three dependent
+// loads: 11 us cold for 16384 keys of 4 heads, 17 MB read and 34 MB written.
 constexpr int kCodesKeys = 16;
 __global__ void __launch_bounds__(256) shared_codes_kernel(const CodesParams p)
 {
@@ -772,8 +774,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m_ref = m_new;
                     }
                     // P = 2^(s * scale * log2 e - m) written over S as pairs of the values' own type: bf16 (weights
-                    // in [0, 2^8], each rounded by 2^-9 of it at most), or fp16 with 2^kBias times the weight
-                    // (2^-12; the weights that fp16 cannot hold, below 2^-31 of the largest, are lost: 2^-16 of
+                    // in [0, 2^8], each rounded by 2^-8 of it at most), or fp16 with 2^kBias times the weight
+                    // (2^-11; the weights that fp16 cannot hold, below 2^-31 of the largest, are lost: 2^-16 of
                     // the sum over 32768 keys).  The row sum stays fp32.
                     const uint64_t sl2x2 = ptx::f2(sl2, sl2);
                     const float negm = m_ref == -INFINITY ? 0.f : kBias - m_ref;
@@ -1157,7 +1159,9 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    auto combine = split == 1 ? shared_combine_kernel<D, 1> : split == 4 ? shared_combine_kernel<D, 4> : shared_combine_kernel<D, 8>;
+    auto combine = split == 1   ? shared_combine_kernel<D, 1>
+                   : split == 4 ? shared_combine_kernel<D, 4>
+                                : shared_combine_kernel<D, 8>;
     const cudaError_t e =
         cudaLaunchKernelEx(&cfg, combine, (const float *)a.part_o, (const float *)a.part_lse,
                            reinterpret_cast<const int2 *>(a.seq_parts), static_cast<__nv_bfloat16 *>(a.out),

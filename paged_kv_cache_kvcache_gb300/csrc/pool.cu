@@ -928,8 +928,8 @@ int launch_pool_compact(const PoolArgs &a, int32_t *remap, int32_t *tables_out, 
     const int64_t cells = (int64_t)a.pool.num_rows * a.pool.max_blocks;
     const int64_t units = std::max<int64_t>((cells + kMoveThreads - 1) / kMoveThreads,
                                             (int64_t)(a.dims.num_blocks / 2) * 2 * q.layers * q.pieces);
-    return launch_ex("pool move", pool_move_kernel, (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, sms * 8)), kMoveThreads, 1,
-                     stream, params_of(a), q,                     (const int32_t *)remap, tables_out, a.workspace);
+    return launch_ex("pool move", pool_move_kernel, (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, sms * 8)),
+                     kMoveThreads, 1, stream, params_of(a), q, (const int32_t *)remap, tables_out, a.workspace);
 }
 
 int read_pool_error(uint32_t *code)

@@ -24,8 +24,8 @@ EXPORTS = ("pa_pack_prefill", "pa_pack_decode", "pa_upload", "pa_store_kvcache",
            "pa_decode", "pa_decode_static", "pa_copy_blocks", "pa_store_kvcache_int8", "pa_decode_int8",
            "pa_prefill_varlen_int8", "pa_pack_decode_fixed", "pa_decode_fused", "pa_copy_blocks_int8",
            "pa_decode_int8_fused", "pa_prefill_varlen_fused", "pa_prefill_varlen_int8_fused",
-           "pa_pack_decode_shared", "pa_decode_shared", "pa_decode_shared_int8", "pa_pool_workspace", "pa_pool_append", "pa_pool_fork",
-           "pa_pool_free", "pa_pool_compact",
+           "pa_pack_decode_shared", "pa_decode_shared", "pa_decode_shared_int8", "pa_pool_workspace", "pa_pool_append",
+           "pa_pool_fork", "pa_pool_free", "pa_pool_compact",
            "pa_last_error_string", "pa_read_device_error", "pa_selftest_bounded_wait", "pa_stream_read",
            "pa_version")
 

@@ -5,6 +5,9 @@ bf16 before the value product (at most 2^-8 of each weight) and the result once 
 it); everything else is fp32 (scores of up to 128 products and a few hundred in magnitude,
 2^-24 each: below 2e-4 of the weights).  With a = sum_j w_j |v_j| >= |out|:
     |err| <= 2^-8 (a + |out|) + 2e-4 a.
+On an INT8 cache the weights and the products' values are fp16 (2^-11 each), which leaves 2^-8 a - 2^-10 a for the
+scores' error d: |err| <= 2 d a, so d up to 1.4e-3.  It comes from the keys' fp16 rounding, 2^-11 / sqrt(3) of each
+product in the mean, with signs of its own: about 3e-4 for the sums of 64 and 128 products here.
 """
 import numpy as np
 import pytest
