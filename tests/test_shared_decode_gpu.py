@@ -573,3 +573,34 @@ def test_order_with_the_launches_before(case, int8):
         call(dims, q, *kv, *scales, batches[0], d ** -0.5, out, wss[0])
         torch.cuda.synchronize()
         assert torch.equal(results[1], out)
+
+
+@pytest.mark.parametrize("case", CHAINS, ids=range(len(CHAINS)))
+def test_padded_batch_and_a_row_named_twice(case):
+    """Rows of q and out behind the last sequence are neither read nor written; sequences may name one table row."""
+    n, sh, tails, split = case
+    bs, hq, hkv, d = 16, 28, 4, 128
+    ctx, lists, groups, nb = make_batch(30, [n], [sh], tails, bs)
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    kc, vc = pool(nb, bs, hkv, d, 200, ctx, lists)
+    cache, dense = int8_pool(nb, bs, hkv, d, 201, ctx, lists)
+    width = max(len(x) for x in lists) + 1
+    table = torch.full((n + 2, width), -1, dtype=torch.int32)
+    for b, x in enumerate(lists):
+        table[b + 1, :len(x)] = torch.tensor(np.asarray(x, np.int32))
+    rows = [b + 1 for b in range(n)]
+    rows[n - 2], ctx[n - 2], lists[n - 2] = rows[n - 1], ctx[n - 1] - 1, lists[n - 1]  # one token behind its twin
+    plan = pa.pa_pack_decode_shared(dims, ctx, groups, shared_lens=[sh * bs], table_rows=rows, max_blocks=width,
+                                    split_tokens=split).upload()
+    q = values((n + 3, hq, d), 202)
+    q[n:] = float("nan")
+    ws, bt = pa.shared_workspace(plan), table.cuda()
+    for int8 in (False, True):
+        out = torch.full_like(q, 7.0)
+        if int8:
+            pa.pa_decode_shared_int8(dims, q, *cache, plan, d ** -0.5, out, ws, block_tables=bt)
+        else:
+            pa.pa_decode_shared(dims, q, kc, vc, plan, d ** -0.5, out, ws, block_tables=bt)
+        ref, a = reference(q[:n], *(dense if int8 else (kc, vc)), lists, ctx, bs, d ** -0.5)
+        assert_within(out[:n], ref, a, f"padded {case[:2]} int8 {int8}")
+        assert (out[n:] == 7.0).all()
