@@ -177,47 +177,66 @@ struct PoolParams {
     int32_t row_tokens; // most tokens a row can hold (an int32 with room for a page)
 };
 
-// Counts of 16 consecutive ids; those past the pool count as used.
-__device__ __forceinline__ void load_refs(const PoolParams &p, int id, int4 (&r)[kIds / 4])
+// A round looks at `words` (up to kIds) ids per thread, as few as one round of all threads needs.  A
+// warp's 32 * words consecutive ids begin at first_id; its lane has the ids + 32 e + lane, so that what
+// it reads and writes for them is contiguous (16 consecutive ids per thread took 9 us of a round for
+// the list of 16384 free pages alone, each store of a warp touching 32 sectors).
+template <bool kCluster>
+__device__ __forceinline__ int round_words(const Team<kCluster> &team, const PoolParams &p)
 {
+    return min(kIds, (p.num_blocks + team.threads() - 1) / team.threads());
+}
+template <bool kCluster>
+__device__ __forceinline__ int first_id(const Team<kCluster> &team, const PoolParams &p, int words, int64_t base)
+{
+    return (int)min(base + (int64_t)(team.thread() & ~31) * words, (int64_t)p.num_blocks);
+}
+// Counts of this lane's ids; those past the pool count as used.
+__device__ __forceinline__ void load_refs(const PoolParams &p, int words, int first, int (&r)[kIds])
+{
+    const int left = p.num_blocks - first - (int)(threadIdx.x & 31u);
+    const int32_t *at = p.refs + first + (threadIdx.x & 31u);
 #pragma unroll
-    for (int i = 0; i < kIds / 4; ++i) {
-        const int at = id + 4 * i;
-        r[i] = make_int4(1, 1, 1, 1);
-        if (at + 4 <= p.num_blocks) {
-            r[i] = *reinterpret_cast<const int4 *>(p.refs + at); // 16-byte aligned: checked on the host
-        } else if (at < p.num_blocks) {
-            r[i].x = p.refs[at];
-            r[i].y = at + 1 < p.num_blocks ? p.refs[at + 1] : 1;
-            r[i].z = at + 2 < p.num_blocks ? p.refs[at + 2] : 1;
-        }
+    for (int e = 0; e < kIds; ++e) {
+        if (e >= words)
+            break;
+        r[e] = 32 * e < left ? at[32 * e] : 1;
     }
 }
-__device__ __forceinline__ uint32_t free_mask(const int4 (&r)[kIds / 4])
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < kIds / 4; ++i)
-        m |= (uint32_t)((r[i].x == 0) | (r[i].y == 0) << 1 | (r[i].z == 0) << 2 | (r[i].w == 0) << 3) << (4 * i);
-    return m;
-}
+__device__ __forceinline__ uint32_t lanes_below() { return (1u << (threadIdx.x & 31u)) - 1u; }
 
 // The lowest `want` ids of count 0 into list; returns how many there are (at most want).  `r`:
 // the counts of this thread's ids of the first round, loaded by the caller ahead of time.
 template <bool kCluster>
-__device__ int lowest_free(Team<kCluster> &team, const PoolParams &p, int want, int32_t *list, int4 (&r)[kIds / 4])
+__device__ int lowest_free(Team<kCluster> &team, const PoolParams &p, int want, int32_t *list, int (&r)[kIds])
 {
-    const int per_round = team.threads() * kIds;
+    const int words = round_words(team, p);
+    const int lane = threadIdx.x & 31;
     int found = 0;
-    for (int64_t base = 0; base < p.num_blocks && found < want; base += per_round) {
-        const int id = (int)min(base + (int64_t)team.thread() * kIds, (int64_t)p.num_blocks);
+    for (int64_t base = 0; base < p.num_blocks && found < want; base += (int64_t)team.threads() * words) {
+        const int first = first_id(team, p, words, base);
         if (base > 0)
-            load_refs(p, id, r);
-        uint32_t m = free_mask(r);
+            load_refs(p, words, first, r);
+        uint32_t m[kIds];
+        int mine = 0;
+#pragma unroll
+        for (int e = 0; e < kIds; ++e) {
+            if (e >= words)
+                break;
+            m[e] = __ballot_sync(0xffffffffu, r[e] == 0);
+            mine += __popc(m[e]);
+        }
         int sum;
-        int at = found + team.scan(__popc(m), &sum);
-        for (; m && at < want; m &= m - 1)
-            list[at++] = id + __ffs(m) - 1;
+        int at = found + __shfl_sync(0xffffffffu, team.scan(lane == 0 ? mine : 0, &sum), 0);
+#pragma unroll
+        for (int e = 0; e < kIds; ++e) {
+            if (e >= words || at >= want)
+                break;
+            const int k = at + __popc(m[e] & lanes_below());
+            if ((m[e] >> lane & 1u) && k < want)
+                list[k] = first + 32 * e + lane;
+            at += __popc(m[e]);
+        }
         found += sum;
     }
     return min(found, want);
@@ -268,9 +287,10 @@ __device__ __forceinline__ int last_at_most_warp(const int32_t *a, int n, int x)
 
 // What the planning kernels begin with: shared memory cleared, this thread's counts on their way.
 template <bool kCluster>
-__device__ __forceinline__ void plan_begin(Team<kCluster> &team, const PoolParams &p, int4 (&refs)[kIds / 4])
+__device__ __forceinline__ void plan_begin(Team<kCluster> &team, const PoolParams &p, int (&refs)[kIds])
 {
-    load_refs(p, (int)min((int64_t)team.thread() * kIds, (int64_t)p.num_blocks), refs);
+    const int per_thread = round_words(team, p);
+    load_refs(p, per_thread, first_id(team, p, per_thread, 0), refs);
     const int words = (min(p.num_rows, kRowBits) + 31) / 32;
     if (team.rank() == 0)
         for (int i = threadIdx.x; i < words; i += kThreads)
@@ -302,7 +322,7 @@ __global__ void __launch_bounds__(kThreads)
     Team<kCluster> team(sm);
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
     const int nt = team.threads(), me = team.thread(), bs = p.block_size;
-    int4 refs[kIds / 4];
+    int refs[kIds];
     plan_begin(team, p, refs);
     const bool small = n <= kThreads; // the rows' counts stay in shared memory
     int32_t *starts = small ? sm.starts : w.starts, *lens = small ? sm.lens : w.lens;
@@ -449,7 +469,7 @@ __global__ void __launch_bounds__(kThreads)
     Team<kCluster> team(sm);
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
     const int nt = team.threads(), me = team.thread(), bs = p.block_size;
-    int4 refs[kIds / 4];
+    int refs[kIds];
     plan_begin(team, p, refs);
     const bool small = n <= kThreads;
     int32_t *starts = small ? sm.starts : w.starts, *lens = small ? sm.lens : w.lens;
@@ -703,28 +723,47 @@ __global__ void __launch_bounds__(kThreads)
     Team<kCluster> team(sm);
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
     const int nt = team.threads(), me = team.thread(), N = p.num_blocks;
-    const int per_round = nt * kIds;
-    int4 refs[kIds / 4];
-    // U and, where one round holds all ids, u(this thread's first id)
+    const int words = round_words(team, p), lane = threadIdx.x & 31;
+    const int64_t per_round = (int64_t)nt * words;
+    uint32_t used[kIds]; // of this warp's ids: lane l of word e is id first + 32 e + l
+    auto look = [&](int first) {
+        int refs[kIds];
+        load_refs(p, words, first, refs);
+        int sum = 0;
+#pragma unroll
+        for (int e = 0; e < kIds; ++e) {
+            if (e >= words)
+                break;
+            used[e] = __ballot_sync(0xffffffffu, refs[e] != 0 && 32 * e + lane < N - first);
+            sum += __popc(used[e]);
+        }
+        return sum;
+    };
+    // sum over the warps before this one, of a value that its lanes agree on
+    auto before_warp = [&](int v, int *total) { return __shfl_sync(0xffffffffu, team.scan(lane == 0 ? v : 0, total), 0); };
+    // U and, where one round holds all ids, u(this warp's first id)
     int mine = 0;
     const bool one = N <= per_round;
-    for (int64_t base = 0; base < N; base += per_round) {
-        const int id = (int)min(base + (int64_t)me * kIds, (int64_t)N);
-        load_refs(p, id, refs);
-        mine += min(kIds, N - id) - __popc(free_mask(refs));
-    }
-    int U, before = team.scan(mine, &U);
-    // u(U): by the thread that holds id U, in the round that holds it
+    for (int64_t base = 0; base < N; base += per_round)
+        mine += look(first_id(team, p, words, base));
+    int U, before = before_warp(mine, &U);
+    // u(U): by the warp that holds id U, in the round that holds it
     int seen = 0;
     for (int64_t base = 0; base < N; base += per_round) {
-        const int id = (int)min(base + (int64_t)me * kIds, (int64_t)N);
+        const int first = first_id(team, p, words, base);
         int sum = U;
-        if (!one) {
-            load_refs(p, id, refs);
-            before = seen + team.scan(min(kIds, N - id) - __popc(free_mask(refs)), &sum);
+        if (!one)
+            before = seen + before_warp(look(first), &sum);
+        const int at = U - first;
+        if (at >= 0 && at < 32 * words && U < N) {
+            int u = before;
+#pragma unroll
+            for (int e = 0; e < kIds; ++e)
+                if (e <= at >> 5)
+                    u += __popc(e < at >> 5 ? used[e] : used[e] & ((1u << (at & 31)) - 1u));
+            if (lane == 0)
+                w.head[2] = u;
         }
-        if (id <= U && U < id + kIds && id < N)
-            w.head[2] = before + __popc(~free_mask(refs) & ((1u << (U - id)) - 1u));
         seen += sum;
     }
     if (me == 0 && U == N)
@@ -733,29 +772,31 @@ __global__ void __launch_bounds__(kThreads)
     const int below = w.head[2];
     seen = 0;
     for (int64_t base = 0; base < N; base += per_round) {
-        const int id = (int)min(base + (int64_t)me * kIds, (int64_t)N);
-        int sum;
+        const int first = first_id(team, p, words, base);
         if (!one) {
-            load_refs(p, id, refs);
-            before = seen + team.scan(min(kIds, N - id) - __popc(free_mask(refs)), &sum);
+            int sum;
+            before = seen + before_warp(look(first), &sum);
             seen += sum;
         }
-        const uint32_t m = free_mask(refs);
-        int u = before;
-        for (int e = 0; e < kIds && id + e < N; ++e) {
-            const bool is_free = m >> e & 1u;
-            const int x = id + e;
-            if (is_free) {
-                if (x < U)
-                    w.list[x - u] = x;
-                remap[x] = -1;
-            } else {
-                if (x >= U)
-                    w.list2[u - below] = x;
-                else
-                    remap[x] = x;
-                ++u;
+        int u0 = before;
+#pragma unroll
+        for (int e = 0; e < kIds; ++e) {
+            if (e >= words)
+                break;
+            if (32 * e + lane < N - first) {
+                const int x = first + 32 * e + lane, u = u0 + __popc(used[e] & lanes_below());
+                if (used[e] >> lane & 1u) {
+                    if (x >= U)
+                        w.list2[u - below] = x;
+                    else
+                        remap[x] = x;
+                } else {
+                    if (x < U)
+                        w.list[x - u] = x;
+                    remap[x] = -1;
+                }
             }
+            u0 += __popc(used[e]);
         }
     }
     const int moves = U - below;
