@@ -900,14 +900,14 @@ int launch_ex(const char *what, void (*kernel)(P...), unsigned grid, unsigned bl
     return PA_OK;
 }
 
-// One CTA looks through 16384 ids in a round, a cluster through 131072, but it takes 2.5 us more to
-// start and meet.  A search for free pages ends when it has found enough: a round over pages in use
-// costs one CTA 1.6 us, so in a pool half full the two meet at 3 rounds (8 tokens appended to 8
-// rows, then freed, one CTA against the cluster: 49152 pages 9.9 / 10.9 us, 131072 14.9 / 10.9).
-// A compaction goes through all ids three times and writes them all, 14 us a round (16384 pages
-// 14.9 / 16.4 us, 24000 24.1 / 16.5, 49152 44.4 / 16.9).
+// One CTA looks through 16384 ids in a round, a cluster through 131072, but it takes 2 us more to
+// start and meet.  A search for free pages ends when it has found enough.  8 tokens appended to 8
+// rows, then freed, one CTA against the cluster, in a pool empty / half full / 0.95 full: 32768 pages
+// 7.2 / 10.2 / 10.9 us against 9.3 / 9.8 / 9.9, 49152 pages 7.0 / 10.8 / 12.7 against 9.4 / 10.1 / 9.3.
+// A compaction goes through all ids, three times if they take several rounds: 8192 pages 6.3 us
+// against 7.8, 16384 pages 8.3 / 8.1, 32768 pages 19.1 / 8.7.
 constexpr int kRoundIds = kThreads * kIds;
-bool search_by_cluster(const PoolArgs &a) { return a.dims.num_blocks > 3 * kRoundIds; }
+bool search_by_cluster(const PoolArgs &a) { return a.dims.num_blocks > 2 * kRoundIds; }
 bool compact_by_cluster(const PoolArgs &a) { return a.dims.num_blocks > kRoundIds; }
 
 } // namespace

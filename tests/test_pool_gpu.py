@@ -450,3 +450,27 @@ def test_order_with_the_launches_before():
     assert pa.pa_read_device_error() == 0
     assert_same(pool, m, "end")
     m.check()
+
+
+@pytest.mark.parametrize("nb", [31, 32, 33, 1023, 1024, 1025, 2049, 8193, 16383, 16384, 16385, 32768, 32769, 131072, 131073])
+def test_sizes_around_the_words_and_rounds_of_ids(nb):
+    """A search and a compaction where warps, CTAs and rounds end, with the border between kept and moved pages at
+    and beside a word's ends."""
+    for used in sorted({1, min(32, nb), min(33, nb), nb // 2 // 32 * 32 or 1, nb // 2 + 1, nb - 1, nb}):
+        dims, pool, m = both(layers=1, nb=nb, bs=16, hkv=1, d=64, rows=3, width=max(nb, 4), seed=6)
+        rng = np.random.default_rng(nb * 7 + used)
+        ids = np.sort(rng.permutation(nb)[:used]).astype(np.int32)
+        m.tables[0, :used], m.ctx[0], m.refs[ids] = ids, 16 * used, 1
+        pool.block_tables.copy_(i32(m.tables)), pool.context_lens.copy_(i32(m.ctx)), pool.ref_counts.copy_(i32(m.refs))
+        n = min(nb - used, 70)
+        assert append(dims, pool, m, [1], [16 * n])
+        assert np.array_equal(pool.block_tables[1].cpu().numpy(), m.tables[1])
+        pa.pa_pool_free(dims, pool, i32([1]))
+        m.free([1])
+        if used < nb:  # one page too many is refused
+            assert not append(dims, pool, m, [1], [16 * (nb - used) + 1])
+            assert pa.pa_read_device_error() == NO_ROOM
+        remap = torch.empty(nb, dtype=torch.int32, device="cuda")
+        pa.pa_pool_compact(dims, pool, remap)
+        assert np.array_equal(remap.cpu().numpy(), m.compact())
+        assert_same(pool, m, f"compact {nb} {used}")
