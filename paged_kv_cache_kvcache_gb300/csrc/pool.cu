@@ -69,7 +69,7 @@ constexpr int kWsRowInts = 8, kWsBlockInts = 2;
 
 struct Smem {
     int warp[2][kWarps];
-    int total[2];          // this CTA's total of a scan, by scan parity
+    int total[2][kClusterCtas]; // the CTAs' totals of a scan, by scan parity
     int bad;               // first CTA: refusal bits
     int want;              // and pages the call needs
     uint32_t bits[kRowBits / 32];
@@ -133,12 +133,14 @@ struct Team {
             *total = mine;
             return before;
         }
-        if (threadIdx.x == 0)
-            s.total[turn] = mine;
+        // every CTA tells every other (all threads reading all totals from there took 2 us)
+        if (threadIdx.x < kClusterCtas)
+            *cg::this_cluster().map_shared_rank(&s.total[turn][rank()], threadIdx.x) = mine;
         sync();
         int base = 0, sum = 0;
-        for (int c = 0; c < ctas(); ++c) {
-            const int t = *cg::this_cluster().map_shared_rank(&s.total[turn], c);
+#pragma unroll
+        for (int c = 0; c < kClusterCtas; ++c) {
+            const int t = s.total[turn][c];
             base += c < rank() ? t : 0;
             sum += t;
         }
