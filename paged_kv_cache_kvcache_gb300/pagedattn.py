@@ -181,30 +181,28 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
-def _device() -> int:
-    return _cur_device() if _cur_device is not None else torch.cuda.current_device()
+_device = _cur_device if _cur_device is not None else torch.cuda.current_device
 
 
 def _elsewhere(t, dev: int):
     return ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
 
 
-def _here(plan_device: int, *tensors) -> list:
-    """Addresses of tensors (or None); refuses one that is not on the current device, the plan's (a kernel
-    launched there could not read it), or not contiguous."""
-    dev, at = _device(), []
+def _refuse(plan_device: int, *tensors) -> None:
+    """Why a call's plan and tensors are refused (the calls test for it themselves: a loop here is 0.2 us a tensor)."""
+    dev = _device()
     if plan_device != dev:
         raise ValueError(f"the plan is on cuda:{plan_device}, the current device is cuda:{dev}")
     for t in tensors:
-        if t is None:
-            at.append(None)
-        elif t.get_device() != dev:
+        if t is not None and t.get_device() != dev:  # a kernel launched on this device could not read it
             raise _elsewhere(t, dev)
-        elif not t.is_contiguous():
+        if t is not None and not t.is_contiguous():
             raise ValueError(f"tensors must be contiguous, got strides {t.stride()}")
-        else:
-            at.append(t.data_ptr())
-    return at
+
+
+def _stream_of(dev: int, stream) -> Optional[int]:
+    """_stream on a device that is known and in use."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def _int32(t, what: str, count: Optional[int] = None, dev: Optional[int] = None) -> int:
@@ -482,23 +480,38 @@ def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale
 
     ``block_tables``: the device table a plan without block lists was packed for.
     """
-    bt = _shared_tables(plan, block_tables)
-    q, k_cache, v_cache, out, ws, _ = _here(plan.device, q, k_cache, v_cache, out, workspace, block_tables)
-    _check((_lib or lib()).pa_decode_shared(ctypes.byref(dims), q, k_cache, v_cache, bt, scale, out, plan.call_ref,
-                                            *plan.call_arrays, ws, 0 if ws is None else workspace.numel(),
-                                            _stream(stream)), "pa_decode_shared")
+    bt, dev = _shared_tables(plan, block_tables), _device()
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    if not (plan.device == dev == q.get_device() == k_cache.get_device() == v_cache.get_device() == out.get_device()
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and out.is_contiguous()
+            and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
+            and (block_tables is None or block_tables.get_device() == dev)):
+        _refuse(plan.device, q, k_cache, v_cache, out, workspace, block_tables)
+    rc = (_lib or lib()).pa_decode_shared(ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), bt,
+                                          scale, out.data_ptr(), plan.call_ref, *plan.call_arrays, ws, ws_bytes,
+                                          _stream_of(dev, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_decode_shared")
 
 
 def pa_decode_shared_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, plan: SharedPlan, scale: float, out,
                           workspace=None, block_tables=None, stream=None):
     """pa_decode_shared over an INT8 cache (same plan and workspace)."""
-    bt = _shared_tables(plan, block_tables)
-    q, k_cache, v_cache, k_scale, v_scale, out, ws, _ = _here(plan.device, q, k_cache, v_cache, k_scale, v_scale, out,
-                                                              workspace, block_tables)
-    _check((_lib or lib()).pa_decode_shared_int8(ctypes.byref(dims), q, k_cache, v_cache, k_scale, v_scale, bt, scale,
-                                                 out, plan.call_ref, *plan.call_arrays, plan.call_tiles, ws,
-                                                 0 if ws is None else workspace.numel(), _stream(stream)),
-           "pa_decode_shared_int8")
+    bt, dev = _shared_tables(plan, block_tables), _device()
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    if not (plan.device == dev == q.get_device() == k_cache.get_device() == v_cache.get_device() == out.get_device()
+            == k_scale.get_device() == v_scale.get_device()
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and out.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
+            and (block_tables is None or block_tables.get_device() == dev)):
+        _refuse(plan.device, q, k_cache, v_cache, k_scale, v_scale, out, workspace, block_tables)
+    rc = (_lib or lib()).pa_decode_shared_int8(ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                               k_scale.data_ptr(), v_scale.data_ptr(), bt, scale, out.data_ptr(),
+                                               plan.call_ref, *plan.call_arrays, plan.call_tiles, ws, ws_bytes,
+                                               _stream_of(dev, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_decode_shared_int8")
 
 
 def pa_copy_blocks(dims: pa_dims, k_cache, v_cache, triples, num_triples: Optional[int] = None, stream=None):
@@ -545,11 +558,12 @@ class PagePool:
         self.workspace = torch.empty(n.value, dtype=torch.uint8, device=block_tables.device)
         self.ws = (self.workspace.data_ptr(), n.value)
         self.device = block_tables.get_device()
-        self.dims = bytes(dims)
+        self.dims = pa_dims.from_buffer_copy(dims)  # the calls go by this copy
+        self.dims_ref, self.dims_bytes = ctypes.byref(self.dims), bytes(dims)
 
     def check(self, dims: pa_dims) -> None:
         """Refuses a call with other dims than the pool's, or made with another device current."""
-        if bytes(dims) != self.dims:
+        if bytes(dims) != self.dims_bytes:
             raise ValueError("the pool was made with other dims")
         if self.device < 0 or _device() != self.device:
             raise ValueError(f"the pool is on {self.block_tables.device}, which is not the current CUDA device")
@@ -578,8 +592,9 @@ def pa_pool_append(dims: pa_dims, pool: PagePool, rows, cu_new, slot_mapping, st
     args = (_int32(rows, "rows", None, dev), _int32(cu_new, "cu_new", n + 1, dev), n,
             _int32(slot_mapping, "slot_mapping", None, dev), tokens)
     pool.check(dims)
-    _check((_lib or lib()).pa_pool_append(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
-           "pa_pool_append")
+    rc = (_lib or lib()).pa_pool_append(pool.dims_ref, pool.ref, *args, *pool.ws, _stream_of(pool.device, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_pool_append")
 
 
 def pa_pool_fork(dims: pa_dims, pool: PagePool, parents, children, stream=None):
@@ -587,15 +602,18 @@ def pa_pool_fork(dims: pa_dims, pool: PagePool, parents, children, stream=None):
     dev, n = pool.device, children.numel()
     args = (_int32(parents, "parents", n, dev), _int32(children, "children", None, dev), n)
     pool.check(dims)
-    _check((_lib or lib()).pa_pool_fork(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)), "pa_pool_fork")
+    rc = (_lib or lib()).pa_pool_fork(pool.dims_ref, pool.ref, *args, *pool.ws, _stream_of(pool.device, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_pool_fork")
 
 
 def pa_pool_free(dims: pa_dims, pool: PagePool, rows, stream=None):
     """Empty the rows and give their pages back."""
     at = _int32(rows, "rows", None, pool.device)
     pool.check(dims)
-    _check((_lib or lib()).pa_pool_free(ctypes.byref(dims), pool.ref, at, rows.numel(), _stream(stream)),
-           "pa_pool_free")
+    rc = (_lib or lib()).pa_pool_free(pool.dims_ref, pool.ref, at, rows.numel(), _stream_of(pool.device, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_pool_free")
 
 
 def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None, ref_counts_out=None, stream=None):
@@ -608,8 +626,9 @@ def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None,
     args = (_int32(remap, "remap", pages, dev), _int32(tables, "block_tables_out", pool.block_tables.numel(), dev),
             _int32(refs, "ref_counts_out", pages, dev))
     pool.check(dims)
-    _check((_lib or lib()).pa_pool_compact(ctypes.byref(dims), pool.ref, *args, *pool.ws, _stream(stream)),
-           "pa_pool_compact")
+    rc = (_lib or lib()).pa_pool_compact(pool.dims_ref, pool.ref, *args, *pool.ws, _stream_of(pool.device, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_pool_compact")
 
 
 def int8_cache(dims: pa_dims, device="cuda"):
