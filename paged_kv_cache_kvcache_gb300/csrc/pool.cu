@@ -98,6 +98,18 @@ struct Team {
         else
             __syncthreads();
     }
+    // Before the first scan every CTA must run: its shared memory is written by the others.  Where no
+    // sync() stands before it, the kernel begins with arrive() and waits here after its first loads.
+    __device__ void arrive()
+    {
+        if constexpr (kCluster)
+            cg::this_cluster().barrier_arrive();
+    }
+    __device__ void all_run()
+    {
+        if constexpr (kCluster)
+            cg::this_cluster().barrier_wait();
+    }
     // exclusive sum of v over the CTA's threads before this one; *total = the CTA's sum
     __device__ int scan_cta(int v, int *total)
     {
@@ -723,6 +735,7 @@ __global__ void __launch_bounds__(kThreads)
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     Team<kCluster> team(sm);
+    team.arrive();
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
     const int nt = team.threads(), me = team.thread(), N = p.num_blocks;
     const int words = round_words(team, p), lane = threadIdx.x & 31;
@@ -748,6 +761,7 @@ __global__ void __launch_bounds__(kThreads)
     const bool one = N <= per_round;
     for (int64_t base = 0; base < N; base += per_round)
         mine += look(first_id(team, p, words, base));
+    team.all_run();
     int U, before = before_warp(mine, &U);
     // u(U): by the warp that holds id U, in the round that holds it
     int seen = 0;
