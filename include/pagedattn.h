@@ -408,6 +408,10 @@ int pa_decode_fused(const pa_dims *dims, const void *q, const void *k, const voi
  *   workspace:     device memory of at least meta->workspace_bytes (may be NULL
  *                  when that is 0), 256-byte aligned; calls in flight at once
  *                  need separate workspaces
+ * The launch is set up during the kernel before it in the stream, if there is
+ * one, and reads the plan's arrays (nothing else) then: bring them by a copy
+ * (pa_upload), on this stream or on one that it waits for, not by a kernel right
+ * before the call.
  * A block id outside [0, num_blocks) among a context's blocks reads as zeros
  * (as do the key's score and value) and sets bit 6 of the device error word; a
  * bounded wait that runs out sets bit 5 and leaves `out` undefined.

@@ -99,13 +99,13 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1) decode_split_kern
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    if constexpr (SHARED)
+        ptx::launch_dependents();
     const int4 item = p.items[blockIdx.x / p.num_kv_heads];
     const int b = item.x, k0 = item.y, pslot = item.w;
-    if constexpr (SHARED) { // the items are the plan's; everything else may be the launch before's
-        ptx::launch_dependents();
-        if (!p.beside)
+    if constexpr (SHARED)
+        if (!p.beside) // the items are the plan's; everything else may be the launch before's
             ptx::grid_dependency_wait();
-    }
     const int g = blockIdx.x % p.num_kv_heads;
     const int G = p.group;
     const int Hq = p.num_heads;

@@ -173,13 +173,13 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int r = lane >> 2, c = lane & 3;
+    if constexpr (SHARED)
+        ptx::launch_dependents();
     const int4 item = p.items[blockIdx.x / p.num_kv_heads];
     const int b = item.x, k0 = item.y, pslot = item.w;
-    if constexpr (SHARED) { // the items are the plan's; everything else may be the launch before's
-        ptx::launch_dependents();
-        if (!p.beside)
+    if constexpr (SHARED)
+        if (!p.beside) // the items are the plan's; everything else may be the launch before's
             ptx::grid_dependency_wait();
-    }
     // FUSED: does this item hold the new token?  Then the cache supplies keys k0 .. ctx-2.
     const bool has_new = FUSED && item.z > 0 && item.z == __ldg(p.context_lens + b);
     const int k1 = has_new ? item.z - 1 : item.z;

@@ -202,18 +202,18 @@ struct SharedArgs {
     const int32_t *items;
     const int32_t *cta_items;
     const int32_t *seq_parts;
-    const int32_t *single_items; // INT8 cache only
+    const int32_t *single_items; // parts of single sequences that run apart
     const int32_t *table_rows;
     const int32_t *direct_items; // set: every context is decoded whole, nothing is shared
     const int32_t *scratch_tiles;
-    void *scratch; // fp16: the shared prefixes' K, then V, then the queries
+    void *scratch; // INT8: what the items read, in fp16: K, then V, then the queries
     int32_t num_scratch_tiles;
     void *out;
     float *part_o;   // [num_partials][Hq][D]
     float *part_lse; // [num_partials][Hq]
     float scale;
     int32_t num_seqs;
-    int32_t num_items; // to launch: INT8 those of several sequences, bf16 all
+    int32_t num_items; // of the CTAs' lists
     int32_t num_single_items;
     int32_t num_ctas;
     int32_t rows_per_tile;

@@ -604,3 +604,45 @@ def test_padded_batch_and_a_row_named_twice(case):
         ref, a = reference(q[:n], *(dense if int8 else (kc, vc)), lists, ctx, bs, d ** -0.5)
         assert_within(out[:n], ref, a, f"padded {case[:2]} int8 {int8}")
         assert (out[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("case", CHAINS, ids=range(len(CHAINS)))
+def test_plan_uploaded_on_another_stream(case, int8):
+    """A plan that a copy stream brings late: the call waits for it, although it may be set up during a kernel."""
+    n, sh, tails, split = case
+    bs, hq, hkv, d = 16, 28, 4, 128
+    plans = []
+    for seed in (40, 41):
+        ctx, lists, groups, nb = make_batch(seed, [n], [sh], tails, bs)
+        dims = pa.make_dims(nb, bs, hq, hkv, d)
+        plans.append(pa.pa_pack_decode_shared(dims, ctx, groups, block_lists=lists, split_tokens=split))
+    image = torch.empty(int(max(p.meta.total_bytes for p in plans)), dtype=torch.uint8, device="cuda")
+    for p in plans:
+        p.dev = image
+    if int8:
+        cache, _ = int8_pool(nb, bs, hkv, d, 210, [nb * bs], [list(range(nb))])
+        call = lambda q, p, out, ws: pa.pa_decode_shared_int8(dims, q, *cache, p, d ** -0.5, out, ws)
+    else:
+        kc, vc = values((nb, bs, hkv, d), 211), values((nb, bs, hkv, d), 212)
+        call = lambda q, p, out, ws: pa.pa_decode_shared(dims, q, kc, vc, p, d ** -0.5, out, ws)
+    q0, ws = values((n, hq, d), 213), pa.shared_workspace(plans[0])
+    q, out, want = torch.empty_like(q0), torch.empty_like(q0), []
+    for p in plans:
+        p.upload()
+        torch.cuda.synchronize()
+        call(q0, p, out, ws)
+        want.append(out.clone())
+    assert not torch.equal(*want)
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    for i in range(4):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(400_000)  # a few hundred microseconds
+            plans[i & 1].upload(stream=side)
+        q.zero_()
+        torch.mul(q0, 1, out=q)         # the kernel right before the call, done long before the copy
+        main.wait_stream(side)
+        call(q, plans[i & 1], out, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i & 1]), i
