@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
     const int bs = p.block_size;
     const int Hkv = p.num_kv_heads;
     int blk_cache = 0;
+    uint32_t outside = 0; // SHARED: bit s, the chunk in stage s is of a block outside the pool
 
     if (lane == 0) {
         for (int s = 0; s < kStages; ++s)
@@ -213,21 +214,23 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
             blk_cache = key < k1 ? __ldg(bt_row + key / bs) : 0;
         }
         int phys = __shfl_sync(0xffffffffu, blk_cache, i & 31);
-        if (lane == 0) {
-            bool inside = true;
-            if constexpr (SHARED) {
-                inside = (uint32_t)phys < (uint32_t)p.num_blocks;
-                if (!inside) {
-                    phys = p.num_blocks; // past the pool: the codes read as zeros
+        const int st = i % kStages;
+        bool inside = true;
+        if constexpr (SHARED) {
+            inside = (uint32_t)phys < (uint32_t)p.num_blocks;
+            outside = (outside & ~(1u << st)) | (inside ? 0u : 1u << st);
+            if (!inside) {
+                phys = p.num_blocks; // past the pool: the codes read as zeros
+                if (lane == 0)
                     atomicOr(&g_decode_error, 2u);
-                }
             }
+        }
+        if (lane == 0) {
             const int key0 = k0 + 16 * (warp + W * i);
             const int off0 = key0 & (bs - 1); // a chunk never crosses a block (bs >= 16, key0 % 16 == 0)
-            const int st = i % kStages;
             const uint32_t bar = bar_base + 8 * st;
             const uint32_t dst = wbase + st * L::kStageBytes;
-            const size_t si = inside ? ((size_t)phys * Hkv + g) * bs + off0 : 0; // (zeros times any scale)
+            const size_t si = inside ? ((size_t)phys * Hkv + g) * bs + off0 : 0; // (outside: not used)
             ptx::mbar_arrive_expect_tx(bar, L::kTxBytes);
             ptx::tma_load_3d(dst, &tm_k, bar, 0, g, phys * bs + off0);
             ptx::tma_load_3d(dst + L::kChunkBytes, &tm_v, bar, 0, g, phys * bs + off0);
@@ -315,12 +318,15 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
                 ptx::mma_16816_f16(sc[nt], a0, a1, a2, a3, qf[nt][kk][0], qf[nt][kk][1]);
         }
 
-        const float ks0 = lds_half(sb + 2 * r) * p.scale_log2;
-        const float ks1 = lds_half(sb + 2 * (r + 8)) * p.scale_log2;
+        // a block outside the pool is zeros, scales too: whoever's scales came with the zero codes may
+        // be NaN or infinite
+        const bool real = !SHARED || !(outside >> st & 1u);
+        const float ks0 = real ? lds_half(sb + 2 * r) * p.scale_log2 : 0.f;
+        const float ks1 = real ? lds_half(sb + 2 * (r + 8)) * p.scale_log2 : 0.f;
         const bool v0 = key0 + r < k1;
         const bool v1 = key0 + r + 8 < k1;
-        const float vs0 = v0 ? lds_half(sb + 32 + 2 * r) : 0.f; // rows past the context: weight 0
-        const float vs1 = v1 ? lds_half(sb + 32 + 2 * (r + 8)) : 0.f;
+        const float vs0 = v0 && real ? lds_half(sb + 32 + 2 * r) : 0.f; // rows past the context: weight 0
+        const float vs1 = v1 && real ? lds_half(sb + 32 + 2 * (r + 8)) : 0.f;
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
