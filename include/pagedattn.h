@@ -486,6 +486,8 @@ int pa_pool_append(const pa_dims *dims, const pa_pool *pool, const int32_t *rows
  * bit for bit; the new page's other rows stay as they were.
  *   parents, children: device int32 [n]; a parent may occur several times, a
  *                      child once, empty before, and not as a parent
+ * A parent whose length covers an entry that lies outside the pool or names a
+ * page of count 0 (or below) sets bit 8 and refuses the call.
  */
 int pa_pool_fork(const pa_dims *dims, const pa_pool *pool, const int32_t *parents, const int32_t *children, int32_t n,
                  void *workspace, size_t workspace_bytes, pa_stream_t stream);

@@ -41,14 +41,17 @@ constexpr int kMoveThreads = 256;
 constexpr int kPieceBytes = 16 << 10; // one CTA's unit of page copying: 4 x 16 bytes per thread
 constexpr int kRowBits = 65536;       // rows whose use in a call is kept in a bitmap in shared memory
 constexpr int kSmallList = 4096;      // free ids kept in shared memory
+constexpr int kPlanCells = 4096;      // table cells that a plan looks at by itself
+constexpr int kCheckCtas = 608;       // CTAs that look at more, at most (a planning CTA has a thread for each)
 
 // Workspace: header, copies int4 [num_rows], marks, starts, lens, cums [num_rows],
-// list [num_blocks], list2 [num_blocks].
+// list [num_blocks], list2 [num_blocks], checks [kCheckCtas].
 struct Ws {
     int32_t *head; // [0] copies or moves of the call, -1: refused; [1] pieces of the copies; [2] compact: u(U)
     int4 *copies;
     int32_t *marks, *starts, *lens, *cums;
     int32_t *list, *list2;
+    int32_t *checks; // verdicts of pool_check_kernel's CTAs
 };
 
 __host__ __device__ inline Ws carve(void *p, int num_rows, int num_blocks)
@@ -63,6 +66,7 @@ __host__ __device__ inline Ws carve(void *p, int num_rows, int num_blocks)
     w.cums = w.lens + num_rows;
     w.list = w.cums + num_rows;
     w.list2 = w.list + num_blocks;
+    w.checks = w.list2 + num_blocks;
     return w;
 }
 constexpr int kWsRowInts = 8, kWsBlockInts = 2;
@@ -98,8 +102,8 @@ struct Team {
         else
             __syncthreads();
     }
-    // Before the first scan every CTA must run: its shared memory is written by the others.  Where no
-    // sync() stands before it, the kernel begins with arrive() and waits here after its first loads.
+    // Before the first scan or refuse() every CTA must run: its shared memory is written by the others.
+    // Where no sync() stands before it, the kernel begins with arrive() and waits here after its first loads.
     __device__ void arrive()
     {
         if constexpr (kCluster)
@@ -159,6 +163,16 @@ struct Team {
         turn ^= 1;
         *total = sum;
         return base + before;
+    }
+    // notes in every CTA that the call is refused: after all_run(), seen after the next sync() or scan()
+    __device__ void refuse(int bits)
+    {
+        if constexpr (kCluster) {
+            for (int c = 0; c < kClusterCtas; ++c)
+                atomicOr(cg::this_cluster().map_shared_rank(&s.bad, c), bits);
+        } else {
+            atomicOr(&s.bad, bits);
+        }
     }
     // a word of the first CTA's shared memory, after the barrier that follows its write
     __device__ int of_first(int *word)
@@ -312,6 +326,57 @@ __device__ __forceinline__ void plan_begin(Team<kCluster> &team, const PoolParam
     if (threadIdx.x == 0)
         team.s.bad = 0;
     __syncthreads();
+}
+
+// ---------------------------------------------------------------- checks
+
+// Whether one of this thread's cells (from, from + step, ...) of the parents' table rows, up to their
+// lengths, names no page in use.  Four at a time: each is a chain of four dependent loads.
+__device__ __forceinline__ bool bad_cells(const PoolParams &p, const int32_t *__restrict__ parents, int n, int from,
+                                          int step)
+{
+    constexpr int kU = 4;
+    const int64_t cells = (int64_t)n * p.max_blocks;
+    bool bad = false;
+    for (int64_t c0 = from; c0 < cells; c0 += (int64_t)kU * step) {
+        int id[kU];
+        bool look[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int64_t c = c0 + (int64_t)u * step;
+            const int i = (int)c / p.max_blocks, j = (int)c % p.max_blocks; // (cells fit an int32)
+            const int r = c < cells ? parents[i] : -1;
+            look[u] = (uint32_t)r < (uint32_t)p.num_rows && j < pages(p.context_lens[r], p.block_size);
+            id[u] = look[u] ? p.tables[(size_t)r * p.max_blocks + j] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            bad |= look[u] && ((uint32_t)id[u] >= (uint32_t)p.num_blocks || p.refs[id[u]] <= 0);
+    }
+    return bad;
+}
+
+// Many cells, over the whole grid: a verdict per CTA, which the plan behind collects.  (A fork of 64 rows
+// into 256, 5632 cells, one token each and their end took 48.2 us with the cells looked at in the plan, 48.4
+// with this launch, 45.7 unchecked; more cells take the planning CTA a chain of loads per 4096, this less.)
+__global__ void __launch_bounds__(256)
+    pool_check_kernel(const PoolParams p, const int32_t *__restrict__ parents, int n, void *workspace)
+{
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int any = __syncthreads_or(bad_cells(p, parents, n, (int)blockIdx.x * 256 + (int)threadIdx.x, (int)gridDim.x * 256));
+    if (threadIdx.x == 0)
+        carve(workspace, p.num_rows, p.num_blocks).checks[blockIdx.x] = any;
+}
+
+// The plan's side: the verdicts of `checked` CTAs, or this thread's share of the cells itself.
+template <bool kCluster>
+__device__ __forceinline__ bool found_bad(const Team<kCluster> &team, const PoolParams &p, const Ws &w,
+                                          const int32_t *parents, int n, int checked)
+{
+    if (checked == 0)
+        return bad_cells(p, parents, n, team.thread(), team.threads());
+    return team.thread() < checked && w.checks[team.thread()] != 0;
 }
 
 // ---------------------------------------------------------------- append
@@ -475,7 +540,7 @@ __global__ void __launch_bounds__(256)
 template <bool kCluster>
 __global__ void __launch_bounds__(kThreads)
     pool_fork_kernel(const PoolParams p, const int32_t *__restrict__ parents, const int32_t *__restrict__ children,
-                     int n, int row_bytes, void *workspace)
+                     int n, int row_bytes, int checked, void *workspace)
 {
     __shared__ Smem sm;
     ptx::launch_dependents();
@@ -485,6 +550,11 @@ __global__ void __launch_bounds__(kThreads)
     const int nt = team.threads(), me = team.thread(), bs = p.block_size;
     int refs[kIds];
     plan_begin(team, p, refs);
+    team.arrive();
+    const bool wrong = found_bad(team, p, w, parents, n, checked);
+    team.all_run();
+    if (wrong)
+        team.refuse(2);
     const bool small = n <= kThreads;
     int32_t *starts = small ? sm.starts : w.starts, *lens = small ? sm.lens : w.lens;
     if (team.rank() == 0) {
@@ -504,9 +574,6 @@ __global__ void __launch_bounds__(kThreads)
                     } else if (ctx % bs != 0) {
                         need = 1;
                         bits = (int)(((int64_t)(ctx % bs) * row_bytes + kPieceBytes - 1) / kPieceBytes);
-                        const int page = p.tables[(size_t)r * p.max_blocks + ctx / bs];
-                        if ((uint32_t)page >= (uint32_t)p.num_blocks)
-                            bad |= 2;
                     }
                 }
                 lens[i] = ctx;
@@ -673,11 +740,8 @@ __global__ void __launch_bounds__(kMoveThreads)
         const int32_t *from = p.tables + (size_t)parents[i] * p.max_blocks;
         int32_t *to = p.tables + (size_t)children[i] * p.max_blocks;
         for (int j = threadIdx.x; j < c.w; j += kMoveThreads) {
-            const int id = from[j];
-            if ((uint32_t)id < (uint32_t)p.num_blocks)
-                atomicAdd(p.refs + id, 1);
-            else
-                atomicOr(&g_pool_error, 2u);
+            const int id = from[j]; // (in the pool and in use: checked before the plan)
+            atomicAdd(p.refs + id, 1);
             to[j] = id;
         }
         if (threadIdx.x == 0 && c.y >= 0)
@@ -926,11 +990,17 @@ constexpr int kRoundIds = kThreads * kIds;
 bool search_by_cluster(const PoolArgs &a) { return a.dims.num_blocks > 2 * kRoundIds; }
 bool compact_by_cluster(const PoolArgs &a) { return a.dims.num_blocks > kRoundIds; }
 
+// CTAs of the launch that looks at a call's table cells; 0: they are few, the plan does it
+int check_ctas(int64_t cells)
+{
+    return cells <= kPlanCells ? 0 : (int)std::min<int64_t>(kCheckCtas, (cells + 1023) / 1024);
+}
+
 } // namespace
 
 size_t pool_workspace_bytes(int num_rows, int num_blocks)
 {
-    return align_up((16 + kWsRowInts * (size_t)num_rows + kWsBlockInts * (size_t)num_blocks) * 4, 256);
+    return align_up((16 + kWsRowInts * (size_t)num_rows + kWsBlockInts * (size_t)num_blocks + kCheckCtas) * 4, 256);
 }
 
 int launch_pool_append(const PoolArgs &a, const int32_t *rows, const int32_t *cu, int n, int32_t *slots, int num_tokens,
@@ -958,8 +1028,13 @@ int launch_pool_fork(const PoolArgs &a, const int32_t *parents, const int32_t *c
     const Planes q = planes_of(a);
     const bool cluster = search_by_cluster(a);
     const unsigned c = cluster ? kClusterCtas : 1;
+    const int checked = check_ctas((int64_t)n * a.pool.max_blocks);
+    if (checked > 0)
+        if (int rc = launch_ex("pool check", pool_check_kernel, (unsigned)checked, 256, 1, stream, params_of(a), parents,
+                               n, a.workspace))
+            return rc;
     if (int rc = launch_ex("pool fork", cluster ? pool_fork_kernel<true> : pool_fork_kernel<false>, c, kThreads, c,
-                           stream, params_of(a), parents, children, n, (int)(q.row_vecs * 16), a.workspace))
+                           stream, params_of(a), parents, children, n, (int)(q.row_vecs * 16), checked, a.workspace))
         return rc;
     const int64_t units = std::max<int64_t>(n, (int64_t)n * 2 * q.layers * q.pieces);
     return launch_ex("pool fork copy", pool_fork_copy_kernel, (unsigned)std::min<int64_t>(units, (int64_t)sms * 8),
