@@ -510,6 +510,10 @@ int pa_pool_free(const pa_dims *dims, const pa_pool *pool, const int32_t *rows, 
  *                     pool's own.  With other arrays the old tables stay valid for
  *                     reading until the next pa_pool_append or pa_pool_fork: the
  *                     pages moved away from keep their contents.
+ * A table entry (behind a row's length too) other than -1 that lies outside the
+ * pool or names a page of count 0, or a negative count, sets bit 8 and refuses
+ * the call: nothing moves, the out arrays are copies of the pool's and remap
+ * leaves every page of a count where it is.
  */
 int pa_pool_compact(const pa_dims *dims, const pa_pool *pool, int32_t *remap, int32_t *block_tables_out,
                     int32_t *ref_counts_out, void *workspace, size_t workspace_bytes, pa_stream_t stream);

@@ -330,8 +330,10 @@ __device__ __forceinline__ void plan_begin(Team<kCluster> &team, const PoolParam
 
 // ---------------------------------------------------------------- checks
 
-// Whether one of this thread's cells (from, from + step, ...) of the parents' table rows, up to their
-// lengths, names no page in use.  Four at a time: each is a chain of four dependent loads.
+// Whether one of this thread's cells (from, from + step, ...) names no page in use: kFork, of the
+// parents' table rows, up to their lengths; else (a compaction) of all n rows, entries of -1 excepted.
+// Four at a time: each is a chain of four (two) dependent loads.
+template <bool kFork>
 __device__ __forceinline__ bool bad_cells(const PoolParams &p, const int32_t *__restrict__ parents, int n, int from,
                                           int step)
 {
@@ -344,6 +346,11 @@ __device__ __forceinline__ bool bad_cells(const PoolParams &p, const int32_t *__
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int64_t c = c0 + (int64_t)u * step;
+            if constexpr (!kFork) {
+                id[u] = c < cells ? p.tables[c] : -1;
+                look[u] = id[u] != -1;
+                continue;
+            }
             const int i = (int)c / p.max_blocks, j = (int)c % p.max_blocks; // (cells fit an int32)
             const int r = c < cells ? parents[i] : -1;
             look[u] = (uint32_t)r < (uint32_t)p.num_rows && j < pages(p.context_lens[r], p.block_size);
@@ -359,23 +366,24 @@ __device__ __forceinline__ bool bad_cells(const PoolParams &p, const int32_t *__
 // Many cells, over the whole grid: a verdict per CTA, which the plan behind collects.  (A fork of 64 rows
 // into 256, 5632 cells, one token each and their end took 48.2 us with the cells looked at in the plan, 48.4
 // with this launch, 45.7 unchecked; more cells take the planning CTA a chain of loads per 4096, this less.)
+template <bool kFork>
 __global__ void __launch_bounds__(256)
     pool_check_kernel(const PoolParams p, const int32_t *__restrict__ parents, int n, void *workspace)
 {
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
-    const int any = __syncthreads_or(bad_cells(p, parents, n, (int)blockIdx.x * 256 + (int)threadIdx.x, (int)gridDim.x * 256));
+    const int any = __syncthreads_or(bad_cells<kFork>(p, parents, n, (int)blockIdx.x * 256 + (int)threadIdx.x, (int)gridDim.x * 256));
     if (threadIdx.x == 0)
         carve(workspace, p.num_rows, p.num_blocks).checks[blockIdx.x] = any;
 }
 
 // The plan's side: the verdicts of `checked` CTAs, or this thread's share of the cells itself.
-template <bool kCluster>
+template <bool kFork, bool kCluster>
 __device__ __forceinline__ bool found_bad(const Team<kCluster> &team, const PoolParams &p, const Ws &w,
                                           const int32_t *parents, int n, int checked)
 {
     if (checked == 0)
-        return bad_cells(p, parents, n, team.thread(), team.threads());
+        return bad_cells<kFork>(p, parents, n, team.thread(), team.threads());
     return team.thread() < checked && w.checks[team.thread()] != 0;
 }
 
@@ -551,7 +559,7 @@ __global__ void __launch_bounds__(kThreads)
     int refs[kIds];
     plan_begin(team, p, refs);
     team.arrive();
-    const bool wrong = found_bad(team, p, w, parents, n, checked);
+    const bool wrong = found_bad<true>(team, p, w, parents, n, checked);
     team.all_run();
     if (wrong)
         team.refuse(2);
@@ -790,20 +798,25 @@ __global__ void __launch_bounds__(128) pool_free_kernel(const PoolParams p, cons
 // remap, the counts under the new ids and the moves (list2[k] -> list[k]).  U used pages: the
 // used ids >= U move, in order, to the free ids < U; sources and destinations are disjoint.  With
 // u(id) the used ids before id, a free id < U is hole id - u(id), and a used id >= U takes
-// hole u(id) - u(U).
+// hole u(id) - u(U).  Refused (a table names a page not in use, a count is negative): remap and the out
+// arrays tell of pages that stay where they are.
 template <bool kCluster>
 __global__ void __launch_bounds__(kThreads)
-    pool_compact_kernel(const PoolParams p, int32_t *__restrict__ remap, int32_t *refs_out, void *workspace)
+    pool_compact_kernel(const PoolParams p, int32_t *__restrict__ remap, int32_t *refs_out, int checked, void *workspace)
 {
     __shared__ Smem sm;
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     Team<kCluster> team(sm);
+    if (threadIdx.x == 0)
+        sm.bad = 0;
+    __syncthreads();
     team.arrive();
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
     const int nt = team.threads(), me = team.thread(), N = p.num_blocks;
     const int words = round_words(team, p), lane = threadIdx.x & 31;
     const int64_t per_round = (int64_t)nt * words;
+    bool wrong = found_bad<false>(team, p, w, nullptr, p.num_rows, checked);
     uint32_t used[kIds]; // of this warp's ids: lane l of word e is id first + 32 e + l
     auto look = [&](int first) {
         int refs[kIds];
@@ -813,6 +826,7 @@ __global__ void __launch_bounds__(kThreads)
         for (int e = 0; e < kIds; ++e) {
             if (e >= words)
                 break;
+            wrong |= refs[e] < 0;
             used[e] = __ballot_sync(0xffffffffu, refs[e] != 0 && 32 * e + lane < N - first);
             sum += __popc(used[e]);
         }
@@ -826,7 +840,22 @@ __global__ void __launch_bounds__(kThreads)
     for (int64_t base = 0; base < N; base += per_round)
         mine += look(first_id(team, p, words, base));
     team.all_run();
+    if (wrong)
+        team.refuse(2);
     int U, before = before_warp(mine, &U);
+    if (sm.bad) {
+        if (me == 0) {
+            atomicOr(&g_pool_error, 2u);
+            w.head[0] = -1;
+        }
+        for (int id = me; id < N; id += nt) {
+            const int count = p.refs[id];
+            remap[id] = count != 0 ? id : -1;
+            if (refs_out != p.refs)
+                refs_out[id] = count;
+        }
+        return;
+    }
     // u(U): by the warp that holds id U, in the round that holds it
     int seen = 0;
     for (int64_t base = 0; base < N; base += per_round) {
@@ -905,20 +934,13 @@ __global__ void __launch_bounds__(kMoveThreads)
     ptx::grid_dependency_wait();
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
     const int64_t cells = (int64_t)p.num_rows * p.max_blocks;
+    const int moves = w.head[0]; // -1: refused
     for (int64_t i = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; i < cells; i += (int64_t)gridDim.x * kMoveThreads) {
-        const int id = p.tables[i];
-        int to = -1;
-        if ((uint32_t)id < (uint32_t)p.num_blocks) {
-            to = remap[id];
-            if (to < 0)
-                atomicOr(&g_pool_error, 2u); // a table names a page of count 0
-        } else if (id != -1) {
-            atomicOr(&g_pool_error, 2u);
-        }
-        tables_out[i] = to;
+        const int id = p.tables[i]; // -1 or (checked before the plan) a page in use
+        tables_out[i] = moves < 0 || id < 0 ? id : remap[id];
     }
     const int per = 2 * q.layers * q.pieces;
-    const int64_t units = (int64_t)w.head[0] * per;
+    const int64_t units = (int64_t)moves * per;
     copy_pieces(q, units, [&](int64_t u) {
         const int k = (int)(u / per), v = (int)(u % per);
         return piece_of(q, v / q.pieces, v % q.pieces, w.list2[k], w.list[k], q.block_size);
@@ -1030,8 +1052,8 @@ int launch_pool_fork(const PoolArgs &a, const int32_t *parents, const int32_t *c
     const unsigned c = cluster ? kClusterCtas : 1;
     const int checked = check_ctas((int64_t)n * a.pool.max_blocks);
     if (checked > 0)
-        if (int rc = launch_ex("pool check", pool_check_kernel, (unsigned)checked, 256, 1, stream, params_of(a), parents,
-                               n, a.workspace))
+        if (int rc = launch_ex("pool check", pool_check_kernel<true>, (unsigned)checked, 256, 1, stream, params_of(a),
+                               parents, n, a.workspace))
             return rc;
     if (int rc = launch_ex("pool fork", cluster ? pool_fork_kernel<true> : pool_fork_kernel<false>, c, kThreads, c,
                            stream, params_of(a), parents, children, n, (int)(q.row_vecs * 16), checked, a.workspace))
@@ -1053,11 +1075,16 @@ int launch_pool_compact(const PoolArgs &a, int32_t *remap, int32_t *tables_out, 
         return rc;
     const bool cluster = compact_by_cluster(a);
     const unsigned c = cluster ? kClusterCtas : 1;
+    const int64_t cells = (int64_t)a.pool.num_rows * a.pool.max_blocks;
+    const int checked = check_ctas(cells);
+    if (checked > 0)
+        if (int rc = launch_ex("pool check", pool_check_kernel<false>, (unsigned)checked, 256, 1, stream, params_of(a),
+                               (const int32_t *)nullptr, a.pool.num_rows, a.workspace))
+            return rc;
     if (int rc = launch_ex("pool compact", cluster ? pool_compact_kernel<true> : pool_compact_kernel<false>, c, kThreads,
-                           c, stream, params_of(a), remap, refs_out, a.workspace))
+                           c, stream, params_of(a), remap, refs_out, checked, a.workspace))
         return rc;
     const Planes q = planes_of(a);
-    const int64_t cells = (int64_t)a.pool.num_rows * a.pool.max_blocks;
     const int64_t units = std::max<int64_t>((cells + kMoveThreads - 1) / kMoveThreads,
                                             (int64_t)(a.dims.num_blocks / 2) * 2 * q.layers * q.pieces);
     return launch_ex("pool move", pool_move_kernel, (unsigned)std::max<int64_t>(1, std::min<int64_t>(units, sms * 8)),
