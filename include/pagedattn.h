@@ -415,6 +415,10 @@ int pa_decode_fused(const pa_dims *dims, const void *q, const void *k, const voi
  * A block id outside [0, num_blocks) among a context's blocks reads as zeros
  * (as do the key's score and value) and sets bit 6 of the device error word; a
  * bounded wait that runs out sets bit 5 and leaves `out` undefined.
+ * Keys of score -inf have no weight; a context of such keys only gives zeros, as
+ * an empty one does.  Otherwise NaN and infinities go through as in the formula,
+ * wherever the plan cuts a context: a NaN or +inf score makes its (sequence, head)
+ * NaN, a NaN value its component.  (pa_decode counts a part whose sum is NaN as empty.)
  * scale must be finite and > 0.
  */
 int pa_decode_shared(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,

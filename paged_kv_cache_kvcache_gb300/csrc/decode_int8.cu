@@ -341,11 +341,13 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
             }
             const float mn0 = fmaxf(m_r[nt][0], mx0), mn1 = fmaxf(m_r[nt][1], mx1);
-            const float al0 = ptx::ex2(m_r[nt][0] - mn0), al1 = ptx::ex2(m_r[nt][1] - mn1);
+            // SHARED: a maximum of -inf (every score so far -inf or NaN) is no reference: -inf - -inf is NaN
+            const float rf0 = SHARED && mn0 == -INFINITY ? 0.f : mn0, rf1 = SHARED && mn1 == -INFINITY ? 0.f : mn1;
+            const float al0 = ptx::ex2(m_r[nt][0] - rf0), al1 = ptx::ex2(m_r[nt][1] - rf1);
             m_r[nt][0] = mn0;
             m_r[nt][1] = mn1;
-            const float p0 = ptx::ex2(s0 - mn0), p1 = ptx::ex2(s1 - mn1);
-            const float p2 = ptx::ex2(s2 - mn0), p3 = ptx::ex2(s3 - mn1);
+            const float p0 = ptx::ex2(s0 - rf0), p1 = ptx::ex2(s1 - rf1);
+            const float p2 = ptx::ex2(s2 - rf0), p3 = ptx::ex2(s3 - rf1);
             l_r[nt][0] = l_r[nt][0] * al0 + p0 + p2;
             l_r[nt][1] = l_r[nt][1] * al1 + p1 + p3;
             if (__any_sync(0xffffffffu, (al0 != 1.f) | (al1 != 1.f))) { // skipped while no row max moves
@@ -502,10 +504,11 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
         float Lsum = 0.f, O = 0.f;
         if (FUSED && has_new)
             M = fmaxf(M, s_new[hl]);
-        if (M != -INFINITY) {
+        if (SHARED || M != -INFINITY) {
+            const float rf = SHARED && M == -INFINITY ? 0.f : M;
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                const float f = ptx::ex2(mrg_m[w * H8 + hl] - M);
+                const float f = ptx::ex2(mrg_m[w * H8 + hl] - rf);
                 Lsum += f * mrg_l[w * H8 + hl];
                 O += f * mrg_o[((size_t)w * H8 + hl) * kRow + d];
             }
@@ -515,14 +518,16 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
                 O += f * v_new[d];
             }
         }
-        const float o = Lsum > 0.f ? O / Lsum : 0.f;
+        // SHARED: NaN goes on, to the output and to the merge (pa_decode counts such a row as empty)
+        const bool some = SHARED ? Lsum != 0.f : Lsum > 0.f;
+        const float o = some ? O / Lsum : SHARED ? O : 0.f; // (no weight: O is 0, or NaN where a value is)
         const size_t h = (size_t)g * G + hl;
         if (pslot < 0) {
             p.out[((size_t)b * Hq + h) * D + d] = __float2bfloat16_rn(o);
         } else {
             p.part_o[((size_t)pslot * Hq + h) * D + d] = o;
             if (d == 0)
-                p.part_lse[(size_t)pslot * Hq + h] = Lsum > 0.f ? M + __log2f(Lsum) : -INFINITY;
+                p.part_lse[(size_t)pslot * Hq + h] = some ? M + __log2f(Lsum) : -INFINITY;
         }
     }
     if constexpr (SHARED) {

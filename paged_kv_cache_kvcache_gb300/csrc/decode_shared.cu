@@ -834,13 +834,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_valid)
                 continue;
             ptx::tc_fence_after();
-            const float inv = (row_valid && l_sum > 0.f) ? 1.f / l_sum : 0.f;
+            // (a sum of NaN goes on, to the output and to the merge)
+            const float inv = (row_valid && l_sum != 0.f) ? 1.f / l_sum : 0.f;
             const size_t head = (size_t)w.g * G + rhead;
             const bool partial = sp.y > 1;
             const size_t slot = (size_t)sp.x + w.part;
             float *po = p.part_o + (slot * p.num_heads + head) * D;
             if (partial && !*abort_flag)
-                p.part_lse[slot * p.num_heads + head] = l_sum > 0.f ? m_ref - kBias + __log2f(l_sum) : -INFINITY;
+                p.part_lse[slot * p.num_heads + head] = l_sum != 0.f ? m_ref - kBias + __log2f(l_sum) : -INFINITY;
             __nv_bfloat16 *orow = p.out + ((size_t)seq * p.num_heads + head) * D;
             uint32_t o[D / 32][32];
 #pragma unroll
@@ -885,7 +886,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // out[b][h] = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over the parts of sequence b: none
-// (empty context) writes zeros, one was written by its work item.  D/32 values per lane, kBatch
+// (empty context) writes zeros, one was written by its work item.  A part whose sum is NaN has the
+// log-sum-exp NaN, and so has the output.  D/32 values per lane, kBatch
 // parts' loads in flight; a (sequence, head)'s parts are shared out in order to kSplit warps (of
 // the four or eight of a block), whose sums meet in shared memory in warp order.  Bound by the
 // latency of the loads: 65 parts in one warp took 18 us, in eight 3.
@@ -965,7 +967,7 @@ __global__ void __launch_bounds__(kSplit == 8 ? 256 : 128)
                 acc[e] += sums[s][lane * E + e];
         }
     }
-    const float inv = W > 0.f ? 1.f / W : 0.f;
+    const float inv = W != 0.f ? 1.f / W : 0.f; // (NaN of a part: NaN)
     uint32_t x[E / 2];
 #pragma unroll
     for (int e = 0; e < E / 2; ++e)
