@@ -651,7 +651,8 @@ int pa_decode_int8_fused(const pa_dims *dims, const void *q, const void *k, cons
  * pa_decode_shared_int8 — pa_decode_shared over an INT8 cache: the same plan
  * (pa_pack_decode_shared), rules and result, with the cached K and V read as
  * code * scale.  A launch turns the keys and values of the plan's items, and q,
- * into fp16 in the workspace (rounded to nearest even, clamped to +-65504); their
+ * into fp16 in the workspace (rounded to nearest even, clamped to +-65504, NaN
+ * kept; so is q in the launches that do without the copy); their
  * products run on those with fp32 accumulation.  Parts of single sequences that
  * run apart are computed as pa_decode_int8 computes them.
  *   scratch_tiles: device copy of the plan's array

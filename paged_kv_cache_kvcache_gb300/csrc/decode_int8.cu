@@ -87,11 +87,14 @@ __device__ __forceinline__ uint32_t codes_to_f16x2(uint32_t u, uint32_t sel)
     return ptx::sub_f16x2(ptx::prmt(u, 0x64646464u, sel), kMagic);
 }
 
+// kNan: NaN stays NaN (else it becomes -65504)
+template <bool kNan>
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w)
 {
-    const float lo = fminf(fmaxf(__uint_as_float(w << 16), -65504.f), 65504.f);
-    const float hi = fminf(fmaxf(__uint_as_float(w & 0xffff0000u), -65504.f), 65504.f);
-    return ptx::pack_f16(lo, hi);
+    const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+    if constexpr (kNan)
+        return ptx::pack_f16(ptx::clamp_f16_nan(lo), ptx::clamp_f16_nan(hi));
+    return ptx::pack_f16(fminf(fmaxf(lo, -65504.f), 65504.f), fminf(fmaxf(hi, -65504.f), 65504.f));
 }
 
 __device__ __forceinline__ float lds_half(uint32_t addr) { return __half2float(__ushort_as_half(ptx::lds_u16(addr))); }
@@ -257,8 +260,8 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const uint2 w = valid ? __ldg(qrow + kk) : make_uint2(0u, 0u);
-            qf[nt][kk][0] = bf16x2_to_f16x2(w.x);
-            qf[nt][kk][1] = bf16x2_to_f16x2(w.y);
+            qf[nt][kk][0] = bf16x2_to_f16x2<SHARED>(w.x);
+            qf[nt][kk][1] = bf16x2_to_f16x2<SHARED>(w.y);
         }
     }
 

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(256) shared_codes_kernel(const CodesParams p)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float lo = __uint_as_float(u[e] << 16), hi = __uint_as_float(u[e] & 0xffff0000u);
-            w[e] = ptx::pack_f16(fminf(fmaxf(lo, -65504.f), 65504.f), fminf(fmaxf(hi, -65504.f), 65504.f));
+            w[e] = ptx::pack_f16(ptx::clamp_f16_nan(lo), ptx::clamp_f16_nan(hi));
         }
         p.q_out[i] = make_uint4(w[0], w[1], w[2], w[3]);
         return;

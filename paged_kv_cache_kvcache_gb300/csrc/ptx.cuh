@@ -477,6 +477,15 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
     return d;
 }
 
+// x within fp16's range; NaN stays NaN
+__device__ __forceinline__ float clamp_f16_nan(float x)
+{
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-65504.f));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(y), "f"(65504.f));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     uint32_t r;
