@@ -181,6 +181,7 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
+_BF16, _FP16, _INT8 = torch.bfloat16, torch.float16, torch.int8
 _device = _cur_device if _cur_device is not None else torch.cuda.current_device
 
 
@@ -188,8 +189,11 @@ def _elsewhere(t, dev: int):
     return ValueError(f"tensor on {t.device}, the current device is cuda:{dev}")
 
 
-def _refuse(plan_device: int, *tensors) -> None:
-    """Why a call's plan and tensors are refused (the calls test for it themselves: a loop here is 0.2 us a tensor)."""
+def _refuse(plan_device: int, tensors, wanted) -> None:
+    """Why a call's plan and tensors are refused (the calls test for it themselves: a loop here is 0.2 us a tensor).
+
+    ``wanted``: (what, tensor, type, least number of values).
+    """
     dev = _device()
     if plan_device != dev:
         raise ValueError(f"the plan is on cuda:{plan_device}, the current device is cuda:{dev}")
@@ -198,6 +202,11 @@ def _refuse(plan_device: int, *tensors) -> None:
             raise _elsewhere(t, dev)
         if t is not None and not t.is_contiguous():
             raise ValueError(f"tensors must be contiguous, got strides {t.stride()}")
+    for what, t, dtype, least in wanted:
+        if t.dtype is not dtype:
+            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+        if t.numel() < least:
+            raise ValueError(f"{what} has {t.numel()} values, the plan and dims need {least}")
 
 
 def _stream_of(dev: int, stream) -> Optional[int]:
@@ -287,6 +296,10 @@ class SharedPlan(_Plan):
         self.call_arrays = tuple(base + x for x in (m.off_items, m.off_cta_items, m.off_seq_parts, m.off_direct_items,
                                                    m.off_table_rows, m.off_single_items))
         self.call_tiles = base + m.off_scratch_tiles
+        # what a call's tensors hold at least: q and out, a page of a cache, a page's scales
+        self.call_rows = m.num_seqs * m.num_heads * m.head_dim
+        self.call_scales = m.block_size * m.num_kv_heads
+        self.call_page = self.call_scales * m.head_dim
         return self
 
     @property
@@ -480,16 +493,22 @@ def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale
 
     ``block_tables``: the device table a plan without block lists was packed for.
     """
-    bt, dev = _shared_tables(plan, block_tables), _device()
+    bt = (plan.call_tables if block_tables is None and plan.dev is not None else None) or _shared_tables(plan, block_tables)
+    dev = _device()
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    cached = dims.num_blocks * plan.call_page
     if not (plan.device == dev == q.get_device() == k_cache.get_device() == v_cache.get_device() == out.get_device()
             and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and out.is_contiguous()
+            and q.dtype is k_cache.dtype is v_cache.dtype is out.dtype is _BF16
+            and q.numel() >= plan.call_rows <= out.numel() and k_cache.numel() >= cached <= v_cache.numel()
             and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
             and (block_tables is None or block_tables.get_device() == dev)):
-        _refuse(plan.device, q, k_cache, v_cache, out, workspace, block_tables)
+        _refuse(plan.device, (q, k_cache, v_cache, out, workspace, block_tables),
+                (("q", q, _BF16, plan.call_rows), ("k_cache", k_cache, _BF16, cached), ("v_cache", v_cache, _BF16, cached),
+                 ("out", out, _BF16, plan.call_rows)))
     rc = (_lib or lib()).pa_decode_shared(ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), bt,
                                           scale, out.data_ptr(), plan.call_ref, *plan.call_arrays, ws, ws_bytes,
-                                          _stream_of(dev, stream))
+                                          _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
     if rc != PA_OK:
         _check(rc, "pa_decode_shared")
 
@@ -497,19 +516,28 @@ def pa_decode_shared(dims: pa_dims, q, k_cache, v_cache, plan: SharedPlan, scale
 def pa_decode_shared_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, plan: SharedPlan, scale: float, out,
                           workspace=None, block_tables=None, stream=None):
     """pa_decode_shared over an INT8 cache (same plan and workspace)."""
-    bt, dev = _shared_tables(plan, block_tables), _device()
+    bt = (plan.call_tables if block_tables is None and plan.dev is not None else None) or _shared_tables(plan, block_tables)
+    dev = _device()
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    pages = dims.num_blocks
+    cached, scales = pages * plan.call_page, pages * plan.call_scales
     if not (plan.device == dev == q.get_device() == k_cache.get_device() == v_cache.get_device() == out.get_device()
             == k_scale.get_device() == v_scale.get_device()
             and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and out.is_contiguous()
             and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and q.dtype is out.dtype is _BF16 and k_cache.dtype is v_cache.dtype is _INT8
+            and k_scale.dtype is v_scale.dtype is _FP16 and q.numel() >= plan.call_rows <= out.numel()
+            and k_cache.numel() >= cached <= v_cache.numel() and k_scale.numel() >= scales <= v_scale.numel()
             and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
             and (block_tables is None or block_tables.get_device() == dev)):
-        _refuse(plan.device, q, k_cache, v_cache, k_scale, v_scale, out, workspace, block_tables)
+        _refuse(plan.device, (q, k_cache, v_cache, k_scale, v_scale, out, workspace, block_tables),
+                (("q", q, _BF16, plan.call_rows), ("k_cache", k_cache, _INT8, cached), ("v_cache", v_cache, _INT8, cached),
+                 ("k_scale", k_scale, _FP16, scales), ("v_scale", v_scale, _FP16, scales),
+                 ("out", out, _BF16, plan.call_rows)))
     rc = (_lib or lib()).pa_decode_shared_int8(ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                                k_scale.data_ptr(), v_scale.data_ptr(), bt, scale, out.data_ptr(),
                                                plan.call_ref, *plan.call_arrays, plan.call_tiles, ws, ws_bytes,
-                                               _stream_of(dev, stream))
+                                               _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
     if rc != PA_OK:
         _check(rc, "pa_decode_shared_int8")
 
