@@ -407,7 +407,7 @@ int pa_decode_fused(const pa_dims *dims, const void *q, const void *k, const voi
  *                  copies of the plan's arrays
  *   workspace:     device memory of at least meta->workspace_bytes (may be NULL
  *                  when that is 0), 256-byte aligned; calls in flight at once
- *                  need separate workspaces
+ *                  need separate workspaces; it needs no initial contents
  * The launch is set up during the kernel before it in the stream, if there is
  * one, and reads the plan's arrays (nothing else) then: bring them by a copy
  * (pa_upload), on this stream or on one that it waits for, not by a kernel right

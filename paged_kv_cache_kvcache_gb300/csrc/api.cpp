@@ -477,7 +477,8 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
         meta->num_shared_items > meta->num_items)
         return fail(PA_ERR_INVALID_ARG, "malformed shared decode meta");
     const bool direct = (meta->direct & (int8 ? 2 : 1)) != 0;
-    const size_t part_bytes = shared_part_bytes(*dims, meta->num_partials);
+    const size_t word_at = shared_part_bytes(*dims, meta->num_partials);
+    const size_t part_bytes = word_at + shared_go_bytes(*meta);
     const uint64_t need = direct ? 0
                           : int8 ? part_bytes + shared_scratch_bytes(*dims, meta->num_scratch_tiles, meta->num_seqs)
                                  : part_bytes;
@@ -504,6 +505,8 @@ static int prepare_shared(const char *fn, bool int8, const pa_dims *dims, const 
         a->part_o = static_cast<float *>(workspace);
         a->part_lse = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                                 shared_part_o_bytes(*dims, meta->num_partials));
+        if (shared_beside(*meta))
+            a->go_word = reinterpret_cast<uint64_t *>(static_cast<char *>(workspace) + word_at);
         a->scratch = static_cast<char *>(workspace) + part_bytes;
     }
     a->num_scratch_tiles = meta->num_scratch_tiles;

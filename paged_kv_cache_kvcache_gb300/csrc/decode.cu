@@ -78,10 +78,13 @@ struct DecParams {
     // a shared-prefix decode's contexts (SHARED kernels only): block-table row of each sequence, pool size
     const int32_t *table_rows;
     int32_t num_blocks;
-    int32_t beside;
+    // beside the launch before: the word that is `go` once everything before that one has ended
+    const uint64_t *go_word; // NULL: not beside
+    uint64_t go;
 };
 
-// bit 0: a fused-store slot outside [-1, num_slots) was skipped; bit 1: SHARED met a block id outside the pool
+// bit 0: a fused-store slot outside [-1, num_slots) was skipped; SHARED: bit 1, a block id outside the pool; bit 2,
+// a bounded wait timed out
 __device__ uint32_t g_fused_error;
 
 // FUSED: the CTA whose work item ends at the sequence's last key (the token
@@ -90,8 +93,10 @@ __device__ uint32_t g_fused_error;
 // no ordering between launches.
 // SHARED: the items are short contexts of a shared-prefix decode, or its parts of single sequences.
 // Their table may be the caller's: a block id outside the pool reads as zeros and sets bit 1 of
-// g_fused_error.  The launch may run beside the one before it (the shared parts); its last block
-// ends after that one.
+// g_fused_error.  The launch may run beside the one before it (the shared parts), whose first block
+// gives a word when everything before itself has ended and is visible to it; this launch's blocks wait
+// for that word (bit 2: in vain), and its last one ends after the launch beside it.  (Read-only loads,
+// which need not see what came by way of such a word, are for the plan's arrays only.)
 template <int D, int NT, bool FUSED, bool SHARED, int W>
 __global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1) decode_split_kernel(const DecParams p)
 {
@@ -103,9 +108,19 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1) decode_split_kern
         ptx::launch_dependents();
     const int4 item = p.items[blockIdx.x / p.num_kv_heads];
     const int b = item.x, k0 = item.y, pslot = item.w;
-    if constexpr (SHARED)
-        if (!p.beside) // the items are the plan's; everything else may be the launch before's
+    if constexpr (SHARED) { // the items are the plan's; everything else may be an earlier launch's
+        if (!p.go_word) {
             ptx::grid_dependency_wait();
+        } else {
+            const bool go = ptx::wait_word(p.go_word, p.go);
+            if (!__syncthreads_and(go)) {
+                if (threadIdx.x == 0)
+                    atomicOr(&g_fused_error, 4u);
+                ptx::grid_dependency_wait();
+                return;
+            }
+        }
+    }
     const int g = blockIdx.x % p.num_kv_heads;
     const int G = p.group;
     const int Hq = p.num_heads;
@@ -123,8 +138,9 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1) decode_split_kern
             reinterpret_cast<const uint32_t *>(p.q + ((size_t)b * Hq + (size_t)g * G + (valid ? hl : 0)) * D);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            qf[nt][kk][0] = valid ? __ldg(qrow + kk * 8 + (lane & 3)) : 0u;
-            qf[nt][kk][1] = valid ? __ldg(qrow + kk * 8 + 4 + (lane & 3)) : 0u;
+            const uint32_t *at = qrow + kk * 8 + (lane & 3);
+            qf[nt][kk][0] = valid ? (SHARED ? at[0] : __ldg(at)) : 0u;
+            qf[nt][kk][1] = valid ? (SHARED ? at[4] : __ldg(at + 4)) : 0u;
         }
     }
 
@@ -139,7 +155,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1) decode_split_kern
     auto issue = [&](int i) {
         if ((i & 31) == 0) { // refresh the block ids of local chunks i .. i+31, one per lane
             const int key = k0 + 16 * (warp + W * (i + lane));
-            blk_cache = key < k1 ? __ldg(bt_row + key / bs) : 0;
+            blk_cache = key < k1 ? (SHARED ? bt_row[key / bs] : __ldg(bt_row + key / bs)) : 0;
         }
         const int phys = __shfl_sync(0xffffffffu, blk_cache, i & 31);
         const int key0 = k0 + 16 * (warp + W * i);
@@ -363,7 +379,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? 2 : 1) decode_split_kern
         }
     }
     if constexpr (SHARED) {
-        if (p.beside && blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
+        if (p.go_word && blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
             ptx::grid_dependency_wait();
     }
 }
@@ -510,7 +526,8 @@ int launch_decode(const DecodeArgs &a, void *stream)
     if (a.table_rows) { // contexts or parts of a shared-prefix decode
         p.table_rows = a.table_rows;
         p.num_blocks = a.dims.num_blocks;
-        p.beside = a.beside;
+        p.go_word = a.go_word;
+        p.go = a.go;
         if (a.few) {
             if (a.dims.head_dim == 128)
                 return two ? launch_split<128, 2, false, true, kFewWarps>(a, p, s)
@@ -548,7 +565,8 @@ int read_fused_error(uint32_t *code)
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "reading fused-store error word: %s", cudaGetErrorString(e));
     *code |= v & 1u;        // same meaning as the store kernel's bit 0
-    *code |= (v & 2u) << 5; // the shared-prefix decode's bit 6
+    *code |= (v & 2u) << 5; // the shared-prefix decode's bits 6
+    *code |= (v & 4u) << 3; // and 5
     return PA_OK;
 }
 

@@ -127,7 +127,9 @@ struct DecParams8 {
     // parts of a shared-prefix decode (SHARED kernels only): block-table row of each sequence, pool size
     const int32_t *table_rows;
     int32_t num_blocks;
-    int32_t beside;
+    // beside the launch before: the word that is `go` once everything before that one has ended
+    const uint64_t *go_word; // NULL: not beside
+    uint64_t go;
 };
 
 __device__ uint32_t g_fused8_error; // bit 0: a fused-store slot outside [-1, num_slots) was skipped
@@ -162,7 +164,7 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[D / 32], float
 // dequantised values the cache now holds) instead of from the cache.
 // SHARED: the items are a shared-prefix decode's parts of single sequences.  Their table may
 // be the caller's: a block id outside the pool reads as zeros and sets bit 1 of g_decode_error.
-// The launch may run beside the one before it (the shared parts); its last block ends after that one.
+// The launch may run beside the one before it (the shared parts): as decode.cu's.
 template <int D, int NT, bool FUSED, bool SHARED, int W>
 __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
     decode_int8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -180,9 +182,20 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
         ptx::launch_dependents();
     const int4 item = p.items[blockIdx.x / p.num_kv_heads];
     const int b = item.x, k0 = item.y, pslot = item.w;
-    if constexpr (SHARED)
-        if (!p.beside) // the items are the plan's; everything else may be the launch before's
+    if constexpr (SHARED) { // the items are the plan's; everything else may be an earlier launch's
+        if (!p.go_word) {
             ptx::grid_dependency_wait();
+        } else {
+            const bool go = ptx::wait_word(p.go_word, p.go);
+            ptx::fence_proxy_async_global();
+            if (!__syncthreads_and(go)) {
+                if (threadIdx.x == 0)
+                    atomicOr(&g_decode_error, 4u);
+                ptx::grid_dependency_wait();
+                return;
+            }
+        }
+    }
     // FUSED: does this item hold the new token?  Then the cache supplies keys k0 .. ctx-2.
     const bool has_new = FUSED && item.z > 0 && item.z == __ldg(p.context_lens + b);
     const int k1 = has_new ? item.z - 1 : item.z;
@@ -214,7 +227,7 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
     auto issue = [&](int i) {
         if ((i & 31) == 0) { // refresh the block ids of local chunks i .. i+31, one per lane
             const int key = k0 + 16 * (warp + W * (i + lane));
-            blk_cache = key < k1 ? __ldg(bt_row + key / bs) : 0;
+            blk_cache = key < k1 ? (SHARED ? bt_row[key / bs] : __ldg(bt_row + key / bs)) : 0;
         }
         int phys = __shfl_sync(0xffffffffu, blk_cache, i & 31);
         const int st = i % kStages;
@@ -259,7 +272,7 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
             p.q + ((size_t)b * Hq + (size_t)g * G + (valid ? hl : 0)) * D + c * (D / 4));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-            const uint2 w = valid ? __ldg(qrow + kk) : make_uint2(0u, 0u);
+            const uint2 w = valid ? (SHARED ? qrow[kk] : __ldg(qrow + kk)) : make_uint2(0u, 0u);
             qf[nt][kk][0] = bf16x2_to_f16x2<SHARED>(w.x);
             qf[nt][kk][1] = bf16x2_to_f16x2<SHARED>(w.y);
         }
@@ -534,7 +547,7 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
         }
     }
     if constexpr (SHARED) {
-        if (p.beside && blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
+        if (p.go_word && blockIdx.x == gridDim.x - 1) // so that whoever waits for this launch has waited for the one before
             ptx::grid_dependency_wait();
     }
 }
@@ -608,7 +621,8 @@ int launch_decode_int8(const DecodeArgs &a, void *stream)
     if (a.table_rows) { // parts of a shared-prefix decode
         p.table_rows = a.table_rows;
         p.num_blocks = a.dims.num_blocks;
-        p.beside = a.beside;
+        p.go_word = a.go_word;
+        p.go = a.go;
         if (a.few) {
             if (a.dims.head_dim == 128)
                 return two ? launch_int8<128, 2, false, true, kFewWarps>(a, p, s)
@@ -660,7 +674,8 @@ int read_decode_error(uint32_t *code)
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "reading decode error word: %s", cudaGetErrorString(e));
     *code |= (v & 1u) << 3;
-    *code |= (v & 2u) << 5; // the shared-prefix decode's bit 6
+    *code |= (v & 2u) << 5; // the shared-prefix decode's bits 6
+    *code |= (v & 4u) << 3; // and 5
     return PA_OK;
 }
 

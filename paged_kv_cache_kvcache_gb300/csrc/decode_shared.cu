@@ -106,6 +106,9 @@ struct ShParams {
     int32_t box_rows;
     int32_t max_blocks;
     int32_t num_blocks;
+    // bf16: `go` into the word (NULL: none), once the launches before have ended, for the launch beside
+    uint64_t *go_word;
+    uint64_t go;
 };
 
 struct Bars {
@@ -235,6 +238,8 @@ struct CodesParams {
     int32_t block_size, max_blocks, num_blocks, num_kv_heads, key_vecs, head_vecs;
     int32_t tile_ctas; // CTAs that convert keys; the others convert queries
     int64_t q_vecs;    // of 8 values
+    uint64_t *go_word; // as ShParams'
+    uint64_t go;
 };
 
 // What the products of the CTAs' lists read on an INT8 cache, in fp16: the shared prefixes' (and,
@@ -245,7 +250,9 @@ struct CodesParams {
 constexpr int kCodesKeys = 16;
 __global__ void __launch_bounds__(256) shared_codes_kernel(const CodesParams p)
 {
-    ptx::grid_dependency_wait(); // (before the line below: what it starts counts on this)
+    ptx::grid_dependency_wait();
+    if (p.go_word && blockIdx.x == 0 && threadIdx.x == 0)
+        ptx::st_release(p.go_word, p.go);
     ptx::launch_dependents();
     if ((int)blockIdx.x >= p.tile_ctas) {
         const int64_t i = (int64_t)((int)blockIdx.x - p.tile_ctas) * 256 + threadIdx.x;
@@ -328,8 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int P = p.rows_per_tile;
 
     // The launch after this one may be set up: a merge, which waits for this grid's end, or the parts of
-    // single sequences, which count on the end of the grid before this one only (INT8: of the one
-    // before the conversion, which has waited for that).
+    // single sequences, which wait for the word that this launch (INT8: the conversion) gives when the
+    // launches before it have ended.
     if (kInt8)
         ptx::launch_dependents();
     if (warp >= 8 && lane == 0) {
@@ -391,6 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= 8) {
         if (!kInt8) { // nothing but the plan is read before
             ptx::grid_dependency_wait();
+            if (p.go_word && blockIdx.x == 0 && warp == kKWarp && lane == 0)
+                ptx::st_release(p.go_word, p.go);
             ptx::launch_dependents();
         }
         const int4 a0 = __ldg(record + 2), a1 = __ldg(record + 3), b0 = __ldg(record + 4), b1 = __ldg(record + 5);
@@ -894,7 +903,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, int kSplit>
 __global__ void __launch_bounds__(kSplit == 8 ? 256 : 128)
     shared_combine_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse,
-                          const int2 *__restrict__ seq_parts, __nv_bfloat16 *__restrict__ out, int num_heads)
+                          const int2 *__restrict__ seq_parts, __nv_bfloat16 *__restrict__ out, int num_heads,
+                          uint64_t *go_word)
 {
     constexpr int E = D / 32;
     constexpr int kBatch = 8;
@@ -904,6 +914,8 @@ __global__ void __launch_bounds__(kSplit == 8 ? 256 : 128)
     const int2 sp = __ldg(seq_parts + b); // the plan's, written long before this launch's predecessor
     ptx::launch_dependents();
     ptx::grid_dependency_wait();          // the parts are complete and visible
+    if (go_word && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+        *go_word = 0; // taken back: a replayed call gives the same one again
     if (sp.y == 1 || h >= num_heads)
         return;
     const int per = kSplit == 1 ? sp.y : (sp.y + kSplit - 1) / kSplit;
@@ -988,7 +1000,7 @@ int encode_cache(CUtensorMap *m, const void *cache, int num_kv_heads, uint64_t r
 }
 
 // INT8: the scratch copies for the CTAs' lists.
-int launch_codes(const SharedArgs &a, cudaStream_t stream)
+int launch_codes(const SharedArgs &a, uint64_t go, cudaStream_t stream)
 {
     const pa_dims &d = a.dims;
     const size_t half = (size_t)a.num_scratch_tiles * 128 * d.num_kv_heads * d.head_dim * 2;
@@ -1011,6 +1023,8 @@ int launch_codes(const SharedArgs &a, cudaStream_t stream)
     c.key_vecs = d.num_kv_heads * c.head_vecs;
     c.tile_ctas = a.num_scratch_tiles * (128 / kCodesKeys);
     c.q_vecs = (int64_t)a.num_seqs * d.num_heads * d.head_dim / 8;
+    c.go_word = a.go_word;
+    c.go = go;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(c.tile_ctas + (c.q_vecs + 255) / 256));
     cfg.blockDim = dim3(256);
@@ -1028,11 +1042,11 @@ int launch_codes(const SharedArgs &a, cudaStream_t stream)
     return PA_OK;
 }
 
-// Items (sequence, key range, partial slot) of single sequences through the decode kernels;
-// `beside`: while the shared parts' products still run, on the SMs that those leave.  (INT8, beside
+// Items (sequence, key range, partial slot) of single sequences through the decode kernels; with a
+// go_word beside the shared parts' products, on the SMs that those leave.  (INT8, beside
 // the conversion instead, with the products after both: 64 x 16384 took 75 us, not 50; these parts
 // are long and few, and the products waited for them.)
-int launch_singles(const SharedArgs &a, const int32_t *items, int32_t num_items, bool beside, cudaStream_t stream)
+int launch_singles(const SharedArgs &a, const int32_t *items, int32_t num_items, uint64_t go, cudaStream_t stream)
 {
     DecodeArgs s{};
     s.dims = a.dims;
@@ -1051,14 +1065,15 @@ int launch_singles(const SharedArgs &a, const int32_t *items, int32_t num_items,
     s.num_items = num_items;
     s.max_blocks_per_seq = a.max_blocks_per_seq;
     s.table_rows = a.table_rows;
-    s.beside = beside;
+    s.go_word = a.go_word;
+    s.go = go;
     int sms = 0;
     if (int rc = sm_count(&sms))
         return rc;
     // then eight warps each instead of four, which shortens the chain of steps: 8 contexts of 300 tokens
     // 6.2 us instead of 6.6, of 808 9.2 instead of 11.0, INT8 10.6 instead of 13.8; with more items than
     // SMs the wider ones have no room beside one another
-    s.few = (int64_t)num_items * a.dims.num_kv_heads <= sms - (beside ? a.num_ctas : 0);
+    s.few = (int64_t)num_items * a.dims.num_kv_heads <= sms - (a.go_word ? a.num_ctas : 0);
     return a.k_scale ? launch_decode_int8(s, stream) : launch_decode(s, stream);
 }
 
@@ -1082,9 +1097,13 @@ int launch(const SharedArgs &a, cudaStream_t stream)
                     kLaunchRegs);
     const pa_dims &d = a.dims;
     const int G = d.num_heads / d.num_kv_heads;
+    // this call's word: another for each call (multiples of an odd number), none that a workspace's first
+    // contents are likely to hold
+    static std::atomic<uint64_t> calls{0};
+    const uint64_t go = a.go_word ? (calls.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9e3779b97f4a7c15ull : 0;
     if (a.num_items > 0) {
         if (kInt8)
-            if (int rc = launch_codes(a, stream))
+            if (int rc = launch_codes(a, go, stream))
                 return rc;
         const uint32_t box_rows = !kInt8 && d.block_size < kBoxRows ? (uint32_t)d.block_size : (uint32_t)kBoxRows;
         // INT8: the products read the scratch cache
@@ -1123,6 +1142,8 @@ int launch(const SharedArgs &a, cudaStream_t stream)
         p.box_rows = (int32_t)box_rows;
         p.max_blocks = a.max_blocks_per_seq;
         p.num_blocks = d.num_blocks;
+        p.go_word = kInt8 ? nullptr : a.go_word;
+        p.go = go;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)a.num_ctas);
         cfg.blockDim = dim3(kThreads);
@@ -1140,9 +1161,9 @@ int launch(const SharedArgs &a, cudaStream_t stream)
         }
     }
     if (a.num_single_items > 0)
-        if (int rc = launch_singles(a, a.single_items, a.num_single_items, a.num_items > 0, stream))
+        if (int rc = launch_singles(a, a.single_items, a.num_single_items, go, stream))
             return rc;
-    if (!a.merge)
+    if (!a.merge && !a.go_word)
         return PA_OK;
     // Programmatic launch: the merge's blocks are set up while the parts still run and wait
     // inside for the end of that grid.  Without a grid before it, it waits for nothing.  (One
@@ -1167,7 +1188,7 @@ int launch(const SharedArgs &a, cudaStream_t stream)
     const cudaError_t e =
         cudaLaunchKernelEx(&cfg, combine, (const float *)a.part_o, (const float *)a.part_lse,
                            reinterpret_cast<const int2 *>(a.seq_parts), static_cast<__nv_bfloat16 *>(a.out),
-                           (int)d.num_heads);
+                           (int)d.num_heads, a.go_word);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(PA_ERR_CUDA, "shared decode merge launch: %s", cudaGetErrorString(e));
@@ -1181,7 +1202,7 @@ int launch_decode_shared(const SharedArgs &a, void *stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (a.direct_items)
-        return launch_singles(a, a.direct_items, a.num_seqs, false, s);
+        return launch_singles(a, a.direct_items, a.num_seqs, 0, s);
     if (a.k_scale)
         return a.dims.head_dim == 128 ? launch<128, true>(a, s) : launch<64, true>(a, s);
     return a.dims.head_dim == 128 ? launch<128, false>(a, s) : launch<64, false>(a, s);

@@ -182,7 +182,8 @@ struct DecodeArgs {
     const int32_t *slot_mapping;
     // contexts or parts of a shared-prefix decode (else NULL): no merge is launched
     const int32_t *table_rows; // block-table row of each sequence
-    bool beside;               // may run beside the launch before it
+    const uint64_t *go_word;   // may run beside the launch before it, once this word is `go` (NULL: may not)
+    uint64_t go;
     bool few;                  // each (item, KV head) has an SM to itself
 };
 int launch_decode(const DecodeArgs &a, void *stream);
@@ -206,6 +207,7 @@ struct SharedArgs {
     const int32_t *table_rows;
     const int32_t *direct_items; // set: every context is decoded whole, nothing is shared
     const int32_t *scratch_tiles;
+    uint64_t *go_word; // given by the shared parts' launches, awaited by the own parts beside them (NULL: none)
     void *scratch; // INT8: what the items read, in fp16: K, then V, then the queries
     int32_t num_scratch_tiles;
     void *out;
@@ -222,7 +224,7 @@ struct SharedArgs {
     bool merge; // some sequence has two or more parts, or none
 };
 int launch_decode_shared(const SharedArgs &a, void *stream);
-// Workspace layout of a shared-prefix decode: partial outputs, their log-sum-exps, then (INT8) the scratch.
+// Workspace layout of a shared-prefix decode: partial outputs, their log-sum-exps, the word, then (INT8) the scratch.
 inline size_t shared_part_o_bytes(const pa_dims &d, int64_t partials)
 {
     return align_up((size_t)partials * d.num_heads * d.head_dim * 4, 256);
@@ -231,6 +233,12 @@ inline size_t shared_part_bytes(const pa_dims &d, int64_t partials)
 {
     return partials > 0 ? shared_part_o_bytes(d, partials) + align_up((size_t)partials * d.num_heads * 4, 256) : 0;
 }
+// Parts of single sequences run beside those of several: a word lies behind the partial results.
+inline bool shared_beside(const pa_shared_meta &m)
+{
+    return m.apart && m.num_items > 0 && m.num_single_items > 0;
+}
+inline size_t shared_go_bytes(const pa_shared_meta &m) { return shared_beside(m) ? 256 : 0; }
 inline size_t shared_scratch_bytes(const pa_dims &d, int64_t tiles, int64_t num_seqs)
 {
     return tiles == 0 ? 0

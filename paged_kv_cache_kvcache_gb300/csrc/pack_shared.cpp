@@ -388,9 +388,9 @@ static int pack_decode_shared(const pa_dims *dims, int32_t num_seqs, const int32
     meta->off_direct_items = L.take(sizeof(int32_t) * 4 * (size_t)num_seqs);
     meta->off_scratch_tiles = L.take(sizeof(int32_t) * 4 * (size_t)scratch_tiles);
     meta->total_bytes = L.off;
-    meta->workspace_bytes = direct ? 0 : shared_part_bytes(d, partials);
-    meta->workspace_bytes_int8 =
-        direct_int8 ? 0 : shared_part_bytes(d, partials) + shared_scratch_bytes(d, scratch_tiles, num_seqs);
+    const size_t results = shared_part_bytes(d, partials) + shared_go_bytes(*meta);
+    meta->workspace_bytes = direct ? 0 : results;
+    meta->workspace_bytes_int8 = direct_int8 ? 0 : results + shared_scratch_bytes(d, scratch_tiles, num_seqs);
     if (!host_buf)
         return PA_OK;
     if (host_buf_bytes < meta->total_bytes)

@@ -29,6 +29,33 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 // for an ordinary launch).
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// ------------------------------------------------------------------ a word between grids
+
+__device__ __forceinline__ void st_release(uint64_t *word, uint64_t v)
+{
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(word), "l"(v) : "memory");
+}
+// Waits until the word is v: what its writer had seen, this thread sees from here on.  Bounded: false
+// after `timeout_ns`.
+__device__ __forceinline__ bool wait_word(const uint64_t *word, uint64_t v, uint64_t timeout_ns = 2000000000ull)
+{
+    uint64_t x, t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(word) : "memory");
+        if (x == v)
+            return true;
+        if (it == 0)
+            t0 = globaltimer();
+        else if ((it & 63u) == 0 && globaltimer() - t0 > timeout_ns)
+            return false;
+    }
+}
+// The copy engine's reads of global memory (TMA, bulk copies) after this come after what this thread has seen.
+__device__ __forceinline__ void fence_proxy_async_global()
+{
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
