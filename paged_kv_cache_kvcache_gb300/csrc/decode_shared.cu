@@ -43,7 +43,7 @@
 // through the decode kernels, which start in less time and have nothing to merge.
 //
 // Every hand-off waits with a time limit; a wait that runs out sets an error bit and the
-// kernel returns.  A block id outside the pool reads as zeros and sets an error bit.
+// kernel returns, once nothing that it issued can be in flight any more.  A block id outside the pool reads as zeros and sets an error bit.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -888,6 +888,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     ptx::tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {
+        // A wait ran out: copies and products issued since may be in flight.  They end within microseconds;
+        // shared and tensor memory are kept for 20 ms.  (Counted, to wait on their barriers, they cost
+        // every call 0.3 to 1 us.)
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < 20000000u) {
+        }
+    }
     if (warp == kMmaWarp) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, kTmemCols);
