@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(256) shared_codes_kernel(const CodesParams p)
         const int64_t i = (int64_t)((int)blockIdx.x - p.tile_ctas) * 256 + threadIdx.x;
         if (i >= p.q_vecs)
             return;
-        const uint4 v = __ldg(p.q + i);
+        const uint4 v = p.q[i];
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
         uint32_t w[4];
 #pragma unroll
@@ -285,15 +285,15 @@ __global__ void __launch_bounds__(256) shared_codes_kernel(const CodesParams p)
             ks[u] = vs[u] = __half2half2(__ushort_as_half(0));
             const int key = first + i / p.key_vecs;
             if (i < total && key < t.z) {
-                const int phys = __ldg(p.block_tables + (size_t)t.x * p.max_blocks + key / bs);
+                const int phys = p.block_tables[(size_t)t.x * p.max_blocks + key / bs];
                 if ((uint32_t)phys < (uint32_t)p.num_blocks) {
                     const int vec = i % p.key_vecs, off = key & (bs - 1);
                     const size_t at = ((size_t)phys * bs + off) * p.key_vecs + vec;
                     const size_t sc = ((size_t)phys * p.num_kv_heads + vec / p.head_vecs) * bs + off;
-                    k[u] = __ldg(p.k_codes + at);
-                    v[u] = __ldg(p.v_codes + at);
-                    ks[u] = __half2half2(__ushort_as_half(__ldg(p.k_scale + sc)));
-                    vs[u] = __half2half2(__ushort_as_half(__ldg(p.v_scale + sc)));
+                    k[u] = p.k_codes[at];
+                    v[u] = p.v_codes[at];
+                    ks[u] = __half2half2(__ushort_as_half(p.k_scale[sc]));
+                    vs[u] = __half2half2(__ushort_as_half(p.v_scale[sc]));
                 } else {
                     atomicOr(&g_shared_error, 2u);
                 }
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return kInt8 ? p.scratch_rows : p.num_blocks * p.block_size;
         if (kInt8)
             return w.scratch + key;
-        const int phys = __ldg(p.block_tables + (size_t)w.row * p.max_blocks + key / p.block_size);
+        const int phys = p.block_tables[(size_t)w.row * p.max_blocks + key / p.block_size];
         if ((uint32_t)phys >= (uint32_t)p.num_blocks) {
             atomicOr(&g_shared_error, 2u);
             return p.num_blocks * p.block_size;
@@ -910,9 +910,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // latency of the loads: 65 parts in one warp took 18 us, in eight 3.
 template <int D, int kSplit>
 __global__ void __launch_bounds__(kSplit == 8 ? 256 : 128)
-    shared_combine_kernel(const float *__restrict__ part_o, const float *__restrict__ part_lse,
-                          const int2 *__restrict__ seq_parts, __nv_bfloat16 *__restrict__ out, int num_heads,
-                          uint64_t *go_word)
+    shared_combine_kernel(const float *part_o, const float *part_lse, const int2 *seq_parts, __nv_bfloat16 *out,
+                          int num_heads, uint64_t *go_word)
 {
     constexpr int E = D / 32;
     constexpr int kBatch = 8;

@@ -334,7 +334,7 @@ __device__ __forceinline__ void plan_begin(Team<kCluster> &team, const PoolParam
 // parents' table rows, up to their lengths; else (a compaction) of all n rows, entries of -1 excepted.
 // Four at a time: each is a chain of four (two) dependent loads.
 template <bool kFork>
-__device__ __forceinline__ bool bad_cells(const PoolParams &p, const int32_t *__restrict__ parents, int n, int from,
+__device__ __forceinline__ bool bad_cells(const PoolParams &p, const int32_t *parents, int n, int from,
                                           int step)
 {
     constexpr int kU = 4;
@@ -368,7 +368,7 @@ __device__ __forceinline__ bool bad_cells(const PoolParams &p, const int32_t *__
 // with this launch, 45.7 unchecked; more cells take the planning CTA a chain of loads per 4096, this less.)
 template <bool kFork>
 __global__ void __launch_bounds__(256)
-    pool_check_kernel(const PoolParams p, const int32_t *__restrict__ parents, int n, void *workspace)
+    pool_check_kernel(const PoolParams p, const int32_t *parents, int n, void *workspace)
 {
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
@@ -399,8 +399,8 @@ __device__ __forceinline__ int slot_of(const PoolParams &p, int row, int pos)
 // are written here (few tokens), else by pool_slots_kernel.
 template <bool kCluster, bool kSlots>
 __global__ void __launch_bounds__(kThreads)
-    pool_append_kernel(const PoolParams p, const int32_t *__restrict__ rows, const int32_t *__restrict__ cu, int n,
-                       int32_t *__restrict__ slots, int num_tokens, void *workspace)
+    pool_append_kernel(const PoolParams p, const int32_t *rows, const int32_t *cu, int n,
+                       int32_t *slots, int num_tokens, void *workspace)
 {
     __shared__ Smem sm;
     if (!kSlots)
@@ -508,8 +508,8 @@ __global__ void __launch_bounds__(kThreads)
 // The slots of many tokens, from the tables as the plan left them: four tokens per thread, the
 // warp's first row found once.
 __global__ void __launch_bounds__(256)
-    pool_slots_kernel(const PoolParams p, const int32_t *__restrict__ rows, const int32_t *__restrict__ cu, int n,
-                      int32_t *__restrict__ slots, int num_tokens, void *workspace)
+    pool_slots_kernel(const PoolParams p, const int32_t *rows, const int32_t *cu, int n,
+                      int32_t *slots, int num_tokens, void *workspace)
 {
     ptx::grid_dependency_wait();
     const bool refused = *static_cast<const int32_t *>(workspace) < 0;
@@ -547,7 +547,7 @@ __global__ void __launch_bounds__(256)
 
 template <bool kCluster>
 __global__ void __launch_bounds__(kThreads)
-    pool_fork_kernel(const PoolParams p, const int32_t *__restrict__ parents, const int32_t *__restrict__ children,
+    pool_fork_kernel(const PoolParams p, const int32_t *parents, const int32_t *children,
                      int n, int row_bytes, int checked, void *workspace)
 {
     __shared__ Smem sm;
@@ -729,8 +729,8 @@ __device__ __forceinline__ void copy_pieces(const Planes &q, int64_t units, F of
 // The forked rows' tables and counts, and their partly filled pages: all layers of the i-th of
 // all pieces before those of the next.
 __global__ void __launch_bounds__(kMoveThreads)
-    pool_fork_copy_kernel(const PoolParams p, const Planes q, const int32_t *__restrict__ parents,
-                          const int32_t *__restrict__ children, void *workspace)
+    pool_fork_copy_kernel(const PoolParams p, const Planes q, const int32_t *parents,
+                          const int32_t *children, void *workspace)
 {
     ptx::grid_dependency_wait();
     const Ws w = carve(workspace, p.num_rows, p.num_blocks);
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 // ---------------------------------------------------------------- free
 
 // One CTA per row.  The context length is taken by exchange, so a row named twice is given back once.
-__global__ void __launch_bounds__(128) pool_free_kernel(const PoolParams p, const int32_t *__restrict__ rows)
+__global__ void __launch_bounds__(128) pool_free_kernel(const PoolParams p, const int32_t *rows)
 {
     __shared__ int s_ctx;
     ptx::grid_dependency_wait();
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(128) pool_free_kernel(const PoolParams p, cons
 // arrays tell of pages that stay where they are.
 template <bool kCluster>
 __global__ void __launch_bounds__(kThreads)
-    pool_compact_kernel(const PoolParams p, int32_t *__restrict__ remap, int32_t *refs_out, int checked, void *workspace)
+    pool_compact_kernel(const PoolParams p, int32_t *remap, int32_t *refs_out, int checked, void *workspace)
 {
     __shared__ Smem sm;
     ptx::launch_dependents();
@@ -928,7 +928,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 __global__ void __launch_bounds__(kMoveThreads)
-    pool_move_kernel(const PoolParams p, const Planes q, const int32_t *__restrict__ remap, int32_t *tables_out,
+    pool_move_kernel(const PoolParams p, const Planes q, const int32_t *remap, int32_t *tables_out,
                      void *workspace)
 {
     ptx::grid_dependency_wait();

@@ -26,7 +26,9 @@ __device__ __forceinline__ uint64_t globaltimer()
 // Lets the next launch of the stream, if it was launched to allow that, be set up now.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 // Waits until the launches this one depends on are complete and their writes visible (at once
-// for an ordinary launch).
+// for an ordinary launch).  What those may have written is read by ordinary loads: a read-only one
+// (__ldg, or through a const __restrict__ parameter) is for data that does not change while the kernel
+// runs, and may be moved before the wait.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------------------ a word between grids
