@@ -451,7 +451,9 @@ int pa_copy_blocks(const pa_dims *dims, void *k_cache, void *v_cache, const int3
  * order with the stores and decodes that use them, so that a step needs no
  * block id from the host (it knows the lengths): the stores take the slots
  * written here, pa_decode_shared(_int8) the pool's tables (its groups may be of
- * one, and an entry that a refused call left -1 reads as zeros there).
+ * one, and an entry that a refused call left -1 reads as zeros there).  The
+ * prefill and pa_decode take block ids that their plans were packed from, on the
+ * host; pool rows can be read by them only through tables copied back.
  * Source: "手搓 vLLM 推理引擎", Step 2 (BlockManager: reference counts,
  * allocate, may_append, deallocate); "vLLM / SGLang 面试源码深挖", section 4
  * (fork).  New pages are always the free pages of the lowest ids, so the

@@ -19,8 +19,9 @@
 // One persistent launch runs every part.  A work item is (rows, KV head, key range, block-table
 // row): a prefix part carries many sequences, a suffix part one.  A CTA holds two query tiles of
 // 128 rows and runs its items in two ways:
-//  * a prefix part of more than 128 rows is a PAIR: both tiles against one stream of K/V, bound
-//    by the tensor core (measured 1.62 us per 128 keys, of which the products are 1.0);
+//  * a prefix part of more than 128 rows is a PAIR: both tiles against one stream of K/V, bound by
+//    what one tile's softmax and hand-offs take beyond the other's products (measured 1.62 us per 128
+//    keys, of which the products are 1.0; tensor pipe 58 % busy on the SMs in use);
 //  * every other part is a SINGLE: one tile, 128 keys whose products take about 1100 cycles of the
 //    tensor core while their 64 KB of K/V take about 2800 cycles of this SM's share of HBM.  But
 //    score product, softmax and value product of one tile follow one another (about 2700 cycles
@@ -61,7 +62,8 @@ namespace {
 
 // warps 0-7: softmax (two warpgroups), 8: K producer, 9: MMA issuer and TMEM owner, 10: V
 // producer, 11: query producer.  168 registers per thread at launch; setmaxnreg moves part of
-// warps 8-11's share to the softmax warps.
+// warps 8-11's share to the softmax warps.  (ptxas -v: 36 bytes of spill stores a thread and 172 of spill
+// loads, not traced to their place.)
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;

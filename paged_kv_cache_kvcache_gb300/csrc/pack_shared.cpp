@@ -20,7 +20,7 @@ constexpr int32_t kTile = kPrefillKeyTile;
 
 // Time model in microseconds, used only to choose the key ranges and to deal the items out
 // (measured on GB300, D = 128).  A pair (two query tiles on one K/V stream) occupies both lanes of
-// its CTA and is bound by the tensor core.  A single occupies one lane; alone in its CTA its step
+// its CTA, its step bound by the softmax and its hand-offs.  A single occupies one lane; alone in its CTA its step
 // takes kSharedStep, beside another's kSingleStep.  An item adds its query load and its output.  A
 // partial costs its bytes written and read again.
 //
