@@ -285,12 +285,14 @@ class DecodePlan(_Plan):
 
 
 class SharedPlan(_Plan):
-    num_rows = 0  # rows that the block table must have
+    num_rows = 0       # rows that the block table must have
+    call_shape = None  # of the plan that was uploaded: those rows, and the table's width
 
     def upload(self, device="cuda", stream=None) -> "SharedPlan":
         super().upload(device, stream)
         m, base = self.meta, self.dev.data_ptr()
         self.device = self.dev.get_device()
+        self.call_shape = (self.num_rows, m.max_blocks_per_seq)
         self.call_ref = ctypes.byref(m)
         self.call_tables = base + m.off_block_tables if m.tables_packed or m.num_seqs == 0 else None
         self.call_arrays = tuple(base + x for x in (m.off_items, m.off_cta_items, m.off_seq_parts, m.off_direct_items,
@@ -481,9 +483,9 @@ def _shared_tables(plan: SharedPlan, block_tables) -> int:
             raise ValueError("the plan was packed for device tables: pass block_tables")
         return plan.call_tables
     at = _int32(block_tables, "block_tables")
-    if block_tables.dim() != 2 or block_tables.shape[1] != plan.meta.max_blocks_per_seq or \
-            block_tables.shape[0] < plan.num_rows:
-        raise ValueError(f"block_tables must be [{plan.num_rows} rows or more, {plan.meta.max_blocks_per_seq}]")
+    rows, width = plan.call_shape or (plan.num_rows, plan.meta.max_blocks_per_seq)
+    if block_tables.dim() != 2 or block_tables.shape[1] != width or block_tables.shape[0] < rows:
+        raise ValueError(f"block_tables must be [{rows} rows or more, {width}]")
     return at
 
 

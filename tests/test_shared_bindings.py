@@ -84,3 +84,27 @@ def test_an_empty_batch_needs_nothing(monkeypatch):
     t = tensors(False)
     pa.pa_decode_shared(pa.make_dims(*DIMS), t["q"][:0], t["k"], t["v"], plan, 0.1, t["out"][:0], stream=0)
     assert recorder.calls[-1] == "pa_decode_shared"
+
+
+def test_a_plan_packed_again_counts_from_its_upload_on(plan_and_calls, monkeypatch):
+    """Until it is uploaded again, calls run the plan on the device: what they need goes by that one."""
+    plan, calls = plan_and_calls  # rows 0, 2 and 1 of a table 3 wide
+    recorder = pa._lib
+    monkeypatch.setattr(pa, "_lib", None)  # the packer is the library's
+    again = pa.pa_pack_decode_shared(pa.make_dims(*DIMS), [10], shared_lens=[0], table_rows=[0], max_blocks=2,
+                                     split_tokens=128, into=plan)
+    assert again is plan and plan.num_rows == 1
+    monkeypatch.setattr(pa, "_lib", recorder)
+    t = tensors(False)
+    for shape in ((1, 2), (2, 3), (3, 2)):
+        with pytest.raises(ValueError, match="3 rows or more, 3"):
+            pa.pa_decode_shared(pa.make_dims(*DIMS), t["q"], t["k"], t["v"], plan, 0.1, t["out"],
+                                block_tables=torch.zeros(*shape, dtype=torch.int32), stream=0)
+    with pytest.raises(ValueError, match="q has"):
+        call(plan, {**t, "q": t["q"][:1]})
+    call(plan, t)
+    plan.upload(device="cpu", stream=0)
+    calls.clear()
+    pa.pa_decode_shared(pa.make_dims(*DIMS), t["q"][:1], t["k"], t["v"], plan, 0.1, t["out"][:1],
+                        block_tables=torch.zeros(1, 2, dtype=torch.int32), stream=0)
+    assert calls == ["pa_decode_shared"]
