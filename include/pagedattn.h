@@ -188,6 +188,24 @@ typedef struct pa_pool {
     uint64_t scale_layer_stride; /* the same for the scales */
 } pa_pool;
 
+/*
+ * Norm and rotation of query and key heads (pa_rope_store).  Pair i of a head's
+ * first rotary_dim values, (i, i + rotary_dim/2) or, interleaved, (2i, 2i + 1),
+ * turns by the angle that row positions[pair_axis[i]][t] of cos_sin gives it; the
+ * values behind them are only normed.
+ */
+typedef struct pa_rope {
+    int32_t rotary_dim;     /* R: a multiple of 16, at most head_dim */
+    int32_t interleaved;    /* 0 or 1 */
+    int32_t num_axes;       /* positions per token, 1 to 4 (time, height, width, ...) */
+    int32_t max_position;   /* rows of cos_sin */
+    float eps;              /* of the norms, >= 0 */
+    uint8_t pair_axis[64];  /* axis of each of the R/2 pairs */
+    const float *cos_sin;   /* device fp32 [max_position][R]: R/2 cosines, then R/2 sines; 16-byte aligned */
+    const void *q_weight;   /* device bf16 [head_dim], 16-byte aligned; NULL: no norm of the queries */
+    const void *k_weight;   /* the same for the keys */
+} pa_rope;
+
 /* ------------------------------------------------------------------ host packing */
 
 /*
@@ -277,6 +295,44 @@ int pa_upload(void *dev_dst, const void *host_src, size_t bytes, pa_stream_t str
 int pa_store_kvcache(const pa_dims *dims, const void *k, const void *v, void *k_cache,
                      void *v_cache, const int32_t *slot_mapping, int32_t num_tokens,
                      pa_stream_t stream);
+
+/*
+ * pa_rope_store — the step in front of the attention: each query and key head's
+ * norm, its rotation by the token's position (one position, or one per axis for
+ * images and video), and the store of the new keys and values, in one pass.
+ * Source: "手搓 vLLM 推理引擎", Step 4 (Attention.forward stores the new K/V and
+ * then attends) and Step 5 (positions and slots of the new tokens).  For each
+ * head row x of a token's queries and keys
+ *   y = x * rsqrt(mean(x^2) + eps) * w     (no norm where the weight is NULL)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)    for each pair
+ * in fp32, rounded once to bf16; values are copied.
+ *   q, k, v:    device bf16; token t's heads are the num_heads (num_kv_heads) *
+ *               head_dim contiguous values from t * q_stride (k_, v_stride) on;
+ *               strides in values, multiples of 8, at least a token's values
+ *               (parts of one projection's output, for instance)
+ *   positions:  device int32 [rope->num_axes][num_tokens].  A token of a position
+ *               outside [0, max_position) is skipped as a whole and flagged
+ *               (pa_read_device_error bit 9)
+ *   slot_mapping: as pa_store_kvcache (-1: the key and value are not stored, the
+ *               query is computed; other slots outside the cache are flagged, bit 0)
+ *   q_out:      device bf16 [num_tokens][num_heads][head_dim]; may be q itself
+ * The launch may be set up during the kernel before it in the stream; it reads
+ * and writes nothing until that has ended.
+ */
+int pa_rope_store(const pa_dims *dims, const pa_rope *rope, const void *q, const void *k, const void *v,
+                  int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *positions,
+                  const int32_t *slot_mapping, int32_t num_tokens, void *q_out, void *k_cache, void *v_cache,
+                  pa_stream_t stream);
+
+/*
+ * pa_rope_store_int8 — pa_rope_store into an INT8 cache: the turned key (in fp32,
+ * not rounded to bf16 first) and the value are quantised as pa_store_kvcache_int8
+ * quantises a row.
+ */
+int pa_rope_store_int8(const pa_dims *dims, const pa_rope *rope, const void *q, const void *k, const void *v,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *positions,
+                       const int32_t *slot_mapping, int32_t num_tokens, void *q_out, void *k_cache, void *v_cache,
+                       void *k_scale, void *v_scale, pa_stream_t stream);
 
 /*
  * pa_prefill_varlen — causal variable-length prefill over the paged cache.
@@ -725,7 +781,8 @@ const char *pa_last_error_string(void);
  * INT8 decode kernel timed out; 4 the wait of pa_selftest_bounded_wait timed
  * out; 5 a bounded wait in the shared-prefix decode timed out; 6 the
  * shared-prefix decode met a block id outside the pool; 7 a pa_pool call was
- * refused for lack of room; 8 a pa_pool call was malformed, or the pool's state.  Synchronises `stream`: for tests and debugging, never on the hot path.
+ * refused for lack of room; 8 a pa_pool call was malformed, or the pool's state; 9 a position of
+ * pa_rope_store lies outside its table.  Synchronises `stream`: for tests and debugging, never on the hot path.
  */
 int pa_read_device_error(uint32_t *code, pa_stream_t stream);
 

@@ -91,6 +91,69 @@ extern "C" int pa_store_kvcache(const pa_dims *dims, const void *k, const void *
     return launch_store_kvcache(*dims, k, v, k_cache, v_cache, slot_mapping, num_tokens, stream);
 }
 
+// Host-side checks of pa_rope_store(_int8), then the launch.
+static int rope_store(const char *fn, const pa_dims *dims, const pa_rope *rope, const void *q, const void *k,
+                      const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *positions,
+                      const int32_t *slot_mapping, int32_t num_tokens, void *q_out, void *k_cache, void *v_cache,
+                      bool int8, void *k_scale, void *v_scale, pa_stream_t stream)
+{
+    int rc = check_dims(dims);
+    if (rc != PA_OK)
+        return rc;
+    if (!rope)
+        return fail(PA_ERR_INVALID_ARG, "%s: rope is NULL", fn);
+    const pa_rope &r = *rope;
+    if (r.rotary_dim < 16 || r.rotary_dim > dims->head_dim || r.rotary_dim % 16 != 0)
+        return fail(PA_ERR_UNSUPPORTED, "%s: rotary_dim %d is not a multiple of 16 in [16, head_dim]", fn, r.rotary_dim);
+    if (r.num_axes < 1 || r.num_axes > 4)
+        return fail(PA_ERR_UNSUPPORTED, "%s: num_axes %d not in [1, 4]", fn, r.num_axes);
+    for (int i = 0; i < r.rotary_dim / 2; ++i)
+        if (r.pair_axis[i] >= r.num_axes)
+            return fail(PA_ERR_INVALID_ARG, "%s: pair %d turns on axis %d of %d", fn, i, r.pair_axis[i], r.num_axes);
+    if ((r.interleaved != 0 && r.interleaved != 1) || r.max_position < 1 || !(r.eps >= 0.f) || !std::isfinite(r.eps))
+        return fail(PA_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1, max_position positive, eps finite and >= 0", fn);
+    if (num_tokens < 0)
+        return fail(PA_ERR_INVALID_ARG, "num_tokens < 0");
+    if (num_tokens == 0)
+        return PA_OK;
+    if (!r.cos_sin || !q || !k || !v || !positions || !slot_mapping || !q_out || !k_cache || !v_cache ||
+        (int8 && (!k_scale || !v_scale)))
+        return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (misaligned(r.cos_sin) || misaligned(r.q_weight) || misaligned(r.k_weight) || misaligned(q) || misaligned(k) ||
+        misaligned(v) || misaligned(q_out) || misaligned(k_cache) || misaligned(v_cache) || misaligned(k_scale) ||
+        misaligned(v_scale))
+        return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+    const int64_t qrow = (int64_t)dims->num_heads * dims->head_dim, krow = (int64_t)dims->num_kv_heads * dims->head_dim;
+    if (q_stride < qrow || k_stride < krow || v_stride < krow || q_stride % 8 || k_stride % 8 || v_stride % 8)
+        return fail(PA_ERR_INVALID_ARG, "%s: strides must be multiples of 8 of at least a token's values", fn);
+    if (q_out == q && q_stride != qrow)
+        return fail(PA_ERR_INVALID_ARG, "%s: q_out may only be q where q's tokens are contiguous", fn);
+    if (dims->num_blocks == 0)
+        return fail(PA_ERR_INVALID_ARG, "empty KV pool");
+    return launch_rope_store({*dims, r, q, k, v, q_stride, k_stride, v_stride, positions, slot_mapping, num_tokens, q_out,
+                              k_cache, v_cache, k_scale, v_scale},
+                             stream);
+}
+
+extern "C" int pa_rope_store(const pa_dims *dims, const pa_rope *rope, const void *q, const void *k, const void *v,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *positions,
+                             const int32_t *slot_mapping, int32_t num_tokens, void *q_out, void *k_cache,
+                             void *v_cache, pa_stream_t stream)
+{
+    return rope_store("pa_rope_store", dims, rope, q, k, v, q_stride, k_stride, v_stride, positions, slot_mapping,
+                      num_tokens, q_out, k_cache, v_cache, false, nullptr, nullptr, stream);
+}
+
+extern "C" int pa_rope_store_int8(const pa_dims *dims, const pa_rope *rope, const void *q, const void *k,
+                                  const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                  const int32_t *positions, const int32_t *slot_mapping, int32_t num_tokens,
+                                  void *q_out, void *k_cache, void *v_cache, void *k_scale, void *v_scale,
+                                  pa_stream_t stream)
+{
+    return rope_store("pa_rope_store_int8", dims, rope, q, k, v, q_stride, k_stride, v_stride, positions, slot_mapping,
+                      num_tokens, q_out, k_cache, v_cache, true, k_scale, v_scale, stream);
+}
+
 // Host-side checks shared by pa_prefill_varlen and pa_prefill_varlen_int8;
 // fills `a`.  Sets *nothing when the plan has no work (then no launch happens).
 static int prepare_prefill(const char *fn, const pa_dims *dims, const void *q, const void *k_cache,
@@ -775,6 +838,8 @@ extern "C" int pa_read_device_error(uint32_t *code, pa_stream_t stream)
         rc = read_shared_error(code);
     if (rc == PA_OK)
         rc = read_pool_error(code);
+    if (rc == PA_OK)
+        rc = read_rope_error(code);
     return rc;
 }
 

@@ -259,6 +259,21 @@ int launch_pool_fork(const PoolArgs &a, const int32_t *parents, const int32_t *c
 int launch_pool_free(const PoolArgs &a, const int32_t *rows, int n, void *stream);
 int launch_pool_compact(const PoolArgs &a, int32_t *remap, int32_t *tables_out, int32_t *refs_out, void *stream);
 
+// Norm, rotation and store (rope_store.cu); k_scale / v_scale NULL: bf16 cache.
+struct RopeArgs {
+    pa_dims dims;
+    pa_rope rope;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *positions;
+    const int32_t *slot_mapping;
+    int32_t num_tokens;
+    void *q_out;
+    void *k_cache, *v_cache;
+    void *k_scale, *v_scale;
+};
+int launch_rope_store(const RopeArgs &a, void *stream);
+
 // Device address of the library-owned decode scratch on the current device
 // (looked up once per device).  Used only by pa_decode_static.
 int decode_static_scratch(void **ptr);
@@ -280,6 +295,7 @@ int read_fused_error(uint32_t *code);
 int read_fused8_error(uint32_t *code);
 int read_shared_error(uint32_t *code); // bit 0 -> 5 (wait), bit 1 -> 6 (block id outside the pool)
 int read_pool_error(uint32_t *code);   // bit 0 -> 7 (no room), bit 1 -> 8 (malformed)
+int read_rope_error(uint32_t *code);   // bit 0 (slot), bit 1 -> 9 (position)
 int launch_selftest_wait(uint32_t timeout_us, int arrive_first, void *stream);
 int read_selftest_error(uint32_t *code);
 int launch_stream_read(const void *src, size_t bytes, uint32_t *sink, void *stream);

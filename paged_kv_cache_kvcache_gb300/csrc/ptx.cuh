@@ -178,6 +178,18 @@ __device__ __forceinline__ int4 ld_nc_v4_now(const int4 *p)
     return v;
 }
 
+// 16-byte global load of data that is read once (it stays out of L1); an ordinary load, so it sees what an
+// earlier launch wrote, after grid_dependency_wait().
+__device__ __forceinline__ uint4 ld_once_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // 32-byte global store (address 32-byte aligned): one whole sector per thread.
 __device__ __forceinline__ void st_global_v8(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e,
                                              uint32_t f, uint32_t g, uint32_t h)

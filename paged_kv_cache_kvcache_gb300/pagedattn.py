@@ -26,6 +26,7 @@ EXPORTS = ("pa_pack_prefill", "pa_pack_decode", "pa_upload", "pa_store_kvcache",
            "pa_decode_int8_fused", "pa_prefill_varlen_fused", "pa_prefill_varlen_int8_fused",
            "pa_pack_decode_shared", "pa_decode_shared", "pa_decode_shared_int8", "pa_pool_workspace", "pa_pool_append",
            "pa_pool_fork", "pa_pool_free", "pa_pool_compact",
+           "pa_rope_store", "pa_rope_store_int8",
            "pa_last_error_string", "pa_read_device_error", "pa_selftest_bounded_wait", "pa_stream_read",
            "pa_version")
 
@@ -84,6 +85,12 @@ class pa_pool(ctypes.Structure):
                 ("scale_layer_stride", ctypes.c_uint64)]
 
 
+class pa_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("max_position", ctypes.c_int32), ("eps", ctypes.c_float), ("pair_axis", ctypes.c_uint8 * 64),
+                ("cos_sin", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
 class PagedAttnError(RuntimeError):
     def __init__(self, code: int, fn: str, msg: str):
         super().__init__(f"{fn} failed with code {code}: {msg}")
@@ -132,6 +139,8 @@ def lib() -> ctypes.CDLL:
             L.pa_pool_fork.argtypes = [P, P, P, P, I32, P, SZ, P]
             L.pa_pool_free.argtypes = [P, P, P, I32, P]
             L.pa_pool_compact.argtypes = [P, P, P, P, P, P, SZ, P]
+            L.pa_rope_store.argtypes = [P] * 5 + [ctypes.c_int64] * 3 + [P, P, I32] + [P] * 4
+            L.pa_rope_store_int8.argtypes = [P] * 5 + [ctypes.c_int64] * 3 + [P, P, I32] + [P] * 6
             L.pa_last_error_string.argtypes = []
             L.pa_last_error_string.restype = ctypes.c_char_p
             L.pa_read_device_error.argtypes = [P, P]
@@ -403,6 +412,94 @@ def pa_store_kvcache(dims: pa_dims, k, v, k_cache, v_cache, slot_mapping, num_to
     n = int(k.shape[0]) if num_tokens is None else int(num_tokens)
     _check(lib().pa_store_kvcache(ctypes.byref(dims), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
                                   _ptr(slot_mapping), n, _stream(stream)), "pa_store_kvcache")
+
+
+class Rope:
+    """Norm and rotation of query and key heads, for pa_rope_store.
+
+    ``cos_sin``: float32 [max_position, R], the cosines of the R/2 pairs, then their sines.  ``pair_axis``: the
+    axis that each pair turns on (None: all on axis 0).  ``q_weight``, ``k_weight``: bf16 [head_dim], or None for
+    no norm.
+    """
+
+    def __init__(self, dims: pa_dims, cos_sin, axes: int = 1, pair_axis=None, interleaved: bool = False,
+                 q_weight=None, k_weight=None, eps: float = 1e-6):
+        if cos_sin.dim() != 2 or cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous():
+            raise ValueError(f"cos_sin must be contiguous float32 [max_position, R], got {cos_sin.dtype} "
+                             f"{tuple(cos_sin.shape)}")
+        pairs = cos_sin.shape[1] // 2
+        axis = [0] * pairs if pair_axis is None else [int(a) for a in pair_axis]
+        if len(axis) != pairs or pairs > 64 or any(a < 0 or a >= axes for a in axis):
+            raise ValueError(f"pair_axis must name an axis below {axes} for each of the {pairs} pairs (at most 64)")
+        self.device = cos_sin.get_device()
+        for what, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is None:
+                continue
+            if w.dtype is not _BF16 or tuple(w.shape) != (dims.head_dim,) or not w.is_contiguous():
+                raise ValueError(f"{what} must be contiguous bfloat16 [{dims.head_dim}], got {w.dtype} {tuple(w.shape)}")
+            if w.get_device() != self.device:
+                raise ValueError(f"{what} is on {w.device}, cos_sin on {cos_sin.device}")
+        self.axes, self.cos_sin, self.q_weight, self.k_weight = int(axes), cos_sin, q_weight, k_weight
+        self.struct = pa_rope(cos_sin.shape[1], 1 if interleaved else 0, self.axes, cos_sin.shape[0], float(eps),
+                              (ctypes.c_uint8 * 64)(*axis), _ptr(cos_sin), _ptr(q_weight), _ptr(k_weight))
+        self.ref = ctypes.byref(self.struct)
+
+
+def _rope_call(dims, rope, q, k, v, positions, slot_mapping, q_out, caches, scales):
+    """The arguments of pa_rope_store(_int8) between `rope` and the caches; refuses what the kernel could not read."""
+    dev, n = _device(), q_out.shape[0]
+    hq, hkv, d = dims.num_heads, dims.num_kv_heads, dims.head_dim
+    cache = _INT8 if scales else _BF16
+    rows = dims.num_blocks * dims.block_size * hkv
+    if not (rope.device == dev and q.dtype is k.dtype is v.dtype is q_out.dtype is _BF16
+            and q.shape == q_out.shape == (n, hq, d) and k.shape == v.shape == (n, hkv, d)
+            and q_out.is_contiguous() and q.stride()[1:] == k.stride()[1:] == v.stride()[1:] == (d, 1)
+            and positions.dtype is slot_mapping.dtype is torch.int32
+            and positions.is_contiguous() and slot_mapping.is_contiguous()
+            and positions.numel() == n * rope.axes and slot_mapping.numel() == n):
+        for what, t, heads in (("q", q, hq), ("k", k, hkv), ("v", v, hkv), ("q_out", q_out, hq)):
+            if t.dtype is not _BF16 or tuple(t.shape) != (n, heads, d):
+                raise ValueError(f"{what} must be bfloat16 [{n}, {heads}, {d}], got {t.dtype} {tuple(t.shape)}")
+            if t.numel() and (t.stride(2) != 1 or heads > 1 and t.stride(1) != d or t is q_out and not t.is_contiguous()):
+                raise ValueError(f"{what}: a token's heads must be contiguous (in q_out the tokens too), got strides "
+                                 f"{t.stride()}")
+        if rope.device != dev:
+            raise ValueError(f"the rope is on cuda:{rope.device}, the current device is cuda:{dev}")
+        _int32(positions, "positions", n * rope.axes, dev)
+        _int32(slot_mapping, "slot_mapping", n, dev)
+    for t in (q, k, v, positions, slot_mapping, q_out, *caches, *scales):
+        if t.get_device() != dev:
+            raise _elsewhere(t, dev)
+    for what, t, dtype, least in (("k_cache", caches[0], cache, rows * d), ("v_cache", caches[1], cache, rows * d),
+                                  *(((("k_scale", scales[0], _FP16, rows), ("v_scale", scales[1], _FP16, rows)))
+                                    if scales else ())):
+        if t.dtype is not dtype or t.numel() < least or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous {dtype} of {least} values, got {t.dtype} {tuple(t.shape)}")
+    row = hkv * d
+    strides = (q.stride(0), k.stride(0), v.stride(0)) if n > 1 else (hq * d, row, row)
+    return (q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, positions.data_ptr(), slot_mapping.data_ptr(), n,
+            q_out.data_ptr(), *(t.data_ptr() for t in caches), *(t.data_ptr() for t in scales))
+
+
+def pa_rope_store(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q_out, k_cache, v_cache, stream=None):
+    """Norm and rotate the queries (into q_out) and the keys, and store keys and values at their slots.
+
+    q [tokens, Hq, D], k, v [tokens, Hkv, D]: bf16, a token's heads contiguous (parts of one projection's output);
+    positions: int32 [tokens], or [axes, tokens].
+    """
+    args = _rope_call(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), ())
+    rc = (_lib or lib()).pa_rope_store(ctypes.byref(dims), rope.ref, *args, _stream_of(rope.device, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_rope_store")
+
+
+def pa_rope_store_int8(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q_out, k_cache, v_cache, k_scale,
+                       v_scale, stream=None):
+    """pa_rope_store into an INT8 cache."""
+    args = _rope_call(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), (k_scale, v_scale))
+    rc = (_lib or lib()).pa_rope_store_int8(ctypes.byref(dims), rope.ref, *args, _stream_of(rope.device, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_rope_store_int8")
 
 
 def pa_prefill_varlen(dims: pa_dims, q, k_cache, v_cache, plan: PrefillPlan, scale: float, out, stream=None):
