@@ -580,6 +580,77 @@ int pa_pool_free(const pa_dims *dims, const pa_pool *pool, const int32_t *rows, 
 int pa_pool_compact(const pa_dims *dims, const pa_pool *pool, int32_t *remap, int32_t *block_tables_out,
                     int32_t *ref_counts_out, void *workspace, size_t workspace_bytes, pa_stream_t stream);
 
+/* ------------------------------------------------------------------ bounded caches */
+
+/*
+ * pa_decode_window — batched single-token GQA decode that sees a window of the
+ * last tokens and a few first ones that stay visible.  Sources: "手搓 vLLM
+ * 推理引擎", Step 4 (decode through block tables); "面试问答准备: nano-vLLM
+ * 推理引擎优化", the Split-K entry (parts merged by log-sum-exp).  Sequence b of
+ * context n sees key j if j < n and (j >= n - window or j < sinks):
+ *   out[b][h] = softmax(scale * q[b][h] . K^T over those keys) V.
+ * No plan: tables and lengths are read on the device (a pa_pool's, for
+ * instance), so a captured call is good for every later step of the same sizes.
+ * Pages that hold no visible key are not looked up: their entries may name
+ * anything, the pages may be others' by now.
+ *   q, out:       device bf16 [num_seqs][num_heads][head_dim]
+ *   context_lens: device int32 [num_rows], each including the token being
+ *                 decoded; 0 gives an output row of zeros
+ *   block_tables: device int32 [num_rows][max_blocks_per_seq]
+ *   table_rows:   device int32 [num_seqs], each sequence's row of the two; NULL: row b
+ *   window:       at least 1 (INT32_MAX: everything);  sinks: at least 0
+ * A block id outside [0, num_blocks) among those of visible keys reads as zeros
+ * (as do the key's score and value), a context longer than its table row is cut
+ * there and a row outside the table is one of context 0; each sets bit 6 of the
+ * device error word.  NaN and infinities as in pa_decode_shared; what the cache
+ * holds at places that are not visible takes no part.  scale must be finite and
+ * > 0.  The launch may be set up during the kernel before it in the stream; it
+ * reads nothing until that has ended.
+ */
+int pa_decode_window(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                     const int32_t *context_lens, const int32_t *block_tables, const int32_t *table_rows,
+                     int32_t num_seqs, int32_t num_rows, int32_t max_blocks_per_seq, int32_t window, int32_t sinks,
+                     float scale, void *out, pa_stream_t stream);
+
+/* pa_decode_window over an INT8 cache: products as pa_decode_int8's. */
+int pa_decode_window_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                          const void *k_scale, const void *v_scale, const int32_t *context_lens,
+                          const int32_t *block_tables, const int32_t *table_rows, int32_t num_seqs, int32_t num_rows,
+                          int32_t max_blocks_per_seq, int32_t window, int32_t sinks, float scale, void *out,
+                          pa_stream_t stream);
+
+/*
+ * pa_decode_weights — a decode over whole contexts that also keeps account of
+ * each key's attention weight, from which pa_pool_evict chooses what stays: with
+ * p[h][j] the softmax weights of the decode, for every key j < n of the row
+ *   scores_out[row][g][j] = decay * scores[row][g][j] + sum over the heads h of KV head g of p[h][j].
+ *   scores, scores_out: device fp32 [num_rows][num_kv_heads][max_blocks_per_seq *
+ *               block_size]; may be one array.  What lies behind a context is
+ *               neither read nor written.  A new token's score must be 0 before its
+ *               first call (pa_pool_evict leaves zeros behind what stays; the scores
+ *               of a row given back to the pool are the caller's to clear)
+ *   decay:      in [0, 1]; 0 takes this step's weights alone (scores are not
+ *               read); layers that share an array decay it once per step
+ *   workspace:  device memory of pa_decode_weights_workspace's bytes, 256-byte
+ *               aligned; no initial contents; calls in flight at once need
+ *               separate ones
+ * Other arguments and rules as pa_decode_window's; a row at most once per call.
+ * The weights are in fp32; a context whose scores are all -inf gives weights of 0.
+ */
+int pa_decode_weights_workspace(const pa_dims *dims, int32_t num_seqs, int32_t max_blocks_per_seq, uint64_t *bytes);
+int pa_decode_weights(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                      const int32_t *context_lens, const int32_t *block_tables, const int32_t *table_rows,
+                      int32_t num_seqs, int32_t num_rows, int32_t max_blocks_per_seq, float scale, float decay,
+                      const float *scores, float *scores_out, void *out, void *workspace, size_t workspace_bytes,
+                      pa_stream_t stream);
+
+/* pa_decode_weights over an INT8 cache. */
+int pa_decode_weights_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                           const void *k_scale, const void *v_scale, const int32_t *context_lens,
+                           const int32_t *block_tables, const int32_t *table_rows, int32_t num_seqs, int32_t num_rows,
+                           int32_t max_blocks_per_seq, float scale, float decay, const float *scores,
+                           float *scores_out, void *out, void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
 /* ------------------------------------------------------------------ INT8 KV cache */
 
 /*
@@ -780,7 +851,8 @@ const char *pa_last_error_string(void);
  * timed out; 2 a block-copy triple was out of range; 3 a bounded wait in the
  * INT8 decode kernel timed out; 4 the wait of pa_selftest_bounded_wait timed
  * out; 5 a bounded wait in the shared-prefix decode timed out; 6 the
- * shared-prefix decode met a block id outside the pool; 7 a pa_pool call was
+ * shared-prefix decode, or one over a bounded cache, met a block id outside the
+ * pool (or a context longer than its table row, or a row outside the table); 7 a pa_pool call was
  * refused for lack of room; 8 a pa_pool call was malformed, or the pool's state; 9 a position of
  * pa_rope_store lies outside its table.  Synchronises `stream`: for tests and debugging, never on the hot path.
  */

@@ -786,6 +786,111 @@ extern "C" int pa_pool_compact(const pa_dims *dims, const pa_pool *pool, int32_t
     return launch_pool_compact(a, remap, block_tables_out, ref_counts_out, stream);
 }
 
+// Host-side checks of the decodes over a bounded cache, then the launch.
+static int decode_bounded(const char *fn, const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                          bool int8, const void *k_scale, const void *v_scale, const int32_t *context_lens,
+                          const int32_t *block_tables, const int32_t *table_rows, int32_t num_seqs, int32_t num_rows,
+                          int32_t max_blocks, int32_t window, int32_t sinks, float scale, void *out, bool weights,
+                          float decay, const float *scores, float *scores_out, void *workspace, size_t workspace_bytes,
+                          pa_stream_t stream)
+{
+    int rc = check_dims(dims);
+    if (rc != PA_OK)
+        return rc;
+    if (!(scale > 0.f) || !std::isfinite(scale))
+        return fail(PA_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (window < 1 || sinks < 0)
+        return fail(PA_ERR_INVALID_ARG, "%s: window must be at least 1, sinks at least 0", fn);
+    if (num_seqs < 0 || num_rows < 1 || max_blocks < 1 || (!table_rows && num_seqs > num_rows))
+        return fail(PA_ERR_INVALID_ARG, "%s: %d sequences, %d rows of %d blocks", fn, num_seqs, num_rows, max_blocks);
+    if ((int64_t)max_blocks * dims->block_size > INT32_MAX - 16)
+        return fail(PA_ERR_UNSUPPORTED, "%s: max_blocks_per_seq * block_size exceeds int32", fn);
+    if ((int64_t)num_seqs * dims->num_kv_heads > INT32_MAX / 8)
+        return fail(PA_ERR_UNSUPPORTED, "%s: num_seqs * num_kv_heads exceeds the grid", fn);
+    if (weights && !(decay >= 0.f && decay <= 1.f))
+        return fail(PA_ERR_INVALID_ARG, "%s: decay must be in [0, 1]", fn);
+    if (num_seqs == 0)
+        return PA_OK;
+    if (!q || !k_cache || !v_cache || !context_lens || !block_tables || !out || (int8 && (!k_scale || !v_scale)) ||
+        (weights && (!scores || !scores_out)))
+        return fail(PA_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (misaligned(q) || misaligned(k_cache) || misaligned(v_cache) || misaligned(k_scale) || misaligned(v_scale) ||
+        misaligned(out) || misaligned(scores) || misaligned(scores_out))
+        return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+    if (dims->num_blocks == 0)
+        return fail(PA_ERR_INVALID_ARG, "empty KV pool");
+    if (weights) {
+        uint64_t need = 0;
+        if ((rc = pa_decode_weights_workspace(dims, num_seqs, max_blocks, &need)) != PA_OK)
+            return rc;
+        if (workspace_bytes < need)
+            return fail(PA_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %llu", fn, workspace_bytes,
+                        (unsigned long long)need);
+        if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+            return fail(PA_ERR_INVALID_ARG, "%s: workspace must be non-NULL and 256-byte aligned", fn);
+    }
+    return launch_decode_window({*dims, q, k_cache, v_cache, k_scale, v_scale, context_lens, block_tables, table_rows,
+                                 num_seqs, num_rows, max_blocks, window, sinks, scale, out,
+                                 weights ? static_cast<float *>(workspace) : nullptr, decay, scores, scores_out},
+                                stream);
+}
+
+extern "C" int pa_decode_window(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *context_lens, const int32_t *block_tables, const int32_t *table_rows,
+                                int32_t num_seqs, int32_t num_rows, int32_t max_blocks_per_seq, int32_t window,
+                                int32_t sinks, float scale, void *out, pa_stream_t stream)
+{
+    return decode_bounded("pa_decode_window", dims, q, k_cache, v_cache, false, nullptr, nullptr, context_lens,
+                          block_tables, table_rows, num_seqs, num_rows, max_blocks_per_seq, window, sinks, scale, out,
+                          false, 0.f, nullptr, nullptr, nullptr, 0, stream);
+}
+
+extern "C" int pa_decode_window_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                                     const void *k_scale, const void *v_scale, const int32_t *context_lens,
+                                     const int32_t *block_tables, const int32_t *table_rows, int32_t num_seqs,
+                                     int32_t num_rows, int32_t max_blocks_per_seq, int32_t window, int32_t sinks,
+                                     float scale, void *out, pa_stream_t stream)
+{
+    return decode_bounded("pa_decode_window_int8", dims, q, k_cache, v_cache, true, k_scale, v_scale, context_lens,
+                          block_tables, table_rows, num_seqs, num_rows, max_blocks_per_seq, window, sinks, scale, out,
+                          false, 0.f, nullptr, nullptr, nullptr, 0, stream);
+}
+
+extern "C" int pa_decode_weights_workspace(const pa_dims *dims, int32_t num_seqs, int32_t max_blocks_per_seq,
+                                           uint64_t *bytes)
+{
+    int rc = check_dims(dims);
+    if (rc != PA_OK)
+        return rc;
+    if (!bytes || num_seqs < 0 || max_blocks_per_seq < 1)
+        return fail(PA_ERR_INVALID_ARG, "pa_decode_weights_workspace: NULL pointer, num_seqs < 0 or no blocks");
+    *bytes = (uint64_t)num_seqs * dims->num_kv_heads * max_blocks_per_seq * dims->block_size * window_raw_heads(*dims) * 4;
+    return PA_OK;
+}
+
+extern "C" int pa_decode_weights(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                                 const int32_t *context_lens, const int32_t *block_tables, const int32_t *table_rows,
+                                 int32_t num_seqs, int32_t num_rows, int32_t max_blocks_per_seq, float scale,
+                                 float decay, const float *scores, float *scores_out, void *out, void *workspace,
+                                 size_t workspace_bytes, pa_stream_t stream)
+{
+    return decode_bounded("pa_decode_weights", dims, q, k_cache, v_cache, false, nullptr, nullptr, context_lens,
+                          block_tables, table_rows, num_seqs, num_rows, max_blocks_per_seq, INT32_MAX, 0, scale, out,
+                          true, decay, scores, scores_out, workspace, workspace_bytes, stream);
+}
+
+extern "C" int pa_decode_weights_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                                      const void *k_scale, const void *v_scale, const int32_t *context_lens,
+                                      const int32_t *block_tables, const int32_t *table_rows, int32_t num_seqs,
+                                      int32_t num_rows, int32_t max_blocks_per_seq, float scale, float decay,
+                                      const float *scores, float *scores_out, void *out, void *workspace,
+                                      size_t workspace_bytes, pa_stream_t stream)
+{
+    return decode_bounded("pa_decode_weights_int8", dims, q, k_cache, v_cache, true, k_scale, v_scale, context_lens,
+                          block_tables, table_rows, num_seqs, num_rows, max_blocks_per_seq, INT32_MAX, 0, scale, out,
+                          true, decay, scores, scores_out, workspace, workspace_bytes, stream);
+}
+
 // pa_decode for callers that cannot allocate: the workspace is the library's
 // own scratch array (see the header for its limit, set-up and sharing rules).
 extern "C" int pa_decode_static(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
@@ -840,6 +945,8 @@ extern "C" int pa_read_device_error(uint32_t *code, pa_stream_t stream)
         rc = read_pool_error(code);
     if (rc == PA_OK)
         rc = read_rope_error(code);
+    if (rc == PA_OK)
+        rc = read_window_error(code);
     return rc;
 }
 

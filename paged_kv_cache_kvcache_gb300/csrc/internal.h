@@ -274,6 +274,32 @@ struct RopeArgs {
 };
 int launch_rope_store(const RopeArgs &a, void *stream);
 
+// Decode over a bounded cache, from tables and lengths on the device (decode_window.cu).
+struct WindowArgs {
+    pa_dims dims;
+    const void *q, *k_cache, *v_cache;
+    const void *k_scale, *v_scale; // INT8 cache only
+    const int32_t *context_lens, *block_tables, *table_rows;
+    int32_t num_seqs, num_rows, max_blocks_per_seq;
+    int32_t window, sinks;
+    float scale;
+    void *out;
+    // pa_decode_weights (else NULL)
+    float *raw;
+    float decay;
+    const float *scores;
+    float *scores_out;
+};
+int launch_decode_window(const WindowArgs &a, void *stream);
+// Scores per key and KV head that pa_decode_weights keeps in its workspace: the group, rounded up to a power of two.
+inline int window_raw_heads(const pa_dims &d)
+{
+    int n = 1;
+    while (n < d.num_heads / d.num_kv_heads)
+        n *= 2;
+    return n;
+}
+
 // Device address of the library-owned decode scratch on the current device
 // (looked up once per device).  Used only by pa_decode_static.
 int decode_static_scratch(void **ptr);
@@ -296,6 +322,7 @@ int read_fused8_error(uint32_t *code);
 int read_shared_error(uint32_t *code); // bit 0 -> 5 (wait), bit 1 -> 6 (block id outside the pool)
 int read_pool_error(uint32_t *code);   // bit 0 -> 7 (no room), bit 1 -> 8 (malformed)
 int read_rope_error(uint32_t *code);   // bit 0 (slot), bit 1 -> 9 (position)
+int read_window_error(uint32_t *code); // bit 0 -> 6 (block id outside the pool)
 int launch_selftest_wait(uint32_t timeout_us, int arrive_first, void *stream);
 int read_selftest_error(uint32_t *code);
 int launch_stream_read(const void *src, size_t bytes, uint32_t *sink, void *stream);

@@ -26,7 +26,8 @@ EXPORTS = ("pa_pack_prefill", "pa_pack_decode", "pa_upload", "pa_store_kvcache",
            "pa_decode_int8_fused", "pa_prefill_varlen_fused", "pa_prefill_varlen_int8_fused",
            "pa_pack_decode_shared", "pa_decode_shared", "pa_decode_shared_int8", "pa_pool_workspace", "pa_pool_append",
            "pa_pool_fork", "pa_pool_free", "pa_pool_compact",
-           "pa_rope_store", "pa_rope_store_int8",
+           "pa_rope_store", "pa_rope_store_int8", "pa_decode_window", "pa_decode_window_int8", "pa_decode_weights",
+           "pa_decode_weights_int8", "pa_decode_weights_workspace",
            "pa_last_error_string", "pa_read_device_error", "pa_selftest_bounded_wait", "pa_stream_read",
            "pa_version")
 
@@ -141,6 +142,11 @@ def lib() -> ctypes.CDLL:
             L.pa_pool_compact.argtypes = [P, P, P, P, P, P, SZ, P]
             L.pa_rope_store.argtypes = [P] * 5 + [ctypes.c_int64] * 3 + [P, P, I32] + [P] * 4
             L.pa_rope_store_int8.argtypes = [P] * 5 + [ctypes.c_int64] * 3 + [P, P, I32] + [P] * 6
+            L.pa_decode_window.argtypes = [P] * 7 + [I32] * 5 + [ctypes.c_float, P, P]
+            L.pa_decode_window_int8.argtypes = [P] * 9 + [I32] * 5 + [ctypes.c_float, P, P]
+            L.pa_decode_weights.argtypes = [P] * 7 + [I32] * 3 + [ctypes.c_float] * 2 + [P] * 4 + [SZ, P]
+            L.pa_decode_weights_int8.argtypes = [P] * 9 + [I32] * 3 + [ctypes.c_float] * 2 + [P] * 4 + [SZ, P]
+            L.pa_decode_weights_workspace.argtypes = [P, I32, I32, P]
             L.pa_last_error_string.argtypes = []
             L.pa_last_error_string.restype = ctypes.c_char_p
             L.pa_read_device_error.argtypes = [P, P]
@@ -756,6 +762,114 @@ def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None,
     rc = (_lib or lib()).pa_pool_compact(pool.dims_ref, pool.ref, *args, *pool.ws, _stream_of(pool.device, stream))
     if rc != PA_OK:
         _check(rc, "pa_pool_compact")
+
+
+def _bounded_call(dims, q, caches, scales, block_tables, context_lens, table_rows, out):
+    """The arguments of a decode over a bounded cache from q to max_blocks_per_seq; refuses what a kernel could not read."""
+    dev, n = _device(), q.shape[0]
+    hq, hkv, d = dims.num_heads, dims.num_kv_heads, dims.head_dim
+    rows, width = block_tables.shape
+    cache = _INT8 if scales else _BF16
+    page = dims.num_blocks * dims.block_size * hkv
+    k, v = caches
+    if not (dev == q.get_device() == out.get_device() == k.get_device() == v.get_device() == block_tables.get_device()
+            == context_lens.get_device()
+            and q.dtype is out.dtype is _BF16 and k.dtype is v.dtype is cache
+            and q.shape == out.shape == (n, hq, d)
+            and block_tables.dtype is context_lens.dtype is torch.int32 and context_lens.shape == (rows,)
+            and q.is_contiguous() and out.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous()
+            and k.numel() >= page * d <= v.numel() and (table_rows is not None or n <= rows)):
+        for what, t in (("q", q), ("out", out)):
+            if tuple(t.shape) != (n, hq, d):
+                raise ValueError(f"{what} must be [{n}, {hq}, {d}], got {tuple(t.shape)}")
+        _int32(block_tables, "block_tables", None, dev)
+        _int32(context_lens, "context_lens", rows, dev)
+        _refuse(dev, (q, out, k, v), (("q", q, _BF16, 0), ("out", out, _BF16, 0), ("k_cache", k, cache, page * d),
+                                      ("v_cache", v, cache, page * d)))
+        raise ValueError(f"{n} sequences, {rows} rows of the block table")
+    if table_rows is not None:
+        _int32(table_rows, "table_rows", n, dev)
+    for what, t in zip(("k_scale", "v_scale"), scales):
+        if t.dtype is not _FP16 or t.numel() < page or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{what} must be contiguous {_FP16} of {page} values on cuda:{dev}, got {t.dtype} "
+                             f"{tuple(t.shape)} on {t.device}")
+    return (q.data_ptr(), k.data_ptr(), v.data_ptr(), *[t.data_ptr() for t in scales], context_lens.data_ptr(),
+            block_tables.data_ptr(), None if table_rows is None else table_rows.data_ptr(), n, rows, width)
+
+
+def pa_decode_window(dims: pa_dims, q, k_cache, v_cache, block_tables, context_lens, window: int, sinks: int,
+                     scale: float, out, table_rows=None, stream=None):
+    """Decode that sees the last ``window`` keys and the first ``sinks`` ones, from tables and lengths on the device.
+
+    block_tables int32 [rows, width] and context_lens int32 [rows] (a PagePool's, for instance); sequence b is row
+    ``table_rows[b]`` of them, or row b.
+    """
+    args = _bounded_call(dims, q, (k_cache, v_cache), (), block_tables, context_lens, table_rows, out)
+    rc = (_lib or lib()).pa_decode_window(ctypes.byref(dims), *args, window, sinks, scale, out.data_ptr(),
+                                          _stream_of(q.get_device(), stream))
+    if rc != PA_OK:
+        _check(rc, "pa_decode_window")
+
+
+def pa_decode_window_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, window: int,
+                          sinks: int, scale: float, out, table_rows=None, stream=None):
+    """pa_decode_window over an INT8 cache."""
+    args = _bounded_call(dims, q, (k_cache, v_cache), (k_scale, v_scale), block_tables, context_lens, table_rows, out)
+    rc = (_lib or lib()).pa_decode_window_int8(ctypes.byref(dims), *args, window, sinks, scale, out.data_ptr(),
+                                               _stream_of(q.get_device(), stream))
+    if rc != PA_OK:
+        _check(rc, "pa_decode_window_int8")
+
+
+def weights_workspace(dims: pa_dims, num_seqs: int, max_blocks: int, device="cuda") -> torch.Tensor:
+    """Workspace of pa_decode_weights(_int8) for so many sequences and a block table of that width."""
+    n = ctypes.c_uint64(0)
+    _check(lib().pa_decode_weights_workspace(ctypes.byref(dims), num_seqs, max_blocks, ctypes.byref(n)),
+           "pa_decode_weights_workspace")
+    return torch.empty(max(n.value, 256), dtype=torch.uint8, device=device)
+
+
+def _score_args(dims, block_tables, scores, scores_out, workspace):
+    """(scores, scores_out, workspace, its bytes) of a call on these tables."""
+    scores_out = scores if scores_out is None else scores_out
+    shape = (block_tables.shape[0], dims.num_kv_heads, block_tables.shape[1] * dims.block_size)
+    dev = block_tables.get_device()
+    for what, t in (("scores", scores), ("scores_out", scores_out)):
+        if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{what} must be contiguous float32 {shape} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
+                             f"on {t.device}")
+    if workspace is None:
+        return scores.data_ptr(), scores_out.data_ptr()
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous, on cuda:{dev}")
+    return scores.data_ptr(), scores_out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def pa_decode_weights(dims: pa_dims, q, k_cache, v_cache, block_tables, context_lens, scale: float, out, scores, workspace,
+                      decay: float = 1.0, scores_out=None, table_rows=None, stream=None):
+    """Decode over whole contexts that adds each key's attention weight to its score.
+
+    scores: float32 [rows, Hkv, width * block_size]; scores_out = decay * scores + the weights, summed over each KV
+    head's query heads (None: in place).
+    """
+    args = _bounded_call(dims, q, (k_cache, v_cache), (), block_tables, context_lens, table_rows, out)
+    s, so, ws, n = _score_args(dims, block_tables, scores, scores_out, workspace)
+    rc = (_lib or lib()).pa_decode_weights(ctypes.byref(dims), *args, scale, decay, s, so, out.data_ptr(), ws, n,
+                                           _stream_of(q.get_device(), stream))
+    if rc != PA_OK:
+        _check(rc, "pa_decode_weights")
+
+
+def pa_decode_weights_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale: float,
+                           out, scores, workspace, decay: float = 1.0, scores_out=None, table_rows=None, stream=None):
+    """pa_decode_weights over an INT8 cache."""
+    args = _bounded_call(dims, q, (k_cache, v_cache), (k_scale, v_scale), block_tables, context_lens, table_rows, out)
+    s, so, ws, n = _score_args(dims, block_tables, scores, scores_out, workspace)
+    rc = (_lib or lib()).pa_decode_weights_int8(ctypes.byref(dims), *args, scale, decay, s, so, out.data_ptr(), ws, n,
+                                                _stream_of(q.get_device(), stream))
+    if rc != PA_OK:
+        _check(rc, "pa_decode_weights_int8")
 
 
 def int8_cache(dims: pa_dims, device="cuda"):
