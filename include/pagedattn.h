@@ -583,6 +583,32 @@ int pa_pool_compact(const pa_dims *dims, const pa_pool *pool, int32_t *remap, in
 /* ------------------------------------------------------------------ bounded caches */
 
 /*
+ * pa_prefill_window — pa_prefill_varlen in which a query sees a window of the
+ * last keys up to its own and a few first ones that stay visible: the query at
+ * position p sees key j <= p if p - j < window or j < sinks.  The plan is
+ * pa_prefill_varlen's, so layers with and without a window share one.
+ *   window: at least 1;  sinks: at least 0
+ * Key tiles that no query of a work item sees are neither loaded nor multiplied;
+ * table entries of blocks that no query of the call sees are not looked up (the
+ * plan's block lists must name some block of the pool there), and what the cache
+ * holds at such places takes no part.  A key that some queries see and others do
+ * not must be finite.  Other arguments, errors and numerics as pa_prefill_varlen.
+ */
+int pa_prefill_window(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                      const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, const int32_t *block_tables,
+                      int32_t window, int32_t sinks, float scale, void *out, const pa_prefill_meta *meta,
+                      const int32_t *tiles, pa_stream_t stream);
+
+/* pa_prefill_window over an INT8 cache, as pa_prefill_varlen_int8: two launches, the workspace and
+ * scratch arrays of the same plan; keys that no query sees are not dequantised. */
+int pa_prefill_window_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                           const void *k_scale, const void *v_scale, const int32_t *cu_seqlens_q,
+                           const int32_t *cu_seqlens_k, const int32_t *block_tables, const int32_t *scratch_tables,
+                           const int32_t *scratch_items, int32_t window, int32_t sinks, float scale, void *out,
+                           const pa_prefill_meta *meta, const int32_t *tiles, void *workspace, size_t workspace_bytes,
+                           pa_stream_t stream);
+
+/*
  * pa_decode_window — batched single-token GQA decode that sees a window of the
  * last tokens and a few first ones that stay visible.  Sources: "手搓 vLLM
  * 推理引擎", Step 4 (decode through block tables); "面试问答准备: nano-vLLM

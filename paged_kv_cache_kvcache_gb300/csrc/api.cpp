@@ -248,7 +248,7 @@ static int prefill_int8(const char *fn, bool store, const pa_dims *dims, const v
                         const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, const int32_t *block_tables,
                         const int32_t *slot_mapping, const int32_t *scratch_tables, const int32_t *scratch_items,
                         float scale, void *out, const pa_prefill_meta *meta, const int32_t *tiles, void *workspace,
-                        size_t workspace_bytes, pa_stream_t stream)
+                        size_t workspace_bytes, pa_stream_t stream, int32_t window = 0, int32_t sinks = 0)
 {
     PrefillArgs a;
     bool nothing = false;
@@ -299,8 +299,12 @@ static int prefill_int8(const char *fn, bool store, const pa_dims *dims, const v
         g.k_scale_w = static_cast<uint16_t *>(const_cast<void *>(k_scale));
         g.v_scale_w = static_cast<uint16_t *>(const_cast<void *>(v_scale));
     }
+    g.window = window;
+    g.sinks = sinks;
     if ((rc = launch_int8_gather(g, stream)) != PA_OK)
         return rc;
+    a.window = window;
+    a.sinks = sinks;
     a.dims.num_blocks = meta->scratch_blocks;
     a.dims.block_size = kPrefillKeyTile;
     a.k_cache = g.k_out;
@@ -334,6 +338,50 @@ extern "C" int pa_prefill_varlen_int8_fused(const pa_dims *dims, const void *q, 
     return prefill_int8("pa_prefill_varlen_int8_fused", true, dims, q, k, v, k_cache, v_cache, k_scale, v_scale,
                         cu_seqlens_q, cu_seqlens_k, block_tables, slot_mapping, scratch_tables, scratch_items, scale,
                         out, meta, tiles, workspace, workspace_bytes, stream);
+}
+
+// The window of a windowed prefill, cut to the batch's longest sequence (no further key is there to be seen).
+static int check_window(const char *fn, const pa_prefill_meta *meta, int32_t *window, int32_t *sinks)
+{
+    if (*window < 1 || *sinks < 0)
+        return fail(PA_ERR_INVALID_ARG, "%s: window must be at least 1, sinks at least 0", fn);
+    const int32_t longest = meta && meta->max_seqlen_k > 0 ? meta->max_seqlen_k : 1;
+    *window = *window < longest ? *window : longest;
+    *sinks = *sinks < longest ? *sinks : longest;
+    return PA_OK;
+}
+
+extern "C" int pa_prefill_window(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                 const int32_t *block_tables, int32_t window, int32_t sinks, float scale, void *out,
+                                 const pa_prefill_meta *meta, const int32_t *tiles, pa_stream_t stream)
+{
+    PrefillArgs a;
+    bool nothing = false;
+    int rc = check_window("pa_prefill_window", meta, &window, &sinks);
+    if (rc == PA_OK)
+        rc = prepare_prefill("pa_prefill_window", dims, q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables,
+                             scale, out, meta, tiles, &a, &nothing);
+    if (rc != PA_OK || nothing)
+        return rc;
+    a.window = window;
+    a.sinks = sinks;
+    return launch_prefill(a, stream);
+}
+
+extern "C" int pa_prefill_window_int8(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
+                                      const void *k_scale, const void *v_scale, const int32_t *cu_seqlens_q,
+                                      const int32_t *cu_seqlens_k, const int32_t *block_tables,
+                                      const int32_t *scratch_tables, const int32_t *scratch_items, int32_t window,
+                                      int32_t sinks, float scale, void *out, const pa_prefill_meta *meta,
+                                      const int32_t *tiles, void *workspace, size_t workspace_bytes,
+                                      pa_stream_t stream)
+{
+    if (int rc = check_window("pa_prefill_window_int8", meta, &window, &sinks))
+        return rc;
+    return prefill_int8("pa_prefill_window_int8", false, dims, q, nullptr, nullptr, k_cache, v_cache, k_scale, v_scale,
+                        cu_seqlens_q, cu_seqlens_k, block_tables, nullptr, scratch_tables, scratch_items, scale, out,
+                        meta, tiles, workspace, workspace_bytes, stream, window, sinks);
 }
 
 // Host-side checks shared by pa_decode and pa_decode_int8; fills `a`.  Sets

@@ -122,6 +122,8 @@ struct GatherArgs {
     const int32_t *slot_mapping;
     int8_t *k_codes_w, *v_codes_w;
     uint16_t *k_scale_w, *v_scale_w;
+    // pa_prefill_window_int8 (else 0): keys that no query sees are left out
+    int32_t window, sinks;
 };
 int launch_int8_gather(const GatherArgs &a, void *stream);
 
@@ -154,6 +156,8 @@ struct PrefillArgs {
     // the cache is the INT8 prefill's scratch (block tables: the plan's scratch tables,
     // so the work entries' block of key 0 does not apply)
     bool scratch_cache;
+    // pa_prefill_window (else 0): a query sees the last `window` keys up to its own and the first `sinks`
+    int32_t window, sinks;
 };
 int launch_prefill(const PrefillArgs &a, void *stream);
 

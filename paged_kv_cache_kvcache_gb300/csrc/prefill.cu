@@ -147,6 +147,8 @@ struct PfParams {
     const int32_t *slot_mapping;
     const uint4 *k_in;
     const uint4 *v_in;
+    // windowed kernels: a query sees the last `window` keys up to its own and the first `sinks`
+    int32_t window, sinks;
 };
 
 // barrier slots (uint64 each) inside the barrier area
@@ -182,23 +184,38 @@ struct Item {
     int nkt0, nkt1, nkt;    // key tiles of each query tile; nkt = max
     bool tail;              // the last key tile runs past the sequence end
     int blk0;               // physical block holding key 0 (read by the short-batch kernel only)
+    // windowed kernels: the item's key tiles are the first `first` ones of the sequence, which hold the first
+    // `sink` keys that its queries see before the window, and then those from tile first + skip on; its
+    // first query's window begins at key lo.  (nkt0, nkt1 and nkt count these tiles, `real` gives their place.)
+    int first, skip, sink, lo;
+    template <bool kWin>
+    __device__ int real(int j) const { return kWin && j >= first ? j + skip : j; }
+    // key tile j holds keys that no query of the item sees: their V rows are zeroed
+    __device__ bool ragged(int j) const
+    {
+        return (j == first - 1 && (sink & 127) != 0) || (j == first && (lo & 127) != 0);
+    }
 };
 
 // The items of this CTA: rounds of gridDim.x consecutive entries of the list
 // (sorted longest first), odd rounds walked backwards so that the CTAs' totals
 // stay even.  The next item's entry is fetched while the current one runs
 // (from its start, or where the caller asks, to keep it out of a register-heavy loop).
+template <bool kWin>
 struct ItemIter {
     const int4 *tiles;
     int n, P, ord, idx;
     int4 a0, a1;
+    int window, sinks;
     __device__ static int index(int ord)
     {
         const int c = (int)gridDim.x;
         return ord * c + ((ord & 1) ? c - 1 - (int)blockIdx.x : (int)blockIdx.x);
     }
-    __device__ ItemIter(const int4 *t, int n_, int P_) : tiles(t), n(n_), P(P_), ord(0), idx(index(0))
+    __device__ ItemIter(const PfParams &p, int P_) : tiles(p.tiles), n(p.num_items), P(P_), ord(0), idx(index(0))
     {
+        if constexpr (kWin)
+            window = p.window, sinks = p.sinks;
         if (idx < n) {
             a0 = __ldg(tiles + 2 * idx);
             a1 = __ldg(tiles + 2 * idx + 1);
@@ -218,6 +235,15 @@ struct ItemIter {
         w.nkt1 = w.npos1 > 0 ? (off + w.q0 + P + w.npos1 + 127) >> 7 : 0;
         w.nkt = max(w.nkt0, w.nkt1);
         w.tail = w.nkt * 128 > w.lk;
+        if constexpr (kWin) {
+            w.lo = max(0, off + w.q0 + 1 - window);
+            w.sink = min(sinks, w.lo);
+            w.first = min((w.sink + 127) >> 7, w.lo >> 7);
+            w.skip = (w.lo >> 7) - w.first;
+            w.nkt0 -= w.skip;
+            w.nkt1 -= w.npos1 > 0 ? w.skip : 0;
+            w.nkt -= w.skip;
+        }
         return w;
     }
     // the current item; advances to the next and (unless told not to) starts fetching its entry
@@ -467,7 +493,9 @@ __device__ __forceinline__ void prefetch_query_tiles(const CUtensorMap *tm_q, co
 // over the INT8 prefill's scratch cache, whose blocks the entries do not name).  The large
 // batches keep the other instantiation, whose register allocation those additions
 // would disturb (measured 1.5-2 % slower there).
-template <int D, bool kShort>
+// kWin: queries see a window of the last keys and a few first ones (pa_prefill_window; never with the store
+// fused): an item's key tiles are two runs of the sequence's, masked at both ends.
+template <int D, bool kShort, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kin,
@@ -494,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp >= 8 && lane == 0) {
             if (warp == kLoaderWarp) {
                 ptx::prefetch_tmap(&tm_q);
-                ptx::prefetch_l1(p.tiles + 2 * ItemIter::index(0));
+                ptx::prefetch_l1(p.tiles + 2 * ItemIter<kWin>::index(0));
             } else if (warp == kKProducerWarp) {
                 ptx::prefetch_tmap(&tm_k);
                 if (p.fused)
@@ -553,15 +581,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int key = j * 128 + lane * box_rows;
             if (lane >= nsub || key >= w.lk)
                 return p.num_slots; // fully out of range: TMA fills zeros
+            if constexpr (kWin) { // a box that no query of the item sees is not looked up
+                if (key >= w.sink && key + box_rows <= w.lo)
+                    return p.num_slots;
+            }
             const int off = w.lk - w.lq; // cached prefix
-            if (p.fused && key >= off)
+            if (!kWin && p.fused && key >= off)
                 return -(w.cq0 + key - off + 1);
             const int phys = kShort && key < bs ? w.blk0 : __ldg(bt + key / bs);
             return phys * bs + (key & (bs - 1));
         };
         if (warp == kLoaderWarp) {
             // ------------------------------------------------------------ bf16: Q producer
-            ItemIter items(p.tiles, p.num_items, P);
+            ItemIter<kWin> items(p, P);
             zero_query_padding<D>(sgen, G * P, lane);
             if (!kShort && lane == 0)
                 ptx::prefetch_tmap(&tm_q);
@@ -582,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 early = 0;
                 if (ok && lane == 0 && items.more())
                     prefetch_query_tiles<D>(&tm_q, items.peek(), G, P);
-                if (ok && p.fused) {
+                if (!kWin && ok && p.fused) {
                     if (items.more()) {
                         // this item's rows, pass by pass; a query buffer that frees meanwhile is
                         // refilled with the next item's tile at once
@@ -607,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kKProducerWarp || warp == kVProducerWarp) {
             // ------------------------------------------------------------ bf16: K and V producers
-            ItemIter items(p.tiles, p.num_items, P);
+            ItemIter<kWin> items(p, P);
             const bool is_k = warp == kKProducerWarp;
             const int nstages = is_k ? L::kKStages : L::kVStages;
             const uint32_t ring = sbase + (is_k ? L::kK : L::kV);
@@ -623,13 +655,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             while (ok && items.more()) {
                 const Item w = items.next();
-                const int jfix = straddle_tile(w, p.fused, box_rows);
+                const int jfix = kWin ? -1 : straddle_tile(w, p.fused, box_rows);
                 const int32_t *bt = p.block_tables + (size_t)w.b * p.max_blocks;
-                int next = sub_row(w, bt, 0);
+                int next = sub_row(w, bt, w.template real<kWin>(0));
                 for (int j = 0; j < w.nkt; ++j, ++X) {
                     const int cur = next;
                     if (j + 1 < w.nkt)
-                        next = sub_row(w, bt, j + 1);
+                        next = sub_row(w, bt, w.template real<kWin>(j + 1));
                     starts = (starts << 1) | (j == 0 ? 1u : 0u);
                     const int st = X % nstages;
                     // slot reuse: free once the tile nstages back is released
@@ -652,7 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                     const bool fix = j == jfix, zero = !is_k && w.tail && j == w.nkt - 1;
-                    if (fix || zero) {
+                    const bool ragged = kWin && !is_k && w.ragged(j);
+                    if (fix || zero || ragged) {
                         if (!(ok = wwait(full, (X / nstages) & 1)))
                             break;
                         uint8_t *tile = sgen + (is_k ? L::kK : L::kV) + st * L::kTileBytes;
@@ -661,11 +694,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (zero) {
                             // V rows of keys past the sequence end may hold anything (even NaN
                             // bit patterns); zero them so that P = 0 cannot turn them into NaN in O.
-                            const int first = w.lk - j * 128;
+                            const int first = w.lk - w.template real<kWin>(j) * 128;
                             const int chunks = (128 - first) * 8;
                             for (int pp = 0; pp < L::kPanels; ++pp)
                                 for (int c = lane; c < chunks; c += 32)
                                     *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + (first + (c >> 3)) * 128 +
+                                                               (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        if constexpr (kWin) { // likewise those of keys between the first ones and the window
+                            const int key0 = w.template real<kWin>(j) * 128;
+                            const int from = max(w.sink - key0, 0);
+                            const int chunks = ragged ? (min(w.lo - key0, 128) - from) * 8 : 0;
+                            for (int pp = 0; pp < L::kPanels; ++pp)
+                                for (int c = lane; c < chunks; c += 32)
+                                    *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + (from + (c >> 3)) * 128 +
                                                                (c & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
                         ptx::fence_proxy_async_smem();
@@ -685,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ------------------------------------------------------------ MMA issuer (the whole warp,
             // one elected lane issuing each MMA and commit)
 
-            ItemIter items(p.tiles, p.num_items, P);
+            ItemIter<kWin> items(p, P);
             constexpr uint32_t idesc_s = ptx::idesc_bf16(128, 128, 0);
             constexpr uint32_t idesc_o = ptx::idesc_bf16(128, D, 1);
             // Shared-memory descriptors: a constant upper word and a lower word of base
@@ -724,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (ok && items.more()) {
                 const Item w = items.next();
                 const uint32_t qpar = w.ord & 1;
-                const int jfix = straddle_tile(w, p.fused, box_rows);
+                const int jfix = kWin ? -1 : straddle_tile(w, p.fused, box_rows);
                 ok = wwait(bars.q_full(0), qpar) && wwait(bars.k_full(ks), kph);
                 if (ok && jfix == 0) { // key tile 0's straddling box patched
                     ok = wwait(bars.k_fix(ks), (fixpar >> ks) & 1u);
@@ -763,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!v_ready) {
                             if (!(ok = wwait(bars.v_full(vs), vph)))
                                 return;
-                            if ((w.tail && j == w.nkt - 1) || j == jfix) {
+                            if ((w.tail && j == w.nkt - 1) || j == jfix || (kWin && w.ragged(j))) {
                                 if (!(ok = wwait(bars.v_tail(vs), (tailpar >> vs) & 1u)))
                                     return;
                                 tailpar ^= 1u << vs;
@@ -814,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax + epilogue
-        ItemIter items(p.tiles, p.num_items, P);
+        ItemIter<kWin> items(p, P);
         ptx::reg_alloc<kSoftmaxRegs>();
         const int t = warp >> 2;                   // query tile of this warpgroup (warps 0-3, 4-7)
         const int quarter = warp & 3;              // TMEM lanes 32*quarter .. +31
@@ -830,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // fused store, one item per CTA: the eight softmax warps copy its new K/V rows
             // while they wait for its first scores (one pass of 8 K and 8 V vectors per
             // thread covers 64 KB of rows), if it has at least 128 positions
-            if (p.fused && items.more() && wide_copy<D>(items.peek()))
+            if (!kWin && p.fused && items.more() && wide_copy<D>(items.peek()))
                 store_item_rows_wide<D>(p, items.peek(), (int)threadIdx.x);
         }
 
@@ -842,26 +884,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             // keys visible to this row; rows that hold no query are never masked (their
             // output is discarded) so that a warp's rows all take the same path
             const int limit = row_valid ? w.lk - w.lq + w.q0 + t * P + rpos + 1 : 0x3fffffff;
+            const int width = kWin && row_valid ? p.window : 0x7fffffff; // windowed
             float m_ref = -INFINITY, l_sum = 0.f;
             for (int j = 0; j < ntile; ++j) {
                 if (!(ok = wwait(bars.s_full(t), ns & 1)))
                     break;
                 ns ^= 1;
                 ptx::tc_fence_after();
-                const int lim = limit - j * 128; // columns this row sees in this tile
+                const int lim = limit - w.template real<kWin>(j) * 128; // columns this row sees in this tile
+                // windowed: of those, the ones from `from` on and those before `sink`
+                const int from = kWin ? lim - width : 0, sink = kWin ? p.sinks - w.template real<kWin>(j) * 128 : 0;
                 // the whole score row in registers: one TMEM round trip per tile.  Tiles no row
                 // of the warp sees only in part take the row max from the loads themselves
                 // (tcgen05.ld.red); tiles crossing the causal diagonal mask first, then reduce.
                 uint32_t sr[128];
                 float mx;
-                if (__any_sync(0xffffffffu, lim < 128)) {
+                if (__any_sync(0xffffffffu, lim < 128 || (kWin && min(from, 128) > max(sink, 0)))) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         ptx::tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
                     ptx::tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
-                        sr[c] = c < lim ? sr[c] : __float_as_uint(-INFINITY);
+                        sr[c] = c < lim && (!kWin || c >= from || c < sink) ? sr[c] : __float_as_uint(-INFINITY);
                     float m8[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -997,11 +1042,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int D, bool kShort>
+template <int D, bool kShort, bool kWin = false>
 int launch(const PrefillArgs &a, cudaStream_t stream, int sms)
 {
     using L = PfLayout<D>;
-    if (int rc = ensure_smem<prefill_kernel<D, kShort>>(L::kSmemBytes, "prefill"))
+    if (int rc = ensure_smem<prefill_kernel<D, kShort, kWin>>(L::kSmemBytes, "prefill"))
         return rc;
     // The register hand-over inside the kernel assumes kLaunchRegs per thread at
     // launch; with fewer the softmax warpgroups' request could never be granted.
@@ -1009,7 +1054,7 @@ int launch(const PrefillArgs &a, cudaStream_t stream, int sms)
     int nreg = launch_regs.load(std::memory_order_acquire);
     if (nreg == 0) {
         cudaFuncAttributes fa{};
-        const cudaError_t e = cudaFuncGetAttributes(&fa, prefill_kernel<D, kShort>);
+        const cudaError_t e = cudaFuncGetAttributes(&fa, prefill_kernel<D, kShort, kWin>);
         if (e != cudaSuccess)
             return fail(PA_ERR_CUDA, "prefill kernel attributes: %s", cudaGetErrorString(e));
         launch_regs.store(nreg = fa.numRegs, std::memory_order_release);
@@ -1070,9 +1115,11 @@ int launch(const PrefillArgs &a, cudaStream_t stream, int sms)
     p.v_in = static_cast<const uint4 *>(a.v_in);
     p.k_cache = static_cast<uint4 *>(const_cast<void *>(a.k_cache));
     p.v_cache = static_cast<uint4 *>(const_cast<void *>(a.v_cache));
+    p.window = a.window;
+    p.sinks = a.sinks;
     // persistent: one CTA per SM (shared memory and TMEM admit one), each walking its items
     const int grid = a.num_tiles < sms ? a.num_tiles : sms;
-    prefill_kernel<D, kShort><<<(unsigned)grid, kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, tkin, tvin, p);
+    prefill_kernel<D, kShort, kWin><<<(unsigned)grid, kThreads, L::kSmemBytes, stream>>>(tq, tk, tv, tkin, tvin, p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -1089,6 +1136,11 @@ int launch_prefill(const PrefillArgs &a, void *stream)
     int sms = 0;
     if (int rc = sm_count(&sms))
         return rc;
+    if (a.window > 0) {
+        if (a.num_tiles <= sms && !a.scratch_cache)
+            return a.dims.head_dim == 128 ? launch<128, true, true>(a, s, sms) : launch<64, true, true>(a, s, sms);
+        return a.dims.head_dim == 128 ? launch<128, false, true>(a, s, sms) : launch<64, false, true>(a, s, sms);
+    }
     if (a.num_tiles <= sms && !a.scratch_cache) // at most one work item per CTA
         return a.dims.head_dim == 128 ? launch<128, true>(a, s, sms) : launch<64, true>(a, s, sms);
     return a.dims.head_dim == 128 ? launch<128, false>(a, s, sms) : launch<64, false>(a, s, sms);

@@ -126,7 +126,9 @@ int launch_store_kvcache_int8(const pa_dims &d, const void *k, const void *v, vo
 // adjacent threads (32 values each): unit u is row u / (2 Hkv), then K heads, then
 // V heads, so a warp reads and writes whole rows of K and of V (coalesced).  One
 // unit per thread group; HBM-bound: 3 bytes moved per value (1 read, 2 written).
-template <int D, bool kStore>
+// kWin (pa_prefill_window_int8): keys before the window of a sequence's first query, but for the first `sinks`
+// ones, are seen by none; their rows are left as they are and their blocks not looked up.
+template <int D, bool kStore, bool kWin>
 __global__ void __launch_bounds__(256) int8_gather_kernel(const GatherArgs a)
 {
     constexpr int TPR = quant::kThreadsPerRow<D>;
@@ -144,6 +146,8 @@ __global__ void __launch_bounds__(256) int8_gather_kernel(const GatherArgs a)
     const int b = e.x, pos = e.y + (int)(r & 127), lk = e.z, cached = e.w;
     if (pos >= lk)
         return; // past the sequence end: the attention never reads this row's values
+    if (kWin && pos >= a.sinks && pos <= cached - a.window)
+        return;
     uint32_t code[8];
     float sc;
     if (kStore && pos >= cached) {
@@ -198,8 +202,10 @@ int launch_int8_gather(const GatherArgs &a, void *stream)
         return fail(PA_ERR_UNSUPPORTED, "INT8 prefill scratch of %lld (row, tensor, head) units exceeds int32",
                     (long long)(n / (a.head_dim / 32)));
     const bool st = a.k_in != nullptr;
-    auto kern = a.head_dim == 128 ? (st ? int8_gather_kernel<128, true> : int8_gather_kernel<128, false>)
-                                  : (st ? int8_gather_kernel<64, true> : int8_gather_kernel<64, false>);
+    auto kern = a.head_dim == 128 ? (st ? int8_gather_kernel<128, true, false> : int8_gather_kernel<128, false, false>)
+                                  : (st ? int8_gather_kernel<64, true, false> : int8_gather_kernel<64, false, false>);
+    if (a.window > 0) // (never with the store)
+        kern = a.head_dim == 128 ? int8_gather_kernel<128, false, true> : int8_gather_kernel<64, false, true>;
     kern<<<(unsigned)((n + threads - 1) / threads), threads, 0, (cudaStream_t)stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)

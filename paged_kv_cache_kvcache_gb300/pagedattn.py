@@ -27,7 +27,7 @@ EXPORTS = ("pa_pack_prefill", "pa_pack_decode", "pa_upload", "pa_store_kvcache",
            "pa_pack_decode_shared", "pa_decode_shared", "pa_decode_shared_int8", "pa_pool_workspace", "pa_pool_append",
            "pa_pool_fork", "pa_pool_free", "pa_pool_compact",
            "pa_rope_store", "pa_rope_store_int8", "pa_decode_window", "pa_decode_window_int8", "pa_decode_weights",
-           "pa_decode_weights_int8", "pa_decode_weights_workspace",
+           "pa_decode_weights_int8", "pa_decode_weights_workspace", "pa_prefill_window", "pa_prefill_window_int8",
            "pa_last_error_string", "pa_read_device_error", "pa_selftest_bounded_wait", "pa_stream_read",
            "pa_version")
 
@@ -142,6 +142,8 @@ def lib() -> ctypes.CDLL:
             L.pa_pool_compact.argtypes = [P, P, P, P, P, P, SZ, P]
             L.pa_rope_store.argtypes = [P] * 5 + [ctypes.c_int64] * 3 + [P, P, I32] + [P] * 4
             L.pa_rope_store_int8.argtypes = [P] * 5 + [ctypes.c_int64] * 3 + [P, P, I32] + [P] * 6
+            L.pa_prefill_window.argtypes = [P] * 7 + [I32, I32, ctypes.c_float] + [P] * 4
+            L.pa_prefill_window_int8.argtypes = [P] * 11 + [I32, I32, ctypes.c_float] + [P] * 4 + [SZ, P]
             L.pa_decode_window.argtypes = [P] * 7 + [I32] * 5 + [ctypes.c_float, P, P]
             L.pa_decode_window_int8.argtypes = [P] * 9 + [I32] * 5 + [ctypes.c_float, P, P]
             L.pa_decode_weights.argtypes = [P] * 7 + [I32] * 3 + [ctypes.c_float] * 2 + [P] * 4 + [SZ, P]
@@ -870,6 +872,31 @@ def pa_decode_weights_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale,
                                                 _stream_of(q.get_device(), stream))
     if rc != PA_OK:
         _check(rc, "pa_decode_weights_int8")
+
+
+def pa_prefill_window(dims: pa_dims, q, k_cache, v_cache, plan: PrefillPlan, window: int, sinks: int, scale: float,
+                      out, stream=None):
+    """pa_prefill_varlen in which a query sees the last ``window`` keys up to its own and the first ``sinks`` ones
+    (the same plan)."""
+    m = plan.meta
+    _check(lib().pa_prefill_window(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                   plan.dptr(m.off_cu_seqlens_q), plan.dptr(m.off_cu_seqlens_k),
+                                   plan.dptr(m.off_block_tables), int(window), int(sinks), float(scale), _ptr(out),
+                                   ctypes.byref(m), plan.dptr(m.off_tiles), _stream(stream)), "pa_prefill_window")
+
+
+def pa_prefill_window_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, plan: PrefillPlan, window: int,
+                           sinks: int, scale: float, out, workspace=None, stream=None):
+    """pa_prefill_window over an INT8 cache (plan and workspace as pa_prefill_varlen_int8's)."""
+    m = plan.meta
+    workspace = _call_workspace(plan, workspace, q.device, stream)
+    ws_bytes = int(workspace.numel()) if isinstance(workspace, torch.Tensor) else 0
+    _check(lib().pa_prefill_window_int8(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                        _ptr(v_scale), plan.dptr(m.off_cu_seqlens_q), plan.dptr(m.off_cu_seqlens_k),
+                                        plan.dptr(m.off_block_tables), plan.dptr(m.off_scratch_tables),
+                                        plan.dptr(m.off_scratch_items), int(window), int(sinks), float(scale), _ptr(out),
+                                        ctypes.byref(m), plan.dptr(m.off_tiles), _ptr(workspace), ws_bytes,
+                                        _stream(stream)), "pa_prefill_window_int8")
 
 
 def int8_cache(dims: pa_dims, device="cuda"):

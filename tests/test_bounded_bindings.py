@@ -125,3 +125,24 @@ def test_library_refusals():
     assert rc("weights", ws_bytes=2 * 32 * 2 * 4 - 1) == pa.PA_ERR_WORKSPACE
     assert L.pa_decode_weights_workspace(ctypes.byref(d), -1, 2, ctypes.byref(need)) == bad
     assert L.pa_decode_weights_workspace(ctypes.byref(d), 1, 2, None) == bad
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_prefill_window_refusals(int8):
+    L = pa.lib()
+    dims = pa.make_dims(*DIMS)
+    plan = pa.pa_pack_prefill(dims, [20, 5], [20, 5], [[0, 1], [2]], pin=False)
+
+    def rc(window=8, sinks=0, scale=0.1, q=64, ws_bytes=1 << 30, meta=True):
+        m = ctypes.byref(plan.meta) if meta else None
+        head = (ctypes.byref(dims), q, 64, 64, *((64, 64) if int8 else ()), 64, 64, 64, *((64, 64) if int8 else ()), window,
+                sinks, ctypes.c_float(scale), 64, m, 64)
+        return L.pa_prefill_window_int8(*head, 64, ws_bytes, None) if int8 else L.pa_prefill_window(*head, None)
+
+    for kw in (dict(window=0), dict(window=-1), dict(sinks=-1), dict(scale=0.0), dict(q=None), dict(q=8), dict(meta=False)):
+        assert rc(**kw) == pa.PA_ERR_INVALID_ARG, kw
+    if int8:
+        assert rc(ws_bytes=16) == pa.PA_ERR_WORKSPACE
+    empty = pa.pa_pack_prefill(dims, [5], [0], [[0]], pin=False)
+    plan.meta = empty.meta
+    assert rc() == pa.PA_OK

@@ -1,0 +1,107 @@
+"""pa_prefill_window(_int8) against its formula in 64 bits.
+
+The cache holds NaN and infinities wherever no query looks; the plan names such a page where a table entry is not needed."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_kvcache_gb300 import pagedattn as pa
+from tests.bounded_model import Case, near, seen
+
+pytestmark = pytest.mark.gpu
+
+EVERYTHING = 2 ** 31 - 1
+HEADS = [(16, 8, 128), (28, 4, 128), (12, 1, 64), (7, 1, 128), (8, 8, 128), (4, 2, 64), (16, 1, 128)]
+CASES = [  # (length, new tokens) of each sequence, window, sinks, block size
+    ([(1, 1), (2, 2), (17, 17), (5, 0), (130, 1)], 1, 0, 16),
+    ([(300, 300), (129, 128)], 16, 4, 16),
+    ([(700, 50), (400, 400), (33, 33)], 100, 130, 32),
+    ([(1000, 1), (777, 3)], 128, 1, 256),
+    ([(600, 600)], 255, 257, 64),
+    ([(500, 200)], EVERYTHING, 0, 16),
+    ([(900, 100), (20, 20)], 300, EVERYTHING, 128),
+    ([(1400, 300)], 1000, 200, 1024),
+]
+MANY = [([(1600, 1600)], 200, 4, 16), ([(900, 700), (1200, 500)], 333, 150, 128)]  # more work items than SMs
+
+
+def model(c, q, new):
+    """(out, size) of the packed queries."""
+    out, size, at = np.zeros(q.shape), np.zeros(q.shape), 0
+    x, g = q.double().numpy(), c.hq // c.hkv
+    for n, lq, slots in zip(c.lens, new, c.slots):
+        mask = np.stack([seen(n, n - lq + i, c.window, c.sinks) for i in range(lq)]) if lq else np.zeros((0, n), bool)
+        for h in range(c.hq):
+            k, v = c.kd[slots, h // g], c.vd[slots, h // g]
+            cols = mask.any(0)
+            s = np.where(mask[:, cols], x[at:at + lq, h] @ k[cols].T * c.scale, -np.inf)
+            if lq:
+                p = np.exp(s - s.max(1, keepdims=True))
+                p /= p.sum(1, keepdims=True)
+                out[at:at + lq, h], size[at:at + lq, h] = p @ v[cols], p @ np.abs(v[cols])
+        at += lq
+    return out, size
+
+
+def run(seqs, window, sinks, bs, heads, int8, seed):
+    lens, new = [n for n, _ in seqs], [m for _, m in seqs]
+    c = Case(lens, *heads, bs, window, sinks, int8, seed=seed, first_new=[n - m for n, m in seqs])
+    if int8:  # a prompt reads code * scale as bf16
+        c.kd, c.vd = (torch.tensor(x).to(torch.bfloat16).double().numpy() for x in (c.kd, c.vd))
+    unseen = np.setdiff1d(np.arange(c.blocks), c.table[c.table >= 0])
+    lists = [np.where(t[:-(-n // bs)] < 0, unseen[0], t[:-(-n // bs)]) for t, n in zip(c.table, lens)]
+    q = torch.randn(sum(new), c.hq, c.d, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
+    plan = pa.pa_pack_prefill(c.dims, lens, new, lists).upload()
+    out = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device="cuda")
+    if int8:
+        ws = pa.prefill_workspace(plan).fill_(255)  # NaN wherever nothing is written
+        pa.pa_prefill_window_int8(c.dims, q.cuda(), *c.gpu, plan, window, sinks, c.scale, out, ws)
+    else:
+        pa.pa_prefill_window(c.dims, q.cuda(), *c.gpu, plan, window, sinks, c.scale, out)
+    near(out, *model(c, q, new))
+    return c, q, plan, out
+
+
+@pytest.mark.parametrize("int8", [False, True], ids=["bf16", "int8"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+@pytest.mark.parametrize("heads", HEADS, ids=lambda h: "-".join(map(str, h)))
+def test_prefill_window(heads, case, int8):
+    run(*CASES[case], heads, int8, seed=case)
+
+
+@pytest.mark.parametrize("int8", [False, True], ids=["bf16", "int8"])
+@pytest.mark.parametrize("case", range(len(MANY)))
+@pytest.mark.parametrize("heads", [(28, 4, 128), (16, 2, 64)], ids=lambda h: "-".join(map(str, h)))
+def test_many_work_items(heads, case, int8):
+    run(*MANY[case], heads, int8, seed=case)
+
+
+def test_a_wide_window_is_the_prefill_without_one_and_a_plan_serves_both():
+    c, q, plan, out = run([(1100, 900), (300, 300)], EVERYTHING, 0, 16, (28, 4, 128), False, 3)
+    plain = torch.empty_like(out)
+    pa.pa_prefill_varlen(c.dims, q.cuda(), *c.gpu, plan, c.scale, plain)
+    assert torch.equal(out, plain)
+    pa.pa_prefill_window(c.dims, q.cuda(), *c.gpu, plan, 5, EVERYTHING, c.scale, out)  # everything is a first token
+    assert torch.equal(out, plain)
+    pa.pa_prefill_window(c.dims, q.cuda(), *c.gpu, plan, 1, 0, c.scale, out)  # only itself
+    own = np.concatenate([c.vd[s[-m:]] for s, m in zip(c.slots, (900, 300))]).repeat(7, 1)
+    near(out, own, np.abs(own))
+
+
+def test_captured_and_on_another_stream():
+    c, q, plan, out = run([(800, 800)], 100, 4, 16, (16, 8, 128), False, 4)
+    want = out.clone()
+    qc, st, graph = q.cuda(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    out.zero_()
+    torch.cuda.synchronize()
+    pa.pa_prefill_window(c.dims, qc, *c.gpu, plan, 100, 4, c.scale, out, stream=st)
+    st.synchronize()
+    assert torch.equal(out, want)
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            pa.pa_prefill_window(c.dims, qc, *c.gpu, plan, 100, 4, c.scale, out)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
