@@ -515,7 +515,7 @@ int pa_copy_blocks(const pa_dims *dims, void *k_cache, void *v_cache, const int3
  * (fork).  New pages are always the free pages of the lowest ids, so the
  * result depends on the state alone.
  *
- * append, fork and compact are all or nothing: a call that cannot be carried out
+ * append, fork, compact and evict are all or nothing: a call that cannot be carried out
  * changes neither tables, lengths, counts nor pages and sets the device error
  * word, bit 7 (too few free pages, or a row longer than its table row) or bit 8
  * (an argument or a state the call's rules exclude).  Calls on one pool use its
@@ -676,6 +676,35 @@ int pa_decode_weights_int8(const pa_dims *dims, const void *q, const void *k_cac
                            const int32_t *block_tables, const int32_t *table_rows, int32_t num_seqs, int32_t num_rows,
                            int32_t max_blocks_per_seq, float scale, float decay, const float *scores,
                            float *scores_out, void *out, void *workspace, size_t workspace_bytes, pa_stream_t stream);
+
+/*
+ * pa_pool_evict — rows of a pool shrink to `budget` tokens by the attention
+ * weight that pa_decode_weights kept for them.  Of a row of n > budget tokens
+ * stay the first `first`, the last `last` and, of the others, those of the largest
+ * sum of scores over the KV heads (the exact sum rounded to fp32; NaN is below
+ * every number; of equal ones the lower index).  They move together in order, in
+ * all layers, K and V (and scales), bit for bit; the pages behind them lose an
+ * entry and the length becomes budget.  Slots behind the new length keep what
+ * they held.  Rows of at most budget tokens stay as they are.
+ *   rows:       device int32 [n], each row at most once
+ *   scores, scores_out: device fp32 [pool->num_rows][num_kv_heads][max_blocks *
+ *               block_size]; may be one array.  A row's scores move with its
+ *               tokens; behind the new length up to the old one scores_out gets
+ *               zeros.  What lies behind that, and other rows, stay
+ *   first, last: at least 0, together at most budget
+ *   kept:       device int32 [n][budget]: the place that each token had before, -1
+ *               behind a row of fewer (positions stay a token's own: whoever turns
+ *               keys and queries by position goes on counting from the old length)
+ *   workspace:  the pool's (pa_pool_workspace)
+ * All or nothing, as the other calls: a row outside the tables or named twice, a
+ * length or a page outside its bounds, a page of count 0, or a page that would be
+ * written while other entries name it (tokens in front of the first one that goes
+ * are not written, so a shared prefix within `first` may stay shared) set bit 8;
+ * then nothing changes, and kept is -1.
+ */
+int pa_pool_evict(const pa_dims *dims, const pa_pool *pool, const int32_t *rows, int32_t n, const float *scores,
+                  float *scores_out, int32_t budget, int32_t first, int32_t last, int32_t *kept, void *workspace,
+                  size_t workspace_bytes, pa_stream_t stream);
 
 /* ------------------------------------------------------------------ INT8 KV cache */
 

@@ -20,7 +20,7 @@ LIB = os.path.join(BUILD, "libpagedattn.so")
 
 SOURCES = ["api.cpp", "pack.cpp", "pack_shared.cpp", "store_kv.cu", "decode.cu", "decode_int8.cu", "decode_shared.cu",
            "prefill.cu", "copy_blocks.cu", "pool.cu", "rope_store.cu",
-           "decode_window.cu", "tmap.cpp", "selftest.cu"]
+           "decode_window.cu", "evict.cu", "tmap.cpp", "selftest.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

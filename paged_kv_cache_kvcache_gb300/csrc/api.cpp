@@ -834,6 +834,28 @@ extern "C" int pa_pool_compact(const pa_dims *dims, const pa_pool *pool, int32_t
     return launch_pool_compact(a, remap, block_tables_out, ref_counts_out, stream);
 }
 
+extern "C" int pa_pool_evict(const pa_dims *dims, const pa_pool *pool, const int32_t *rows, int32_t n,
+                             const float *scores, float *scores_out, int32_t budget, int32_t first, int32_t last,
+                             int32_t *kept, void *workspace, size_t workspace_bytes, pa_stream_t stream)
+{
+    PoolArgs a;
+    int rc = prepare_pool("pa_pool_evict", dims, pool, workspace, workspace_bytes, true, true, &a);
+    if (rc != PA_OK)
+        return rc;
+    if (n < 0 || n > pool->num_rows)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_evict: %d rows (the pool has %d)", n, pool->num_rows);
+    if (budget < 1 || first < 0 || last < 0 || (int64_t)first + last > budget)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_evict: budget %d must be positive and hold the first %d and last %d tokens",
+                    budget, first, last);
+    if ((int64_t)pool->max_blocks * dims->block_size > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "pa_pool_evict: max_blocks * block_size exceeds int32");
+    if (n == 0)
+        return PA_OK;
+    if (!rows || !scores || !scores_out || !kept)
+        return fail(PA_ERR_INVALID_ARG, "pa_pool_evict: NULL pointer");
+    return launch_pool_evict(a, rows, n, scores, scores_out, budget, first, last, kept, stream);
+}
+
 // Host-side checks of the decodes over a bounded cache, then the launch.
 static int decode_bounded(const char *fn, const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                           bool int8, const void *k_scale, const void *v_scale, const int32_t *context_lens,
@@ -995,6 +1017,8 @@ extern "C" int pa_read_device_error(uint32_t *code, pa_stream_t stream)
         rc = read_rope_error(code);
     if (rc == PA_OK)
         rc = read_window_error(code);
+    if (rc == PA_OK)
+        rc = read_evict_error(code);
     return rc;
 }
 

@@ -1,0 +1,449 @@
+// Rows of a page pool shrink to a budget of tokens: what the attention weighed least goes.
+//
+// Of a row of n > budget tokens stay the first `first`, the last `last` and, of the others, those of the largest
+// totals: total_j = sum over the KV heads of score[g][j] (pa_decode_weights keeps the scores), of equal ones the
+// lower index.  What stays moves together in order: token kept[k] goes to place k, its keys and values in all
+// layers, its scores, and the pages behind place budget - 1 lose an entry.
+//
+// Sources (page title, section): "手搓 vLLM 推理引擎", Step 2 (BlockManager: block tables, reference counts);
+// "vLLM / SGLang 面试源码深挖", section 4 (shared blocks must not be written).
+//
+// Two launches.  The choice: one CTA per row, totals once into shared memory as ordered integers, the smallest
+// one that stays by three rounds of counting (11, 11 and 10 bits), then ballots give every kept token its place;
+// bound by reading the row's scores with one SM.  The move: a CTA takes a slice of the token rows of one (row,
+// layer, K or V) and walks the places upwards: as kept[k] >= k, a batch's places lie below the next
+// batch's sources, so it moves in place, the next batch's loads in flight while this one's are stored.  Bound by
+// HBM (each moved token read and written once).  The last CTA of a row changes its table, length and counts.
+// The call is all or nothing: the choice checks every row, and the move looks at all verdicts first.
+#include <algorithm>
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace pa {
+
+__device__ uint32_t g_evict_error; // bit 0: a malformed call or state
+
+namespace {
+
+constexpr int kChooseThreads = 1024;
+constexpr int kChooseWarps = kChooseThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kKeysInSmem = 49152;
+constexpr int kMoveThreads = 256;
+constexpr int kVecs = 4; // 16-byte vectors per thread and batch
+constexpr int kBatchTokens = kMoveThreads * kVecs; // at most: of one vector, value or scale each
+
+struct EvictParams {
+    int32_t *tables, *context_lens, *refs;
+    const int32_t *rows;
+    int32_t n, num_rows, max_blocks, num_blocks, block_size, num_kv_heads;
+    const float *scores;
+    float *scores_out;
+    int32_t budget, first, last;
+    int32_t *kept;   // [n][budget]
+    int32_t *state;  // [n] length of the row, -1: refused
+    int32_t *moved;  // [n] first place whose token moves
+    uint32_t *done;  // [n] units of the move that are through
+    int32_t keys;    // places of the key buffer in shared memory
+};
+
+// Larger totals have larger keys; NaN is below every number.
+__device__ __forceinline__ uint32_t order(float x)
+{
+    if (x != x)
+        return 0u;
+    const uint32_t u = __float_as_uint(x + 0.f); // (-0 is 0)
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// The sum over the heads, as exact as a 64-bit sum to within fp32's last bit: s + e is carried without
+// rounding errors but those of e (two-sum; fp64 adds run at 1/64 of fp32's rate and took longer than the reads).
+__device__ __forceinline__ uint32_t total_of(const float *at, int heads, int64_t pitch)
+{
+    float s = 0.f, e = 0.f;
+    for (int h = 0; h < heads; ++h) {
+        const float x = at[h * pitch];
+        const float t = __fadd_rn(s, x);
+        const float b = __fsub_rn(t, s);
+        e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
+        s = t;
+    }
+    return order(isfinite(s) ? __fadd_rn(s, e) : s);
+}
+
+// exclusive sum over the CTA's threads; *sum: all
+__device__ __forceinline__ int scan_cta(int v, int *warps, int *sum)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads(); // warps[] may still be read
+    if (lane == 31)
+        warps[warp] = x;
+    __syncthreads();
+    int w = warps[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o)
+            w += y;
+    }
+    *sum = __shfl_sync(0xffffffffu, w, 31);
+    const int before = warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
+    return before + x - v;
+}
+
+__global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const EvictParams p)
+{
+    extern __shared__ uint32_t keys[];
+    __shared__ int hist[kBins];
+    __shared__ int warps[kChooseWarps], warps2[kChooseWarps];
+    __shared__ int digit, above, lowest;
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int bs = p.block_size, room = p.max_blocks * bs, budget = p.budget;
+    const int row = p.rows[i];
+    const bool in = (uint32_t)row < (uint32_t)p.num_rows;
+    const int n = in ? p.context_lens[row] : -1;
+    bool bad = n < 0 || n > room;
+    for (int x = tid; x < i; x += kChooseThreads) // a row once
+        bad = bad || p.rows[x] == row;
+    int32_t *kept = p.kept + (int64_t)i * budget;
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) {
+            p.state[i] = -1;
+            atomicOr(&g_evict_error, 1u);
+        }
+        return;
+    }
+    if (n <= budget) {
+        for (int k = tid; k < budget; k += kChooseThreads)
+            kept[k] = k < n ? k : -1;
+        if (tid == 0) {
+            p.state[i] = n;
+            p.moved[i] = n;
+            p.done[i] = 0u;
+        }
+        return;
+    }
+
+    const float *scores = p.scores + (int64_t)row * p.num_kv_heads * room;
+    const bool stored = n <= p.keys;
+    const int begin = p.first, end = n - p.last; // of those to choose from
+    if (stored) {
+        for (int j = tid; j < n; j += kChooseThreads)
+            keys[j] = j >= begin && j < end ? total_of(scores + j, p.num_kv_heads, room) : 0u;
+    }
+    auto key = [&](int j) { return stored ? keys[j] : total_of(scores + j, p.num_kv_heads, room); };
+    if (tid == 0)
+        lowest = n;
+
+    // the m-th largest key: its bits from the top, and how many of the keys equal to it stay
+    int need = budget - p.first - p.last;
+    uint32_t prefix = 0;
+    const bool any = need > 0;
+    for (int round = 0; any && round < 3; ++round) {
+        const int shift = round == 0 ? 21 : round == 1 ? 10 : 0, bits = round == 2 ? 10 : 11;
+        for (int x = tid; x < kBins; x += kChooseThreads)
+            hist[x] = 0;
+        __syncthreads();
+        for (int j = begin + tid; j < end; j += kChooseThreads) {
+            const uint32_t x = key(j);
+            if (round == 0 || x >> (shift + bits) == prefix)
+                atomicAdd(&hist[(x >> shift) & ((1u << bits) - 1u)], 1);
+        }
+        __syncthreads();
+        // two bins per thread, from the largest down
+        const int hi = kBins - 1 - 2 * tid;
+        const int a = hist[hi], b = hist[hi - 1];
+        int sum;
+        const int before = scan_cta(a + b, warps, &sum);
+        if (before < need && need <= before + a) {
+            digit = hi;
+            above = before;
+        } else if (before + a < need && need <= before + a + b) {
+            digit = hi - 1;
+            above = before + a;
+        }
+        __syncthreads();
+        prefix = (prefix << bits) | (uint32_t)digit;
+        need -= above;
+        __syncthreads();
+    }
+
+    // places: a warp has a run of tokens; of what lies before it, `more` stay for sure and `equal` are of the last key
+    const int run = ((n + kChooseWarps - 1) / kChooseWarps + 31) & ~31;
+    const int from = min(warp * run, n), to = min(from + run, n);
+    auto look = [&](int j, bool &sure, bool &same) {
+        sure = same = false;
+        if (j < to) {
+            if (j < begin || j >= end) {
+                sure = true;
+            } else if (any) {
+                const uint32_t x = key(j);
+                sure = x > prefix;
+                same = x == prefix;
+            }
+        }
+    };
+    __syncthreads(); // (keys, where nothing was counted)
+    int more = 0, equal = 0;
+    for (int j = from; j < to; j += 32) {
+        bool sure, same;
+        look(j + lane, sure, same);
+        more += __popc(__ballot_sync(0xffffffffu, sure));
+        equal += __popc(__ballot_sync(0xffffffffu, same));
+    }
+    if (lane == 0) {
+        warps[warp] = more;
+        warps2[warp] = equal;
+    }
+    __syncthreads();
+    more = equal = 0;
+    for (int w = 0; w < warp; ++w) {
+        more += warps[w];
+        equal += warps2[w];
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    for (int j = from; j < to; j += 32) {
+        bool sure, same;
+        look(j + lane, sure, same);
+        const uint32_t ms = __ballot_sync(0xffffffffu, sure), me = __ballot_sync(0xffffffffu, same);
+        const int eq = equal + __popc(me & below);
+        const bool stays = sure || (same && eq < need);
+        if (stays)
+            kept[more + __popc(ms & below) + min(eq, need)] = j + lane;
+        const uint32_t gone = __ballot_sync(0xffffffffu, !stays && j + lane < to);
+        if (gone && lane == 0)
+            atomicMin(&lowest, j + __ffs(gone) - 1);
+        more += __popc(ms);
+        equal += __popc(me);
+    }
+    __syncthreads();
+
+    // the row's pages are in use, and those that are written are its own
+    const int moved = lowest; // the tokens before the first that goes stay where they are
+    const int32_t *table = p.tables + (int64_t)row * p.max_blocks;
+    for (int x = tid; x < (n + bs - 1) / bs; x += kChooseThreads) {
+        const int page = table[x];
+        const bool written = moved < budget && x >= moved / bs && x < (budget + bs - 1) / bs;
+        bad = bad || (uint32_t)page >= (uint32_t)p.num_blocks || p.refs[page] < 1 || (written && p.refs[page] != 1);
+    }
+    bad = __syncthreads_or(bad);
+    if (tid == 0) {
+        p.state[i] = bad ? -1 : n;
+        p.moved[i] = moved;
+        p.done[i] = 0u;
+        if (bad)
+            atomicOr(&g_evict_error, 1u);
+    }
+}
+
+struct MovePlanes {
+    char *k, *v, *ks, *vs; // layer 0; scales NULL: bf16
+    uint64_t layer, scale_layer; // bytes between layers
+    int32_t layers, token_bytes; // bytes of a token's row in one layer of k (or v)
+    int32_t slice_vecs;          // 16-byte vectors of a slice
+    int32_t slices;              // slices of a token's row
+    int32_t units;               // per row: (layer, K or V, slice), then (layer, K or V, head) of the scales, then heads
+                                 // of the scores
+};
+
+// Elements T of the places [from, count) from where their tokens are: place and source give an element's address.
+// A batch has `tokens` places of kThreadVecs x kMoveThreads elements.
+template <class T, class Dst, class Src>
+__device__ __forceinline__ void move_up(int from, int count, int per, Dst dst, Src src)
+{
+    const int tokens = kBatchTokens / per;
+    T a[kVecs], b[kVecs];
+    auto load = [&](int base, T(&x)[kVecs]) {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            const int e = u * kMoveThreads + (int)threadIdx.x;
+            const int k = base + e / per;
+            if (e < tokens * per && k < count)
+                x[u] = *src(k, e % per);
+        }
+    };
+    auto store = [&](int base, const T(&x)[kVecs]) {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            const int e = u * kMoveThreads + (int)threadIdx.x;
+            const int k = base + e / per;
+            if (e < tokens * per && k < count)
+                *dst(k, e % per) = x[u];
+        }
+    };
+    load(from, a);
+    for (int base = from; base < count; base += 2 * tokens) {
+        load(base + tokens, b);
+        __syncthreads(); // every thread has this batch's values: its places may be written
+        store(base, a);
+        load(base + 2 * tokens, a);
+        __syncthreads();
+        store(base + tokens, b);
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, const MovePlanes q)
+{
+    __shared__ uint32_t place;
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int i = blockIdx.x / q.units;
+    int unit = blockIdx.x - i * q.units;
+    const int tid = threadIdx.x, bs = p.block_size, budget = p.budget;
+    bool refused = false;
+    for (int x = tid; x < p.n; x += kMoveThreads)
+        refused = refused || p.state[x] < 0;
+    int32_t *kept = p.kept + (int64_t)i * budget;
+    if (__syncthreads_or(refused)) { // nothing moves
+        if (unit == 0)
+            for (int k = tid; k < budget; k += kMoveThreads)
+                kept[k] = -1;
+        return;
+    }
+    const int row = p.rows[i], n = p.state[i];
+    const int left = min(n, budget);
+    const int64_t room = (int64_t)p.max_blocks * bs;
+    int32_t *table = p.tables + (int64_t)row * p.max_blocks;
+    const int planes = 2 * q.layers;
+    const int moved = p.moved[i];
+    auto slot = [&](int token) { return (int64_t)table[token / bs] * bs + (token & (bs - 1)); };
+
+    if (unit < planes * q.slices) {
+        const int plane = unit / q.slices, slice = unit - plane * q.slices;
+        const int per = min(q.slice_vecs, q.token_bytes / 16 - slice * q.slice_vecs);
+        char *base = (plane & 1 ? q.v : q.k) + (plane >> 1) * q.layer + (int64_t)slice * q.slice_vecs * 16;
+        if (moved < left)
+            move_up<uint4>(
+                moved, left, per, [&](int k, int e) { return reinterpret_cast<uint4 *>(base + slot(k) * q.token_bytes) + e; },
+                [&](int k, int e) { return reinterpret_cast<const uint4 *>(base + slot(kept[k]) * q.token_bytes) + e; });
+    } else if ((unit -= planes * q.slices) < (q.ks ? planes * p.num_kv_heads : 0)) {
+        const int plane = unit / p.num_kv_heads, head = unit - plane * p.num_kv_heads;
+        uint16_t *base = reinterpret_cast<uint16_t *>((plane & 1 ? q.vs : q.ks) + (plane >> 1) * q.scale_layer);
+        auto at = [&](int token) {
+            return base + ((int64_t)table[token / bs] * p.num_kv_heads + head) * bs + (token & (bs - 1));
+        };
+        if (moved < left)
+            move_up<uint16_t>(moved, left, 1, [&](int k, int) { return at(k); },
+                              [&](int k, int) { return (const uint16_t *)at(kept[k]); });
+    } else {
+        unit -= q.ks ? planes * p.num_kv_heads : 0;
+        const int64_t at = ((int64_t)row * p.num_kv_heads + unit) * room;
+        const float *from = p.scores + at;
+        float *to = p.scores_out + at;
+        const int start = from == to ? moved : 0;
+        if (start < left)
+            move_up<float>(start, left, 1, [&](int k, int) { return to + k; }, [&](int k, int) { return from + kept[k]; });
+        __syncthreads();
+        for (int k = left + tid; k < n; k += kMoveThreads)
+            to[k] = 0.f;
+    }
+
+    // the row's last unit: nothing reads its table any more
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();
+        place = atomicAdd(p.done + i, 1u);
+    }
+    __syncthreads();
+    if (place == (uint32_t)q.units - 1u && n > budget) {
+        for (int x = (budget + bs - 1) / bs + tid; x < (n + bs - 1) / bs; x += kMoveThreads) {
+            atomicSub(p.refs + table[x], 1); // (another row of the call may give back the same page)
+            table[x] = -1;
+        }
+        if (tid == 0)
+            p.context_lens[row] = budget;
+    }
+}
+
+template <class... Args>
+int launch_ex(const char *what, void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
+              const Args &...args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PA_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    }
+    return PA_OK;
+}
+
+} // namespace
+
+int launch_pool_evict(const PoolArgs &a, const int32_t *rows, int n, const float *scores, float *scores_out, int budget,
+                      int first, int last, int32_t *kept, void *stream)
+{
+    int sms = 0;
+    if (int rc = sm_count(&sms))
+        return rc;
+    const pa_dims &d = a.dims;
+    const pa_pool &o = a.pool;
+    EvictParams p{};
+    p.tables = o.block_tables, p.context_lens = o.context_lens, p.refs = o.ref_counts;
+    p.rows = rows, p.n = n, p.num_rows = o.num_rows, p.max_blocks = o.max_blocks;
+    p.num_blocks = d.num_blocks, p.block_size = d.block_size, p.num_kv_heads = d.num_kv_heads;
+    p.scores = scores, p.scores_out = scores_out;
+    p.budget = budget, p.first = first, p.last = last, p.kept = kept;
+    p.state = static_cast<int32_t *>(a.workspace); // of the pool's 8 ints and more per row
+    p.moved = p.state + o.num_rows;
+    p.done = reinterpret_cast<uint32_t *>(p.moved + o.num_rows);
+    p.keys = (int)std::min<int64_t>((int64_t)o.max_blocks * d.block_size, kKeysInSmem);
+    MovePlanes q{};
+    q.k = static_cast<char *>(o.k_cache), q.v = static_cast<char *>(o.v_cache);
+    q.ks = static_cast<char *>(o.k_scale), q.vs = static_cast<char *>(o.v_scale);
+    q.layer = o.layer_stride, q.scale_layer = o.scale_layer_stride;
+    q.layers = o.num_layers;
+    q.token_bytes = d.num_kv_heads * d.head_dim * (o.k_scale ? 1 : 2);
+    // slices: the whole row of a token, or less (down to 64 bytes) while that gives the SMs too few CTAs
+    const int vecs = q.token_bytes / 16;
+    q.slice_vecs = std::min(vecs, 64);
+    while (q.slice_vecs > 4 && (int64_t)n * q.layers * 2 * ((vecs + q.slice_vecs - 1) / q.slice_vecs) < 8 * sms)
+        q.slice_vecs = (q.slice_vecs + 1) / 2;
+    q.slices = (vecs + q.slice_vecs - 1) / q.slice_vecs;
+    const int64_t units = (int64_t)2 * q.layers * (q.slices + (q.ks ? d.num_kv_heads : 0)) + d.num_kv_heads;
+    if (units * n > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "pa_pool_evict: %d rows of %d layers exceed one launch", n, q.layers);
+    q.units = (int32_t)units;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t smem = (size_t)p.keys * 4;
+    if (int rc = ensure_smem<evict_choose_kernel>(kKeysInSmem * 4, "evict"))
+        return rc;
+    if (int rc = launch_ex("evict choice", evict_choose_kernel, (unsigned)n, kChooseThreads, smem, s, p))
+        return rc;
+    return launch_ex("evict move", evict_move_kernel, (unsigned)(units * n), kMoveThreads, 0, s, p, q);
+}
+
+int read_evict_error(uint32_t *code)
+{
+    uint32_t v = 0, zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_evict_error, sizeof v);
+    if (e == cudaSuccess)
+        e = cudaMemcpyToSymbol(g_evict_error, &zero, sizeof zero);
+    if (e != cudaSuccess)
+        return fail(PA_ERR_CUDA, "reading evict error word: %s", cudaGetErrorString(e));
+    *code |= (v & 1u) << 8;
+    return PA_OK;
+}
+
+} // namespace pa

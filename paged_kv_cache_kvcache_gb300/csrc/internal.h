@@ -262,6 +262,8 @@ int launch_pool_append(const PoolArgs &a, const int32_t *rows, const int32_t *cu
 int launch_pool_fork(const PoolArgs &a, const int32_t *parents, const int32_t *children, int n, void *stream);
 int launch_pool_free(const PoolArgs &a, const int32_t *rows, int n, void *stream);
 int launch_pool_compact(const PoolArgs &a, int32_t *remap, int32_t *tables_out, int32_t *refs_out, void *stream);
+int launch_pool_evict(const PoolArgs &a, const int32_t *rows, int n, const float *scores, float *scores_out, int budget,
+                      int first, int last, int32_t *kept, void *stream); // evict.cu
 
 // Norm, rotation and store (rope_store.cu); k_scale / v_scale NULL: bf16 cache.
 struct RopeArgs {
@@ -327,6 +329,7 @@ int read_shared_error(uint32_t *code); // bit 0 -> 5 (wait), bit 1 -> 6 (block i
 int read_pool_error(uint32_t *code);   // bit 0 -> 7 (no room), bit 1 -> 8 (malformed)
 int read_rope_error(uint32_t *code);   // bit 0 (slot), bit 1 -> 9 (position)
 int read_window_error(uint32_t *code); // bit 0 -> 6 (block id outside the pool)
+int read_evict_error(uint32_t *code);  // bit 0 -> 8 (malformed)
 int launch_selftest_wait(uint32_t timeout_us, int arrive_first, void *stream);
 int read_selftest_error(uint32_t *code);
 int launch_stream_read(const void *src, size_t bytes, uint32_t *sink, void *stream);

@@ -28,6 +28,7 @@ EXPORTS = ("pa_pack_prefill", "pa_pack_decode", "pa_upload", "pa_store_kvcache",
            "pa_pool_fork", "pa_pool_free", "pa_pool_compact",
            "pa_rope_store", "pa_rope_store_int8", "pa_decode_window", "pa_decode_window_int8", "pa_decode_weights",
            "pa_decode_weights_int8", "pa_decode_weights_workspace", "pa_prefill_window", "pa_prefill_window_int8",
+           "pa_pool_evict",
            "pa_last_error_string", "pa_read_device_error", "pa_selftest_bounded_wait", "pa_stream_read",
            "pa_version")
 
@@ -142,6 +143,7 @@ def lib() -> ctypes.CDLL:
             L.pa_pool_compact.argtypes = [P, P, P, P, P, P, SZ, P]
             L.pa_rope_store.argtypes = [P] * 5 + [ctypes.c_int64] * 3 + [P, P, I32] + [P] * 4
             L.pa_rope_store_int8.argtypes = [P] * 5 + [ctypes.c_int64] * 3 + [P, P, I32] + [P] * 6
+            L.pa_pool_evict.argtypes = [P, P, P, I32, P, P, I32, I32, I32, P, P, SZ, P]
             L.pa_prefill_window.argtypes = [P] * 7 + [I32, I32, ctypes.c_float] + [P] * 4
             L.pa_prefill_window_int8.argtypes = [P] * 11 + [I32, I32, ctypes.c_float] + [P] * 4 + [SZ, P]
             L.pa_decode_window.argtypes = [P] * 7 + [I32] * 5 + [ctypes.c_float, P, P]
@@ -897,6 +899,24 @@ def pa_prefill_window_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale,
                                         plan.dptr(m.off_scratch_items), int(window), int(sinks), float(scale), _ptr(out),
                                         ctypes.byref(m), plan.dptr(m.off_tiles), _ptr(workspace), ws_bytes,
                                         _stream(stream)), "pa_prefill_window_int8")
+
+
+def pa_pool_evict(dims: pa_dims, pool: PagePool, rows, scores, budget: int, kept, first: int = 0, last: int = 0,
+                  scores_out=None, stream=None):
+    """Shrink rows to ``budget`` tokens: the first and last ones, and of the others those of the largest scores.
+
+    scores: float32 [pool rows, Hkv, width * block_size], as pa_decode_weights keeps them (moved with the tokens, in
+    place or into ``scores_out``); kept: int32 [rows, budget], each kept token's place before.
+    """
+    dev, n = pool.device, rows.numel()
+    at = _int32(rows, "rows", None, dev)
+    places = _int32(kept, "kept", n * budget, dev)
+    s, so = _score_args(pool.dims, pool.block_tables, scores, scores_out, None)
+    pool.check(dims)
+    rc = (_lib or lib()).pa_pool_evict(pool.dims_ref, pool.ref, at, n, s, so, budget, first, last, places, *pool.ws,
+                                       _stream_of(pool.device, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_pool_evict")
 
 
 def int8_cache(dims: pa_dims, device="cuda"):
