@@ -45,6 +45,51 @@ __device__ __forceinline__ int code_of(float x, float scale, float rcp)
     return __float2int_rz(q >= 0.f ? __fadd_rn(q, 0.5f) : __fsub_rn(q, 0.5f));
 }
 
+// code_of of 16 values, as four words (lowest byte first).  q' + 1.5 * 2^23 rounds q' to the nearest integer and
+// leaves it in the sum's low bits, so its low byte is the code wherever q' is further from a half-integer than
+// |q'| * 2^-20 <= 127 * 2^-20 (where both ways of rounding and q itself agree): five instructions a value.
+// The values nearer than that, and NaN, go through code_of one by one (kept small: 16 copies of it cost more in
+// instruction fetches than they ran).
+__device__ __forceinline__ void codes_of_16(const float (&x)[16], float scale, float rcp, uint32_t (&c)[4])
+{
+    constexpr float kMagic = 12582912.0f, kNear = 0.5f - 0x1p-13f; // 2^-13 > 127.001 * 2^-20
+    auto away = [&](float q, float m) { return fabsf(__fsub_rn(q, __fsub_rn(m, kMagic))) <= kNear; };
+    bool clear = true;
+    uint32_t u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float q = __fmul_rn(x[i], rcp);
+        const float m = __fadd_rn(q, kMagic);
+        u[i] = __float_as_uint(m);
+        clear = clear && away(q, m);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c[i] = __byte_perm(__byte_perm(u[4 * i], u[4 * i + 1], 0x0040), __byte_perm(u[4 * i + 2], u[4 * i + 3], 0x0040), 0x5410);
+    if (clear)
+        return;
+    uint32_t left = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float q = __fmul_rn(x[i], rcp);
+        left |= (away(q, __fadd_rn(q, kMagic)) ? 0u : 1u) << i;
+    }
+#pragma unroll 1
+    while (left) {
+        const int i = __ffs((int)left) - 1;
+        left &= left - 1u;
+        float v = x[0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e)
+            v = i == e ? x[e] : v;
+        const uint32_t code = (uint32_t)(code_of(v, scale, rcp) & 0xff);
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            if (i >> 2 == w)
+                c[w] = (c[w] & ~(0xffu << (8 * (i & 3)))) | code << (8 * (i & 3));
+    }
+}
+
 template <int D>
 constexpr int kThreadsPerRow = D / 32;
 

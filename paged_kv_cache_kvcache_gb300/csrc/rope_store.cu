@@ -12,9 +12,9 @@
 // tokens); "面试问答准备: nano-vLLM 推理引擎优化", Q3 (the INT8 quantiser).
 //
 // Work: D / 16 adjacent lanes per head row, 16 values each: lane j has pairs 8j .. 8j + 7 whole, so a turn
-// needs no shuffle, and a row's sum of squares (or its max|x|) log2(D / 16) of them.  A group takes
-// kHeads rows of one token, whose cos and sin it loads once.  Bound: HBM for prompts (each row read and
-// written once), the latency of one launch for decode steps.
+// needs no shuffle, and a row's sum of squares (or its max|x|) log2(D / 16) of them.  A warp takes a few
+// rows (the same heads, so that its lanes do not part) of 512 / D tokens, whose cos and sin it loads once.
+// Bound: HBM for prompts (each row read and written once), the latency of one launch for decode steps.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -29,7 +29,7 @@ __device__ uint32_t g_rope_error; // bit 0: a slot outside [-1, num_slots); bit 
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct RopeParams {
     const __nv_bfloat16 *q, *k, *v;
@@ -45,7 +45,8 @@ struct RopeParams {
     float eps;
     int32_t num_tokens, num_heads, num_kv_heads, block_size;
     int32_t num_axes, max_position, pairs; // pairs: R / 2
-    int32_t units;                         // groups per token
+    int32_t heads_per_unit;                // a token's rows are cut into units of so many at most
+    int32_t units, q_units, kv_units;
     int64_t num_slots;
 };
 
@@ -65,129 +66,93 @@ __device__ __forceinline__ uint4 pack8(const float *x)
                       ptx::pack_bf16(x[6], x[7]));
 }
 
-// kNext: pairs (2i, 2i + 1).  kAxes: more than one position per token.
-template <int D, bool kInt8, bool kNext, bool kAxes, int kHeads>
-__global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeParams p)
+// The lane's two pieces of 8 values of a row: of a turned part its 8 pairs, of the rest 16 consecutive values.
+struct Place {
+    int c0, c1;
+    bool turn;
+};
+
+template <int D>
+__device__ __forceinline__ void load_row(const __nv_bfloat16 *src, int h, const Place &at, uint4 (&x)[2])
 {
-    constexpr int kLanes = D / 16; // of a row
-    ptx::launch_dependents();
-    ptx::grid_dependency_wait();
-    const uint32_t group = blockIdx.x * (uint32_t)(kThreads / kLanes) + threadIdx.x / kLanes;
-    const int j = threadIdx.x % kLanes;
-    const uint32_t token = group / (uint32_t)p.units;
-    const int h0 = (int)(group - token * (uint32_t)p.units) * kHeads;
-    const int heads = p.num_heads + 2 * p.num_kv_heads;
-    // every lane stays to the end: the groups of a warp shuffle together
-    const int t = (int)min(token, (uint32_t)p.num_tokens - 1u);
-    bool live = token < (uint32_t)p.num_tokens;
+    x[0] = ptx::ld_once_v4(src + h * D + at.c0);
+    x[1] = ptx::ld_once_v4(src + h * D + at.c1);
+}
 
-    // the lane's two pieces of 8 values: of a turned part its 8 pairs, of the rest 16 consecutive values
-    const int half = p.pairs;
-    const bool turn = 8 * j < half;
-    const int c0 = kNext || !turn ? 16 * j : 8 * j;
-    const int c1 = kNext || !turn ? c0 + 8 : c0 + half;
-
-    uint4 raw[kHeads][2];
-#pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-        const int h = h0 + u;
-        raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && h < heads) {
-            const __nv_bfloat16 *row =
-                h < p.num_heads ? p.q + (int64_t)t * p.q_stride + (int64_t)h * D
-                : h < p.num_heads + p.num_kv_heads
-                    ? p.k + (int64_t)t * p.k_stride + (int64_t)(h - p.num_heads) * D
-                    : p.v + (int64_t)t * p.v_stride + (int64_t)(h - p.num_heads - p.num_kv_heads) * D;
-            raw[u][0] = ptx::ld_once_v4(row + c0);
-            raw[u][1] = ptx::ld_once_v4(row + c1);
-        }
+// count rows from src on (a token's, D values apart; raw: the first kRows) to dst; every lane of the warp is here,
+// `write` is its token's.  kKind: 0 queries, 1 keys, 2 values.  w: the norm's weight or NULL.
+template <int D, bool kInt8, bool kNext, int kRows, int kKind>
+__device__ __forceinline__ void turn_rows(const __nv_bfloat16 *src, uint4 (&raw)[kRows][2], int count, const Place &at, const float (&cs)[8],
+                                          const float (&sn)[8], const __nv_bfloat16 *w, float eps, void *dst_rows,
+                                          __half *scales, int scale_step, bool write)
+{
+    constexpr int kLanes = D / 16;
+    constexpr bool kCodes = kInt8 && kKind != 0;
+    uint4 wt[2];
+    if (kKind != 2 && w) {
+        wt[0] = *reinterpret_cast<const uint4 *>(w + at.c0);
+        wt[1] = *reinterpret_cast<const uint4 *>(w + at.c1);
     }
-    const int32_t slot = p.slots[t];
-    float cs[8], sn[8];
-    if constexpr (!kAxes) {
-        const int pos = p.positions[t];
-        const bool inside = (uint32_t)pos < (uint32_t)p.max_position;
-        if (!inside && live && j == 0 && h0 == 0)
-            atomicOr(&g_rope_error, 2u);
-        live = live && inside;
-        if (turn && inside) {
-            const float4 *at = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * half + 8 * j);
-            const float4 *as = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * half + half + 8 * j);
-            *reinterpret_cast<float4 *>(cs) = at[0], *reinterpret_cast<float4 *>(cs + 4) = at[1];
-            *reinterpret_cast<float4 *>(sn) = as[0], *reinterpret_cast<float4 *>(sn + 4) = as[1];
+    auto finish = [&](int h, const uint4(&in)[2]) {
+        if constexpr (kKind == 2 && !kCodes) { // a value's row goes as it is
+            if (write) {
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(dst_rows) + h * D;
+                *reinterpret_cast<uint4 *>(dst + at.c0) = in[0];
+                *reinterpret_cast<uint4 *>(dst + at.c1) = in[1];
+            }
+            return;
         }
-    } else {
-        int pos[4];
-        bool inside = true;
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            pos[a] = a < p.num_axes ? p.positions[(int64_t)a * p.num_tokens + t] : 0;
-            inside = inside && (uint32_t)pos[a] < (uint32_t)p.max_position;
-        }
-        if (!inside && live && j == 0 && h0 == 0)
-            atomicOr(&g_rope_error, 2u);
-        live = live && inside;
-        if (turn && inside) {
-            const uint32_t bits = (uint32_t)(p.axis_bits[j >> 2] >> (16 * (j & 3)));
+        float x[16];
+        unpack8(in[0], x);
+        unpack8(in[1], x + 8);
+        if (kKind != 2 && w) {
+            uint64_t two[8], sum2[2] = {ptx::f2(0.f, 0.f), ptx::f2(0.f, 0.f)};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int a = (bits >> (2 * i)) & 3;
-                const int at = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
-                const float *row = p.cos_sin + (int64_t)at * 2 * half + 8 * j + i;
-                cs[i] = row[0];
-                sn[i] = row[half];
+                two[i] = ptx::f2(x[2 * i], x[2 * i + 1]);
+                sum2[i & 1] = ptx::f2_fma(two[i], two[i], sum2[i & 1]);
             }
-        }
-    }
-    const bool stored = slot >= 0 && slot < p.num_slots;
-    if (!stored && slot != -1 && live && j == 0 && h0 == 0)
-        atomicOr(&g_rope_error, 1u);
-
-#pragma unroll
-    for (int u = 0; u < kHeads; ++u) {
-        const int h = h0 + u;
-        const bool is_q = h < p.num_heads, is_v = h >= p.num_heads + p.num_kv_heads;
-        const bool write = live && h < heads && (is_q || stored);
-        float x[16];
-        unpack8(raw[u][0], x);
-        unpack8(raw[u][1], x + 8);
-        const __nv_bfloat16 *w = is_q ? p.q_weight : p.k_weight;
-        if (p.q_weight != nullptr || p.k_weight != nullptr) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                sum = fmaf(x[i], x[i], sum);
+            float s0, s1;
+            ptx::f2_split(ptx::f2_add(sum2[0], sum2[1]), s0, s1);
+            float sum = s0 + s1;
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (!is_v && w != nullptr) {
-                const float r = rsqrtf(sum * (1.f / D) + p.eps);
-                float y[16];
-                unpack8(*reinterpret_cast<const uint4 *>(w + c0), y);
-                unpack8(*reinterpret_cast<const uint4 *>(w + c1), y + 8);
+            const float r = rsqrtf(sum * (1.f / D) + eps);
+            float y[16];
+            unpack8(wt[0], y);
+            unpack8(wt[1], y + 8);
+            const uint64_t r2 = ptx::f2(r, r);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    x[i] = x[i] * r * y[i];
+            for (int i = 0; i < 8; ++i)
+                ptx::f2_split(ptx::f2_mul(ptx::f2_mul(two[i], r2), ptx::f2(y[2 * i], y[2 * i + 1])), x[2 * i], x[2 * i + 1]);
+        }
+        if (kKind != 2 && at.turn) {
+            if constexpr (kNext) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float a = x[2 * i], b = x[2 * i + 1];
+                    x[2 * i] = a * cs[i] - b * sn[i];
+                    x[2 * i + 1] = b * cs[i] + a * sn[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const uint64_t a = ptx::f2(x[i], x[i + 1]), b = ptx::f2(x[i + 8], x[i + 9]);
+                    const uint64_t c2 = ptx::f2(cs[i], cs[i + 1]), s2 = ptx::f2(sn[i], sn[i + 1]);
+                    const uint64_t minus = ptx::f2(-x[i + 8], -x[i + 9]);
+                    ptx::f2_split(ptx::f2_fma(minus, s2, ptx::f2_mul(a, c2)), x[i], x[i + 1]);
+                    ptx::f2_split(ptx::f2_fma(a, s2, ptx::f2_mul(b, c2)), x[i + 8], x[i + 9]);
+                }
             }
         }
-        if (turn && !is_v) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int ia = kNext ? 2 * i : i, ib = kNext ? 2 * i + 1 : i + 8;
-                const float a = x[ia], b = x[ib];
-                x[ia] = a * cs[i] - b * sn[i];
-                x[ib] = b * cs[i] + a * sn[i];
+        if constexpr (!kCodes) {
+            if (write) {
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(dst_rows) + h * D;
+                *reinterpret_cast<uint4 *>(dst + at.c0) = pack8(x);
+                *reinterpret_cast<uint4 *>(dst + at.c1) = pack8(x + 8);
             }
-        }
-        const int g = is_v ? h - p.num_heads - p.num_kv_heads : h - p.num_heads; // KV head, if it is one
-        if (write && (!kInt8 || is_q)) { // a value's row goes as it is
-            __nv_bfloat16 *dst = is_q ? p.q_out + ((int64_t)t * p.num_heads + h) * D
-                                      : static_cast<__nv_bfloat16 *>(is_v ? p.v_cache : p.k_cache) +
-                                            ((int64_t)slot * p.num_kv_heads + g) * D;
-            *reinterpret_cast<uint4 *>(dst + c0) = is_v ? raw[u][0] : pack8(x);
-            *reinterpret_cast<uint4 *>(dst + c1) = is_v ? raw[u][1] : pack8(x + 8);
-        }
-        if constexpr (kInt8) {
+        } else {
             float a = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -195,40 +160,151 @@ __global__ void __launch_bounds__(kThreads) rope_store_kernel(const RopeParams p
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1)
                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            if (!is_q && write) {
-                const float scale = fmaxf(__fdiv_rn(a, 127.0f), 1e-8f);
-                const float rcp = __frcp_rn(scale);
-                uint32_t c[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    c[i] = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        c[i] |= (uint32_t)(quant::code_of(x[4 * i + e], scale, rcp) & 0xff) << (8 * e);
-                }
-                int8_t *dst = static_cast<int8_t *>(is_v ? p.v_cache : p.k_cache) + ((int64_t)slot * p.num_kv_heads + g) * D;
-                *reinterpret_cast<uint2 *>(dst + c0) = make_uint2(c[0], c[1]);
-                *reinterpret_cast<uint2 *>(dst + c1) = make_uint2(c[2], c[3]);
-                if (j == 0)
-                    (is_v ? p.v_scale : p.k_scale)[((int64_t)(slot / p.block_size) * p.num_kv_heads + g) * p.block_size +
-                                                   slot % p.block_size] = __float2half_rn(scale);
+            const float scale = fmaxf(__fdiv_rn(a, 127.0f), 1e-8f);
+            uint32_t c[4];
+            quant::codes_of_16(x, scale, __frcp_rn(scale), c);
+            if (write) {
+                int8_t *dst = static_cast<int8_t *>(dst_rows) + h * D;
+                *reinterpret_cast<uint2 *>(dst + at.c0) = make_uint2(c[0], c[1]);
+                *reinterpret_cast<uint2 *>(dst + at.c1) = make_uint2(c[2], c[3]);
+                if ((threadIdx.x & (kLanes - 1)) == 0)
+                    scales[h * scale_step] = __float2half_rn(scale);
             }
         }
+    };
+#pragma unroll 1
+    for (int h = 0; h < count; ++h) {
+        const uint4 now[2] = {raw[0][0], raw[0][1]};
+#pragma unroll
+        for (int u = 0; u + 1 < kRows; ++u) {
+            raw[u][0] = raw[u + 1][0];
+            raw[u][1] = raw[u + 1][1];
+        }
+        if (h + kRows < count)
+            load_row<D>(src, h + kRows, at, raw[kRows - 1]);
+        finish(h, now);
     }
 }
 
-template <int D, bool kInt8, bool kNext, bool kAxes, int kHeads>
-int launch(const RopeParams &p0, cudaStream_t stream)
+// kNext: pairs (2i, 2i + 1).  kAxes: more than one position per token.  kRows: rows in flight.
+template <int D, bool kInt8, bool kNext, bool kAxes, int kRows>
+__global__ void __launch_bounds__(kThreads, kRows > 1 ? 5 : 6) rope_store_kernel(const RopeParams p)
 {
+    constexpr int kLanes = D / 16; // of a row
+    ptx::launch_dependents();
+    ptx::grid_dependency_wait();
+    const int lane = threadIdx.x & 31, j = lane % kLanes;
+    const uint32_t warp = blockIdx.x * (uint32_t)(kThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t tokens = warp / (uint32_t)p.units;
+    int unit = (int)(warp - tokens * (uint32_t)p.units);
+    // every lane stays to the end: the groups of a warp shuffle together
+    const uint32_t token = tokens * (32 / kLanes) + lane / kLanes;
+    const int t = (int)min(token, (uint32_t)p.num_tokens - 1u);
+    bool live = token < (uint32_t)p.num_tokens;
+    const bool first = live && j == 0 && unit == 0; // flags a token's errors
+    // the unit's rows: heads h0 .. h0 + count - 1 of the queries, the keys or the values
+    const int kind = unit < p.q_units ? 0 : unit < p.q_units + p.kv_units ? 1 : 2;
+    unit -= kind == 0 ? 0 : kind == 1 ? p.q_units : p.q_units + p.kv_units;
+    const int h0 = unit * p.heads_per_unit;
+    const int count = min(p.heads_per_unit, (kind == 0 ? p.num_heads : p.num_kv_heads) - h0);
+
+    const int half = p.pairs;
+    Place at;
+    at.turn = 8 * j < half;
+    at.c0 = kNext || !at.turn ? 16 * j : 8 * j;
+    at.c1 = kNext || !at.turn ? at.c0 + 8 : at.c0 + half;
+
+    const int32_t slot = p.slots[t];
+    int pos[4];
+#pragma unroll
+    for (int a = 0; a < (kAxes ? 4 : 1); ++a)
+        pos[a] = a == 0 || a < p.num_axes ? p.positions[(int64_t)a * p.num_tokens + t] : 0;
+    // the first rows are on their way before the position is known
+    const __nv_bfloat16 *src = (kind == 0   ? p.q + (int64_t)t * p.q_stride
+                                : kind == 1 ? p.k + (int64_t)t * p.k_stride
+                                            : p.v + (int64_t)t * p.v_stride) +
+                               h0 * D;
+    uint4 raw[kRows][2];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+        if (u < count)
+            load_row<D>(src, u, at, raw[u]);
+
+    bool inside = true;
+#pragma unroll
+    for (int a = 0; a < (kAxes ? 4 : 1); ++a)
+        inside = inside && (uint32_t)pos[a] < (uint32_t)p.max_position;
+    if (!inside && first)
+        atomicOr(&g_rope_error, 2u);
+    live = live && inside;
+    float cs[8], sn[8];
+    if constexpr (!kAxes) {
+        if (at.turn && inside && kind != 2) {
+            const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos[0] * 2 * half + 8 * j);
+            *reinterpret_cast<float4 *>(cs) = row[0], *reinterpret_cast<float4 *>(cs + 4) = row[1];
+            *reinterpret_cast<float4 *>(sn) = row[half / 4], *reinterpret_cast<float4 *>(sn + 4) = row[half / 4 + 1];
+        }
+    } else {
+        if (at.turn && inside && kind != 2) {
+            // the rows of the axes that the lane's pairs turn on, 16 bytes at a time (one axis for most lanes)
+            const uint32_t bits = (uint32_t)(p.axis_bits[j >> 2] >> (16 * (j & 3))) & 0xffffu;
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const uint32_t x = bits ^ (0x5555u * a);
+                const uint32_t off = x | (x >> 1); // bit 2i is clear where pair i turns on axis a
+                if ((~off & 0x5555u) == 0u)
+                    continue;
+                const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos[a] * 2 * half + 8 * j);
+                float c8[8], s8[8];
+                *reinterpret_cast<float4 *>(c8) = row[0], *reinterpret_cast<float4 *>(c8 + 4) = row[1];
+                *reinterpret_cast<float4 *>(s8) = row[half / 4], *reinterpret_cast<float4 *>(s8 + 4) = row[half / 4 + 1];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const bool mine = ((off >> (2 * i)) & 1u) == 0u;
+                    cs[i] = mine ? c8[i] : cs[i];
+                    sn[i] = mine ? s8[i] : sn[i];
+                }
+            }
+        }
+    }
+    const bool stored = slot >= 0 && slot < p.num_slots;
+    if (!stored && slot != -1 && first && live)
+        atomicOr(&g_rope_error, 1u);
+
+    if (kind == 0) {
+        turn_rows<D, kInt8, kNext, kRows, 0>(src, raw, count, at, cs, sn, p.q_weight, p.eps,
+                                             p.q_out + ((int64_t)t * p.num_heads + h0) * D, nullptr, 0, live);
+        return;
+    }
+    const int64_t to = ((int64_t)(stored ? slot : 0) * p.num_kv_heads + h0) * D * (kInt8 ? 1 : 2);
+    const int64_t st = kInt8 && stored ? ((int64_t)(slot / p.block_size) * p.num_kv_heads + h0) * p.block_size +
+                                             slot % p.block_size
+                                       : 0;
+    if (kind == 1)
+        turn_rows<D, kInt8, kNext, kRows, 1>(src, raw, count, at, cs, sn, p.k_weight, p.eps,
+                                             static_cast<char *>(p.k_cache) + to, p.k_scale + st, p.block_size,
+                                             live && stored);
+    else
+        turn_rows<D, kInt8, kNext, kRows, 2>(src, raw, count, at, cs, sn, nullptr, p.eps,
+                                             static_cast<char *>(p.v_cache) + to, p.v_scale + st, p.block_size,
+                                             live && stored);
+}
+
+template <int D, bool kInt8, bool kNext, bool kAxes, int kRows>
+int launch(const RopeParams &p0, int heads_per_unit, cudaStream_t stream)
+{
+    constexpr int kTokens = 512 / D; // of a warp
     RopeParams p = p0;
-    p.units = (p.num_heads + 2 * p.num_kv_heads + kHeads - 1) / kHeads;
-    const int64_t groups = (int64_t)p.num_tokens * p.units, per = kThreads / (D / 16);
-    if (groups > INT32_MAX)
+    p.heads_per_unit = heads_per_unit;
+    p.q_units = (p.num_heads + heads_per_unit - 1) / heads_per_unit;
+    p.kv_units = (p.num_kv_heads + heads_per_unit - 1) / heads_per_unit;
+    p.units = p.q_units + 2 * p.kv_units;
+    const int64_t warps = ((int64_t)p.num_tokens + kTokens - 1) / kTokens * p.units;
+    if (warps > INT32_MAX)
         return fail(PA_ERR_UNSUPPORTED, "rope store: %d tokens of %d heads are too many for one call", p.num_tokens,
                     p.num_heads + 2 * p.num_kv_heads);
-    const int64_t blocks = (groups + per - 1) / per;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
@@ -236,7 +312,7 @@ int launch(const RopeParams &p0, cudaStream_t stream)
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_store_kernel<D, kInt8, kNext, kAxes, kHeads>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_store_kernel<D, kInt8, kNext, kAxes, kRows>, p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(PA_ERR_CUDA, "rope store launch: %s", cudaGetErrorString(e));
@@ -247,9 +323,13 @@ int launch(const RopeParams &p0, cudaStream_t stream)
 template <int D, bool kInt8, bool kNext, bool kAxes>
 int launch_heads(const RopeParams &p, cudaStream_t stream)
 {
-    // a prompt's tokens are many: four rows per group, whose loads are in flight together and share cos and sin
+    // A prompt's tokens are many: four heads share their cos and sin.  bf16 is bound by the loads' latency and keeps all
+    // four rows in flight (16384 tokens of 28 + 8 heads: 52.6 us, 59.8 with one), INT8 by instructions, and has more warps
+    // with one (5000 tokens of 16 + 16: 17.9 us, 20.0 with four).  A decode step's rows each have a warp's lanes at
+    // once (8 tokens of 16 + 16: 1.85 us, 2.3 with four heads a warp).
     const int64_t rows = (int64_t)p.num_tokens * (p.num_heads + 2 * p.num_kv_heads);
-    return rows >= 65536 ? launch<D, kInt8, kNext, kAxes, 4>(p, stream) : launch<D, kInt8, kNext, kAxes, 1>(p, stream);
+    return rows >= 65536 ? launch<D, kInt8, kNext, kAxes, kInt8 ? 1 : 4>(p, 4, stream)
+                         : launch<D, kInt8, kNext, kAxes, 1>(p, 1, stream);
 }
 
 template <int D, bool kInt8>
