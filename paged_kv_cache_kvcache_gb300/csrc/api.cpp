@@ -114,6 +114,9 @@ static int rope_store(const char *fn, const pa_dims *dims, const pa_rope *rope, 
         return fail(PA_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1, max_position positive, eps finite and >= 0", fn);
     if (num_tokens < 0)
         return fail(PA_ERR_INVALID_ARG, "num_tokens < 0");
+    if ((int64_t)num_tokens * (dims->num_heads + 2 * dims->num_kv_heads) > INT32_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "%s: %d tokens of %d heads exceed an int32", fn, num_tokens,
+                    dims->num_heads + 2 * dims->num_kv_heads);
     if (num_tokens == 0)
         return PA_OK;
     if (!r.cos_sin || !q || !k || !v || !positions || !slot_mapping || !q_out || !k_cache || !v_cache ||

@@ -19,6 +19,8 @@
 // that are not seen is not read: those rows are zeros in shared memory, whatever the cache has there.
 // Weights need M and L before any of them can be formed: the scores s' wait in the workspace (16 keys of one
 // head group are 512 contiguous bytes) until the cluster has met.
+#include <algorithm>
+
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -150,13 +152,21 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
         return 16 * (v < sink_chunks ? v : v + skip);
     };
     auto seen = [&](int key) { return (key >= lo && key < ctx) || key < sink_end; };
+    auto whole = [&](int key0) { return (key0 >= lo && key0 + 16 <= ctx) || key0 + 16 <= sink_end; };
 
     const uint32_t wbase = ptx::smem_u32(smem) + warp * L::kWarpBytes;
     const uint32_t sc_base = ptx::smem_u32(smem) + L::kScaleOff + warp * kStages * 64;
     int blk_cache = 0;
 
-    // chunk i of this warp into stage i % kStages
-    auto issue = [&](int i) {
+    // Chunk i of this warp into stage st.  A lane copies vector v0 of the rows t0, t0 + kRowsPer, ...
+    constexpr int kVec = L::kRowBytes / 16;     // 16-byte vectors per row
+    constexpr int kRowsPer = 32 / kVec;         // rows per instruction
+    const int t0 = lane / kVec, v0 = lane % kVec;
+    const size_t token_bytes = (size_t)Hkv * L::kRowBytes;
+    const size_t lane_off = t0 * token_bytes + (size_t)g * L::kRowBytes + v0 * 16;
+    const char *k_lane = static_cast<const char *>(p.k_cache) + lane_off;
+    const char *v_lane = static_cast<const char *>(p.v_cache) + lane_off;
+    auto issue = [&](int i, int st) {
         if ((i & 31) == 0) { // the block ids of chunks i .. i + 31, one per lane
             blk_cache = 0;
             if (i + lane < my_n) {
@@ -169,26 +179,34 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
         }
         const int phys = __shfl_sync(0xffffffffu, blk_cache, i & 31);
         const int key0 = first_key(i);
-        const bool inside = phys >= 0;
-        const int64_t row0 = (int64_t)(inside ? phys : 0) * bs + (key0 & (bs - 1));
-        const uint32_t sbase = wbase + (i % kStages) * L::kStageBytes;
-        constexpr int kVec = L::kRowBytes / 16; // 16-byte vectors per row
+        const uint32_t sbase = wbase + st * L::kStageBytes;
+        const int64_t row0 = (int64_t)phys * bs + (key0 & (bs - 1));
+        const char *kp = k_lane + row0 * token_bytes, *vp = v_lane + row0 * token_bytes;
+        if (phys >= 0 && whole(key0)) {
 #pragma unroll
-        for (int x = 0; x < kVec / 2; ++x) {
-            const int e = x * 32 + lane;
-            const int t = e / kVec, v = e % kVec;
-            const bool valid = inside && seen(key0 + t);
-            const size_t off = ((size_t)(row0 + t) * Hkv + g) * L::kRowBytes + v * 16;
-            const uint32_t dst = sbase + swz<L::kRowBytes>(t, v);
-            ptx::cp_async_16(dst, static_cast<const char *>(p.k_cache) + (valid ? off : 0), valid ? 16u : 0u);
-            ptx::cp_async_16(dst + L::kChunkBytes, static_cast<const char *>(p.v_cache) + (valid ? off : 0),
-                             valid ? 16u : 0u);
+            for (int x = 0; x < 16 / kRowsPer; ++x) {
+                const uint32_t dst = sbase + swz<L::kRowBytes>(x * kRowsPer + t0, v0);
+                ptx::cp_async_16(dst, kp + x * kRowsPer * token_bytes, 16u);
+                ptx::cp_async_16(dst + L::kChunkBytes, vp + x * kRowsPer * token_bytes, 16u);
+            }
+        } else { // rows that are not seen, or of a block outside the pool, are zeros
+#pragma unroll
+            for (int x = 0; x < 16 / kRowsPer; ++x) {
+                const int t = x * kRowsPer + t0;
+                const bool valid = phys >= 0 && seen(key0 + t);
+                const uint32_t dst = sbase + swz<L::kRowBytes>(t, v0);
+                ptx::cp_async_16(dst, valid ? kp + x * kRowsPer * token_bytes : static_cast<const char *>(p.k_cache),
+                                 valid ? 16u : 0u);
+                ptx::cp_async_16(dst + L::kChunkBytes,
+                                 valid ? vp + x * kRowsPer * token_bytes : static_cast<const char *>(p.v_cache),
+                                 valid ? 16u : 0u);
+            }
         }
         if constexpr (kInt8) {
             if (lane < 4) { // 16 fp16 scales of K, 16 of V (a block outside the pool: zeros)
-                const size_t si = ((size_t)(inside ? phys : 0) * Hkv + g) * bs + (key0 & (bs - 1)) + (lane & 1) * 8;
-                ptx::cp_async_16(sc_base + (i % kStages) * 64 + lane * 16, (lane < 2 ? p.k_scale : p.v_scale) + si,
-                                 inside ? 16u : 0u);
+                const size_t si = ((size_t)max(phys, 0) * Hkv + g) * bs + (key0 & (bs - 1)) + (lane & 1) * 8;
+                ptx::cp_async_16(sc_base + st * 64 + lane * 16, (lane < 2 ? p.k_scale : p.v_scale) + si,
+                                 phys >= 0 ? 16u : 0u);
             }
         }
     };
@@ -196,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
         if (s < my_n)
-            issue(s);
+            issue(s, s);
         ptx::cp_async_commit();
     }
 
@@ -241,15 +259,15 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
 
     float *raw = kWeights ? p.raw + (size_t)unit * room * p.raw_heads : nullptr;
 
-    for (int i = 0; i < my_n; ++i) {
+    for (int i = 0, st = 0; i < my_n; ++i, st = st + 1 < kStages ? st + 1 : 0) {
         __syncwarp();
         if (i + kStages - 1 < my_n)
-            issue(i + kStages - 1);
+            issue(i + kStages - 1, st > 0 ? st - 1 : kStages - 1);
         ptx::cp_async_commit();
         ptx::cp_async_wait<kStages - 1>();
         __syncwarp();
 
-        const uint32_t kb = wbase + (i % kStages) * L::kStageBytes;
+        const uint32_t kb = wbase + st * L::kStageBytes;
         const uint32_t vb = kb + L::kChunkBytes;
         const int key0 = first_key(i);
 
@@ -277,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
                 for (int nt = 0; nt < NT; ++nt)
                     ptx::mma_16816_f16(sc[nt], a0, a1, a2, a3, qf[nt][kk][0], qf[nt][kk][1]);
             }
-            const uint32_t sb = sc_base + (i % kStages) * 64;
+            const uint32_t sb = sc_base + st * 64;
             ks0 *= lds_half(sb + 2 * r);
             ks1 *= lds_half(sb + 2 * (r + 8));
             vs0 = lds_half(sb + 32 + 2 * r);
@@ -293,18 +311,18 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
             }
         }
 
-        const bool v0 = seen(key0 + r), v1 = seen(key0 + r + 8);
+        const bool all = whole(key0), seen0 = all || seen(key0 + r), seen1 = all || seen(key0 + r + 8);
         if constexpr (kInt8) { // the scales of keys that are not seen may be anything
-            vs0 = v0 ? vs0 : 0.f;
-            vs1 = v1 ? vs1 : 0.f;
+            vs0 = seen0 ? vs0 : 0.f;
+            vs1 = seen1 ? vs1 : 0.f;
         }
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float s0 = v0 ? sc[nt][0] * ks0 : -INFINITY;
-            const float s1 = v0 ? sc[nt][1] * ks0 : -INFINITY;
-            const float s2 = v1 ? sc[nt][2] * ks1 : -INFINITY;
-            const float s3 = v1 ? sc[nt][3] * ks1 : -INFINITY;
+            const float s0 = seen0 ? sc[nt][0] * ks0 : -INFINITY;
+            const float s1 = seen0 ? sc[nt][1] * ks0 : -INFINITY;
+            const float s2 = seen1 ? sc[nt][2] * ks1 : -INFINITY;
+            const float s3 = seen1 ? sc[nt][3] * ks1 : -INFINITY;
             if constexpr (kWeights) {
                 const int h0 = nt * 8 + 2 * c;
                 float *at = raw + (size_t)(key0 + r) * p.raw_heads + h0;
@@ -452,7 +470,10 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
             sum += e * mrg_l[w * H8 + hl];
             o += e * mrg_o[(size_t)(w * H8 + hl) * L::kRow + d];
         }
-        part_o[idx] = o;
+        if (ctas == 1) // no weight at all: 0, or NaN where a value is
+            p.out[((size_t)b * Hq + (size_t)g * G) * D + idx] = __float2bfloat16_rn(sum != 0.f ? o / sum : o);
+        else
+            part_o[idx] = o;
         if (d == 0) {
             part_m[hl] = M;
             part_l[hl] = sum;
@@ -460,12 +481,14 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
     }
     if (ctas > 1)
         cluster.sync();
-    else
+    else if (kWeights)
         __syncthreads();
+    else
+        return;
 
     // the cluster's: each CTA a share of the output
     auto of = [&](float *at, int cta) { return ctas > 1 ? cluster.map_shared_rank(at, cta) : at; };
-    for (int idx = rank * kThreads + (int)threadIdx.x; idx < G * D; idx += ctas * kThreads) {
+    for (int idx = rank * kThreads + (int)threadIdx.x; ctas > 1 && idx < G * D; idx += ctas * kThreads) {
         const int hl = idx / D;
         float M = -INFINITY;
         for (int x = 0; x < ctas; ++x)
@@ -477,7 +500,6 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
             sum += e * of(part_l, x)[hl];
             o += e * of(part_o, x)[idx];
         }
-        // no weight at all: 0, or NaN where a value is
         p.out[((size_t)b * Hq + (size_t)g * G) * D + idx] = __float2bfloat16_rn(sum != 0.f ? o / sum : o);
     }
     if constexpr (kWeights) {
@@ -567,13 +589,15 @@ int launch_decode_window(const WindowArgs &a, void *stream)
     p.window = a.window, p.sinks = a.sinks;
     p.decay = a.decay, p.scores = a.scores, p.scores_out = a.scores_out, p.raw = a.raw;
     p.raw_heads = window_raw_heads(a.dims);
-    // CTAs per (sequence, KV head): up to eight while the grid is small, none without a chunk for each warp
+    // CTAs per (sequence, KV head): as many as run at once (more than one wave of clusters costs more than it gives:
+    // 200 sequences of 4 KV heads and 1000 keys took 66.8 us with one CTA each, 88.2 with two; 19 of 16384 keys 141
+    // with one, 100 with two), up to eight, none without a chunk of keys for each of its warps.
     const int64_t units = (int64_t)a.num_seqs * a.dims.num_kv_heads;
     const int64_t room = (int64_t)a.max_blocks_per_seq * a.dims.block_size;
     const int64_t keys = a.raw ? room : room < (int64_t)a.window + a.sinks ? room : (int64_t)a.window + a.sinks;
-    int ctas = 1;
-    while (ctas < 8 && units * ctas < 4 * sms && keys > ctas * kWarps * 16)
-        ctas *= 2;
+    const int64_t slots = (int64_t)sms * (!a.k_scale ? 2 : p.group > 8 ? 3 : 4); // (the kernels' launch bounds)
+    int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(8, slots / units));
+    ctas = (int)std::min<int64_t>(ctas, (keys + kWarps * 16 - 1) / (kWarps * 16));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool two = p.group > 8;
     if (a.dims.head_dim == 128)

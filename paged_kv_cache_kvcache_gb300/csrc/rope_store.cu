@@ -299,10 +299,7 @@ int launch(const RopeParams &p0, int heads_per_unit, cudaStream_t stream)
     p.q_units = (p.num_heads + heads_per_unit - 1) / heads_per_unit;
     p.kv_units = (p.num_kv_heads + heads_per_unit - 1) / heads_per_unit;
     p.units = p.q_units + 2 * p.kv_units;
-    const int64_t warps = ((int64_t)p.num_tokens + kTokens - 1) / kTokens * p.units;
-    if (warps > INT32_MAX)
-        return fail(PA_ERR_UNSUPPORTED, "rope store: %d tokens of %d heads are too many for one call", p.num_tokens,
-                    p.num_heads + 2 * p.num_kv_heads);
+    const int64_t warps = ((int64_t)p.num_tokens + kTokens - 1) / kTokens * p.units; // (fewer than heads: an int32)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
     cfg.blockDim = dim3(kThreads);

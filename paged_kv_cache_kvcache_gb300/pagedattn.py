@@ -200,7 +200,7 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
-_BF16, _FP16, _INT8 = torch.bfloat16, torch.float16, torch.int8
+_BF16, _FP16, _INT8, _INT32, _FP32 = torch.bfloat16, torch.float16, torch.int8, torch.int32, torch.float32
 _device = _cur_device if _cur_device is not None else torch.cuda.current_device
 
 
@@ -453,42 +453,37 @@ class Rope:
         self.struct = pa_rope(cos_sin.shape[1], 1 if interleaved else 0, self.axes, cos_sin.shape[0], float(eps),
                               (ctypes.c_uint8 * 64)(*axis), _ptr(cos_sin), _ptr(q_weight), _ptr(k_weight))
         self.ref = ctypes.byref(self.struct)
+        # what the calls go by: the dims, and of each tensor the shape behind its tokens and the strides
+        self.dims = pa_dims.from_buffer_copy(dims)
+        self.dims_ref, self.dims_bytes = ctypes.byref(self.dims), bytes(dims)
+        self.heads = (dims.num_heads, dims.num_kv_heads, dims.head_dim)
+        self.rows = dims.num_blocks * dims.block_size * dims.num_kv_heads
 
 
-def _rope_call(dims, rope, q, k, v, positions, slot_mapping, q_out, caches, scales):
-    """The arguments of pa_rope_store(_int8) between `rope` and the caches; refuses what the kernel could not read."""
-    dev, n = _device(), q_out.shape[0]
-    hq, hkv, d = dims.num_heads, dims.num_kv_heads, dims.head_dim
-    cache = _INT8 if scales else _BF16
-    rows = dims.num_blocks * dims.block_size * hkv
-    if not (rope.device == dev and q.dtype is k.dtype is v.dtype is q_out.dtype is _BF16
-            and q.shape == q_out.shape == (n, hq, d) and k.shape == v.shape == (n, hkv, d)
-            and q_out.is_contiguous() and q.stride()[1:] == k.stride()[1:] == v.stride()[1:] == (d, 1)
-            and positions.dtype is slot_mapping.dtype is torch.int32
-            and positions.is_contiguous() and slot_mapping.is_contiguous()
-            and positions.numel() == n * rope.axes and slot_mapping.numel() == n):
-        for what, t, heads in (("q", q, hq), ("k", k, hkv), ("v", v, hkv), ("q_out", q_out, hq)):
-            if t.dtype is not _BF16 or tuple(t.shape) != (n, heads, d):
-                raise ValueError(f"{what} must be bfloat16 [{n}, {heads}, {d}], got {t.dtype} {tuple(t.shape)}")
-            if t.numel() and (t.stride(2) != 1 or heads > 1 and t.stride(1) != d or t is q_out and not t.is_contiguous()):
-                raise ValueError(f"{what}: a token's heads must be contiguous (in q_out the tokens too), got strides "
-                                 f"{t.stride()}")
-        if rope.device != dev:
-            raise ValueError(f"the rope is on cuda:{rope.device}, the current device is cuda:{dev}")
-        _int32(positions, "positions", n * rope.axes, dev)
-        _int32(slot_mapping, "slot_mapping", n, dev)
-    for t in (q, k, v, positions, slot_mapping, q_out, *caches, *scales):
+def _rope_refuse(dims, rope, q, k, v, positions, slot_mapping, q_out, caches, scales):
+    """Why a call's tensors are refused (the calls test for it themselves)."""
+    if bytes(dims) != rope.dims_bytes:
+        raise ValueError("the rope was made with other dims")
+    dev, n = _device(), slot_mapping.numel()
+    hq, hkv, d = rope.heads
+    if rope.device != dev:
+        raise ValueError(f"the rope is on cuda:{rope.device}, the current device is cuda:{dev}")
+    for what, t, heads in (("q", q, hq), ("k", k, hkv), ("v", v, hkv), ("q_out", q_out, hq)):
+        if t.dtype is not _BF16 or tuple(t.shape) != (n, heads, d):
+            raise ValueError(f"{what} must be bfloat16 [{n}, {heads}, {d}], got {t.dtype} {tuple(t.shape)}")
+        if t.numel() and (t.stride(2) != 1 or heads > 1 and t.stride(1) != d or t is q_out and not t.is_contiguous()):
+            raise ValueError(f"{what}: a token's heads must be contiguous (in q_out the tokens too), got strides "
+                             f"{t.stride()}")
+    _int32(positions, "positions", n * rope.axes, dev)
+    _int32(slot_mapping, "slot_mapping", n, dev)
+    for t in (q, k, v, q_out, *caches, *scales):
         if t.get_device() != dev:
             raise _elsewhere(t, dev)
-    for what, t, dtype, least in (("k_cache", caches[0], cache, rows * d), ("v_cache", caches[1], cache, rows * d),
-                                  *(((("k_scale", scales[0], _FP16, rows), ("v_scale", scales[1], _FP16, rows)))
-                                    if scales else ())):
+    cache = _INT8 if scales else _BF16
+    for what, t, dtype, least in zip(("k_cache", "v_cache", "k_scale", "v_scale"), (*caches, *scales),
+                                     (cache, cache, _FP16, _FP16), (rope.rows * d, rope.rows * d, rope.rows, rope.rows)):
         if t.dtype is not dtype or t.numel() < least or not t.is_contiguous():
             raise ValueError(f"{what} must be contiguous {dtype} of {least} values, got {t.dtype} {tuple(t.shape)}")
-    row = hkv * d
-    strides = (q.stride(0), k.stride(0), v.stride(0)) if n > 1 else (hq * d, row, row)
-    return (q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, positions.data_ptr(), slot_mapping.data_ptr(), n,
-            q_out.data_ptr(), *(t.data_ptr() for t in caches), *(t.data_ptr() for t in scales))
 
 
 def pa_rope_store(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q_out, k_cache, v_cache, stream=None):
@@ -497,8 +492,25 @@ def pa_rope_store(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q
     q [tokens, Hq, D], k, v [tokens, Hkv, D]: bf16, a token's heads contiguous (parts of one projection's output);
     positions: int32 [tokens], or [axes, tokens].
     """
-    args = _rope_call(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), ())
-    rc = (_lib or lib()).pa_rope_store(ctypes.byref(dims), rope.ref, *args, _stream_of(rope.device, stream))
+    n, dev, (hq, hkv, d) = slot_mapping.numel(), rope.device, rope.heads
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    kv = k.shape
+    if not (dev == _device() == q.get_device() == k.get_device() == v.get_device() == positions.get_device()
+            == slot_mapping.get_device() == q_out.get_device() == k_cache.get_device() == v_cache.get_device()
+            and q.dtype is k.dtype is v.dtype is q_out.dtype is k_cache.dtype is v_cache.dtype is _BF16
+            and positions.dtype is slot_mapping.dtype is _INT32
+            and q.shape == (n, hq, d) == q_out.shape and kv == (n, hkv, d) and kv == v.shape
+            and qs[1] == ks[1] == vs[1] == d and qs[2] == ks[2] == vs[2] == 1
+            and q_out.is_contiguous() and positions.is_contiguous() and slot_mapping.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and positions.numel() == n * rope.axes
+            and k_cache.numel() >= rope.rows * d <= v_cache.numel() and bytes(dims) == rope.dims_bytes):
+        _rope_refuse(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), ())
+    row = hkv * d
+    rc = (_lib or lib()).pa_rope_store(
+        rope.dims_ref, rope.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0] if n > 1 else hq * d,
+        ks[0] if n > 1 else row, vs[0] if n > 1 else row, positions.data_ptr(), slot_mapping.data_ptr(), n,
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
     if rc != PA_OK:
         _check(rc, "pa_rope_store")
 
@@ -506,8 +518,28 @@ def pa_rope_store(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q
 def pa_rope_store_int8(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q_out, k_cache, v_cache, k_scale,
                        v_scale, stream=None):
     """pa_rope_store into an INT8 cache."""
-    args = _rope_call(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), (k_scale, v_scale))
-    rc = (_lib or lib()).pa_rope_store_int8(ctypes.byref(dims), rope.ref, *args, _stream_of(rope.device, stream))
+    n, dev, (hq, hkv, d) = slot_mapping.numel(), rope.device, rope.heads
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    kv = k.shape
+    if not (dev == _device() == q.get_device() == k.get_device() == v.get_device() == positions.get_device()
+            == slot_mapping.get_device() == q_out.get_device() == k_cache.get_device() == v_cache.get_device()
+            == k_scale.get_device() == v_scale.get_device()
+            and q.dtype is k.dtype is v.dtype is q_out.dtype is _BF16 and k_cache.dtype is v_cache.dtype is _INT8
+            and k_scale.dtype is v_scale.dtype is _FP16 and positions.dtype is slot_mapping.dtype is _INT32
+            and q.shape == (n, hq, d) == q_out.shape and kv == (n, hkv, d) and kv == v.shape
+            and qs[1] == ks[1] == vs[1] == d and qs[2] == ks[2] == vs[2] == 1
+            and q_out.is_contiguous() and positions.is_contiguous() and slot_mapping.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous() and positions.numel() == n * rope.axes
+            and k_cache.numel() >= rope.rows * d <= v_cache.numel() and k_scale.numel() >= rope.rows <= v_scale.numel()
+            and bytes(dims) == rope.dims_bytes):
+        _rope_refuse(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), (k_scale, v_scale))
+    row = hkv * d
+    rc = (_lib or lib()).pa_rope_store_int8(
+        rope.dims_ref, rope.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0] if n > 1 else hq * d,
+        ks[0] if n > 1 else row, vs[0] if n > 1 else row, positions.data_ptr(), slot_mapping.data_ptr(), n,
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        _raw_stream(dev) if stream is None and _raw_stream else _stream(stream))
     if rc != PA_OK:
         _check(rc, "pa_rope_store_int8")
 
@@ -768,38 +800,68 @@ def pa_pool_compact(dims: pa_dims, pool: PagePool, remap, block_tables_out=None,
         _check(rc, "pa_pool_compact")
 
 
-def _bounded_call(dims, q, caches, scales, block_tables, context_lens, table_rows, out):
-    """The arguments of a decode over a bounded cache from q to max_blocks_per_seq; refuses what a kernel could not read."""
+def _bounded_refuse(dims, q, caches, scales, block_tables, context_lens, table_rows, out):
+    """Why the tensors of a decode over a bounded cache are refused (the calls test for it in one expression)."""
     dev, n = _device(), q.shape[0]
     hq, hkv, d = dims.num_heads, dims.num_kv_heads, dims.head_dim
-    rows, width = block_tables.shape
+    rows = block_tables.shape[0]
     cache = _INT8 if scales else _BF16
     page = dims.num_blocks * dims.block_size * hkv
-    k, v = caches
-    if not (dev == q.get_device() == out.get_device() == k.get_device() == v.get_device() == block_tables.get_device()
-            == context_lens.get_device()
-            and q.dtype is out.dtype is _BF16 and k.dtype is v.dtype is cache
-            and q.shape == out.shape == (n, hq, d)
-            and block_tables.dtype is context_lens.dtype is torch.int32 and context_lens.shape == (rows,)
-            and q.is_contiguous() and out.is_contiguous() and k.is_contiguous() and v.is_contiguous()
-            and block_tables.is_contiguous() and context_lens.is_contiguous()
-            and k.numel() >= page * d <= v.numel() and (table_rows is not None or n <= rows)):
-        for what, t in (("q", q), ("out", out)):
-            if tuple(t.shape) != (n, hq, d):
-                raise ValueError(f"{what} must be [{n}, {hq}, {d}], got {tuple(t.shape)}")
-        _int32(block_tables, "block_tables", None, dev)
-        _int32(context_lens, "context_lens", rows, dev)
-        _refuse(dev, (q, out, k, v), (("q", q, _BF16, 0), ("out", out, _BF16, 0), ("k_cache", k, cache, page * d),
-                                      ("v_cache", v, cache, page * d)))
-        raise ValueError(f"{n} sequences, {rows} rows of the block table")
+    for what, t in (("q", q), ("out", out)):
+        if tuple(t.shape) != (n, hq, d):
+            raise ValueError(f"{what} must be [{n}, {hq}, {d}], got {tuple(t.shape)}")
+    _int32(block_tables, "block_tables", None, dev)
+    _int32(context_lens, "context_lens", rows, dev)
     if table_rows is not None:
         _int32(table_rows, "table_rows", n, dev)
-    for what, t in zip(("k_scale", "v_scale"), scales):
-        if t.dtype is not _FP16 or t.numel() < page or not t.is_contiguous() or t.get_device() != dev:
-            raise ValueError(f"{what} must be contiguous {_FP16} of {page} values on cuda:{dev}, got {t.dtype} "
-                             f"{tuple(t.shape)} on {t.device}")
-    return (q.data_ptr(), k.data_ptr(), v.data_ptr(), *[t.data_ptr() for t in scales], context_lens.data_ptr(),
-            block_tables.data_ptr(), None if table_rows is None else table_rows.data_ptr(), n, rows, width)
+    elif n > rows:
+        raise ValueError(f"{n} sequences, {rows} rows of the block table")
+    _refuse(dev, (q, out, *caches, *scales),
+            (("q", q, _BF16, 0), ("out", out, _BF16, 0), ("k_cache", caches[0], cache, page * d),
+             ("v_cache", caches[1], cache, page * d),
+             *((what, t, _FP16, page) for what, t in zip(("k_scale", "v_scale"), scales))))
+
+
+def _bounded_call(dims, q, k, v, block_tables, context_lens, table_rows, out):
+    """The arguments of a decode over a bounded bf16 cache from q to max_blocks_per_seq."""
+    dev, shape = _device(), q.shape
+    n = shape[0]
+    rows, width = block_tables.shape
+    least = dims.num_blocks * dims.block_size * dims.num_kv_heads * dims.head_dim
+    if not (dev == q.get_device() == out.get_device() == k.get_device() == v.get_device() == block_tables.get_device()
+            == context_lens.get_device()
+            and q.dtype is out.dtype is k.dtype is v.dtype is _BF16 and block_tables.dtype is context_lens.dtype is _INT32
+            and shape == (n, dims.num_heads, dims.head_dim) and shape == out.shape and context_lens.numel() == rows
+            and q.is_contiguous() and out.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+            and block_tables.is_contiguous() and context_lens.is_contiguous() and k.numel() >= least <= v.numel()
+            and (n <= rows if table_rows is None else table_rows.get_device() == dev and table_rows.dtype is _INT32
+                 and table_rows.numel() == n and table_rows.is_contiguous())):
+        _bounded_refuse(dims, q, (k, v), (), block_tables, context_lens, table_rows, out)
+    return (ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), context_lens.data_ptr(), block_tables.data_ptr(),
+            None if table_rows is None else table_rows.data_ptr(), n, rows, width)
+
+
+def _bounded_call_int8(dims, q, k, v, ks, vs, block_tables, context_lens, table_rows, out):
+    """The same over an INT8 cache."""
+    dev, shape = _device(), q.shape
+    n = shape[0]
+    rows, width = block_tables.shape
+    page = dims.num_blocks * dims.block_size * dims.num_kv_heads
+    least = page * dims.head_dim
+    if not (dev == q.get_device() == out.get_device() == k.get_device() == v.get_device() == ks.get_device()
+            == vs.get_device() == block_tables.get_device() == context_lens.get_device()
+            and q.dtype is out.dtype is _BF16 and k.dtype is v.dtype is _INT8 and ks.dtype is vs.dtype is _FP16
+            and block_tables.dtype is context_lens.dtype is _INT32
+            and shape == (n, dims.num_heads, dims.head_dim) and shape == out.shape and context_lens.numel() == rows
+            and q.is_contiguous() and out.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+            and ks.is_contiguous() and vs.is_contiguous() and block_tables.is_contiguous() and context_lens.is_contiguous()
+            and k.numel() >= least <= v.numel() and ks.numel() >= page <= vs.numel()
+            and (n <= rows if table_rows is None else table_rows.get_device() == dev and table_rows.dtype is _INT32
+                 and table_rows.numel() == n and table_rows.is_contiguous())):
+        _bounded_refuse(dims, q, (k, v), (ks, vs), block_tables, context_lens, table_rows, out)
+    return (ctypes.byref(dims), q.data_ptr(), k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+            context_lens.data_ptr(), block_tables.data_ptr(), None if table_rows is None else table_rows.data_ptr(), n,
+            rows, width)
 
 
 def pa_decode_window(dims: pa_dims, q, k_cache, v_cache, block_tables, context_lens, window: int, sinks: int,
@@ -809,9 +871,9 @@ def pa_decode_window(dims: pa_dims, q, k_cache, v_cache, block_tables, context_l
     block_tables int32 [rows, width] and context_lens int32 [rows] (a PagePool's, for instance); sequence b is row
     ``table_rows[b]`` of them, or row b.
     """
-    args = _bounded_call(dims, q, (k_cache, v_cache), (), block_tables, context_lens, table_rows, out)
-    rc = (_lib or lib()).pa_decode_window(ctypes.byref(dims), *args, window, sinks, scale, out.data_ptr(),
-                                          _stream_of(q.get_device(), stream))
+    args = _bounded_call(dims, q, k_cache, v_cache, block_tables, context_lens, table_rows, out)
+    rc = (_lib or lib()).pa_decode_window(*args, window, sinks, scale, out.data_ptr(),
+                                          _stream_of(_device(), stream))
     if rc != PA_OK:
         _check(rc, "pa_decode_window")
 
@@ -819,9 +881,9 @@ def pa_decode_window(dims: pa_dims, q, k_cache, v_cache, block_tables, context_l
 def pa_decode_window_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, window: int,
                           sinks: int, scale: float, out, table_rows=None, stream=None):
     """pa_decode_window over an INT8 cache."""
-    args = _bounded_call(dims, q, (k_cache, v_cache), (k_scale, v_scale), block_tables, context_lens, table_rows, out)
-    rc = (_lib or lib()).pa_decode_window_int8(ctypes.byref(dims), *args, window, sinks, scale, out.data_ptr(),
-                                               _stream_of(q.get_device(), stream))
+    args = _bounded_call_int8(dims, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, table_rows, out)
+    rc = (_lib or lib()).pa_decode_window_int8(*args, window, sinks, scale, out.data_ptr(),
+                                               _stream_of(_device(), stream))
     if rc != PA_OK:
         _check(rc, "pa_decode_window_int8")
 
@@ -834,19 +896,29 @@ def weights_workspace(dims: pa_dims, num_seqs: int, max_blocks: int, device="cud
     return torch.empty(max(n.value, 256), dtype=torch.uint8, device=device)
 
 
-def _score_args(dims, block_tables, scores, scores_out, workspace):
-    """(scores, scores_out, workspace, its bytes) of a call on these tables."""
-    scores_out = scores if scores_out is None else scores_out
+def _score_refuse(dims, block_tables, scores, scores_out, workspace):
+    """Why a call's scores or workspace are refused."""
     shape = (block_tables.shape[0], dims.num_kv_heads, block_tables.shape[1] * dims.block_size)
     dev = block_tables.get_device()
     for what, t in (("scores", scores), ("scores_out", scores_out)):
-        if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        if t.dtype is not _FP32 or tuple(t.shape) != shape or not t.is_contiguous() or t.get_device() != dev:
             raise ValueError(f"{what} must be contiguous float32 {shape} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} "
                              f"on {t.device}")
+    raise ValueError(f"the workspace must be contiguous, on cuda:{dev}")
+
+
+def _score_args(dims, block_tables, scores, scores_out, workspace):
+    """(scores, scores_out) of a call on these tables, and (workspace, its bytes) where it needs one."""
+    scores_out = scores if scores_out is None else scores_out
+    dev, shape = block_tables.get_device(), scores.shape
+    rows, width = block_tables.shape
+    if not (scores.dtype is scores_out.dtype is _FP32 and scores.get_device() == scores_out.get_device() == dev
+            and shape == (rows, dims.num_kv_heads, width * dims.block_size) and shape == scores_out.shape
+            and scores.is_contiguous() and scores_out.is_contiguous()
+            and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous())):
+        _score_refuse(dims, block_tables, scores, scores_out, workspace)
     if workspace is None:
         return scores.data_ptr(), scores_out.data_ptr()
-    if workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be contiguous, on cuda:{dev}")
     return scores.data_ptr(), scores_out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -857,10 +929,10 @@ def pa_decode_weights(dims: pa_dims, q, k_cache, v_cache, block_tables, context_
     scores: float32 [rows, Hkv, width * block_size]; scores_out = decay * scores + the weights, summed over each KV
     head's query heads (None: in place).
     """
-    args = _bounded_call(dims, q, (k_cache, v_cache), (), block_tables, context_lens, table_rows, out)
+    args = _bounded_call(dims, q, k_cache, v_cache, block_tables, context_lens, table_rows, out)
     s, so, ws, n = _score_args(dims, block_tables, scores, scores_out, workspace)
-    rc = (_lib or lib()).pa_decode_weights(ctypes.byref(dims), *args, scale, decay, s, so, out.data_ptr(), ws, n,
-                                           _stream_of(q.get_device(), stream))
+    rc = (_lib or lib()).pa_decode_weights(*args, scale, decay, s, so, out.data_ptr(), ws, n,
+                                           _stream_of(_device(), stream))
     if rc != PA_OK:
         _check(rc, "pa_decode_weights")
 
@@ -868,10 +940,10 @@ def pa_decode_weights(dims: pa_dims, q, k_cache, v_cache, block_tables, context_
 def pa_decode_weights_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale: float,
                            out, scores, workspace, decay: float = 1.0, scores_out=None, table_rows=None, stream=None):
     """pa_decode_weights over an INT8 cache."""
-    args = _bounded_call(dims, q, (k_cache, v_cache), (k_scale, v_scale), block_tables, context_lens, table_rows, out)
+    args = _bounded_call_int8(dims, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, table_rows, out)
     s, so, ws, n = _score_args(dims, block_tables, scores, scores_out, workspace)
-    rc = (_lib or lib()).pa_decode_weights_int8(ctypes.byref(dims), *args, scale, decay, s, so, out.data_ptr(), ws, n,
-                                                _stream_of(q.get_device(), stream))
+    rc = (_lib or lib()).pa_decode_weights_int8(*args, scale, decay, s, so, out.data_ptr(), ws, n,
+                                                _stream_of(_device(), stream))
     if rc != PA_OK:
         _check(rc, "pa_decode_weights_int8")
 
