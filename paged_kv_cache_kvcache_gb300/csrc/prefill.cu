@@ -100,6 +100,7 @@ constexpr float kRescaleThreshold = 8.0f; // log2 units
 // (one extra per item boundary), so 8 barriers keep every parity wait
 // unambiguous for rings of up to 4 slots.
 constexpr int kIterRing = 8;
+constexpr int kWinBox = 16; // rows of a key tile's box in the windowed kernels
 
 template <int D>
 struct PfLayout {
@@ -184,17 +185,14 @@ struct Item {
     int nkt0, nkt1, nkt;    // key tiles of each query tile; nkt = max
     bool tail;              // the last key tile runs past the sequence end
     int blk0;               // physical block holding key 0 (read by the short-batch kernel only)
-    // windowed kernels: the item's key tiles are the first `first` ones of the sequence, which hold the first
-    // `sink` keys that its queries see before the window, and then those from tile first + skip on; its
-    // first query's window begins at key lo.  (nkt0, nkt1 and nkt count these tiles, `real` gives their place.)
-    int first, skip, sink, lo;
-    template <bool kWin>
-    __device__ int real(int j) const { return kWin && j >= first ? j + skip : j; }
-    // key tile j holds keys that no query of the item sees: their V rows are zeroed
-    __device__ bool ragged(int j) const
-    {
-        return (j == first - 1 && (sink & 127) != 0) || (j == first && (lo & 127) != 0);
-    }
+    // windowed kernels: the item's keys are the `sink` first ones that its queries see before the window and those
+    // from lo (where its first query's window begins) on, both in boxes of 16, one run behind the other: key k of
+    // the window is at place k - gap, and places before `start` are the first keys'.  (nkt0, nkt1, nkt count tiles of
+    // places.)
+    int sink, lo, start, gap;
+    // key tile j holds keys that no query of the item sees, at the places from `sink` to lo - gap: their V rows
+    // are zeroed
+    __device__ bool ragged(int j) const { return sink < lo - gap && j >= sink >> 7 && j <= (lo - gap - 1) >> 7; }
 };
 
 // The items of this CTA: rounds of gridDim.x consecutive entries of the list
@@ -238,11 +236,12 @@ struct ItemIter {
         if constexpr (kWin) {
             w.lo = max(0, off + w.q0 + 1 - window);
             w.sink = min(sinks, w.lo);
-            w.first = min((w.sink + 127) >> 7, w.lo >> 7);
-            w.skip = (w.lo >> 7) - w.first;
-            w.nkt0 -= w.skip;
-            w.nkt1 -= w.npos1 > 0 ? w.skip : 0;
-            w.nkt -= w.skip;
+            w.start = min((w.sink + kWinBox - 1) & ~(kWinBox - 1), w.lo & ~(kWinBox - 1));
+            w.gap = (w.lo & ~(kWinBox - 1)) - w.start;
+            w.nkt0 = (off + w.q0 + w.npos0 - w.gap + 127) >> 7;
+            w.nkt1 = w.npos1 > 0 ? (off + w.q0 + P + w.npos1 - w.gap + 127) >> 7 : 0;
+            w.nkt = max(w.nkt0, w.nkt1);
+            w.tail = w.nkt * 128 + w.gap > w.lk;
         }
         return w;
     }
@@ -578,13 +577,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a cache row, or -(r + 1) for row r of the new keys' input (fused store); a box that
         // starts in the cached prefix comes from the cache (its new rows are patched in later)
         auto sub_row = [&](const Item &w, const int32_t *bt, int j) -> int {
-            const int key = j * 128 + lane * box_rows;
+            int key = j * 128 + lane * box_rows;
+            if (kWin && key >= w.start)
+                key += w.gap;
             if (lane >= nsub || key >= w.lk)
                 return p.num_slots; // fully out of range: TMA fills zeros
-            if constexpr (kWin) { // a box that no query of the item sees is not looked up
-                if (key >= w.sink && key + box_rows <= w.lo)
-                    return p.num_slots;
-            }
             const int off = w.lk - w.lq; // cached prefix
             if (!kWin && p.fused && key >= off)
                 return -(w.cq0 + key - off + 1);
@@ -657,11 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Item w = items.next();
                 const int jfix = kWin ? -1 : straddle_tile(w, p.fused, box_rows);
                 const int32_t *bt = p.block_tables + (size_t)w.b * p.max_blocks;
-                int next = sub_row(w, bt, w.template real<kWin>(0));
+                int next = sub_row(w, bt, 0);
                 for (int j = 0; j < w.nkt; ++j, ++X) {
                     const int cur = next;
                     if (j + 1 < w.nkt)
-                        next = sub_row(w, bt, w.template real<kWin>(j + 1));
+                        next = sub_row(w, bt, j + 1);
                     starts = (starts << 1) | (j == 0 ? 1u : 0u);
                     const int st = X % nstages;
                     // slot reuse: free once the tile nstages back is released
@@ -694,17 +691,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (zero) {
                             // V rows of keys past the sequence end may hold anything (even NaN
                             // bit patterns); zero them so that P = 0 cannot turn them into NaN in O.
-                            const int first = w.lk - w.template real<kWin>(j) * 128;
+                            const int first = w.lk - (kWin ? w.gap : 0) - j * 128;
                             const int chunks = (128 - first) * 8;
                             for (int pp = 0; pp < L::kPanels; ++pp)
                                 for (int c = lane; c < chunks; c += 32)
                                     *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + (first + (c >> 3)) * 128 +
                                                                (c & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
-                        if constexpr (kWin) { // likewise those of keys between the first ones and the window
-                            const int key0 = w.template real<kWin>(j) * 128;
-                            const int from = max(w.sink - key0, 0);
-                            const int chunks = ragged ? (min(w.lo - key0, 128) - from) * 8 : 0;
+                        if constexpr (kWin) { // likewise those between the first keys and the window
+                            const int from = max(w.sink - j * 128, 0);
+                            const int chunks = ragged ? (min(w.lo - w.gap - j * 128, 128) - from) * 8 : 0;
                             for (int pp = 0; pp < L::kPanels; ++pp)
                                 for (int c = lane; c < chunks; c += 32)
                                     *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + (from + (c >> 3)) * 128 +
@@ -891,9 +887,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 ns ^= 1;
                 ptx::tc_fence_after();
-                const int lim = limit - w.template real<kWin>(j) * 128; // columns this row sees in this tile
+                const int lim = limit - (kWin ? w.gap : 0) - j * 128; // columns this row sees in this tile
                 // windowed: of those, the ones from `from` on and those before `sink`
-                const int from = kWin ? lim - width : 0, sink = kWin ? p.sinks - w.template real<kWin>(j) * 128 : 0;
+                const int from = kWin ? lim - width : 0, sink = kWin ? p.sinks - j * 128 : 0;
                 // the whole score row in registers: one TMEM round trip per tile.  Tiles no row
                 // of the warp sees only in part take the row max from the loads themselves
                 // (tcgen05.ld.red); tiles crossing the causal diagonal mask first, then reduce.
@@ -904,9 +900,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int q = 0; q < 4; ++q)
                         ptx::tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
                     ptx::tmem_wait_ld();
+                    if constexpr (kWin) { // as bits: [0, sink) and [from, lim)
+                        auto ones = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        sr[c] = c < lim && (!kWin || c >= from || c < sink) ? sr[c] : __float_as_uint(-INFINITY);
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t see = (ones(sink - 32 * q) | ~ones(from - 32 * q)) & ones(lim - 32 * q);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                sr[32 * q + c] = (see >> c) & 1u ? sr[32 * q + c] : __float_as_uint(-INFINITY);
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            sr[c] = c < lim ? sr[c] : __float_as_uint(-INFINITY);
+                    }
                     float m8[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -1076,7 +1083,7 @@ int launch(const PrefillArgs &a, cudaStream_t stream, int sms)
     // One box per physical block (or per 128-key tile); for a fused store whose cached
     // prefixes end inside a box, boxes of 16 rows, so a straddling box has at most 15 new
     // rows for the producer to patch in.
-    const uint32_t box_rows = a.k_in && a.small_boxes ? 16u : d.block_size < 128 ? (uint32_t)d.block_size : 128u;
+    const uint32_t box_rows = kWin ? (uint32_t)kWinBox : a.k_in && a.small_boxes ? 16u : d.block_size < 128 ? (uint32_t)d.block_size : 128u;
     if ((rc = encode_tmap_3d(&tk, bf16, a.k_cache, D, d.num_kv_heads, rows, (uint64_t)D * 2,
                              (uint64_t)d.num_kv_heads * D * 2, 64, 1, box_rows, sw, "k_cache")) != PA_OK)
         return rc;
