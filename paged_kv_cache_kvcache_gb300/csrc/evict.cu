@@ -63,13 +63,20 @@ __device__ __forceinline__ uint32_t order(float x)
 // rounding errors but those of e (two-sum; fp64 adds run at 1/64 of fp32's rate and took longer than the reads).
 __device__ __forceinline__ uint32_t total_of(const float *at, int heads, int64_t pitch)
 {
+    constexpr int kLoads = 8; // in flight together
     float s = 0.f, e = 0.f;
-    for (int h = 0; h < heads; ++h) {
-        const float x = at[h * pitch];
-        const float t = __fadd_rn(s, x);
-        const float b = __fsub_rn(t, s);
-        e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x, b)));
-        s = t;
+    for (int h0 = 0; h0 < heads; h0 += kLoads) {
+        float x[kLoads];
+#pragma unroll
+        for (int h = 0; h < kLoads; ++h)
+            x[h] = h0 + h < heads ? at[(h0 + h) * pitch] : 0.f;
+#pragma unroll
+        for (int h = 0; h < kLoads; ++h) {
+            const float t = __fadd_rn(s, x[h]);
+            const float b = __fsub_rn(t, s);
+            e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x[h], b)));
+            s = t;
+        }
     }
     return order(isfinite(s) ? __fadd_rn(s, e) : s);
 }
@@ -106,7 +113,7 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
     extern __shared__ uint32_t keys[];
     __shared__ int hist[kBins];
     __shared__ int warps[kChooseWarps], warps2[kChooseWarps];
-    __shared__ int digit, above, lowest;
+    __shared__ int digit, above, equals, lowest;
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -136,6 +143,11 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
         return;
     }
 
+    // the row's first pages, looked up while the totals are formed
+    const int32_t *table = p.tables + (int64_t)row * p.max_blocks;
+    const int pages = (n + bs - 1) / bs;
+    const int page0 = tid < pages ? table[tid] : 0;
+    const int refs0 = tid < pages && (uint32_t)page0 < (uint32_t)p.num_blocks ? p.refs[page0] : 0;
     const float *scores = p.scores + (int64_t)row * p.num_kv_heads * room;
     const bool stored = n <= p.keys;
     const int begin = p.first, end = n - p.last; // of those to choose from
@@ -147,8 +159,9 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
     if (tid == 0)
         lowest = n;
 
-    // the m-th largest key: its bits from the top, and how many of the keys equal to it stay
-    int need = budget - p.first - p.last;
+    // the m-th largest key: its bits from the top, and how many of the keys that share them stay (no more bits are
+    // needed once all of those do)
+    int need = budget - p.first - p.last, low = 0;
     uint32_t prefix = 0;
     const bool any = need > 0;
     for (int round = 0; any && round < 3; ++round) {
@@ -170,13 +183,18 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
         if (before < need && need <= before + a) {
             digit = hi;
             above = before;
+            equals = a;
         } else if (before + a < need && need <= before + a + b) {
             digit = hi - 1;
             above = before + a;
+            equals = b;
         }
         __syncthreads();
         prefix = (prefix << bits) | (uint32_t)digit;
         need -= above;
+        low = shift;
+        if (need == equals)
+            break;
         __syncthreads();
     }
 
@@ -189,7 +207,7 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
             if (j < begin || j >= end) {
                 sure = true;
             } else if (any) {
-                const uint32_t x = key(j);
+                const uint32_t x = key(j) >> low;
                 sure = x > prefix;
                 same = x == prefix;
             }
@@ -232,11 +250,12 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
 
     // the row's pages are in use, and those that are written are its own
     const int moved = lowest; // the tokens before the first that goes stay where they are
-    const int32_t *table = p.tables + (int64_t)row * p.max_blocks;
-    for (int x = tid; x < (n + bs - 1) / bs; x += kChooseThreads) {
-        const int page = table[x];
-        const bool written = moved < budget && x >= moved / bs && x < (budget + bs - 1) / bs;
-        bad = bad || (uint32_t)page >= (uint32_t)p.num_blocks || p.refs[page] < 1 || (written && p.refs[page] != 1);
+    const int own = moved < budget ? moved / bs : pages, own_end = (budget + bs - 1) / bs;
+    for (int x = tid; x < pages; x += kChooseThreads) {
+        const int page = x == tid ? page0 : table[x];
+        const bool inside = (uint32_t)page < (uint32_t)p.num_blocks;
+        const int refs = x == tid ? refs0 : inside ? p.refs[page] : 0;
+        bad = bad || !inside || refs < 1 || (x >= own && x < own_end && refs != 1);
     }
     bad = __syncthreads_or(bad);
     if (tid == 0) {
@@ -252,51 +271,61 @@ struct MovePlanes {
     char *k, *v, *ks, *vs; // layer 0; scales NULL: bf16
     uint64_t layer, scale_layer; // bytes between layers
     int32_t layers, token_bytes; // bytes of a token's row in one layer of k (or v)
-    int32_t slice_vecs;          // 16-byte vectors of a slice
+    int32_t log_slice;           // 16-byte vectors of a slice, as a power of two
     int32_t slices;              // slices of a token's row
     int32_t units;               // per row: (layer, K or V, slice), then (layer, K or V, head) of the scales, then heads
                                  // of the scores
 };
 
-// Elements T of the places [from, count) from where their tokens are: place and source give an element's address.
-// A batch has `tokens` places of kThreadVecs x kMoveThreads elements.
-template <class T, class Dst, class Src>
-__device__ __forceinline__ void move_up(int from, int count, int per, Dst dst, Src src)
+// Elements T of the places [from, count) from where their tokens are: `map` (of kBatchTokens places at a time) holds
+// each place's and its token's slot, element e of slot x is at(x, e); a token has per <= 2^log_per of them.
+template <class T, class At>
+__device__ __forceinline__ void move_up(const int32_t *kept, const int32_t *table, int log_bs, int from, int count, int per,
+                                        int log_per, int2 *map, At at)
 {
-    const int tokens = kBatchTokens / per;
-    T a[kVecs], b[kVecs];
-    auto load = [&](int base, T(&x)[kVecs]) {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            const int e = u * kMoveThreads + (int)threadIdx.x;
-            const int k = base + e / per;
-            if (e < tokens * per && k < count)
-                x[u] = *src(k, e % per);
-        }
-    };
-    auto store = [&](int base, const T(&x)[kVecs]) {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) {
-            const int e = u * kMoveThreads + (int)threadIdx.x;
-            const int k = base + e / per;
-            if (e < tokens * per && k < count)
-                *dst(k, e % per) = x[u];
-        }
-    };
-    load(from, a);
-    for (int base = from; base < count; base += 2 * tokens) {
-        load(base + tokens, b);
-        __syncthreads(); // every thread has this batch's values: its places may be written
-        store(base, a);
-        load(base + 2 * tokens, a);
+    const int tokens = kBatchTokens >> log_per; // of a batch
+    auto slot = [&](int token) { return (table[token >> log_bs] << log_bs) + (token & ((1 << log_bs) - 1)); };
+    for (int base = from; base < count; base += kBatchTokens) {
+        const int n = min(count - base, kBatchTokens);
+        __syncthreads(); // the map may still be read
+        for (int x = threadIdx.x; x < n; x += kMoveThreads)
+            map[x] = make_int2(slot(base + x), slot(kept[base + x]));
         __syncthreads();
-        store(base + tokens, b);
+        T a[kVecs], b[kVecs];
+        auto load = [&](int first, T(&x)[kVecs]) {
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u) {
+                const int e = u * kMoveThreads + (int)threadIdx.x;
+                const int k = first + (e >> log_per), v = e & ((1 << log_per) - 1);
+                if (k < n && v < per)
+                    x[u] = *at(map[k].y, v);
+            }
+        };
+        auto store = [&](int first, const T(&x)[kVecs]) {
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u) {
+                const int e = u * kMoveThreads + (int)threadIdx.x;
+                const int k = first + (e >> log_per), v = e & ((1 << log_per) - 1);
+                if (k < n && v < per)
+                    *at(map[k].x, v) = x[u];
+            }
+        };
+        load(0, a);
+        for (int k = 0; k < n; k += 2 * tokens) {
+            load(k + tokens, b);
+            __syncthreads(); // every thread has this batch's values: its places may be written
+            store(k, a);
+            load(k + 2 * tokens, a);
+            __syncthreads();
+            store(k + tokens, b);
+        }
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, const MovePlanes q)
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p, const MovePlanes q)
 {
     __shared__ uint32_t place;
+    __shared__ int2 map[kBatchTokens];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const int i = blockIdx.x / q.units;
@@ -317,34 +346,40 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     const int64_t room = (int64_t)p.max_blocks * bs;
     int32_t *table = p.tables + (int64_t)row * p.max_blocks;
     const int planes = 2 * q.layers;
-    const int moved = p.moved[i];
-    auto slot = [&](int token) { return (int64_t)table[token / bs] * bs + (token & (bs - 1)); };
+    const int moved = min(p.moved[i], left);
+    const int log_bs = __ffs(bs) - 1;
 
     if (unit < planes * q.slices) {
         const int plane = unit / q.slices, slice = unit - plane * q.slices;
-        const int per = min(q.slice_vecs, q.token_bytes / 16 - slice * q.slice_vecs);
-        char *base = (plane & 1 ? q.v : q.k) + (plane >> 1) * q.layer + (int64_t)slice * q.slice_vecs * 16;
-        if (moved < left)
-            move_up<uint4>(
-                moved, left, per, [&](int k, int e) { return reinterpret_cast<uint4 *>(base + slot(k) * q.token_bytes) + e; },
-                [&](int k, int e) { return reinterpret_cast<const uint4 *>(base + slot(kept[k]) * q.token_bytes) + e; });
+        const int per = min(1 << q.log_slice, q.token_bytes / 16 - (slice << q.log_slice));
+        char *base = (plane & 1 ? q.v : q.k) + (plane >> 1) * q.layer + ((int64_t)slice << q.log_slice) * 16;
+        move_up<uint4>(kept, table, log_bs, moved, left, per, q.log_slice, map, [&](int slot, int v) {
+            return reinterpret_cast<uint4 *>(base + (int64_t)slot * q.token_bytes) + v;
+        });
     } else if ((unit -= planes * q.slices) < (q.ks ? planes * p.num_kv_heads : 0)) {
         const int plane = unit / p.num_kv_heads, head = unit - plane * p.num_kv_heads;
         uint16_t *base = reinterpret_cast<uint16_t *>((plane & 1 ? q.vs : q.ks) + (plane >> 1) * q.scale_layer);
-        auto at = [&](int token) {
-            return base + ((int64_t)table[token / bs] * p.num_kv_heads + head) * bs + (token & (bs - 1));
-        };
-        if (moved < left)
-            move_up<uint16_t>(moved, left, 1, [&](int k, int) { return at(k); },
-                              [&](int k, int) { return (const uint16_t *)at(kept[k]); });
-    } else {
+        move_up<uint16_t>(kept, table, log_bs, moved, left, 1, 0, map, [&](int slot, int) {
+            return base + ((((int64_t)(slot >> log_bs) * p.num_kv_heads + head) << log_bs) + (slot & (bs - 1)));
+        });
+    } else { // one head's scores, a batch read before it is written as above
         unit -= q.ks ? planes * p.num_kv_heads : 0;
         const int64_t at = ((int64_t)row * p.num_kv_heads + unit) * room;
         const float *from = p.scores + at;
         float *to = p.scores_out + at;
         const int start = from == to ? moved : 0;
-        if (start < left)
-            move_up<float>(start, left, 1, [&](int k, int) { return to + k; }, [&](int k, int) { return from + kept[k]; });
+        float a[kVecs];
+        for (int k0 = start; k0 < left; k0 += kBatchTokens) {
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u)
+                if (const int k = k0 + u * kMoveThreads + tid; k < left)
+                    a[u] = from[kept[k]];
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < kVecs; ++u)
+                if (const int k = k0 + u * kMoveThreads + tid; k < left)
+                    to[k] = a[u];
+        }
         __syncthreads();
         for (int k = left + tid; k < n; k += kMoveThreads)
             to[k] = 0.f;
@@ -415,12 +450,12 @@ int launch_pool_evict(const PoolArgs &a, const int32_t *rows, int n, const float
     q.layer = o.layer_stride, q.scale_layer = o.scale_layer_stride;
     q.layers = o.num_layers;
     q.token_bytes = d.num_kv_heads * d.head_dim * (o.k_scale ? 1 : 2);
-    // slices: the whole row of a token, or less (down to 64 bytes) while that gives the SMs too few CTAs
+    // slices: up to 1 KB of a token's row, less (down to 64 bytes) while that gives the SMs too few CTAs
     const int vecs = q.token_bytes / 16;
-    q.slice_vecs = std::min(vecs, 64);
-    while (q.slice_vecs > 4 && (int64_t)n * q.layers * 2 * ((vecs + q.slice_vecs - 1) / q.slice_vecs) < 8 * sms)
-        q.slice_vecs = (q.slice_vecs + 1) / 2;
-    q.slices = (vecs + q.slice_vecs - 1) / q.slice_vecs;
+    q.log_slice = 6;
+    while (q.log_slice > 2 && (int64_t)n * q.layers * 2 * ((vecs + (1 << q.log_slice) - 1) >> q.log_slice) < 4 * sms)
+        --q.log_slice;
+    q.slices = (vecs + (1 << q.log_slice) - 1) >> q.log_slice;
     const int64_t units = (int64_t)2 * q.layers * (q.slices + (q.ks ? d.num_kv_heads : 0)) + d.num_kv_heads;
     if (units * n > INT32_MAX)
         return fail(PA_ERR_UNSUPPORTED, "pa_pool_evict: %d rows of %d layers exceed one launch", n, q.layers);
