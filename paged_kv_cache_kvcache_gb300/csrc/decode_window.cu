@@ -40,11 +40,11 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int NT, bool kInt8>
 struct WinLayout {
+    static constexpr int kStages = kInt8 ? 3 : 2;
     static constexpr int kRowBytes = kInt8 ? D : D * 2;  // one head's row of one token
     static constexpr int kChunkBytes = 16 * kRowBytes;   // 16 tokens of K (or V)
     static constexpr int kStageBytes = 2 * kChunkBytes;
@@ -84,7 +84,7 @@ struct WinParams {
     const float *scores;
     float *scores_out;
     float *raw;        // [sequence][KV head][max_blocks * block_size][raw_heads]
-    int32_t raw_heads; // the group, rounded up to a power of two
+    int32_t raw_heads; // the group, rounded up to 4, 8 or 16
 };
 
 constexpr uint32_t kFlip = 0x80808080u;  // int8 -> offset binary (x + 128), per byte
@@ -116,9 +116,11 @@ __device__ __forceinline__ uint32_t swz(int t, int v)
 }
 
 template <int D, int NT, bool kInt8, bool kWeights>
-__global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decode_window_kernel(const WinParams p)
+__global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : NT == 1 ? 3 : 2)
+    decode_window_kernel(const WinParams p)
 {
     using L = WinLayout<D, NT, kInt8>;
+    constexpr int kStages = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -157,6 +159,8 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
     const uint32_t wbase = ptx::smem_u32(smem) + warp * L::kWarpBytes;
     const uint32_t sc_base = ptx::smem_u32(smem) + L::kScaleOff + warp * kStages * 64;
     int blk_cache = 0;
+    // the keys and values of a step are read once: of L2, what waits there for the weights goes last
+    const uint64_t once = ptx::policy_evict_first();
 
     // Chunk i of this warp into stage st.  A lane copies vector v0 of the rows t0, t0 + kRowsPer, ...
     constexpr int kVec = L::kRowBytes / 16;     // 16-byte vectors per row
@@ -166,6 +170,12 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
     const size_t lane_off = t0 * token_bytes + (size_t)g * L::kRowBytes + v0 * 16;
     const char *k_lane = static_cast<const char *>(p.k_cache) + lane_off;
     const char *v_lane = static_cast<const char *>(p.v_cache) + lane_off;
+    auto copy = [&](uint32_t dst, const char *src, uint32_t bytes) {
+        if constexpr (kWeights)
+            ptx::cp_async_16_hint(dst, src, bytes, once);
+        else
+            ptx::cp_async_16(dst, src, bytes);
+    };
     auto issue = [&](int i, int st) {
         if ((i & 31) == 0) { // the block ids of chunks i .. i + 31, one per lane
             blk_cache = 0;
@@ -186,8 +196,8 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
 #pragma unroll
             for (int x = 0; x < 16 / kRowsPer; ++x) {
                 const uint32_t dst = sbase + swz<L::kRowBytes>(x * kRowsPer + t0, v0);
-                ptx::cp_async_16(dst, kp + x * kRowsPer * token_bytes, 16u);
-                ptx::cp_async_16(dst + L::kChunkBytes, vp + x * kRowsPer * token_bytes, 16u);
+                copy(dst, kp + x * kRowsPer * token_bytes, 16u);
+                copy(dst + L::kChunkBytes, vp + x * kRowsPer * token_bytes, 16u);
             }
         } else { // rows that are not seen, or of a block outside the pool, are zeros
 #pragma unroll
@@ -325,13 +335,8 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
             const float s3 = seen1 ? sc[nt][3] * ks1 : -INFINITY;
             if constexpr (kWeights) {
                 const int h0 = nt * 8 + 2 * c;
-                float *at = raw + (size_t)(key0 + r) * p.raw_heads + h0;
-                if (p.raw_heads == 1) {
-                    if (h0 == 0) {
-                        at[0] = s0;
-                        at[8] = s2;
-                    }
-                } else if (h0 < p.raw_heads) {
+                if (h0 < p.raw_heads) {
+                    float *at = raw + (size_t)(key0 + r) * p.raw_heads + h0;
                     *reinterpret_cast<float2 *>(at) = make_float2(s0, s1);
                     *reinterpret_cast<float2 *>(at + (size_t)8 * p.raw_heads) = make_float2(s2, s3);
                 }
@@ -517,17 +522,43 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : 2) decod
             all_l[hl] = sum != 0.f ? 1.f / sum : 0.f; // (every weight is 0 then)
         }
         __syncthreads();
-        // two chunks of this warp at a time, a key per lane
+        // a key per lane and 16 of a chunk, kKeys loads of each in flight
+        constexpr int kKeys = 8;
         const size_t srow = ((size_t)row * Hkv + g) * room;
-        for (int i = lane >> 4; i < my_n; i += 2) {
-            const int key = first_key(i) + (lane & 15);
-            if (key >= ctx)
-                continue;
-            const float *at = raw + (size_t)key * p.raw_heads;
-            float w = 0.f;
-            for (int hl = 0; hl < G; ++hl)
-                w += ptx::ex2(at[hl] - all_m[hl]) * all_l[hl];
-            p.scores_out[srow + key] = p.decay != 0.f ? p.decay * p.scores[srow + key] + w : w;
+        const bool keep = p.decay != 0.f;
+        for (int i0 = lane >> 4; i0 < my_n; i0 += 2 * kKeys) {
+            float4 x[kKeys][2 * NT];
+            float old[kKeys];
+#pragma unroll
+            for (int u = 0; u < kKeys; ++u) {
+                const int i = i0 + 2 * u, key = i < my_n ? first_key(i) + (lane & 15) : ctx;
+                if (key < ctx) {
+                    const float4 *at = reinterpret_cast<const float4 *>(raw + (size_t)key * p.raw_heads);
+#pragma unroll
+                    for (int e = 0; e < 2 * NT; ++e)
+                        if (4 * e < p.raw_heads)
+                            x[u][e] = at[e];
+                    old[u] = keep ? p.scores[srow + key] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kKeys; ++u) {
+                const int i = i0 + 2 * u, key = i < my_n ? first_key(i) + (lane & 15) : ctx;
+                if (key < ctx) {
+                    float w = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 2 * NT; ++e) {
+                        const float y[4] = {x[u][e].x, x[u][e].y, x[u][e].z, x[u][e].w};
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int hl = 4 * e + z;
+                            if (hl < G)
+                                w += ptx::ex2(y[z] - all_m[hl]) * all_l[hl];
+                        }
+                    }
+                    p.scores_out[srow + key] = keep ? fmaf(p.decay, old[u], w) : w;
+                }
+            }
         }
     }
     if (ctas > 1)
@@ -589,20 +620,25 @@ int launch_decode_window(const WindowArgs &a, void *stream)
     p.window = a.window, p.sinks = a.sinks;
     p.decay = a.decay, p.scores = a.scores, p.scores_out = a.scores_out, p.raw = a.raw;
     p.raw_heads = window_raw_heads(a.dims);
-    // CTAs per (sequence, KV head): as many as run at once (more than one wave of clusters costs more than it gives:
-    // 200 sequences of 4 KV heads and 1000 keys took 66.8 us with one CTA each, 88.2 with two; 19 of 16384 keys 141
-    // with one, 100 with two), up to eight, none without a chunk of keys for each of its warps.
+    // CTAs per (sequence, KV head), up to eight: as many as run at once (clusters of a second wave wait for whole ones of
+    // the first: 200 sequences of 4 KV heads and 1000 keys took 66.8 us with one CTA each, 88.2 with two; 19 of 16384
+    // keys 141 with one, 100 with two), a little less than the SMs have room for, since a cluster stays in one GPC (64
+    // clusters of six 6.2 us, of seven, in 456 places, 9.2).  Where contexts are seen whole their lengths differ, and
+    // up to four CTAs, 1024 in all, even them out (64 of 4096 to 8192 keys: 175 us with one, 153 with four; 256 of up
+    // to 2000: 98 with one, 118 with four).  No more than have a chunk of keys for each warp.
     const int64_t units = (int64_t)a.num_seqs * a.dims.num_kv_heads;
     const int64_t room = (int64_t)a.max_blocks_per_seq * a.dims.block_size;
-    const int64_t keys = a.raw ? room : room < (int64_t)a.window + a.sinks ? room : (int64_t)a.window + a.sinks;
-    const int64_t slots = (int64_t)sms * (!a.k_scale ? 2 : p.group > 8 ? 3 : 4); // (the kernels' launch bounds)
-    int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(8, slots / units));
-    ctas = (int)std::min<int64_t>(ctas, (keys + kWarps * 16 - 1) / (kWarps * 16));
+    const int64_t most = (int64_t)a.window + a.sinks;
+    const int64_t slots = (int64_t)sms * (!a.k_scale ? p.group > 8 ? 2 : 3 : p.group > 8 ? 3 : 4); // (the launch bounds)
+    int64_t ctas = std::max<int64_t>(1, slots * 85 / 100 / units);
+    if (room <= most)
+        ctas = std::max(ctas, std::min<int64_t>(4, (1024 + units - 1) / units));
+    ctas = std::min({ctas, (int64_t)8, (std::min(room, most) + kWarps * 16 - 1) / (kWarps * 16)});
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool two = p.group > 8;
     if (a.dims.head_dim == 128)
-        return two ? launch_kind<128, 2>(a, p, ctas, s) : launch_kind<128, 1>(a, p, ctas, s);
-    return two ? launch_kind<64, 2>(a, p, ctas, s) : launch_kind<64, 1>(a, p, ctas, s);
+        return two ? launch_kind<128, 2>(a, p, (int)ctas, s) : launch_kind<128, 1>(a, p, (int)ctas, s);
+    return two ? launch_kind<64, 2>(a, p, (int)ctas, s) : launch_kind<64, 1>(a, p, (int)ctas, s);
 }
 
 int read_window_error(uint32_t *code)

@@ -297,10 +297,10 @@ struct WindowArgs {
     float *scores_out;
 };
 int launch_decode_window(const WindowArgs &a, void *stream);
-// Scores per key and KV head that pa_decode_weights keeps in its workspace: the group, rounded up to a power of two.
+// Scores per key and KV head that pa_decode_weights keeps in its workspace: the group, rounded up to 4, 8 or 16.
 inline int window_raw_heads(const pa_dims &d)
 {
-    int n = 1;
+    int n = 4;
     while (n < d.num_heads / d.num_kv_heads)
         n *= 2;
     return n;

@@ -121,8 +121,8 @@ def test_library_refusals():
     need = ctypes.c_uint64()
     d = pa.make_dims(*DIMS)
     assert L.pa_decode_weights_workspace(ctypes.byref(d), 3, 2, ctypes.byref(need)) == pa.PA_OK
-    assert need.value == 3 * 2 * 32 * 2 * 4
-    assert rc("weights", ws_bytes=2 * 32 * 2 * 4 - 1) == pa.PA_ERR_WORKSPACE
+    assert need.value == 3 * 2 * 32 * 4 * 4
+    assert rc("weights", ws_bytes=2 * 32 * 4 * 4 - 1) == pa.PA_ERR_WORKSPACE
     assert L.pa_decode_weights_workspace(ctypes.byref(d), -1, 2, ctypes.byref(need)) == bad
     assert L.pa_decode_weights_workspace(ctypes.byref(d), 1, 2, None) == bad
 
