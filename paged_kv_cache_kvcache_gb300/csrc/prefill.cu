@@ -165,7 +165,8 @@ struct Bars {
     __device__ uint32_t p_full(int t) const { return base + 8 * (22 + t); }
     // the item's last PV MMA of query tile t is complete: O_t is final
     __device__ uint32_t o_full(int t) const { return base + 8 * (24 + t); }
-    // V slot s holds an item's last key tile with its rows past the sequence end zeroed
+    // V slot s holds an item's last key tile with its rows past the sequence end zeroed (windowed: the loads of a tile
+    // with rows to be zeroed have landed)
     __device__ uint32_t v_tail(int s) const { return base + 8 * (26 + s); }
     __device__ uint32_t tmem_slot() const { return base + 8 * 30; }
     // fused store: K slot s holds the key tile whose straddling box (cached prefix, then
@@ -193,6 +194,7 @@ struct Item {
     // key tile j holds keys that no query of the item sees, at the places from `sink` to lo - gap: their V rows
     // are zeroed
     __device__ bool ragged(int j) const { return sink < lo - gap && j >= sink >> 7 && j <= (lo - gap - 1) >> 7; }
+    __device__ bool holes(int j) const { return ragged(j) || (tail && j == nkt - 1); }
 };
 
 // The items of this CTA: rounds of gridDim.x consecutive entries of the list
@@ -595,6 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!kShort && lane == 0)
                 ptx::prefetch_tmap(&tm_q);
             bool ok = true;
+            int Xv = 0;           // windowed: global key tile of the current item's first
+            uint32_t landpar = 0; // windowed: bit s, parity of the tiles that have landed on v_tail(s)
             uint32_t early = 0; // bit t: query tile t of the current item was loaded during the previous item's copy
             while (ok && items.more()) {
                 const Item w = items.next();
@@ -611,6 +615,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 early = 0;
                 if (ok && lane == 0 && items.more())
                     prefetch_query_tiles<D>(&tm_q, items.peek(), G, P);
+                if constexpr (kWin) {
+                    // V rows of keys that no query of the item sees, between the first keys and the window and past the
+                    // sequence end, are zeroed here: nearly every item has some, and the V producer would wait
+                    // for them to land before it could issue the next load.  Such a tile lands on v_tail and is
+                    // full once it is zeroed (one use of v_tail at a time: the slot's next load waits for this
+                    // tile's products).
+                    for (int j = 0; ok && j < w.nkt; ++j) {
+                        if (!w.holes(j))
+                            continue;
+                        const int st = (Xv + j) % L::kVStages;
+                        if (!(ok = wwait(bars.v_tail(st), (landpar >> st) & 1u)))
+                            break;
+                        landpar ^= 1u << st;
+                        const int from = w.ragged(j) ? max(w.sink - j * 128, 0) : 0;
+                        const int to = w.ragged(j) ? min(w.lo - w.gap - j * 128, 128) : 0;
+                        const int tail = w.tail && j == w.nkt - 1 ? w.lk - w.gap - j * 128 : 128;
+                        uint8_t *tile = sgen + L::kV + st * L::kTileBytes;
+                        const int n = (to - from) * 8, chunks = n + (128 - tail) * 8;
+                        for (int pp = 0; pp < L::kPanels; ++pp)
+                            for (int c = lane; c < chunks; c += 32) {
+                                const int row = c < n ? from + (c >> 3) : tail + ((c - n) >> 3);
+                                *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + row * 128 + (c & 7) * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            ptx::mbar_arrive(bars.v_full(st));
+                    }
+                    Xv += w.nkt;
+                }
                 if (!kWin && ok && p.fused) {
                     if (items.more()) {
                         // this item's rows, pass by pass; a query buffer that frees meanwhile is
@@ -667,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!(ok = wwait(bars.released(e), (e / kIterRing) & 1)))
                             break;
                     }
-                    const uint32_t full = is_k ? bars.k_full(st) : bars.v_full(st);
+                    const uint32_t full = is_k ? bars.k_full(st) : kWin && w.holes(j) ? bars.v_tail(st) : bars.v_full(st);
                     const uint32_t dst = ring + st * L::kTileBytes;
                     if (lane == 0)
                         ptx::mbar_arrive_expect_tx(full, (uint32_t)L::kTileBytes);
@@ -680,9 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              w.g, row);
                     }
                     __syncwarp();
-                    const bool fix = j == jfix, zero = !is_k && w.tail && j == w.nkt - 1;
-                    const bool ragged = kWin && !is_k && w.ragged(j);
-                    if (fix || zero || ragged) {
+                    const bool fix = j == jfix, zero = !kWin && !is_k && w.tail && j == w.nkt - 1;
+                    if (fix || zero) {
                         if (!(ok = wwait(full, (X / nstages) & 1)))
                             break;
                         uint8_t *tile = sgen + (is_k ? L::kK : L::kV) + st * L::kTileBytes;
@@ -691,19 +725,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (zero) {
                             // V rows of keys past the sequence end may hold anything (even NaN
                             // bit patterns); zero them so that P = 0 cannot turn them into NaN in O.
-                            const int first = w.lk - (kWin ? w.gap : 0) - j * 128;
+                            const int first = w.lk - j * 128;
                             const int chunks = (128 - first) * 8;
                             for (int pp = 0; pp < L::kPanels; ++pp)
                                 for (int c = lane; c < chunks; c += 32)
                                     *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + (first + (c >> 3)) * 128 +
-                                                               (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        if constexpr (kWin) { // likewise those between the first keys and the window
-                            const int from = max(w.sink - j * 128, 0);
-                            const int chunks = ragged ? (min(w.lo - w.gap - j * 128, 128) - from) * 8 : 0;
-                            for (int pp = 0; pp < L::kPanels; ++pp)
-                                for (int c = lane; c < chunks; c += 32)
-                                    *reinterpret_cast<uint4 *>(tile + pp * L::kPanelBytes + (from + (c >> 3)) * 128 +
                                                                (c & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
                         ptx::fence_proxy_async_smem();
@@ -801,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!v_ready) {
                             if (!(ok = wwait(bars.v_full(vs), vph)))
                                 return;
-                            if ((w.tail && j == w.nkt - 1) || j == jfix || (kWin && w.ragged(j))) {
+                            if (!kWin && ((w.tail && j == w.nkt - 1) || j == jfix)) {
                                 if (!(ok = wwait(bars.v_tail(vs), (tailpar >> vs) & 1u)))
                                     return;
                                 tailpar ^= 1u << vs;
@@ -895,25 +921,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (tcgen05.ld.red); tiles crossing the causal diagonal mask first, then reduce.
                 uint32_t sr[128];
                 float mx;
-                if (__any_sync(0xffffffffu, lim < 128 || (kWin && min(from, 128) > max(sink, 0)))) {
+                if (kWin && __any_sync(0xffffffffu, lim < 128 || min(from, 128) > max(sink, 0))) {
+                    // what the row sees as bits, [0, sink) and [from, lim), 32 columns at a time
+                    auto ones = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        ptx::tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
+                    uint32_t see[4], some = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        see[q] = (ones(sink - 32 * q) | ~ones(from - 32 * q)) & ones(lim - 32 * q);
+                        some |= (see[q] != 0xffffffffu ? 1u : 0u) << q;
+                    }
+                    some = __reduce_or_sync(0xffffffffu, some); // bit q: some row of the warp does not see all of them
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (some >> q & 1u) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                sr[32 * q + c] = (see[q] >> c) & 1u ? sr[32 * q + c] : __float_as_uint(-INFINITY);
+                        }
+                    float m8[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        m8[i] = ptx::max3(__uint_as_float(sr[16 * i]), __uint_as_float(sr[16 * i + 1]),
+                                          __uint_as_float(sr[16 * i + 2]));
+#pragma unroll
+                    for (int c = 3; c < 16; c += 2)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            m8[i] = c + 1 < 16 ? ptx::max3(m8[i], __uint_as_float(sr[16 * i + c]),
+                                                           __uint_as_float(sr[16 * i + c + 1]))
+                                               : fmaxf(m8[i], __uint_as_float(sr[16 * i + c]));
+                    mx = fmaxf(fmaxf(ptx::max3(m8[0], m8[1], m8[2]), ptx::max3(m8[3], m8[4], m8[5])),
+                               fmaxf(m8[6], m8[7]));
+                } else if (!kWin && __any_sync(0xffffffffu, lim < 128)) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         ptx::tmem_ld32(s_col + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
                     ptx::tmem_wait_ld();
-                    if constexpr (kWin) { // as bits: [0, sink) and [from, lim)
-                        auto ones = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t see = (ones(sink - 32 * q) | ~ones(from - 32 * q)) & ones(lim - 32 * q);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                sr[32 * q + c] = (see >> c) & 1u ? sr[32 * q + c] : __float_as_uint(-INFINITY);
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 128; ++c)
-                            sr[c] = c < lim ? sr[c] : __float_as_uint(-INFINITY);
-                    }
+                    for (int c = 0; c < 128; ++c)
+                        sr[c] = c < lim ? sr[c] : __float_as_uint(-INFINITY);
                     float m8[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
