@@ -226,11 +226,9 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
         warps2[warp] = equal;
     }
     __syncthreads();
-    more = equal = 0;
-    for (int w = 0; w < warp; ++w) {
-        more += warps[w];
-        equal += warps2[w];
-    }
+    static_assert(kChooseWarps == 32, "a warp's lane looks at each warp's counts");
+    more = __reduce_add_sync(0xffffffffu, lane < warp ? warps[lane] : 0);
+    equal = __reduce_add_sync(0xffffffffu, lane < warp ? warps2[lane] : 0);
     const uint32_t below = (1u << lane) - 1u;
     for (int j = from; j < to; j += 32) {
         bool sure, same;
@@ -332,6 +330,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
     int unit = blockIdx.x - i * q.units;
     const int tid = threadIdx.x, bs = p.block_size, budget = p.budget;
     bool refused = false;
+    const int row = p.rows[i], n = p.state[i], first_moved = p.moved[i]; // (used if no row is refused)
     for (int x = tid; x < p.n; x += kMoveThreads)
         refused = refused || p.state[x] < 0;
     int32_t *kept = p.kept + (int64_t)i * budget;
@@ -341,12 +340,11 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
                 kept[k] = -1;
         return;
     }
-    const int row = p.rows[i], n = p.state[i];
     const int left = min(n, budget);
     const int64_t room = (int64_t)p.max_blocks * bs;
     int32_t *table = p.tables + (int64_t)row * p.max_blocks;
     const int planes = 2 * q.layers;
-    const int moved = min(p.moved[i], left);
+    const int moved = min(first_moved, left);
     const int log_bs = __ffs(bs) - 1;
 
     if (unit < planes * q.slices) {
