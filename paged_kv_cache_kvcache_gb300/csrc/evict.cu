@@ -81,6 +81,9 @@ __device__ __forceinline__ uint32_t total_of(const float *at, int heads, int64_t
     return order(isfinite(s) ? __fadd_rn(s, e) : s);
 }
 
+// The same out of line, for rows whose keys do not fit shared memory.
+__device__ __noinline__ uint32_t total_far(const float *at, int heads, int64_t pitch) { return total_of(at, heads, pitch); }
+
 // exclusive sum over the CTA's threads; *sum: all
 __device__ __forceinline__ int scan_cta(int v, int *warps, int *sum)
 {
@@ -147,7 +150,6 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
     const int32_t *table = p.tables + (int64_t)row * p.max_blocks;
     const int pages = (n + bs - 1) / bs;
     const int page0 = tid < pages ? table[tid] : 0;
-    const int refs0 = tid < pages && (uint32_t)page0 < (uint32_t)p.num_blocks ? p.refs[page0] : 0;
     const float *scores = p.scores + (int64_t)row * p.num_kv_heads * room;
     const bool stored = n <= p.keys;
     const int begin = p.first, end = n - p.last; // of those to choose from
@@ -155,7 +157,8 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
         for (int j = tid; j < n; j += kChooseThreads)
             keys[j] = j >= begin && j < end ? total_of(scores + j, p.num_kv_heads, room) : 0u;
     }
-    auto key = [&](int j) { return stored ? keys[j] : total_of(scores + j, p.num_kv_heads, room); };
+    const int refs0 = tid < pages && (uint32_t)page0 < (uint32_t)p.num_blocks ? p.refs[page0] : 0;
+    auto key = [&](int j) { return stored ? keys[j] : total_far(scores + j, p.num_kv_heads, room); };
     if (tid == 0)
         lowest = n;
 
