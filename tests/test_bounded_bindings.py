@@ -146,3 +146,29 @@ def test_prefill_window_refusals(int8):
     empty = pa.pa_pack_prefill(dims, [5], [0], [[0]], pin=False)
     plan.meta = empty.meta
     assert rc() == pa.PA_OK
+
+
+def test_evict_library_refusals():
+    L = pa.lib()
+    need = ctypes.c_uint64()
+    d0 = pa.make_dims(*DIMS)
+    assert L.pa_pool_workspace(ctypes.byref(d0), ctypes.byref(pa.pa_pool(5, 4, 1)), ctypes.byref(need)) == pa.PA_OK
+
+    def rc(n=1, budget=8, first=0, last=0, rows=64, scores=64, out=64, kept=64, ws=256, ws_bytes=need.value, dims=DIMS,
+           **pool):
+        fields = dict(num_rows=5, max_blocks=4, num_layers=1, block_tables=64, context_lens=64, ref_counts=64, k_cache=64,
+                      v_cache=64) | pool
+        d, p = pa.make_dims(*dims), pa.pa_pool(**fields)
+        return L.pa_pool_evict(ctypes.byref(d), ctypes.byref(p), rows, n, scores, out, budget, first, last, kept, ws, ws_bytes,
+                               None)
+
+    bad = pa.PA_ERR_INVALID_ARG
+    assert rc(n=0) == pa.PA_OK
+    for kw in (dict(n=-1), dict(n=6), dict(budget=0), dict(budget=-3), dict(first=-1), dict(last=-1), dict(first=5, last=4),
+               dict(first=2 ** 31 - 1, last=2 ** 31 - 1), dict(rows=None), dict(scores=None), dict(out=None), dict(kept=None),
+               dict(ws=None), dict(ws=64), dict(k_cache=None), dict(v_cache=8), dict(k_scale=64), dict(ref_counts=4),
+               dict(num_rows=0), dict(num_layers=2, layer_stride=8)):
+        assert rc(**kw) == bad, kw
+    assert rc(ws_bytes=need.value - 1) == pa.PA_ERR_WORKSPACE
+    assert rc(max_blocks=2 ** 28, dims=(6, 16, 4, 2, 64)) == pa.PA_ERR_UNSUPPORTED
+    assert rc(dims=(6, 24, 4, 2, 64)) == pa.PA_ERR_UNSUPPORTED

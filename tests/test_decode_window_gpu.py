@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from paged_kv_cache_kvcache_gb300 import pagedattn as pa
-from tests.bounded_model import Case, near
+from tests.bounded_model import Case, attend, near
 
 pytestmark = pytest.mark.gpu
 
@@ -205,3 +205,61 @@ def test_weights_of_other_rows_stay():
     for row, w in ((2, a[2]), (0, b[0])):
         assert np.abs(got[row][:, :w.shape[1]] - 3 * w).max() <= 4e-4
         assert abs(got[row].sum() - 3 * 8) <= 1e-3
+
+
+def test_two_captured_graphs_share_a_workspace():
+    cs = [Case([700, 90, 333], 8, 2, 128, 16, EVERYTHING, 0, int8, seed=4 + int8) for int8 in (False, True)]
+    ws = pa.weights_workspace(cs[0].dims, 3, cs[0].width)
+    runs = []
+    for c in cs:
+        q = queries(c, 3).cuda()
+        scores, out = torch.zeros(3, 2, c.width * 16, device="cuda"), torch.empty_like(q)
+        call = pa.pa_decode_weights_int8 if c.int8 else pa.pa_decode_weights
+        args = (c.dims, q, *c.gpu, c.bt, c.ctx, c.scale, out, scores, ws)
+        call(*args)
+        scores.zero_()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(*args)
+        runs.append((graph, c, q, scores, out))
+    for _ in range(3):
+        for r in runs:
+            r[0].replay()
+    for _, c, q, scores, out in runs:
+        want, size, w = c.decode(q.cpu())
+        near(out, want, size)
+        for b, x in enumerate(w):
+            assert np.abs(scores[b, :, :x.shape[1]].cpu().numpy() - 3 * x).max() <= 5e-4
+
+
+@pytest.mark.parametrize("int8", [False, True], ids=["bf16", "int8"])
+def test_offsets_past_32_bits(int8):
+    """Pages behind 2^32 bytes of a pool, rotated and stored there and decoded from there."""
+    nb, bs, hq, hkv, d = (80000 if int8 else 40000), 32, 8, 8, 128  # 2.6 GB a plane
+    dims = pa.make_dims(nb, bs, hq, hkv, d)
+    if int8:
+        caches = pa.int8_cache(dims)
+    else:
+        caches = tuple(torch.zeros(nb, bs, hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (torch.randn(100, 8, d, generator=g).to(torch.bfloat16) for _ in range(3))
+    cs = torch.zeros(4, d)
+    cs[:, :d // 2] = 1  # no turn
+    rope = pa.Rope(dims, cs.cuda())
+    pages = nb - 1 - np.arange(4)
+    slots = torch.tensor(pages[np.arange(100) // bs] * bs + np.arange(100) % bs, dtype=torch.int32, device="cuda")
+    out = torch.empty(100, hq, d, dtype=torch.bfloat16, device="cuda")
+    store = pa.pa_rope_store_int8 if int8 else pa.pa_rope_store
+    store(dims, rope, q.cuda(), k.cuda(), v.cuda(), torch.zeros(100, dtype=torch.int32, device="cuda"), slots, out, *caches)
+    assert torch.equal(out.cpu(), q)
+    bt = torch.tensor(pages[None], dtype=torch.int32, device="cuda")
+    ctx = torch.tensor([100], dtype=torch.int32, device="cuda")
+    got = torch.empty(1, hq, d, dtype=torch.bfloat16, device="cuda")
+    look = pa.pa_decode_window_int8 if int8 else pa.pa_decode_window
+    look(dims, q[:1].cuda(), *caches, bt, ctx, 60, 5, d ** -0.5, got)
+    mask = np.r_[np.ones(5, bool), np.zeros(35, bool), np.ones(60, bool)]
+    kd, vd = k.double().numpy(), v.double().numpy()
+    want, size = (x[None] for x in attend(q[0].double().numpy(), kd, vd, mask, d ** -0.5)[:2])
+    if int8:  # codes: within half a step of max|x| / 127 of the values, and scores of those of the keys
+        size = size + 2.0 ** 8 * 0.02
+    near(got, want, size)
