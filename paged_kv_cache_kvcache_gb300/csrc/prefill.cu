@@ -495,7 +495,13 @@ __device__ __forceinline__ void prefetch_query_tiles(const CUtensorMap *tm_q, co
 // batches keep the other instantiation, whose register allocation those additions
 // would disturb (measured 1.5-2 % slower there).
 // kWin: queries see a window of the last keys and a few first ones (pa_prefill_window; never with the store
-// fused): an item's key tiles are two runs of the sequence's, masked at both ends.
+// fused).  An item's keys are two runs, laid behind one another in its key tiles in boxes of 16, so that four first keys
+// cost a box and not a tile (4 x 4096 queries of 28 heads, window 1024: 236 us with tiles of whole 128-key places,
+// 177 so, 1190 TFLOP/s).  Against the kernel without a window, whose items have more tiles, an item's own time counts
+// more: about 1.55 us a tile and 2.5 us an item (its last products, the output's way out of tensor memory and the next
+// item's first softmax follow one another).  Tried and not kept: half products and weights for a last tile of no more than
+// 64 places (185 us), the row max from the loads for the columns that a warp sees whole in a masked tile (219), two K stages
+// (179).
 template <int D, bool kShort, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
