@@ -171,4 +171,5 @@ def test_evict_library_refusals():
         assert rc(**kw) == bad, kw
     assert rc(ws_bytes=need.value - 1) == pa.PA_ERR_WORKSPACE
     assert rc(max_blocks=2 ** 28, dims=(6, 16, 4, 2, 64)) == pa.PA_ERR_UNSUPPORTED
+    assert rc(max_blocks=2 ** 27 - 1, dims=(6, 16, 4, 2, 64)) == pa.PA_ERR_UNSUPPORTED  # a row of nearly 2^31 tokens
     assert rc(dims=(6, 24, 4, 2, 64)) == pa.PA_ERR_UNSUPPORTED
