@@ -46,6 +46,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCtas = 16; // of a cluster
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int NT, bool kInt8>
@@ -499,35 +500,57 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : NT == 1 
     else
         return;
 
-    // the cluster's: each CTA a share of the output
+    // the cluster's: each CTA a share of the output.  Eight CTAs' results are on their way at once (16: a microsecond less
+    // for a cluster of 16, one more for one of five).
+    constexpr int kAtOnce = 8;
     auto of = [&](float *at, int cta) { return ctas > 1 ? cluster.map_shared_rank(at, cta) : at; };
-    for (int idx = rank * kThreads + (int)threadIdx.x; ctas > 1 && idx < G * D; idx += ctas * kThreads) {
-        const int hl = idx / D;
+    auto maximum = [&](int hl) { // 0 where it is -inf
         float M = -INFINITY;
-        for (int x = 0; x < ctas; ++x)
-            M = fmaxf(M, of(part_m, x)[hl]);
-        const float rf = M == -INFINITY ? 0.f : M;
-        float sum = 0.f, o = 0.f;
-        for (int x = 0; x < ctas; ++x) {
-            const float e = ptx::ex2(of(part_m, x)[hl] - rf);
-            sum += e * of(part_l, x)[hl];
-            o += e * of(part_o, x)[idx];
+        for (int x0 = 0; x0 < ctas; x0 += kAtOnce) {
+            float m[kAtOnce];
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x)
+                m[x] = x0 + x < ctas ? of(part_m, x0 + x)[hl] : -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x)
+                M = fmaxf(M, m[x]);
         }
+        return M == -INFINITY ? 0.f : M;
+    };
+    // the sums of 2^(m - M) l and 2^(m - M) o, in the CTAs' order
+    auto totals = [&](int hl, int idx, float M, float &sum, float &o) {
+        sum = o = 0.f;
+        for (int x0 = 0; x0 < ctas; x0 += kAtOnce) {
+            float m[kAtOnce], l[kAtOnce], v[kAtOnce];
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x)
+                if (x0 + x < ctas) {
+                    m[x] = of(part_m, x0 + x)[hl];
+                    l[x] = of(part_l, x0 + x)[hl];
+                    v[x] = of(part_o, x0 + x)[idx];
+                }
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x)
+                if (x0 + x < ctas) {
+                    const float e = ptx::ex2(m[x] - M);
+                    sum += e * l[x];
+                    o += e * v[x];
+                }
+        }
+    };
+    for (int idx = rank * kThreads + (int)threadIdx.x; ctas > 1 && idx < G * D; idx += ctas * kThreads) {
+        float sum, o;
+        totals(idx / D, idx, maximum(idx / D), sum, o);
         p.out[((size_t)b * Hq + (size_t)g * G) * D + idx] = __float2bfloat16_rn(sum != 0.f ? o / sum : o);
     }
     if constexpr (kWeights) {
         float *all_m = f + L::kAllM, *all_l = f + L::kAllL;
         if (threadIdx.x < (unsigned)G) {
-            const int hl = threadIdx.x;
-            float M = -INFINITY;
-            for (int x = 0; x < ctas; ++x)
-                M = fmaxf(M, of(part_m, x)[hl]);
-            const float rf = M == -INFINITY ? 0.f : M;
-            float sum = 0.f;
-            for (int x = 0; x < ctas; ++x)
-                sum += ptx::ex2(of(part_m, x)[hl] - rf) * of(part_l, x)[hl];
-            all_m[hl] = rf;
-            all_l[hl] = sum != 0.f ? 1.f / sum : 0.f; // (every weight is 0 then)
+            float sum, o;
+            const float M = maximum(threadIdx.x);
+            totals(threadIdx.x, 0, M, sum, o);
+            all_m[threadIdx.x] = M;
+            all_l[threadIdx.x] = sum != 0.f ? 1.f / sum : 0.f; // (every weight is 0 then)
         }
         __syncthreads();
         // a key per lane and 16 of a chunk, kKeys loads of each in flight
@@ -579,6 +602,8 @@ int launch(const WindowArgs &a, const WinParams &p, int ctas, cudaStream_t strea
     using L = WinLayout<D, NT, kInt8>;
     if (int rc = ensure_smem<decode_window_kernel<D, NT, kInt8, kWeights>>(L::kSmemBytes, "window decode"))
         return rc;
+    if (int rc = ensure_wide_clusters<decode_window_kernel<D, NT, kInt8, kWeights>>("window decode"))
+        return rc;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.num_seqs * a.dims.num_kv_heads * ctas));
     cfg.blockDim = dim3(kThreads);
@@ -628,20 +653,25 @@ int launch_decode_window(const WindowArgs &a, void *stream)
     p.window = a.window, p.sinks = a.sinks;
     p.decay = a.decay, p.scores = a.scores, p.scores_out = a.scores_out, p.raw = a.raw;
     p.raw_heads = window_raw_heads(a.dims);
-    // CTAs per (sequence, KV head), up to eight: as many as run at once (clusters of a second wave wait for whole ones of
-    // the first: 200 sequences of 4 KV heads and 1000 keys took 66.8 us with one CTA each, 88.2 with two; 19 of 16384
-    // keys 141 with one, 100 with two), a little less than the SMs have room for, since a cluster stays in one GPC (64
-    // clusters of six 6.2 us, of seven, in 456 places, 9.2).  Where contexts are seen whole their lengths differ, and
-    // up to four CTAs, 1024 in all, even them out (64 of 4096 to 8192 keys: 175 us with one, 153 with four; 256 of up
-    // to 2000: 98 with one, 118 with four).  No more than have a chunk of keys for each warp.
+    // CTAs per (sequence, KV head): as many as run at once (clusters of a second wave wait for whole ones of the first: 200
+    // sequences of 4 KV heads and 1000 keys took 66.8 us with one CTA each, 88.2 with two; 19 of 16384 keys 141 with
+    // one, 100 with two), a little less than the SMs have room for, since a cluster stays in one GPC (64 clusters of six
+    // 6.2 us, of seven, in 456 places, 9.2).  Where contexts are seen whole their lengths differ, and up to four CTAs,
+    // 1024 in all, even them out (64 of 4096 to 8192 keys: 175 us with one, 153 with four; 256 of up to 2000: 98 with
+    // one, 118 with four).
     const int64_t units = (int64_t)a.num_seqs * a.dims.num_kv_heads;
     const int64_t room = (int64_t)a.max_blocks_per_seq * a.dims.block_size;
-    const int64_t most = (int64_t)a.window + a.sinks;
+    const int64_t most = (int64_t)a.window + a.sinks, keys = std::min(room, most);
     const int64_t slots = (int64_t)sms * (!a.k_scale ? p.group > 8 ? 2 : 3 : p.group > 8 ? 3 : 4); // (the launch bounds)
     int64_t ctas = std::max<int64_t>(1, slots * 85 / 100 / units);
     if (room <= most)
         ctas = std::max(ctas, std::min<int64_t>(4, (1024 + units - 1) / units));
-    ctas = std::min({ctas, (int64_t)8, (std::min(room, most) + kWarps * 16 - 1) / (kWarps * 16)});
+    // No more than eight, with two chunks of keys a warp (eight sequences of 516 keys and 8 KV heads, INT8: 6.3 us with
+    // four, 7.2 with five to eight), or than 16, with five (one sequence of 8192 keys and 4 KV heads: 13.0 us with
+    // eight, 9.9 with 16; five of 2000 keys 7.7 and 8.5).
+    const int64_t chunk = kWarps * 16;
+    ctas = std::min(ctas, std::max(std::clamp<int64_t>(keys / (2 * chunk), 1, 8),
+                                   std::min<int64_t>(kMaxCtas, keys / (5 * chunk))));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool two = p.group > 8;
     if (a.dims.head_dim == 128)

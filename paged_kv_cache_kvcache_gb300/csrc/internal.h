@@ -75,6 +75,25 @@ int ensure_smem(int bytes, const char *what)
     return PA_OK;
 }
 
+// Allow a kernel clusters of more than eight CTAs, once per device.
+template <auto Kernel>
+int ensure_wide_clusters(const char *what)
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return fail(PA_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit))
+        return PA_OK;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess)
+        return fail(PA_ERR_CUDA, "%s cluster attribute: %s", what, cudaGetErrorString(e));
+    done.fetch_or(bit, std::memory_order_release);
+    return PA_OK;
+}
+
 // Number of SMs of the current device (looked up once per device).
 inline int sm_count(int *n)
 {
