@@ -22,6 +22,7 @@ WINDOWS = [  # lengths, window, sinks, block size
     ([900, 40, 0, 2500], EVERYTHING, 0, 16),
     ([257] * 40, 31, 300, 16),
     ([1024] * 3, 5, 5, 1024),
+    ([70000, 2, 65537], 1000, 30, 16),
 ]
 
 

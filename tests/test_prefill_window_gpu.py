@@ -105,3 +105,8 @@ def test_captured_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("int8", [False, True], ids=["bf16", "int8"])
+def test_a_few_queries_far_into_long_sequences(int8):
+    run([(70000, 40), (33000, 200), (65537, 1)], 300, 10, 16, (4, 1, 64), int8, 7)
