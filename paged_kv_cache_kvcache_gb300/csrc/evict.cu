@@ -14,10 +14,11 @@
 // rounds of counting 2, the places 2).  The move: a CTA takes a slice of the token rows of one (row,
 // layer, K or V) and walks the places upwards: as kept[k] >= k, a batch's places lie below the next
 // batch's sources, so it moves in place, the next batch's loads in flight while this one's are stored.  Bound by
-// HBM (each moved token read and written once: 16 rows of 4096 to 2048 tokens in 28 layers 605 us, 6.2 TB/s; a row's
+// HBM (each moved token read and written once: 16 rows of 4096 to 2048 tokens in 28 layers 600 us, 6.3 TB/s; a row's
 // places and tokens are looked up 1024 at a time, which took it from 1013).  The last CTA of a row changes its table, length and counts.
 // The call is all or nothing: the choice checks every row, and the move looks at all verdicts first.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -63,28 +64,44 @@ __device__ __forceinline__ uint32_t order(float x)
 
 // The sum over the heads, as exact as a 64-bit sum to within fp32's last bit: s + e is carried without
 // rounding errors but those of e (two-sum; fp64 adds run at 1/64 of fp32's rate and took longer than the reads).
-__device__ __forceinline__ uint32_t total_of(const float *at, int heads, int64_t pitch)
+// Of kTokens tokens, `step` apart and before `left`, with kHeads of each one's scores in flight together.
+template <int kTokens, int kHeads, class Out>
+__device__ __forceinline__ void totals_of(const float *at, int left, int step, int heads, int64_t pitch, Out out)
 {
-    constexpr int kLoads = 8; // in flight together
-    float s = 0.f, e = 0.f;
-    for (int h0 = 0; h0 < heads; h0 += kLoads) {
-        float x[kLoads];
+    float s[kTokens], e[kTokens];
 #pragma unroll
-        for (int h = 0; h < kLoads; ++h)
-            x[h] = h0 + h < heads ? at[(h0 + h) * pitch] : 0.f;
+    for (int t = 0; t < kTokens; ++t)
+        s[t] = e[t] = 0.f;
+    for (int h0 = 0; h0 < heads; h0 += kHeads) {
+        float x[kTokens][kHeads];
 #pragma unroll
-        for (int h = 0; h < kLoads; ++h) {
-            const float t = __fadd_rn(s, x[h]);
-            const float b = __fsub_rn(t, s);
-            e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(x[h], b)));
-            s = t;
-        }
+        for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t)
+                x[t][h] = h0 + h < heads && t * step < left ? at[(h0 + h) * pitch + t * step] : 0.f;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+            for (int t = 0; t < kTokens; ++t) {
+                const float u = __fadd_rn(s[t], x[t][h]);
+                const float b = __fsub_rn(u, s[t]);
+                e[t] = __fadd_rn(e[t], __fadd_rn(__fsub_rn(s[t], __fsub_rn(u, b)), __fsub_rn(x[t][h], b)));
+                s[t] = u;
+            }
     }
-    return order(isfinite(s) ? __fadd_rn(s, e) : s);
+#pragma unroll
+    for (int t = 0; t < kTokens; ++t)
+        if (t * step < left)
+            out(t * step, order(isfinite(s[t]) ? __fadd_rn(s[t], e[t]) : s[t]));
 }
 
 // The same out of line, for rows whose keys do not fit shared memory.
-__device__ __noinline__ uint32_t total_far(const float *at, int heads, int64_t pitch) { return total_of(at, heads, pitch); }
+__device__ __noinline__ uint32_t total_far(const float *at, int heads, int64_t pitch)
+{
+    uint32_t key;
+    totals_of<1, 8>(at, 1, 1, heads, pitch, [&](int, uint32_t x) { key = x; });
+    return key;
+}
 
 // exclusive sum over the CTA's threads; *sum: all
 __device__ __forceinline__ int scan_cta(int v, int *warps, int *sum)
@@ -156,8 +173,19 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
     const bool stored = n <= p.keys;
     const int begin = p.first, end = n - p.last; // of those to choose from
     if (stored) {
-        for (int j = tid; j < n; j += kChooseThreads)
-            keys[j] = j >= begin && j < end ? total_of(scores + j, p.num_kv_heads, room) : 0u;
+        // eight or more scores of a thread in flight together
+        auto form = [&](auto tokens, auto heads) {
+            for (int j = begin + tid; j < end; j += tokens.value * kChooseThreads)
+                totals_of<tokens.value, heads.value>(scores + j, end - j, kChooseThreads, p.num_kv_heads, room,
+                                                     [&](int o, uint32_t x) { keys[j + o] = x; });
+        };
+        using std::integral_constant;
+        if (p.num_kv_heads == 1)
+            form(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+        else if (p.num_kv_heads <= 4)
+            form(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+        else
+            form(integral_constant<int, 2>{}, integral_constant<int, 8>{});
     }
     const int refs0 = tid < pages && (uint32_t)page0 < (uint32_t)p.num_blocks ? p.refs[page0] : 0;
     auto key = [&](int j) { return stored ? keys[j] : total_far(scores + j, p.num_kv_heads, room); };
@@ -276,17 +304,27 @@ struct MovePlanes {
     int32_t layers, token_bytes; // bytes of a token's row in one layer of k (or v)
     int32_t log_slice;           // 16-byte vectors of a slice, as a power of two
     int32_t slices;              // slices of a token's row
-    int32_t units;               // per row: (layer, K or V, slice), then (layer, K or V, head) of the scales, then heads
+    int32_t log_heads;           // heads whose scales move together, as a power of two
+    int32_t parts;               // such groups of heads; bf16: 0
+    int32_t units;               // per row: (layer, K or V, slice), then (layer, K or V, part) of the scales, then heads
                                  // of the scores
 };
 
 // Elements T of the places [from, count) from where their tokens are: `map` (of kBatchTokens places at a time) holds
-// each place's and its token's slot, element e of slot x is at(x, e); a token has per <= 2^log_per of them.
-template <class T, class At>
+// each place's and its token's slot, element e of slot x is at(x, e); a token has per <= 2^log_per of them.  Threads of a
+// warp take elements of one token or, kAcross, tokens of one element: what lies side by side in a page.
+template <class T, bool kAcross, class At>
 __device__ __forceinline__ void move_up(const int32_t *kept, const int32_t *table, int log_bs, int from, int count, int per,
                                         int log_per, int2 *map, At at)
 {
-    const int tokens = kBatchTokens >> log_per; // of a batch
+    static_assert(kMoveThreads == 256 && kVecs == 4, "shifts below");
+    // log of a batch's tokens; thread t's u-th element is of token (t & mask) or t >> log_per, and so on
+    const int log_tokens = 10 - log_per, tokens = 1 << log_tokens;
+    const int tid = threadIdx.x;
+    auto token_of = [&](int u) {
+        return kAcross ? (u * kMoveThreads + tid) & (tokens - 1) : (tid >> log_per) + u * (kMoveThreads >> log_per);
+    };
+    auto elem_of = [&](int u) { return kAcross ? (u * kMoveThreads + tid) >> log_tokens : tid & ((1 << log_per) - 1); };
     auto slot = [&](int token) { return (table[token >> log_bs] << log_bs) + (token & ((1 << log_bs) - 1)); };
     for (int base = from; base < count; base += kBatchTokens) {
         const int n = min(count - base, kBatchTokens);
@@ -298,8 +336,7 @@ __device__ __forceinline__ void move_up(const int32_t *kept, const int32_t *tabl
         auto load = [&](int first, T(&x)[kVecs]) {
 #pragma unroll
             for (int u = 0; u < kVecs; ++u) {
-                const int e = u * kMoveThreads + (int)threadIdx.x;
-                const int k = first + (e >> log_per), v = e & ((1 << log_per) - 1);
+                const int k = first + token_of(u), v = elem_of(u);
                 if (k < n && v < per)
                     x[u] = *at(map[k].y, v);
             }
@@ -307,8 +344,7 @@ __device__ __forceinline__ void move_up(const int32_t *kept, const int32_t *tabl
         auto store = [&](int first, const T(&x)[kVecs]) {
 #pragma unroll
             for (int u = 0; u < kVecs; ++u) {
-                const int e = u * kMoveThreads + (int)threadIdx.x;
-                const int k = first + (e >> log_per), v = e & ((1 << log_per) - 1);
+                const int k = first + token_of(u), v = elem_of(u);
                 if (k < n && v < per)
                     *at(map[k].x, v) = x[u];
             }
@@ -356,17 +392,18 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
         const int plane = unit / q.slices, slice = unit - plane * q.slices;
         const int per = min(1 << q.log_slice, q.token_bytes / 16 - (slice << q.log_slice));
         char *base = (plane & 1 ? q.v : q.k) + (plane >> 1) * q.layer + ((int64_t)slice << q.log_slice) * 16;
-        move_up<uint4>(kept, table, log_bs, moved, left, per, q.log_slice, map, [&](int slot, int v) {
+        move_up<uint4, false>(kept, table, log_bs, moved, left, per, q.log_slice, map, [&](int slot, int v) {
             return reinterpret_cast<uint4 *>(base + (int64_t)slot * q.token_bytes) + v;
         });
-    } else if ((unit -= planes * q.slices) < (q.ks ? planes * p.num_kv_heads : 0)) {
-        const int plane = unit / p.num_kv_heads, head = unit - plane * p.num_kv_heads;
+    } else if ((unit -= planes * q.slices) < planes * q.parts) {
+        const int plane = unit / q.parts, head = (unit - plane * q.parts) << q.log_heads;
+        const int per = min(1 << q.log_heads, p.num_kv_heads - head);
         uint16_t *base = reinterpret_cast<uint16_t *>((plane & 1 ? q.vs : q.ks) + (plane >> 1) * q.scale_layer);
-        move_up<uint16_t>(kept, table, log_bs, moved, left, 1, 0, map, [&](int slot, int) {
-            return base + ((((int64_t)(slot >> log_bs) * p.num_kv_heads + head) << log_bs) + (slot & (bs - 1)));
+        move_up<uint16_t, true>(kept, table, log_bs, moved, left, per, q.log_heads, map, [&](int slot, int v) {
+            return base + ((((int64_t)(slot >> log_bs) * p.num_kv_heads + head + v) << log_bs) + (slot & (bs - 1)));
         });
     } else { // one head's scores, a batch read before it is written as above
-        unit -= q.ks ? planes * p.num_kv_heads : 0;
+        unit -= planes * q.parts;
         const int64_t at = ((int64_t)row * p.num_kv_heads + unit) * room;
         const float *from = p.scores + at;
         float *to = p.scores_out + at;
@@ -453,13 +490,20 @@ int launch_pool_evict(const PoolArgs &a, const int32_t *rows, int n, const float
     q.layer = o.layer_stride, q.scale_layer = o.scale_layer_stride;
     q.layers = o.num_layers;
     q.token_bytes = d.num_kv_heads * d.head_dim * (o.k_scale ? 1 : 2);
-    // slices: up to 1 KB of a token's row, less (down to 64 bytes) while that gives the SMs too few CTAs
-    const int vecs = q.token_bytes / 16;
-    q.log_slice = 6;
-    while (q.log_slice > 2 && (int64_t)n * q.layers * 2 * ((vecs + (1 << q.log_slice) - 1) >> q.log_slice) < 4 * sms)
-        --q.log_slice;
-    q.slices = (vecs + (1 << q.log_slice) - 1) >> q.log_slice;
-    const int64_t units = (int64_t)2 * q.layers * (q.slices + (q.ks ? d.num_kv_heads : 0)) + d.num_kv_heads;
+    // slices: up to 512 bytes of a token's row (of 1 KB 16 rows of 4096 to 2048 tokens in 28 layers took 616 us, of 256
+    // bytes 631, of 512 600), less (down to 64 bytes) while that gives the SMs too few CTAs.  Scales: of all heads, of
+    // fewer by the same rule (a CTA per head took 30 us longer where 36 short rows of 22 layers of 8 heads hardly move).
+    auto cut = [&](int elems, int most, int least, int32_t *log) {
+        auto parts = [&] { return (elems + (1 << *log) - 1) >> *log; };
+        for (*log = 0; *log < most && 1 << *log < elems;)
+            ++*log;
+        while (*log > least && (int64_t)n * q.layers * 2 * parts() < 4 * sms)
+            --*log;
+        return parts();
+    };
+    q.slices = cut(q.token_bytes / 16, 5, 2, &q.log_slice);
+    q.parts = q.ks ? cut(d.num_kv_heads, 6, 0, &q.log_heads) : 0;
+    const int64_t units = (int64_t)2 * q.layers * (q.slices + q.parts) + d.num_kv_heads;
     if (units * n > INT32_MAX)
         return fail(PA_ERR_UNSUPPORTED, "pa_pool_evict: %d rows of %d layers exceed one launch", n, q.layers);
     q.units = (int32_t)units;

@@ -72,6 +72,8 @@ SHAPES = [  # layers, hkv, d, bs, gap, lengths, budget, first, last
     (28, 2, 64, 16, 0, [150] * 8, 64, 4, 32),
     (1, 2, 64, 16, 0, [100, 50], 60, 60, 0),
     (1, 2, 64, 16, 0, [100, 50], 60, 0, 60),
+    (28, 3, 64, 16, 2, [90, 130] * 6, 70, 3, 9),  # (of INT8, scales of three heads move together, of four and one)
+    (16, 5, 64, 16, 0, [130, 40] * 5, 33, 0, 4),
 ]
 
 
