@@ -19,13 +19,16 @@
 // that are not seen is not read: those rows are zeros in shared memory, whatever the cache has there.  Two stages and
 // three CTAs on an SM (bf16) hide more than three stages and two did (64 x 4160 keys 86.6 -> 84.5 us, 6.5 TB/s).  INT8 codes
 // come by cp.async too: TMA boxes took a quarter fewer instructions and no less time (200 x 1004 keys 49 us against
-// 47.5, 4.2 TB/s), and five or six CTAs of two stages took 46 to 48: what is left above the bytes is the ramp, three
-// dependent look-ups and the merge of 1.3 waves, about 8 us each.
+// 47.5, now 45.4, 4.4 TB/s), and five or six CTAs of two stages took 46 to 48: what is left above the bytes is the ramp, three
+// dependent look-ups and the merge of 1.3 waves, about 7 us each.  The merges take four values a thread, with every
+// part's maximum, sum and values on their way together (8 x 600 keys with weights 8.1 -> 6.7 us; with one value a
+// thread, and the maxima first, a pair of CTAs of 16 heads spent 4 us there).
 // Weights need M and L before any of them can be formed: the scores s' wait in the workspace (16 keys of one
 // head group are 512 contiguous bytes) until the cluster has met; keys and values leave L2 first, so they wait there.
-// 64 contexts of 4096 to 8192 keys take 153 us (5.4 TB/s), 121 without weights: writing s' costs 10 of that, the second
+// 64 contexts of 4096 to 8192 keys take 150 us (5.5 TB/s), 121 without weights: writing s' costs 10 of that, the second
 // pass over them, latency for the most part, 20.
 #include <algorithm>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -123,7 +126,7 @@ __device__ __forceinline__ uint32_t swz(int t, int v)
 }
 
 template <int D, int NT, bool kInt8, bool kWeights>
-__global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, (kInt8 ? 5 : 4) - NT)
     decode_window_kernel(const WinParams p)
 {
     using L = WinLayout<D, NT, kInt8>;
@@ -469,25 +472,35 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : NT == 1 
         }
     }
     __syncthreads();
+    // four values of the output per thread and turn
     float *part_m = f + L::kPartM, *part_l = f + L::kPartL, *part_o = f + L::kPartO;
-    for (int idx = threadIdx.x; idx < G * D; idx += kThreads) {
+    __nv_bfloat16 *out = p.out + ((size_t)b * Hq + (size_t)g * G) * D;
+    auto put = [&](int idx, float sum, float4 o) { // no weight at all: 0, or NaN where a value is
+        const float x = sum != 0.f ? 1.f / sum : 1.f;
+        *reinterpret_cast<uint2 *>(out + idx) = make_uint2(ptx::pack_bf16(o.x * x, o.y * x), ptx::pack_bf16(o.z * x, o.w * x));
+    };
+    auto add = [](float4 &o, float e, float4 v) {
+        o = make_float4(fmaf(e, v.x, o.x), fmaf(e, v.y, o.y), fmaf(e, v.z, o.z), fmaf(e, v.w, o.w));
+    };
+    for (int idx = 4 * (int)threadIdx.x; idx < G * D; idx += 4 * kThreads) {
         const int hl = idx / D, d = idx % D;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w)
             M = fmaxf(M, mrg_m[w * H8 + hl]);
         const float rf = M == -INFINITY ? 0.f : M;
-        float sum = 0.f, o = 0.f;
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float e = ptx::ex2(mrg_m[w * H8 + hl] - rf);
             sum += e * mrg_l[w * H8 + hl];
-            o += e * mrg_o[(size_t)(w * H8 + hl) * L::kRow + d];
+            add(o, e, *reinterpret_cast<const float4 *>(mrg_o + (size_t)(w * H8 + hl) * L::kRow + d));
         }
-        if (ctas == 1) // no weight at all: 0, or NaN where a value is
-            p.out[((size_t)b * Hq + (size_t)g * G) * D + idx] = __float2bfloat16_rn(sum != 0.f ? o / sum : o);
+        if (ctas == 1)
+            put(idx, sum, o);
         else
-            part_o[idx] = o;
+            *reinterpret_cast<float4 *>(part_o + idx) = o;
         if (d == 0) {
             part_m[hl] = M;
             part_l[hl] = sum;
@@ -504,52 +517,50 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : NT == 1 
     // for a cluster of 16, one more for one of five).
     constexpr int kAtOnce = 8;
     auto of = [&](float *at, int cta) { return ctas > 1 ? cluster.map_shared_rank(at, cta) : at; };
-    auto maximum = [&](int hl) { // 0 where it is -inf
-        float M = -INFINITY;
-        for (int x0 = 0; x0 < ctas; x0 += kAtOnce) {
-            float m[kAtOnce];
-#pragma unroll
-            for (int x = 0; x < kAtOnce; ++x)
-                m[x] = x0 + x < ctas ? of(part_m, x0 + x)[hl] : -INFINITY;
-#pragma unroll
-            for (int x = 0; x < kAtOnce; ++x)
-                M = fmaxf(M, m[x]);
-        }
-        return M == -INFINITY ? 0.f : M;
-    };
     // the sums of 2^(m - M) l and 2^(m - M) o, in the CTAs' order
-    auto totals = [&](int hl, int idx, float M, float &sum, float &o) {
-        sum = o = 0.f;
+    auto totals = [&](auto with, int hl, int idx, float &M, float &sum, float4 &o) {
+        M = -INFINITY, sum = 0.f, o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int x0 = 0; x0 < ctas; x0 += kAtOnce) {
-            float m[kAtOnce], l[kAtOnce], v[kAtOnce];
+            float m[kAtOnce], l[kAtOnce];
+            float4 v[kAtOnce];
 #pragma unroll
-            for (int x = 0; x < kAtOnce; ++x)
+            for (int x = 0; x < kAtOnce; ++x) {
+                m[x] = -INFINITY, l[x] = 0.f, v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (x0 + x < ctas) {
                     m[x] = of(part_m, x0 + x)[hl];
                     l[x] = of(part_l, x0 + x)[hl];
-                    v[x] = of(part_o, x0 + x)[idx];
+                    if constexpr (with.value)
+                        v[x] = *reinterpret_cast<const float4 *>(of(part_o, x0 + x) + idx);
                 }
+            }
+            const float before = M;
 #pragma unroll
             for (int x = 0; x < kAtOnce; ++x)
-                if (x0 + x < ctas) {
-                    const float e = ptx::ex2(m[x] - M);
-                    sum += e * l[x];
-                    o += e * v[x];
-                }
+                M = fmaxf(M, m[x]);
+            const float rf = M == -INFINITY ? 0.f : M, al = ptx::ex2(before - rf);
+            sum *= al;
+            o = make_float4(o.x * al, o.y * al, o.z * al, o.w * al);
+#pragma unroll
+            for (int x = 0; x < kAtOnce; ++x) {
+                const float e = ptx::ex2(m[x] - rf);
+                sum += e * l[x];
+                add(o, e, v[x]);
+            }
         }
     };
-    for (int idx = rank * kThreads + (int)threadIdx.x; ctas > 1 && idx < G * D; idx += ctas * kThreads) {
-        float sum, o;
-        totals(idx / D, idx, maximum(idx / D), sum, o);
-        p.out[((size_t)b * Hq + (size_t)g * G) * D + idx] = __float2bfloat16_rn(sum != 0.f ? o / sum : o);
+    for (int idx = 4 * (rank * kThreads + (int)threadIdx.x); ctas > 1 && idx < G * D; idx += 4 * ctas * kThreads) {
+        float M, sum;
+        float4 o;
+        totals(std::true_type{}, idx / D, idx, M, sum, o);
+        put(idx, sum, o);
     }
     if constexpr (kWeights) {
         float *all_m = f + L::kAllM, *all_l = f + L::kAllL;
         if (threadIdx.x < (unsigned)G) {
-            float sum, o;
-            const float M = maximum(threadIdx.x);
-            totals(threadIdx.x, 0, M, sum, o);
-            all_m[threadIdx.x] = M;
+            float M, sum;
+            float4 o;
+            totals(std::false_type{}, threadIdx.x, 0, M, sum, o);
+            all_m[threadIdx.x] = M == -INFINITY ? 0.f : M;
             all_l[threadIdx.x] = sum != 0.f ? 1.f / sum : 0.f; // (every weight is 0 then)
         }
         __syncthreads();
@@ -596,13 +607,54 @@ __global__ void __launch_bounds__(kThreads, kInt8 ? (NT == 1 ? 4 : 3) : NT == 1 
         cluster.sync(); // the others may still read this CTA's results
 }
 
+// CTAs per (sequence, KV head): as many as run at once (clusters of a second wave wait for whole ones of the first: 200
+// sequences of 4 KV heads and 1000 keys took 66.8 us with one CTA each, 88.2 with two; 19 of 16384 keys 141 with
+// one, 100 with two).  A cluster stays in one GPC, so that fewer fit than there are places (64 clusters of six 6.2 us, of seven,
+// in 456 places, 9.2).
 template <int D, int NT, bool kInt8, bool kWeights>
-int launch(const WindowArgs &a, const WinParams &p, int ctas, cudaStream_t stream)
+int count_ctas(const WindowArgs &a, int *ctas)
+{
+    using L = WinLayout<D, NT, kInt8>;
+    const int64_t units = (int64_t)a.num_seqs * a.dims.num_kv_heads;
+    const int64_t room = (int64_t)a.max_blocks_per_seq * a.dims.block_size;
+    const int64_t most = (int64_t)a.window + a.sinks, keys = std::min(room, most);
+    // No more than four, with 64 keys each (one sequence of 320 keys and 8 KV heads, INT8: 7.0 us with one, 6.0 with two,
+    // 5.5 with four to eight), than eight, with 128, or than 16, with 224 (six of 3624 keys 17.1 us with four, 11.4 with
+    // eight, 9.5 with 16; ten of 2480 10.5 with eight, 9.5 with twelve, 9.9 with 16).
+    int64_t n = std::max({std::clamp<int64_t>(keys / 64, 1, 4), std::min<int64_t>(8, keys / 128),
+                          std::min<int64_t>(kMaxCtas, keys / 224)});
+    auto fit = [&](int64_t c, int *clusters) {
+        return active_clusters<decode_window_kernel<D, NT, kInt8, kWeights>>("window decode", (int)c, kThreads, L::kSmemBytes,
+                                                                             clusters);
+    };
+    int at_once = 0;
+    if (int rc = fit(1, &at_once))
+        return rc;
+    for (n = std::clamp<int64_t>(at_once / units, 1, n); n > 1; --n) {
+        if (int rc = fit(n, &at_once))
+            return rc;
+        if (at_once >= units)
+            break;
+    }
+    // Where contexts are seen whole their lengths differ, and up to eight CTAs of 1024 keys, 1024 CTAs in all, even them
+    // out (64 sequences of 4096 to 8192 keys and 4 KV heads: 175 us with one, 153 with four; 18 of up to 13634 and 8: 120
+    // with three, 111 with eight; 60 of up to 516 and 8: 12.2 with one, 19.2 with two).
+    if (room <= most)
+        n = std::max(n, std::min({(int64_t)8, (1024 + units - 1) / units, room / 1024}));
+    *ctas = (int)n;
+    return PA_OK;
+}
+
+template <int D, int NT, bool kInt8, bool kWeights>
+int launch(const WindowArgs &a, const WinParams &p, cudaStream_t stream)
 {
     using L = WinLayout<D, NT, kInt8>;
     if (int rc = ensure_smem<decode_window_kernel<D, NT, kInt8, kWeights>>(L::kSmemBytes, "window decode"))
         return rc;
     if (int rc = ensure_wide_clusters<decode_window_kernel<D, NT, kInt8, kWeights>>("window decode"))
+        return rc;
+    int ctas = 1;
+    if (int rc = count_ctas<D, NT, kInt8, kWeights>(a, &ctas))
         return rc;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.num_seqs * a.dims.num_kv_heads * ctas));
@@ -625,20 +677,17 @@ int launch(const WindowArgs &a, const WinParams &p, int ctas, cudaStream_t strea
 }
 
 template <int D, int NT>
-int launch_kind(const WindowArgs &a, const WinParams &p, int ctas, cudaStream_t s)
+int launch_kind(const WindowArgs &a, const WinParams &p, cudaStream_t s)
 {
     if (a.raw)
-        return a.k_scale ? launch<D, NT, true, true>(a, p, ctas, s) : launch<D, NT, false, true>(a, p, ctas, s);
-    return a.k_scale ? launch<D, NT, true, false>(a, p, ctas, s) : launch<D, NT, false, false>(a, p, ctas, s);
+        return a.k_scale ? launch<D, NT, true, true>(a, p, s) : launch<D, NT, false, true>(a, p, s);
+    return a.k_scale ? launch<D, NT, true, false>(a, p, s) : launch<D, NT, false, false>(a, p, s);
 }
 
 } // namespace
 
 int launch_decode_window(const WindowArgs &a, void *stream)
 {
-    int sms = 0;
-    if (int rc = sm_count(&sms))
-        return rc;
     WinParams p{};
     p.q = static_cast<const __nv_bfloat16 *>(a.q);
     p.k_cache = a.k_cache, p.v_cache = a.v_cache;
@@ -653,30 +702,11 @@ int launch_decode_window(const WindowArgs &a, void *stream)
     p.window = a.window, p.sinks = a.sinks;
     p.decay = a.decay, p.scores = a.scores, p.scores_out = a.scores_out, p.raw = a.raw;
     p.raw_heads = window_raw_heads(a.dims);
-    // CTAs per (sequence, KV head): as many as run at once (clusters of a second wave wait for whole ones of the first: 200
-    // sequences of 4 KV heads and 1000 keys took 66.8 us with one CTA each, 88.2 with two; 19 of 16384 keys 141 with
-    // one, 100 with two), a little less than the SMs have room for, since a cluster stays in one GPC (64 clusters of six
-    // 6.2 us, of seven, in 456 places, 9.2).  Where contexts are seen whole their lengths differ, and up to four CTAs,
-    // 1024 in all, even them out (64 of 4096 to 8192 keys: 175 us with one, 153 with four; 256 of up to 2000: 98 with
-    // one, 118 with four).
-    const int64_t units = (int64_t)a.num_seqs * a.dims.num_kv_heads;
-    const int64_t room = (int64_t)a.max_blocks_per_seq * a.dims.block_size;
-    const int64_t most = (int64_t)a.window + a.sinks, keys = std::min(room, most);
-    const int64_t slots = (int64_t)sms * (!a.k_scale ? p.group > 8 ? 2 : 3 : p.group > 8 ? 3 : 4); // (the launch bounds)
-    int64_t ctas = std::max<int64_t>(1, slots * 85 / 100 / units);
-    if (room <= most)
-        ctas = std::max(ctas, std::min<int64_t>(4, (1024 + units - 1) / units));
-    // No more than eight, with two chunks of keys a warp (eight sequences of 516 keys and 8 KV heads, INT8: 6.3 us with
-    // four, 7.2 with five to eight), or than 16, with five (one sequence of 8192 keys and 4 KV heads: 13.0 us with
-    // eight, 9.9 with 16; five of 2000 keys 7.7 and 8.5).
-    const int64_t chunk = kWarps * 16;
-    ctas = std::min(ctas, std::max(std::clamp<int64_t>(keys / (2 * chunk), 1, 8),
-                                   std::min<int64_t>(kMaxCtas, keys / (5 * chunk))));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool two = p.group > 8;
     if (a.dims.head_dim == 128)
-        return two ? launch_kind<128, 2>(a, p, (int)ctas, s) : launch_kind<128, 1>(a, p, (int)ctas, s);
-    return two ? launch_kind<64, 2>(a, p, (int)ctas, s) : launch_kind<64, 1>(a, p, (int)ctas, s);
+        return two ? launch_kind<128, 2>(a, p, s) : launch_kind<128, 1>(a, p, s);
+    return two ? launch_kind<64, 2>(a, p, s) : launch_kind<64, 1>(a, p, s);
 }
 
 int read_window_error(uint32_t *code)

@@ -1,6 +1,7 @@
 // Internal declarations shared by the host-side translation units of libpagedattn.
 #pragma once
 
+#include <algorithm>
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
@@ -91,6 +92,38 @@ int ensure_wide_clusters(const char *what)
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "%s cluster attribute: %s", what, cudaGetErrorString(e));
     done.fetch_or(bit, std::memory_order_release);
+    return PA_OK;
+}
+
+// How many clusters of `ctas` CTAs (of up to 16) the current device runs at once, asked once per device.
+template <auto Kernel>
+int active_clusters(const char *what, int ctas, unsigned threads, size_t smem, int *n)
+{
+    static std::atomic<int> cached[64][17];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return fail(PA_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    const bool slot = dev >= 0 && dev < 64;
+    if (slot && (*n = cached[dev][ctas].load(std::memory_order_relaxed)) > 0)
+        return PA_OK;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {(unsigned)ctas, 1, 1};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(n, Kernel, &cfg);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PA_ERR_CUDA, "%s clusters: %s", what, cudaGetErrorString(e));
+    }
+    *n = std::max(*n, 1);
+    if (slot)
+        cached[dev][ctas].store(*n, std::memory_order_relaxed);
     return PA_OK;
 }
 
