@@ -365,7 +365,6 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
 {
     __shared__ uint32_t place;
     __shared__ int2 map[kBatchTokens];
-    ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const int i = blockIdx.x / q.units;
     int unit = blockIdx.x - i * q.units;
@@ -424,6 +423,8 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
         for (int k = left + tid; k < n; k += kMoveThreads)
             to[k] = 0.f;
     }
+
+    ptx::launch_dependents(); // (at the start the next launch's CTAs would take this one's places)
 
     // the row's last unit: nothing reads its table any more
     __syncthreads();
