@@ -564,14 +564,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0u;
         ptx::fence_mbar_init();
     }
+    // Launched while the one ahead drains: nothing of memory is read before here, and no tensor memory held, which a
+    // launch further ahead may yet ask for (in a stream 4 x 4096, window 1024, 178.9 -> 176.9 us, 16 INT8 chunks 86.2 ->
+    // 84.0; let in at the start of the gather, the CTAs take its places: 87.7).
+    if constexpr (kWin)
+        ptx::grid_dependency_wait();
     if (warp == kMmaWarp) {
         ptx::tmem_alloc(bars.tmem_slot(), kTmemCols);
         ptx::tmem_relinquish();
     }
-    // Launched while the one ahead drains: nothing of memory is read before here (in a stream 4 x 4096, window 1024, 178.9 ->
-    // 176.9 us, 16 INT8 chunks 86.2 -> 84.0; let in at the start of the gather, the CTAs take its places: 87.7).
-    if constexpr (kWin)
-        ptx::grid_dependency_wait();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();

@@ -110,3 +110,61 @@ def test_captured_and_on_another_stream():
 @pytest.mark.parametrize("int8", [False, True], ids=["bf16", "int8"])
 def test_a_few_queries_far_into_long_sequences(int8):
     run([(70000, 40), (33000, 200), (65537, 1)], 300, 10, 16, (4, 1, 64), int8, 7)
+
+
+@pytest.mark.parametrize("int8", [False, True], ids=["bf16", "int8"])
+@pytest.mark.parametrize("heads", [(16, 8, 128), (4, 2, 64)], ids=lambda h: "-".join(map(str, h)))
+def test_behind_the_launch_that_writes_its_queries_and_keys(heads, int8):
+    """Rotation and store, prefill and a step of decode without a pause, many times over: as with one after each call."""
+    (hq, hkv, d), bs, lens, window, sinks = heads, 16, [700, 33, 1200], 300, 20
+    blocks = sum(-(-n // bs) for n in lens)
+    dims = pa.make_dims(blocks, bs, hq, hkv, d)
+    g = np.random.default_rng(3)
+    ids = np.split(g.permutation(blocks), np.cumsum([-(-n // bs) for n in lens])[:-1])
+    at = [i[np.arange(n) // bs] * bs + np.arange(n) % bs for i, n in zip(ids, lens)]
+    slots = torch.tensor(np.concatenate(at), dtype=torch.int32, device="cuda")
+    pos = torch.tensor(np.concatenate([np.arange(n) for n in lens]), dtype=torch.int32, device="cuda")
+    table = np.zeros((len(lens), max(map(len, ids))), np.int32)
+    for row, i in zip(table, ids):
+        row[:len(i)] = i
+    table, ctx = torch.tensor(table, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    plan = pa.pa_pack_prefill(dims, lens, lens, [list(i) for i in ids]).upload()
+    ws = pa.prefill_workspace(plan) if int8 else None
+    angle = torch.arange(2000)[:, None] * 1e4 ** (-torch.arange(d // 2) / (d // 2))
+    rope = pa.Rope(dims, torch.cat([angle.cos(), angle.sin()], 1).float().contiguous().cuda())
+    caches = pa.int8_cache(dims) if int8 else tuple(torch.zeros(blocks, bs, hkv, d, dtype=torch.bfloat16, device="cuda")
+                                                    for _ in range(2))
+    store, prefill, decode = ((pa.pa_rope_store_int8, pa.pa_prefill_window_int8, pa.pa_decode_window_int8) if int8 else
+                              (pa.pa_rope_store, pa.pa_prefill_window, pa.pa_decode_window))
+    scale = d ** -0.5
+    gen = torch.Generator("cuda").manual_seed(1)
+    rounds = [torch.randn(sum(lens), hq + 2 * hkv, d, device="cuda", generator=gen).to(torch.bfloat16) for _ in range(12)]
+
+    def go(pause):
+        outs = []
+        for x in rounds:
+            q, out = (torch.empty(sum(lens), hq, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+            step = torch.empty(len(lens), hq, d, dtype=torch.bfloat16, device="cuda")
+            pause()
+            store(dims, rope, x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:], pos, slots, q, *caches)
+            pause()
+            prefill(dims, q, *caches, plan, window, sinks, scale, out, *([ws] if int8 else []))
+            pause()
+            decode(dims, x[:len(lens), :hq].contiguous(), *caches, table, ctx, window, sinks, scale, step)
+            pause()
+            outs += [q, out, step]
+        torch.cuda.synchronize()
+        return outs
+
+    want = go(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(go(lambda: None), want))
+    # the last round against the formula, on what the cache holds
+    kv = [c.flatten(0, 1).double().cpu().numpy() for c in caches[:2]]
+    if int8:  # code * scale: as bf16 for the prompts
+        kv = [c * s.transpose(1, 2).flatten(0, 1).double().cpu().numpy()[..., None] for c, s in zip(kv, caches[2:])]
+        kv = [torch.tensor(c).to(torch.bfloat16).double().numpy() for c in kv]
+    c = Case.__new__(Case)
+    c.hq, c.hkv, c.lens, c.slots, c.window, c.sinks, c.scale, c.kd, c.vd = hq, hkv, lens, at, window, sinks, scale, *kv
+    out, size = model(c, want[-3].cpu(), lens)
+    near(want[-2], out, size)
