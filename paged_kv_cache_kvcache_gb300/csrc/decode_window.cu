@@ -37,6 +37,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "quant.cuh"
 
 namespace pa {
 
@@ -261,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, (kInt8 ? 5 : 4) - NT)
 
     float acc[NT][D / 16][4];
     float m_r[NT][2], l_r[NT][2];
+    float by = quant::kProductsBy; // INT8: acc is this many times the sums
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         m_r[nt][0] = m_r[nt][1] = -INFINITY;
@@ -334,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, (kInt8 ? 5 : 4) - NT)
         if constexpr (kInt8) { // the scales of keys that are not seen may be anything
             vs0 = seen0 ? vs0 : 0.f;
             vs1 = seen1 ? vs1 : 0.f;
+            quant::fit_products(vs0, vs1, by, acc);
         }
         uint32_t pb[NT][2];
 #pragma unroll
@@ -375,7 +378,8 @@ __global__ void __launch_bounds__(kThreads, (kInt8 ? 5 : 4) - NT)
                     acc[nt][mi][3] *= al1;
                 }
             }
-            // weights in the products' type: bf16 (2^-8), over INT8 f16 (2^-11), both within the result's rounding
+            // weights in the products' type: bf16 (2^-8), over INT8, with the value's scale and a factor that keeps them
+            // among fp16's normal numbers, f16 (2^-11), both within the result's rounding
             if constexpr (kInt8) {
                 pb[nt][0] = ptx::movmatrix_trans(ptx::pack_f16(p0 * vs0, p1 * vs0));
                 pb[nt][1] = ptx::movmatrix_trans(ptx::pack_f16(p2 * vs1, p3 * vs1));
@@ -439,6 +443,17 @@ __global__ void __launch_bounds__(kThreads, (kInt8 ? 5 : 4) - NT)
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1)
                 l_r[nt][j] += __shfl_xor_sync(0xffffffffu, l_r[nt][j], o);
+
+    if constexpr (kInt8) {
+        const float x = __fdiv_rn(1.f, by);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mi = 0; mi < D / 16; ++mi)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[nt][mi][e] *= x;
+    }
 
     // the warps' results meet in the ring
     __syncthreads();

@@ -90,6 +90,38 @@ __device__ __forceinline__ void codes_of_16(const float (&x)[16], float scale, f
     }
 }
 
+// The factor of a warp's fp16 products P v_scale (P <= 1): a power of two, `by`, that keeps the largest v_scale so far
+// times by in [2^14, 2^15) or a little above it, so that a product is rounded by 2^-11 of itself down to P of 2^-28 (an
+// unscaled one, below 2^-14, by 2^-25: the keys behind a first key that outweighs them by e^10 lost up to all of their
+// share).  In come the scales of two keys of a 16-key chunk (0 for keys that are not seen), out they go times by; where
+// one would pass fp16's range by falls, and the sums that hold it follow.  Starts at kProductsBy, for fp16's smallest scale;
+// falls with the first chunk and then hardly ever, so that a chunk costs two products, a maximum and a vote.
+constexpr float kProductsBy = 0x1p+38f;
+template <int NT, int M>
+__device__ __forceinline__ void fit_products(float &vs0, float &vs1, float &by, float (&acc)[NT][M][4])
+{
+    constexpr float kTop = 0x1.ep+15f; // under 65504 by more than the products' rounding
+    vs0 *= by;
+    vs1 *= by;
+    const float top = fmaxf(fabsf(vs0), fabsf(vs1));
+    if (__any_sync(0xffffffffu, top > kTop)) {
+        // 2^14 over the largest one's power of two; an infinite scale leaves by at fp16's least, 1/2
+        const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(top)) >> 23;
+        const float next = fmaxf(by * __uint_as_float((268u - e) << 23), 0.5f);
+        const float al = __fdiv_rn(next, by); // (of powers of two)
+        by = next;
+        vs0 *= al;
+        vs1 *= al;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[nt][m][i] *= al;
+    }
+}
+
 template <int D>
 constexpr int kThreadsPerRow = D / 32;
 
