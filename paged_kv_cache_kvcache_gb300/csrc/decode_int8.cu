@@ -24,8 +24,9 @@
 //    pair).  Both MMAs therefore run as f16 m16n8k16 with fp32 accumulation:
 //        S^T[16 tok x 8 heads] = K_codes . Q^T,  then s *= k_scale[tok]
 //        O^T[D x 8 heads]     += V_codes^T . (P * v_scale[tok])^T
-//    The softmax normaliser sums the unscaled P.  P * v_scale never exceeds
-//    the fp16 scale itself (P <= 1), so it stays in fp16 range.
+//    The softmax normaliser sums the unscaled P.  P * v_scale carries a power
+//    of two that keeps it in fp16's range and, down to P of 2^-28, among its
+//    normal numbers (quant::fit_products).
 //  * Q is rounded to fp16 once per CTA (exact for bf16 values of magnitude in
 //    [2^-14, 65504], clamped beyond).
 //  * Operand order: the MMA contraction and the O^T rows may be permuted at
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
 
     float acc[NT][D / 16][4];
     float m_r[NT][2], l_r[NT][2];
+    float by = quant::kProductsBy; // acc is this many times the sums
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         m_r[nt][0] = m_r[nt][1] = -INFINITY;
@@ -341,8 +343,9 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
         const float ks1 = real ? lds_half(sb + 2 * (r + 8)) * p.scale_log2 : 0.f;
         const bool v0 = key0 + r < k1;
         const bool v1 = key0 + r + 8 < k1;
-        const float vs0 = v0 && real ? lds_half(sb + 32 + 2 * r) : 0.f; // rows past the context: weight 0
-        const float vs1 = v1 && real ? lds_half(sb + 32 + 2 * (r + 8)) : 0.f;
+        float vs0 = v0 && real ? lds_half(sb + 32 + 2 * r) : 0.f; // rows past the context: weight 0
+        float vs1 = v1 && real ? lds_half(sb + 32 + 2 * (r + 8)) : 0.f;
+        quant::fit_products(vs0, vs1, by, acc);
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -427,6 +430,17 @@ __global__ void __launch_bounds__(W * 32, W != kWarps ? 1 : NT == 1 ? 4 : 3)
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1)
                 l_r[nt][j] += __shfl_xor_sync(0xffffffffu, l_r[nt][j], o);
+
+    {
+        const float x = __fdiv_rn(1.f, by);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mi = 0; mi < D / 16; ++mi)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[nt][mi][e] *= x;
+    }
 
     // merge the 4 warps through shared memory (pipeline buffers are free now)
     __syncthreads();

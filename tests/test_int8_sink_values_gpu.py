@@ -72,7 +72,7 @@ CASES = [
 
 
 @pytest.mark.parametrize("c", CASES, ids=lambda c: f"{c[0]}x{c[2]}-{c[3]}-{c[4]}")
-@pytest.mark.parametrize("call", ["window", "weights"])
+@pytest.mark.parametrize("call", ["window", "weights", "plan"])
 def test_small_weights_count(c, call):
     seqs, heads, n, gap, size = c
     decode(Rows(seqs, *heads, n, gap, np.full(n, size)), call)
@@ -90,6 +90,10 @@ def decode(x, call):
         want = x.w.reshape(4, x.dims.num_kv_heads, group, -1).sum(2)[np.arange(x.seqs) % 4]
         got = scores[:, :, :x.n].double().cpu().numpy()
         assert (np.abs(got - want) <= 2e-4 * want + 1e-30).all()
+    else:
+        plan = pa.pa_pack_decode(x.dims, [x.n] * x.seqs, [list(x.ids)] * x.seqs).upload()
+        ws = torch.empty(max(256, plan.meta.workspace_bytes), dtype=torch.uint8, device="cuda")
+        pa.pa_decode_int8(x.dims, x.q_gpu, *x.gpu, plan, x.scale, out, ws)
     x.check(out)
 
 
@@ -105,6 +109,6 @@ SIZES = {  # of the values along the context
 
 
 @pytest.mark.parametrize("size", SIZES)
-@pytest.mark.parametrize("call", ["window", "weights"])
+@pytest.mark.parametrize("call", ["window", "weights", "plan"])
 def test_values_of_different_sizes(size, call):
     decode(Rows(5, 28, 4, 128, 2001, 2.0, SIZES[size](2001), high=2), call)
