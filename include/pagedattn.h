@@ -593,6 +593,8 @@ int pa_pool_compact(const pa_dims *dims, const pa_pool *pool, int32_t *remap, in
  * plan's block lists must name some block of the pool there), and what the cache
  * holds at such places takes no part.  A key that some queries see and others do
  * not must be finite.  Other arguments, errors and numerics as pa_prefill_varlen.
+ * The launch may be set up during the kernel before it in the stream; it reads
+ * nothing until that has ended, so block_tables and tiles may be what that writes.
  */
 int pa_prefill_window(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                       const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, const int32_t *block_tables,
@@ -700,7 +702,9 @@ int pa_decode_weights_int8(const pa_dims *dims, const void *q, const void *k_cac
  * length or a page outside its bounds, a page of count 0, or a page that would be
  * written while other entries name it (tokens in front of the first one that goes
  * are not written, so a shared prefix within `first` may stay shared) set bit 8;
- * then nothing changes, and kept is -1.
+ * then nothing changes, and kept is -1.  Two launches, which may be set up during
+ * the kernel before them in the stream; they read and write nothing until that has
+ * ended.
  */
 int pa_pool_evict(const pa_dims *dims, const pa_pool *pool, const int32_t *rows, int32_t n, const float *scores,
                   float *scores_out, int32_t budget, int32_t first, int32_t last, int32_t *kept, void *workspace,

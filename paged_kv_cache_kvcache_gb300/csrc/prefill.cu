@@ -201,6 +201,7 @@ struct Item {
 // (sorted longest first), odd rounds walked backwards so that the CTAs' totals
 // stay even.  The next item's entry is fetched while the current one runs
 // (from its start, or where the caller asks, to keep it out of a register-heavy loop).
+// kWin: the kernel is set up while the launch ahead may still write the list (and the block table): ordinary loads.
 template <bool kWin>
 struct ItemIter {
     const int4 *tiles;
@@ -217,8 +218,8 @@ struct ItemIter {
         if constexpr (kWin)
             window = p.window, sinks = p.sinks;
         if (idx < n) {
-            a0 = __ldg(tiles + 2 * idx);
-            a1 = __ldg(tiles + 2 * idx + 1);
+            a0 = kWin ? tiles[2 * idx] : __ldg(tiles + 2 * idx);
+            a1 = kWin ? tiles[2 * idx + 1] : __ldg(tiles + 2 * idx + 1);
         }
     }
     __device__ bool more() const { return idx < n; }
@@ -260,8 +261,8 @@ struct ItemIter {
     __device__ void fetch()
     {
         if (idx < n) {
-            a0 = ptx::ld_nc_v4_now(tiles + 2 * idx);
-            a1 = ptx::ld_nc_v4_now(tiles + 2 * idx + 1);
+            a0 = kWin ? ptx::ld_v4_now(tiles + 2 * idx) : ptx::ld_nc_v4_now(tiles + 2 * idx);
+            a1 = kWin ? ptx::ld_v4_now(tiles + 2 * idx + 1) : ptx::ld_nc_v4_now(tiles + 2 * idx + 1);
         }
     }
     // the item next() returns next (valid while more())
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int off = w.lk - w.lq; // cached prefix
             if (!kWin && p.fused && key >= off)
                 return -(w.cq0 + key - off + 1);
-            const int phys = kShort && key < bs ? w.blk0 : __ldg(bt + key / bs);
+            const int phys = kShort && key < bs ? w.blk0 : kWin ? bt[key / bs] : __ldg(bt + key / bs);
             return phys * bs + (key & (bs - 1));
         };
         if (warp == kLoaderWarp) {

@@ -178,6 +178,18 @@ __device__ __forceinline__ int4 ld_nc_v4_now(const int4 *p)
     return v;
 }
 
+// The same by an ordinary load, of data that an earlier launch may still have written while this kernel ran (after
+// grid_dependency_wait()).
+__device__ __forceinline__ int4 ld_v4_now(const int4 *p)
+{
+    int4 v;
+    asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // 16-byte global load of data that is read once (it stays out of L1); an ordinary load, so it sees what an
 // earlier launch wrote, after grid_dependency_wait().
 __device__ __forceinline__ uint4 ld_once_v4(const void *p)
