@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "cta_count.h"
 #include "internal.h"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -50,7 +51,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCtas = 16; // of a cluster
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int NT, bool kInt8>
@@ -622,42 +622,17 @@ __global__ void __launch_bounds__(kThreads, (kInt8 ? 5 : 4) - NT)
         cluster.sync(); // the others may still read this CTA's results
 }
 
-// CTAs per (sequence, KV head): as many as run at once (clusters of a second wave wait for whole ones of the first: 200
-// sequences of 4 KV heads and 1000 keys took 66.8 us with one CTA each, 88.2 with two; 19 of 16384 keys 141 with
-// one, 100 with two).  A cluster stays in one GPC, so that fewer fit than there are places (64 clusters of six 6.2 us, of seven,
-// in 456 places, 9.2).
 template <int D, int NT, bool kInt8, bool kWeights>
 int count_ctas(const WindowArgs &a, int *ctas)
 {
     using L = WinLayout<D, NT, kInt8>;
-    const int64_t units = (int64_t)a.num_seqs * a.dims.num_kv_heads;
-    const int64_t room = (int64_t)a.max_blocks_per_seq * a.dims.block_size;
-    const int64_t most = (int64_t)a.window + a.sinks, keys = std::min(room, most);
-    // No more than four, with 64 keys each (one sequence of 320 keys and 8 KV heads, INT8: 7.0 us with one, 6.0 with two,
-    // 5.5 with four to eight), than eight, with 128, or than 16, with 224 (six of 3624 keys 17.1 us with four, 11.4 with
-    // eight, 9.5 with 16; ten of 2480 10.5 with eight, 9.5 with twelve, 9.9 with 16).
-    int64_t n = std::max({std::clamp<int64_t>(keys / 64, 1, 4), std::min<int64_t>(8, keys / 128),
-                          std::min<int64_t>(kMaxCtas, keys / 224)});
-    auto fit = [&](int64_t c, int *clusters) {
-        return active_clusters<decode_window_kernel<D, NT, kInt8, kWeights>>("window decode", (int)c, kThreads, L::kSmemBytes,
-                                                                             clusters);
-    };
-    int at_once = 0;
-    if (int rc = fit(1, &at_once))
-        return rc;
-    for (n = std::clamp<int64_t>(at_once / units, 1, n); n > 1; --n) {
-        if (int rc = fit(n, &at_once))
-            return rc;
-        if (at_once >= units)
-            break;
-    }
-    // Where contexts are seen whole their lengths differ, and up to eight CTAs of 1024 keys, 1024 CTAs in all, even them
-    // out (64 sequences of 4096 to 8192 keys and 4 KV heads: 175 us with one, 153 with four; 18 of up to 13634 and 8: 120
-    // with three, 111 with eight; 60 of up to 516 and 8: 12.2 with one, 19.2 with two).
-    if (room <= most)
-        n = std::max(n, std::min({(int64_t)8, (1024 + units - 1) / units, room / 1024}));
-    *ctas = (int)n;
-    return PA_OK;
+    const int64_t room = (int64_t)a.max_blocks_per_seq * a.dims.block_size, most = (int64_t)a.window + a.sinks;
+    return count_cluster_ctas((int64_t)a.num_seqs * a.dims.num_kv_heads, std::min(room, most), room <= most,
+                              [](int c, int *clusters) {
+                                  return active_clusters<decode_window_kernel<D, NT, kInt8, kWeights>>(
+                                      "window decode", c, kThreads, L::kSmemBytes, clusters);
+                              },
+                              ctas);
 }
 
 template <int D, int NT, bool kInt8, bool kWeights>

@@ -1,7 +1,6 @@
 // Internal declarations shared by the host-side translation units of libpagedattn.
 #pragma once
 
-#include <algorithm>
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
@@ -95,18 +94,20 @@ int ensure_wide_clusters(const char *what)
     return PA_OK;
 }
 
-// How many clusters of `ctas` CTAs (of up to 16) the current device runs at once, asked once per device.
+// How many clusters of `ctas` CTAs (of up to 16) the current device runs at once, 0 if none; asked once per device.
 template <auto Kernel>
 int active_clusters(const char *what, int ctas, unsigned threads, size_t smem, int *n)
 {
-    static std::atomic<int> cached[64][17];
+    static std::atomic<int> cached[64][17]; // the answer + 1; 0: not asked yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return fail(PA_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
     const bool slot = dev >= 0 && dev < 64;
-    if (slot && (*n = cached[dev][ctas].load(std::memory_order_relaxed)) > 0)
+    if (const int known = slot ? cached[dev][ctas].load(std::memory_order_relaxed) : 0) {
+        *n = known - 1;
         return PA_OK;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(threads);
@@ -117,13 +118,15 @@ int active_clusters(const char *what, int ctas, unsigned threads, size_t smem, i
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(n, Kernel, &cfg);
-    if (e != cudaSuccess) {
+    if (e == cudaErrorInvalidClusterSize) {
+        cudaGetLastError();
+        *n = 0;
+    } else if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(PA_ERR_CUDA, "%s clusters: %s", what, cudaGetErrorString(e));
     }
-    *n = std::max(*n, 1);
     if (slot)
-        cached[dev][ctas].store(*n, std::memory_order_relaxed);
+        cached[dev][ctas].store(*n + 1, std::memory_order_relaxed);
     return PA_OK;
 }
 
