@@ -693,7 +693,8 @@ int pa_decode_weights_int8(const pa_dims *dims, const void *q, const void *k_cac
  *               block_size]; may be one array.  A row's scores move with its
  *               tokens; behind the new length up to the old one scores_out gets
  *               zeros.  What lies behind that, and other rows, stay
- *   first, last: at least 0, together at most budget
+ *   budget:     at least 1, at most 2^31 - 4097;  first, last: at least 0, together
+ *               at most budget
  *   kept:       device int32 [n][budget]: the place that each token had before, -1
  *               behind a row of fewer (positions stay a token's own: whoever turns
  *               keys and queries by position goes on counting from the old length)

@@ -850,8 +850,9 @@ extern "C" int pa_pool_evict(const pa_dims *dims, const pa_pool *pool, const int
     if (budget < 1 || first < 0 || last < 0 || (int64_t)first + last > budget)
         return fail(PA_ERR_INVALID_ARG, "pa_pool_evict: budget %d must be positive and hold the first %d and last %d tokens",
                     budget, first, last);
-    if ((int64_t)pool->max_blocks * dims->block_size > INT32_MAX - 4096) // (the choice counts past a row's end)
-        return fail(PA_ERR_UNSUPPORTED, "pa_pool_evict: max_blocks * block_size exceeds int32");
+    // (the choice counts past a row's end, and past the budget's)
+    if ((int64_t)pool->max_blocks * dims->block_size > INT32_MAX - 4096 || budget > INT32_MAX - 4096)
+        return fail(PA_ERR_UNSUPPORTED, "pa_pool_evict: max_blocks * block_size or the budget exceeds int32");
     if (n == 0)
         return PA_OK;
     if (!rows || !scores || !scores_out || !kept)
