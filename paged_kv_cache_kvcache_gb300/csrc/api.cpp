@@ -938,7 +938,12 @@ extern "C" int pa_decode_weights_workspace(const pa_dims *dims, int32_t num_seqs
         return rc;
     if (!bytes || num_seqs < 0 || max_blocks_per_seq < 1)
         return fail(PA_ERR_INVALID_ARG, "pa_decode_weights_workspace: NULL pointer, num_seqs < 0 or no blocks");
-    *bytes = (uint64_t)num_seqs * dims->num_kv_heads * max_blocks_per_seq * dims->block_size * window_raw_heads(*dims) * 4;
+    const uint64_t units = (uint64_t)num_seqs * dims->num_kv_heads, room = (uint64_t)max_blocks_per_seq * dims->block_size;
+    const uint64_t key = (uint64_t)window_raw_heads(*dims) * 4;
+    if (units > INT32_MAX / 8 || room > INT32_MAX - 16 || units * room > UINT64_MAX / key) // (the decode's limits)
+        return fail(PA_ERR_UNSUPPORTED, "pa_decode_weights_workspace: %d sequences of %d blocks are too many", num_seqs,
+                    max_blocks_per_seq);
+    *bytes = units * room * key;
     return PA_OK;
 }
 
