@@ -475,6 +475,9 @@ def _rope_refuse(dims, rope, q, k, v, positions, slot_mapping, q_out, caches, sc
             raise ValueError(f"{what}: a token's heads must be contiguous (in q_out the tokens too), got strides "
                              f"{t.stride()}")
     _int32(positions, "positions", n * rope.axes, dev)
+    if positions.shape not in ((rope.axes, n), (n,) if rope.axes == 1 else ()):
+        raise ValueError(f"positions must be [{rope.axes}, {n}]" + (f" or [{n}]" if rope.axes == 1 else "") +
+                         f", got {tuple(positions.shape)}")
     _int32(slot_mapping, "slot_mapping", n, dev)
     for t in (q, k, v, q_out, *caches, *scales):
         if t.get_device() != dev:
@@ -490,7 +493,7 @@ def pa_rope_store(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q
     """Norm and rotate the queries (into q_out) and the keys, and store keys and values at their slots.
 
     q [tokens, Hq, D], k, v [tokens, Hkv, D]: bf16, a token's heads contiguous (parts of one projection's output);
-    positions: int32 [tokens], or [axes, tokens].
+    positions: int32 [axes, tokens], or [tokens] where there is one axis.
     """
     n, dev, (hq, hkv, d) = slot_mapping.numel(), rope.device, rope.heads
     qs, ks, vs = q.stride(), k.stride(), v.stride()
@@ -502,7 +505,8 @@ def pa_rope_store(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q
             and q.shape == (n, hq, d) == q_out.shape and kv == (n, hkv, d) and kv == v.shape
             and qs[1] == ks[1] == vs[1] == d and qs[2] == ks[2] == vs[2] == 1
             and q_out.is_contiguous() and positions.is_contiguous() and slot_mapping.is_contiguous()
-            and k_cache.is_contiguous() and v_cache.is_contiguous() and positions.numel() == n * rope.axes
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and positions.shape in ((rope.axes, n), (n,) if rope.axes == 1 else ())
             and k_cache.numel() >= rope.rows * d <= v_cache.numel() and bytes(dims) == rope.dims_bytes):
         _rope_refuse(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), ())
     row = hkv * d
@@ -530,7 +534,7 @@ def pa_rope_store_int8(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mappi
             and qs[1] == ks[1] == vs[1] == d and qs[2] == ks[2] == vs[2] == 1
             and q_out.is_contiguous() and positions.is_contiguous() and slot_mapping.is_contiguous()
             and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
-            and v_scale.is_contiguous() and positions.numel() == n * rope.axes
+            and v_scale.is_contiguous() and positions.shape in ((rope.axes, n), (n,) if rope.axes == 1 else ())
             and k_cache.numel() >= rope.rows * d <= v_cache.numel() and k_scale.numel() >= rope.rows <= v_scale.numel()
             and bytes(dims) == rope.dims_bytes):
         _rope_refuse(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), (k_scale, v_scale))
