@@ -243,6 +243,11 @@ def _int32(t, what: str, count: Optional[int] = None, dev: Optional[int] = None)
     return t.data_ptr()
 
 
+def _c_int(x: int) -> int:
+    """x, or where 32 bits do not hold it the end of their range (ctypes would pass on its low 32 bits)."""
+    return x if -2147483648 <= x <= 2147483647 else 2147483647 if x > 0 else -2147483648
+
+
 def make_dims(num_blocks: int, block_size: int, num_heads: int, num_kv_heads: int, head_dim: int) -> pa_dims:
     return pa_dims(num_blocks, block_size, num_heads, num_kv_heads, head_dim)
 
@@ -876,7 +881,7 @@ def pa_decode_window(dims: pa_dims, q, k_cache, v_cache, block_tables, context_l
     ``table_rows[b]`` of them, or row b.
     """
     args = _bounded_call(dims, q, k_cache, v_cache, block_tables, context_lens, table_rows, out)
-    rc = (_lib or lib()).pa_decode_window(*args, window, sinks, scale, out.data_ptr(),
+    rc = (_lib or lib()).pa_decode_window(*args, _c_int(window), _c_int(sinks), scale, out.data_ptr(),
                                           _stream_of(_device(), stream))
     if rc != PA_OK:
         _check(rc, "pa_decode_window")
@@ -886,7 +891,7 @@ def pa_decode_window_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, 
                           sinks: int, scale: float, out, table_rows=None, stream=None):
     """pa_decode_window over an INT8 cache."""
     args = _bounded_call_int8(dims, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, table_rows, out)
-    rc = (_lib or lib()).pa_decode_window_int8(*args, window, sinks, scale, out.data_ptr(),
+    rc = (_lib or lib()).pa_decode_window_int8(*args, _c_int(window), _c_int(sinks), scale, out.data_ptr(),
                                                _stream_of(_device(), stream))
     if rc != PA_OK:
         _check(rc, "pa_decode_window_int8")
@@ -959,7 +964,7 @@ def pa_prefill_window(dims: pa_dims, q, k_cache, v_cache, plan: PrefillPlan, win
     m = plan.meta
     _check(lib().pa_prefill_window(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                    plan.dptr(m.off_cu_seqlens_q), plan.dptr(m.off_cu_seqlens_k),
-                                   plan.dptr(m.off_block_tables), int(window), int(sinks), float(scale), _ptr(out),
+                                   plan.dptr(m.off_block_tables), _c_int(window), _c_int(sinks), float(scale), _ptr(out),
                                    ctypes.byref(m), plan.dptr(m.off_tiles), _stream(stream)), "pa_prefill_window")
 
 
@@ -972,8 +977,8 @@ def pa_prefill_window_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale,
     _check(lib().pa_prefill_window_int8(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
                                         _ptr(v_scale), plan.dptr(m.off_cu_seqlens_q), plan.dptr(m.off_cu_seqlens_k),
                                         plan.dptr(m.off_block_tables), plan.dptr(m.off_scratch_tables),
-                                        plan.dptr(m.off_scratch_items), int(window), int(sinks), float(scale), _ptr(out),
-                                        ctypes.byref(m), plan.dptr(m.off_tiles), _ptr(workspace), ws_bytes,
+                                        plan.dptr(m.off_scratch_items), _c_int(window), _c_int(sinks), float(scale),
+                                        _ptr(out), ctypes.byref(m), plan.dptr(m.off_tiles), _ptr(workspace), ws_bytes,
                                         _stream(stream)), "pa_prefill_window_int8")
 
 
@@ -989,8 +994,8 @@ def pa_pool_evict(dims: pa_dims, pool: PagePool, rows, scores, budget: int, kept
     places = _int32(kept, "kept", n * budget, dev)
     s, so = _score_args(pool.dims, pool.block_tables, scores, scores_out, None)
     pool.check(dims)
-    rc = (_lib or lib()).pa_pool_evict(pool.dims_ref, pool.ref, at, n, s, so, budget, first, last, places, *pool.ws,
-                                       _stream_of(pool.device, stream))
+    rc = (_lib or lib()).pa_pool_evict(pool.dims_ref, pool.ref, at, n, s, so, _c_int(budget), _c_int(first), _c_int(last),
+                                       places, *pool.ws, _stream_of(pool.device, stream))
     if rc != PA_OK:
         _check(rc, "pa_pool_evict")
 

@@ -52,3 +52,35 @@ def test_positions_of_other_shapes_are_refused(calls, int8):
         with pytest.raises(ValueError):
             call(*bad)
     assert len(calls) == 4
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_windows_past_32_bits_are_everything(calls, int8):
+    """An int of C takes the low 32 bits of what it is given: 2^32 + 5 was a window of 5."""
+    dims, n = pa.make_dims(*DIMS), 3
+    q, table, ctx = torch.zeros(n, 4, 64, dtype=BF), torch.zeros(n, 2, dtype=torch.int32), torch.zeros(n, dtype=torch.int32)
+    f = pa.pa_decode_window_int8 if int8 else pa.pa_decode_window
+    for x, want in ((8, 8), (MOST, MOST), (2 ** 31, MOST), (2 ** 32 + 5, MOST), (2 ** 63, MOST)):
+        f(dims, q, *cache(int8), table, ctx, x, x, 0.1, torch.zeros_like(q), stream=0)
+        assert calls[-1][1][-5:-3] == (want, want)
+    f(dims, q, *cache(int8), table, ctx, 5 - 2 ** 32, -2 ** 40, 0.1, torch.zeros_like(q), stream=0)
+    assert all(x < 0 for x in calls[-1][1][-5:-3])  # which the library refuses
+
+
+def test_first_and_last_tokens_past_32_bits_are_refused(calls):
+    """first = 2^32 + 4 was 4."""
+    dims, n = pa.make_dims(*DIMS), 2
+    table, ctx, refs = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.zeros(6, dtype=torch.int32)
+    pool = object.__new__(pa.PagePool)
+    pool.dims, pool.dims_ref, pool.ref, pool.ws, pool.device, pool.block_tables = dims, 1, 1, (256, 1), -1, table
+    pool.check = lambda dims: None
+    rows, kept = torch.zeros(n, dtype=torch.int32), torch.zeros(n, 8, dtype=torch.int32)
+    scores = torch.zeros(4, 2, 32)
+
+    def call(first, last):
+        pa.pa_pool_evict(dims, pool, rows, scores, 8, kept, first=first, last=last, stream=0)
+        return calls[-1][1][7:9]
+
+    assert call(3, 2) == (3, 2)
+    assert call(2 ** 32 + 4, 2 ** 40) == (MOST, MOST)  # more than the budget: refused
+    assert all(x < 0 for x in call(4 - 2 ** 32, -2 ** 40))
