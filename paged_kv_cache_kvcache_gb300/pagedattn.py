@@ -297,6 +297,8 @@ class _Plan:
 
 
 class PrefillPlan(_Plan):
+    dims_bytes = None  # what it was packed for
+
     @property
     def slot_mapping(self) -> int:
         return self.dptr(self.meta.off_slot_mapping)
@@ -362,7 +364,9 @@ def pa_pack_prefill(dims: pa_dims, seq_lens, query_lens, block_lists, pin: bool 
     seq_lens, query_lens = _i32(seq_lens), _i32(query_lens)
     off, ids = _flatten(block_lists)
     args = (ctypes.byref(dims), len(seq_lens), _np_ptr(seq_lens), _np_ptr(query_lens), _np_ptr(off), _np_ptr(ids))
-    return _pack("pa_pack_prefill", pa_prefill_meta(), args, into, pin, PrefillPlan)
+    plan = _pack("pa_pack_prefill", pa_prefill_meta(), args, into, pin, PrefillPlan)
+    plan.dims_bytes = bytes(dims)
+    return plan
 
 
 def pa_pack_decode(dims: pa_dims, context_lens, block_lists, split_tokens: int = 0, pin: bool = True,
@@ -957,29 +961,70 @@ def pa_decode_weights_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale,
         _check(rc, "pa_decode_weights_int8")
 
 
+def _prefill_window_refuse(dims, q, caches, scales, plan, out, workspace):
+    """Why the tensors of a windowed prefill are refused (the calls test for it in one expression)."""
+    if bytes(dims) != plan.dims_bytes:
+        raise ValueError("the plan was packed for other dims")
+    cache = _INT8 if scales else _BF16
+    page = dims.num_blocks * dims.block_size * dims.num_kv_heads
+    want = (plan.meta.total_q, dims.num_heads, dims.head_dim)
+    for what, t in (("q", q), ("out", out)):
+        if tuple(t.shape) != want:
+            raise ValueError(f"{what} must be {list(want)}, got {tuple(t.shape)}")
+    _refuse(plan.dev.get_device(), (q, out, *caches, *scales, workspace),
+            (("q", q, _BF16, 0), ("out", out, _BF16, 0), ("k_cache", caches[0], cache, page * dims.head_dim),
+             ("v_cache", caches[1], cache, page * dims.head_dim),
+             *((what, t, _FP16, page) for what, t in zip(("k_scale", "v_scale"), scales))))
+
+
 def pa_prefill_window(dims: pa_dims, q, k_cache, v_cache, plan: PrefillPlan, window: int, sinks: int, scale: float,
                       out, stream=None):
     """pa_prefill_varlen in which a query sees the last ``window`` keys up to its own and the first ``sinks`` ones
-    (the same plan)."""
-    m = plan.meta
-    _check(lib().pa_prefill_window(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                   plan.dptr(m.off_cu_seqlens_q), plan.dptr(m.off_cu_seqlens_k),
-                                   plan.dptr(m.off_block_tables), _c_int(window), _c_int(sinks), float(scale), _ptr(out),
-                                   ctypes.byref(m), plan.dptr(m.off_tiles), _stream(stream)), "pa_prefill_window")
+    (the same plan, packed for the same dims).  q, out: bf16 [tokens, Hq, D]."""
+    m, dev, shape = plan.meta, _device(), q.shape
+    base = plan.dptr(0)
+    least = dims.num_blocks * dims.block_size * dims.num_kv_heads * dims.head_dim
+    if not (dev == plan.dev.get_device() == q.get_device() == k_cache.get_device() == v_cache.get_device() == out.get_device()
+            and q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is _BF16
+            and shape == (m.total_q, dims.num_heads, dims.head_dim) and shape == out.shape
+            and q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_cache.numel() >= least <= v_cache.numel() and bytes(dims) == plan.dims_bytes):
+        _prefill_window_refuse(dims, q, (k_cache, v_cache), (), plan, out, None)
+    rc = (_lib or lib()).pa_prefill_window(ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                           base + m.off_cu_seqlens_q, base + m.off_cu_seqlens_k, base + m.off_block_tables,
+                                           _c_int(window), _c_int(sinks), float(scale), out.data_ptr(),
+                                           ctypes.byref(m), base + m.off_tiles, _stream_of(dev, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_prefill_window")
 
 
 def pa_prefill_window_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, plan: PrefillPlan, window: int,
                            sinks: int, scale: float, out, workspace=None, stream=None):
     """pa_prefill_window over an INT8 cache (plan and workspace as pa_prefill_varlen_int8's)."""
-    m = plan.meta
+    m, dev, shape = plan.meta, _device(), q.shape
+    base = plan.dptr(0)
+    page = dims.num_blocks * dims.block_size * dims.num_kv_heads
+    least = page * dims.head_dim
+    if not (dev == plan.dev.get_device() == q.get_device() == k_cache.get_device() == v_cache.get_device() == out.get_device()
+            == k_scale.get_device() == v_scale.get_device()
+            and q.dtype is out.dtype is _BF16 and k_cache.dtype is v_cache.dtype is _INT8
+            and k_scale.dtype is v_scale.dtype is _FP16
+            and shape == (m.total_q, dims.num_heads, dims.head_dim) and shape == out.shape
+            and q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and k_cache.numel() >= least <= v_cache.numel() and k_scale.numel() >= page <= v_scale.numel()
+            and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
+            and bytes(dims) == plan.dims_bytes):
+        _prefill_window_refuse(dims, q, (k_cache, v_cache), (k_scale, v_scale), plan, out, workspace)
     workspace = _call_workspace(plan, workspace, q.device, stream)
-    ws_bytes = int(workspace.numel()) if isinstance(workspace, torch.Tensor) else 0
-    _check(lib().pa_prefill_window_int8(ctypes.byref(dims), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                        _ptr(v_scale), plan.dptr(m.off_cu_seqlens_q), plan.dptr(m.off_cu_seqlens_k),
-                                        plan.dptr(m.off_block_tables), plan.dptr(m.off_scratch_tables),
-                                        plan.dptr(m.off_scratch_items), _c_int(window), _c_int(sinks), float(scale),
-                                        _ptr(out), ctypes.byref(m), plan.dptr(m.off_tiles), _ptr(workspace), ws_bytes,
-                                        _stream(stream)), "pa_prefill_window_int8")
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    rc = (_lib or lib()).pa_prefill_window_int8(
+        ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        base + m.off_cu_seqlens_q, base + m.off_cu_seqlens_k, base + m.off_block_tables, base + m.off_scratch_tables,
+        base + m.off_scratch_items, _c_int(window), _c_int(sinks), float(scale), out.data_ptr(), ctypes.byref(m),
+        base + m.off_tiles, ws, ws_bytes, _stream_of(dev, stream))
+    if rc != PA_OK:
+        _check(rc, "pa_prefill_window_int8")
 
 
 def pa_pool_evict(dims: pa_dims, pool: PagePool, rows, scores, budget: int, kept, first: int = 0, last: int = 0,

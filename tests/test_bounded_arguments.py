@@ -84,3 +84,42 @@ def test_first_and_last_tokens_past_32_bits_are_refused(calls):
     assert call(3, 2) == (3, 2)
     assert call(2 ** 32 + 4, 2 ** 40) == (MOST, MOST)  # more than the budget: refused
     assert all(x < 0 for x in call(4 - 2 ** 32, -2 ** 40))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_prefill_window_refuses_wrong_tensors_and_dims(monkeypatch, int8):
+    """What it took for the plan's tensors, whatever their type, shape, strides and device."""
+    dims = pa.make_dims(*DIMS)
+    plan = pa.pa_pack_prefill(dims, [20, 5], [7, 5], [[0, 1], [2]], pin=False)
+    plan.dev = torch.zeros(int(plan.meta.total_bytes), dtype=torch.uint8)
+    recorder = Recorder()
+    monkeypatch.setattr(pa, "_lib", recorder)
+    monkeypatch.setattr(pa, "_device", lambda: -1)
+    calls, f = recorder.calls, pa.pa_prefill_window_int8 if int8 else pa.pa_prefill_window
+    good = {"q": torch.zeros(12, 4, 64, dtype=BF), "out": torch.zeros(12, 4, 64, dtype=BF)}
+    good.update(zip(("k", "v", "ks", "vs"), cache(int8)))
+    ws = [torch.zeros(max(256, int(plan.meta.workspace_bytes)), dtype=torch.uint8)] if int8 else []
+
+    def call(dims=dims, plan=plan, ws=ws, **kw):
+        t = {**good, **kw}
+        f(dims, t["q"], t["k"], t["v"], *((t["ks"], t["vs"]) if int8 else ()), plan, 8, 2, 0.1, t["out"], *ws, stream=0)
+
+    call()
+    nb, bs, hq, hkv, d = DIMS
+    call(k=torch.zeros(8, bs, hkv, d, dtype=good["k"].dtype))  # more pages than the dims name
+    assert len(calls) == 2
+    bad = [dict(q=good["q"].float()), dict(q=good["q"].half()), dict(q=good["q"][:11]), dict(q=torch.zeros(12, 8, 64, dtype=BF)),
+           dict(q=torch.zeros(12, 64, 4, dtype=BF).transpose(1, 2)), dict(out=good["out"].float()),
+           dict(out=torch.zeros(24, 4, 64, dtype=BF)[::2]), dict(out=good["out"][:11]), dict(k=good["k"][:5]),
+           dict(v=good["v"].float()), dict(v=good["v"].transpose(1, 2)),
+           dict(dims=pa.make_dims(nb + 1, bs, hq, hkv, d)), dict(dims=pa.make_dims(nb, 32, hq, hkv, d)),
+           dict(dims=pa.make_dims(nb, bs, hkv, hq, d)), dict(dims=pa.make_dims(nb, bs, 2 * hq, 2 * hkv, d))]
+    if int8:
+        bad += [dict(ks=good["ks"].float()), dict(vs=good["vs"][:5]), dict(ws=[torch.zeros(1 << 20, dtype=torch.uint8)[::2]])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            call(**kw)
+    monkeypatch.setattr(pa, "_device", lambda: 0)  # the tensors and the plan are elsewhere
+    with pytest.raises(ValueError):
+        call()
+    assert len(calls) == 2
