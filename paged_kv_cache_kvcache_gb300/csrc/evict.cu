@@ -35,6 +35,7 @@ constexpr int kChooseThreads = 1024;
 constexpr int kChooseWarps = kChooseThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKeysInSmem = 49152;
+constexpr int kUnsure = 1024; // totals that total_exact forms without all the others
 constexpr int kMoveThreads = 256;
 constexpr int kVecs = 4; // 16-byte vectors per thread and batch
 constexpr int kBatchTokens = kMoveThreads * kVecs; // at most: of one vector, value or scale each
@@ -62,16 +63,96 @@ __device__ __forceinline__ uint32_t order(float x)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// The sum over the heads, as exact as a 64-bit sum to within fp32's last bit: s + e is carried without
-// rounding errors but those of e (two-sum; fp64 adds run at 1/64 of fp32's rate and took longer than the reads).
-// Of kTokens tokens, `step` apart and before `left`, with kHeads of each one's scores in flight together.
+// The exact sum of a token's scores, rounded to fp32: a fixed-point sum of 320 bits in units of 2^-149 (out of line, for
+// the few tokens whose sum totals_of is not sure of).
+__device__ __noinline__ float total_exact(const float *at, int heads, int64_t pitch)
+{
+    constexpr int kWords = 5; // 2^31 scores below 2^128, and a sign
+    uint64_t sum[kWords] = {};
+    bool up = false, down = false; // an infinity
+    for (int h = 0; h < heads; ++h) {
+        const uint32_t u = __float_as_uint(at[h * pitch]), ex = u >> 23 & 255u;
+        const bool minus = u >> 31;
+        if (ex == 255u) {
+            if (u & 0x7fffffu)
+                return __uint_as_float(0x7fffffffu); // NaN
+            (minus ? down : up) = true;
+            continue;
+        }
+        const uint64_t m = (u & 0x7fffffu) | (ex ? 0x800000u : 0u);
+        const int shift = ex ? (int)ex - 1 : 0, word = shift >> 6, off = shift & 63;
+        const uint64_t lo = m << off, hi = off > 40 ? m >> (64 - off) : 0;
+        uint64_t carry = minus; // (minus x: its complement and 1)
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const uint64_t part = w == word ? lo : w == word + 1 ? hi : 0;
+            const uint64_t add = minus ? ~part : part;
+            const uint64_t a = sum[w] + add, b = a + carry;
+            carry = (a < add) | (b < a);
+            sum[w] = b;
+        }
+    }
+    if (up || down)
+        return up && down ? __uint_as_float(0x7fffffffu) : up ? INFINITY : -INFINITY;
+    const bool minus = sum[kWords - 1] >> 63;
+    uint64_t carry = minus;
+    int top = -1; // its highest bit
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+        if (minus) {
+            sum[w] = ~sum[w] + carry;
+            carry = carry && sum[w] == 0;
+        }
+        if (sum[w])
+            top = 64 * w + 63 - __clzll((long long)sum[w]);
+    }
+    uint32_t bits;
+    if (top < 24) { // (all of it; 0 where there is none)
+        bits = (uint32_t)sum[0];
+    } else {
+        const int cut = top - 23; // bits below the 24 that stay
+        uint64_t below = 0, head = 0;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const int at_bit = cut - 64 * w; // of this word
+            if (at_bit >= 64)
+                below |= sum[w] != 0 && at_bit > 64 ? 1u : 0u;
+            if (at_bit > 0 && at_bit < 64)
+                head |= sum[w] >> at_bit;
+            else if (at_bit <= 0 && at_bit > -64)
+                head |= sum[w] << -at_bit;
+        }
+        bool half = false;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const int bit = cut - 1 - 64 * w; // the first that goes
+            if (bit >= 0 && bit < 64) {
+                half = sum[w] >> bit & 1u;
+                below |= sum[w] & ((1ull << bit) - 1ull);
+            }
+        }
+        const uint32_t m = (uint32_t)head & 0xffffffu;
+        // the leading bit counts one in the exponent; rounding up carries into it
+        bits = m + ((uint32_t)cut << 23) + (half && (below || (m & 1u)) ? 1u : 0u);
+        bits = cut > 253 || bits > 0x7f800000u ? 0x7f800000u : bits;
+    }
+    return __uint_as_float(bits | (minus ? 0x80000000u : 0u));
+}
+
+// The sum over the heads, rounded to fp32, of kTokens tokens, `step` apart and before `left`, with kHeads of each one's
+// scores in flight together (one: there is no other): out(o, key, sure).  s + e is carried with the errors of e's own sums
+// alone (two-sum; fp64 adds run at 1/64 of fp32's rate and took longer than the reads).  Of scores that are not negative,
+// as weights are, those are below heads^2 2^-48 of the sum, and none where every score is above heads 2^-24 of it (the
+// errors are multiples of its last bit then, zeros aside).  So a sum is sure if both ends of twice that range round to it, or if there is
+// no error; others (next to the middle of two numbers, with a negative score, past fp32's range) are total_exact's.
 template <int kTokens, int kHeads, class Out>
 __device__ __forceinline__ void totals_of(const float *at, int left, int step, int heads, int64_t pitch, Out out)
 {
     float s[kTokens], e[kTokens];
+    uint32_t signs[kTokens], least[kTokens];
 #pragma unroll
     for (int t = 0; t < kTokens; ++t)
-        s[t] = e[t] = 0.f;
+        s[t] = e[t] = 0.f, signs[t] = 0u, least[t] = 0xffffffffu;
     for (int h0 = 0; h0 < heads; h0 += kHeads) {
         float x[kTokens][kHeads];
 #pragma unroll
@@ -83,24 +164,51 @@ __device__ __forceinline__ void totals_of(const float *at, int left, int step, i
         for (int h = 0; h < kHeads; ++h)
 #pragma unroll
             for (int t = 0; t < kTokens; ++t) {
-                const float u = __fadd_rn(s[t], x[t][h]);
-                const float b = __fsub_rn(u, s[t]);
-                e[t] = __fadd_rn(e[t], __fadd_rn(__fsub_rn(s[t], __fsub_rn(u, b)), __fsub_rn(x[t][h], b)));
-                s[t] = u;
+                if constexpr (kHeads == 1) {
+                    s[t] = x[t][h];
+                } else {
+                    const float u = __fadd_rn(s[t], x[t][h]);
+                    const float b = __fsub_rn(u, s[t]);
+                    e[t] = __fadd_rn(e[t], __fadd_rn(__fsub_rn(s[t], __fsub_rn(u, b)), __fsub_rn(x[t][h], b)));
+                    s[t] = u;
+                    signs[t] |= __float_as_uint(x[t][h]);
+                    least[t] = min(least[t], __float_as_uint(x[t][h]) - 1u); // (0 is none)
+                }
             }
     }
+    const float range = (float)heads * (float)heads * 0x1p-47f, above = (float)heads * 0x1p-23f;
 #pragma unroll
     for (int t = 0; t < kTokens; ++t)
-        if (t * step < left)
-            out(t * step, order(isfinite(s[t]) ? __fadd_rn(s[t], e[t]) : s[t]));
+        if (t * step < left) {
+            if constexpr (kHeads == 1) {
+                out(t * step, order(s[t]), true);
+            } else {
+                const float d = __fmul_rn(s[t], range);
+                const float r = __fadd_rn(s[t], __fadd_rn(e[t], d)), r0 = __fadd_rn(s[t], __fsub_rn(e[t], d));
+                const bool exact = __uint_as_float(least[t]) > __fmul_rn(s[t], above) && s[t] <= 0x1p+127f;
+                out(t * step, order(exact ? __fadd_rn(s[t], e[t]) : r), (int)signs[t] >= 0 && (r == r0 || exact));
+            }
+        }
 }
 
 // The same out of line, for rows whose keys do not fit shared memory.
 __device__ __noinline__ uint32_t total_far(const float *at, int heads, int64_t pitch)
 {
     uint32_t key;
-    totals_of<1, 8>(at, 1, 1, heads, pitch, [&](int, uint32_t x) { key = x; });
+    totals_of<1, 8>(at, 1, 1, heads, pitch,
+                    [&](int, uint32_t x, bool sure) { key = sure ? x : order(total_exact(at, heads, pitch)); });
     return key;
+}
+
+// Keys of the n places that the list names, from the exact sums; of all from begin to end if there are more than it holds.
+__device__ __noinline__ void mend_keys(uint32_t *keys, const int *list, int n, const float *scores, int heads, int64_t pitch,
+                                       int begin, int end)
+{
+    const bool all = n > kUnsure;
+    for (int x = threadIdx.x; x < (all ? end - begin : n); x += kChooseThreads) {
+        const int j = all ? begin + x : list[x];
+        keys[j] = order(total_exact(scores + j, heads, pitch));
+    }
 }
 
 // exclusive sum over the CTA's threads; *sum: all
@@ -135,7 +243,8 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
     extern __shared__ uint32_t keys[];
     __shared__ int hist[kBins];
     __shared__ int warps[kChooseWarps], warps2[kChooseWarps];
-    __shared__ int digit, above, equals, lowest;
+    __shared__ int digit, above, equals, lowest, unsure;
+    __shared__ int unsure_at[kUnsure];
     ptx::launch_dependents();
     ptx::grid_dependency_wait();
     const int i = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -147,6 +256,8 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
     for (int x = tid; x < i; x += kChooseThreads) // a row once
         bad = bad || p.rows[x] == row;
     int32_t *kept = p.kept + (int64_t)i * budget;
+    if (tid == 0)
+        unsure = 0;
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
             p.state[i] = -1;
@@ -177,7 +288,12 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
         auto form = [&](auto tokens, auto heads) {
             for (int j = begin + tid; j < end; j += tokens.value * kChooseThreads)
                 totals_of<tokens.value, heads.value>(scores + j, end - j, kChooseThreads, p.num_kv_heads, room,
-                                                     [&](int o, uint32_t x) { keys[j + o] = x; });
+                                                     [&](int o, uint32_t x, bool sure) {
+                                                         keys[j + o] = x;
+                                                         if (!sure)
+                                                             if (const int to = atomicAdd(&unsure, 1); to < kUnsure)
+                                                                 unsure_at[to] = j + o;
+                                                     });
         };
         using std::integral_constant;
         if (p.num_kv_heads == 1)
@@ -187,6 +303,9 @@ __global__ void __launch_bounds__(kChooseThreads) evict_choose_kernel(const Evic
         else
             form(integral_constant<int, 2>{}, integral_constant<int, 8>{});
     }
+    __syncthreads();
+    if (unsure > 0) // (seldom)
+        mend_keys(keys, unsure_at, unsure, scores, p.num_kv_heads, room, begin, end);
     const int refs0 = tid < pages && (uint32_t)page0 < (uint32_t)p.num_blocks ? p.refs[page0] : 0;
     auto key = [&](int j) { return stored ? keys[j] : total_far(scores + j, p.num_kv_heads, room); };
     if (tid == 0)
