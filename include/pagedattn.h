@@ -656,7 +656,9 @@ int pa_decode_window_int8(const pa_dims *dims, const void *q, const void *k_cach
  *               block_size]; may be one array.  What lies behind a context is
  *               neither read nor written.  A new token's score must be 0 before its
  *               first call (pa_pool_evict leaves zeros behind what stays; the scores
- *               of a row given back to the pool are the caller's to clear)
+ *               of a row given back to the pool are the caller's to clear, and a
+ *               forked row's, which pa_pool_fork knows nothing of, to copy from its
+ *               parent's, up to the parent's length, with zeros behind)
  *   decay:      in [0, 1]; 0 takes this step's weights alone (scores are not
  *               read); layers that share an array decay it once per step
  *   workspace:  device memory of pa_decode_weights_workspace's bytes, 256-byte
@@ -687,7 +689,9 @@ int pa_decode_weights_int8(const pa_dims *dims, const void *q, const void *k_cac
  * every number; of equal ones the lower index).  They move together in order, in
  * all layers, K and V (and scales), bit for bit; the pages behind them lose an
  * entry and the length becomes budget.  Slots behind the new length keep what
- * they held.  Rows of at most budget tokens stay as they are.
+ * they held.  Rows of at most budget tokens stay as they are.  (Scores come from
+ * decode steps: of a row that has had none since its prompt, all equal, the first
+ * budget - last tokens stay.)
  *   rows:       device int32 [n], each row at most once
  *   scores, scores_out: device fp32 [pool->num_rows][num_kv_heads][max_blocks *
  *               block_size]; may be one array.  A row's scores move with its
