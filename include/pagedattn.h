@@ -594,7 +594,8 @@ int pa_pool_compact(const pa_dims *dims, const pa_pool *pool, int32_t *remap, in
  * holds at such places takes no part.  A key that some queries see and others do
  * not must be finite.  Other arguments, errors and numerics as pa_prefill_varlen.
  * The launch may be set up during the kernel before it in the stream; it reads
- * nothing until that has ended, so block_tables and tiles may be what that writes.
+ * nothing until that has ended, so block_tables and tiles may be what that writes
+ * (the tiles name the block of a sequence's key 0 too, as the table has to).
  */
 int pa_prefill_window(const pa_dims *dims, const void *q, const void *k_cache, const void *v_cache,
                       const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, const int32_t *block_tables,
