@@ -19,14 +19,14 @@
 // that are not seen is not read: those rows are zeros in shared memory, whatever the cache has there.  Two stages and
 // three CTAs on an SM (bf16) hide more than three stages and two did (64 x 4160 keys 86.6 -> 84.5 us, 6.5 TB/s).  INT8 codes
 // come by cp.async too: TMA boxes took a quarter fewer instructions and no less time (200 x 1004 keys 49 us against
-// 47.5, now 45.4, 4.4 TB/s), and five or six CTAs of two stages took 46 to 48: what is left above the bytes is the ramp, three
+// 47.5, now 45.7, 4.4 TB/s), and five or six CTAs of two stages took 46 to 48: what is left above the bytes is the ramp, three
 // dependent look-ups and the merge of 1.3 waves, about 7 us each.  The merges take four values a thread, with every
 // part's maximum, sum and values on their way together (8 x 600 keys with weights 8.1 -> 6.7 us; with one value a
 // thread, and the maxima first, a pair of CTAs of 16 heads spent 4 us there).
 // Weights need M and L before any of them can be formed: the scores s' wait in the workspace (16 keys of one
 // head group are 512 contiguous bytes) until the cluster has met; keys and values leave L2 first, so they wait there.
-// 64 contexts of 4096 to 8192 keys take 150 us (5.5 TB/s), 121 without weights: writing s' costs 10 of that, the second
-// pass over them, latency for the most part, 20.
+// 64 contexts of 4096 to 8192 keys take 150 to 155 us (5.4 to 5.5 TB/s), over INT8 111 (3.9), 121 without weights: writing
+// s' costs 10 of that, the second pass over them, latency for the most part, 20.
 #include <algorithm>
 #include <type_traits>
 

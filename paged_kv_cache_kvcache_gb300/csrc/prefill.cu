@@ -498,7 +498,7 @@ __device__ __forceinline__ void prefetch_query_tiles(const CUtensorMap *tm_q, co
 // kWin: queries see a window of the last keys and a few first ones (pa_prefill_window; never with the store
 // fused).  An item's keys are two runs, laid behind one another in its key tiles in boxes of 16, so that four first keys
 // cost a box and not a tile (4 x 4096 queries of 28 heads, window 1024: 236 us with tiles of whole 128-key places,
-// 177 so, 1190 TFLOP/s).  Against the kernel without a window, whose items have more tiles, an item's own time counts
+// 175 to 187 so on several machines, 1130 to 1210 TFLOP/s).  Against the kernel without a window, whose items have more tiles, an item's own time counts
 // more: about 1.55 us a tile and 2.5 us an item (its last products, the output's way out of tensor memory and the next
 // item's first softmax follow one another).  Tried and not kept: half products and weights for a last tile of no more than
 // 64 places (185 us), the row max from the loads for the columns that a warp sees whole in a masked tile (219), two K stages

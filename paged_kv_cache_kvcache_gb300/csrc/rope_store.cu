@@ -15,8 +15,8 @@
 // needs no shuffle, and a row's sum of squares (or its max|x|) log2(D / 16) of them.  A warp takes a few
 // rows (the same heads, so that its lanes do not part) of 512 / D tokens, whose cos and sin it loads once.
 // Bound: HBM for prompts (each row read and written once: 16384 tokens of 28 + 2 x 4 heads of 128 in 52.4 us, 5.8 TB/s),
-// the loads' latency and the codes' instructions into an INT8 cache (5000 tokens of 16 + 2 x 8 heads 17.9 us, 4.1 TB/s), the
-// latency of one launch for decode steps (8 tokens 1.65 us in a graph).
+// the loads' latency and the codes' instructions into an INT8 cache (5000 tokens of 16 + 2 x 8 heads 17.8 us of inputs that
+// L2 holds, 21.5 of others, 3.4 TB/s), the latency of one launch for decode steps (8 tokens 1.8 us in a graph).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -326,8 +326,8 @@ int launch_heads(const RopeParams &p, cudaStream_t stream)
 {
     // A prompt's tokens are many: four heads share their cos and sin.  bf16 is bound by the loads' latency and keeps all
     // four rows in flight (16384 tokens of 28 + 8 heads: 52.6 us, 59.8 with one), INT8 by instructions, and has more warps
-    // with one (5000 tokens of 16 + 16: 17.9 us, 20.0 with four).  A decode step's rows each have a warp's lanes at
-    // once (8 tokens of 16 + 16: 1.85 us, 2.3 with four heads a warp).
+    // with one (5000 tokens of 16 + 16, in L2: 17.8 us, 20.0 with four).  A decode step's rows each have a warp's lanes at
+    // once (8 tokens of 16 + 16: 1.8 us, 2.3 with four heads a warp).
     const int64_t rows = (int64_t)p.num_tokens * (p.num_heads + 2 * p.num_kv_heads);
     return rows >= 65536 ? launch<D, kInt8, kNext, kAxes, kInt8 ? 1 : 4>(p, 4, stream)
                          : launch<D, kInt8, kNext, kAxes, 1>(p, 1, stream);
