@@ -297,7 +297,7 @@ class _Plan:
 
 
 class PrefillPlan(_Plan):
-    dims_bytes = None  # what it was packed for
+    packed_for = None  # the dims behind num_blocks, and that
 
     @property
     def slot_mapping(self) -> int:
@@ -365,8 +365,14 @@ def pa_pack_prefill(dims: pa_dims, seq_lens, query_lens, block_lists, pin: bool 
     off, ids = _flatten(block_lists)
     args = (ctypes.byref(dims), len(seq_lens), _np_ptr(seq_lens), _np_ptr(query_lens), _np_ptr(off), _np_ptr(ids))
     plan = _pack("pa_pack_prefill", pa_prefill_meta(), args, into, pin, PrefillPlan)
-    plan.dims_bytes = bytes(dims)
+    plan.packed_for = bytes(dims)[4:], dims.num_blocks
     return plan
+
+
+def _fits(plan: PrefillPlan, dims: pa_dims) -> bool:
+    """Whether dims are those that the plan was packed for, of as many blocks or more."""
+    for_ = plan.packed_for
+    return for_ is None or (bytes(dims)[4:] == for_[0] and dims.num_blocks >= for_[1])
 
 
 def pa_pack_decode(dims: pa_dims, context_lens, block_lists, split_tokens: int = 0, pin: bool = True,
@@ -484,9 +490,8 @@ def _rope_refuse(dims, rope, q, k, v, positions, slot_mapping, q_out, caches, sc
             raise ValueError(f"{what}: a token's heads must be contiguous (in q_out the tokens too), got strides "
                              f"{t.stride()}")
     _int32(positions, "positions", n * rope.axes, dev)
-    if positions.shape not in ((rope.axes, n), (n,) if rope.axes == 1 else ()):
-        raise ValueError(f"positions must be [{rope.axes}, {n}]" + (f" or [{n}]" if rope.axes == 1 else "") +
-                         f", got {tuple(positions.shape)}")
+    if rope.axes > 1 and positions.shape[-1] not in (n, n * rope.axes):  # the tokens of an axis lie side by side
+        raise ValueError(f"positions must be [{rope.axes}, {n}], got {tuple(positions.shape)}")
     _int32(slot_mapping, "slot_mapping", n, dev)
     for t in (q, k, v, q_out, *caches, *scales):
         if t.get_device() != dev:
@@ -515,7 +520,7 @@ def pa_rope_store(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mapping, q
             and qs[1] == ks[1] == vs[1] == d and qs[2] == ks[2] == vs[2] == 1
             and q_out.is_contiguous() and positions.is_contiguous() and slot_mapping.is_contiguous()
             and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and positions.shape in ((rope.axes, n), (n,) if rope.axes == 1 else ())
+            and positions.numel() == n * rope.axes and (rope.axes == 1 or positions.shape[-1] in (n, n * rope.axes))
             and k_cache.numel() >= rope.rows * d <= v_cache.numel() and bytes(dims) == rope.dims_bytes):
         _rope_refuse(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), ())
     row = hkv * d
@@ -543,7 +548,8 @@ def pa_rope_store_int8(dims: pa_dims, rope: Rope, q, k, v, positions, slot_mappi
             and qs[1] == ks[1] == vs[1] == d and qs[2] == ks[2] == vs[2] == 1
             and q_out.is_contiguous() and positions.is_contiguous() and slot_mapping.is_contiguous()
             and k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
-            and v_scale.is_contiguous() and positions.shape in ((rope.axes, n), (n,) if rope.axes == 1 else ())
+            and v_scale.is_contiguous() and positions.numel() == n * rope.axes
+            and (rope.axes == 1 or positions.shape[-1] in (n, n * rope.axes))
             and k_cache.numel() >= rope.rows * d <= v_cache.numel() and k_scale.numel() >= rope.rows <= v_scale.numel()
             and bytes(dims) == rope.dims_bytes):
         _rope_refuse(dims, rope, q, k, v, positions, slot_mapping, q_out, (k_cache, v_cache), (k_scale, v_scale))
@@ -963,16 +969,13 @@ def pa_decode_weights_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale,
 
 def _prefill_window_refuse(dims, q, caches, scales, plan, out, workspace):
     """Why the tensors of a windowed prefill are refused (the calls test for it in one expression)."""
-    if bytes(dims) != plan.dims_bytes:
+    if not _fits(plan, dims):
         raise ValueError("the plan was packed for other dims")
     cache = _INT8 if scales else _BF16
     page = dims.num_blocks * dims.block_size * dims.num_kv_heads
-    want = (plan.meta.total_q, dims.num_heads, dims.head_dim)
-    for what, t in (("q", q), ("out", out)):
-        if tuple(t.shape) != want:
-            raise ValueError(f"{what} must be {list(want)}, got {tuple(t.shape)}")
+    rows = plan.meta.total_q * dims.num_heads * dims.head_dim
     _refuse(plan.dev.get_device(), (q, out, *caches, *scales, workspace),
-            (("q", q, _BF16, 0), ("out", out, _BF16, 0), ("k_cache", caches[0], cache, page * dims.head_dim),
+            (("q", q, _BF16, rows), ("out", out, _BF16, rows), ("k_cache", caches[0], cache, page * dims.head_dim),
              ("v_cache", caches[1], cache, page * dims.head_dim),
              *((what, t, _FP16, page) for what, t in zip(("k_scale", "v_scale"), scales))))
 
@@ -980,19 +983,19 @@ def _prefill_window_refuse(dims, q, caches, scales, plan, out, workspace):
 def pa_prefill_window(dims: pa_dims, q, k_cache, v_cache, plan: PrefillPlan, window: int, sinks: int, scale: float,
                       out, stream=None):
     """pa_prefill_varlen in which a query sees the last ``window`` keys up to its own and the first ``sinks`` ones
-    (the same plan, packed for the same dims).  q, out: bf16 [tokens, Hq, D]."""
-    m, dev, shape = plan.meta, _device(), q.shape
-    base = plan.dptr(0)
+    (the same plan, packed for these dims).  q, out: bf16 [tokens, Hq, D]."""
+    m, dev = plan.meta, _device()
+    base, rows = plan.dptr(0), m.total_q * dims.num_heads * dims.head_dim
     least = dims.num_blocks * dims.block_size * dims.num_kv_heads * dims.head_dim
     if not (dev == plan.dev.get_device() == q.get_device() == k_cache.get_device() == v_cache.get_device() == out.get_device()
             and q.dtype is out.dtype is k_cache.dtype is v_cache.dtype is _BF16
-            and shape == (m.total_q, dims.num_heads, dims.head_dim) and shape == out.shape
-            and q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and k_cache.numel() >= least <= v_cache.numel() and bytes(dims) == plan.dims_bytes):
+            and q.numel() >= rows <= out.numel() and q.is_contiguous() and out.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_cache.numel() >= least <= v_cache.numel() and _fits(plan, dims)):
         _prefill_window_refuse(dims, q, (k_cache, v_cache), (), plan, out, None)
     rc = (_lib or lib()).pa_prefill_window(ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                            base + m.off_cu_seqlens_q, base + m.off_cu_seqlens_k, base + m.off_block_tables,
-                                           _c_int(window), _c_int(sinks), float(scale), out.data_ptr(),
+                                           _c_int(int(window)), _c_int(int(sinks)), float(scale), out.data_ptr(),
                                            ctypes.byref(m), base + m.off_tiles, _stream_of(dev, stream))
     if rc != PA_OK:
         _check(rc, "pa_prefill_window")
@@ -1001,27 +1004,27 @@ def pa_prefill_window(dims: pa_dims, q, k_cache, v_cache, plan: PrefillPlan, win
 def pa_prefill_window_int8(dims: pa_dims, q, k_cache, v_cache, k_scale, v_scale, plan: PrefillPlan, window: int,
                            sinks: int, scale: float, out, workspace=None, stream=None):
     """pa_prefill_window over an INT8 cache (plan and workspace as pa_prefill_varlen_int8's)."""
-    m, dev, shape = plan.meta, _device(), q.shape
-    base = plan.dptr(0)
+    m, dev = plan.meta, _device()
+    base, rows = plan.dptr(0), m.total_q * dims.num_heads * dims.head_dim
     page = dims.num_blocks * dims.block_size * dims.num_kv_heads
     least = page * dims.head_dim
     if not (dev == plan.dev.get_device() == q.get_device() == k_cache.get_device() == v_cache.get_device() == out.get_device()
             == k_scale.get_device() == v_scale.get_device()
             and q.dtype is out.dtype is _BF16 and k_cache.dtype is v_cache.dtype is _INT8
             and k_scale.dtype is v_scale.dtype is _FP16
-            and shape == (m.total_q, dims.num_heads, dims.head_dim) and shape == out.shape
-            and q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and q.numel() >= rows <= out.numel() and q.is_contiguous() and out.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
             and k_scale.is_contiguous() and v_scale.is_contiguous()
             and k_cache.numel() >= least <= v_cache.numel() and k_scale.numel() >= page <= v_scale.numel()
             and (workspace is None or workspace.get_device() == dev and workspace.is_contiguous())
-            and bytes(dims) == plan.dims_bytes):
+            and _fits(plan, dims)):
         _prefill_window_refuse(dims, q, (k_cache, v_cache), (k_scale, v_scale), plan, out, workspace)
     workspace = _call_workspace(plan, workspace, q.device, stream)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     rc = (_lib or lib()).pa_prefill_window_int8(
         ctypes.byref(dims), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         base + m.off_cu_seqlens_q, base + m.off_cu_seqlens_k, base + m.off_block_tables, base + m.off_scratch_tables,
-        base + m.off_scratch_items, _c_int(window), _c_int(sinks), float(scale), out.data_ptr(), ctypes.byref(m),
+        base + m.off_scratch_items, _c_int(int(window)), _c_int(int(sinks)), float(scale), out.data_ptr(), ctypes.byref(m),
         base + m.off_tiles, ws, ws_bytes, _stream_of(dev, stream))
     if rc != PA_OK:
         _check(rc, "pa_prefill_window_int8")

@@ -45,13 +45,13 @@ def test_positions_of_other_shapes_are_refused(calls, int8):
         f = pa.pa_rope_store_int8 if int8 else pa.pa_rope_store
         f(dims, rope, q, k, v, torch.zeros(shape, dtype=torch.int32), slots, out, *cache(int8), stream=0)
 
-    for good in ((1, n), (1, 1, n), (2, 2, n), (4, 4, n)):
-        call(*good)
-    assert len(calls) == 4
-    for bad in ((1, n, 1), (2, n, 2), (2, 2 * n), (4, n, 4), (4, 2, 2, n), (2, n), (1, n + 1)):
+    for good in ((1, n), (1, 1, n), (1, n, 1), (2, 2, n), (2, 2 * n), (4, 4, n), (4, 2, 2, n)):
+        call(*good)  # the tokens of an axis lie side by side
+    assert len(calls) == 7
+    for bad in ((2, n, 2), (4, n, 4), (4, n, 2, 2), (2, n), (1, n + 1), (2, 2, n + 1)):
         with pytest.raises(ValueError):
             call(*bad)
-    assert len(calls) == 4
+    assert len(calls) == 7
 
 
 @pytest.mark.parametrize("int8", [False, True])
@@ -107,12 +107,17 @@ def test_prefill_window_refuses_wrong_tensors_and_dims(monkeypatch, int8):
     call()
     nb, bs, hq, hkv, d = DIMS
     call(k=torch.zeros(8, bs, hkv, d, dtype=good["k"].dtype))  # more pages than the dims name
-    assert len(calls) == 2
-    bad = [dict(q=good["q"].float()), dict(q=good["q"].half()), dict(q=good["q"][:11]), dict(q=torch.zeros(12, 8, 64, dtype=BF)),
+    call(q=torch.zeros(12, 256, dtype=BF), out=torch.zeros(16, 4, 64, dtype=BF))  # a bucket's rows
+    call(dims=pa.make_dims(nb + 1, bs, hq, hkv, d), k=torch.zeros(7, bs, hkv, d, dtype=good["k"].dtype),
+         v=torch.zeros(7, bs, hkv, d, dtype=good["k"].dtype), **({x: torch.zeros(7, hkv, bs, dtype=torch.float16)
+                                                                 for x in ("ks", "vs")} if int8 else {}))
+    assert len(calls) == 4
+    bad = [dict(q=good["q"].float()), dict(q=good["q"].half()), dict(q=good["q"][:11]),
            dict(q=torch.zeros(12, 64, 4, dtype=BF).transpose(1, 2)), dict(out=good["out"].float()),
            dict(out=torch.zeros(24, 4, 64, dtype=BF)[::2]), dict(out=good["out"][:11]), dict(k=good["k"][:5]),
            dict(v=good["v"].float()), dict(v=good["v"].transpose(1, 2)),
-           dict(dims=pa.make_dims(nb + 1, bs, hq, hkv, d)), dict(dims=pa.make_dims(nb, 32, hq, hkv, d)),
+           dict(dims=pa.make_dims(nb + 1, bs, hq, hkv, d)), dict(dims=pa.make_dims(nb - 1, bs, hq, hkv, d)),
+           dict(dims=pa.make_dims(nb, 32, hq, hkv, d)),
            dict(dims=pa.make_dims(nb, bs, hkv, hq, d)), dict(dims=pa.make_dims(nb, bs, 2 * hq, 2 * hkv, d))]
     if int8:
         bad += [dict(ks=good["ks"].float()), dict(vs=good["vs"][:5]), dict(ws=[torch.zeros(1 << 20, dtype=torch.uint8)[::2]])]
@@ -122,4 +127,4 @@ def test_prefill_window_refuses_wrong_tensors_and_dims(monkeypatch, int8):
     monkeypatch.setattr(pa, "_device", lambda: 0)  # the tensors and the plan are elsewhere
     with pytest.raises(ValueError):
         call()
-    assert len(calls) == 2
+    assert len(calls) == 4
